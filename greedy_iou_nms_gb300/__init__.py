@@ -17,6 +17,15 @@ import math
 import os
 from typing import Optional
 
+from . import head
+from .head import (NMS_ACT_GELU, NMS_ACT_NONE, NMS_ACT_RELU, NMS_ACT_SILU, NMS_NORM_MAX_BATCH,  # noqa: F401
+                   NMS_NORM_MAX_CHANNELS, NMS_NORM_MAX_PIXELS, NMS_RELATION_MAX_AXES, NMS_RELATION_MAX_BUCKETS,
+                   NMS_RELATION_MAX_HEADS, NMS_RELATION_MAX_REACH, NMS_TYPE_BF16, NMS_TYPE_F16, NMS_TYPE_F32, dropout,
+                   dropout_grad, group_norm_act, group_norm_act_grad, nms_dropout_run, nms_group_norm_grad_run,
+                   nms_group_norm_run, nms_group_norm_workspace_size, nms_relation_buckets_run,
+                   nms_relation_grad_workspace_size, nms_relation_softmax_grad_run, nms_relation_softmax_run,
+                   relation_buckets, relation_lut_cells, relation_lut_log, relation_softmax, relation_softmax_grad)
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_build", "libgbnms.so")
 
@@ -34,7 +43,7 @@ EXPORTED = ("nms_status_string", "nms_workspace_size", "nms_run", "nms_fast_run"
             "nms_matrix_workspace_size", "nms_matrix_run", "nms_mask_row_words", "nms_iou_mask",
             "nms_resolve_mask", "nms_resolve_mask_noalloc", "nms_decode_workspace_size", "nms_decode_boxes7",
             "nms_boxes7_workspace_size", "nms_boxes7_run", "nms_mapped_pointer", "nms_copy", "nms_lane_workspace_size",
-            "nms_lane_run")
+            "nms_lane_run") + head.EXPORTED
 NMS_NOALLOC_MAX_N = 16384
 NMS_LANE_VALUES = 77  # values of one lane candidate (nms_lane_run)
 NMS_LANE_ROWS = 72
@@ -106,6 +115,7 @@ def load():
     lib.nms_lane_workspace_size.restype = ctypes.c_int
     lib.nms_lane_run.argtypes = [vp, vp, i64, f32, i32, vp, i64, vp, vp, vp, sz, vp]
     lib.nms_lane_run.restype = ctypes.c_int
+    head.declare(lib)
     _lib = lib
     return lib
 

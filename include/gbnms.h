@@ -419,6 +419,152 @@ nms_status nms_lane_run(const float* props, const float* scores, int64_t n, floa
 nms_status nms_resolve_mask_noalloc(const uint64_t* mask, int64_t n, const int32_t* perm,
                                     int32_t max_out, int64_t* keep, int64_t* count, void* stream);
 
+/*
+ * Operators of a trainable detection head: what runs between a detector's
+ * convolutions and the decode above, and between its candidates, forward and
+ * backward.  Conventions as everywhere here: the caller owns every buffer, no
+ * call allocates or synchronises, host-detected errors return before anything
+ * is enqueued.  Inputs and outputs must not overlap unless said otherwise.
+ * Element types of features, scores and weights; sums, statistics and
+ * softmax terms are held in binary32, and a result is rounded to its type
+ * once, to nearest even.
+ */
+#define NMS_TYPE_F32 0
+#define NMS_TYPE_F16 1
+#define NMS_TYPE_BF16 2
+
+/* Activations of nms_group_norm_run: z, max(z, 0), z / (1 + e^-z),
+ * z (1 + erf(z / sqrt 2)) / 2. */
+#define NMS_ACT_NONE 0
+#define NMS_ACT_RELU 1
+#define NMS_ACT_SILU 2
+#define NMS_ACT_GELU 3
+
+#define NMS_NORM_MAX_CHANNELS 16384
+#define NMS_NORM_MAX_BATCH (1 << 20)
+#define NMS_NORM_MAX_PIXELS (1 << 28)
+
+/*
+ * Dropout.  Element e of a tensor (its row-major index) is kept iff its
+ * 16-bit field is below T = floor((1 - drop_p) * 65536 + 1/2); a kept element
+ * is multiplied by 65536 / T, a dropped one is 0 whatever its value was.  The
+ * field is bits 16 (e mod 2) and up of word (e mod 8) / 2 of Philox 4x32-10
+ * (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3", 2011) with
+ * key `seed` and counter (e / 8, offset), each 64 bits, low word first.  So
+ * the mask depends on nothing but the three numbers, is never stored, and a
+ * gradient draws it again.
+ *   y = drop(x), or residual + drop(x) with a residual of the same type.  The
+ *   gradient is the same call on the incoming gradient, without residual.
+ *   n        elements, contiguous; y may be x or residual itself.
+ *   drop_p   in [0, 1].
+ * Errors: NMS_ERR_INVALID_ARG (type, drop_p, NULL or misaligned pointers),
+ *         NMS_ERR_CAPACITY (n > 2^47), NMS_ERR_CUDA.
+ */
+nms_status nms_dropout_run(const void* x, const void* residual, int32_t type, int64_t n, double drop_p,
+                           uint64_t seed, uint64_t offset, void* y, void* stream);
+
+/*
+ * Group normalisation of a channels-last map [batch][pixels][channels] with
+ * its affine map, activation and dropout:
+ *   u = (x - mean) * rstd,  z = u * weight + bias,  y = drop(act(z)),
+ * mean and the biased variance over the pixels and the channels / groups
+ * consecutive channels of one group of one image, rstd = 1 / sqrt(variance +
+ * eps); drop as for nms_dropout_run, by the element's index in y.
+ *   x          device, `type`; image b's pixel s starts at element b *
+ *              x_image + s * x_pixel, its channels are consecutive
+ *              (x_pixel >= channels: a slice of a wider map is fine).
+ *   weight, bias  device [channels] of param_type (NMS_TYPE_F32, or `type`),
+ *              or NULL (1 and 0).
+ *   y          device [batch][pixels][channels] contiguous, `type`.
+ *   mean, rstd device float [batch][groups] for the gradient, or NULL.  With
+ *              no pixels both are 0.
+ *   workspace  >= nms_group_norm_workspace_size() bytes, 256-byte aligned.
+ * The gradient, from the incoming gradient dy (laid out like x, with strides
+ * of its own) and the forward's mean, rstd and dropout numbers:
+ *   dz = drop(dy) * act'(z), dbias = sum dz, dweight = sum dz * u over images
+ *   and pixels, dx = rstd * (du - avg(du) - u * avg(du * u)), du = dz * weight,
+ * the averages over the group of the image; relu'(0) = 0.  dweight and dbias
+ * (float [channels]) may be NULL.  Sums are taken in a fixed order: the same
+ * call gives the same bits.
+ * Errors: NMS_ERR_INVALID_ARG (types, act, eps < 0 or not finite, drop_p,
+ *         shapes, channels not a multiple of groups, strides that overlap,
+ *         NULL or misaligned pointers), NMS_ERR_CAPACITY (limits above, batch *
+ *         groups above 2^31 - 1 or more than 2^47 elements), NMS_ERR_WORKSPACE, NMS_ERR_CUDA.
+ */
+nms_status nms_group_norm_workspace_size(int64_t batch, int64_t pixels, int32_t channels, int32_t groups,
+                                         size_t* bytes);
+nms_status nms_group_norm_run(const void* x, int64_t x_image, int64_t x_pixel, int32_t type, int64_t batch,
+                              int64_t pixels, int32_t channels, int32_t groups, const void* weight,
+                              const void* bias, int32_t param_type, float eps, int32_t act, double drop_p,
+                              uint64_t seed, uint64_t offset, void* y, float* mean, float* rstd,
+                              void* workspace, size_t workspace_bytes, void* stream);
+nms_status nms_group_norm_grad_run(const void* dy, int64_t dy_image, int64_t dy_pixel, const void* x,
+                                   int64_t x_image, int64_t x_pixel, int32_t type, int64_t batch, int64_t pixels,
+                                   int32_t channels, int32_t groups, const float* mean, const float* rstd,
+                                   const void* weight, const void* bias, int32_t param_type, int32_t act,
+                                   double drop_p, uint64_t seed, uint64_t offset, void* dx, float* dweight,
+                                   float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+#define NMS_RELATION_MAX_BUCKETS 1024
+#define NMS_RELATION_MAX_HEADS 4096
+#define NMS_RELATION_MAX_AXES 4
+#define NMS_RELATION_MAX_REACH (1 << 20)
+
+/*
+ * The bucket of every (query, key) pair by their relative position, for
+ * nms_relation_softmax_run: the sum over the axes of lut[axis][reach +
+ * clamp(k - q, -reach, reach)], or -1 (a masked pair) when a part is negative
+ * or the sum is above 32767.  Each axis has a table of its own, so a map by
+ * (row, column) cells holds rows * width parts in one and column parts in the
+ * other, and distances in logarithmic buckets, or keys that lie ahead masked,
+ * are a table too.
+ *   q_pos, k_pos  device int32 [q_sets][queries][axes], [k_sets][keys][axes];
+ *                 the set counts are equal, or one of them is 1 (shared).
+ *   lut           device int32 [axes][2 * reach + 1].
+ *   buckets       device int16 [max sets][queries][keys].
+ * Errors: NMS_ERR_INVALID_ARG, NMS_ERR_CAPACITY (limits above), NMS_ERR_CUDA.
+ */
+nms_status nms_relation_buckets_run(const int32_t* q_pos, int64_t q_sets, const int32_t* k_pos, int64_t k_sets,
+                                    int64_t queries, int64_t keys, int32_t axes, const int32_t* lut,
+                                    int32_t reach, int16_t* buckets, void* stream);
+
+/*
+ * Attention weights with a learned bias by bucket:
+ *   probs[b][h][i][:] = softmax over the valid keys j of
+ *       scale * scores[b][h][i][j] + table[bucket][h].
+ * A pair is masked when its bucket is outside [0, num_buckets) or its key's
+ * mask is 0; a masked pair has weight 0 and its score (NaN and infinities
+ * too) is never looked at; a row whose pairs are all masked, or all -inf, is
+ * all 0.
+ *   scores, probs device [batch][heads][queries][keys] of `type`.
+ *   buckets       device int16 [sets][queries][keys], sets = 1 (one map for
+ *                 all images) or batch.
+ *   table         device float [num_buckets][heads].
+ *   key_mask      device uint8 [batch][keys], non-zero where the key takes
+ *                 part, or NULL (all do).
+ * The gradient, from the incoming gradient dprobs and the forward's probs
+ * (masked places are again not looked at):
+ *   da = probs * (dprobs - sum_j probs * dprobs), dscores = scale * da (0 for
+ *   a masked pair), dtable[u][h] = sum of da over the pairs of bucket u
+ *   (float [num_buckets][heads], every entry written), summed in a fixed
+ *   order.
+ *   workspace     >= nms_relation_grad_workspace_size() bytes, 256-byte
+ *                 aligned.
+ * Errors: NMS_ERR_INVALID_ARG, NMS_ERR_CAPACITY (limits above, or more than
+ *         2^40 rows or 2^47 elements), NMS_ERR_WORKSPACE, NMS_ERR_CUDA.
+ */
+nms_status nms_relation_softmax_run(const void* scores, int32_t type, int64_t batch, int32_t heads,
+                                    int64_t queries, int64_t keys, const int16_t* buckets, int64_t sets,
+                                    const float* table, int32_t num_buckets, const uint8_t* key_mask, float scale,
+                                    void* probs, void* stream);
+nms_status nms_relation_grad_workspace_size(int64_t batch, int32_t heads, int64_t queries, int64_t keys,
+                                            int32_t num_buckets, size_t* bytes);
+nms_status nms_relation_softmax_grad_run(const void* dprobs, const void* probs, int32_t type, int64_t batch,
+                                         int32_t heads, int64_t queries, int64_t keys, const int16_t* buckets,
+                                         int64_t sets, int32_t num_buckets, const uint8_t* key_mask, float scale,
+                                         void* dscores, float* dtable, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
 #ifdef __cplusplus
 }
 #endif

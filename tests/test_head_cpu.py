@@ -1,0 +1,135 @@
+"""The detection-head operators without a GPU: the generator's published
+vectors (of the tests' own restatement), host-side argument checks of the C
+entries, workspace sizes and the position tables."""
+import math
+
+import pytest
+
+import greedy_iou_nms_gb300 as g
+
+torch = pytest.importorskip("torch")
+import head_reference as R  # noqa: E402
+
+FAKE = 1 << 20  # an aligned non-null address; never dereferenced on these paths
+BIG = 1 << 40
+BAD, CAP, WS = g.NMS_ERR_INVALID_ARG, g.NMS_ERR_CAPACITY, g.NMS_ERR_WORKSPACE
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    g.build()
+    return g.load()
+
+
+def test_philox_vectors():
+    """Philox 4x32-10 known answers for all-zero and all-one counter and key."""
+    assert R.philox(0, 0, 0) == [0x6627e8d5, 0xe169c58d, 0xbc57ac4c, 0x9b00dbd8]
+    ones = (1 << 64) - 1
+    assert R.philox(ones, ones, ones) == [0x408f276d, 0x41c83b0e, 0xa20bc7c6, 0x6d5451fd]
+
+
+def test_dropout_checks():
+    a = dict(x=FAKE, residual=0, type=g.NMS_TYPE_BF16, n=10, drop_p=0.5, seed=1, offset=0, y=FAKE, stream=0)
+    for bad, code in ((dict(type=3), BAD), (dict(type=-1), BAD), (dict(n=-1), BAD), (dict(drop_p=-0.01), BAD),
+                      (dict(drop_p=1.01), BAD), (dict(drop_p=math.nan), BAD), (dict(x=0), BAD), (dict(y=0), BAD),
+                      (dict(x=FAKE + 1), BAD), (dict(y=FAKE + 1), BAD), (dict(residual=FAKE + 1), BAD),
+                      (dict(type=g.NMS_TYPE_F32, x=FAKE + 2), BAD), (dict(n=(1 << 47) + 1), CAP)):
+        assert g.nms_dropout_run(**dict(a, **bad)) == code, bad
+    assert g.nms_dropout_run(**dict(a, n=0, x=0, y=0)) == g.NMS_OK
+
+
+def _norm(**kw):
+    a = dict(x=FAKE, x_image=640, x_pixel=64, type=g.NMS_TYPE_F32, batch=2, pixels=10, channels=64, groups=8,
+             weight=0, bias=0, param_type=g.NMS_TYPE_F32, eps=1e-5, act=g.NMS_ACT_SILU, drop_p=0.0, seed=0, offset=0,
+             y=FAKE, mean=FAKE, rstd=FAKE, workspace=FAKE, workspace_bytes=BIG, stream=0)
+    a.update(kw)
+    return g.nms_group_norm_run(**a)
+
+
+def _norm_grad(**kw):
+    a = dict(dy=FAKE, dy_image=640, dy_pixel=64, x=FAKE, x_image=640, x_pixel=64, type=g.NMS_TYPE_F32, batch=2,
+             pixels=10, channels=64, groups=8, mean=FAKE, rstd=FAKE, weight=0, bias=0, param_type=g.NMS_TYPE_F32,
+             act=g.NMS_ACT_SILU, drop_p=0.0, seed=0, offset=0, dx=FAKE, dweight=FAKE, dbias=FAKE, workspace=FAKE,
+             workspace_bytes=BIG, stream=0)
+    a.update(kw)
+    return g.nms_group_norm_grad_run(**a)
+
+
+def test_norm_checks():
+    shared = ((dict(type=7), BAD), (dict(param_type=g.NMS_TYPE_F16), BAD), (dict(act=4), BAD), (dict(act=-1), BAD),
+              (dict(drop_p=2.0), BAD), (dict(batch=-1), BAD), (dict(pixels=-1), BAD), (dict(channels=0), BAD),
+              (dict(groups=0), BAD), (dict(groups=7), BAD), (dict(x_pixel=63), BAD), (dict(x_pixel=-64), BAD),
+              (dict(x_image=-1), BAD), (dict(x=0), BAD), (dict(x=FAKE + 2), BAD), (dict(weight=FAKE + 2), BAD),
+              (dict(mean=FAKE + 2), BAD), (dict(workspace=0), WS), (dict(workspace=FAKE + 8), WS),
+              (dict(workspace_bytes=g.nms_group_norm_workspace_size(2, 10, 64, 8) - 1), WS),
+              (dict(channels=16392, x_pixel=16392), CAP), (dict(batch=(1 << 20) + 1), CAP),
+              (dict(pixels=(1 << 28) + 1), CAP), (dict(x_image=1 << 60), BAD), (dict(x_pixel=1 << 60), BAD),
+              (dict(batch=1 << 20, channels=16384, groups=4096, x_pixel=16384), CAP))
+    for run in (_norm, _norm_grad):
+        for bad, code in shared:
+            assert run(**bad) == code, (run, bad)
+    for bad, code in ((dict(y=0), BAD), (dict(eps=-1.0), BAD), (dict(eps=math.nan), BAD), (dict(eps=math.inf), BAD)):
+        assert _norm(**bad) == code, bad
+    for bad, code in ((dict(dx=0), BAD), (dict(dy=0), BAD), (dict(mean=0), BAD), (dict(rstd=0), BAD),
+                      (dict(dy_pixel=1), BAD), (dict(dweight=FAKE + 2), BAD)):
+        assert _norm_grad(**bad) == code, bad
+    assert _norm(batch=0, x=0, y=0, workspace=0) == g.NMS_OK
+    with pytest.raises(g.NmsError):
+        g.nms_group_norm_workspace_size(1, 1, 10, 3)
+
+
+def test_relation_checks():
+    f = dict(scores=FAKE, type=g.NMS_TYPE_F16, batch=2, heads=3, queries=4, keys=5, buckets=FAKE, sets=2, table=FAKE,
+             num_buckets=6, key_mask=0, scale=1.0, probs=FAKE, stream=0)
+    b = dict(dprobs=FAKE, probs=FAKE, type=g.NMS_TYPE_F16, batch=2, heads=3, queries=4, keys=5, buckets=FAKE, sets=2,
+             num_buckets=6, key_mask=0, scale=1.0, dscores=FAKE, dtable=FAKE, workspace=FAKE, workspace_bytes=BIG,
+             stream=0)
+    for run, a in ((g.nms_relation_softmax_run, f), (g.nms_relation_softmax_grad_run, b)):
+        for bad, code in ((dict(type=9), BAD), (dict(batch=-1), BAD), (dict(heads=0), BAD), (dict(queries=-1), BAD),
+                          (dict(keys=-1), BAD), (dict(sets=3), BAD), (dict(sets=0), BAD), (dict(num_buckets=0), BAD),
+                          (dict(num_buckets=1025), CAP), (dict(heads=4097), CAP), (dict(scale=math.nan), BAD),
+                          (dict(probs=0), BAD), (dict(probs=FAKE + 1), BAD), (dict(buckets=0), BAD),
+                          (dict(buckets=FAKE + 1), BAD), (dict(batch=1 << 30, sets=1, queries=1 << 20), CAP)):
+            assert run(**dict(a, **bad)) == code, bad
+    assert g.nms_relation_softmax_run(**dict(f, table=FAKE + 2)) == BAD
+    for bad, code in ((dict(dtable=0), BAD), (dict(dprobs=0), BAD), (dict(dscores=FAKE + 1), BAD), (dict(workspace=0), WS),
+                      (dict(workspace_bytes=g.nms_relation_grad_workspace_size(2, 3, 4, 5, 6) - 1), WS)):
+        assert g.nms_relation_softmax_grad_run(**dict(b, **bad)) == code, bad
+    m = dict(q_pos=FAKE, q_sets=1, k_pos=FAKE, k_sets=3, queries=4, keys=5, axes=2, lut=FAKE, reach=3, buckets=FAKE,
+             stream=0)
+    for bad, code in ((dict(q_sets=2), BAD), (dict(q_sets=-1), BAD), (dict(queries=-1), BAD), (dict(axes=0), BAD),
+                      (dict(axes=5), CAP), (dict(reach=-1), BAD), (dict(reach=(1 << 20) + 1), CAP), (dict(lut=0), BAD),
+                      (dict(q_pos=FAKE + 2), BAD), (dict(buckets=FAKE + 1), BAD), (dict(keys=1 << 48), CAP)):
+        assert g.nms_relation_buckets_run(**dict(m, **bad)) == code, bad
+
+
+def test_tensor_functions_refuse_cpu_tensors():
+    x = torch.randn(2, 9, 12)
+    m = torch.zeros(1, 4, 5, dtype=torch.int16)
+    for call in (lambda: g.group_norm_act(x, 3), lambda: g.dropout(x, 0.5, 0),
+                 lambda: g.relation_softmax(torch.randn(1, 2, 4, 5), torch.randn(3, 2), m),
+                 lambda: g.relation_buckets(m.int(), m.int(), torch.zeros(5, 3, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_logarithmic_table():
+    lut = g.relation_lut_log(8, 64)[0].tolist()
+    assert len(lut) == 129 and lut == lut[::-1]  # as far behind as ahead
+    back = lut[64:]
+    assert back[:4] == [0, 1, 2, 3] and back == sorted(back) and back[64] == 7 and set(back) == set(range(8))
+    assert all(b == 4 + int(math.log(d / 4) / math.log(16) * 4 + 1e-12) for d, b in enumerate(back) if 4 < d < 64)
+    own = g.relation_lut_log(8, 64, ahead="own")[0].tolist()
+    assert own[:65] == lut[:65] and own[65:] == [8 + b for b in back[1:]]
+    masked = g.relation_lut_log(8, 64, ahead="mask")[0].tolist()
+    assert masked[:65] == lut[:65] and masked[65:] == [-1] * 64
+    for bad in ((1, 64), (8, 3)):
+        with pytest.raises(ValueError):
+            g.relation_lut_log(*bad)
+    with pytest.raises(ValueError):
+        g.relation_lut_log(8, 64, ahead="none")
+
+
+def test_cell_table():
+    lut = g.relation_lut_cells(1, 2)
+    assert lut.tolist() == [[0, 0, 5, 10, 10], [0, 1, 2, 3, 4]] and lut.dtype == torch.int32
