@@ -43,7 +43,7 @@ int64_t product(int64_t a, int64_t b, int64_t most)
 }
 
 constexpr int64_t kMostElements = int64_t(1) << 47;
-constexpr int64_t kMostRows = int64_t(1) << 40;
+constexpr int64_t kMostRows = INT32_MAX;
 
 // Shape of a feature map: 0, or the status to return.
 nms_status check_map(int64_t batch, int64_t pixels, int32_t channels, int32_t groups)

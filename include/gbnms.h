@@ -522,7 +522,8 @@ nms_status nms_group_norm_grad_run(const void* dy, int64_t dy_image, int64_t dy_
  *                 the set counts are equal, or one of them is 1 (shared).
  *   lut           device int32 [axes][2 * reach + 1].
  *   buckets       device int16 [max sets][queries][keys].
- * Errors: NMS_ERR_INVALID_ARG, NMS_ERR_CAPACITY (limits above), NMS_ERR_CUDA.
+ * Errors: NMS_ERR_INVALID_ARG, NMS_ERR_CAPACITY (limits above, or more than
+ *         2^31 - 1 rows of queries or 2^47 pairs), NMS_ERR_CUDA.
  */
 nms_status nms_relation_buckets_run(const int32_t* q_pos, int64_t q_sets, const int32_t* k_pos, int64_t k_sets,
                                     int64_t queries, int64_t keys, int32_t axes, const int32_t* lut,
@@ -551,7 +552,7 @@ nms_status nms_relation_buckets_run(const int32_t* q_pos, int64_t q_sets, const 
  *   workspace     >= nms_relation_grad_workspace_size() bytes, 256-byte
  *                 aligned.
  * Errors: NMS_ERR_INVALID_ARG, NMS_ERR_CAPACITY (limits above, or more than
- *         2^40 rows or 2^47 elements), NMS_ERR_WORKSPACE, NMS_ERR_CUDA.
+ *         2^31 - 1 rows or 2^47 elements), NMS_ERR_WORKSPACE, NMS_ERR_CUDA.
  */
 nms_status nms_relation_softmax_run(const void* scores, int32_t type, int64_t batch, int32_t heads,
                                     int64_t queries, int64_t keys, const int16_t* buckets, int64_t sets,
