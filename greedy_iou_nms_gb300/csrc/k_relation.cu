@@ -56,7 +56,7 @@ void launch_relation_softmax(const RelationArgs& a, cudaStream_t st)
 }
 
 // Lanes of a row's team (k_relation.cuh).
-static int team_lanes(int64_t keys) { return keys <= 64 ? 8 : keys <= 1024 ? 32 : 256; }
+static int team_lanes(int64_t keys) { return keys <= 64 ? 8 : keys <= 128 ? 16 : keys <= 1024 ? 32 : 256; }
 
 RelationGradPlan relation_grad_plan(int64_t batch, int heads, int64_t queries, int64_t keys, int num_buckets,
                                     bool image)
@@ -65,7 +65,7 @@ RelationGradPlan relation_grad_plan(int64_t batch, int heads, int64_t queries, i
     const int lanes = keys > RELATION_MOST ? 32 : team_lanes(keys);
     if (image) {
         // One table a block, small enough for four blocks on an SM.
-        p.columns = num_buckets * 128 <= 48 * 1024 ? 32 : 8;
+        p.columns = (num_buckets + 1) * 128 <= 48 * 1024 ? 32 : 8;
         p.warps = 8;
         const int64_t teams = 256 / lanes;
         p.blocks = (queries + teams - 1) / teams;
@@ -78,11 +78,11 @@ RelationGradPlan relation_grad_plan(int64_t batch, int heads, int64_t queries, i
     // A table a warp: 32 columns if six warps' fit, else fewer.
     constexpr int ROOM = 208 * 1024;
     const int need = lanes == 256 ? 8 : 6;
-    for (p.columns = 32; p.columns > 4 && need * num_buckets * 4 * p.columns > ROOM; p.columns /= 2) {}
-    const int fit = ROOM / (num_buckets * 4 * p.columns);
+    for (p.columns = 32; p.columns > 4 && need * (num_buckets + 1) * 4 * p.columns > ROOM; p.columns /= 2) {}
+    const int fit = ROOM / ((num_buckets + 1) * 4 * p.columns);
     p.warps = fit > 8 ? 8 : fit;
     const int64_t teams = p.warps * 32 / lanes, rows = batch * queries, want = (rows + teams - 1) / teams;
-    const int resident = ROOM / (p.warps * num_buckets * 4 * p.columns);
+    const int resident = ROOM / (p.warps * (num_buckets + 1) * 4 * p.columns);
     const int64_t most = (152 * static_cast<int64_t>(resident < 4 ? resident : 4) + heads - 1) / heads;
     p.blocks = want < most ? want : most;
     p.chunks = 1;
