@@ -8,6 +8,8 @@
 
 namespace gbnms {
 
+constexpr int SMS = 152;  // of a GB300; launches are sized by it
+
 // Dropout of one call: an element is kept when its 16-bit field is below
 // limit (65536: every element), and a kept one is multiplied by factor.
 struct DropArgs {

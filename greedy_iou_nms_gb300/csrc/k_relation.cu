@@ -36,7 +36,7 @@ relation_buckets_kernel(BucketArgs a)
 void launch_relation_buckets(const BucketArgs& a, cudaStream_t st)
 {
     const int64_t want = (a.sets * a.queries * a.keys + BK_THREADS - 1) / BK_THREADS;
-    relation_buckets_kernel<<<static_cast<unsigned>(want < 152 * 64 ? want : 152 * 64), BK_THREADS, 0, st>>>(a);
+    relation_buckets_kernel<<<static_cast<unsigned>(want < SMS * 64 ? want : SMS * 64), BK_THREADS, 0, st>>>(a);
 }
 
 // ---------------------------------------------------------------- dispatch
@@ -64,13 +64,15 @@ RelationGradPlan relation_grad_plan(int64_t batch, int heads, int64_t queries, i
     RelationGradPlan p{};
     const int lanes = keys > RELATION_MOST ? 32 : team_lanes(keys);
     if (image) {
-        // One table a block, small enough for four blocks on an SM.
-        p.columns = (num_buckets + 1) * 128 <= 48 * 1024 ? 32 : 8;
+        // One table a block, small enough for several blocks on an SM.
+        p.columns = (num_buckets + 1) * 128 <= 46 * 1024 ? 32 : 8;
         p.warps = 8;
         const int64_t teams = 256 / lanes;
         p.blocks = (queries + teams - 1) / teams;
-        const int64_t want = (152 * 8 + p.blocks * heads - 1) / (p.blocks * heads);
-        p.chunks = want > batch ? batch : want;
+        const int64_t held = (keys + lanes - 1) / lanes;  // elements a lane
+        const int resident = held <= 8 ? 3 : held <= 16 ? 2 : 1;
+        const int64_t want = SMS * resident / (p.blocks * heads);  // one wave
+        p.chunks = want < 1 ? 1 : want > batch ? batch : want;
         p.per = (batch + p.chunks - 1) / p.chunks;
         p.chunks = (batch + p.per - 1) / p.per;
         return p;
@@ -83,7 +85,7 @@ RelationGradPlan relation_grad_plan(int64_t batch, int heads, int64_t queries, i
     p.warps = fit > 8 ? 8 : fit;
     const int64_t teams = p.warps * 32 / lanes, rows = batch * queries, want = (rows + teams - 1) / teams;
     const int resident = ROOM / (p.warps * (num_buckets + 1) * 4 * p.columns);
-    const int64_t most = (152 * static_cast<int64_t>(resident < 4 ? resident : 4) + heads - 1) / heads;
+    const int64_t most = (SMS * static_cast<int64_t>(resident < 4 ? resident : 4) + heads - 1) / heads;
     p.blocks = want < most ? want : most;
     p.chunks = 1;
     return p;

@@ -9,8 +9,8 @@
 //   dtable[u][h] = sum of da over the pairs of bucket u.
 //
 // Both directions read each operand once and write the result once, so HBM
-// bounds them.  A row stays in the registers of its team: L lanes, E elements
-// a lane, moved as vectors of EV.  What a row needs besides (its buckets, its
+// bounds them.  A row stays in the registers of its team: L lanes, NV vectors
+// of EV elements a lane.  What a row needs besides (its buckets, its
 // bias) is the same for many rows, so a team stays with one (query, map) and
 // goes through the rows that share it, loading the next row before it works
 // on the present one:
@@ -62,184 +62,332 @@ __device__ __forceinline__ float team_reduce(float v, float* s)
     return v;
 }
 
-template <typename T, int EV, int L, int NV>
-__device__ __forceinline__ void load_vectors(Pack<T, EV> (&q)[NV], const T* row, int K, int lane)
+__device__ __forceinline__ float reciprocal(float x)
 {
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int j = (v * L + lane) * EV;
-        if (j < K) q[v] = *reinterpret_cast<const Pack<T, EV>*>(row + j);
-    }
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// What a lane knows of its elements' pairs: the bucket index, num_buckets for
-// a masked pair or an element past the row, and which are valid, as a mask of
-// the packed operand (PACKED: two 16-bit elements to a word) or as bits.
-template <typename T, int EV, int NV>
-struct Pairs {
-    static constexpr bool PACKED = sizeof(T) == 2 && EV % 2 == 0;
-    static constexpr int WORDS = PACKED ? NV * EV / 2 : 1;
-    Pack<uint16_t, EV> u[NV];
-    uint32_t valid[WORDS];
+// 0xffff in each half (byte pair) of x whose top bit is set.
+__device__ __forceinline__ uint32_t spread_top_bits(uint32_t x)
+{
+    uint32_t y;
+    asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(y) : "r"(x));
+    return y;
+}
 
-    template <int L>
-    __device__ __forceinline__ void set(const Pack<int16_t, EV> (&q)[NV], const uint8_t* mask, int K, int lane, int nb)
-    {
-        if (!PACKED) valid[0] = 0;
+// The same from the top bits of the low (HIGH: high) two bytes.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t spread_byte_bits(uint32_t x)
+{
+    uint32_t y;
+    if (HIGH) asm("prmt.b32 %0, %1, 0, 0xbbaa;" : "=r"(y) : "r"(x));
+    else asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <typename T> __device__ __forceinline__ uint32_t pack_two(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack_two<__half>(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack_two<__nv_bfloat16>(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack_two<float>(float, float) { return 0; }  // never called
+
+// Rounds EV results to their type.
+template <typename T, int EV>
+__device__ __forceinline__ Pack<T, EV> pack_results(const float (&x)[EV])
+{
+    Pack<T, EV> q;
+    if constexpr (sizeof(T) == 2 && EV % 2 == 0) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int j = (v * L + lane) * EV;
-            const bool in = j < K;
-            if (PACKED) {
-                Pack<uint8_t, EV> m;
-                if (mask && in) m = *reinterpret_cast<const Pack<uint8_t, EV>*>(mask + j);
+        for (int e = 0; e < EV; e += 2) reinterpret_cast<uint32_t*>(&q)[e / 2] = pack_two<T>(x[e], x[e + 1]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < EV; ++e) q.v[e] = from_f32<T>(x[e]);
+    }
+    return q;
+}
+
+__device__ __forceinline__ void unpack_two(uint32_t w, float& lo, float& hi, __nv_bfloat16)
+{
+    lo = __uint_as_float(w << 16);
+    hi = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack_two(uint32_t w, float& lo, float& hi, __half)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    lo = f.x;
+    hi = f.y;
+}
+__device__ __forceinline__ void unpack_two(uint32_t, float&, float&, float) {}  // never called
+
+__device__ __forceinline__ uint32_t bits_of(float x) { return __float_as_uint(x); }
+__device__ __forceinline__ uint32_t bits_of(__half x) { return __half_as_ushort(x); }
+__device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
+__device__ __forceinline__ float of_bits(uint32_t w, float) { return __uint_as_float(w); }
+__device__ __forceinline__ float of_bits(uint32_t w, __half) { return to_f32(__ushort_as_half(static_cast<unsigned short>(w))); }
+__device__ __forceinline__ float of_bits(uint32_t w, __nv_bfloat16) { return __uint_as_float(w << 16); }
+
+// How a team holds a row: L lanes by NV vectors of EV elements, of which all
+// but the last SLACK vectors lie inside every row that the shape serves.
+template <typename T_, int EV_, int L_, int NV_, int SLACK_>
+struct Shape {
+    using T = T_;
+    static constexpr int EV = EV_, L = L_, NV = NV_, SLACK = SLACK_, E = EV * NV;
+    // Two 16-bit elements to a word.
+    static constexpr bool PACKED = sizeof(T) == 2 && EV % 2 == 0;
+    // Blocks that an SM holds at least (the launches count on it).
+    static constexpr int BLOCKS = (E > 16 ? 1 : E > 8 ? 2 : 3) + (PACKED ? 1 : 0);
+    static constexpr int GRAD_BLOCKS = E > 16 ? 1 : E > 8 ? 2 : 3;
+
+    static __device__ __forceinline__ int first(int v, int lane) { return (v * L + lane) * EV; }
+    static __device__ __forceinline__ bool inside(int v, int lane, int K)
+    {
+        return v < NV - SLACK || first(v, lane) < K;
+    }
+    // A row's vectors; one past the row reads the row's start instead.
+    template <typename U>
+    static __device__ __forceinline__ void load(Pack<U, EV> (&q)[NV], const U* row, int K, int lane)
+    {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            q[v] = *reinterpret_cast<const Pack<U, EV>*>(row + (inside(v, lane, K) ? first(v, lane) : 0));
+    }
+    // Vector v as binary32.
+    static __device__ __forceinline__ void widen(float (&x)[EV], const Pack<T, EV>& q)
+    {
+        if constexpr (PACKED) {
+#pragma unroll
+            for (int e = 0; e < EV; e += 2)
+                unpack_two(reinterpret_cast<const uint32_t*>(&q)[e / 2], x[e], x[e + 1], T{});
+        } else {
+#pragma unroll
+            for (int e = 0; e < EV; ++e) x[e] = to_f32(q.v[e]);
+        }
+    }
+};
+
+// Bucket indices of a lane's elements, num_buckets for a masked pair or an
+// element past the row: two to a word when PACKED.
+template <typename S>
+struct Buckets {
+    uint32_t u[S::PACKED ? S::E / 2 : S::E];
+
+    // From the map's vectors and (or NULL) the key mask's.
+    __device__ __forceinline__ void set(const Pack<int16_t, S::EV> (&q)[S::NV], const Pack<uint8_t, S::EV> (&key)[S::NV],
+                                        bool keyed, int K, int lane, int nb)
+    {
+        constexpr int EV = S::EV;
+#pragma unroll
+        for (int v = 0; v < S::NV; ++v) {
+            const bool in = S::inside(v, lane, K);
+            if constexpr (S::PACKED) {
+                uint32_t on[(EV + 3) / 4];  // top bit of a byte: the key takes part
+#pragma unroll
+                for (int k = 0; k < (EV + 3) / 4; ++k) {
+                    uint32_t m = 0xffffffffu;
+                    if (keyed)
+                        m = EV >= 4 ? reinterpret_cast<const uint32_t*>(&key[v])[k]
+                                    : *reinterpret_cast<const uint16_t*>(&key[v]);
+                    on[k] = ((m & 0x7f7f7f7fu) + 0x7f7f7f7fu) | m;
+                }
 #pragma unroll
                 for (int e = 0; e < EV; e += 2) {
-                    uint32_t w = in ? static_cast<uint16_t>(q[v].v[e]) |
-                                          static_cast<uint32_t>(static_cast<uint16_t>(q[v].v[e + 1])) << 16
-                                    : 0xffffffffu;
-                    if (mask && in) w |= (m.v[e] ? 0u : 0xffffu) | (m.v[e + 1] ? 0u : 0xffff0000u);
-                    const uint32_t most = static_cast<uint32_t>(nb) * 0x10001u;
-                    w = __vminu2(w, most);
-                    valid[(v * EV + e) / 2] = ~__vcmpeq2(w, most);
-                    u[v].v[e] = static_cast<uint16_t>(w);
-                    u[v].v[e + 1] = static_cast<uint16_t>(w >> 16);
+                    uint32_t w = reinterpret_cast<const uint32_t*>(&q[v])[e / 2];
+                    if (keyed)
+                        w |= ~(e % 4 ? spread_byte_bits<true>(on[e / 4]) : spread_byte_bits<false>(on[e / 4]));
+                    if (!in) w = 0xffffffffu;
+                    u[(v * EV + e) / 2] = __vminu2(w, static_cast<uint32_t>(nb) * 0x10001u);
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < EV; ++e) {
-                    int x = nb;
-                    if (in) x = static_cast<uint16_t>(q[v].v[e]);
-                    if (x > nb || (mask && in && !mask[j + e])) x = nb;
-                    u[v].v[e] = static_cast<uint16_t>(x);
-                    valid[0] |= (x < nb ? 1u : 0u) << (v * EV + e);
+                    const uint32_t x = static_cast<uint16_t>(q[v].v[e]), most = static_cast<uint32_t>(nb);
+                    u[v * EV + e] = !in || x > most || (keyed && !key[v].v[e]) ? most : x;
                 }
             }
         }
     }
 
-    // No pair is valid.
     __device__ __forceinline__ void clear(int nb)
     {
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int e = 0; e < EV; ++e) u[v].v[e] = static_cast<uint16_t>(nb);
-#pragma unroll
-        for (int w = 0; w < WORDS; ++w) valid[w] = 0;
+        for (int k = 0; k < (S::PACKED ? S::E / 2 : S::E); ++k)
+            u[k] = static_cast<uint32_t>(nb) * (S::PACKED ? 0x10001u : 1u);
     }
 
-    // Element e of vector v as binary32, 0 where the pair is masked.
-    __device__ __forceinline__ void take(float (&x)[EV], const Pack<T, EV>& q, int v) const
+    __device__ __forceinline__ int operator()(int v, int e) const
     {
-        if (PACKED) {
+        const int k = v * S::EV + e;
+        if (!S::PACKED) return static_cast<int>(u[k]);
+        return static_cast<int>(k & 1 ? u[k / 2] >> 16 : u[k / 2] & 0xffffu);
+    }
+};
+
+// Ones over the operands of valid pairs: packed like Buckets, or a word for
+// each element, or beyond eight unpacked elements a bit each.
+template <typename S>
+struct Valid {
+    static constexpr bool BITS = !S::PACKED && S::E > 8;
+    uint32_t m[S::PACKED ? S::E / 2 : BITS ? 1 : S::E];
+
+    __device__ __forceinline__ void set(const Buckets<S>& b, int nb)
+    {
+        if constexpr (S::PACKED) {
+            // nb - u is 0 in a masked half and 1 .. 1024 else: the sum carries into its top bit.
 #pragma unroll
-            for (int e = 0; e < EV; e += 2) {
-                Pack<T, 2> two{{q.v[e], q.v[e + 1]}};
-                uint32_t w = *reinterpret_cast<uint32_t*>(&two) & valid[(v * EV + e) / 2];
-                two = *reinterpret_cast<Pack<T, 2>*>(&w);
-                x[e] = to_f32(two.v[0]);
-                x[e + 1] = to_f32(two.v[1]);
+            for (int k = 0; k < S::E / 2; ++k)
+                m[k] = spread_top_bits(static_cast<uint32_t>(nb) * 0x10001u - b.u[k] + 0x7fff7fffu);
+        } else {
+            if (BITS) m[0] = 0;
+#pragma unroll
+            for (int k = 0; k < S::E; ++k) {
+                const bool ok = b.u[k] != static_cast<uint32_t>(nb);
+                if (BITS) m[0] |= (ok ? 1u : 0u) << k;
+                else m[k] = ok ? 0xffffffffu : 0u;
             }
+        }
+    }
+
+    __device__ __forceinline__ bool operator()(int v, int e) const
+    {
+        const int k = v * S::EV + e;
+        if (S::PACKED) return (m[k / 2] >> (k & 1 ? 16 : 0)) & 1u;
+        return BITS ? (m[0] >> k) & 1u : m[k] != 0;
+    }
+
+    // Vector v as binary32, 0 where the pair is masked.
+    __device__ __forceinline__ void take(float (&x)[S::EV], const Pack<typename S::T, S::EV>& q, int v) const
+    {
+        constexpr int EV = S::EV;
+        if constexpr (S::PACKED) {
+#pragma unroll
+            for (int e = 0; e < EV; e += 2)
+                unpack_two(reinterpret_cast<const uint32_t*>(&q)[e / 2] & m[(v * EV + e) / 2], x[e], x[e + 1],
+                           typename S::T{});
         } else {
 #pragma unroll
-            for (int e = 0; e < EV; ++e) x[e] = (valid[0] >> (v * EV + e)) & 1 ? to_f32(q.v[e]) : 0.0f;
+            for (int e = 0; e < EV; ++e) {
+                const int k = v * EV + e;
+                if (BITS) x[e] = (m[0] >> k) & 1u ? to_f32(q.v[e]) : 0.0f;
+                else x[e] = of_bits(bits_of(q.v[e]) & m[k], typename S::T{});
+            }
         }
     }
 };
 
 // ----------------------------------------------------------------- forward
 
-template <typename T, int EV, int L, int E, bool BY_IMAGE>
-__global__ void __launch_bounds__(256, E == 32 ? 2 : E == 16 ? 3 : 4)
+template <typename S, bool BY_IMAGE>
+__global__ void __launch_bounds__(256, S::BLOCKS)
 relation_softmax_kernel(RelationArgs a, int per)
 {
-    constexpr int NV = E / EV;
-    extern __shared__ float tab[];  // by head: [heads of the chunk][num_buckets + 1]
+    using T = typename S::T;
+    constexpr int EV = S::EV, NV = S::NV, L = S::L;
+    extern __shared__ float tab[];  // by head: [heads of the chunk][num_buckets + 1], -inf last
     __shared__ float red[4][8];
     const int K = static_cast<int>(a.keys), nb = a.num_buckets, H = a.heads;
     const int lane = static_cast<int>(threadIdx.x) % L;
-    const int64_t inner = BY_IMAGE ? a.batch : H;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * per, t1 = t0 + per < inner ? t0 + per : inner;
+    const int inner = static_cast<int>(BY_IMAGE ? a.batch : H);
+    const int t0 = static_cast<int>(blockIdx.y) * per, t1 = t0 + per < inner ? t0 + per : inner;
     if (!BY_IMAGE) {
-        for (int x = threadIdx.x; x < static_cast<int>(t1 - t0) * (nb + 1); x += 256) {
+        for (int x = threadIdx.x; x < (t1 - t0) * (nb + 1); x += 256) {
             const int h = x / (nb + 1), u = x % (nb + 1);
             tab[x] = u < nb ? a.table[static_cast<int64_t>(u) * H + t0 + h] : -INFINITY;
         }
         __syncthreads();
     }
-    const int64_t anchors = (BY_IMAGE ? H : a.batch) * a.queries;
-    const int64_t want = static_cast<int64_t>(blockIdx.x) * (256 / L) + threadIdx.x / L;
+    const unsigned Q = static_cast<unsigned>(a.queries);
+    const unsigned anchors = static_cast<unsigned>(BY_IMAGE ? H : a.batch) * Q;
+    const unsigned want = blockIdx.x * (256 / L) + threadIdx.x / L;
     const bool real = want < anchors;  // a team without a row follows another one and stores nothing
-    const int64_t anchor = real ? want : anchors - 1, i = anchor % a.queries, outer = anchor / a.queries;
+    const unsigned anchor = real ? want : anchors - 1, outer = anchor / Q, i = anchor % Q;
     // Rows of the inner index t: first + t * step.
-    const int64_t step = (BY_IMAGE ? H * a.queries : a.queries) * K;
-    const int64_t first = (BY_IMAGE ? anchor : outer * H * a.queries + i) * K;
+    const int64_t step = (BY_IMAGE ? static_cast<int64_t>(H) * Q : static_cast<int64_t>(Q)) * K;
+    const int64_t first = (BY_IMAGE ? static_cast<int64_t>(anchor) : static_cast<int64_t>(outer) * H * Q + i) * K;
     const T* s = static_cast<const T*>(a.scores) + first + t0 * step;
     T* p = static_cast<T*>(a.out) + first + t0 * step;
     Pack<T, EV> next[NV];
-    load_vectors<T, EV, L>(next, s, K, lane);
-    Pairs<T, EV, NV> pairs;
-    float bias[BY_IMAGE ? E : 1];
+    S::load(next, s, K, lane);
+    Buckets<S> bucket;
+    float bias[BY_IMAGE ? S::E : 1];
     {
         Pack<int16_t, EV> q[NV];
-        load_vectors<int16_t, EV, L>(q, a.buckets + ((a.sets == 1 ? 0 : outer) * a.queries + i) * K, K, lane);
-        pairs.template set<L>(q, !BY_IMAGE && a.key_mask ? a.key_mask + outer * K : nullptr, K, lane, nb);
+        Pack<uint8_t, EV> key[NV];
+        S::load(q, a.buckets + (static_cast<int64_t>(a.sets == 1 ? 0 : outer) * Q + i) * K, K, lane);
+        const bool keyed = !BY_IMAGE && a.key_mask;
+        if (keyed) S::load(key, a.key_mask + static_cast<int64_t>(outer) * K, K, lane);
+        bucket.set(q, key, keyed, K, lane, nb);
     }
     if (BY_IMAGE) {
 #pragma unroll
-        for (int x = 0; x < E; ++x) {
-            const int u = pairs.u[x / EV].v[x % EV];
-            bias[x] = u < nb ? a.table[static_cast<int64_t>(u) * H + outer] : -INFINITY;
-        }
-    }
-    const float* row_tab = tab;
-    for (int64_t t = t0; t < t1; ++t) {
-        Pack<T, EV> cur[NV];
-#pragma unroll
-        for (int v = 0; v < NV; ++v) cur[v] = next[v];
-        s += step;
-        if (t + 1 < t1) load_vectors<T, EV, L>(next, s, K, lane);
-        float x[NV][EV];
-        float top = -INFINITY;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            if (v * L * EV >= K) break;
-            pairs.take(x[v], cur[v], v);
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int e = 0; e < EV; ++e) {
-                // A masked pair: 0 * scale - inf.
-                x[v][e] = fmaf(x[v][e], a.scale, BY_IMAGE ? bias[v * EV + e] : row_tab[pairs.u[v].v[e]]);
+                const int u = bucket(v, e);
+                bias[v * EV + e] = u < nb ? a.table[static_cast<int64_t>(u) * H + outer] : -INFINITY;
+            }
+    }
+    const float* row_tab = tab;
+    for (int t = t0; t < t1; ++t) {
+        float x[NV][EV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) S::widen(x[v], next[v]);
+        s += step;
+        if (t + 1 < t1) S::load(next, s, K, lane);
+        // A masked pair's logit is -inf, or NaN if its score is NaN or infinite; the maximum passes over both.
+        float top = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < EV; ++e) {
+                x[v][e] = fmaf(x[v][e], a.scale, BY_IMAGE ? bias[v * EV + e] : row_tab[bucket(v, e)]);
                 top = fmaxf(top, x[v][e]);
             }
-        }
         top = team_reduce<L, true>(top, red[t & 1]);
         const float base = top == -INFINITY ? 0.0f : top;
         float sum = 0.0f;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            if (v * L * EV >= K) break;
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int e = 0; e < EV; ++e) {
                 x[v][e] = exp2_fast((x[v][e] - base) * LOG2E);
                 sum += x[v][e];
             }
-        }
         sum = team_reduce<L, false>(sum, red[2 + (t & 1)]);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        float inv = sum == 0.0f ? 0.0f : reciprocal(sum);
+        if (__any_sync(FULL, inv != inv)) {  // a NaN or +inf, perhaps of masked pairs alone: once more without those
+            if (L > 32) __syncthreads();     // red is still being read
+            sum = 0.0f;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int j = (v * L + lane) * EV;
-            if (v * L * EV >= K) break;
-            Pack<T, EV> q;
+            for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int e = 0; e < EV; ++e) q.v[e] = from_f32<T>(x[v][e] * inv);
-            if (inv != inv) {  // a row that met an infinity or NaN leaves its masked places 0 all the same
+                for (int e = 0; e < EV; ++e) {
+                    if ((BY_IMAGE ? bias[v * EV + e] : row_tab[bucket(v, e)]) == -INFINITY) x[v][e] = 0.0f;
+                    sum += x[v][e];
+                }
+            sum = team_reduce<L, false>(sum, red[2 + (t & 1)]);
+            inv = sum == 0.0f ? 0.0f : reciprocal(sum);
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
 #pragma unroll
                 for (int e = 0; e < EV; ++e)
-                    if (pairs.u[v].v[e] == nb) q.v[e] = from_f32<T>(0.0f);
-            }
-            if (j < K && real) *reinterpret_cast<Pack<T, EV>*>(p + j) = q;
+                    x[v][e] = (BY_IMAGE ? bias[v * EV + e] : row_tab[bucket(v, e)]) == -INFINITY ? 0.0f : x[v][e] * inv;
+            inv = 1.0f;
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+#pragma unroll
+            for (int e = 0; e < EV; ++e) x[v][e] *= inv;
+            if (real && S::inside(v, lane, K))
+                *reinterpret_cast<Pack<T, EV>*>(p + S::first(v, lane)) = pack_results<T, EV>(x[v]);
         }
         p += step;
         row_tab += nb + 1;
@@ -263,8 +411,9 @@ relation_softmax_long_kernel(RelationArgs a, int64_t rows)
         auto logit = [&](int64_t j, float& x) {
             const int u = static_cast<uint16_t>(map[j]);
             if (u >= a.num_buckets || (mask && !mask[j])) return false;
-            x = fmaf(to_f32(s[j]), a.scale, a.table[static_cast<int64_t>(u) * a.heads + head]);
-            return true;
+            const float bias = a.table[static_cast<int64_t>(u) * a.heads + head];
+            x = fmaf(to_f32(s[j]), a.scale, bias);
+            return bias != -INFINITY;
         };
         float top = -INFINITY, sum = 0.0f, x;
         for (int64_t j = threadIdx.x; j < a.keys; j += 256) {
@@ -330,74 +479,89 @@ __device__ __forceinline__ void join_columns(const float* hist, int lists, int c
 }
 
 // One row: da into x (binary32) from the packed operands, dscores stored.
-template <typename T, int EV, int L, int NV>
-__device__ __forceinline__ void grad_row(float (&x)[NV][EV], const Pack<T, EV> (&pq)[NV], const Pack<T, EV> (&dq)[NV],
-                                         const Pairs<T, EV, NV>& pairs, const RelationArgs& a, T* ds, int lane,
-                                         bool store, float* red)
+template <typename S>
+__device__ __forceinline__ void grad_row(float (&x)[S::NV][S::EV], const Pack<typename S::T, S::EV> (&pq)[S::NV],
+                                         const Pack<typename S::T, S::EV> (&dq)[S::NV], const Valid<S>& valid,
+                                         float scale, typename S::T* ds, int K, int lane, bool store, float* red)
 {
-    const int K = static_cast<int>(a.keys);
+    constexpr int EV = S::EV, NV = S::NV;
     float dot = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        if (v * L * EV >= K) break;
         float p[EV], d[EV];
-        pairs.take(p, pq[v], v);
-        pairs.take(d, dq[v], v);
+        valid.take(p, pq[v], v);
+        valid.take(d, dq[v], v);
 #pragma unroll
         for (int e = 0; e < EV; ++e) dot = fmaf(p[e], d[e], dot);
     }
-    dot = team_reduce<L, false>(dot, red);
+    dot = team_reduce<S::L, false>(dot, red);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int j = (v * L + lane) * EV;
-        if (v * L * EV >= K) break;
         float p[EV], d[EV];
-        pairs.take(p, pq[v], v);
-        pairs.take(d, dq[v], v);
-        Pack<T, EV> q;
+        valid.take(p, pq[v], v);
+        valid.take(d, dq[v], v);
 #pragma unroll
-        for (int e = 0; e < EV; ++e) {
-            x[v][e] = p[e] * (d[e] - dot);
-            // A row that met an infinity or NaN leaves its masked places 0 all the same.
-            if (!(fabsf(dot) < INFINITY) && pairs.u[v].v[e] == a.num_buckets) x[v][e] = 0.0f;
-            q.v[e] = from_f32<T>(a.scale * x[v][e]);
-        }
-        if (store && j < K) *reinterpret_cast<Pack<T, EV>*>(ds + j) = q;
+        for (int e = 0; e < EV; ++e) x[v][e] = p[e] * (d[e] - dot);
+    }
+    if (__any_sync(FULL, !(fabsf(dot) < INFINITY))) {
+        // A row that met an infinity or NaN leaves its masked places 0 all the same.
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < EV; ++e)
+                if (!valid(v, e)) x[v][e] = 0.0f;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        float y[EV];
+#pragma unroll
+        for (int e = 0; e < EV; ++e) y[e] = scale * x[v][e];
+        if (store && S::inside(v, lane, K))
+            *reinterpret_cast<Pack<typename S::T, EV>*>(ds + S::first(v, lane)) = pack_results<typename S::T, EV>(y);
     }
 }
 
 // By image: block (x, y, z) = (query tile, image chunk, head).
-template <typename T, int EV, int L, int E>
-__global__ void __launch_bounds__(256)
+template <typename S>
+__global__ void __launch_bounds__(256, S::GRAD_BLOCKS)
 relation_grad_image_kernel(RelationArgs a, int per, int columns, float* part)
 {
-    constexpr int NV = E / EV;
+    using T = typename S::T;
+    constexpr int EV = S::EV, NV = S::NV, L = S::L;
     extern __shared__ float hist[];  // [num_buckets + 1][columns]
     __shared__ float red[2][8];
     const int K = static_cast<int>(a.keys), nb = a.num_buckets, head = static_cast<int>(blockIdx.z);
     const int lane = static_cast<int>(threadIdx.x) % L;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * per, t1 = t0 + per < a.batch ? t0 + per : a.batch;
-    for (int x = threadIdx.x; x < (nb + 1) * columns; x += blockDim.x) hist[x] = 0.0f;
-    const int64_t want = static_cast<int64_t>(blockIdx.x) * (blockDim.x / L) + threadIdx.x / L;
-    const bool real = want < a.queries;
-    const int64_t i = real ? want : a.queries - 1;
-    const int64_t step = a.heads * a.queries * K, first = (head * a.queries + i) * K + t0 * step;
+    const int batch = static_cast<int>(a.batch);
+    const int t0 = static_cast<int>(blockIdx.y) * per, t1 = t0 + per < batch ? t0 + per : batch;
+    for (int x = threadIdx.x; x < (nb + 1) * columns; x += 256) hist[x] = 0.0f;
+    const unsigned Q = static_cast<unsigned>(a.queries), want = blockIdx.x * (256 / L) + threadIdx.x / L;
+    const bool real = want < Q;
+    const int64_t i = real ? want : Q - 1;
+    const int64_t step = static_cast<int64_t>(a.heads) * Q * K;
+    const int64_t first = (static_cast<int64_t>(head) * Q + i) * K + t0 * step;
     const T* p = static_cast<const T*>(a.probs) + first;
     const T* dp = static_cast<const T*>(a.scores) + first;
     T* ds = static_cast<T*>(a.out) + first;
     Pack<T, EV> pn[NV], dn[NV];
-    load_vectors<T, EV, L>(pn, p, K, lane);
-    load_vectors<T, EV, L>(dn, dp, K, lane);
-    Pairs<T, EV, NV> pairs;
-    {
+    S::load(pn, p, K, lane);
+    S::load(dn, dp, K, lane);
+    Buckets<S> bucket;
+    Valid<S> valid;
+    auto map = [&]() {
         Pack<int16_t, EV> q[NV];
-        load_vectors<int16_t, EV, L>(q, a.buckets + i * K, K, lane);
-        pairs.template set<L>(q, nullptr, K, lane, nb);
-    }
+        Pack<uint8_t, EV> key[NV];
+        S::load(q, a.buckets + i * K, K, lane);
+        bucket.set(q, key, false, K, lane, nb);
+    };
+    map();
+    valid.set(bucket, nb);
     float acc[NV][EV];
 #pragma unroll
-    for (int k = 0; k < E; ++k) acc[k / EV][k % EV] = 0.0f;
-    for (int64_t t = t0; t < t1; ++t) {
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < EV; ++e) acc[v][e] = 0.0f;
+    for (int t = t0; t < t1; ++t) {
         Pack<T, EV> pq[NV], dq[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -407,29 +571,27 @@ relation_grad_image_kernel(RelationArgs a, int per, int columns, float* part)
         p += step;
         dp += step;
         if (t + 1 < t1) {
-            load_vectors<T, EV, L>(pn, p, K, lane);
-            load_vectors<T, EV, L>(dn, dp, K, lane);
+            S::load(pn, p, K, lane);
+            S::load(dn, dp, K, lane);
         }
         float x[NV][EV];
-        grad_row<T, EV, L, NV>(x, pq, dq, pairs, a, ds, lane, real, red[t & 1]);
+        grad_row<S>(x, pq, dq, valid, a.scale, ds, K, lane, real, red[t & 1]);
         ds += step;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            if (v * L * EV >= K) break;
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int e = 0; e < EV; ++e) acc[v][e] += x[v][e];
-        }
     }
-    // The warps add their sums in turn.
-    for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) {
+    // The warps add their sums in turn (the map is read again: its indices need not live through the loop).
+    map();
+    if (!real) bucket.clear(nb);
+    for (int w = 0; w < 8; ++w) {
         __syncthreads();
         if (static_cast<int>(threadIdx.x) / 32 == w) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                if (v * L * EV >= K) break;
+            for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int e = 0; e < EV; ++e) add_in_turn(hist, real ? pairs.u[v].v[e] : nb, acc[v][e], columns);
-            }
+                for (int e = 0; e < EV; ++e) add_in_turn(hist, bucket(v, e), acc[v][e], columns);
         }
     }
     join_columns(hist, 1, columns, nb,
@@ -437,12 +599,13 @@ relation_grad_image_kernel(RelationArgs a, int per, int columns, float* part)
 }
 
 // By head: block (x, y) = (share of the rows, head); each warp has a table of
-// its own.
-template <typename T, int EV, int L, int E>
+// its own, of 32 columns (WIDE) or fewer.
+template <typename S, bool WIDE>
 __global__ void __launch_bounds__(256)
 relation_grad_head_kernel(RelationArgs a, int columns, float* part)
 {
-    constexpr int NV = E / EV;
+    using T = typename S::T;
+    constexpr int EV = S::EV, NV = S::NV, L = S::L;
     extern __shared__ float hist[];  // [warps][num_buckets + 1][columns]
     __shared__ float red[2][8];
     const int K = static_cast<int>(a.keys), nb = a.num_buckets, head = static_cast<int>(blockIdx.y);
@@ -460,23 +623,26 @@ relation_grad_head_kernel(RelationArgs a, int columns, float* part)
     unsigned b = (bi + team) / Q, i = (bi + team) % Q;
     Pack<T, EV> pn[NV], dn[NV];
     Pack<int16_t, EV> un[NV];
+    Pack<uint8_t, EV> kn[NV];
     int64_t off_next = 0;
-    const uint8_t* mask_next = nullptr;
-    auto fetch = [&](bool real) {  // a team without a row reads the block's first ones and stores nothing
+    const bool keyed = a.key_mask != nullptr;
+    auto fetch = [&](bool real) {  // a team without a row reads the first one and stores nothing
         const int64_t fb = real ? b : 0, fi = real ? i : 0;
         off_next = ((fb * a.heads + head) * Q + fi) * K;
-        mask_next = a.key_mask ? a.key_mask + fb * K : nullptr;
-        load_vectors<T, EV, L>(pn, static_cast<const T*>(a.probs) + off_next, K, lane);
-        load_vectors<T, EV, L>(dn, static_cast<const T*>(a.scores) + off_next, K, lane);
-        load_vectors<int16_t, EV, L>(un, a.buckets + ((a.sets == 1 ? 0 : fb * Q) + fi) * K, K, lane);
+        S::load(pn, static_cast<const T*>(a.probs) + off_next, K, lane);
+        S::load(dn, static_cast<const T*>(a.scores) + off_next, K, lane);
+        S::load(un, a.buckets + ((a.sets == 1 ? 0 : fb * Q) + fi) * K, K, lane);
+        if (keyed) S::load(kn, a.key_mask + fb * K, K, lane);
     };
     if (bi < rows) fetch(bi + team < rows);
     for (int turn = 0; bi < rows; turn ^= 1) {
         const bool real = bi + team < rows;
-        const int64_t off = off_next;
-        Pairs<T, EV, NV> pairs;
-        pairs.template set<L>(un, mask_next, K, lane, nb);
-        if (!real) pairs.clear(nb);
+        T* ds = static_cast<T*>(a.out) + off_next;
+        Buckets<S> bucket;
+        Valid<S> valid;
+        bucket.set(un, kn, keyed, K, lane, nb);
+        if (!real) bucket.clear(nb);
+        valid.set(bucket, nb);
         Pack<T, EV> pq[NV], dq[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -492,28 +658,19 @@ relation_grad_head_kernel(RelationArgs a, int columns, float* part)
         }
         if (bi < rows) fetch(bi + team < rows);
         float x[NV][EV];
-        grad_row<T, EV, L, NV>(x, pq, dq, pairs, a, static_cast<T*>(a.out) + off, lane, real, red[turn]);
+        grad_row<S>(x, pq, dq, valid, a.scale, ds, K, lane, real, red[turn]);
+        if (WIDE) {
+            float* column = mine + lane_id();
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            if (v * L * EV >= K) break;
-            if (columns == 32) {
-                float* column = mine + lane_id();
-                if (EV == 1) {
-                    if (v & 1) continue;
-                    if (v + 1 < NV && (v + 1) * L < K)
-                        add_two(column, pairs.u[v].v[0], x[v][0], pairs.u[v + 1 < NV ? v + 1 : v].v[0],
-                                x[v + 1 < NV ? v + 1 : v][0]);
-                    else
-                        column[pairs.u[v].v[0] * 32] += x[v][0];
-                } else {
+            for (int k = 0; k + 1 < S::E; k += 2)
+                add_two(column, bucket(k / EV, k % EV), x[k / EV][k % EV], bucket((k + 1) / EV, (k + 1) % EV),
+                        x[(k + 1) / EV][(k + 1) % EV]);
+            if (S::E % 2) column[bucket(NV - 1, EV - 1) * 32] += x[NV - 1][EV - 1];
+        } else {
 #pragma unroll
-                    for (int e = 0; e + 1 < EV; e += 2)
-                        add_two(column, pairs.u[v].v[e], x[v][e], pairs.u[v].v[e + 1], x[v][e + 1]);
-                }
-            } else {
+            for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int e = 0; e < EV; ++e) add_in_turn(mine, pairs.u[v].v[e], x[v][e], columns);
-            }
+                for (int e = 0; e < EV; ++e) add_in_turn(mine, bucket(v, e), x[v][e], columns);
         }
     }
     join_columns(hist, warps, columns, nb, part + (static_cast<int64_t>(head) * gridDim.x + blockIdx.x) * nb);
@@ -564,62 +721,88 @@ inline int relation_vector(const RelationArgs& a, int most)
 {
     auto fits = [&](const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
     const int e = a.type == NMS_TYPE_F32 ? 4 : 2;
-    for (int v = most; v > 1; v = v == 8 ? 2 : 1)
+    for (int v = most; v > 1; v /= 2)
         if (a.keys % v == 0 && fits(a.scores, v * e) && fits(a.probs, v * e) && fits(a.out, v * e) &&
             fits(a.buckets, v * 2) && (!a.key_mask || fits(a.key_mask, v)))
             return v;
     return 1;
 }
 
-// f(EV, L, E as integral constants) for the row's shape.
+// f(Shape) with the first of the vector counts NV that holds the row; each
+// count serves the rows that the one before does not.
+template <typename T, int EV, int L, int PREV, typename F>
+inline void pick_count(const RelationArgs&, F) {}
+
+template <typename T, int EV, int L, int PREV, int NV, int... MORE, typename F>
+inline void pick_count(const RelationArgs& a, F f)
+{
+    if (a.keys <= NV * L * EV || sizeof...(MORE) == 0) f(Shape<T, EV, L, NV, NV - PREV>{});
+    else pick_count<T, EV, L, NV, MORE...>(a, f);
+}
+
+// f(Shape) for the row's length and vector width.  Eight lanes a row up to 64
+// keys, 16 up to 128, a warp up to 1024, a block up to 8192.
 template <typename T, typename F>
 inline void relation_shape(const RelationArgs& a, F f)
 {
     constexpr int MOST = sizeof(T) == 2 ? 8 : 4;
-    auto shape = [&](auto ev) {
-        using std::integral_constant;
-        if (a.keys <= 64) f(ev, integral_constant<int, 8>{}, integral_constant<int, 8>{});
-        else if (a.keys <= 128) f(ev, integral_constant<int, 16>{}, integral_constant<int, 8>{});
-        else if (a.keys <= 256) f(ev, integral_constant<int, 32>{}, integral_constant<int, 8>{});
-        else if (a.keys <= 512) f(ev, integral_constant<int, 32>{}, integral_constant<int, 16>{});
-        else if (a.keys <= 1024) f(ev, integral_constant<int, 32>{}, integral_constant<int, 32>{});
-        else f(ev, integral_constant<int, 256>{}, integral_constant<int, 32>{});
-    };
     const int v = relation_vector(a, MOST);
-    if (v == MOST) shape(std::integral_constant<int, MOST>{});
-    else if (v == 2) shape(std::integral_constant<int, 2>{});
-    else shape(std::integral_constant<int, 1>{});
+    const int64_t K = a.keys;
+    if (v == 8) {
+        if constexpr (MOST == 8) {
+            if (K <= 64) pick_count<T, 8, 8, 0, 1>(a, f);
+            else if (K <= 128) pick_count<T, 8, 16, 0, 1>(a, f);
+            else if (K <= 1024) pick_count<T, 8, 32, 0, 1, 2, 3, 4>(a, f);
+            else pick_count<T, 8, 256, 0, 1, 2, 4>(a, f);
+        }
+    } else if (v == 4) {
+        if (K <= 64) pick_count<T, 4, 8, 0, 1, 2>(a, f);
+        else if (K <= 128) pick_count<T, 4, 16, 1, 2>(a, f);
+        else if (K <= 1024) pick_count<T, 4, 32, 1, 2, 3, 4, 6, 8>(a, f);
+        else pick_count<T, 4, 256, 1, 2, 4, 8>(a, f);
+    } else if (v == 2) {
+        if (K <= 64) pick_count<T, 2, 8, 0, 1, 2, 3, 4>(a, f);
+        else if (K <= 128) pick_count<T, 2, 16, 2, 4>(a, f);
+        else if (K <= 1024) pick_count<T, 2, 32, 2, 4, 8, 12, 16>(a, f);
+        else pick_count<T, 2, 256, 2, 8, 16>(a, f);
+    } else {
+        if (K <= 64) pick_count<T, 1, 8, 0, 1, 2, 4, 6, 7, 8>(a, f);
+        else if (K <= 128) pick_count<T, 1, 16, 4, 6, 8>(a, f);
+        else if (K <= 1024) pick_count<T, 1, 32, 4, 6, 8, 12, 16, 24, 32>(a, f);
+        else pick_count<T, 1, 256, 4, 8, 16, 32>(a, f);
+    }
 }
+
+constexpr int64_t blocks_over(int64_t n, int64_t each) { return (n + each - 1) / each; }
 
 template <typename T>
 inline void softmax_type(const RelationArgs& a, cudaStream_t st)
 {
     if (a.keys > RELATION_MOST) {
         const int64_t rows = a.batch * a.heads * a.queries;
-        relation_softmax_long_kernel<T><<<static_cast<unsigned>(rows < 152 * 8 ? rows : 152 * 8), 256, 0, st>>>(a, rows);
+        relation_softmax_long_kernel<T><<<static_cast<unsigned>(rows < SMS * 8 ? rows : SMS * 8), 256, 0, st>>>(a, rows);
         return;
     }
-    relation_shape<T>(a, [&](auto ev, auto l, auto e) {
-        constexpr int EV = decltype(ev)::value, L = decltype(l)::value, E = decltype(e)::value;
+    relation_shape<T>(a, [&](auto shape) {
+        using S = decltype(shape);
         const bool image = relation_by_image(a);
         const int64_t anchors = (image ? a.heads : a.batch) * a.queries, inner = image ? a.batch : a.heads;
-        const int64_t blocks = (anchors + 256 / L - 1) / (256 / L);
-        // Chunks of the inner index: enough blocks for every SM eight times over.
-        int64_t chunks = (152 * 8 + blocks - 1) / blocks;
+        const int64_t blocks = blocks_over(anchors, 256 / S::L);
+        // Chunks of the inner index: one wave of resident blocks.
+        int64_t chunks = SMS * S::BLOCKS / blocks;
+        if (chunks < 1) chunks = 1;
         if (chunks > inner) chunks = inner;
         if (!image) {  // the chunk's tables have to fit
-            const int64_t most = 96 * 1024 / (4 * (a.num_buckets + 1));
-            if (chunks < (inner + most - 1) / most) chunks = (inner + most - 1) / most;
+            const int64_t most = 40 * 1024 / (4 * (a.num_buckets + 1));
+            if (chunks < blocks_over(inner, most)) chunks = blocks_over(inner, most);
         }
-        if (chunks > 65535) chunks = 65535;
-        const int per = static_cast<int>((inner + chunks - 1) / chunks);
-        const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((inner + per - 1) / per));
+        const int per = static_cast<int>(blocks_over(inner, chunks));
+        const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(blocks_over(inner, per)));
         if (image) {
-            relation_softmax_kernel<T, EV, L, E, true><<<grid, 256, 0, st>>>(a, per);
+            relation_softmax_kernel<S, true><<<grid, 256, 0, st>>>(a, per);
         } else {
             const size_t smem = 4 * static_cast<size_t>(per) * (a.num_buckets + 1);
-            ensure_dynamic_smem(reinterpret_cast<const void*>(relation_softmax_kernel<T, EV, L, E, false>), smem);
-            relation_softmax_kernel<T, EV, L, E, false><<<grid, 256, smem, st>>>(a, per);
+            relation_softmax_kernel<S, false><<<grid, 256, smem, st>>>(a, per);
         }
     });
 }
@@ -636,15 +819,14 @@ inline void grad_type(const RelationArgs& a, float* part, cudaStream_t st)
                                        st>>>(a, p.columns, part);
         return;
     }
-    relation_shape<T>(a, [&](auto ev, auto l, auto e) {
-        constexpr int EV = decltype(ev)::value, L = decltype(l)::value, E = decltype(e)::value;
+    relation_shape<T>(a, [&](auto shape) {
+        using S = decltype(shape);
         if (image) {
-            auto* k = relation_grad_image_kernel<T, EV, L, E>;
-            ensure_dynamic_smem(reinterpret_cast<const void*>(k), table);
-            k<<<dim3(static_cast<unsigned>(p.blocks), static_cast<unsigned>(p.chunks), a.heads), p.warps * 32, table,
-                st>>>(a, static_cast<int>(p.per), p.columns, part);
+            relation_grad_image_kernel<S><<<dim3(static_cast<unsigned>(p.blocks), static_cast<unsigned>(p.chunks),
+                                                 a.heads), 256, table, st>>>(a, static_cast<int>(p.per), p.columns,
+                                                                             part);
         } else {
-            auto* k = relation_grad_head_kernel<T, EV, L, E>;
+            auto* k = p.columns == 32 ? relation_grad_head_kernel<S, true> : relation_grad_head_kernel<S, false>;
             ensure_dynamic_smem(reinterpret_cast<const void*>(k), table * p.warps);
             k<<<dim3(static_cast<unsigned>(p.blocks), a.heads), p.warps * 32, table * p.warps, st>>>(a, p.columns,
                                                                                                     part);
