@@ -85,27 +85,85 @@ __device__ __forceinline__ void drop(float (&v)[V], uint64_t first, const DropAr
 }
 
 // ---------------------------------------------------------------- activation
+//
+// The hardware's 2^x and 1/x (each right to about 2^-22 of its result) carry
+// the sigmoid and the normal distribution; the error is of the size of
+// binary32's own in the argument and far below that of 16-bit results.
 
-template <int ACT>
-__device__ __forceinline__ float act_value(float z)
+__device__ __forceinline__ float exp2_fast(float x)
 {
-    if (ACT == NMS_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
-    if (ACT == NMS_ACT_SILU) return z / (1.0f + expf(-z));
-    if (ACT == NMS_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    return z;
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-template <int ACT>
-__device__ __forceinline__ float act_slope(float z)
+__device__ __forceinline__ float reciprocal(float x)
 {
-    if (ACT == NMS_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    if (ACT == NMS_ACT_SILU) {
-        const float r = 1.0f / (1.0f + expf(-z));
-        return r * fmaf(z, 1.0f - r, 1.0f);
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float LOG2E = 1.44269504f;
+
+__device__ __forceinline__ float sigmoid(float z) { return reciprocal(1.0f + exp2_fast(-LOG2E * z)); }
+
+// The normal distribution function and e^(-z^2 / 2): Hastings' rational
+// approximation of erf (Abramowitz and Stegun 7.1.26, absolute error 1.5e-7),
+// whose factor e^(-x^2) at x = z / sqrt 2 is that exponential.
+__device__ __forceinline__ float normal_cdf(float z, float& bell)
+{
+    const float x = fabsf(z) * 0.70710678f;
+    bell = exp2_fast(-0.5f * LOG2E * z * z);
+    const float t = reciprocal(fmaf(0.3275911f, x, 1.0f));
+    float q = fmaf(1.061405429f, t, -1.453152027f);
+    q = fmaf(q, t, 1.421413741f);
+    q = fmaf(q, t, -0.284496736f);
+    q = fmaf(q, t, 0.254829592f);
+    const float tail = 0.5f * q * t * bell;  // beyond |z|
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+
+// v = act(v), one uniform branch for V elements.
+template <int V>
+__device__ __forceinline__ void act_values(float (&v)[V], int act)
+{
+    if (act == NMS_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] *= sigmoid(v[i]);
+    } else if (act == NMS_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
+    } else if (act == NMS_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float bell;
+            v[i] *= normal_cdf(v[i], bell);
+        }
     }
-    if (ACT == NMS_ACT_GELU)
-        return fmaf(0.39894228f * z, expf(-0.5f * z * z), 0.5f * (1.0f + erff(z * 0.70710678f)));
-    return 1.0f;
+}
+
+// d *= act'(z).
+template <int V>
+__device__ __forceinline__ void act_slopes(float (&d)[V], const float (&z)[V], int act)
+{
+    if (act == NMS_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float r = sigmoid(z[i]);
+            d[i] *= r * fmaf(z[i], 1.0f - r, 1.0f);
+        }
+    } else if (act == NMS_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = z[i] > 0.0f ? d[i] : 0.0f;
+    } else if (act == NMS_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float bell;
+            const float cdf = normal_cdf(z[i], bell);
+            d[i] *= fmaf(0.39894228f * z[i], bell, cdf);
+        }
+    }
 }
 
 // ----------------------------------------------------------------- reductions

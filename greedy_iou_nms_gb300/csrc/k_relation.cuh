@@ -31,16 +31,7 @@
 
 namespace gbnms {
 
-constexpr float LOG2E = 1.44269504f;
-
-// 2^x with results below the smallest normal number flushed to zero: such a
-// weight is under 2^-126.
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
+// A weight below 2^-126 is flushed to zero (exp2_fast).
 
 // Reduction over a team.  L <= 32: neighbouring lanes of a warp; L = 256: the
 // block, by way of s (8 floats; alternate between two of them).
@@ -60,13 +51,6 @@ __device__ __forceinline__ float team_reduce(float v, float* s)
         for (int k = 1; k < L / 32; ++k) v = MAX ? fmaxf(v, s[k]) : v + s[k];
     }
     return v;
-}
-
-__device__ __forceinline__ float reciprocal(float x)
-{
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // 0xffff in each half (byte pair) of x whose top bit is set.
