@@ -29,6 +29,34 @@ template <> __device__ __forceinline__ float from_f32<float>(float x) { return x
 template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+template <typename T> __device__ __forceinline__ uint32_t pack_two(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack_two<__half>(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack_two<__nv_bfloat16>(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack_two<float>(float, float) { return 0; }  // never called
+
+// Rounds EV results to their type.
+template <typename T, int EV>
+__device__ __forceinline__ Pack<T, EV> pack_results(const float (&x)[EV])
+{
+    Pack<T, EV> q;
+    if constexpr (sizeof(T) == 2 && EV % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < EV; e += 2) reinterpret_cast<uint32_t*>(&q)[e / 2] = pack_two<T>(x[e], x[e + 1]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < EV; ++e) q.v[e] = from_f32<T>(x[e]);
+    }
+    return q;
+}
+
 // A norm parameter: binary32, or the type of the features.
 template <typename T>
 __device__ __forceinline__ float load_param(const void* p, int is_f32, int64_t i)
@@ -61,27 +89,39 @@ __device__ __forceinline__ uint4 philox(uint64_t block, const DropArgs& d)
     return make_uint4(c0, c1, c2, c3);
 }
 
-__device__ __forceinline__ uint32_t philox_field(const uint4& w, int i)
+// v[i] = 0 for the dropped of the elements first .. first + V - 1 (first a
+// multiple of V, so they lie in one block), whatever their value was; the
+// caller applies the factor.  A field is compared in the top half of a word.
+template <int V>
+__device__ __forceinline__ void drop_mask(float (&v)[V], uint64_t first, const DropArgs& d)
 {
-    const uint32_t x = i < 4 ? (i < 2 ? w.x : w.y) : (i < 6 ? w.z : w.w);
-    return (i & 1) ? x >> 16 : x & 0xffffu;
+    const uint4 w = philox(first >> 3, d);
+    const uint32_t limit = d.limit << 16;
+    if (V == 8) {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = (i & 1 ? x[i / 2] : x[i / 2] << 16) < limit ? v[i] : 0.0f;
+    } else {
+        // The parts of a block one after another: from word at / 2 on, and within it from field at % 2 on.
+        const int at = static_cast<int>(first & 7);
+        uint32_t x0 = at < 4 ? w.x : w.z, x1 = at < 4 ? w.y : w.w;
+        if (V < 4 && (at & 2)) x0 = x1;
+        if (V < 2 && (at & 1)) x0 = x0 & 0xffff0000u;
+        else if (V < 2) x0 <<= 16;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t word = i < 2 ? x0 : x1;
+            v[i] = (V < 2 ? word : i & 1 ? word : word << 16) < limit ? v[i] : 0.0f;
+        }
+    }
 }
 
-// v[0..V) *= mask / keep for the elements first .. first + V - 1 (first a
-// multiple of V, so they lie in one block).  A dropped element is 0 whatever
-// its value was.
 template <int V>
 __device__ __forceinline__ void drop(float (&v)[V], uint64_t first, const DropArgs& d)
 {
-    const uint4 w = philox(first >> 3, d);
-    if (V == 8) {
+    drop_mask<V>(v, first, d);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = philox_field(w, i) < d.limit ? v[i] * d.factor : 0.0f;
-    } else {
-        const int at = static_cast<int>(first & 7);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = philox_field(w, at + i) < d.limit ? v[i] * d.factor : 0.0f;
-    }
+    for (int i = 0; i < V; ++i) v[i] *= d.factor;
 }
 
 // ---------------------------------------------------------------- activation
@@ -108,19 +148,18 @@ constexpr float LOG2E = 1.44269504f;
 
 __device__ __forceinline__ float sigmoid(float z) { return reciprocal(1.0f + exp2_fast(-LOG2E * z)); }
 
-// The normal distribution function and e^(-z^2 / 2): Hastings' rational
-// approximation of erf (Abramowitz and Stegun 7.1.26, absolute error 1.5e-7),
-// whose factor e^(-x^2) at x = z / sqrt 2 is that exponential.
-__device__ __forceinline__ float normal_cdf(float z, float& bell)
+// The normal distribution function and density at z: Abramowitz and Stegun
+// 26.2.17 (Hastings), the tail beyond |z| as the density times a polynomial
+// in 1 / (1 + 0.2316419 |z|), absolute error below 7.5e-8.
+__device__ __forceinline__ float normal_cdf(float z, float& density)
 {
-    const float x = fabsf(z) * 0.70710678f;
-    bell = exp2_fast(-0.5f * LOG2E * z * z);
-    const float t = reciprocal(fmaf(0.3275911f, x, 1.0f));
-    float q = fmaf(1.061405429f, t, -1.453152027f);
-    q = fmaf(q, t, 1.421413741f);
-    q = fmaf(q, t, -0.284496736f);
-    q = fmaf(q, t, 0.254829592f);
-    const float tail = 0.5f * q * t * bell;  // beyond |z|
+    density = exp2_fast(fmaf(-0.5f * LOG2E * z, z, -1.32574806f));  // log2 of 1 / sqrt(2 pi)
+    const float t = reciprocal(fmaf(0.2316419f, fabsf(z), 1.0f));
+    float q = fmaf(1.330274429f, t, -1.821255978f);
+    q = fmaf(q, t, 1.781477937f);
+    q = fmaf(q, t, -0.356563782f);
+    q = fmaf(q, t, 0.319381530f);
+    const float tail = q * t * density;
     return z < 0.0f ? tail : 1.0f - tail;
 }
 
@@ -137,8 +176,8 @@ __device__ __forceinline__ void act_values(float (&v)[V], int act)
     } else if (act == NMS_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float bell;
-            v[i] *= normal_cdf(v[i], bell);
+            float density;
+            v[i] *= normal_cdf(v[i], density);
         }
     }
 }
@@ -159,9 +198,9 @@ __device__ __forceinline__ void act_slopes(float (&d)[V], const float (&z)[V], i
     } else if (act == NMS_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float bell;
-            const float cdf = normal_cdf(z[i], bell);
-            d[i] *= fmaf(0.39894228f * z[i], bell, cdf);
+            float density;
+            const float cdf = normal_cdf(z[i], density);
+            d[i] *= fmaf(z[i], density, cdf);
         }
     }
 }

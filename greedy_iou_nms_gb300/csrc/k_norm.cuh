@@ -23,268 +23,378 @@
 
 namespace gbnms {
 
-constexpr int NT = 256;           // threads of a block
-constexpr int NORM_CTAS = 1216;   // blocks that a call aims at: eight for each of 152 SMs
+constexpr int NT = 256;  // threads of a block
 
-// Row pieces of an image (a function of the shape alone: the workspace's size
-// depends on it).
-inline int64_t norm_pieces(int64_t batch, int64_t pixels)
+// ---------------------------------------------------------------- streaming
+//
+// Large maps in three launches: sums by rows' pieces, their join, and the
+// results.  The second reading comes from L2 as far as that holds the map:
+// the last launch goes through the pieces backwards and its stores are marked
+// as streaming.
+
+// Row pieces of an image: one wave of blocks, 32 rows at least (a
+// function of the shape alone: the workspace's size depends on it).
+inline int64_t norm_pieces(int64_t batch, int64_t pixels, int channels)
 {
-    const int64_t by_rows = (pixels + 63) / 64, by_ctas = (NORM_CTAS + batch - 1) / batch;
+    const int64_t tiles = channels > 256 ? channels / 256 : 1, ctas = SMS * 4;
+    const int64_t by_rows = (pixels + 31) / 32, by_ctas = ctas / (batch * tiles);
     const int64_t p = by_rows < by_ctas ? by_rows : by_ctas;
     return p < 1 ? 1 : p;
 }
 
-// Scratch: three partial planes [batch][pieces][channels] (mean high, M2, mean
-// low; the gradient's two sums), two of [batch][groups].
+// Scratch: three partial planes [batch][pieces][channels] (forward: mean high,
+// M2, mean low; the gradient's two sums), two of [batch][channels] (the
+// gradient's sums of an image) and two of [batch][groups].
 struct NormScratch {
-    float *pa, *pb, *pc, *ga, *gb;
+    float *pa, *pb, *pc, *ca, *cb, *ga, *gb;
 };
 
 inline NormScratch scratch(const NormArgs& a, void* ws)
 {
     NormScratch s;
-    const size_t plane = static_cast<size_t>(a.batch) * norm_pieces(a.batch, a.pixels) * a.channels;
+    const size_t image = static_cast<size_t>(a.batch) * a.channels;
+    const size_t plane = image * norm_pieces(a.batch, a.pixels, a.channels);
     s.pa = static_cast<float*>(ws);
     s.pb = s.pa + plane;
     s.pc = s.pb + plane;
-    s.ga = s.pc + plane;
+    s.ca = s.pc + plane;
+    s.cb = s.ca + image;
+    s.ga = s.cb + image;
     s.gb = s.ga + static_cast<size_t>(a.batch) * a.groups;
     return s;
 }
 
 // Tile of a block: `wide` vectors of V channels by NT / wide rows at a time.
 struct NormTile {
-    int wide;       // vectors a row of the tile
-    int tiles;      // tiles a row of the map
-    int64_t pieces;
+    int wide;    // vectors a row of the tile
+    int tiles;   // tiles a row of the map
+    int pieces;  // of an image
+    int per;     // rows a piece
 };
 
 template <typename T, int V>
-__device__ __forceinline__ void load_row(const T* p, float (&v)[V])
+__device__ __forceinline__ void widen(float (&v)[V], const Pack<T, V>& q)
 {
-    const Pack<T, V> q = *reinterpret_cast<const Pack<T, V>*>(p);
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = to_f32(q.v[i]);
 }
 
 template <typename T, int V>
+__device__ __forceinline__ void load_row(const T* p, float (&v)[V])
+{
+    widen(v, *reinterpret_cast<const Pack<T, V>*>(p));
+}
+
+template <typename T, int V>
 __device__ __forceinline__ void store_row(T* p, const float (&v)[V])
 {
-    Pack<T, V> q;
-#pragma unroll
-    for (int i = 0; i < V; ++i) q.v[i] = from_f32<T>(v[i]);
-    *reinterpret_cast<Pack<T, V>*>(p) = q;
+    *reinterpret_cast<Pack<T, V>*>(p) = pack_results<T, V>(v);
+}
+
+// store_row for results that nothing here reads again: kept out of L2's way.
+template <typename T, int V>
+__device__ __forceinline__ void stream_row(T* p, const float (&v)[V])
+{
+    const Pack<T, V> q = pack_results<T, V>(v);
+    if constexpr (sizeof(q) == 16) __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&q));
+    else *reinterpret_cast<Pack<T, V>*>(p) = q;
 }
 
 // Where a thread stands: image, row range of the piece, first channel.
 struct Spot {
-    int64_t image, piece, row, row_end;
-    int channel, ty, rows;
+    int64_t image;
+    int piece, row, row_end;
+    int channel, tx, ty, rows;
     bool in;
 };
 
 template <int V>
-__device__ __forceinline__ Spot spot(const NormArgs& a, const NormTile& t)
+__device__ __forceinline__ Spot spot(const NormArgs& a, const NormTile& t, unsigned block)
 {
     Spot s;
-    s.image = blockIdx.x / t.pieces;
-    s.piece = blockIdx.x % t.pieces;
+    s.image = block / static_cast<unsigned>(t.pieces);
+    s.piece = static_cast<int>(block % static_cast<unsigned>(t.pieces));
     s.rows = NT / t.wide;
+    s.tx = static_cast<int>(threadIdx.x) % t.wide;
     s.ty = static_cast<int>(threadIdx.x) / t.wide;
-    const int vec = static_cast<int>(blockIdx.y) * t.wide + static_cast<int>(threadIdx.x) % t.wide;
-    s.channel = vec * V;
+    s.channel = (static_cast<int>(blockIdx.y) * t.wide + s.tx) * V;
     s.in = s.ty < s.rows && s.channel < a.channels;
-    const int64_t per = (a.pixels + t.pieces - 1) / t.pieces;
-    s.row = s.piece * per;
-    s.row_end = s.row + per < a.pixels ? s.row + per : a.pixels;
+    const int pixels = static_cast<int>(a.pixels);
+    s.row = s.piece * t.per < pixels ? s.piece * t.per : pixels;
+    s.row_end = s.row + t.per < pixels ? s.row + t.per : pixels;
     return s;
 }
 
-// Per-channel (mean, squared deviations) of each row piece.
-template <typename T, int V>
-__global__ void __launch_bounds__(NT)
+// Rows that piece number `piece` has.
+__device__ __forceinline__ float piece_rows(const NormArgs& a, const NormTile& t, int piece)
+{
+    const int left = static_cast<int>(a.pixels) - piece * t.per;
+    return static_cast<float>(left < t.per ? (left > 0 ? left : 0) : t.per);
+}
+
+// f(row, vectors...) for a thread's rows, B of them loaded before the first
+// is worked on.
+template <int B, typename T, int V, typename F>
+__device__ __forceinline__ void each_row(const T* x, int64_t pitch, int r, int end, int step, F f)
+{
+    x += r * pitch;
+    const int64_t stride = step * pitch;
+    for (; r < end; r += B * step) {
+        Pack<T, V> q[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k, x += stride)
+            if (r + k * step < end) q[k] = *reinterpret_cast<const Pack<T, V>*>(x);
+#pragma unroll
+        for (int k = 0; k < B; ++k)
+            if (r + k * step < end) f(r + k * step, q[k]);
+    }
+}
+
+template <int B, typename T, int V, typename F>
+__device__ __forceinline__ void each_row(const T* x, int64_t pitch, const T* dy, int64_t dpitch, int r, int end,
+                                         int step, F f)
+{
+    x += r * pitch;
+    dy += r * dpitch;
+    const int64_t stride = step * pitch, dstride = step * dpitch;
+    for (; r < end; r += B * step) {
+        Pack<T, V> q[B], d[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k, x += stride, dy += dstride)
+            if (r + k * step < end) {
+                q[k] = *reinterpret_cast<const Pack<T, V>*>(x);
+                d[k] = *reinterpret_cast<const Pack<T, V>*>(dy);
+            }
+#pragma unroll
+        for (int k = 0; k < B; ++k)
+            if (r + k * step < end) f(r + k * step, q[k], d[k]);
+    }
+}
+
+// (mean, squared deviations) of each row piece by column: a vector (ONE: its
+// channels are of one group) or a channel.
+template <typename T, int V, bool ONE>
+__global__ void __launch_bounds__(NT, 4)
 norm_partial_kernel(NormArgs a, NormTile t, NormScratch w)
 {
-    __shared__ float s_high[NT * V], s_low[NT * V], s_m2[NT * V];
+    constexpr int P = ONE ? 1 : V;
+    __shared__ float s_high[NT * P], s_low[NT * P], s_m2[NT * P];
     __shared__ int s_count[NT];
-    const Spot p = spot<V>(a, t);
-    float first[V], s[V], q[V];
-    int count = 0;
+    pdl_release();
+    const Spot p = spot<V>(a, t, blockIdx.x);
+    float first[P], s[P], q[P];
+    int rows = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) first[i] = s[i] = q[i] = 0.0f;
+    for (int i = 0; i < P; ++i) first[i] = s[i] = q[i] = 0.0f;
     if (p.in) {
         const T* x = static_cast<const T*>(a.x) + p.image * a.x_image + p.channel;
-        for (int64_t r = p.row + p.ty; r < p.row_end; r += p.rows, ++count) {
+        const int begin = p.row + p.ty;
+        if (begin < p.row_end) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) first[i] = to_f32(x[begin * a.x_pixel + i]);
+        }
+        each_row<4, T, V>(x, a.x_pixel, begin, p.row_end, p.rows, [&](int, const Pack<T, V>& pack) {
             float v[V];
-            load_row<T, V>(x + r * a.x_pixel, v);
+            widen(v, pack);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                if (count == 0) first[i] = v[i];
-                const float d = v[i] - first[i];
-                s[i] += d;
-                q[i] = fmaf(d, d, q[i]);
+                const float d = v[i] - first[ONE ? 0 : i];
+                s[ONE ? 0 : i] += d;
+                q[ONE ? 0 : i] = fmaf(d, d, q[ONE ? 0 : i]);
             }
+            ++rows;
+        });
+    }
+    const int count = rows * (ONE ? V : 1);
+    if (p.ty < p.rows) {
+        s_count[threadIdx.x] = count;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float m = count ? s[i] / count : 0.0f;
+            s_high[threadIdx.x * P + i] = first[i];
+            s_low[threadIdx.x * P + i] = m;
+            s_m2[threadIdx.x * P + i] = fmaxf(q[i] - s[i] * m, 0.0f);
         }
     }
-    s_count[threadIdx.x] = count;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float m = count ? s[i] / count : 0.0f;
-        s_high[threadIdx.x * V + i] = first[i];
-        s_low[threadIdx.x * V + i] = m;
-        s_m2[threadIdx.x * V + i] = fmaxf(q[i] - s[i] * m, 0.0f);
-    }
     __syncthreads();
-    for (int c = threadIdx.x; c < t.wide * V; c += NT) {
-        const int channel = static_cast<int>(blockIdx.y) * t.wide * V + c;
-        if (channel >= a.channels) continue;
+    const int width = t.wide * P, columns = a.channels / (ONE ? V : 1);
+    for (int c = threadIdx.x; c < width; c += NT) {
+        const int column = static_cast<int>(blockIdx.y) * width + c;
+        if (column >= columns) continue;
         float n = 0.0f, mean = 0.0f, low = 0.0f, m2 = 0.0f;
-        for (int y = 0; y < p.rows; ++y) n += static_cast<float>(s_count[y * t.wide + c / V]);
+        for (int y = 0; y < p.rows; ++y) n += static_cast<float>(s_count[y * t.wide + c / P]);
         if (n == 0.0f) n = 1.0f;
-        const float origin = s_high[c];  // equal values give exactly that mean
+        const float origin = s_high[c], each = 1.0f / n;  // equal values give exactly that mean
         for (int y = 0; y < p.rows; ++y) {
-            const int at = y * t.wide * V + c;
-            mean += static_cast<float>(s_count[y * t.wide + c / V]) / n * (s_high[at] + s_low[at] - origin);
+            const int at = y * width + c;
+            mean = fmaf(static_cast<float>(s_count[y * t.wide + c / P]) * each, s_high[at] + s_low[at] - origin, mean);
         }
         mean += origin;
         for (int y = 0; y < p.rows; ++y) {
-            const int at = y * t.wide * V + c;
-            const float k = static_cast<float>(s_count[y * t.wide + c / V]), d = (s_high[at] - mean) + s_low[at];
+            const int at = y * width + c;
+            const float k = static_cast<float>(s_count[y * t.wide + c / P]), d = (s_high[at] - mean) + s_low[at];
             low = fmaf(k, d, low);
             m2 += fmaf(k * d, d, s_m2[at]);
         }
-        low /= n;
-        const int64_t at = (p.image * t.pieces + p.piece) * a.channels + channel;
+        low *= each;
+        const int64_t at = (p.image * t.pieces + p.piece) * static_cast<int64_t>(columns) + column;
         w.pa[at] = mean;
         w.pb[at] = fmaxf(m2 - n * low * low, 0.0f);
         w.pc[at] = low;
     }
 }
 
-// mean and rstd of each (image, group) from the pieces; one warp each.
-static __global__ void __launch_bounds__(NT)
-norm_finish_kernel(NormArgs a, NormTile t, NormScratch w)
+// Sum over a team of 32 threads (a warp) or NT (the block; s: 8 floats).
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float v, float* s)
 {
-    const int64_t which = (static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x) / 32;
-    if (which >= a.batch * a.groups) return;
-    const int64_t image = which / a.groups;
-    const int D = a.channels / a.groups, c0 = static_cast<int>(which % a.groups) * D;
-    const int64_t per = (a.pixels + t.pieces - 1) / t.pieces, items = t.pieces * D;
-    const float all = static_cast<float>(a.pixels) * static_cast<float>(D);
-    const float origin = w.pa[image * t.pieces * a.channels + c0];
-    float mean = 0.0f, low = 0.0f, m2 = 0.0f;
-    for (int64_t i = lane_id(); i < items; i += 32) {
-        const int64_t piece = i / D, left = a.pixels - piece * per;
-        const float k = static_cast<float>(left < per ? (left > 0 ? left : 0) : per);
-        if (k > 0.0f) mean += (w.pa[(image * t.pieces + piece) * a.channels + c0 + i % D] - origin) * (k / all);
+    v = warp_sum(v);
+    if (TEAM > 32) {
+        if (lane_id() == 0) s[threadIdx.x / 32] = v;
+        __syncthreads();
+        v = s[0];
+#pragma unroll
+        for (int k = 1; k < TEAM / 32; ++k) v += s[k];
     }
-    mean = origin + warp_sum(mean);
-    for (int64_t i = lane_id(); i < items; i += 32) {
-        const int64_t piece = i / D, left = a.pixels - piece * per;
-        const float k = static_cast<float>(left < per ? (left > 0 ? left : 0) : per);
-        const int64_t at = (image * t.pieces + piece) * a.channels + c0 + i % D;
-        const float d = (w.pa[at] - mean) + w.pc[at];
+    return v;
+}
+
+// mean and rstd of each (image, group) from the pieces of `each` columns of
+// `values` channels a group; TEAM threads each.
+template <int TEAM>
+__global__ void __launch_bounds__(NT)
+norm_finish_kernel(NormArgs a, NormTile t, NormScratch w, int each, int values)
+{
+    __shared__ float red[3][NT / 32];
+    pdl_wait();
+    pdl_release();
+    const int64_t which = (static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x) / TEAM;
+    if (which >= a.batch * a.groups) return;  // whole teams
+    const int lane = static_cast<int>(threadIdx.x) % TEAM;
+    const int64_t image = which / a.groups;
+    const int columns = a.channels / values, items = t.pieces * each;
+    const int64_t base = image * t.pieces * columns + which % a.groups * each;
+    const float all = static_cast<float>(a.pixels) * static_cast<float>(a.channels / a.groups), each_all = 1.0f / all;
+    // Deviations of the pieces' means from the first piece's: equal means give exactly that mean.
+    const float origin = w.pa[base];
+    float mean = 0.0f, low = 0.0f, m2 = 0.0f;
+#pragma unroll 4
+    for (int i = lane; i < items; i += TEAM) {
+        const int piece = i / each;
+        const float k = piece_rows(a, t, piece) * values;
+        const float high = w.pa[base + static_cast<int64_t>(piece) * columns + (i - piece * each)];
+        if (k > 0.0f) mean = fmaf(high - origin, k * each_all, mean);
+    }
+    mean = origin + team_sum<TEAM>(mean, red[0]);
+#pragma unroll 4
+    for (int i = lane; i < items; i += TEAM) {
+        const int piece = i / each;
+        const int64_t at = base + static_cast<int64_t>(piece) * columns + (i - piece * each);
+        const float k = piece_rows(a, t, piece) * values, d = (w.pa[at] - mean) + w.pc[at], m = w.pb[at];
         if (k > 0.0f) {
-            low = fmaf(d, k / all, low);
-            m2 += fmaf(d * k, d, w.pb[at]);
+            low = fmaf(d, k * each_all, low);
+            m2 += fmaf(d * k, d, m);
         }
     }
-    low = warp_sum(low);
-    m2 = warp_sum(m2);
-    if (lane_id() == 0) {
+    low = team_sum<TEAM>(low, red[1]);
+    m2 = team_sum<TEAM>(m2, red[2]);
+    if (lane == 0) {
         a.mean[which] = mean + low;
         a.rstd[which] = 1.0f / sqrtf(fmaxf(m2 / all - low * low, 0.0f) + a.eps);
     }
 }
 
-template <typename T, int V>
+template <typename T, int V, bool ONE, int ACT>
 __global__ void __launch_bounds__(NT)
 norm_apply_kernel(NormArgs a, NormTile t)
 {
-    const Spot p = spot<V>(a, t);
+    constexpr int P = ONE ? 1 : V;
+    const Spot p = spot<V>(a, t, gridDim.x - 1 - blockIdx.x);  // the pieces read last come first
+    pdl_wait();
     if (!p.in) return;
     const int D = a.channels / a.groups;
-    float mean[V], scale[V], shift[V];
+    float mean[P], scale[V], shift[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int64_t g = p.image * a.groups + (p.channel + i) / D;
-        mean[i] = a.mean[g];
+        if (i < P) mean[i] = a.mean[g];
         scale[i] = a.rstd[g] * (a.weight ? load_param<T>(a.weight, a.param_f32, p.channel + i) : 1.0f);
         shift[i] = a.bias ? load_param<T>(a.bias, a.param_f32, p.channel + i) : 0.0f;
     }
     const T* x = static_cast<const T*>(a.x) + p.image * a.x_image + p.channel;
     T* y = static_cast<T*>(a.out);
-    for (int64_t r = p.row + p.ty; r < p.row_end; r += p.rows) {
+    each_row<4, T, V>(x, a.x_pixel, p.row + p.ty, p.row_end, p.rows, [&](int r, const Pack<T, V>& q) {
         float v[V];
-        load_row<T, V>(x + r * a.x_pixel, v);
+        widen(v, q);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = fmaf(v[i] - mean[i], scale[i], shift[i]);
-        act_values<V>(v, a.act);
+        for (int i = 0; i < V; ++i) v[i] = fmaf(v[i] - mean[ONE ? 0 : i], scale[i], shift[i]);
+        act_values<V>(v, ACT);
         const int64_t at = (p.image * a.pixels + r) * a.channels + p.channel;
         if (a.drop.limit < 65536u) drop<V>(v, static_cast<uint64_t>(at), a.drop);
-        store_row<T, V>(y + at, v);
-    }
+        stream_row<T, V>(y + at, v);
+    });
 }
 
-// dz and u of one vector.
-template <typename T, int V>
-__device__ __forceinline__ void slope_row(const NormArgs& a, const float (&mean)[V], const float (&rstd)[V],
-                                          const float (&weight)[V], const float (&bias)[V], const T* x, const T* dy,
-                                          uint64_t at, float (&u)[V], float (&dz)[V])
-{
-    float z[V];
-    load_row<T, V>(x, u);
-    load_row<T, V>(dy, dz);
-    if (a.drop.limit < 65536u) drop<V>(dz, at, a.drop);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        u[i] = (u[i] - mean[i]) * rstd[i];
-        z[i] = fmaf(u[i], weight[i], bias[i]);
-    }
-    act_slopes<V>(dz, z, a.act);
-}
-
-template <typename T, int V>
-__device__ __forceinline__ void load_channels(const NormArgs& a, const Spot& p, float (&mean)[V], float (&rstd)[V],
-                                              float (&weight)[V], float (&bias)[V])
+// The factors of a thread's channels: z = (x - mean) * scale + bias.
+template <typename T, int V, int P>
+__device__ __forceinline__ void load_channels(const NormArgs& a, const Spot& p, float (&mean)[P], float (&scale)[V],
+                                              float (&bias)[V])
 {
     const int D = a.channels / a.groups;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int64_t g = p.image * a.groups + (p.channel + i) / D;
-        mean[i] = a.mean[g];
-        rstd[i] = a.rstd[g];
-        weight[i] = a.weight ? load_param<T>(a.weight, a.param_f32, p.channel + i) : 1.0f;
+        if (i < P) mean[i] = a.mean[g];
+        scale[i] = a.rstd[g] * (a.weight ? load_param<T>(a.weight, a.param_f32, p.channel + i) : 1.0f);
         bias[i] = a.bias ? load_param<T>(a.bias, a.param_f32, p.channel + i) : 0.0f;
     }
 }
 
-// Per-channel sums of dz and dz * u of each row piece.
-template <typename T, int V>
+// x - mean, and dz but for the dropout's factor, of one vector.
+template <int ACT, typename T, int V, int P>
+__device__ __forceinline__ void slope_row(const NormArgs& a, const float (&mean)[P], const float (&scale)[V],
+                                          const float (&bias)[V], const Pack<T, V>& x, const Pack<T, V>& dy,
+                                          uint64_t at, float (&d)[V], float (&dz)[V])
+{
+    float z[V];
+    widen(d, x);
+    widen(dz, dy);
+    if (a.drop.limit < 65536u) drop_mask<V>(dz, at, a.drop);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        d[i] -= mean[P == 1 ? 0 : i];
+        z[i] = fmaf(d[i], scale[i], bias[i]);
+    }
+    act_slopes<V>(dz, z, ACT);
+}
+
+// Sums by channel of dz and dz * (x - mean) of each row piece.
+template <typename T, int V, bool ONE, int ACT>
 __global__ void __launch_bounds__(NT)
 norm_grad_partial_kernel(NormArgs a, NormTile t, NormScratch w)
 {
+    constexpr int P = ONE ? 1 : V;
     __shared__ float s_a[NT * V], s_b[NT * V];
-    const Spot p = spot<V>(a, t);
+    pdl_release();
+    const Spot p = spot<V>(a, t, blockIdx.x);
     float sa[V], sb[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) sa[i] = sb[i] = 0.0f;
     if (p.in) {
-        float mean[V], rstd[V], weight[V], bias[V];
-        load_channels<T, V>(a, p, mean, rstd, weight, bias);
-        const T* x = static_cast<const T*>(a.x) + p.image * a.x_image + p.channel;
-        const T* dy = static_cast<const T*>(a.dy) + p.image * a.dy_image + p.channel;
-        for (int64_t r = p.row + p.ty; r < p.row_end; r += p.rows) {
-            float u[V], dz[V];
-            slope_row<T, V>(a, mean, rstd, weight, bias, x + r * a.x_pixel, dy + r * a.dy_pixel,
-                                 static_cast<uint64_t>((p.image * a.pixels + r) * a.channels + p.channel), u, dz);
+        float mean[P], scale[V], bias[V];
+        load_channels<T, V, P>(a, p, mean, scale, bias);
+        each_row<2, T, V>(static_cast<const T*>(a.x) + p.image * a.x_image + p.channel, a.x_pixel,
+                          static_cast<const T*>(a.dy) + p.image * a.dy_image + p.channel, a.dy_pixel, p.row + p.ty,
+                          p.row_end, p.rows, [&](int r, const Pack<T, V>& x, const Pack<T, V>& dy) {
+            float d[V], dz[V];
+            slope_row<ACT>(a, mean, scale, bias, x, dy,
+                               static_cast<uint64_t>((p.image * a.pixels + r) * a.channels + p.channel), d, dz);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 sa[i] += dz[i];
-                sb[i] = fmaf(dz[i], u[i], sb[i]);
+                sb[i] = fmaf(dz[i], d[i], sb[i]);
             }
-        }
+        });
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -300,116 +410,176 @@ norm_grad_partial_kernel(NormArgs a, NormTile t, NormScratch w)
             va += s_a[y * t.wide * V + c];
             vb += s_b[y * t.wide * V + c];
         }
-        const int64_t at = (p.image * t.pieces + p.piece) * a.channels + channel;
-        w.pa[at] = va;
-        w.pb[at] = vb;
+        const int64_t at = (p.image * t.pieces + p.piece) * static_cast<int64_t>(a.channels) + channel;
+        const float factor = a.drop.limit < 65536u ? a.drop.factor : 1.0f;
+        w.pa[at] = va * factor;
+        w.pb[at] = vb * factor;
     }
 }
 
-// avg(du) and avg(du * u) of each (image, group); one warp each.
+// One block per image and `chunk` channels (whole groups): the image's sums
+// of dz and dz * u by channel, and avg(du) and avg(du * u) by group.
 template <typename T>
 __global__ void __launch_bounds__(NT)
-norm_grad_finish_kernel(NormArgs a, NormTile t, NormScratch w)
+norm_grad_finish_kernel(NormArgs a, NormTile t, NormScratch w, int chunk)
 {
-    const int64_t which = (static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x) / 32;
-    if (which >= a.batch * a.groups) return;
-    const int64_t image = which / a.groups;
-    const int D = a.channels / a.groups, c0 = static_cast<int>(which % a.groups) * D;
-    const float all = static_cast<float>(a.pixels) * static_cast<float>(D);
-    float va = 0.0f, vb = 0.0f;
-    for (int64_t i = lane_id(); i < t.pieces * D; i += 32) {
-        const int c = c0 + static_cast<int>(i % D);
-        const float k = a.weight ? load_param<T>(a.weight, a.param_f32, c) : 1.0f;
-        const int64_t at = (image * t.pieces + i / D) * a.channels + c;
-        va = fmaf(k, w.pa[at], va);
-        vb = fmaf(k, w.pb[at], vb);
-    }
-    va = warp_sum(va);
-    vb = warp_sum(vb);
-    if (lane_id() == 0) {
-        w.ga[which] = va / all;
-        w.gb[which] = vb / all;
-    }
-}
-
-// dweight and dbias: sums over `items` partial rows, 32 channels a block.
-static __global__ void __launch_bounds__(NT)
-norm_grad_param_kernel(NormArgs a, int64_t items, const float* pa, const float* pb)
-{
+    extern __shared__ float s_sum[];  // [2][chunk]
     __shared__ float s_a[NT], s_b[NT];
-    const int c = static_cast<int>(blockIdx.x) * 32 + static_cast<int>(lane_id());
-    float va = 0.0f, vb = 0.0f;
-    if (c < a.channels)
-        for (int64_t i = threadIdx.x / 32; i < items; i += NT / 32) {
-            va += pa[i * a.channels + c];
-            vb += pb[i * a.channels + c];
+    pdl_wait();
+    pdl_release();
+    const int D = a.channels / a.groups, c0 = static_cast<int>(blockIdx.y) * chunk;
+    const int64_t image = blockIdx.x;
+    const int channels = c0 + chunk < a.channels ? chunk : a.channels - c0;
+    const int across = channels < NT ? channels : NT, lists = NT / across;
+    const int x = static_cast<int>(threadIdx.x) % across, y = static_cast<int>(threadIdx.x) / across;
+    for (int c = x; c - x < channels; c += across) {
+        float va = 0.0f, vb = 0.0f;
+        if (y < lists && c < channels) {
+            const int64_t at = image * t.pieces * a.channels + c0 + c;
+#pragma unroll 4
+            for (int k = y; k < t.pieces; k += lists) {
+                va += w.pa[at + static_cast<int64_t>(k) * a.channels];
+                vb += w.pb[at + static_cast<int64_t>(k) * a.channels];
+            }
         }
-    s_a[threadIdx.x] = va;
-    s_b[threadIdx.x] = vb;
-    __syncthreads();
-    if (threadIdx.x < 32 && c < a.channels) {
-        for (int k = 1; k < NT / 32; ++k) {
-            va += s_a[threadIdx.x + 32 * k];
-            vb += s_b[threadIdx.x + 32 * k];
+        s_a[threadIdx.x] = va;
+        s_b[threadIdx.x] = vb;
+        __syncthreads();
+        if (y == 0 && c < channels) {
+            for (int k = 1; k < lists; ++k) {
+                va += s_a[k * across + x];
+                vb += s_b[k * across + x];
+            }
+            const int64_t g = image * a.groups + (c0 + c) / D;
+            const float weight = a.weight ? load_param<T>(a.weight, a.param_f32, c0 + c) : 1.0f;
+            vb *= a.rstd[g];  // u = (x - mean) * rstd
+            w.ca[image * a.channels + c0 + c] = va;
+            w.cb[image * a.channels + c0 + c] = vb;
+            s_sum[c] = va * weight;
+            s_sum[chunk + c] = vb * weight;
         }
-        if (a.dbias) a.dbias[c] = va;
-        if (a.dweight) a.dweight[c] = vb;
+        __syncthreads();
+    }
+    const float each_all = 1.0f / (static_cast<float>(a.pixels) * static_cast<float>(D));
+    for (int g = static_cast<int>(threadIdx.x) / 32; g < channels / D; g += NT / 32) {
+        float va = 0.0f, vb = 0.0f;
+        for (int i = static_cast<int>(lane_id()); i < D; i += 32) {
+            va += s_sum[g * D + i];
+            vb += s_sum[chunk + g * D + i];
+        }
+        va = warp_sum(va);
+        vb = warp_sum(vb);
+        if (lane_id() == 0) {
+            const int64_t at = image * a.groups + c0 / D + g;
+            w.ga[at] = va * each_all;
+            w.gb[at] = vb * each_all;
+        }
     }
 }
 
-template <typename T, int V>
+// dweight and dbias of channel c: the images' sums, added in order.
+__device__ __forceinline__ void param_sums(const NormArgs& a, const float* ca, const float* cb, int c)
+{
+    float va = 0.0f, vb = 0.0f;
+#pragma unroll 8
+    for (int64_t n = 0; n < a.batch; ++n) {
+        va += ca[n * a.channels + c];
+        vb += cb[n * a.channels + c];
+    }
+    if (a.dbias) a.dbias[c] = va;
+    if (a.dweight) a.dweight[c] = vb;
+}
+
+static __global__ void __launch_bounds__(NT)
+norm_grad_param_kernel(NormArgs a, NormScratch w)
+{
+    pdl_wait();
+    const int c = static_cast<int>(blockIdx.x) * NT + static_cast<int>(threadIdx.x);
+    if (c < a.channels) param_sums(a, w.ca, w.cb, c);
+}
+
+// dx; the blocks past the pieces' (the first to run) write dweight and dbias.
+template <typename T, int V, bool ONE, int ACT>
 __global__ void __launch_bounds__(NT)
 norm_grad_apply_kernel(NormArgs a, NormTile t, NormScratch w)
 {
-    const Spot p = spot<V>(a, t);
+    constexpr int P = ONE ? 1 : V;
+    const unsigned block = gridDim.x - 1 - blockIdx.x, main = static_cast<unsigned>(a.batch) * t.pieces;
+    if (block >= main) {
+        pdl_wait();
+        const int c = static_cast<int>(block - main) * NT + static_cast<int>(threadIdx.x);
+        if (blockIdx.y == 0 && c < a.channels) param_sums(a, w.ca, w.cb, c);
+        return;
+    }
+    const Spot p = spot<V>(a, t, block);
+    pdl_wait();
     if (!p.in) return;
     const int D = a.channels / a.groups;
-    float mean[V], rstd[V], weight[V], bias[V], m1[V], m2[V];
-    load_channels<T, V>(a, p, mean, rstd, weight, bias);
+    float mean[P], scale[V], bias[V], m1[P], m2[P];
+    load_channels<T, V, P>(a, p, mean, scale, bias);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < P; ++i) {
         const int64_t g = p.image * a.groups + (p.channel + i) / D;
-        m1[i] = w.ga[g];
-        m2[i] = w.gb[g];
+        const float r = a.rstd[g];
+        m1[i] = -r * w.ga[g];
+        m2[i] = -r * r * w.gb[g];
     }
-    const T* x = static_cast<const T*>(a.x) + p.image * a.x_image + p.channel;
-    const T* dy = static_cast<const T*>(a.dy) + p.image * a.dy_image + p.channel;
-    for (int64_t r = p.row + p.ty; r < p.row_end; r += p.rows) {
-        float u[V], dz[V];
+    each_row<2, T, V>(static_cast<const T*>(a.x) + p.image * a.x_image + p.channel, a.x_pixel,
+                      static_cast<const T*>(a.dy) + p.image * a.dy_image + p.channel, a.dy_pixel, p.row + p.ty,
+                      p.row_end, p.rows, [&](int r, const Pack<T, V>& x, const Pack<T, V>& dy) {
+        float d[V], dz[V];
         const int64_t at = (p.image * a.pixels + r) * a.channels + p.channel;
-        slope_row<T, V>(a, mean, rstd, weight, bias, x + r * a.x_pixel, dy + r * a.dy_pixel,
-                             static_cast<uint64_t>(at), u, dz);
+        slope_row<ACT>(a, mean, scale, bias, x, dy, static_cast<uint64_t>(at), d, dz);
+        if (a.drop.limit < 65536u) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) dz[i] = rstd[i] * (fmaf(dz[i], weight[i], -m1[i]) - u[i] * m2[i]);
-        store_row<T, V>(static_cast<T*>(a.out) + at, dz);
-    }
+            for (int i = 0; i < V; ++i) dz[i] *= a.drop.factor;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            dz[i] = fmaf(dz[i], scale[i], fmaf(d[i], m2[ONE ? 0 : i], m1[ONE ? 0 : i]));
+        stream_row<T, V>(static_cast<T*>(a.out) + at, dz);
+    });
 }
 
 // ------------------------------------------------------------------- clusters
 //
 // Where one image's slab of whole groups (a few dozen channels of every
-// pixel) fits the registers of a cluster, it is read once: each block keeps
-// its rows, the blocks exchange their sums through distributed shared memory,
-// and the results are written from the registers.
+// pixel) fits the shared memory of a cluster, it is read once: each block
+// keeps its rows, every thread the vectors that it copied itself, the blocks
+// exchange their sums through distributed shared memory, and the results are
+// written from what they keep.  Small blocks (several to an SM) overlap one's
+// loads with another's sums and stores.
 
 // Tile of a cluster: `wide` vectors of V channels (whole groups), the rows
 // split over `ctas` blocks of `rows` each.
 struct NormCluster {
     int wide, tiles, ctas;
     int rows;
+    int groups;     // of a tile, at most NT
+    bool shuffles;  // rows and groups are powers of two of lanes
+    int held;       // vectors that a thread keeps, at most
 };
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
-// *p of the block `rank` of the cluster.
-__device__ __forceinline__ float peer_load(const float* p, int rank)
+// Asynchronous copy of one vector into shared memory.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src)
+{
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(at), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(at), "l"(src), "n"(BYTES) : "memory");
+}
+
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// *p of the block `rank` of the cluster = v.
+__device__ __forceinline__ void peer_store(float* p, int rank, float v)
 {
     uint32_t at;
-    float v;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(at), "f"(v) : "memory");
 }
 
 // Where a thread of a cluster's block stands.
@@ -440,142 +610,196 @@ __device__ __forceinline__ ClusterSpot cluster_spot(const NormArgs& a, const Nor
     return p;
 }
 
-// out[q][g] = sum of the threads' partials part[q][ty][...] of group g: `each`
-// entries of a row of `width` belong to a group.  One warp a group.
-template <int N>
-__device__ __forceinline__ void sum_groups(const float* part, int plane, int width, int each, int steps, int groups,
-                                           float* out, int out_plane)
-{
-    __syncthreads();
-    for (int g = static_cast<int>(threadIdx.x) / 32; g < groups; g += NT / 32) {
-        float v[N];
+// Sums by group over a block.  Each thread gives N sums for each of its P
+// parts (P = 1: its vector lies in one group).  Where rows of the tile and
+// groups are powers of two of lanes, lanes of one group join by shuffles and
+// the warps' sums by one pass through shared memory; else every thread's
+// parts go there and a warp adds up each group.
+struct GroupSums {
+    float* part;  // [N][NT * P], or [N][8][32]
+    float* out;   // [N][groups], groups <= plane
+    int wide, each, steps, groups, plane;  // `each` parts of a row of the tile belong to a group
+    bool shuffles;
+
+    template <int N, int P>
+    __device__ __forceinline__ void operator()(const float (&v)[N][P], const ClusterSpot& p)
+    {
+        if (P == 1 && shuffles) {
+            float u[N];
 #pragma unroll
-        for (int q = 0; q < N; ++q) v[q] = 0.0f;
-        for (int k = static_cast<int>(lane_id()); k < steps * each; k += 32) {
-            const int at = k / each * width + g * each + k % each;
+            for (int q = 0; q < N; ++q) {
+                u[q] = v[q][0];
+                for (int o = 16; o >= wide; o >>= 1) u[q] += __shfl_xor_sync(FULL, u[q], o);
+                for (int o = each / 2; o; o >>= 1) u[q] += __shfl_xor_sync(FULL, u[q], o);
+            }
+            const int lane = static_cast<int>(lane_id());
+            if (lane < wide && lane % each == 0)
 #pragma unroll
-            for (int q = 0; q < N; ++q) v[q] += part[q * plane + at];
+                for (int q = 0; q < N; ++q) part[q * NT + threadIdx.x / 32 * 32 + lane / each] = u[q];
+            __syncthreads();
+            for (int k = threadIdx.x; k < N * groups; k += NT) {
+                const int q = k / groups, g = k % groups;
+                float s = 0.0f;
+#pragma unroll
+                for (int w = 0; w < NT / 32; ++w) s += part[q * NT + w * 32 + g];
+                out[q * plane + g] = s;
+            }
+            __syncthreads();
+            return;
         }
+        if (p.ty < steps) {
 #pragma unroll
-        for (int q = 0; q < N; ++q) {
-            v[q] = warp_sum(v[q]);
-            if (lane_id() == 0) out[q * out_plane + g] = v[q];
+            for (int q = 0; q < N; ++q)
+#pragma unroll
+                for (int i = 0; i < P; ++i) part[q * NT * P + (p.ty * wide + p.tx) * P + i] = v[q][i];
         }
+        __syncthreads();
+        for (int g = static_cast<int>(threadIdx.x) / 32; g < groups; g += NT / 32) {
+            float s[N];
+#pragma unroll
+            for (int q = 0; q < N; ++q) s[q] = 0.0f;
+            int y = static_cast<int>(lane_id()) / each, x = static_cast<int>(lane_id()) % each;
+            const int dy = 32 / each, dx = 32 % each;
+            while (y < steps) {
+                const int at = y * wide * P + g * each + x;
+#pragma unroll
+                for (int q = 0; q < N; ++q) s[q] += part[q * NT * P + at];
+                y += dy;
+                x += dx;
+                if (x >= each) {
+                    x -= each;
+                    ++y;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+                s[q] = warp_sum(s[q]);
+                if (lane_id() == 0) out[q * plane + g] = s[q];
+            }
+        }
+        __syncthreads();
     }
-    __syncthreads();
-}
+};
 
 // ONE: a vector lies in one group (its channels' sums are one).
-template <typename T, int V, int NV, bool ONE>
-__global__ void __launch_bounds__(NT)
+template <typename T, int V, bool ONE>
+__global__ void __launch_bounds__(NT, 4)
 norm_cluster_kernel(NormArgs a, NormCluster t)
 {
     constexpr int P = ONE ? 1 : V;  // partial sums of a thread
-    extern __shared__ float smem[];
-    const int CW = t.wide * V, D = a.channels / a.groups;
-    float* part = smem;                  // [2][NT * P]
-    float* s_weight = part + 2 * NT * P; // [CW]
-    float* s_bias = s_weight + CW;       // [CW]
-    float* s_sum = s_bias + CW;          // [2][CW]: sums by group
-    float* s_piece = s_sum + 2 * CW;     // [3][CW]: this block's mean (high, low) and squares by group
-    float* s_mean = s_piece + 3 * CW;    // [CW]: the image's, by group
-    float* s_rstd = s_mean + CW;
+    extern __shared__ uint4 smem[];
+    const int CW = t.wide * V, D = a.channels / a.groups, G = t.groups;
+    Pack<T, V>* keep = reinterpret_cast<Pack<T, V>*>(smem) + threadIdx.x;  // [held][NT]
+    float* part = reinterpret_cast<float*>(reinterpret_cast<Pack<T, V>*>(smem) + t.held * NT);  // [2][NT * P]
+    float* s_weight = part + 2 * NT * P;  // [CW]
+    float* s_bias = s_weight + CW;        // [CW]
+    float* s_sum = s_bias + CW;           // [2][G]: sums by group
+    float* s_piece = s_sum + 2 * G;       // [ctas][3][G]: the blocks' means (high, low) and squares by group
+    float* s_mean = s_piece + 3 * t.ctas * G;  // [G]: the image's, by group
+    float* s_rstd = s_mean + G;
     const ClusterSpot p = cluster_spot<V>(a, t, D);
-    Pack<T, V> q[NV];
-    const T* x = static_cast<const T*>(a.x) + p.image * a.x_image + p.channel;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int r = p.row0 + p.ty + k * p.step;
-        if (p.in && r < p.row_end) q[k] = *reinterpret_cast<const Pack<T, V>*>(x + r * a.x_pixel);
+    if (t.ctas > 1) cluster_arrive();  // every block has begun: waited for before the first store to a peer
+    const int first = p.in ? p.row0 + p.ty : p.row_end;  // a thread outside the map has no rows
+    {
+        const T* x = static_cast<const T*>(a.x) + p.image * a.x_image + first * a.x_pixel + p.channel;
+        const int64_t stride = p.step * a.x_pixel;
+        Pack<T, V>* to = keep;
+        for (int r = first; r < p.row_end; r += p.step, x += stride, to += NT) copy_async<sizeof(T) * V>(to, x);
     }
     for (int c = threadIdx.x; c < CW && p.first_channel + c < a.channels; c += NT) {
         s_weight[c] = a.weight ? load_param<T>(a.weight, a.param_f32, p.first_channel + c) : 1.0f;
         s_bias[c] = a.bias ? load_param<T>(a.bias, a.param_f32, p.first_channel + c) : 0.0f;
     }
-    const int width = ONE ? t.wide : CW, each = ONE ? D / V : D;
-    auto put = [&](int plane, const float (&s)[P]) {
-        if (p.ty < p.step) {
-#pragma unroll
-            for (int i = 0; i < P; ++i) part[plane * NT * P + (p.ty * t.wide + p.tx) * P + i] = s[i];
-        }
-    };
+    GroupSums sums{part, s_sum, t.wide, ONE ? D / V : D, p.step, p.groups, G, t.shuffles};
+    copies_done();  // a thread reads its own copies alone
     // The block's mean by group, then the deviations from it.
     {
-        float s[P];
+        float s[1][P];
 #pragma unroll
-        for (int i = 0; i < P; ++i) s[i] = 0.0f;
+        for (int i = 0; i < P; ++i) s[0][i] = 0.0f;
+        const Pack<T, V>* from = keep;
+#pragma unroll 2
+        for (int r = first; r < p.row_end; r += p.step, from += NT) {
+            float v[V];
+            widen(v, *from);
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (p.in && p.row0 + p.ty + k * p.step < p.row_end) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) s[ONE ? 0 : i] += to_f32(q[k].v[i]);
-            }
-        put(0, s);
+            for (int i = 0; i < V; ++i) s[0][ONE ? 0 : i] += v[i];
+        }
+        sums.template operator()<1, P>(s, p);
     }
-    sum_groups<1>(part, 0, width, each, p.step, p.groups, s_sum, 0);
     const float n = static_cast<float>(p.row_end - p.row0) * static_cast<float>(D);
     const float each_n = n > 0.0f ? 1.0f / n : 0.0f;
+    float mean_here = 0.0f;  // of the group that this thread publishes
+    if (threadIdx.x < p.groups) mean_here = s_sum[threadIdx.x] * each_n;
     {
-        float mean[P], s1[P], s2[P];
+        float mean[P], s[2][P];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             mean[i] = p.in ? s_sum[(p.tx * V + i) / D] * each_n : 0.0f;
-            s1[i] = s2[i] = 0.0f;
+            s[0][i] = s[1][i] = 0.0f;
         }
+        const Pack<T, V>* from = keep;
+#pragma unroll 2
+        for (int r = first; r < p.row_end; r += p.step, from += NT) {
+            float v[V];
+            widen(v, *from);
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (p.in && p.row0 + p.ty + k * p.step < p.row_end) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float d = to_f32(q[k].v[i]) - mean[ONE ? 0 : i];
-                    s1[ONE ? 0 : i] += d;
-                    s2[ONE ? 0 : i] = fmaf(d, d, s2[ONE ? 0 : i]);
-                }
+            for (int i = 0; i < V; ++i) {
+                const float d = v[i] - mean[ONE ? 0 : i];
+                s[0][ONE ? 0 : i] += d;
+                s[1][ONE ? 0 : i] = fmaf(d, d, s[1][ONE ? 0 : i]);
             }
-        put(0, s1);
-        put(1, s2);
-        for (int g = threadIdx.x; g < p.groups; g += NT) s_piece[g] = s_sum[g] * each_n;
+        }
+        sums.template operator()<2, P>(s, p);
     }
-    sum_groups<2>(part, NT * P, width, each, p.step, p.groups, s_sum, CW);
-    for (int g = threadIdx.x; g < p.groups; g += NT) {
-        const float low = s_sum[g] * each_n;
-        s_piece[CW + g] = low;
-        s_piece[2 * CW + g] = fmaxf(s_sum[CW + g] - s_sum[g] * low, 0.0f);
+    // Every block's pieces go to every block, which joins them in the same order.
+    if (t.ctas > 1) cluster_wait();
+    if (threadIdx.x < p.groups) {  // groups <= NT
+        const int g = threadIdx.x;
+        const float low = s_sum[g] * each_n, m2 = fmaxf(s_sum[G + g] - s_sum[g] * low, 0.0f);
+        float* at = s_piece + p.rank * 3 * G + g;
+        for (int k = 0; k < t.ctas; ++k) {
+            if (t.ctas > 1) {
+                peer_store(at, k, mean_here);
+                peer_store(at + G, k, low);
+                peer_store(at + 2 * G, k, m2);
+            } else {
+                at[0] = mean_here;
+                at[G] = low;
+                at[2 * G] = m2;
+            }
+        }
     }
-    // The blocks' pieces, joined by every block in the same order.
     if (t.ctas > 1) {
         cluster_arrive();
         cluster_wait();
-    } else {
-        __syncthreads();
     }
-    const float all = static_cast<float>(a.pixels) * static_cast<float>(D);
-    for (int g = threadIdx.x; g < p.groups; g += NT) {
-        float mean, low = 0.0f, m2 = 0.0f;
-        if (t.ctas == 1) {
-            mean = s_piece[g];
-            low = s_piece[CW + g];
-            m2 = s_piece[2 * CW + g];
-        } else {
-            const float origin = peer_load(s_piece + g, 0);
-            mean = 0.0f;
-            for (int k = 0; k < t.ctas; ++k) {
+    if (threadIdx.x < p.groups) {
+        const int g = threadIdx.x;
+        const float all = static_cast<float>(a.pixels) * static_cast<float>(D);
+        float m = s_piece[g], low = s_piece[G + g], m2 = s_piece[2 * G + g];
+        if (t.ctas > 1) {
+            const float origin = m, each_all = 1.0f / all;
+            float mean = 0.0f;
+            auto values = [&](int k) {  // of block k's rows
                 const int64_t left = a.pixels - static_cast<int64_t>(k) * t.rows;
-                const float share = static_cast<float>(left < t.rows ? (left > 0 ? left : 0) : t.rows) * D / all;
-                mean = fmaf(share, peer_load(s_piece + g, k) - origin, mean);
-            }
+                return static_cast<float>(left < t.rows ? (left > 0 ? left : 0) : t.rows) * D;
+            };
+            for (int k = 1; k < t.ctas; ++k)
+                if (values(k) > 0.0f) mean = fmaf(values(k) * each_all, s_piece[k * 3 * G + g] - origin, mean);
             mean += origin;
+            low = m2 = 0.0f;
             for (int k = 0; k < t.ctas; ++k) {
-                const int64_t left = a.pixels - static_cast<int64_t>(k) * t.rows;
-                const float m = static_cast<float>(left < t.rows ? (left > 0 ? left : 0) : t.rows) * D;
-                if (m == 0.0f) break;
-                const float d = (peer_load(s_piece + g, k) - mean) + peer_load(s_piece + CW + g, k);
-                low = fmaf(d, m / all, low);
-                m2 += fmaf(d * m, d, peer_load(s_piece + 2 * CW + g, k));
+                const float w = values(k), d = (s_piece[k * 3 * G + g] - mean) + s_piece[(k * 3 + 1) * G + g];
+                if (w == 0.0f) break;
+                low = fmaf(d, w * each_all, low);
+                m2 += fmaf(d * w, d, s_piece[(k * 3 + 2) * G + g]);
             }
             m2 -= all * low * low;
+            m = mean;
         }
-        const float var = fmaxf(m2 / all, 0.0f), m = mean + low, r = 1.0f / sqrtf(var + a.eps);
+        m += low;
+        const float r = 1.0f / sqrtf(fmaxf(m2 / all, 0.0f) + a.eps);
         s_mean[g] = m;
         s_rstd[g] = r;
         if (p.rank == 0) {
@@ -584,7 +808,6 @@ norm_cluster_kernel(NormArgs a, NormCluster t)
             if (a.rstd) a.rstd[at] = r;
         }
     }
-    if (t.ctas > 1) cluster_arrive();  // done with the peers' memory; waited for at the end
     __syncthreads();
     if (p.in) {
         float mean[P], scale[V], shift[V];
@@ -595,49 +818,86 @@ norm_cluster_kernel(NormArgs a, NormCluster t)
             scale[i] = s_rstd[ONE ? p.tx * V / D : (p.tx * V + i) / D] * s_weight[p.tx * V + i];
             shift[i] = s_bias[p.tx * V + i];
         }
-        T* y = static_cast<T*>(a.out);
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int r = p.row0 + p.ty + k * p.step;
-            if (r >= p.row_end) break;
+        const int64_t stride = static_cast<int64_t>(p.step) * a.channels;
+        int64_t at = (p.image * a.pixels + first) * a.channels + p.channel;
+        T* y = static_cast<T*>(a.out) + at;
+        const Pack<T, V>* from = keep;
+        for (int r = first; r < p.row_end; r += p.step, from += NT, at += stride, y += stride) {
             float v[V];
+            widen(v, *from);
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = fmaf(to_f32(q[k].v[i]) - mean[ONE ? 0 : i], scale[i], shift[i]);
+            for (int i = 0; i < V; ++i) v[i] = fmaf(v[i] - mean[ONE ? 0 : i], scale[i], shift[i]);
             act_values<V>(v, a.act);
-            const int64_t at = (p.image * a.pixels + r) * a.channels + p.channel;
             if (a.drop.limit < 65536u) drop<V>(v, static_cast<uint64_t>(at), a.drop);
-            store_row<T, V>(y + at, v);
+            store_row<T, V>(y, v);
         }
     }
-    if (t.ctas > 1) cluster_wait();
 }
 
-// The gradient: x stays packed and dz in binary32 (its activation is worked
-// out once).  Rank 0 writes the image's channel sums for dweight and dbias.
-template <typename T, int V, int NV, bool ONE>
-__global__ void __launch_bounds__(NT)
+// V numbers of binary32, 16 bytes at a time NT threads apart.
+template <int V>
+__device__ __forceinline__ void keep_floats(char* at, const float (&v)[V])
+{
+    constexpr int W = V < 4 ? V : 4;
+#pragma unroll
+    for (int i = 0; i < V; i += W) {
+        Pack<float, W> q;
+#pragma unroll
+        for (int j = 0; j < W; ++j) q.v[j] = v[i + j];
+        *reinterpret_cast<Pack<float, W>*>(at + (i / W) * NT * W * 4) = q;
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void kept_floats(float (&v)[V], const char* at)
+{
+    constexpr int W = V < 4 ? V : 4;
+#pragma unroll
+    for (int i = 0; i < V; i += W) {
+        const Pack<float, W> q = *reinterpret_cast<const Pack<float, W>*>(at + (i / W) * NT * W * 4);
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[i + j] = q.v[j];
+    }
+}
+
+// The gradient: x is kept as it came and dz in binary32 (its activation is
+// worked out once), in the place that dy was copied to.  The dropout's factor
+// is left to the sums and the weights.  Rank 0 writes the image's channel
+// sums for dweight and dbias.
+template <typename T, int V, bool ONE>
+__global__ void __launch_bounds__(NT, 3)
 norm_grad_cluster_kernel(NormArgs a, NormCluster t, NormScratch w)
 {
-    constexpr int P = ONE ? 1 : V;
-    extern __shared__ float smem[];
+    constexpr int P = ONE ? 1 : V, W = V < 4 ? V : 4;
+    constexpr int DZ = NT * V * 4;  // bytes of a pass's dz
+    extern __shared__ uint4 smem[];
     const int CW = t.wide * V, D = a.channels / a.groups;
-    float* part = smem;                   // [2][NT * V]
+    Pack<T, V>* keep = reinterpret_cast<Pack<T, V>*>(smem) + threadIdx.x;  // [held][NT]
+    char* base = reinterpret_cast<char*>(reinterpret_cast<Pack<T, V>*>(smem) + t.held * NT);
+    char* keep_dz = base + threadIdx.x * W * 4;                // [held][V / W][NT] of W floats
+    float* part = reinterpret_cast<float*>(base + t.held * DZ);  // [2][NT * V]
     float* s_weight = part + 2 * NT * V;  // [CW]
     float* s_bias = s_weight + CW;        // [CW]
     float* s_mine = s_bias + CW;          // [2][CW]: this block's sums by channel
-    float* s_all = s_mine + 2 * CW;       // [2][CW]: the image's
-    float* s_avg = s_all + 2 * CW;        // [2][CW]: averages by group
+    float* s_image = s_mine + 2 * CW;     // [ctas][2][CW]: the blocks', in rank 0
+    float* s_piece = s_image + 2 * t.ctas * CW;  // [ctas][2][G]: the blocks' sums by group, in every block
+    const int G = t.groups;
     const ClusterSpot p = cluster_spot<V>(a, t, D);
-    Pack<T, V> q[NV];
-    Pack<T, V> dq[NV];
-    const T* x = static_cast<const T*>(a.x) + p.image * a.x_image + p.channel;
-    const T* dy = static_cast<const T*>(a.dy) + p.image * a.dy_image + p.channel;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int r = p.row0 + p.ty + k * p.step;
-        if (p.in && r < p.row_end) {
-            q[k] = *reinterpret_cast<const Pack<T, V>*>(x + r * a.x_pixel);
-            dq[k] = *reinterpret_cast<const Pack<T, V>*>(dy + r * a.dy_pixel);
+    if (t.ctas > 1) cluster_arrive();  // every block has begun: waited for before the first store to a peer
+    const int first = p.in ? p.row0 + p.ty : p.row_end;  // a thread outside the map has no rows
+    {
+        const T* x = static_cast<const T*>(a.x) + p.image * a.x_image + first * a.x_pixel + p.channel;
+        const T* dy = static_cast<const T*>(a.dy) + p.image * a.dy_image + first * a.dy_pixel + p.channel;
+        const int64_t stride = p.step * a.x_pixel, dstride = p.step * a.dy_pixel;
+        Pack<T, V>* to = keep;
+        char* dto = keep_dz;
+        for (int r = first; r < p.row_end; r += p.step) {
+            copy_async<sizeof(T) * V>(to, x);
+            copy_async<sizeof(T) * V>(dto, dy);
+            x += stride;
+            dy += dstride;
+            to += NT;
+            dto += DZ;
         }
     }
     for (int c = threadIdx.x; c < CW && p.first_channel + c < a.channels; c += NT) {
@@ -651,60 +911,117 @@ norm_grad_cluster_kernel(NormArgs a, NormCluster t, NormScratch w)
         mean[i] = p.in ? a.mean[g] : 0.0f;
         rstd[i] = p.in ? a.rstd[g] : 0.0f;
     }
+    const float factor = a.drop.limit < 65536u ? a.drop.factor : 1.0f;
+    copies_done();
     __syncthreads();
-    float dz[NV][V], sa[V], sb[V];
+    float sa[V], sb[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) sa[i] = sb[i] = 0.0f;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int r = p.row0 + p.ty + k * p.step;
-        if (!p.in || r >= p.row_end) continue;
-        float z[V];
+    {
+        float weight[V], bias[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            dz[k][i] = to_f32(dq[k].v[i]);
-            z[i] = fmaf((to_f32(q[k].v[i]) - mean[ONE ? 0 : i]) * rstd[ONE ? 0 : i], s_weight[p.tx * V + i],
-                        s_bias[p.tx * V + i]);
+            weight[i] = s_weight[p.tx * V + i];
+            bias[i] = s_bias[p.tx * V + i];
         }
-        if (a.drop.limit < 65536u)
-            drop<V>(dz[k], static_cast<uint64_t>((p.image * a.pixels + r) * a.channels + p.channel), a.drop);
-        act_slopes<V>(dz[k], z, a.act);
+        const int64_t stride = static_cast<int64_t>(p.step) * a.channels;
+        int64_t at = (p.image * a.pixels + first) * a.channels + p.channel;
+        const Pack<T, V>* from = keep;
+        char* dat = keep_dz;
+        for (int r = first; r < p.row_end; r += p.step, at += stride, from += NT, dat += DZ) {
+            float u[V], z[V], dz[V];
+            widen(u, *from);
+            widen(dz, *reinterpret_cast<const Pack<T, V>*>(dat));
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            sa[i] += dz[k][i];
-            sb[i] = fmaf(dz[k][i], (to_f32(q[k].v[i]) - mean[ONE ? 0 : i]) * rstd[ONE ? 0 : i], sb[i]);
+            for (int i = 0; i < V; ++i) {
+                u[i] = (u[i] - mean[ONE ? 0 : i]) * rstd[ONE ? 0 : i];
+                z[i] = fmaf(u[i], weight[i], bias[i]);
+            }
+            if (a.drop.limit < 65536u) drop_mask<V>(dz, static_cast<uint64_t>(at), a.drop);
+            act_slopes<V>(dz, z, a.act);
+            keep_floats<V>(dat, dz);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                sa[i] += dz[i];
+                sb[i] = fmaf(dz[i], u[i], sb[i]);
+            }
         }
     }
-    if (p.ty < p.step) {
+    // Sums by channel over the block's rows: lanes of one channel by shuffles
+    // where the tile's rows are powers of two of lanes, then `lists` partial
+    // sums a channel, then one.
+    const bool fast = t.wide <= 32 && (t.wide & (t.wide - 1)) == 0;
+    int lists;
+    if (fast) {
+        lists = NT / 32;
+        for (int o = 16; o >= t.wide; o >>= 1)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            part[(p.ty * t.wide + p.tx) * V + i] = sa[i];
-            part[NT * V + (p.ty * t.wide + p.tx) * V + i] = sb[i];
+            for (int i = 0; i < V; ++i) {
+                sa[i] += __shfl_xor_sync(FULL, sa[i], o);
+                sb[i] += __shfl_xor_sync(FULL, sb[i], o);
+            }
+        if (static_cast<int>(lane_id()) < t.wide)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                part[static_cast<int>(threadIdx.x) / 32 * CW + p.tx * V + i] = sa[i];
+                part[NT * V + static_cast<int>(threadIdx.x) / 32 * CW + p.tx * V + i] = sb[i];
+            }
+    } else {
+        lists = CW < NT ? NT / CW : 1;
+        if (p.ty < p.step) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                part[(p.ty * t.wide + p.tx) * V + i] = sa[i];
+                part[NT * V + (p.ty * t.wide + p.tx) * V + i] = sb[i];
+            }
         }
+        __syncthreads();
+        for (int k = threadIdx.x; k < lists * CW; k += NT) {
+            float va = 0.0f, vb = 0.0f;
+            for (int y = k / CW; y < p.step; y += lists) {
+                va += part[y * CW + k % CW];
+                vb += part[NT * V + y * CW + k % CW];
+            }
+            // Entry k is read by this thread alone.
+            part[k] = va;
+            part[NT * V + k] = vb;
+        }
+        if (lists > p.step) lists = p.step;
     }
-    // Sums by channel over the block's rows, in two steps: `lists` threads a channel, then one.
-    const int lists = CW < NT ? NT / CW : 1;
     __syncthreads();
-    for (int k = threadIdx.x; k < lists * CW; k += NT) {
-        const int c = k % CW;
-        float va = 0.0f, vb = 0.0f;
-        for (int y = k / CW; y < p.step; y += lists) {
-            va += part[y * CW + c];
-            vb += part[NT * V + y * CW + c];
-        }
-        // Each entry (k / CW, c) was read by this thread alone.
-        part[k] = va;
-        part[NT * V + k] = vb;
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < CW; c += NT) {
+    if (t.ctas > 1) cluster_wait();
+    for (int c = threadIdx.x; c < CW && p.first_channel + c < a.channels; c += NT) {
         float va = 0.0f, vb = 0.0f;
         for (int y = 0; y < lists; ++y) {
             va += part[y * CW + c];
             vb += part[NT * V + y * CW + c];
         }
-        s_mine[c] = va;
-        s_mine[CW + c] = vb;
+        va *= factor;
+        vb *= factor;
+        s_mine[c] = va * s_weight[c];
+        s_mine[CW + c] = vb * s_weight[c];
+        if (t.ctas > 1) {
+            peer_store(s_image + p.rank * 2 * CW + c, 0, va);
+            peer_store(s_image + (p.rank * 2 + 1) * CW + c, 0, vb);
+        } else {
+            s_image[c] = va;
+            s_image[CW + c] = vb;
+        }
+    }
+    __syncthreads();
+    // A thread adds up a small group, a warp a large one.
+    const int team = D > 32 ? 32 : 1;
+    for (int k = static_cast<int>(threadIdx.x) / team; k < 2 * p.groups; k += NT / team) {
+        const int q = k / p.groups, g = k % p.groups, l = static_cast<int>(threadIdx.x) % team;
+        float v = 0.0f;
+        for (int i = l; i < D; i += team) v += s_mine[q * CW + g * D + i];
+        if (team > 1) v = warp_sum(v);
+        if (l != 0) continue;
+        float* at = s_piece + (p.rank * 2 + q) * G + g;
+        if (t.ctas > 1)
+            for (int r = 0; r < t.ctas; ++r) peer_store(at, r, v);
+        else
+            *at = v;
     }
     if (t.ctas > 1) {
         cluster_arrive();
@@ -712,50 +1029,54 @@ norm_grad_cluster_kernel(NormArgs a, NormCluster t, NormScratch w)
     } else {
         __syncthreads();
     }
-    for (int c = threadIdx.x; c < CW && p.first_channel + c < a.channels; c += NT) {
-        float va = 0.0f, vb = 0.0f;
-        if (t.ctas == 1) {
-            va = s_mine[c];
-            vb = s_mine[CW + c];
-        } else {
-            for (int k = 0; k < t.ctas; ++k) {
-                va += peer_load(s_mine + c, k);
-                vb += peer_load(s_mine + CW + c, k);
+    if (p.rank == 0)
+        for (int c = threadIdx.x; c < CW && p.first_channel + c < a.channels; c += NT) {
+            float va = 0.0f, vb = 0.0f;
+            for (int r = 0; r < t.ctas; ++r) {
+                va += s_image[r * 2 * CW + c];
+                vb += s_image[(r * 2 + 1) * CW + c];
             }
+            w.ca[p.image * a.channels + p.first_channel + c] = va;
+            w.cb[p.image * a.channels + p.first_channel + c] = vb;
         }
-        s_all[c] = va * s_weight[c];
-        s_all[CW + c] = vb * s_weight[c];
-        if (p.rank == 0) {
-            w.pa[p.image * a.channels + p.first_channel + c] = va;
-            w.pb[p.image * a.channels + p.first_channel + c] = vb;
-        }
-    }
-    if (t.ctas > 1) cluster_arrive();
-    sum_groups<2>(s_all, CW, CW, D, 1, p.groups, s_avg, CW);
     if (p.in) {
         const float each_n = 1.0f / (static_cast<float>(a.pixels) * static_cast<float>(D));
         float m1[P], m2[P];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int g = (p.tx * V + i) / D;
-            m1[i] = s_avg[g] * each_n;
-            m2[i] = s_avg[CW + g] * each_n;
-        }
-        T* dx = static_cast<T*>(a.out);
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int r = p.row0 + p.ty + k * p.step;
-            if (r >= p.row_end) break;
-            float v[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float u = (to_f32(q[k].v[i]) - mean[ONE ? 0 : i]) * rstd[ONE ? 0 : i];
-                v[i] = rstd[ONE ? 0 : i] * (fmaf(dz[k][i], s_weight[p.tx * V + i], -m1[ONE ? 0 : i]) - u * m2[ONE ? 0 : i]);
+            float va = 0.0f, vb = 0.0f;
+            for (int r = 0; r < t.ctas; ++r) {
+                va += s_piece[r * 2 * G + g];
+                vb += s_piece[(r * 2 + 1) * G + g];
             }
-            store_row<T, V>(dx + (p.image * a.pixels + r) * a.channels + p.channel, v);
+            m1[i] = va * each_n;
+            m2[i] = vb * each_n;
+        }
+        // dx = dz * (weight * factor * rstd) - (x - mean) * (rstd^2 * m2) - rstd * m1.
+        float scale[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) scale[i] = s_weight[p.tx * V + i] * factor * rstd[ONE ? 0 : i];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            m1[i] *= -rstd[i];
+            m2[i] *= -rstd[i] * rstd[i];
+        }
+        const int64_t stride = static_cast<int64_t>(p.step) * a.channels;
+        T* dx = static_cast<T*>(a.out) + (p.image * a.pixels + first) * a.channels + p.channel;
+        const Pack<T, V>* from = keep;
+        const char* dat = keep_dz;
+#pragma unroll 2
+        for (int r = first; r < p.row_end; r += p.step, dx += stride, from += NT, dat += DZ) {
+            float x[V], dz[V];
+            widen(x, *from);
+            kept_floats<V>(dz, dat);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                dz[i] = fmaf(dz[i], scale[i], fmaf(x[i] - mean[ONE ? 0 : i], m2[ONE ? 0 : i], m1[ONE ? 0 : i]));
+            store_row<T, V>(dx, dz);
         }
     }
-    if (t.ctas > 1) cluster_wait();
 }
 
 // ------------------------------------------------------------------- launches
@@ -780,7 +1101,8 @@ inline NormTile tile(const NormArgs& a, int v)
     const int vecs = a.channels / v;
     t.wide = vecs <= 64 ? vecs : 32;
     t.tiles = (vecs + t.wide - 1) / t.wide;
-    t.pieces = norm_pieces(a.batch, a.pixels);
+    t.pieces = static_cast<int>(norm_pieces(a.batch, a.pixels, a.channels));
+    t.per = static_cast<int>((a.pixels + t.pieces - 1) / t.pieces);
     return t;
 }
 
@@ -788,6 +1110,7 @@ inline NormTile tile(const NormArgs& a, int v)
 template <typename K, typename... Args>
 static void launch_clusters(K k, const NormArgs& a, const NormCluster& t, size_t smem, cudaStream_t st, Args... args)
 {
+    if (smem > 48 * 1024) ensure_dynamic_smem(reinterpret_cast<const void*>(k), smem);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.batch * t.tiles * t.ctas));
     cfg.blockDim = dim3(NT);
@@ -802,88 +1125,107 @@ static void launch_clusters(K k, const NormArgs& a, const NormCluster& t, size_t
     cudaLaunchKernelEx(&cfg, k, a, t, args...);
 }
 
-// f(NV) with the first of the counts that holds n vectors.
-template <int NV, int... MORE, typename F>
-static void pick_held(int n, F f)
-{
-    if constexpr (sizeof...(MORE) == 0) {
-        f(std::integral_constant<int, NV>{});
-    } else {
-        if (n <= NV) f(std::integral_constant<int, NV>{});
-        else pick_held<MORE...>(n, f);
-    }
-}
-
-// The cluster kernels, where a slab fits (else false).  A thread holds up to
-// 64 elements forward, 32 of x and dz each backward; row segments are of 64
-// bytes, or of 32 where that makes the slab fit.
+// The cluster kernels, where a slab fits (else false).  Small blocks before
+// large ones, and row segments of 64 bytes before 32.
 template <typename T, int V>
 static bool norm_in_clusters(const NormArgs& a, void* ws, cudaStream_t st, bool grad)
 {
     const int e = sizeof(T), D = a.channels / a.groups, vecs = a.channels / V;
-    const int most = (grad ? 32 : 64) / V;
+    // Beyond these sizes streaming is faster (16 x 6400 x 256 bf16, 52 MB: 57 against 34 us forward, 89 against 65
+    // backward; 4 x 6400 x 256, 13 MB: 17 against 27 forward, 25 against 27 backward; 16 x 1600 x 256, 13 MB: 16
+    // against 19 forward, 38 against 26 backward).
+    if (static_cast<double>(a.batch) * a.pixels * a.channels * e > (grad ? 8e6 : 16e6)) return false;
     int whole = 1;  // vectors that hold whole groups: lcm(D, V) / V
     while (whole * V % D != 0) ++whole;
-    for (int bytes = 64; bytes >= 32; bytes /= 2) {
-        NormCluster t{};
-        const int want = bytes / (V * e) > 0 ? bytes / (V * e) : 1;
-        t.wide = (want + whole - 1) / whole * whole;
-        if (t.wide > vecs) t.wide = vecs;
-        if (t.wide > 64) return false;
-        t.tiles = (vecs + t.wide - 1) / t.wide;
-        const int step = NT / t.wide;
-        const int64_t passes = (a.pixels + step - 1) / step;
-        for (t.ctas = 1; t.ctas < 8 && passes > static_cast<int64_t>(t.ctas) * most; t.ctas *= 2) {}
-        if (passes > static_cast<int64_t>(t.ctas) * most || a.batch * t.tiles * t.ctas > INT32_MAX) continue;
-        const int held = static_cast<int>((passes + t.ctas - 1) / t.ctas), CW = t.wide * V;
-        t.rows = held * step;
-        const bool one = D % V == 0;
-        if (!grad) {
-            const size_t smem = 4 * (2 * NT * (one ? 1 : V) + 9 * static_cast<size_t>(CW));
-            pick_held<16 / V, 32 / V, 64 / V>(held, [&](auto count) {
-                constexpr int NV = decltype(count)::value;
-                launch_clusters(one ? norm_cluster_kernel<T, V, NV, true> : norm_cluster_kernel<T, V, NV, false>, a, t,
-                                smem, st);
-            });
-        } else {
-            const size_t smem = 4 * (2 * NT * V + 8 * static_cast<size_t>(CW));
-            const NormScratch w = scratch(a, ws);
-            pick_held<8 / V, 16 / V, 32 / V>(held, [&](auto count) {
-                constexpr int NV = decltype(count)::value;
-                launch_clusters(one ? norm_grad_cluster_kernel<T, V, NV, true> : norm_grad_cluster_kernel<T, V, NV, false>,
-                                a, t, smem, st, w);
-            });
-            if (a.dweight || a.dbias)
-                norm_grad_param_kernel<<<(a.channels + 31) / 32, NT, 0, st>>>(a, a.batch, w.pa, w.pb);
+    const int pass = NT * V * (grad ? e + 4 : e);  // bytes that a pass over the block's rows keeps
+    for (const int room : {36 * 1024, 72 * 1024, 108 * 1024})
+        for (int bytes = 64; bytes >= 32; bytes /= 2) {
+            NormCluster t{};
+            const int want = bytes / (V * e) > 0 ? bytes / (V * e) : 1;
+            t.wide = (want + whole - 1) / whole * whole;
+            if (t.wide > vecs) t.wide = vecs;
+            if (t.wide > 64) return false;
+            t.tiles = (vecs + t.wide - 1) / t.wide;
+            const int step = NT / t.wide, most = room / pass;
+            const int64_t passes = (a.pixels + step - 1) / step;
+            for (t.ctas = 1; t.ctas < 8 && passes > static_cast<int64_t>(t.ctas) * most; t.ctas *= 2) {}
+            if (passes > static_cast<int64_t>(t.ctas) * most || a.batch * t.tiles * t.ctas > INT32_MAX) continue;
+            t.held = static_cast<int>((passes + t.ctas - 1) / t.ctas);
+            t.rows = t.held * step;
+            const int CW = t.wide * V;
+            t.groups = CW / D;
+            if (t.groups > NT) return false;
+            const bool one = D % V == 0;
+            auto power = [](int n) { return (n & (n - 1)) == 0; };
+            t.shuffles = one && t.wide <= 32 && power(t.wide) && power(D / V);
+            if (!grad) {
+                const size_t smem = static_cast<size_t>(t.held) * pass +
+                                    4 * (2 * NT * (one ? 1 : V) + 2 * static_cast<size_t>(CW) + (4 + 3 * t.ctas) * t.groups);
+                launch_clusters(one ? norm_cluster_kernel<T, V, true> : norm_cluster_kernel<T, V, false>, a, t, smem, st);
+            } else {
+                const size_t smem = static_cast<size_t>(t.held) * pass +
+                                    4 * (2 * NT * V + (4 + 2 * t.ctas) * static_cast<size_t>(CW) + 2 * t.ctas * t.groups);
+                const NormScratch w = scratch(a, ws);
+                launch_clusters(one ? norm_grad_cluster_kernel<T, V, true> : norm_grad_cluster_kernel<T, V, false>, a, t,
+                                smem, st, w);
+                if (a.dweight || a.dbias)
+                    launch_pdl(norm_grad_param_kernel, dim3((a.channels + NT - 1) / NT), dim3(NT), 0, st, a, w);
+            }
+            return true;
         }
-        return true;
-    }
     return false;
+}
+
+template <typename T, int V, bool ONE, int ACT>
+static void norm_streamed(const NormArgs& a, void* ws, cudaStream_t st, bool grad)
+{
+    const NormTile t = tile(a, V);
+    const NormScratch w = scratch(a, ws);
+    const dim3 grid(static_cast<unsigned>(a.batch * t.pieces), t.tiles), block(NT);
+    const int D = a.channels / a.groups;
+    if (!grad) {
+        NormArgs b = a;
+        if (!b.mean) b.mean = w.ga;
+        if (!b.rstd) b.rstd = w.gb;
+        norm_partial_kernel<T, V, ONE><<<grid, block, 0, st>>>(b, t, w);
+        const int each = ONE ? D / V : D, values = ONE ? V : 1;
+        const int64_t groups = a.batch * a.groups;
+        if (t.pieces * each > 128)
+            launch_pdl(norm_finish_kernel<NT>, dim3(static_cast<unsigned>(groups)), block, 0, st, b, t, w, each, values);
+        else
+            launch_pdl(norm_finish_kernel<32>, dim3(static_cast<unsigned>((groups + NT / 32 - 1) / (NT / 32))), block, 0,
+                       st, b, t, w, each, values);
+        launch_pdl(norm_apply_kernel<T, V, ONE, ACT>, grid, block, 0, st, b, t);
+    } else {
+        const int chunk = D > 32 ? D : 32 / D * D;
+        norm_grad_partial_kernel<T, V, ONE, ACT><<<grid, block, 0, st>>>(a, t, w);
+        if (chunk > 4096) ensure_dynamic_smem(reinterpret_cast<const void*>(norm_grad_finish_kernel<T>), 8 * static_cast<size_t>(chunk));
+        launch_pdl(norm_grad_finish_kernel<T>,
+                   dim3(static_cast<unsigned>(a.batch), static_cast<unsigned>((a.channels + chunk - 1) / chunk)), block,
+                   8 * static_cast<size_t>(chunk), st, a, t, w, chunk);
+        const unsigned params = a.dweight || a.dbias ? (a.channels + NT - 1) / NT : 0;
+        launch_pdl(norm_grad_apply_kernel<T, V, ONE, ACT>, dim3(grid.x + params, grid.y), block, 0, st, a, t, w);
+    }
+}
+
+template <typename T, int V, bool ONE>
+static void norm_streamed(const NormArgs& a, void* ws, cudaStream_t st, bool grad)
+{
+    switch (a.act) {
+    case NMS_ACT_RELU: return norm_streamed<T, V, ONE, NMS_ACT_RELU>(a, ws, st, grad);
+    case NMS_ACT_SILU: return norm_streamed<T, V, ONE, NMS_ACT_SILU>(a, ws, st, grad);
+    case NMS_ACT_GELU: return norm_streamed<T, V, ONE, NMS_ACT_GELU>(a, ws, st, grad);
+    default: return norm_streamed<T, V, ONE, NMS_ACT_NONE>(a, ws, st, grad);
+    }
 }
 
 template <typename T, int V>
 static void norm_width(const NormArgs& a, void* ws, cudaStream_t st, bool grad)
 {
-    if constexpr (V > 1)
+    if constexpr (V * sizeof(T) >= 4)
         if (norm_in_clusters<T, V>(a, ws, st, grad)) return;
-    const NormTile t = tile(a, V);
-    const NormScratch w = scratch(a, ws);
-    const dim3 grid(static_cast<unsigned>(a.batch * t.pieces), t.tiles);
-    const unsigned finish = static_cast<unsigned>((a.batch * a.groups + NT / 32 - 1) / (NT / 32));
-    if (!grad) {
-        NormArgs b = a;
-        if (!b.mean) b.mean = w.ga;
-        if (!b.rstd) b.rstd = w.gb;
-        norm_partial_kernel<T, V><<<grid, NT, 0, st>>>(b, t, w);
-        norm_finish_kernel<<<finish, NT, 0, st>>>(b, t, w);
-        norm_apply_kernel<T, V><<<grid, NT, 0, st>>>(b, t);
-    } else {
-        norm_grad_partial_kernel<T, V><<<grid, NT, 0, st>>>(a, t, w);
-        norm_grad_finish_kernel<T><<<finish, NT, 0, st>>>(a, t, w);
-        norm_grad_apply_kernel<T, V><<<grid, NT, 0, st>>>(a, t, w);
-        if (a.dweight || a.dbias)
-            norm_grad_param_kernel<<<(a.channels + 31) / 32, NT, 0, st>>>(a, a.batch * t.pieces, w.pa, w.pb);
-    }
+    if (a.channels / a.groups % V == 0) norm_streamed<T, V, true>(a, ws, st, grad);
+    else if constexpr (V > 1) norm_streamed<T, V, false>(a, ws, st, grad);
 }
 
 template <typename T>

@@ -71,34 +71,6 @@ __device__ __forceinline__ uint32_t spread_byte_bits(uint32_t x)
     return y;
 }
 
-template <typename T> __device__ __forceinline__ uint32_t pack_two(float lo, float hi);
-template <> __device__ __forceinline__ uint32_t pack_two<__half>(float lo, float hi)
-{
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <> __device__ __forceinline__ uint32_t pack_two<__nv_bfloat16>(float lo, float hi)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <> __device__ __forceinline__ uint32_t pack_two<float>(float, float) { return 0; }  // never called
-
-// Rounds EV results to their type.
-template <typename T, int EV>
-__device__ __forceinline__ Pack<T, EV> pack_results(const float (&x)[EV])
-{
-    Pack<T, EV> q;
-    if constexpr (sizeof(T) == 2 && EV % 2 == 0) {
-#pragma unroll
-        for (int e = 0; e < EV; e += 2) reinterpret_cast<uint32_t*>(&q)[e / 2] = pack_two<T>(x[e], x[e + 1]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < EV; ++e) q.v[e] = from_f32<T>(x[e]);
-    }
-    return q;
-}
-
 __device__ __forceinline__ void unpack_two(uint32_t w, float& lo, float& hi, __nv_bfloat16)
 {
     lo = __uint_as_float(w << 16);
