@@ -11,8 +11,8 @@ greedy_iou_nms_gb300.autograd has the same operators for torch's autograd.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
-from typing import Optional
 
 NMS_TYPE_F32 = 0
 NMS_TYPE_F16 = 1
@@ -57,9 +57,15 @@ def declare(lib) -> None:
         fn.restype = ctypes.c_int
 
 
+_loaded = None
+
+
 def _lib():
-    from . import load
-    return load()
+    global _loaded
+    if _loaded is None:
+        from . import load
+        _loaded = load()
+    return _loaded
 
 
 def _raise(code: int, where: str):
@@ -75,6 +81,7 @@ def nms_dropout_run(x: int, residual: int, type: int, n: int, drop_p: float, see
                                   stream or None)
 
 
+@functools.lru_cache(maxsize=4096)
 def nms_group_norm_workspace_size(batch: int, pixels: int, channels: int, groups: int) -> int:
     out = ctypes.c_size_t(0)
     st = _lib().nms_group_norm_workspace_size(batch, pixels, channels, groups, ctypes.byref(out))
@@ -118,6 +125,7 @@ def nms_relation_softmax_run(scores: int, type: int, batch: int, heads: int, que
                                            stream or None)
 
 
+@functools.lru_cache(maxsize=4096)
 def nms_relation_grad_workspace_size(batch: int, heads: int, queries: int, keys: int, num_buckets: int) -> int:
     out = ctypes.c_size_t(0)
     st = _lib().nms_relation_grad_workspace_size(batch, heads, queries, keys, num_buckets, ctypes.byref(out))
@@ -139,15 +147,18 @@ def nms_relation_softmax_grad_run(dprobs: int, probs: int, type: int, batch: int
 # ----------------------------------------------------------- tensor helpers
 
 _torch_module = None
-_types = None
+_types = {}
+_raw_stream = None
 
 
 def _torch():
-    global _torch_module, _types
+    global _torch_module, _raw_stream
     if _torch_module is None:
         import torch
+        _types.update({torch.float32: NMS_TYPE_F32, torch.float16: NMS_TYPE_F16, torch.bfloat16: NMS_TYPE_BF16})
+        # The current stream's handle without a Stream object around it, where this torch has that.
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _torch_module = torch
-        _types = {torch.float32: NMS_TYPE_F32, torch.float16: NMS_TYPE_F16, torch.bfloat16: NMS_TYPE_BF16}
     return _torch_module
 
 
@@ -160,7 +171,14 @@ def _type(x, where: str, name: str) -> int:
 
 
 def _stream(x) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(x.get_device())
     return _torch().cuda.current_stream(x.device).cuda_stream
+
+
+def _like(x):
+    """An uninitialised contiguous tensor of x's shape and type."""
+    return _torch_module.empty_like(x, memory_format=_torch_module.contiguous_format)
 
 
 def _same(x, like, where: str, name: str) -> None:
@@ -168,29 +186,28 @@ def _same(x, like, where: str, name: str) -> None:
         raise ValueError(f"{where}: {name} must have the shape, type and device of the other operand")
 
 
-def _probability(p: float, where: str) -> None:
+def _drop_numbers(p: float, seed: int, offset: int, where: str) -> None:
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"{where}: p must lie in [0, 1]")
-
-
-def _number(v: int, where: str, name: str) -> int:
-    if not 0 <= v < 1 << 64:
-        raise ValueError(f"{where}: {name} must be an integer of 64 bits, not negative")
-    return v
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError(f"{where}: seed and offset must be integers of 64 bits, not negative")
 
 
 def _map(x, where: str):
     """(tensor, image stride, pixel stride, batch, pixels, channels) of a
     channels-last map [batch, ..., channels]; copied only where its pixels do
     not lie at one stride."""
-    if x.dim() < 2:
+    shape = x.shape
+    if len(shape) < 2:
         raise ValueError(f"{where}: the map must be [batch, ..., channels]")
-    shape, stride = x.shape, x.stride()
     batch, channels, pixels = shape[0], shape[-1], 1
     for n in shape[1:-1]:
         pixels *= n
+    if x.is_contiguous():
+        return x, channels * pixels, channels, batch, pixels, channels
     # One pixel stride: the last pixel axis of more than one entry sets it and
     # each axis before it spans the axes after it.
+    stride = x.stride()
     step, span, fits = channels, None, channels <= 1 or stride[-1] == 1
     for n, s in zip(reversed(shape[1:-1]), reversed(stride[1:-1])):
         if n == 1:
@@ -201,11 +218,9 @@ def _map(x, where: str):
         elif s != span:
             fits = False
         span = s * n
-    image = stride[0] if batch > 1 else 0
-    if not fits or image < 0:
-        x = x.contiguous()
-        step, image = channels, channels * pixels
-    return x, image, step, batch, pixels, channels
+    if not fits:
+        return x.contiguous(), channels * pixels, channels, batch, pixels, channels
+    return x, stride[0] if batch > 1 else 0, step, batch, pixels, channels
 
 
 def _params(x, channels: int, weight, bias, where: str):
@@ -235,23 +250,22 @@ def group_norm_act(x, groups: int, weight=None, bias=None, *, eps: float = 1e-5,
     element's index, as `dropout`.  With return_stats also mean and rstd
     [batch, groups] (float32), which `group_norm_act_grad` takes.
     """
-    where = "group_norm_act"
-    kind = _type(x, where, "x")
-    if act not in _ACTS:
+    kind = _type(x, "group_norm_act", "x")
+    code = _ACTS.get(act)
+    if code is None:
         raise ValueError("group_norm_act: act must be 'none', 'relu', 'silu' or 'gelu'")
-    _probability(p, where)
-    torch = _torch()
-    xs, image, pixel, batch, pixels, channels = _map(x, where)
-    wp, bp, ptype = _params(x, channels, weight, bias, where)
-    dev = x.device
+    _drop_numbers(p, seed, offset, "group_norm_act")
+    torch = _torch_module
+    xs, image, pixel, batch, pixels, channels = _map(x, "group_norm_act")
+    wp, bp, ptype = _params(x, channels, weight, bias, "group_norm_act")
     wsb = nms_group_norm_workspace_size(batch, pixels, channels, groups)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    mean = torch.empty((batch, groups), dtype=torch.float32, device=dev) if return_stats else None
-    rstd = torch.empty_like(mean) if return_stats else None
-    ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
+    y, mean, rstd = _like(x), None, None
+    if return_stats:
+        mean = torch.empty((batch, groups), dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=x.device)
     st = _lib().nms_group_norm_run(xs.data_ptr(), image, pixel, kind, batch, pixels, channels, groups, wp, bp, ptype,
-                                   eps, _ACTS[act], p, _number(seed, where, "seed"),
-                                   _number(offset, where, "offset"), y.data_ptr(),
+                                   eps, code, p, seed, offset, y.data_ptr(),
                                    mean.data_ptr() if return_stats else None,
                                    rstd.data_ptr() if return_stats else None, ws.data_ptr(), wsb, _stream(x))
     if st:
@@ -267,27 +281,27 @@ def group_norm_act_grad(dy, x, mean, rstd, groups: int, weight=None, bias=None, 
     where = "group_norm_act_grad"
     kind = _type(x, where, "x")
     _same(dy, x, where, "dy")
-    if act not in _ACTS:
+    code = _ACTS.get(act)
+    if code is None:
         raise ValueError("group_norm_act_grad: act must be 'none', 'relu', 'silu' or 'gelu'")
-    _probability(p, where)
-    torch = _torch()
+    _drop_numbers(p, seed, offset, where)
+    torch = _torch_module
     xs, image, pixel, batch, pixels, channels = _map(x, where)
     dys, dimage, dpixel = _map(dy, where)[:3]
     wp, bp, ptype = _params(x, channels, weight, bias, where)
-    dev = x.device
-    for name, s in (("mean", mean), ("rstd", rstd)):
-        if s.shape != (batch, groups) or s.dtype != torch.float32 or s.device != dev or not s.is_contiguous():
-            raise ValueError(f"group_norm_act_grad: {name} must be a contiguous float32 [batch, groups] tensor")
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dparam = torch.empty((2, channels), dtype=torch.float32, device=dev)
-    dweight, dbias = dparam.unbind(0)
+    for s in (mean, rstd):
+        if s.shape != (batch, groups) or s.dtype != torch.float32 or s.device != x.device or not s.is_contiguous():
+            raise ValueError("group_norm_act_grad: mean and rstd must be contiguous float32 [batch, groups] tensors "
+                             "beside x")
     wsb = nms_group_norm_workspace_size(batch, pixels, channels, groups)
-    ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
+    dx = _like(x)
+    dweight = torch.empty(channels, dtype=torch.float32, device=x.device)
+    dbias = torch.empty_like(dweight)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=x.device)
     st = _lib().nms_group_norm_grad_run(dys.data_ptr(), dimage, dpixel, xs.data_ptr(), image, pixel, kind, batch,
                                         pixels, channels, groups, mean.data_ptr(), rstd.data_ptr(), wp, bp, ptype,
-                                        _ACTS[act], p, _number(seed, where, "seed"),
-                                        _number(offset, where, "offset"), dx.data_ptr(), dweight.data_ptr(),
-                                        dbias.data_ptr(), ws.data_ptr(), wsb, _stream(x))
+                                        code, p, seed, offset, dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(),
+                                        ws.data_ptr(), wsb, _stream(x))
     if st:
         _raise(st, "nms_group_norm_grad_run")
     return dx, dweight, dbias
@@ -297,17 +311,15 @@ def dropout(x, p: float, seed: int, offset: int = 0, *, residual=None):
     """residual + x * mask / keep (no residual: the product alone), the mask a
     function of (seed, offset, element index): the same numbers give the same
     mask.  keep = 1 - p, rounded to a 65536th."""
-    where = "dropout"
-    kind = _type(x, where, "x")
-    _probability(p, where)
+    kind = _type(x, "dropout", "x")
+    _drop_numbers(p, seed, offset, "dropout")
     if residual is not None:
-        _same(residual, x, where, "residual")
+        _same(residual, x, "dropout", "residual")
         residual = residual.contiguous()
     x = x.contiguous()
-    y = _torch().empty(x.shape, dtype=x.dtype, device=x.device)
+    y = _like(x)
     st = _lib().nms_dropout_run(x.data_ptr(), None if residual is None else residual.data_ptr(), kind, x.numel(), p,
-                                _number(seed, where, "seed"), _number(offset, where, "offset"), y.data_ptr(),
-                                _stream(x))
+                                seed, offset, y.data_ptr(), _stream(x))
     if st:
         _raise(st, "nms_dropout_run")
     return y
@@ -357,31 +369,32 @@ def relation_buckets(q_pos, k_pos, lut):
     k_pos [sets or 1, keys, axes] and lut [axes, 2 * reach + 1] (see
     `relation_lut_log`, `relation_lut_cells`); -1 masks the pair."""
     torch = _torch()
-    for name, t, dims in (("q_pos", q_pos, 3), ("k_pos", k_pos, 3), ("lut", lut, 2)):
-        if not t.is_cuda or t.dtype != torch.int32 or t.dim() != dims or t.device != q_pos.device:
-            raise ValueError(f"relation_buckets: {name} must be an int32 CUDA tensor of {dims} dimensions")
-    if q_pos.shape[2] != k_pos.shape[2] or lut.shape[0] != q_pos.shape[2] or lut.shape[1] % 2 == 0:
+    if not (q_pos.dtype == k_pos.dtype == lut.dtype == torch.int32 and q_pos.is_cuda and
+            q_pos.device == k_pos.device == lut.device):
+        raise ValueError("relation_buckets: q_pos, k_pos and lut must be int32 tensors on one CUDA device")
+    if q_pos.dim() != 3 or k_pos.dim() != 3 or lut.dim() != 2:
+        raise ValueError("relation_buckets: positions must be [sets, length, axes] and lut [axes, 2 * reach + 1]")
+    (qs, Q, axes), (ks, K, k_axes), (l_axes, width) = q_pos.shape, k_pos.shape, lut.shape
+    if axes != k_axes or axes != l_axes or width % 2 == 0:
         raise ValueError("relation_buckets: lut must be [axes, 2 * reach + 1] with the positions' axes")
-    q_pos, k_pos, lut = q_pos.contiguous(), k_pos.contiguous(), lut.contiguous()
-    qs, Q, axes = q_pos.shape
-    ks, K, _ = k_pos.shape
     if qs != ks and qs != 1 and ks != 1:
         raise ValueError("relation_buckets: q_pos and k_pos must have as many sets, or one of them one")
+    q_pos, k_pos, lut = q_pos.contiguous(), k_pos.contiguous(), lut.contiguous()
     out = torch.empty((ks if qs == 1 else qs, Q, K), dtype=torch.int16, device=q_pos.device)
     st = _lib().nms_relation_buckets_run(q_pos.data_ptr(), qs, k_pos.data_ptr(), ks, Q, K, axes, lut.data_ptr(),
-                                         lut.shape[1] // 2, out.data_ptr(), _stream(q_pos))
+                                         width // 2, out.data_ptr(), _stream(q_pos))
     if st:
         _raise(st, "nms_relation_buckets_run")
     return out
 
 
 def _relation(scores, buckets, key_mask, where: str):
-    torch = _torch()
+    torch = _torch_module
     if scores.dim() != 4:
         raise ValueError(f"{where}: scores must be [batch, heads, queries, keys]")
     B, H, Q, K = scores.shape
-    if not buckets.is_cuda or buckets.dtype != torch.int16 or buckets.dim() != 3 or buckets.device != scores.device or \
-            buckets.shape[0] not in (1, B) or buckets.shape[1:] != (Q, K):
+    if buckets.dtype != torch.int16 or buckets.device != scores.device or buckets.dim() != 3 or \
+            buckets.shape[0] not in (1, B) or buckets.shape[1] != Q or buckets.shape[2] != K:
         raise ValueError(f"{where}: buckets must be int16 [1 or batch, queries, keys] beside the scores")
     if key_mask is not None:
         if key_mask.shape != (B, K) or key_mask.dtype not in (torch.bool, torch.uint8) or \
@@ -401,14 +414,14 @@ def relation_softmax(scores, table, buckets, *, scale: float = 1.0, key_mask=Non
     a row without valid pairs is all 0.  Returns weights like scores.
     """
     where = "relation_softmax"
-    torch = _torch()
     kind = _type(scores, where, "scores")
+    torch = _torch_module
     B, H, Q, K, buckets, key_mask = _relation(scores, buckets, key_mask, where)
     if table.dim() != 2 or table.shape[1] != H or table.device != scores.device:
         raise ValueError("relation_softmax: table must be [num_buckets, heads] beside the scores")
     table = table.to(torch.float32).contiguous()
     scores = scores.contiguous()
-    out = torch.empty(scores.shape, dtype=scores.dtype, device=scores.device)
+    out = _like(scores)
     st = _lib().nms_relation_softmax_run(scores.data_ptr(), kind, B, H, Q, K, buckets.data_ptr(), buckets.shape[0],
                                          table.data_ptr(), table.shape[0],
                                          None if key_mask is None else key_mask.data_ptr(), scale, out.data_ptr(),
@@ -423,15 +436,15 @@ def relation_softmax_grad(dprobs, probs, buckets, num_buckets: int, *, scale: fl
     [num_buckets, heads]) from the incoming gradient and the forward's
     weights, map, scale and mask."""
     where = "relation_softmax_grad"
-    torch = _torch()
     kind = _type(probs, where, "probs")
+    torch = _torch_module
     _same(dprobs, probs, where, "dprobs")
     B, H, Q, K, buckets, key_mask = _relation(probs, buckets, key_mask, where)
     dprobs, probs = dprobs.contiguous(), probs.contiguous()
     dev = probs.device
     wsb = nms_relation_grad_workspace_size(B, H, Q, K, num_buckets)
     ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
-    ds = torch.empty(probs.shape, dtype=probs.dtype, device=dev)
+    ds = _like(probs)
     dtable = torch.empty((num_buckets, H), dtype=torch.float32, device=dev)
     st = _lib().nms_relation_softmax_grad_run(dprobs.data_ptr(), probs.data_ptr(), kind, B, H, Q, K,
                                               buckets.data_ptr(), buckets.shape[0], num_buckets,
