@@ -8,35 +8,78 @@ namespace gbnms {
 
 // --------------------------------------------------------------------- map
 
-constexpr int BK_THREADS = 256;
+constexpr int BK_THREADS = 128, BK_EACH = 4, BK_ROWS = 16, BK_TABLE = 4096;
 
 // buckets[set][i][j] = sum over the axes of lut[axis][clamp(k - q)], -1 when
-// a part is negative or the sum does not fit.
+// a part is negative or the sum does not fit.  A block takes BK_THREADS *
+// BK_EACH keys (four neighbours a thread) of BK_ROWS queries of one set; the
+// tables lie in shared memory where they fit and serve several rows
+// (SHARED), else they come from L1.
+template <bool SHARED>
 __global__ void __launch_bounds__(BK_THREADS)
-relation_buckets_kernel(BucketArgs a)
+relation_buckets_kernel(BucketArgs a, unsigned tiles)
 {
-    const int64_t all = a.sets * a.queries * a.keys, step = static_cast<int64_t>(gridDim.x) * BK_THREADS;
-    for (int64_t e = static_cast<int64_t>(blockIdx.x) * BK_THREADS + threadIdx.x; e < all; e += step) {
-        const int64_t j = e % a.keys, row = e / a.keys, i = row % a.queries, set = row / a.queries;
-        const int32_t* q = a.q_pos + ((a.q_sets == 1 ? 0 : set) * a.queries + i) * a.axes;
-        const int32_t* k = a.k_pos + ((a.k_sets == 1 ? 0 : set) * a.keys + j) * a.axes;
-        int64_t sum = 0;
-        bool masked = false;
-        for (int x = 0; x < a.axes; ++x) {
-            int64_t d = static_cast<int64_t>(k[x]) - q[x];
-            d = d < -a.reach ? -a.reach : (d > a.reach ? a.reach : d);
-            const int part = a.lut[x * (2 * a.reach + 1) + a.reach + d];
-            masked |= part < 0;
-            sum += part;
+    __shared__ int s_lut[SHARED ? BK_TABLE : 1];
+    const int width = 2 * a.reach + 1, axes = a.axes;
+    if (SHARED) {
+        for (int x = threadIdx.x; x < axes * width; x += BK_THREADS) s_lut[x] = a.lut[x];
+        __syncthreads();
+    }
+    const int* lut = SHARED ? s_lut : a.lut;
+    const unsigned Q = static_cast<unsigned>(a.queries), set = blockIdx.x / tiles, first = blockIdx.x % tiles * BK_ROWS;
+    const int32_t* q = a.q_pos + static_cast<int64_t>(a.q_sets == 1 ? 0 : set) * Q * axes;
+    const int32_t* k = a.k_pos + (a.k_sets == 1 ? 0 : set) * a.keys * axes;
+    const bool wide = a.keys % 4 == 0 && reinterpret_cast<uintptr_t>(a.buckets) % 8 == 0;
+    for (int64_t j0 = (static_cast<int64_t>(blockIdx.y) * BK_THREADS + threadIdx.x) * BK_EACH; j0 < a.keys;
+         j0 += static_cast<int64_t>(gridDim.y) * BK_THREADS * BK_EACH) {
+        const int here = a.keys - j0 < BK_EACH ? static_cast<int>(a.keys - j0) : BK_EACH;
+        int at[BK_EACH][NMS_RELATION_MAX_AXES];
+#pragma unroll
+        for (int e = 0; e < BK_EACH; ++e)
+#pragma unroll
+            for (int x = 0; x < NMS_RELATION_MAX_AXES; ++x)
+                at[e][x] = x < axes ? k[(j0 + (e < here ? e : 0)) * axes + x] : 0;
+        for (unsigned i = first; i < first + BK_ROWS && i < Q; ++i) {
+            Pack<int16_t, BK_EACH> out;
+            int from[NMS_RELATION_MAX_AXES];
+#pragma unroll
+            for (int x = 0; x < NMS_RELATION_MAX_AXES; ++x) from[x] = x < axes ? q[static_cast<int64_t>(i) * axes + x] : 0;
+#pragma unroll
+            for (int e = 0; e < BK_EACH; ++e) {
+                int64_t sum = 0;
+                bool masked = false;
+#pragma unroll
+                for (int x = 0; x < NMS_RELATION_MAX_AXES; ++x) {
+                    if (x >= axes) break;
+                    const int64_t d = static_cast<int64_t>(at[e][x]) - from[x];
+                    const int c = d < -a.reach ? -a.reach : d > a.reach ? a.reach : static_cast<int>(d);
+                    const int part = lut[x * width + a.reach + c];
+                    masked |= part < 0;
+                    sum += part;
+                }
+                out.v[e] = static_cast<int16_t>(masked || sum > 32767 ? -1 : sum);
+            }
+            int16_t* to = a.buckets + (static_cast<int64_t>(set) * Q + i) * a.keys + j0;
+            if (wide) {
+                *reinterpret_cast<Pack<int16_t, BK_EACH>*>(to) = out;
+            } else {
+#pragma unroll
+                for (int e = 0; e < BK_EACH; ++e)
+                    if (e < here) to[e] = out.v[e];
+            }
         }
-        a.buckets[e] = static_cast<int16_t>(masked || sum > 32767 ? -1 : sum);
     }
 }
 
 void launch_relation_buckets(const BucketArgs& a, cudaStream_t st)
 {
-    const int64_t want = (a.sets * a.queries * a.keys + BK_THREADS - 1) / BK_THREADS;
-    relation_buckets_kernel<<<static_cast<unsigned>(want < SMS * 64 ? want : SMS * 64), BK_THREADS, 0, st>>>(a);
+    const int64_t chunks = (a.keys + BK_THREADS * BK_EACH - 1) / (BK_THREADS * BK_EACH);
+    const unsigned tiles = static_cast<unsigned>((a.queries + BK_ROWS - 1) / BK_ROWS);
+    const dim3 grid(static_cast<unsigned>(a.sets) * tiles, static_cast<unsigned>(chunks < 4096 ? chunks : 4096));
+    if (a.queries >= 4 && a.axes * (2 * a.reach + 1) <= BK_TABLE)
+        relation_buckets_kernel<true><<<grid, BK_THREADS, 0, st>>>(a, tiles);
+    else
+        relation_buckets_kernel<false><<<grid, BK_THREADS, 0, st>>>(a, tiles);
 }
 
 // ---------------------------------------------------------------- dispatch

@@ -12,8 +12,8 @@
 // bounds them.  A row stays in the registers of its team: L lanes, NV vectors
 // of EV elements a lane.  What a row needs besides (its buckets, its
 // bias) is the same for many rows, so a team stays with one (query, map) and
-// goes through the rows that share it, loading the next row before it works
-// on the present one:
+// goes through the rows that share it, several short ones at a time, or
+// loading the next long one before it works on the present one:
 //   by image  (one map for all images, no key mask): the rows of one head and
 //             query over the images; bias in registers.
 //   by head   (a map or mask for each image): the rows of one image and query
@@ -33,24 +33,26 @@ namespace gbnms {
 
 // A weight below 2^-126 is flushed to zero (exp2_fast).
 
-// Reduction over a team.  L <= 32: neighbouring lanes of a warp; L = 256: the
-// block, by way of s (8 floats; alternate between two of them).
-template <int L, bool MAX>
-__device__ __forceinline__ float team_reduce(float v, float* s)
+// Reductions over a team, of R rows at once.  L <= 32: neighbouring lanes of
+// a warp; L = 256: the block, by way of s (8 floats; alternate between two of
+// them), R = 1.
+template <int L, bool MAX, int R>
+__device__ __forceinline__ void team_reduce(float (&v)[R], float* s)
 {
 #pragma unroll
-    for (int o = (L < 32 ? L : 32) / 2; o; o >>= 1) {
-        const float u = __shfl_xor_sync(FULL, v, o);
-        v = MAX ? fmaxf(v, u) : v + u;
-    }
-    if (L > 32) {
-        if (lane_id() == 0) s[threadIdx.x / 32] = v;
-        __syncthreads();
-        v = s[0];
+    for (int o = (L < 32 ? L : 32) / 2; o; o >>= 1)
 #pragma unroll
-        for (int k = 1; k < L / 32; ++k) v = MAX ? fmaxf(v, s[k]) : v + s[k];
+        for (int r = 0; r < R; ++r) {
+            const float u = __shfl_xor_sync(FULL, v[r], o);
+            v[r] = MAX ? fmaxf(v[r], u) : v[r] + u;
+        }
+    if (L > 32) {
+        if (lane_id() == 0) s[threadIdx.x / 32] = v[0];
+        __syncthreads();
+        v[0] = s[0];
+#pragma unroll
+        for (int k = 1; k < L / 32; ++k) v[0] = MAX ? fmaxf(v[0], s[k]) : v[0] + s[k];
     }
-    return v;
 }
 
 // 0xffff in each half (byte pair) of x whose top bit is set.
@@ -100,8 +102,10 @@ struct Shape {
     // Two 16-bit elements to a word.
     static constexpr bool PACKED = sizeof(T) == 2 && EV % 2 == 0;
     // Blocks that an SM holds at least (the launches count on it).
-    static constexpr int BLOCKS = (E > 16 ? 1 : E > 8 ? 2 : 3) + (PACKED ? 1 : 0);
+    static constexpr int BLOCKS = E > 16 ? (PACKED ? 2 : 1) : E > 8 ? 2 : 3;
     static constexpr int GRAD_BLOCKS = E > 16 ? 1 : E > 8 ? 2 : 3;
+    // Rows that a team works on at a time: short ones side by side, to have enough loads and shuffles under way.
+    static constexpr int ROWS = L > 32 || E > 16 ? 1 : E > 8 ? 2 : 4;
 
     static __device__ __forceinline__ int first(int v, int lane) { return (v * L + lane) * EV; }
     static __device__ __forceinline__ bool inside(int v, int lane, int K)
@@ -270,8 +274,9 @@ relation_softmax_kernel(RelationArgs a, int per)
     const int64_t first = (BY_IMAGE ? static_cast<int64_t>(anchor) : static_cast<int64_t>(outer) * H * Q + i) * K;
     const T* s = static_cast<const T*>(a.scores) + first + t0 * step;
     T* p = static_cast<T*>(a.out) + first + t0 * step;
-    Pack<T, EV> next[NV];
-    S::load(next, s, K, lane);
+    constexpr int R = S::ROWS;
+    Pack<T, EV> next[R][NV];
+    if (R == 1) S::load(next[0], s, K, lane);
     Buckets<S> bucket;
     float bias[BY_IMAGE ? S::E : 1];
     {
@@ -292,61 +297,91 @@ relation_softmax_kernel(RelationArgs a, int per)
             }
     }
     const float* row_tab = tab;
-    for (int t = t0; t < t1; ++t) {
-        float x[NV][EV];
+    for (int t = t0; t < t1; t += R) {
+        float x[R][NV][EV], top[R], sum[R], inv[R];
+        if (R > 1) {  // past the last row: that row again, not stored
 #pragma unroll
-        for (int v = 0; v < NV; ++v) S::widen(x[v], next[v]);
-        s += step;
-        if (t + 1 < t1) S::load(next, s, K, lane);
+            for (int r = 0; r < R; ++r) S::load(next[r], s + (t + r < t1 ? r : t1 - 1 - t) * step, K, lane);
+        }
+        s += R * step;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int v = 0; v < NV; ++v) S::widen(x[r][v], next[r][v]);
+        if (R == 1 && t + 1 < t1) S::load(next[0], s, K, lane);
+        auto bias_of = [&](int r, int v, int e) {
+            return BY_IMAGE ? bias[v * EV + e] : row_tab[(t + r < t1 ? r : 0) * (nb + 1) + bucket(v, e)];
+        };
         // A masked pair's logit is -inf, or NaN if its score is NaN or infinite; the maximum passes over both.
-        float top = -INFINITY;
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int e = 0; e < EV; ++e) {
-                x[v][e] = fmaf(x[v][e], a.scale, BY_IMAGE ? bias[v * EV + e] : row_tab[bucket(v, e)]);
-                top = fmaxf(top, x[v][e]);
-            }
-        top = team_reduce<L, true>(top, red[t & 1]);
-        const float base = top == -INFINITY ? 0.0f : top;
-        float sum = 0.0f;
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int e = 0; e < EV; ++e) {
-                x[v][e] = exp2_fast((x[v][e] - base) * LOG2E);
-                sum += x[v][e];
-            }
-        sum = team_reduce<L, false>(sum, red[2 + (t & 1)]);
-        float inv = sum == 0.0f ? 0.0f : reciprocal(sum);
-        if (__any_sync(FULL, inv != inv)) {  // a NaN or +inf, perhaps of masked pairs alone: once more without those
-            if (L > 32) __syncthreads();     // red is still being read
-            sum = 0.0f;
+        for (int r = 0; r < R; ++r) {
+            top[r] = -INFINITY;
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
                 for (int e = 0; e < EV; ++e) {
-                    if ((BY_IMAGE ? bias[v * EV + e] : row_tab[bucket(v, e)]) == -INFINITY) x[v][e] = 0.0f;
-                    sum += x[v][e];
+                    x[r][v][e] = fmaf(x[r][v][e], a.scale, bias_of(r, v, e));
+                    top[r] = fmaxf(top[r], x[r][v][e]);
                 }
-            sum = team_reduce<L, false>(sum, red[2 + (t & 1)]);
-            inv = sum == 0.0f ? 0.0f : reciprocal(sum);
+        }
+        team_reduce<L, true>(top, red[t & 1]);
+        bool odd = false;  // a row met a NaN or +inf
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float base = top[r] == -INFINITY ? 0.0f : top[r];
+            sum[r] = 0.0f;
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int e = 0; e < EV; ++e)
-                    x[v][e] = (BY_IMAGE ? bias[v * EV + e] : row_tab[bucket(v, e)]) == -INFINITY ? 0.0f : x[v][e] * inv;
-            inv = 1.0f;
+                for (int e = 0; e < EV; ++e) {
+                    x[r][v][e] = exp2_fast((x[r][v][e] - base) * LOG2E);
+                    sum[r] += x[r][v][e];
+                }
+        }
+        team_reduce<L, false>(sum, red[2 + (t & 1)]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            inv[r] = sum[r] == 0.0f ? 0.0f : reciprocal(sum[r]);
+            odd |= inv[r] != inv[r];
+        }
+        if (__any_sync(FULL, odd)) {  // perhaps of masked pairs alone: once more without those
+            if (L > 32) __syncthreads();  // red is still being read
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                sum[r] = 0.0f;
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+#pragma unroll
+                    for (int e = 0; e < EV; ++e) {
+                        if (bias_of(r, v, e) == -INFINITY) x[r][v][e] = 0.0f;
+                        sum[r] += x[r][v][e];
+                    }
+            }
+            team_reduce<L, false>(sum, red[2 + (t & 1)]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                inv[r] = sum[r] == 0.0f ? 0.0f : reciprocal(sum[r]);
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+#pragma unroll
+                    for (int e = 0; e < EV; ++e)
+                        x[r][v][e] = bias_of(r, v, e) == -INFINITY ? 0.0f : x[r][v][e] * inv[r];
+                inv[r] = 1.0f;
+            }
         }
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
+        for (int r = 0; r < R; ++r) {
+            if (t + r >= t1) break;
 #pragma unroll
-            for (int e = 0; e < EV; ++e) x[v][e] *= inv;
-            if (real && S::inside(v, lane, K))
-                *reinterpret_cast<Pack<T, EV>*>(p + S::first(v, lane)) = pack_results<T, EV>(x[v]);
+            for (int v = 0; v < NV; ++v) {
+#pragma unroll
+                for (int e = 0; e < EV; ++e) x[r][v][e] *= inv[r];
+                if (real && S::inside(v, lane, K))
+                    *reinterpret_cast<Pack<T, EV>*>(p + S::first(v, lane)) = pack_results<T, EV>(x[r][v]);
+            }
+            p += step;
         }
-        p += step;
-        row_tab += nb + 1;
+        row_tab += R * (nb + 1);
     }
 }
 
@@ -380,11 +415,12 @@ relation_softmax_long_kernel(RelationArgs a, int64_t rows)
             }
             sum += x == -INFINITY ? 0.0f : exp2_fast((x - top) * LOG2E);
         }
-        const float all = team_reduce<256, true>(top, red[0]);
-        const float base = all == -INFINITY ? 0.0f : all;
-        sum = team_reduce<256, false>(top == -INFINITY && sum == 0.0f ? 0.0f : sum * exp2_fast((top - base) * LOG2E),
-                                      red[1]);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        float all[1] = {top}, total[1];
+        team_reduce<256, true>(all, red[0]);
+        const float base = all[0] == -INFINITY ? 0.0f : all[0];
+        total[0] = top == -INFINITY && sum == 0.0f ? 0.0f : sum * exp2_fast((top - base) * LOG2E);
+        team_reduce<256, false>(total, red[1]);
+        const float inv = total[0] == 0.0f ? 0.0f : reciprocal(total[0]);
         for (int64_t j = threadIdx.x; j < a.keys; j += 256)
             p[j] = from_f32<T>(logit(j, x) ? exp2_fast((x - base) * LOG2E) * inv : 0.0f);
         __syncthreads();
@@ -434,46 +470,56 @@ __device__ __forceinline__ void join_columns(const float* hist, int lists, int c
     }
 }
 
-// One row: da into x (binary32) from the packed operands, dscores stored.
-template <typename S>
-__device__ __forceinline__ void grad_row(float (&x)[S::NV][S::EV], const Pack<typename S::T, S::EV> (&pq)[S::NV],
-                                         const Pack<typename S::T, S::EV> (&dq)[S::NV], const Valid<S>& valid,
-                                         float scale, typename S::T* ds, int K, int lane, bool store, float* red)
+// R rows: da into p from probs p and gradients d (0 where masked), dscores
+// stored for the first `stored` of them, `step` elements apart.
+template <typename S, int R>
+__device__ __forceinline__ void grad_rows(float (&p)[R][S::NV][S::EV], float (&d)[R][S::NV][S::EV],
+                                          const Buckets<S>& bucket, const RelationArgs& a, typename S::T* ds,
+                                          int64_t step, int lane, int stored, float* red)
 {
     constexpr int EV = S::EV, NV = S::NV;
-    float dot = 0.0f;
+    const int K = static_cast<int>(a.keys);
+    float dot[R];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        float p[EV], d[EV];
-        valid.take(p, pq[v], v);
-        valid.take(d, dq[v], v);
-#pragma unroll
-        for (int e = 0; e < EV; ++e) dot = fmaf(p[e], d[e], dot);
-    }
-    dot = team_reduce<S::L, false>(dot, red);
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        float p[EV], d[EV];
-        valid.take(p, pq[v], v);
-        valid.take(d, dq[v], v);
-#pragma unroll
-        for (int e = 0; e < EV; ++e) x[v][e] = p[e] * (d[e] - dot);
-    }
-    if (__any_sync(FULL, !(fabsf(dot) < INFINITY))) {
-        // A row that met an infinity or NaN leaves its masked places 0 all the same.
+    for (int r = 0; r < R; ++r) {
+        dot[r] = 0.0f;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int e = 0; e < EV; ++e)
-                if (!valid(v, e)) x[v][e] = 0.0f;
+            for (int e = 0; e < EV; ++e) dot[r] = fmaf(p[r][v][e], d[r][v][e], dot[r]);
+    }
+    team_reduce<S::L, false>(dot, red);
+    bool odd = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        odd |= !(fabsf(dot[r]) < INFINITY);
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < EV; ++e) p[r][v][e] *= d[r][v][e] - dot[r];
+    }
+    if (__any_sync(FULL, odd)) {
+        // A row that met an infinity or NaN leaves its masked places 0 all the same.
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int e = 0; e < EV; ++e)
+                    if (bucket(v, e) == a.num_buckets) p[r][v][e] = 0.0f;
     }
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        float y[EV];
+    for (int r = 0; r < R; ++r) {
+        if (r >= stored) break;
 #pragma unroll
-        for (int e = 0; e < EV; ++e) y[e] = scale * x[v][e];
-        if (store && S::inside(v, lane, K))
-            *reinterpret_cast<Pack<typename S::T, EV>*>(ds + S::first(v, lane)) = pack_results<typename S::T, EV>(y);
+        for (int v = 0; v < NV; ++v) {
+            float y[EV];
+#pragma unroll
+            for (int e = 0; e < EV; ++e) y[e] = a.scale * p[r][v][e];
+            if (S::inside(v, lane, K))
+                *reinterpret_cast<Pack<typename S::T, EV>*>(ds + r * step + S::first(v, lane)) =
+                    pack_results<typename S::T, EV>(y);
+        }
     }
 }
 
@@ -499,9 +545,12 @@ relation_grad_image_kernel(RelationArgs a, int per, int columns, float* part)
     const T* p = static_cast<const T*>(a.probs) + first;
     const T* dp = static_cast<const T*>(a.scores) + first;
     T* ds = static_cast<T*>(a.out) + first;
-    Pack<T, EV> pn[NV], dn[NV];
-    S::load(pn, p, K, lane);
-    S::load(dn, dp, K, lane);
+    constexpr int R = S::ROWS;
+    Pack<T, EV> pn[R][NV], dn[R][NV];
+    if (R == 1) {
+        S::load(pn[0], p, K, lane);
+        S::load(dn[0], dp, K, lane);
+    }
     Buckets<S> bucket;
     Valid<S> valid;
     auto map = [&]() {
@@ -517,26 +566,39 @@ relation_grad_image_kernel(RelationArgs a, int per, int columns, float* part)
     for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int e = 0; e < EV; ++e) acc[v][e] = 0.0f;
-    for (int t = t0; t < t1; ++t) {
-        Pack<T, EV> pq[NV], dq[NV];
+    for (int t = t0; t < t1; t += R) {
+        const int rows = t + R < t1 ? R : t1 - t;
+        if (R > 1) {  // past the last row: that row again, neither stored nor added
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            pq[v] = pn[v];
-            dq[v] = dn[v];
+            for (int r = 0; r < R; ++r) {
+                S::load(pn[r], p + (r < rows ? r : rows - 1) * step, K, lane);
+                S::load(dn[r], dp + (r < rows ? r : rows - 1) * step, K, lane);
+            }
         }
-        p += step;
-        dp += step;
-        if (t + 1 < t1) {
-            S::load(pn, p, K, lane);
-            S::load(dn, dp, K, lane);
+        p += R * step;
+        dp += R * step;
+        float x[R][NV][EV], d[R][NV][EV];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                valid.take(x[r][v], pn[r][v], v);
+                valid.take(d[r][v], dn[r][v], v);
+            }
+        if (R == 1 && t + 1 < t1) {
+            S::load(pn[0], p, K, lane);
+            S::load(dn[0], dp, K, lane);
         }
-        float x[NV][EV];
-        grad_row<S>(x, pq, dq, valid, a.scale, ds, K, lane, real, red[t & 1]);
-        ds += step;
+        grad_rows<S, R>(x, d, bucket, a, ds, step, lane, real ? rows : 0, red[t & 1]);
+        ds += R * step;
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+        for (int r = 0; r < R; ++r) {
+            if (r >= rows) break;
 #pragma unroll
-            for (int e = 0; e < EV; ++e) acc[v][e] += x[v][e];
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int e = 0; e < EV; ++e) acc[v][e] += x[r][v][e];
+        }
     }
     // The warps add their sums in turn (the map is read again: its indices need not live through the loop).
     map();
@@ -599,11 +661,11 @@ relation_grad_head_kernel(RelationArgs a, int columns, float* part)
         bucket.set(un, kn, keyed, K, lane, nb);
         if (!real) bucket.clear(nb);
         valid.set(bucket, nb);
-        Pack<T, EV> pq[NV], dq[NV];
+        float x[1][NV][EV], d[1][NV][EV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            pq[v] = pn[v];
-            dq[v] = dn[v];
+            valid.take(x[0][v], pn[v], v);
+            valid.take(d[0][v], dn[v], v);
         }
         bi += stride;
         b += step_b;
@@ -613,20 +675,19 @@ relation_grad_head_kernel(RelationArgs a, int columns, float* part)
             ++b;
         }
         if (bi < rows) fetch(bi + team < rows);
-        float x[NV][EV];
-        grad_row<S>(x, pq, dq, valid, a.scale, ds, K, lane, real, red[turn]);
+        grad_rows<S, 1>(x, d, bucket, a, ds, 0, lane, real ? 1 : 0, red[turn]);
         if (WIDE) {
             float* column = mine + lane_id();
 #pragma unroll
             for (int k = 0; k + 1 < S::E; k += 2)
-                add_two(column, bucket(k / EV, k % EV), x[k / EV][k % EV], bucket((k + 1) / EV, (k + 1) % EV),
-                        x[(k + 1) / EV][(k + 1) % EV]);
-            if (S::E % 2) column[bucket(NV - 1, EV - 1) * 32] += x[NV - 1][EV - 1];
+                add_two(column, bucket(k / EV, k % EV), x[0][k / EV][k % EV], bucket((k + 1) / EV, (k + 1) % EV),
+                        x[0][(k + 1) / EV][(k + 1) % EV]);
+            if (S::E % 2) column[bucket(NV - 1, EV - 1) * 32] += x[0][NV - 1][EV - 1];
         } else {
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int e = 0; e < EV; ++e) add_in_turn(mine, bucket(v, e), x[v][e], columns);
+                for (int e = 0; e < EV; ++e) add_in_turn(mine, bucket(v, e), x[0][v][e], columns);
         }
     }
     join_columns(hist, warps, columns, nb, part + (static_cast<int64_t>(head) * gridDim.x + blockIdx.x) * nb);
