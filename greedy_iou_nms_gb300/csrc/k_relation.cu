@@ -8,24 +8,24 @@ namespace gbnms {
 
 // --------------------------------------------------------------------- map
 
-constexpr int BK_THREADS = 128, BK_EACH = 4, BK_ROWS = 16, BK_TABLE = 4096;
+constexpr int BK_THREADS = 128, BK_EACH = 4, BK_ROWS = 4, BK_TABLE = 4096;
 
 // buckets[set][i][j] = sum over the axes of lut[axis][clamp(k - q)], -1 when
 // a part is negative or the sum does not fit.  A block takes BK_THREADS *
 // BK_EACH keys (four neighbours a thread) of BK_ROWS queries of one set; the
 // tables lie in shared memory where they fit and serve several rows
 // (SHARED), else they come from L1.
-template <bool SHARED>
+template <int AXES, bool SHARED>
 __global__ void __launch_bounds__(BK_THREADS)
 relation_buckets_kernel(BucketArgs a, unsigned tiles)
 {
     __shared__ int s_lut[SHARED ? BK_TABLE : 1];
-    const int width = 2 * a.reach + 1, axes = a.axes;
+    const int width = 2 * a.reach + 1, axes = AXES < NMS_RELATION_MAX_AXES ? AXES : a.axes;
     if (SHARED) {
         for (int x = threadIdx.x; x < axes * width; x += BK_THREADS) s_lut[x] = a.lut[x];
         __syncthreads();
     }
-    const int* lut = SHARED ? s_lut : a.lut;
+    const int* lut = (SHARED ? s_lut : a.lut) + a.reach;
     const unsigned Q = static_cast<unsigned>(a.queries), set = blockIdx.x / tiles, first = blockIdx.x % tiles * BK_ROWS;
     const int32_t* q = a.q_pos + static_cast<int64_t>(a.q_sets == 1 ? 0 : set) * Q * axes;
     const int32_t* k = a.k_pos + (a.k_sets == 1 ? 0 : set) * a.keys * axes;
@@ -33,32 +33,35 @@ relation_buckets_kernel(BucketArgs a, unsigned tiles)
     for (int64_t j0 = (static_cast<int64_t>(blockIdx.y) * BK_THREADS + threadIdx.x) * BK_EACH; j0 < a.keys;
          j0 += static_cast<int64_t>(gridDim.y) * BK_THREADS * BK_EACH) {
         const int here = a.keys - j0 < BK_EACH ? static_cast<int>(a.keys - j0) : BK_EACH;
-        int at[BK_EACH][NMS_RELATION_MAX_AXES];
+        int at[BK_EACH][AXES];
 #pragma unroll
         for (int e = 0; e < BK_EACH; ++e)
 #pragma unroll
-            for (int x = 0; x < NMS_RELATION_MAX_AXES; ++x)
-                at[e][x] = x < axes ? k[(j0 + (e < here ? e : 0)) * axes + x] : 0;
-        for (unsigned i = first; i < first + BK_ROWS && i < Q; ++i) {
-            Pack<int16_t, BK_EACH> out;
-            int from[NMS_RELATION_MAX_AXES];
+            for (int x = 0; x < AXES; ++x) at[e][x] = x < axes ? k[(j0 + (e < here ? e : 0)) * axes + x] : 0;
 #pragma unroll
-            for (int x = 0; x < NMS_RELATION_MAX_AXES; ++x) from[x] = x < axes ? q[static_cast<int64_t>(i) * axes + x] : 0;
+        for (int r = 0; r < BK_ROWS; ++r) {
+            const unsigned i = first + r;
+            if (i >= Q) break;
+            int sum[BK_EACH] = {}, signs[BK_EACH] = {};
 #pragma unroll
-            for (int e = 0; e < BK_EACH; ++e) {
-                int64_t sum = 0;
-                bool masked = false;
+            for (int x = 0; x < AXES; ++x) {
+                if (x >= axes) break;
+                // Keys are clamped to the reach about the query: no difference leaves 32 bits.
+                const int from = q[static_cast<int64_t>(i) * axes + x];
+                const int64_t least = static_cast<int64_t>(from) - a.reach, most = static_cast<int64_t>(from) + a.reach;
+                const int lo = least < INT32_MIN ? INT32_MIN : static_cast<int>(least);
+                const int hi = most > INT32_MAX ? INT32_MAX : static_cast<int>(most);
 #pragma unroll
-                for (int x = 0; x < NMS_RELATION_MAX_AXES; ++x) {
-                    if (x >= axes) break;
-                    const int64_t d = static_cast<int64_t>(at[e][x]) - from[x];
-                    const int c = d < -a.reach ? -a.reach : d > a.reach ? a.reach : static_cast<int>(d);
-                    const int part = lut[x * width + a.reach + c];
-                    masked |= part < 0;
-                    sum += part;
+                for (int e = 0; e < BK_EACH; ++e) {
+                    const int part = lut[x * width + (min(max(at[e][x], lo), hi) - from)];
+                    signs[e] |= part;
+                    sum[e] += min(part, 32768);
                 }
-                out.v[e] = static_cast<int16_t>(masked || sum > 32767 ? -1 : sum);
             }
+            Pack<int16_t, BK_EACH> out;
+#pragma unroll
+            for (int e = 0; e < BK_EACH; ++e)
+                out.v[e] = static_cast<int16_t>(signs[e] < 0 || sum[e] > 32767 ? -1 : sum[e]);
             int16_t* to = a.buckets + (static_cast<int64_t>(set) * Q + i) * a.keys + j0;
             if (wide) {
                 *reinterpret_cast<Pack<int16_t, BK_EACH>*>(to) = out;
@@ -76,10 +79,11 @@ void launch_relation_buckets(const BucketArgs& a, cudaStream_t st)
     const int64_t chunks = (a.keys + BK_THREADS * BK_EACH - 1) / (BK_THREADS * BK_EACH);
     const unsigned tiles = static_cast<unsigned>((a.queries + BK_ROWS - 1) / BK_ROWS);
     const dim3 grid(static_cast<unsigned>(a.sets) * tiles, static_cast<unsigned>(chunks < 4096 ? chunks : 4096));
-    if (a.queries >= 4 && a.axes * (2 * a.reach + 1) <= BK_TABLE)
-        relation_buckets_kernel<true><<<grid, BK_THREADS, 0, st>>>(a, tiles);
-    else
-        relation_buckets_kernel<false><<<grid, BK_THREADS, 0, st>>>(a, tiles);
+    const bool shared = a.queries >= BK_ROWS && a.axes * (2 * a.reach + 1) <= BK_TABLE;
+    auto run = [&](auto kernel) { kernel<<<grid, BK_THREADS, 0, st>>>(a, tiles); };
+    if (a.axes == 1) shared ? run(relation_buckets_kernel<1, true>) : run(relation_buckets_kernel<1, false>);
+    else if (a.axes == 2) shared ? run(relation_buckets_kernel<2, true>) : run(relation_buckets_kernel<2, false>);
+    else shared ? run(relation_buckets_kernel<4, true>) : run(relation_buckets_kernel<4, false>);
 }
 
 // ---------------------------------------------------------------- dispatch
@@ -120,7 +124,9 @@ RelationGradPlan relation_grad_plan(int64_t batch, int heads, int64_t queries, i
         p.chunks = (batch + p.per - 1) / p.per;
         return p;
     }
-    // A table a warp: 32 columns if six warps' fit, else fewer.
+    // A table a warp: 32 columns if six warps' fit, else fewer (16 columns and
+    // two turns, to have 14 warps on an SM and not 7, took 436 us for 264 on
+    // 16 x 8 x 1000 x 1000 bf16 with 225 buckets).
     constexpr int ROOM = 208 * 1024;
     const int need = lanes == 256 ? 8 : 6;
     for (p.columns = 32; p.columns > 4 && need * (num_buckets + 1) * 4 * p.columns > ROOM; p.columns /= 2) {}

@@ -792,6 +792,13 @@ inline void relation_shape(const RelationArgs& a, F f)
 
 constexpr int64_t blocks_over(int64_t n, int64_t each) { return (n + each - 1) / each; }
 
+// Blocks of 256 threads of a kernel that an SM holds.
+inline int resident_blocks(const void* kernel)
+{
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, 256, 0) == cudaSuccess && n > 0 ? n : 1;
+}
+
 template <typename T>
 inline void softmax_type(const RelationArgs& a, cudaStream_t st)
 {
@@ -806,7 +813,8 @@ inline void softmax_type(const RelationArgs& a, cudaStream_t st)
         const int64_t anchors = (image ? a.heads : a.batch) * a.queries, inner = image ? a.batch : a.heads;
         const int64_t blocks = blocks_over(anchors, 256 / S::L);
         // Chunks of the inner index: one wave of resident blocks.
-        int64_t chunks = SMS * S::BLOCKS / blocks;
+        static const int held = resident_blocks(reinterpret_cast<const void*>(relation_softmax_kernel<S, true>));
+        int64_t chunks = SMS * (image ? held : S::BLOCKS) / blocks;
         if (chunks < 1) chunks = 1;
         if (chunks > inner) chunks = inner;
         if (!image) {  // the chunk's tables have to fit
