@@ -11,7 +11,6 @@
 namespace gbnms {
 
 constexpr int DR_THREADS = 256;
-constexpr int DR_BATCH = 4;  // blocks of eight elements a thread has in flight
 
 // One block of eight elements: V of them an access (all, or 1 where a
 // pointer is not aligned).
@@ -28,9 +27,10 @@ struct Eight {
 
 // RES: with a residual.  DROP: some element may be dropped.
 template <typename T, int V, bool RES, bool DROP>
-__global__ void __launch_bounds__(DR_THREADS)
+__global__ void __launch_bounds__(DR_THREADS, 3)
 dropout_kernel(const T* x, const T* residual, T* y, int64_t n, DropArgs d)
 {
+    constexpr int DR_BATCH = RES ? 2 : 4;  // blocks of eight elements a thread has in flight
     const int64_t whole = n / 8, step = static_cast<int64_t>(gridDim.x) * DR_THREADS;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * DR_THREADS + threadIdx.x;
     for (int64_t b = first; b < whole; b += DR_BATCH * step) {
@@ -82,7 +82,7 @@ static void launch(const void* x, const void* residual, void* y, int64_t n, cons
     auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     const bool wide = aligned(x) && aligned(residual) && aligned(y), res = residual != nullptr, drop = d.limit < 65536u;
     // Short tensors: a block a thread.  Long ones: full SMs, each thread many.
-    const int64_t want = (n / 8 + DR_THREADS - 1) / DR_THREADS, most = SMS * 16;
+    const int64_t want = (n / 8 + DR_THREADS - 1) / DR_THREADS, most = SMS * 3;
     const unsigned grid = static_cast<unsigned>(want < 1 ? 1 : want < most ? want : most);
     auto run = [&](auto kernel) {
         kernel<<<grid, DR_THREADS, 0, st>>>(static_cast<const T*>(x), static_cast<const T*>(residual), static_cast<T*>(y),

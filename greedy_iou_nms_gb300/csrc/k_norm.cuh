@@ -32,8 +32,9 @@ constexpr int NT = 256;  // threads of a block
 // the last launch goes through the pieces backwards and its stores are marked
 // as streaming.
 
-// Row pieces of an image: one wave of blocks, 32 rows at least (a
-// function of the shape alone: the workspace's size depends on it).
+// Row pieces of an image, at most: 32 rows each at least, and one wave of
+// four blocks on every SM (a function of the shape alone: the workspace's
+// size depends on it).
 inline int64_t norm_pieces(int64_t batch, int64_t pixels, int channels)
 {
     const int64_t tiles = channels > 256 ? channels / 256 : 1, ctas = SMS * 4;
@@ -305,7 +306,7 @@ norm_finish_kernel(NormArgs a, NormTile t, NormScratch w, int each, int values)
 }
 
 template <typename T, int V, bool ONE, int ACT>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, 3)
 norm_apply_kernel(NormArgs a, NormTile t)
 {
     constexpr int P = ONE ? 1 : V;
@@ -370,7 +371,7 @@ __device__ __forceinline__ void slope_row(const NormArgs& a, const float (&mean)
 
 // Sums by channel of dz and dz * (x - mean) of each row piece.
 template <typename T, int V, bool ONE, int ACT>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, ONE ? 3 : 2)
 norm_grad_partial_kernel(NormArgs a, NormTile t, NormScratch w)
 {
     constexpr int P = ONE ? 1 : V;
@@ -500,7 +501,7 @@ norm_grad_param_kernel(NormArgs a, NormScratch w)
 
 // dx; the blocks past the pieces' (the first to run) write dweight and dbias.
 template <typename T, int V, bool ONE, int ACT>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, ONE ? 3 : 2)
 norm_grad_apply_kernel(NormArgs a, NormTile t, NormScratch w)
 {
     constexpr int P = ONE ? 1 : V;
@@ -1176,18 +1177,39 @@ static bool norm_in_clusters(const NormArgs& a, void* ws, cudaStream_t st, bool 
     return false;
 }
 
+// Blocks of NT threads of a kernel that an SM holds.
+inline int resident_blocks(const void* kernel)
+{
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, NT, 0) == cudaSuccess && n > 0 ? n : 1;
+}
+
+// The tile with pieces for one wave of `resident` blocks on every SM, at most
+// those of the workspace.
+inline NormTile one_wave(const NormArgs& a, NormTile t, int resident)
+{
+    const int64_t wave = static_cast<int64_t>(SMS) * resident / (a.batch * t.tiles);
+    if (wave < t.pieces) t.pieces = wave < 1 ? 1 : static_cast<int>(wave);
+    t.per = static_cast<int>((a.pixels + t.pieces - 1) / t.pieces);
+    return t;
+}
+
 template <typename T, int V, bool ONE, int ACT>
 static void norm_streamed(const NormArgs& a, void* ws, cudaStream_t st, bool grad)
 {
-    const NormTile t = tile(a, V);
+    const NormTile most = tile(a, V);
     const NormScratch w = scratch(a, ws);
-    const dim3 grid(static_cast<unsigned>(a.batch * t.pieces), t.tiles), block(NT);
+    const dim3 block(NT);
+    auto grid = [&](const NormTile& t) { return dim3(static_cast<unsigned>(a.batch * t.pieces), t.tiles); };
     const int D = a.channels / a.groups;
     if (!grad) {
+        static const int sums = resident_blocks(reinterpret_cast<const void*>(norm_partial_kernel<T, V, ONE>));
+        static const int rows = resident_blocks(reinterpret_cast<const void*>(norm_apply_kernel<T, V, ONE, ACT>));
+        const NormTile t = one_wave(a, most, sums), u = one_wave(a, most, rows);
         NormArgs b = a;
         if (!b.mean) b.mean = w.ga;
         if (!b.rstd) b.rstd = w.gb;
-        norm_partial_kernel<T, V, ONE><<<grid, block, 0, st>>>(b, t, w);
+        norm_partial_kernel<T, V, ONE><<<grid(t), block, 0, st>>>(b, t, w);
         const int each = ONE ? D / V : D, values = ONE ? V : 1;
         const int64_t groups = a.batch * a.groups;
         if (t.pieces * each > 128)
@@ -1195,16 +1217,20 @@ static void norm_streamed(const NormArgs& a, void* ws, cudaStream_t st, bool gra
         else
             launch_pdl(norm_finish_kernel<32>, dim3(static_cast<unsigned>((groups + NT / 32 - 1) / (NT / 32))), block, 0,
                        st, b, t, w, each, values);
-        launch_pdl(norm_apply_kernel<T, V, ONE, ACT>, grid, block, 0, st, b, t);
+        launch_pdl(norm_apply_kernel<T, V, ONE, ACT>, grid(u), block, 0, st, b, u);
     } else {
+        static const int sums = resident_blocks(reinterpret_cast<const void*>(norm_grad_partial_kernel<T, V, ONE, ACT>));
+        static const int rows = resident_blocks(reinterpret_cast<const void*>(norm_grad_apply_kernel<T, V, ONE, ACT>));
+        const NormTile t = one_wave(a, most, sums), u = one_wave(a, most, rows);
         const int chunk = D > 32 ? D : 32 / D * D;
-        norm_grad_partial_kernel<T, V, ONE, ACT><<<grid, block, 0, st>>>(a, t, w);
-        if (chunk > 4096) ensure_dynamic_smem(reinterpret_cast<const void*>(norm_grad_finish_kernel<T>), 8 * static_cast<size_t>(chunk));
+        norm_grad_partial_kernel<T, V, ONE, ACT><<<grid(t), block, 0, st>>>(a, t, w);
+        const size_t smem = 8 * static_cast<size_t>(chunk);
+        if (chunk > 4096) ensure_dynamic_smem(reinterpret_cast<const void*>(norm_grad_finish_kernel<T>), smem);
         launch_pdl(norm_grad_finish_kernel<T>,
                    dim3(static_cast<unsigned>(a.batch), static_cast<unsigned>((a.channels + chunk - 1) / chunk)), block,
-                   8 * static_cast<size_t>(chunk), st, a, t, w, chunk);
+                   smem, st, a, t, w, chunk);
         const unsigned params = a.dweight || a.dbias ? (a.channels + NT - 1) / NT : 0;
-        launch_pdl(norm_grad_apply_kernel<T, V, ONE, ACT>, dim3(grid.x + params, grid.y), block, 0, st, a, t, w);
+        launch_pdl(norm_grad_apply_kernel<T, V, ONE, ACT>, dim3(grid(u).x + params, u.tiles), block, 0, st, a, u, w);
     }
 }
 
