@@ -243,16 +243,78 @@ struct Valid {
     }
 };
 
+// ----------------------------------------------------------------- staging
+//
+// Short rows of odd lengths: read and written element by element they cost a
+// memory request for every few bytes (57% of the SM's request slots at 2304 x
+// 8 x 49 x 49 fp16).  Neighbouring teams' rows of one image are one stretch of
+// memory, a multiple of 16 bytes long but for the last block's; so, where an
+// image's rows are a multiple of that too, the block moves it as 16-byte
+// vectors through shared memory, the next rows' while it works on the present
+// ones'.
+template <typename S>
+struct Stretch {
+    using T = typename S::T;
+    static constexpr bool USED = S::EV == 1 && S::L <= 16;
+    static constexpr int VE = 16 / sizeof(T), TEAMS = 256 / S::L;
+    static constexpr int MOST = (TEAMS * S::NV * S::L / VE + 255) / 256;  // vectors of a thread
+    int whole, all;  // elements of the block's stretch: in whole vectors, and in all
+
+    __device__ __forceinline__ explicit Stretch(int n) : whole(n / VE * VE), all(n) {}
+
+    // buf[0 .. all) = from[0 .. all), asynchronously.
+    __device__ __forceinline__ void fetch(T* buf, const T* from) const
+    {
+#pragma unroll
+        for (int k = 0; k < MOST; ++k) {
+            const int at = (k * 256 + static_cast<int>(threadIdx.x)) * VE;
+            if (at < whole) {
+                const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(buf + at));
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to), "l"(from + at) : "memory");
+            }
+        }
+        const int last = whole + static_cast<int>(threadIdx.x);
+        if (last < all) buf[last] = from[last];
+    }
+    static __device__ __forceinline__ void fetched()
+    {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+    }
+    // to[0 .. all) = buf[0 .. all).
+    __device__ __forceinline__ void put(const T* buf, T* to) const
+    {
+#pragma unroll
+        for (int k = 0; k < MOST; ++k) {
+            const int at = (k * 256 + static_cast<int>(threadIdx.x)) * VE;
+            if (at < whole) *reinterpret_cast<uint4*>(to + at) = *reinterpret_cast<const uint4*>(buf + at);
+        }
+        const int last = whole + static_cast<int>(threadIdx.x);
+        if (last < all) to[last] = buf[last];
+    }
+};
+
+// Whether an image's rows and the operands lie on 16-byte boundaries.
+template <typename S>
+inline bool stretches(const RelationArgs& a)
+{
+    auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+    return Stretch<S>::USED && static_cast<int64_t>(a.heads) * a.queries * a.keys % Stretch<S>::VE == 0 &&
+           aligned(a.scores) && aligned(a.probs) && aligned(a.out);
+}
+
 // ----------------------------------------------------------------- forward
 
-template <typename S, bool BY_IMAGE>
+template <typename S, bool BY_IMAGE, bool STAGED>
 __global__ void __launch_bounds__(256, S::BLOCKS)
 relation_softmax_kernel(RelationArgs a, int per)
 {
     using T = typename S::T;
     constexpr int EV = S::EV, NV = S::NV, L = S::L;
-    extern __shared__ float tab[];  // by head: [heads of the chunk][num_buckets + 1], -inf last
+    // By head: [heads of the chunk][num_buckets + 1], -inf last.  Staged: two times R rows' stretches.
+    extern __shared__ __align__(16) float tab[];
     __shared__ float red[4][8];
+    using Rows = Stretch<S>;
     const int K = static_cast<int>(a.keys), nb = a.num_buckets, H = a.heads;
     const int lane = static_cast<int>(threadIdx.x) % L;
     const int inner = static_cast<int>(BY_IMAGE ? a.batch : H);
@@ -276,7 +338,21 @@ relation_softmax_kernel(RelationArgs a, int per)
     T* p = static_cast<T*>(a.out) + first + t0 * step;
     constexpr int R = S::ROWS;
     Pack<T, EV> next[R][NV];
-    if (R == 1) S::load(next[0], s, K, lane);
+    if (R == 1 && !STAGED) S::load(next[0], s, K, lane);
+    T* const stage = reinterpret_cast<T*>(tab);
+    const int pitch = Rows::TEAMS * K, team = static_cast<int>(threadIdx.x) / L;
+    const unsigned rows_left = anchors - blockIdx.x * Rows::TEAMS;
+    const Rows rows(static_cast<int>(rows_left < Rows::TEAMS ? rows_left : Rows::TEAMS) * K);
+    const int64_t start = t0 * step + static_cast<int64_t>(blockIdx.x) * pitch;
+    const T* from = static_cast<const T*>(a.scores) + start;
+    T* to_all = static_cast<T*>(a.out) + start;
+    auto fetch = [&](int t, int half) {
+#pragma unroll
+        for (int r = 0; r < R; ++r, from += step)
+            if (t + r < t1) rows.fetch(stage + (half * R + r) * pitch, from);
+    };
+    int half = 0;
+    if (STAGED) fetch(t0, 0);
     Buckets<S> bucket;
     float bias[BY_IMAGE ? S::E : 1];
     {
@@ -299,16 +375,29 @@ relation_softmax_kernel(RelationArgs a, int per)
     const float* row_tab = tab;
     for (int t = t0; t < t1; t += R) {
         float x[R][NV][EV], top[R], sum[R], inv[R];
-        if (R > 1) {  // past the last row: that row again, not stored
+        T* mine[R];  // staged: the team's row
+        if constexpr (STAGED) {
+            Rows::fetched();
+            if (t + R < t1) fetch(t + R, half ^ 1);
 #pragma unroll
-            for (int r = 0; r < R; ++r) S::load(next[r], s + (t + r < t1 ? r : t1 - 1 - t) * step, K, lane);
+            for (int r = 0; r < R; ++r) {
+                mine[r] = stage + (half * R + r) * pitch + team * K;
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+                    x[r][v][0] = real && t + r < t1 ? to_f32(mine[r][S::inside(v, lane, K) ? S::first(v, lane) : 0]) : 0.0f;
+            }
+        } else {
+            if (R > 1) {  // past the last row: that row again, not stored
+#pragma unroll
+                for (int r = 0; r < R; ++r) S::load(next[r], s + (t + r < t1 ? r : t1 - 1 - t) * step, K, lane);
+            }
+            s += R * step;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int v = 0; v < NV; ++v) S::widen(x[r][v], next[r][v]);
+            if (R == 1 && t + 1 < t1) S::load(next[0], s, K, lane);
         }
-        s += R * step;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int v = 0; v < NV; ++v) S::widen(x[r][v], next[r][v]);
-        if (R == 1 && t + 1 < t1) S::load(next[0], s, K, lane);
         auto bias_of = [&](int r, int v, int e) {
             return BY_IMAGE ? bias[v * EV + e] : row_tab[(t + r < t1 ? r : 0) * (nb + 1) + bucket(v, e)];
         };
@@ -376,12 +465,20 @@ relation_softmax_kernel(RelationArgs a, int per)
             for (int v = 0; v < NV; ++v) {
 #pragma unroll
                 for (int e = 0; e < EV; ++e) x[r][v][e] *= inv[r];
+                T* to = STAGED ? mine[r] : p;
                 if (real && S::inside(v, lane, K))
-                    *reinterpret_cast<Pack<T, EV>*>(p + S::first(v, lane)) = pack_results<T, EV>(x[r][v]);
+                    *reinterpret_cast<Pack<T, EV>*>(to + S::first(v, lane)) = pack_results<T, EV>(x[r][v]);
             }
             p += step;
         }
         row_tab += R * (nb + 1);
+        if constexpr (STAGED) {
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < R; ++r, to_all += step)
+                if (t + r < t1) rows.put(stage + (half * R + r) * pitch, to_all);
+            half ^= 1;
+        }
     }
 }
 
@@ -812,9 +909,12 @@ inline void softmax_type(const RelationArgs& a, cudaStream_t st)
         const bool image = relation_by_image(a);
         const int64_t anchors = (image ? a.heads : a.batch) * a.queries, inner = image ? a.batch : a.heads;
         const int64_t blocks = blocks_over(anchors, 256 / S::L);
+        const bool staged = image && stretches<S>(a);
+        size_t smem = staged ? 2 * S::ROWS * sizeof(T) * Stretch<S>::TEAMS * a.keys : 0;
         // Chunks of the inner index: one wave of resident blocks.
-        static const int held = resident_blocks(reinterpret_cast<const void*>(relation_softmax_kernel<S, true>));
-        int64_t chunks = SMS * (image ? held : S::BLOCKS) / blocks;
+        static const int held = resident_blocks(reinterpret_cast<const void*>(relation_softmax_kernel<S, true, false>));
+        const int fit = staged ? static_cast<int>(220 * 1024 / (smem + 1024)) : held;
+        int64_t chunks = SMS * (!image ? S::BLOCKS : fit < held ? fit : held) / blocks;
         if (chunks < 1) chunks = 1;
         if (chunks > inner) chunks = inner;
         if (!image) {  // the chunk's tables have to fit
@@ -823,11 +923,18 @@ inline void softmax_type(const RelationArgs& a, cudaStream_t st)
         }
         const int per = static_cast<int>(blocks_over(inner, chunks));
         const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(blocks_over(inner, per)));
+        auto run = [&](auto* kernel) {
+            if (smem > 40 * 1024) ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
+            kernel<<<grid, 256, smem, st>>>(a, per);
+        };
         if (image) {
-            relation_softmax_kernel<S, true><<<grid, 256, 0, st>>>(a, per);
+            if constexpr (Stretch<S>::USED) {
+                if (staged) return run(relation_softmax_kernel<S, true, true>);
+            }
+            run(relation_softmax_kernel<S, true, false>);
         } else {
-            const size_t smem = 4 * static_cast<size_t>(per) * (a.num_buckets + 1);
-            relation_softmax_kernel<S, false><<<grid, 256, smem, st>>>(a, per);
+            smem = 4 * static_cast<size_t>(per) * (a.num_buckets + 1);
+            run(relation_softmax_kernel<S, false, false>);
         }
     });
 }
