@@ -133,43 +133,60 @@ __device__ __forceinline__ float piece_rows(const NormArgs& a, const NormTile& t
     return static_cast<float>(left < t.per ? (left > 0 ? left : 0) : t.per);
 }
 
-// f(row, vectors...) for a thread's rows, B of them loaded before the first
-// is worked on.
+// f(vectors..., index in the result) for a thread's rows, B of them loaded
+// before the first is worked on.
 template <int B, typename T, int V, typename F>
-__device__ __forceinline__ void each_row(const T* x, int64_t pitch, int r, int end, int step, F f)
+__device__ __forceinline__ void each_row(const NormArgs& a, const Spot& p, F f)
 {
-    x += r * pitch;
-    const int64_t stride = step * pitch;
-    for (; r < end; r += B * step) {
+    int n = (p.row_end - p.row - p.ty + p.rows - 1) / p.rows;  // rows of this thread; below 1 for none
+    const T* x = static_cast<const T*>(a.x) + p.image * a.x_image + (p.row + p.ty) * a.x_pixel + p.channel;
+    const int64_t stride = p.rows * a.x_pixel, advance = static_cast<int64_t>(p.rows) * a.channels;
+    int64_t at = (p.image * a.pixels + p.row + p.ty) * a.channels + p.channel;
+    for (; n >= B; n -= B) {
         Pack<T, V> q[B];
 #pragma unroll
-        for (int k = 0; k < B; ++k, x += stride)
-            if (r + k * step < end) q[k] = *reinterpret_cast<const Pack<T, V>*>(x);
+        for (int k = 0; k < B; ++k, x += stride) q[k] = *reinterpret_cast<const Pack<T, V>*>(x);
 #pragma unroll
-        for (int k = 0; k < B; ++k)
-            if (r + k * step < end) f(r + k * step, q[k]);
+        for (int k = 0; k < B; ++k, at += advance) f(q[k], at);
     }
+    Pack<T, V> q[B];
+#pragma unroll
+    for (int k = 0; k < B - 1; ++k, x += stride)
+        if (k < n) q[k] = *reinterpret_cast<const Pack<T, V>*>(x);
+#pragma unroll
+    for (int k = 0; k < B - 1; ++k, at += advance)
+        if (k < n) f(q[k], at);
 }
 
 template <int B, typename T, int V, typename F>
-__device__ __forceinline__ void each_row(const T* x, int64_t pitch, const T* dy, int64_t dpitch, int r, int end,
-                                         int step, F f)
+__device__ __forceinline__ void each_row_pair(const NormArgs& a, const Spot& p, F f)
 {
-    x += r * pitch;
-    dy += r * dpitch;
-    const int64_t stride = step * pitch, dstride = step * dpitch;
-    for (; r < end; r += B * step) {
+    int n = (p.row_end - p.row - p.ty + p.rows - 1) / p.rows;
+    const T* x = static_cast<const T*>(a.x) + p.image * a.x_image + (p.row + p.ty) * a.x_pixel + p.channel;
+    const T* dy = static_cast<const T*>(a.dy) + p.image * a.dy_image + (p.row + p.ty) * a.dy_pixel + p.channel;
+    const int64_t stride = p.rows * a.x_pixel, dstride = p.rows * a.dy_pixel;
+    const int64_t advance = static_cast<int64_t>(p.rows) * a.channels;
+    int64_t at = (p.image * a.pixels + p.row + p.ty) * a.channels + p.channel;
+    for (; n >= B; n -= B) {
         Pack<T, V> q[B], d[B];
 #pragma unroll
-        for (int k = 0; k < B; ++k, x += stride, dy += dstride)
-            if (r + k * step < end) {
-                q[k] = *reinterpret_cast<const Pack<T, V>*>(x);
-                d[k] = *reinterpret_cast<const Pack<T, V>*>(dy);
-            }
+        for (int k = 0; k < B; ++k, x += stride, dy += dstride) {
+            q[k] = *reinterpret_cast<const Pack<T, V>*>(x);
+            d[k] = *reinterpret_cast<const Pack<T, V>*>(dy);
+        }
 #pragma unroll
-        for (int k = 0; k < B; ++k)
-            if (r + k * step < end) f(r + k * step, q[k], d[k]);
+        for (int k = 0; k < B; ++k, at += advance) f(q[k], d[k], at);
     }
+    Pack<T, V> q[B], d[B];
+#pragma unroll
+    for (int k = 0; k < B - 1; ++k, x += stride, dy += dstride)
+        if (k < n) {
+            q[k] = *reinterpret_cast<const Pack<T, V>*>(x);
+            d[k] = *reinterpret_cast<const Pack<T, V>*>(dy);
+        }
+#pragma unroll
+    for (int k = 0; k < B - 1; ++k, at += advance)
+        if (k < n) f(q[k], d[k], at);
 }
 
 // (mean, squared deviations) of each row piece by column: a vector (ONE: its
@@ -188,13 +205,14 @@ norm_partial_kernel(NormArgs a, NormTile t, NormScratch w)
 #pragma unroll
     for (int i = 0; i < P; ++i) first[i] = s[i] = q[i] = 0.0f;
     if (p.in) {
-        const T* x = static_cast<const T*>(a.x) + p.image * a.x_image + p.channel;
         const int begin = p.row + p.ty;
         if (begin < p.row_end) {
+            const T* x = static_cast<const T*>(a.x) + p.image * a.x_image + begin * a.x_pixel + p.channel;
 #pragma unroll
-            for (int i = 0; i < P; ++i) first[i] = to_f32(x[begin * a.x_pixel + i]);
+            for (int i = 0; i < P; ++i) first[i] = to_f32(x[i]);
+            rows = (p.row_end - begin + p.rows - 1) / p.rows;
         }
-        each_row<4, T, V>(x, a.x_pixel, begin, p.row_end, p.rows, [&](int, const Pack<T, V>& pack) {
+        each_row<4, T, V>(a, p, [&](const Pack<T, V>& pack, int64_t) {
             float v[V];
             widen(v, pack);
 #pragma unroll
@@ -203,7 +221,6 @@ norm_partial_kernel(NormArgs a, NormTile t, NormScratch w)
                 s[ONE ? 0 : i] += d;
                 q[ONE ? 0 : i] = fmaf(d, d, q[ONE ? 0 : i]);
             }
-            ++rows;
         });
     }
     const int count = rows * (ONE ? V : 1);
@@ -322,16 +339,15 @@ norm_apply_kernel(NormArgs a, NormTile t)
         scale[i] = a.rstd[g] * (a.weight ? load_param<T>(a.weight, a.param_f32, p.channel + i) : 1.0f);
         shift[i] = a.bias ? load_param<T>(a.bias, a.param_f32, p.channel + i) : 0.0f;
     }
-    const T* x = static_cast<const T*>(a.x) + p.image * a.x_image + p.channel;
     T* y = static_cast<T*>(a.out);
-    each_row<4, T, V>(x, a.x_pixel, p.row + p.ty, p.row_end, p.rows, [&](int r, const Pack<T, V>& q) {
+    const bool dropping = a.drop.limit < 65536u;
+    each_row<4, T, V>(a, p, [&](const Pack<T, V>& q, int64_t at) {
         float v[V];
         widen(v, q);
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = fmaf(v[i] - mean[ONE ? 0 : i], scale[i], shift[i]);
         act_values<V>(v, ACT);
-        const int64_t at = (p.image * a.pixels + r) * a.channels + p.channel;
-        if (a.drop.limit < 65536u) drop<V>(v, static_cast<uint64_t>(at), a.drop);
+        if (dropping) drop<V>(v, static_cast<uint64_t>(at), a.drop);
         stream_row<T, V>(y + at, v);
     });
 }
@@ -384,12 +400,9 @@ norm_grad_partial_kernel(NormArgs a, NormTile t, NormScratch w)
     if (p.in) {
         float mean[P], scale[V], bias[V];
         load_channels<T, V, P>(a, p, mean, scale, bias);
-        each_row<2, T, V>(static_cast<const T*>(a.x) + p.image * a.x_image + p.channel, a.x_pixel,
-                          static_cast<const T*>(a.dy) + p.image * a.dy_image + p.channel, a.dy_pixel, p.row + p.ty,
-                          p.row_end, p.rows, [&](int r, const Pack<T, V>& x, const Pack<T, V>& dy) {
+        each_row_pair<2, T, V>(a, p, [&](const Pack<T, V>& x, const Pack<T, V>& dy, int64_t at) {
             float d[V], dz[V];
-            slope_row<ACT>(a, mean, scale, bias, x, dy,
-                               static_cast<uint64_t>((p.image * a.pixels + r) * a.channels + p.channel), d, dz);
+            slope_row<ACT>(a, mean, scale, bias, x, dy, static_cast<uint64_t>(at), d, dz);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 sa[i] += dz[i];
@@ -525,11 +538,8 @@ norm_grad_apply_kernel(NormArgs a, NormTile t, NormScratch w)
         m1[i] = -r * w.ga[g];
         m2[i] = -r * r * w.gb[g];
     }
-    each_row<2, T, V>(static_cast<const T*>(a.x) + p.image * a.x_image + p.channel, a.x_pixel,
-                      static_cast<const T*>(a.dy) + p.image * a.dy_image + p.channel, a.dy_pixel, p.row + p.ty,
-                      p.row_end, p.rows, [&](int r, const Pack<T, V>& x, const Pack<T, V>& dy) {
+    each_row_pair<2, T, V>(a, p, [&](const Pack<T, V>& x, const Pack<T, V>& dy, int64_t at) {
         float d[V], dz[V];
-        const int64_t at = (p.image * a.pixels + r) * a.channels + p.channel;
         slope_row<ACT>(a, mean, scale, bias, x, dy, static_cast<uint64_t>(at), d, dz);
         if (a.drop.limit < 65536u) {
 #pragma unroll
