@@ -247,3 +247,13 @@ def test_refusals():
               (p.repeat(2, 1, 1), p.repeat(3, 1, 1)[:3], lut)):
         with pytest.raises(ValueError):
             g.relation_buckets(*a)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("B,H,Q,K", [(9, 8, 49, 49), (5, 8, 33, 25), (6, 16, 9, 9), (3, 8, 81, 81), (7, 8, 40, 121),
+                                     (5, 3, 49, 49), (4, 8, 65, 63), (2, 8, 1, 7)])
+def test_short_odd_rows_by_image(t, B, H, Q, K):
+    """Odd rows of one map for all images: an image's rows are a multiple of
+    16 bytes or not, the last block's rows end inside a vector, images in
+    fours and a remainder."""
+    _check(*_inputs(B + K, B, H, Q, K, t, 31, 1))
