@@ -27,7 +27,8 @@ constexpr int NT = 256;  // threads of a block
 
 // ---------------------------------------------------------------- streaming
 //
-// Large maps in three launches: sums by rows' pieces, their join, and the
+// Large maps in two launches: sums by rows' pieces; then their join (every
+// block for its own groups: some kilobytes from L2 and a launch less) and the
 // results.  The second reading comes from L2 as far as that holds the map:
 // the last launch goes through the pieces backwards and its stores are marked
 // as streaming.
@@ -43,11 +44,11 @@ inline int64_t norm_pieces(int64_t batch, int64_t pixels, int channels)
     return p < 1 ? 1 : p;
 }
 
-// Scratch: three partial planes [batch][pieces][channels] (forward: mean high,
-// M2, mean low; the gradient's two sums), two of [batch][channels] (the
-// gradient's sums of an image) and two of [batch][groups].
+// Scratch: four partial planes [batch][pieces][channels] (forward: mean high,
+// M2, mean low; gradient: two sums by channel, two by column) and two of
+// [batch][channels] (the cluster gradient's sums of an image).
 struct NormScratch {
-    float *pa, *pb, *pc, *ca, *cb, *ga, *gb;
+    float *pa, *pb, *pc, *pd, *ca, *cb;
 };
 
 inline NormScratch scratch(const NormArgs& a, void* ws)
@@ -58,10 +59,9 @@ inline NormScratch scratch(const NormArgs& a, void* ws)
     s.pa = static_cast<float*>(ws);
     s.pb = s.pa + plane;
     s.pc = s.pb + plane;
-    s.ca = s.pc + plane;
+    s.pd = s.pc + plane;
+    s.ca = s.pd + plane;
     s.cb = s.ca + image;
-    s.ga = s.cb + image;
-    s.gb = s.ga + static_cast<size_t>(a.batch) * a.groups;
     return s;
 }
 
@@ -71,6 +71,7 @@ struct NormTile {
     int tiles;   // tiles a row of the map
     int pieces;  // of an image
     int per;     // rows a piece
+    int values;  // channels of a column of the partial planes: a vector's (of one group), one, or a group's
 };
 
 template <typename T, int V>
@@ -236,6 +237,7 @@ norm_partial_kernel(NormArgs a, NormTile t, NormScratch w)
     }
     __syncthreads();
     const int width = t.wide * P, columns = a.channels / (ONE ? V : 1);
+    const bool by_group = t.values > (ONE ? V : 1);
     for (int c = threadIdx.x; c < width; c += NT) {
         const int column = static_cast<int>(blockIdx.y) * width + c;
         if (column >= columns) continue;
@@ -255,89 +257,149 @@ norm_partial_kernel(NormArgs a, NormTile t, NormScratch w)
             m2 += fmaf(k * d, d, s_m2[at]);
         }
         low *= each;
-        const int64_t at = (p.image * t.pieces + p.piece) * static_cast<int64_t>(columns) + column;
+        m2 = fmaxf(m2 - n * low * low, 0.0f);
+        if (by_group) {  // entry c has been read by this thread alone
+            s_high[c] = mean;
+            s_low[c] = low;
+            s_m2[c] = m2;
+        } else {
+            const int64_t at = (p.image * t.pieces + p.piece) * static_cast<int64_t>(columns) + column;
+            w.pa[at] = mean;
+            w.pb[at] = m2;
+            w.pc[at] = low;
+        }
+    }
+    if (!by_group) return;
+    // The tile holds every channel: the columns of a group, alike in count, become one piece.
+    __syncthreads();
+    const int each = t.values / (ONE ? V : 1);
+    const float n = static_cast<float>(p.row_end - p.row) * (ONE ? V : 1), share = 1.0f / each;
+    for (int g = threadIdx.x; g < a.groups; g += NT) {
+        const float origin = s_high[g * each];
+        float mean = 0.0f, low = 0.0f, m2 = 0.0f;
+        for (int c = g * each; c < (g + 1) * each; ++c) mean += s_high[c] + s_low[c] - origin;
+        mean = fmaf(mean, share, origin);
+        for (int c = g * each; c < (g + 1) * each; ++c) {
+            const float d = (s_high[c] - mean) + s_low[c];
+            low += d;
+            m2 += fmaf(n * d, d, s_m2[c]);
+        }
+        low *= share;
+        const int64_t at = (p.image * t.pieces + p.piece) * a.groups + g;
         w.pa[at] = mean;
-        w.pb[at] = fmaxf(m2 - n * low * low, 0.0f);
+        w.pb[at] = fmaxf(m2 - n * each * low * low, 0.0f);
         w.pc[at] = low;
     }
 }
 
-// Sum over a team of 32 threads (a warp) or NT (the block; s: 8 floats).
-template <int TEAM>
-__device__ __forceinline__ float team_sum(float v, float* s)
+// Groups that a tile meets, and the threads (a power of two) that join each
+// one's pieces.
+struct Joint {
+    int first, groups, team;
+};
+
+template <int V>
+__device__ __forceinline__ Joint joint(const NormArgs& a, const NormTile& t)
 {
-    v = warp_sum(v);
-    if (TEAM > 32) {
+    Joint j;
+    const int D = a.channels / a.groups, c0 = static_cast<int>(blockIdx.y) * t.wide * V;
+    const int c1 = c0 + t.wide * V < a.channels ? c0 + t.wide * V : a.channels;
+    j.first = c0 / D;
+    j.groups = (c1 - 1) / D - j.first + 1;
+    for (j.team = NT; j.team > 1 && j.team * j.groups > NT; j.team /= 2) {}
+    return j;
+}
+
+// Sum over each team of a block; every thread calls it.  s: 8 floats.
+__device__ __forceinline__ float team_sum(float v, int team, float* s)
+{
+    for (int o = (team < 32 ? team : 32) / 2; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    if (team > 32) {
+        __syncthreads();
         if (lane_id() == 0) s[threadIdx.x / 32] = v;
         __syncthreads();
-        v = s[0];
-#pragma unroll
-        for (int k = 1; k < TEAM / 32; ++k) v += s[k];
+        const int warps = team / 32, first = static_cast<int>(threadIdx.x) / team * warps;
+        v = 0.0f;
+        for (int k = 0; k < warps; ++k) v += s[first + k];
     }
     return v;
 }
 
-// mean and rstd of each (image, group) from the pieces of `each` columns of
-// `values` channels a group; TEAM threads each.
-template <int TEAM>
-__global__ void __launch_bounds__(NT)
-norm_finish_kernel(NormArgs a, NormTile t, NormScratch w, int each, int values)
+constexpr int MOST_GROUPS = 64 * 8;  // that a tile meets
+
+// mean and rstd of the tile's groups from the pieces (their geometry: from)
+// into s_mean, s_rstd; the first piece's block of the tile that holds a
+// group's first channel writes them out.
+__device__ __forceinline__ void join_moments(const NormArgs& a, const NormTile& from, const Spot& p,
+                                             const NormScratch& w, const Joint& j, int first_channel, float* s_mean,
+                                             float* s_rstd)
 {
-    __shared__ float red[3][NT / 32];
-    pdl_wait();
-    pdl_release();
-    const int64_t which = (static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x) / TEAM;
-    if (which >= a.batch * a.groups) return;  // whole teams
-    const int lane = static_cast<int>(threadIdx.x) % TEAM;
-    const int64_t image = which / a.groups;
-    const int columns = a.channels / values, items = t.pieces * each;
-    const int64_t base = image * t.pieces * columns + which % a.groups * each;
-    const float all = static_cast<float>(a.pixels) * static_cast<float>(a.channels / a.groups), each_all = 1.0f / all;
-    // Deviations of the pieces' means from the first piece's: equal means give exactly that mean.
-    const float origin = w.pa[base];
-    float mean = 0.0f, low = 0.0f, m2 = 0.0f;
+    __shared__ float red[NT / 32];
+    const int D = a.channels / a.groups, values = from.values, each = D / values, columns = a.channels / values;
+    const int items = from.pieces * each, lane = static_cast<int>(threadIdx.x) % j.team;
+    const float all = static_cast<float>(a.pixels) * static_cast<float>(D), each_all = 1.0f / all;
+    for (int k0 = 0; k0 < j.groups; k0 += NT / j.team) {
+        const int k = k0 + static_cast<int>(threadIdx.x) / j.team, g = j.first + (k < j.groups ? k : 0);
+        const int64_t base = p.image * from.pieces * columns + static_cast<int64_t>(g) * each;
+        // Deviations of the pieces' means from the first piece's: equal means give exactly that mean.
+        const float origin = w.pa[base];
+        float mean = 0.0f, low = 0.0f, m2 = 0.0f;
 #pragma unroll 4
-    for (int i = lane; i < items; i += TEAM) {
-        const int piece = i / each;
-        const float k = piece_rows(a, t, piece) * values;
-        const float high = w.pa[base + static_cast<int64_t>(piece) * columns + (i - piece * each)];
-        if (k > 0.0f) mean = fmaf(high - origin, k * each_all, mean);
-    }
-    mean = origin + team_sum<TEAM>(mean, red[0]);
+        for (int i = lane; i < items; i += j.team) {
+            const int piece = i / each;
+            const float n = piece_rows(a, from, piece) * values;
+            const float high = w.pa[base + static_cast<int64_t>(piece) * columns + (i - piece * each)];
+            if (n > 0.0f) mean = fmaf(high - origin, n * each_all, mean);
+        }
+        mean = origin + team_sum(mean, j.team, red);
 #pragma unroll 4
-    for (int i = lane; i < items; i += TEAM) {
-        const int piece = i / each;
-        const int64_t at = base + static_cast<int64_t>(piece) * columns + (i - piece * each);
-        const float k = piece_rows(a, t, piece) * values, d = (w.pa[at] - mean) + w.pc[at], m = w.pb[at];
-        if (k > 0.0f) {
-            low = fmaf(d, k * each_all, low);
-            m2 += fmaf(d * k, d, m);
+        for (int i = lane; i < items; i += j.team) {
+            const int piece = i / each;
+            const int64_t at = base + static_cast<int64_t>(piece) * columns + (i - piece * each);
+            const float n = piece_rows(a, from, piece) * values, d = (w.pa[at] - mean) + w.pc[at], m = w.pb[at];
+            if (n > 0.0f) {
+                low = fmaf(d, n * each_all, low);
+                m2 += fmaf(d * n, d, m);
+            }
+        }
+        low = team_sum(low, j.team, red);
+        m2 = team_sum(m2, j.team, red);
+        if (lane == 0 && k < j.groups) {
+            const float m = mean + low, r = 1.0f / sqrtf(fmaxf(m2 / all - low * low, 0.0f) + a.eps);
+            s_mean[k] = m;
+            s_rstd[k] = r;
+            if (p.piece == 0 && g * D >= first_channel) {
+                if (a.mean) a.mean[p.image * a.groups + g] = m;
+                if (a.rstd) a.rstd[p.image * a.groups + g] = r;
+            }
         }
     }
-    low = team_sum<TEAM>(low, red[1]);
-    m2 = team_sum<TEAM>(m2, red[2]);
-    if (lane == 0) {
-        a.mean[which] = mean + low;
-        a.rstd[which] = 1.0f / sqrtf(fmaxf(m2 / all - low * low, 0.0f) + a.eps);
-    }
+    __syncthreads();
 }
 
 template <typename T, int V, bool ONE, int ACT>
 __global__ void __launch_bounds__(NT, 3)
-norm_apply_kernel(NormArgs a, NormTile t)
+norm_apply_kernel(NormArgs a, NormTile t, NormTile from, NormScratch w)
 {
     constexpr int P = ONE ? 1 : V;
+    __shared__ float s_mean[MOST_GROUPS], s_rstd[MOST_GROUPS];
     const Spot p = spot<V>(a, t, gridDim.x - 1 - blockIdx.x);  // the pieces read last come first
-    pdl_wait();
-    if (!p.in) return;
-    const int D = a.channels / a.groups;
+    const Joint j = joint<V>(a, t);
     float mean[P], scale[V], shift[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int64_t g = p.image * a.groups + (p.channel + i) / D;
-        if (i < P) mean[i] = a.mean[g];
-        scale[i] = a.rstd[g] * (a.weight ? load_param<T>(a.weight, a.param_f32, p.channel + i) : 1.0f);
-        shift[i] = a.bias ? load_param<T>(a.bias, a.param_f32, p.channel + i) : 0.0f;
+        scale[i] = p.in && a.weight ? load_param<T>(a.weight, a.param_f32, p.channel + i) : 1.0f;
+        shift[i] = p.in && a.bias ? load_param<T>(a.bias, a.param_f32, p.channel + i) : 0.0f;
+    }
+    pdl_wait();
+    join_moments(a, from, p, w, j, static_cast<int>(blockIdx.y) * t.wide * V, s_mean, s_rstd);
+    if (!p.in) return;
+    const int D = a.channels / a.groups;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int g = (p.channel + i) / D - j.first;
+        if (i < P) mean[i] = s_mean[g];
+        scale[i] *= s_rstd[g];
     }
     T* y = static_cast<T*>(a.out);
     const bool dropping = a.drop.limit < 65536u;
@@ -416,6 +478,7 @@ norm_grad_partial_kernel(NormArgs a, NormTile t, NormScratch w)
         s_b[threadIdx.x * V + i] = sb[i];
     }
     __syncthreads();
+    const float factor = a.drop.limit < 65536u ? a.drop.factor : 1.0f;
     for (int c = threadIdx.x; c < t.wide * V; c += NT) {
         const int channel = static_cast<int>(blockIdx.y) * t.wide * V + c;
         if (channel >= a.channels) continue;
@@ -424,70 +487,89 @@ norm_grad_partial_kernel(NormArgs a, NormTile t, NormScratch w)
             va += s_a[y * t.wide * V + c];
             vb += s_b[y * t.wide * V + c];
         }
+        va *= factor;
+        vb *= factor;
         const int64_t at = (p.image * t.pieces + p.piece) * static_cast<int64_t>(a.channels) + channel;
-        const float factor = a.drop.limit < 65536u ? a.drop.factor : 1.0f;
-        w.pa[at] = va * factor;
-        w.pb[at] = vb * factor;
+        w.pa[at] = va;
+        w.pb[at] = vb;
+        // For the groups: by column, times the weights.
+        const float weight = a.weight ? load_param<T>(a.weight, a.param_f32, channel) : 1.0f;
+        s_a[c] = va * weight;  // read by this thread alone so far
+        s_b[c] = vb * weight;
+    }
+    __syncthreads();
+    const int width = t.wide * V / t.values, columns = a.channels / t.values;
+    for (int c = threadIdx.x; c < width; c += NT) {
+        const int column = static_cast<int>(blockIdx.y) * width + c;
+        if (column >= columns) continue;
+        float va = 0.0f, vb = 0.0f;
+        for (int i = 0; i < t.values; ++i) {
+            va += s_a[c * t.values + i];
+            vb += s_b[c * t.values + i];
+        }
+        const int64_t at = (p.image * t.pieces + p.piece) * static_cast<int64_t>(columns) + column;
+        w.pc[at] = va;
+        w.pd[at] = vb;
     }
 }
 
-// One block per image and `chunk` channels (whole groups): the image's sums
-// of dz and dz * u by channel, and avg(du) and avg(du * u) by group.
-template <typename T>
-__global__ void __launch_bounds__(NT)
-norm_grad_finish_kernel(NormArgs a, NormTile t, NormScratch w, int chunk)
+// Sums of du and du * (x - mean) of the tile's groups from the pieces.
+__device__ __forceinline__ void join_sums(const NormArgs& a, const NormTile& from, const Spot& p, const NormScratch& w,
+                                          const Joint& j, float* s_a, float* s_b)
 {
-    extern __shared__ float s_sum[];  // [2][chunk]
-    __shared__ float s_a[NT], s_b[NT];
-    pdl_wait();
-    pdl_release();
-    const int D = a.channels / a.groups, c0 = static_cast<int>(blockIdx.y) * chunk;
-    const int64_t image = blockIdx.x;
-    const int channels = c0 + chunk < a.channels ? chunk : a.channels - c0;
-    const int across = channels < NT ? channels : NT, lists = NT / across;
-    const int x = static_cast<int>(threadIdx.x) % across, y = static_cast<int>(threadIdx.x) / across;
-    for (int c = x; c - x < channels; c += across) {
+    __shared__ float red[NT / 32];
+    const int D = a.channels / a.groups, each = D / from.values, columns = a.channels / from.values;
+    const int items = from.pieces * each, lane = static_cast<int>(threadIdx.x) % j.team;
+    for (int k0 = 0; k0 < j.groups; k0 += NT / j.team) {
+        const int k = k0 + static_cast<int>(threadIdx.x) / j.team, g = j.first + (k < j.groups ? k : 0);
+        const int64_t base = p.image * from.pieces * columns + static_cast<int64_t>(g) * each;
         float va = 0.0f, vb = 0.0f;
-        if (y < lists && c < channels) {
-            const int64_t at = image * t.pieces * a.channels + c0 + c;
 #pragma unroll 4
-            for (int k = y; k < t.pieces; k += lists) {
-                va += w.pa[at + static_cast<int64_t>(k) * a.channels];
-                vb += w.pb[at + static_cast<int64_t>(k) * a.channels];
-            }
+        for (int i = lane; i < items; i += j.team) {
+            const int piece = i / each;
+            const int64_t at = base + static_cast<int64_t>(piece) * columns + (i - piece * each);
+            va += w.pc[at];
+            vb += w.pd[at];
         }
-        s_a[threadIdx.x] = va;
-        s_b[threadIdx.x] = vb;
-        __syncthreads();
-        if (y == 0 && c < channels) {
-            for (int k = 1; k < lists; ++k) {
-                va += s_a[k * across + x];
-                vb += s_b[k * across + x];
-            }
-            const int64_t g = image * a.groups + (c0 + c) / D;
-            const float weight = a.weight ? load_param<T>(a.weight, a.param_f32, c0 + c) : 1.0f;
-            vb *= a.rstd[g];  // u = (x - mean) * rstd
-            w.ca[image * a.channels + c0 + c] = va;
-            w.cb[image * a.channels + c0 + c] = vb;
-            s_sum[c] = va * weight;
-            s_sum[chunk + c] = vb * weight;
+        va = team_sum(va, j.team, red);
+        vb = team_sum(vb, j.team, red);
+        if (lane == 0 && k < j.groups) {
+            s_a[k] = va;
+            s_b[k] = vb;
         }
-        __syncthreads();
     }
-    const float each_all = 1.0f / (static_cast<float>(a.pixels) * static_cast<float>(D));
-    for (int g = static_cast<int>(threadIdx.x) / 32; g < channels / D; g += NT / 32) {
-        float va = 0.0f, vb = 0.0f;
-        for (int i = static_cast<int>(lane_id()); i < D; i += 32) {
-            va += s_sum[g * D + i];
-            vb += s_sum[chunk + g * D + i];
+    __syncthreads();
+}
+
+constexpr int PARAMS = 8;  // channels of a block that sums dweight and dbias
+
+// dweight and dbias of PARAMS channels from every image's pieces: 32 threads a
+// channel, joined in order.
+__device__ __forceinline__ void param_pieces(const NormArgs& a, const NormTile& from, const NormScratch& w, int c0)
+{
+    __shared__ float s_a[NT], s_b[NT];
+    const int x = static_cast<int>(threadIdx.x) % PARAMS, y = static_cast<int>(threadIdx.x) / PARAMS, c = c0 + x;
+    float va = 0.0f, vb = 0.0f;
+    if (c < a.channels) {
+        const unsigned items = static_cast<unsigned>(a.batch) * from.pieces, pieces = from.pieces;
+        const int g = c / (a.channels / a.groups);
+#pragma unroll 4
+        for (unsigned i = y; i < items; i += NT / PARAMS) {
+            const int64_t at = static_cast<int64_t>(i) * a.channels + c;
+            va += w.pa[at];
+            vb = fmaf(w.pb[at], a.rstd[static_cast<int64_t>(i / pieces) * a.groups + g], vb);  // u = (x - mean) * rstd
         }
-        va = warp_sum(va);
-        vb = warp_sum(vb);
-        if (lane_id() == 0) {
-            const int64_t at = image * a.groups + c0 / D + g;
-            w.ga[at] = va * each_all;
-            w.gb[at] = vb * each_all;
+    }
+    s_a[threadIdx.x] = va;
+    s_b[threadIdx.x] = vb;
+    __syncthreads();
+    if (y == 0 && c < a.channels) {
+        for (int k = 1; k < NT / PARAMS; ++k) {
+            va += s_a[k * PARAMS + x];
+            vb += s_b[k * PARAMS + x];
         }
+        if (a.dbias) a.dbias[c] = va;
+        if (a.dweight) a.dweight[c] = vb;
     }
 }
 
@@ -515,28 +597,31 @@ norm_grad_param_kernel(NormArgs a, NormScratch w)
 // dx; the blocks past the pieces' (the first to run) write dweight and dbias.
 template <typename T, int V, bool ONE, int ACT>
 __global__ void __launch_bounds__(NT, ONE ? 3 : 2)
-norm_grad_apply_kernel(NormArgs a, NormTile t, NormScratch w)
+norm_grad_apply_kernel(NormArgs a, NormTile t, NormTile from, NormScratch w)
 {
     constexpr int P = ONE ? 1 : V;
+    __shared__ float s_a[MOST_GROUPS], s_b[MOST_GROUPS];
     const unsigned block = gridDim.x - 1 - blockIdx.x, main = static_cast<unsigned>(a.batch) * t.pieces;
     if (block >= main) {
         pdl_wait();
-        const int c = static_cast<int>(block - main) * NT + static_cast<int>(threadIdx.x);
-        if (blockIdx.y == 0 && c < a.channels) param_sums(a, w.ca, w.cb, c);
+        if (blockIdx.y == 0) param_pieces(a, from, w, static_cast<int>(block - main) * PARAMS);
         return;
     }
     const Spot p = spot<V>(a, t, block);
+    const Joint j = joint<V>(a, t);
+    float mean[P], scale[V], bias[V], m1[P], m2[P];
+    if (p.in) load_channels<T, V, P>(a, p, mean, scale, bias);
     pdl_wait();
+    join_sums(a, from, p, w, j, s_a, s_b);
     if (!p.in) return;
     const int D = a.channels / a.groups;
-    float mean[P], scale[V], bias[V], m1[P], m2[P];
-    load_channels<T, V, P>(a, p, mean, scale, bias);
+    const float each_all = 1.0f / (static_cast<float>(a.pixels) * static_cast<float>(D));
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const int64_t g = p.image * a.groups + (p.channel + i) / D;
-        const float r = a.rstd[g];
-        m1[i] = -r * w.ga[g];
-        m2[i] = -r * r * w.gb[g];
+        const int g = (p.channel + i) / D;
+        const float r = a.rstd[p.image * a.groups + g];
+        m1[i] = -r * s_a[g - j.first] * each_all;
+        m2[i] = -r * r * r * s_b[g - j.first] * each_all;
     }
     each_row_pair<2, T, V>(a, p, [&](const Pack<T, V>& x, const Pack<T, V>& dy, int64_t at) {
         float d[V], dz[V];
@@ -1114,6 +1199,10 @@ inline NormTile tile(const NormArgs& a, int v)
     t.tiles = (vecs + t.wide - 1) / t.wide;
     t.pieces = static_cast<int>(norm_pieces(a.batch, a.pixels, a.channels));
     t.per = static_cast<int>((a.pixels + t.pieces - 1) / t.pieces);
+    // Pieces by group where a block sees every channel and a group has few columns.
+    const int D = a.channels / a.groups;
+    t.values = D % v == 0 ? v : 1;
+    if (t.tiles == 1 && D / t.values <= 16) t.values = D;
     return t;
 }
 
@@ -1211,36 +1300,19 @@ static void norm_streamed(const NormArgs& a, void* ws, cudaStream_t st, bool gra
     const NormScratch w = scratch(a, ws);
     const dim3 block(NT);
     auto grid = [&](const NormTile& t) { return dim3(static_cast<unsigned>(a.batch * t.pieces), t.tiles); };
-    const int D = a.channels / a.groups;
     if (!grad) {
         static const int sums = resident_blocks(reinterpret_cast<const void*>(norm_partial_kernel<T, V, ONE>));
         static const int rows = resident_blocks(reinterpret_cast<const void*>(norm_apply_kernel<T, V, ONE, ACT>));
         const NormTile t = one_wave(a, most, sums), u = one_wave(a, most, rows);
-        NormArgs b = a;
-        if (!b.mean) b.mean = w.ga;
-        if (!b.rstd) b.rstd = w.gb;
-        norm_partial_kernel<T, V, ONE><<<grid(t), block, 0, st>>>(b, t, w);
-        const int each = ONE ? D / V : D, values = ONE ? V : 1;
-        const int64_t groups = a.batch * a.groups;
-        if (t.pieces * each > 128)
-            launch_pdl(norm_finish_kernel<NT>, dim3(static_cast<unsigned>(groups)), block, 0, st, b, t, w, each, values);
-        else
-            launch_pdl(norm_finish_kernel<32>, dim3(static_cast<unsigned>((groups + NT / 32 - 1) / (NT / 32))), block, 0,
-                       st, b, t, w, each, values);
-        launch_pdl(norm_apply_kernel<T, V, ONE, ACT>, grid(u), block, 0, st, b, u);
+        norm_partial_kernel<T, V, ONE><<<grid(t), block, 0, st>>>(a, t, w);
+        launch_pdl(norm_apply_kernel<T, V, ONE, ACT>, grid(u), block, 0, st, a, u, t, w);
     } else {
         static const int sums = resident_blocks(reinterpret_cast<const void*>(norm_grad_partial_kernel<T, V, ONE, ACT>));
         static const int rows = resident_blocks(reinterpret_cast<const void*>(norm_grad_apply_kernel<T, V, ONE, ACT>));
         const NormTile t = one_wave(a, most, sums), u = one_wave(a, most, rows);
-        const int chunk = D > 32 ? D : 32 / D * D;
         norm_grad_partial_kernel<T, V, ONE, ACT><<<grid(t), block, 0, st>>>(a, t, w);
-        const size_t smem = 8 * static_cast<size_t>(chunk);
-        if (chunk > 4096) ensure_dynamic_smem(reinterpret_cast<const void*>(norm_grad_finish_kernel<T>), smem);
-        launch_pdl(norm_grad_finish_kernel<T>,
-                   dim3(static_cast<unsigned>(a.batch), static_cast<unsigned>((a.channels + chunk - 1) / chunk)), block,
-                   smem, st, a, t, w, chunk);
-        const unsigned params = a.dweight || a.dbias ? (a.channels + NT - 1) / NT : 0;
-        launch_pdl(norm_grad_apply_kernel<T, V, ONE, ACT>, dim3(grid(u).x + params, u.tiles), block, 0, st, a, u, w);
+        const unsigned params = a.dweight || a.dbias ? (a.channels + PARAMS - 1) / PARAMS : 0;
+        launch_pdl(norm_grad_apply_kernel<T, V, ONE, ACT>, dim3(grid(u).x + params, u.tiles), block, 0, st, a, u, t, w);
     }
 }
 
@@ -1267,7 +1339,11 @@ static void norm_width(const NormArgs& a, void* ws, cudaStream_t st, bool grad)
 template <typename T>
 static void norm_type(const NormArgs& a, void* ws, cudaStream_t st, bool grad)
 {
-    const int v = vector_width(a);
+    int v = vector_width(a);
+    // Eight-byte vectors that lie in one group before sixteen-byte ones that do not (their sums and moments are kept
+    // by channel: 8 x 25600 x 128 in groups of 4, 47 us forward for 40), but where a generator's block serves eight.
+    if (a.drop.limit == 65536u && v * sizeof(T) == 16 && a.channels / a.groups % v != 0 && a.channels / a.groups % (v / 2) == 0)
+        v /= 2;
     if constexpr (sizeof(T) == 2)
         if (v == 8) return norm_width<T, 8>(a, ws, st, grad);
     if (v == 4) return norm_width<T, 4>(a, ws, st, grad);
