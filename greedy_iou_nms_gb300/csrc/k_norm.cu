@@ -7,8 +7,7 @@ namespace gbnms {
 size_t norm_workspace_bytes(int64_t batch, int64_t pixels, int channels, int groups)
 {
     const size_t image = static_cast<size_t>(batch) * channels;
-    (void)groups;
-    return 16 * image * norm_pieces(batch, pixels, channels) + 8 * image + 256;
+    return 16 * image * norm_pieces(batch, pixels, channels) + 8 * image + 8 * static_cast<size_t>(batch) * groups + 256;
 }
 
 void norm_f32(const NormArgs& a, void* ws, cudaStream_t st, bool grad);

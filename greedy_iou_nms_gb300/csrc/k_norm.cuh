@@ -28,8 +28,8 @@ constexpr int NT = 256;  // threads of a block
 // ---------------------------------------------------------------- streaming
 //
 // Large maps in two launches: sums by rows' pieces; then their join (every
-// block for its own groups: some kilobytes from L2 and a launch less) and the
-// results.  The second reading comes from L2 as far as that holds the map:
+// block for its own groups: some kilobytes from L2 and a launch less; images
+// of many pieces in a launch of its own) and the results.  The second reading comes from L2 as far as that holds the map:
 // the last launch goes through the pieces backwards and its stores are marked
 // as streaming.
 
@@ -45,11 +45,17 @@ inline int64_t norm_pieces(int64_t batch, int64_t pixels, int channels)
 }
 
 // Scratch: four partial planes [batch][pieces][channels] (forward: mean high,
-// M2, mean low; gradient: two sums by channel, two by column) and two of
-// [batch][channels] (the cluster gradient's sums of an image).
+// M2, mean low; gradient: two sums by channel, two by column), two of
+// [batch][channels] (the cluster gradient's sums of an image) and two of
+// [batch][groups] (joined values).
 struct NormScratch {
-    float *pa, *pb, *pc, *pd, *ca, *cb;
+    float *pa, *pb, *pc, *pd, *ca, *cb, *ga, *gb;
 };
+
+// Columns of an image's pieces, for one group, that each block may join
+// itself; more are joined in a launch of their own (with 608 pieces of one
+// image the blocks' own joins took 40 us).
+constexpr int OWN_JOIN = 96;
 
 inline NormScratch scratch(const NormArgs& a, void* ws)
 {
@@ -62,6 +68,8 @@ inline NormScratch scratch(const NormArgs& a, void* ws)
     s.pd = s.pc + plane;
     s.ca = s.pd + plane;
     s.cb = s.ca + image;
+    s.ga = s.cb + image;
+    s.gb = s.ga + static_cast<size_t>(a.batch) * a.groups;
     return s;
 }
 
@@ -377,9 +385,20 @@ __device__ __forceinline__ void join_moments(const NormArgs& a, const NormTile& 
     __syncthreads();
 }
 
+// The joined values of the tile's groups, from two planes [batch][groups].
+__device__ __forceinline__ void load_joined(const NormArgs& a, const Spot& p, const Joint& j, const float* from_a,
+                                            const float* from_b, float* s_a, float* s_b)
+{
+    for (int k = threadIdx.x; k < j.groups; k += NT) {
+        s_a[k] = from_a[p.image * a.groups + j.first + k];
+        s_b[k] = from_b[p.image * a.groups + j.first + k];
+    }
+    __syncthreads();
+}
+
 template <typename T, int V, bool ONE, int ACT>
 __global__ void __launch_bounds__(NT, 3)
-norm_apply_kernel(NormArgs a, NormTile t, NormTile from, NormScratch w)
+norm_apply_kernel(NormArgs a, NormTile t, NormTile from, NormScratch w, bool joined)
 {
     constexpr int P = ONE ? 1 : V;
     __shared__ float s_mean[MOST_GROUPS], s_rstd[MOST_GROUPS];
@@ -392,7 +411,8 @@ norm_apply_kernel(NormArgs a, NormTile t, NormTile from, NormScratch w)
         shift[i] = p.in && a.bias ? load_param<T>(a.bias, a.param_f32, p.channel + i) : 0.0f;
     }
     pdl_wait();
-    join_moments(a, from, p, w, j, static_cast<int>(blockIdx.y) * t.wide * V, s_mean, s_rstd);
+    if (joined) load_joined(a, p, j, a.mean, a.rstd, s_mean, s_rstd);
+    else join_moments(a, from, p, w, j, static_cast<int>(blockIdx.y) * t.wide * V, s_mean, s_rstd);
     if (!p.in) return;
     const int D = a.channels / a.groups;
 #pragma unroll
@@ -541,6 +561,29 @@ __device__ __forceinline__ void join_sums(const NormArgs& a, const NormTile& fro
     __syncthreads();
 }
 
+// The join in a launch of its own: a block for each (image, group).
+template <bool GRAD>
+__global__ void __launch_bounds__(NT)
+norm_join_kernel(NormArgs a, NormTile from, NormScratch w)
+{
+    __shared__ float s_a[1], s_b[1];
+    pdl_wait();
+    pdl_release();
+    const unsigned G = static_cast<unsigned>(a.groups);
+    Spot p{};
+    p.image = blockIdx.x / G;
+    const Joint j{static_cast<int>(blockIdx.x % G), 1, NT};
+    if (!GRAD) {
+        join_moments(a, from, p, w, j, 0, s_a, s_b);
+    } else {
+        join_sums(a, from, p, w, j, s_a, s_b);
+        if (threadIdx.x == 0) {
+            w.ga[blockIdx.x] = s_a[0];
+            w.gb[blockIdx.x] = s_b[0];
+        }
+    }
+}
+
 constexpr int PARAMS = 8;  // channels of a block that sums dweight and dbias
 
 // dweight and dbias of PARAMS channels from every image's pieces: 32 threads a
@@ -597,7 +640,7 @@ norm_grad_param_kernel(NormArgs a, NormScratch w)
 // dx; the blocks past the pieces' (the first to run) write dweight and dbias.
 template <typename T, int V, bool ONE, int ACT>
 __global__ void __launch_bounds__(NT, ONE ? 3 : 2)
-norm_grad_apply_kernel(NormArgs a, NormTile t, NormTile from, NormScratch w)
+norm_grad_apply_kernel(NormArgs a, NormTile t, NormTile from, NormScratch w, bool joined)
 {
     constexpr int P = ONE ? 1 : V;
     __shared__ float s_a[MOST_GROUPS], s_b[MOST_GROUPS];
@@ -612,7 +655,8 @@ norm_grad_apply_kernel(NormArgs a, NormTile t, NormTile from, NormScratch w)
     float mean[P], scale[V], bias[V], m1[P], m2[P];
     if (p.in) load_channels<T, V, P>(a, p, mean, scale, bias);
     pdl_wait();
-    join_sums(a, from, p, w, j, s_a, s_b);
+    if (joined) load_joined(a, p, j, w.ga, w.gb, s_a, s_b);
+    else join_sums(a, from, p, w, j, s_a, s_b);
     if (!p.in) return;
     const int D = a.channels / a.groups;
     const float each_all = 1.0f / (static_cast<float>(a.pixels) * static_cast<float>(D));
@@ -1231,10 +1275,12 @@ template <typename T, int V>
 static bool norm_in_clusters(const NormArgs& a, void* ws, cudaStream_t st, bool grad)
 {
     const int e = sizeof(T), D = a.channels / a.groups, vecs = a.channels / V;
-    // Beyond these sizes streaming is faster (16 x 6400 x 256 bf16, 52 MB: 57 against 34 us forward, 89 against 65
-    // backward; 4 x 6400 x 256, 13 MB: 17 against 27 forward, 25 against 27 backward; 16 x 1600 x 256, 13 MB: 16
-    // against 19 forward, 38 against 26 backward).
-    if (static_cast<double>(a.batch) * a.pixels * a.channels * e > (grad ? 8e6 : 16e6)) return false;
+    // One launch and one reading where latency counts; beyond these sizes streaming is faster.  bf16, 256 channels in
+    // 32 groups, cluster and streaming: forward 1 x 400 pixels 6.7 and 6.9 us, 16 x 400 7.2 and 9.0, 4 x 1600 8.5 and
+    // 11.9, 1 x 6400 11.7 and 9.0, 16 x 1600 15.9 and 14.6; backward 1 x 400 5.9 and 8.6, 4 x 400 7.2 and 8.8,
+    // 16 x 400 13.6 and 10.7, 16 x 1600 38 and 23.
+    const double size = static_cast<double>(a.batch) * a.pixels * a.channels * e;
+    if (grad ? size > 1.5e6 : size > 4e6 || a.pixels > 4096) return false;
     int whole = 1;  // vectors that hold whole groups: lcm(D, V) / V
     while (whole * V % D != 0) ++whole;
     const int pass = NT * V * (grad ? e + 4 : e);  // bytes that a pass over the block's rows keeps
@@ -1300,19 +1346,32 @@ static void norm_streamed(const NormArgs& a, void* ws, cudaStream_t st, bool gra
     const NormScratch w = scratch(a, ws);
     const dim3 block(NT);
     auto grid = [&](const NormTile& t) { return dim3(static_cast<unsigned>(a.batch * t.pieces), t.tiles); };
+    // Whether the join takes a launch of its own.
+    auto own = [&](const NormTile& t) { return t.pieces * (a.channels / a.groups / t.values) > OWN_JOIN; };
     if (!grad) {
         static const int sums = resident_blocks(reinterpret_cast<const void*>(norm_partial_kernel<T, V, ONE>));
         static const int rows = resident_blocks(reinterpret_cast<const void*>(norm_apply_kernel<T, V, ONE, ACT>));
         const NormTile t = one_wave(a, most, sums), u = one_wave(a, most, rows);
+        NormArgs b = a;
         norm_partial_kernel<T, V, ONE><<<grid(t), block, 0, st>>>(a, t, w);
-        launch_pdl(norm_apply_kernel<T, V, ONE, ACT>, grid(u), block, 0, st, a, u, t, w);
+        const bool joined = own(t);
+        if (joined) {
+            if (!b.mean) b.mean = w.ga;
+            if (!b.rstd) b.rstd = w.gb;
+            launch_pdl(norm_join_kernel<false>, dim3(static_cast<unsigned>(a.batch * a.groups)), block, 0, st, b, t, w);
+        }
+        launch_pdl(norm_apply_kernel<T, V, ONE, ACT>, grid(u), block, 0, st, b, u, t, w, joined);
     } else {
         static const int sums = resident_blocks(reinterpret_cast<const void*>(norm_grad_partial_kernel<T, V, ONE, ACT>));
         static const int rows = resident_blocks(reinterpret_cast<const void*>(norm_grad_apply_kernel<T, V, ONE, ACT>));
         const NormTile t = one_wave(a, most, sums), u = one_wave(a, most, rows);
         norm_grad_partial_kernel<T, V, ONE, ACT><<<grid(t), block, 0, st>>>(a, t, w);
         const unsigned params = a.dweight || a.dbias ? (a.channels + PARAMS - 1) / PARAMS : 0;
-        launch_pdl(norm_grad_apply_kernel<T, V, ONE, ACT>, dim3(grid(u).x + params, u.tiles), block, 0, st, a, u, t, w);
+        const bool joined = own(t);
+        if (joined)
+            launch_pdl(norm_join_kernel<true>, dim3(static_cast<unsigned>(a.batch * a.groups)), block, 0, st, a, t, w);
+        launch_pdl(norm_grad_apply_kernel<T, V, ONE, ACT>, dim3(grid(u).x + params, u.tiles), block, 0, st, a, u, t, w,
+                   joined);
     }
 }
 
