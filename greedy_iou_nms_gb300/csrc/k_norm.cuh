@@ -1176,8 +1176,13 @@ norm_grad_cluster_kernel(NormArgs a, NormCluster t, NormScratch w)
                 va += s_image[r * 2 * CW + c];
                 vb += s_image[(r * 2 + 1) * CW + c];
             }
-            w.ca[p.image * a.channels + p.first_channel + c] = va;
-            w.cb[p.image * a.channels + p.first_channel + c] = vb;
+            if (a.batch == 1) {  // the image's sums are the gradients
+                if (a.dbias) a.dbias[p.first_channel + c] = va;
+                if (a.dweight) a.dweight[p.first_channel + c] = vb;
+            } else {
+                w.ca[p.image * a.channels + p.first_channel + c] = va;
+                w.cb[p.image * a.channels + p.first_channel + c] = vb;
+            }
         }
     if (p.in) {
         const float each_n = 1.0f / (static_cast<float>(a.pixels) * static_cast<float>(D));
@@ -1314,7 +1319,7 @@ static bool norm_in_clusters(const NormArgs& a, void* ws, cudaStream_t st, bool 
                 const NormScratch w = scratch(a, ws);
                 launch_clusters(one ? norm_grad_cluster_kernel<T, V, true> : norm_grad_cluster_kernel<T, V, false>, a, t,
                                 smem, st, w);
-                if (a.dweight || a.dbias)
+                if (a.batch > 1 && (a.dweight || a.dbias))
                     launch_pdl(norm_grad_param_kernel, dim3((a.channels + NT - 1) / NT), dim3(NT), 0, st, a, w);
             }
             return true;

@@ -265,3 +265,12 @@ def test_refusals():
         g.group_norm_act_grad(x[:1], x, stats, stats, 3)
     with pytest.raises(ValueError):
         g.group_norm_act_grad(x, x, stats[:1], stats, 3)
+
+
+@pytest.mark.parametrize("N,S,C,groups", [(1, 4000, 16, 2), (3, 2047, 24, 3), (1, 4096, 64, 1), (2, 700, 30, 2),
+                                          (1, 9000, 256, 32), (1, 30000, 36, 9), (40, 1, 64, 8)])
+@pytest.mark.parametrize("t", [torch.float32, torch.float16])
+def test_slabs_over_blocks_and_pieces(t, N, S, C, groups):
+    """Slabs over two to eight blocks of a cluster with a short last one, and
+    images of few and of many pieces."""
+    _check(*_inputs(S, N, S, C, t), groups, "gelu", p=0.1)
