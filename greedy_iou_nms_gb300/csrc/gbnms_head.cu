@@ -42,7 +42,7 @@ int64_t product(int64_t a, int64_t b, int64_t most)
     return a > most / b ? -1 : a * b;
 }
 
-constexpr int64_t kMostElements = int64_t(1) << 47;
+constexpr int64_t kMostElements = int64_t(1) << 40;
 constexpr int64_t kMostRows = INT32_MAX;
 
 // Shape of a feature map: 0, or the status to return.

@@ -29,19 +29,23 @@ constexpr int NT = 256;  // threads of a block
 //
 // Large maps in two launches: sums by rows' pieces; then their join (every
 // block for its own groups: some kilobytes from L2 and a launch less; images
-// of many pieces in a launch of its own) and the results.  The second reading comes from L2 as far as that holds the map:
-// the last launch goes through the pieces backwards and its stores are marked
-// as streaming.
+// of many pieces in a launch of its own) and the results.  The second reading
+// comes from L2 as far as that holds the map: the last launch goes through the
+// pieces backwards.
+
+// Rows of a piece, at most: a thread's sums are chains of some hundred
+// additions.
+constexpr int MOST_ROWS = 1024;
 
 // Row pieces of an image, at most: 32 rows each at least, and one wave of
-// four blocks on every SM (a function of the shape alone: the workspace's
-// size depends on it).
+// four blocks on every SM, more where MOST_ROWS asks for it (a function of
+// the shape alone: the workspace's size depends on it).
 inline int64_t norm_pieces(int64_t batch, int64_t pixels, int channels)
 {
     const int64_t tiles = channels > 256 ? channels / 256 : 1, ctas = SMS * 4;
     const int64_t by_rows = (pixels + 31) / 32, by_ctas = ctas / (batch * tiles);
-    const int64_t p = by_rows < by_ctas ? by_rows : by_ctas;
-    return p < 1 ? 1 : p;
+    const int64_t p = by_rows < by_ctas ? by_rows : by_ctas, least = (pixels + MOST_ROWS - 1) / MOST_ROWS;
+    return p < least ? least : p;
 }
 
 // Scratch: four partial planes [batch][pieces][channels] (forward: mean high,
@@ -90,24 +94,9 @@ __device__ __forceinline__ void widen(float (&v)[V], const Pack<T, V>& q)
 }
 
 template <typename T, int V>
-__device__ __forceinline__ void load_row(const T* p, float (&v)[V])
-{
-    widen(v, *reinterpret_cast<const Pack<T, V>*>(p));
-}
-
-template <typename T, int V>
 __device__ __forceinline__ void store_row(T* p, const float (&v)[V])
 {
     *reinterpret_cast<Pack<T, V>*>(p) = pack_results<T, V>(v);
-}
-
-// store_row for results that nothing here reads again: kept out of L2's way.
-template <typename T, int V>
-__device__ __forceinline__ void stream_row(T* p, const float (&v)[V])
-{
-    const Pack<T, V> q = pack_results<T, V>(v);
-    if constexpr (sizeof(q) == 16) __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&q));
-    else *reinterpret_cast<Pack<T, V>*>(p) = q;
 }
 
 // Where a thread stands: image, row range of the piece, first channel.
@@ -430,7 +419,7 @@ norm_apply_kernel(NormArgs a, NormTile t, NormTile from, NormScratch w, bool joi
         for (int i = 0; i < V; ++i) v[i] = fmaf(v[i] - mean[ONE ? 0 : i], scale[i], shift[i]);
         act_values<V>(v, ACT);
         if (dropping) drop<V>(v, static_cast<uint64_t>(at), a.drop);
-        stream_row<T, V>(y + at, v);
+        store_row<T, V>(y + at, v);
     });
 }
 
@@ -677,7 +666,7 @@ norm_grad_apply_kernel(NormArgs a, NormTile t, NormTile from, NormScratch w, boo
 #pragma unroll
         for (int i = 0; i < V; ++i)
             dz[i] = fmaf(dz[i], scale[i], fmaf(d[i], m2[ONE ? 0 : i], m1[ONE ? 0 : i]));
-        stream_row<T, V>(static_cast<T*>(a.out) + at, dz);
+        store_row<T, V>(static_cast<T*>(a.out) + at, dz);
     });
 }
 
@@ -1339,7 +1328,8 @@ inline int resident_blocks(const void* kernel)
 inline NormTile one_wave(const NormArgs& a, NormTile t, int resident)
 {
     const int64_t wave = static_cast<int64_t>(SMS) * resident / (a.batch * t.tiles);
-    if (wave < t.pieces) t.pieces = wave < 1 ? 1 : static_cast<int>(wave);
+    const int64_t least = (a.pixels + MOST_ROWS - 1) / MOST_ROWS;
+    if (wave < t.pieces) t.pieces = static_cast<int>(wave < least ? least : wave);
     t.per = static_cast<int>((a.pixels + t.pieces - 1) / t.pieces);
     return t;
 }

@@ -119,7 +119,8 @@ RelationGradPlan relation_grad_plan(int64_t batch, int heads, int64_t queries, i
         const int64_t held = (keys + lanes - 1) / lanes;  // elements a lane
         const int resident = held <= 8 ? 3 : held <= 16 ? 2 : 1;
         const int64_t want = SMS * resident / (p.blocks * heads);  // one wave
-        p.chunks = want < 1 ? 1 : want > batch ? batch : want;
+        const int64_t least = (batch + 1023) / 1024;  // chains of at most 1024 additions
+        p.chunks = want < least ? least : want > batch ? batch : want;
         p.per = (batch + p.chunks - 1) / p.chunks;
         p.chunks = (batch + p.per - 1) / p.per;
         return p;

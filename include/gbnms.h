@@ -458,7 +458,7 @@ nms_status nms_resolve_mask_noalloc(const uint64_t* mask, int64_t n, const int32
  *   n        elements, contiguous; y may be x or residual itself.
  *   drop_p   in [0, 1].
  * Errors: NMS_ERR_INVALID_ARG (type, drop_p, NULL or misaligned pointers),
- *         NMS_ERR_CAPACITY (n > 2^47), NMS_ERR_CUDA.
+ *         NMS_ERR_CAPACITY (n > 2^40), NMS_ERR_CUDA.
  */
 nms_status nms_dropout_run(const void* x, const void* residual, int32_t type, int64_t n, double drop_p,
                            uint64_t seed, uint64_t offset, void* y, void* stream);
@@ -489,7 +489,7 @@ nms_status nms_dropout_run(const void* x, const void* residual, int32_t type, in
  * Errors: NMS_ERR_INVALID_ARG (types, act, eps < 0 or not finite, drop_p,
  *         shapes, channels not a multiple of groups, strides that overlap,
  *         NULL or misaligned pointers), NMS_ERR_CAPACITY (limits above, batch *
- *         groups above 2^31 - 1 or more than 2^47 elements), NMS_ERR_WORKSPACE, NMS_ERR_CUDA.
+ *         groups above 2^31 - 1 or more than 2^40 elements), NMS_ERR_WORKSPACE, NMS_ERR_CUDA.
  */
 nms_status nms_group_norm_workspace_size(int64_t batch, int64_t pixels, int32_t channels, int32_t groups,
                                          size_t* bytes);
@@ -523,7 +523,7 @@ nms_status nms_group_norm_grad_run(const void* dy, int64_t dy_image, int64_t dy_
  *   lut           device int32 [axes][2 * reach + 1].
  *   buckets       device int16 [max sets][queries][keys].
  * Errors: NMS_ERR_INVALID_ARG, NMS_ERR_CAPACITY (limits above, or more than
- *         2^31 - 1 rows of queries or 2^47 pairs), NMS_ERR_CUDA.
+ *         2^31 - 1 rows of queries or 2^40 pairs), NMS_ERR_CUDA.
  */
 nms_status nms_relation_buckets_run(const int32_t* q_pos, int64_t q_sets, const int32_t* k_pos, int64_t k_sets,
                                     int64_t queries, int64_t keys, int32_t axes, const int32_t* lut,
@@ -535,16 +535,17 @@ nms_status nms_relation_buckets_run(const int32_t* q_pos, int64_t q_sets, const 
  *       scale * scores[b][h][i][j] + table[bucket][h].
  * A pair is masked when its bucket is outside [0, num_buckets) or its key's
  * mask is 0; a masked pair has weight 0 and its score (NaN and infinities
- * too) is never looked at; a row whose pairs are all masked, or all -inf, is
- * all 0.
+ * too) changes nothing; a row whose pairs are all masked, or all -inf, is all
+ * 0.  A weight below 2^-126 may be 0.
  *   scores, probs device [batch][heads][queries][keys] of `type`.
  *   buckets       device int16 [sets][queries][keys], sets = 1 (one map for
  *                 all images) or batch.
- *   table         device float [num_buckets][heads].
+ *   table         device float [num_buckets][heads]; an entry of -inf masks its
+ *                 pairs too.
  *   key_mask      device uint8 [batch][keys], non-zero where the key takes
  *                 part, or NULL (all do).
  * The gradient, from the incoming gradient dprobs and the forward's probs
- * (masked places are again not looked at):
+ * (what stands in masked places changes nothing again):
  *   da = probs * (dprobs - sum_j probs * dprobs), dscores = scale * da (0 for
  *   a masked pair), dtable[u][h] = sum of da over the pairs of bucket u
  *   (float [num_buckets][heads], every entry written), summed in a fixed
@@ -552,7 +553,7 @@ nms_status nms_relation_buckets_run(const int32_t* q_pos, int64_t q_sets, const 
  *   workspace     >= nms_relation_grad_workspace_size() bytes, 256-byte
  *                 aligned.
  * Errors: NMS_ERR_INVALID_ARG, NMS_ERR_CAPACITY (limits above, or more than
- *         2^31 - 1 rows or 2^47 elements), NMS_ERR_WORKSPACE, NMS_ERR_CUDA.
+ *         2^31 - 1 rows or 2^40 elements), NMS_ERR_WORKSPACE, NMS_ERR_CUDA.
  */
 nms_status nms_relation_softmax_run(const void* scores, int32_t type, int64_t batch, int32_t heads,
                                     int64_t queries, int64_t keys, const int16_t* buckets, int64_t sets,
