@@ -178,11 +178,13 @@ def _stream(x) -> int:
 
 def _like(x):
     """An uninitialised contiguous tensor of x's shape and type."""
+    if x.is_contiguous():
+        return _torch_module.empty_like(x)
     return _torch_module.empty_like(x, memory_format=_torch_module.contiguous_format)
 
 
 def _same(x, like, where: str, name: str) -> None:
-    if x.shape != like.shape or x.dtype != like.dtype or x.device != like.device:
+    if x.shape != like.shape or x.dtype is not like.dtype or x.get_device() != like.get_device():
         raise ValueError(f"{where}: {name} must have the shape, type and device of the other operand")
 
 
@@ -225,17 +227,17 @@ def _map(x, where: str):
 
 def _params(x, channels: int, weight, bias, where: str):
     """Addresses of weight and bias and their type."""
-    f32 = _torch().float32
     kind = None
     for name, p in (("weight", weight), ("bias", bias)):
         if p is None:
             continue
-        if p.shape != (channels,) or p.device != x.device or not p.is_contiguous() or \
-                p.dtype not in (f32, x.dtype) or kind not in (None, p.dtype):
+        t = p.dtype
+        if p.dim() != 1 or p.shape[0] != channels or p.get_device() != x.get_device() or not p.is_contiguous() or \
+                (t is not _torch_module.float32 and t is not x.dtype) or (kind is not None and t is not kind):
             raise ValueError(f"{where}: {name} must be a contiguous [channels] tensor beside x, float32 or of x's "
                              "type, weight and bias alike")
-        kind = p.dtype
-    return (weight.data_ptr() if weight is not None else 0, bias.data_ptr() if bias is not None else 0,
+        kind = t
+    return (0 if weight is None else weight.data_ptr(), 0 if bias is None else bias.data_ptr(),
             NMS_TYPE_F32 if kind is None else _types[kind])
 
 
@@ -290,7 +292,8 @@ def group_norm_act_grad(dy, x, mean, rstd, groups: int, weight=None, bias=None, 
     dys, dimage, dpixel = _map(dy, where)[:3]
     wp, bp, ptype = _params(x, channels, weight, bias, where)
     for s in (mean, rstd):
-        if s.shape != (batch, groups) or s.dtype != torch.float32 or s.device != x.device or not s.is_contiguous():
+        if s.shape != (batch, groups) or s.dtype is not torch.float32 or s.get_device() != x.get_device() or \
+                not s.is_contiguous():
             raise ValueError("group_norm_act_grad: mean and rstd must be contiguous float32 [batch, groups] tensors "
                              "beside x")
     wsb = nms_group_norm_workspace_size(batch, pixels, channels, groups)
@@ -317,7 +320,7 @@ def dropout(x, p: float, seed: int, offset: int = 0, *, residual=None):
         _same(residual, x, "dropout", "residual")
         residual = residual.contiguous()
     x = x.contiguous()
-    y = _like(x)
+    y = _torch_module.empty_like(x)
     st = _lib().nms_dropout_run(x.data_ptr(), None if residual is None else residual.data_ptr(), kind, x.numel(), p,
                                 seed, offset, y.data_ptr(), _stream(x))
     if st:
@@ -369,8 +372,8 @@ def relation_buckets(q_pos, k_pos, lut):
     k_pos [sets or 1, keys, axes] and lut [axes, 2 * reach + 1] (see
     `relation_lut_log`, `relation_lut_cells`); -1 masks the pair."""
     torch = _torch()
-    if not (q_pos.dtype == k_pos.dtype == lut.dtype == torch.int32 and q_pos.is_cuda and
-            q_pos.device == k_pos.device == lut.device):
+    if not (q_pos.dtype is k_pos.dtype is lut.dtype is torch.int32 and q_pos.is_cuda and
+            q_pos.get_device() == k_pos.get_device() == lut.get_device()):
         raise ValueError("relation_buckets: q_pos, k_pos and lut must be int32 tensors on one CUDA device")
     if q_pos.dim() != 3 or k_pos.dim() != 3 or lut.dim() != 2:
         raise ValueError("relation_buckets: positions must be [sets, length, axes] and lut [axes, 2 * reach + 1]")
@@ -393,15 +396,20 @@ def _relation(scores, buckets, key_mask, where: str):
     if scores.dim() != 4:
         raise ValueError(f"{where}: scores must be [batch, heads, queries, keys]")
     B, H, Q, K = scores.shape
-    if buckets.dtype != torch.int16 or buckets.device != scores.device or buckets.dim() != 3 or \
-            buckets.shape[0] not in (1, B) or buckets.shape[1] != Q or buckets.shape[2] != K:
+    place = scores.get_device()
+    if buckets.dtype is not torch.int16 or buckets.get_device() != place or buckets.dim() != 3:
         raise ValueError(f"{where}: buckets must be int16 [1 or batch, queries, keys] beside the scores")
+    sets, queries, keys = buckets.shape
+    if sets not in (1, B) or queries != Q or keys != K:
+        raise ValueError(f"{where}: buckets must be int16 [1 or batch, queries, keys] beside the scores")
+    mask = None
     if key_mask is not None:
         if key_mask.shape != (B, K) or key_mask.dtype not in (torch.bool, torch.uint8) or \
-                key_mask.device != scores.device:
+                key_mask.get_device() != place:
             raise ValueError(f"{where}: key_mask must be bool or uint8 [batch, keys] beside the scores")
         key_mask = key_mask.contiguous()
-    return B, H, Q, K, buckets.contiguous(), key_mask
+        mask = key_mask.data_ptr()
+    return B, H, Q, K, buckets.contiguous(), sets, key_mask, mask
 
 
 def relation_softmax(scores, table, buckets, *, scale: float = 1.0, key_mask=None):
@@ -416,15 +424,15 @@ def relation_softmax(scores, table, buckets, *, scale: float = 1.0, key_mask=Non
     where = "relation_softmax"
     kind = _type(scores, where, "scores")
     torch = _torch_module
-    B, H, Q, K, buckets, key_mask = _relation(scores, buckets, key_mask, where)
-    if table.dim() != 2 or table.shape[1] != H or table.device != scores.device:
+    B, H, Q, K, buckets, sets, key_mask, mask = _relation(scores, buckets, key_mask, where)
+    if table.dim() != 2 or table.shape[1] != H or table.get_device() != scores.get_device():
         raise ValueError("relation_softmax: table must be [num_buckets, heads] beside the scores")
-    table = table.to(torch.float32).contiguous()
-    scores = scores.contiguous()
-    out = _like(scores)
-    st = _lib().nms_relation_softmax_run(scores.data_ptr(), kind, B, H, Q, K, buckets.data_ptr(), buckets.shape[0],
-                                         table.data_ptr(), table.shape[0],
-                                         None if key_mask is None else key_mask.data_ptr(), scale, out.data_ptr(),
+    if table.dtype is not torch.float32:
+        table = table.to(torch.float32)
+    table, scores = table.contiguous(), scores.contiguous()
+    out = torch.empty_like(scores)
+    st = _lib().nms_relation_softmax_run(scores.data_ptr(), kind, B, H, Q, K, buckets.data_ptr(), sets,
+                                         table.data_ptr(), table.shape[0], mask, scale, out.data_ptr(),
                                          _stream(scores))
     if st:
         _raise(st, "nms_relation_softmax_run")
@@ -439,17 +447,15 @@ def relation_softmax_grad(dprobs, probs, buckets, num_buckets: int, *, scale: fl
     kind = _type(probs, where, "probs")
     torch = _torch_module
     _same(dprobs, probs, where, "dprobs")
-    B, H, Q, K, buckets, key_mask = _relation(probs, buckets, key_mask, where)
+    B, H, Q, K, buckets, sets, key_mask, mask = _relation(probs, buckets, key_mask, where)
     dprobs, probs = dprobs.contiguous(), probs.contiguous()
-    dev = probs.device
     wsb = nms_relation_grad_workspace_size(B, H, Q, K, num_buckets)
-    ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
-    ds = _like(probs)
-    dtable = torch.empty((num_buckets, H), dtype=torch.float32, device=dev)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=probs.device)
+    ds = torch.empty_like(probs)
+    dtable = torch.empty((num_buckets, H), dtype=torch.float32, device=probs.device)
     st = _lib().nms_relation_softmax_grad_run(dprobs.data_ptr(), probs.data_ptr(), kind, B, H, Q, K,
-                                              buckets.data_ptr(), buckets.shape[0], num_buckets,
-                                              None if key_mask is None else key_mask.data_ptr(), scale,
-                                              ds.data_ptr(), dtable.data_ptr(), ws.data_ptr(), wsb, _stream(probs))
+                                              buckets.data_ptr(), sets, num_buckets, mask, scale, ds.data_ptr(),
+                                              dtable.data_ptr(), ws.data_ptr(), wsb, _stream(probs))
     if st:
         _raise(st, "nms_relation_softmax_grad_run")
     return ds, dtable
