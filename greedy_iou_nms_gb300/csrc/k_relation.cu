@@ -125,16 +125,22 @@ RelationGradPlan relation_grad_plan(int64_t batch, int heads, int64_t queries, i
         p.chunks = (batch + p.per - 1) / p.per;
         return p;
     }
-    // A table a warp: 32 columns if six warps' fit, else fewer (16 columns and
-    // two turns, to have 14 warps on an SM and not 7, took 436 us for 264 on
-    // 16 x 8 x 1000 x 1000 bf16 with 225 buckets).
+    // A table a warp, in all of an SM's shared memory: 32 columns if twelve
+    // warps' fit, else 16 and two blocks of up to six warps if four each fit,
+    // else 32 or fewer for one block of six warps.
     constexpr int ROOM = 208 * 1024;
-    const int need = lanes == 256 ? 8 : 6;
-    for (p.columns = 32; p.columns > 4 && need * (num_buckets + 1) * 4 * p.columns > ROOM; p.columns /= 2) {}
-    const int fit = ROOM / ((num_buckets + 1) * 4 * p.columns);
-    p.warps = fit > 8 ? 8 : fit;
+    const int row = 4 * (num_buckets + 1), need = lanes == 256 ? 8 : 6;
+    if (lanes <= 32 && keys <= RELATION_MOST && 12 * 32 * row > ROOM && 4 * 16 * row <= ROOM / 2) {
+        p.columns = 16;
+        const int fit = ROOM / 2 / (16 * row);
+        p.warps = fit > 6 ? 6 : fit;
+    } else {
+        for (p.columns = 32; p.columns > 4 && need * p.columns * row > ROOM; p.columns /= 2) {}
+        const int fit = ROOM / (p.columns * row);
+        p.warps = fit > 8 ? 8 : fit;
+    }
     const int64_t teams = p.warps * 32 / lanes, rows = batch * queries, want = (rows + teams - 1) / teams;
-    const int resident = ROOM / (p.warps * (num_buckets + 1) * 4 * p.columns);
+    const int resident = ROOM / (p.warps * p.columns * row);
     const int64_t most = (SMS * static_cast<int64_t>(resident < 4 ? resident : 4) + heads - 1) / heads;
     p.blocks = want < most ? want : most;
     p.chunks = 1;

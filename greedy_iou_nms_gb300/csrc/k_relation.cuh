@@ -714,9 +714,10 @@ relation_grad_image_kernel(RelationArgs a, int per, int columns, float* part)
 }
 
 // By head: block (x, y) = (share of the rows, head); each warp has a table of
-// its own, of 32 columns (WIDE) or fewer.
-template <typename S, bool WIDE>
-__global__ void __launch_bounds__(256)
+// its own, of COLUMNS columns: 32 (one a lane), 16 (lanes l and l + 16 share
+// one), or fewer, taken in turns (0: `columns` says how many).
+template <typename S, int COLUMNS>
+__global__ void __launch_bounds__(COLUMNS == 16 ? 192 : 256, COLUMNS == 16 ? 2 : 1)
 relation_grad_head_kernel(RelationArgs a, int columns, float* part)
 {
     using T = typename S::T;
@@ -773,13 +774,27 @@ relation_grad_head_kernel(RelationArgs a, int columns, float* part)
         }
         if (bi < rows) fetch(bi + team < rows);
         grad_rows<S, 1>(x, d, bucket, a, ds, 0, lane, real ? 1 : 0, red[turn]);
-        if (WIDE) {
+        if (COLUMNS == 32) {
             float* column = mine + lane_id();
 #pragma unroll
             for (int k = 0; k + 1 < S::E; k += 2)
                 add_two(column, bucket(k / EV, k % EV), x[0][k / EV][k % EV], bucket((k + 1) / EV, (k + 1) % EV),
                         x[0][(k + 1) / EV][(k + 1) % EV]);
             if (S::E % 2) column[bucket(NV - 1, EV - 1) * 32] += x[0][NV - 1][EV - 1];
+        } else if (COLUMNS == 16) {
+            // Where both lanes of a column hold pairs of one bucket the lower adds for the other, which adds to the last
+            // row; else their rows differ.
+            float* column = mine + lane_id() % 16;
+            const bool lower = lane_id() < 16;
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int e = 0; e < EV; ++e) {
+                    const int u = bucket(v, e), other = __shfl_xor_sync(FULL, u, 16);
+                    const float d = x[0][v][e], more = __shfl_xor_sync(FULL, d, 16);
+                    const bool same = u == other;
+                    column[(same && !lower ? nb : u) * 16] += same ? d + more : d;
+                }
         } else {
 #pragma unroll
             for (int v = 0; v < NV; ++v)
@@ -856,7 +871,7 @@ inline void pick_count(const RelationArgs& a, F f)
 
 // f(Shape) for the row's length and vector width.  Eight lanes a row up to 64
 // keys, 16 up to 128, a warp up to 1024, a block up to 8192.
-template <typename T, typename F>
+template <typename T, bool GRAD, typename F>
 inline void relation_shape(const RelationArgs& a, F f)
 {
     constexpr int MOST = sizeof(T) == 2 ? 8 : 4;
@@ -882,7 +897,9 @@ inline void relation_shape(const RelationArgs& a, F f)
     } else {
         if (K <= 64) pick_count<T, 1, 8, 0, 1, 2, 4, 6, 7, 8>(a, f);
         else if (K <= 128) pick_count<T, 1, 16, 4, 6, 8>(a, f);
-        else if (K <= 1024) pick_count<T, 1, 32, 4, 6, 8, 12, 16, 24, 32>(a, f);
+        else if (GRAD && K <= 1024) pick_count<T, 1, 32, 4, 6, 8, 12, 16, 24, 32>(a, f);
+        else if (!GRAD && K <= 512) pick_count<T, 1, 32, 4, 6, 8, 12, 16>(a, f);
+        else if (!GRAD) pick_count<T, 1, 256, 2, 3, 4, 8, 16, 32>(a, f);
         else pick_count<T, 1, 256, 4, 8, 16, 32>(a, f);
     }
 }
@@ -904,7 +921,7 @@ inline void softmax_type(const RelationArgs& a, cudaStream_t st)
         relation_softmax_long_kernel<T><<<static_cast<unsigned>(rows < SMS * 8 ? rows : SMS * 8), 256, 0, st>>>(a, rows);
         return;
     }
-    relation_shape<T>(a, [&](auto shape) {
+    relation_shape<T, false>(a, [&](auto shape) {
         using S = decltype(shape);
         const bool image = relation_by_image(a);
         const int64_t anchors = (image ? a.heads : a.batch) * a.queries, inner = image ? a.batch : a.heads;
@@ -951,14 +968,16 @@ inline void grad_type(const RelationArgs& a, float* part, cudaStream_t st)
                                        st>>>(a, p.columns, part);
         return;
     }
-    relation_shape<T>(a, [&](auto shape) {
+    relation_shape<T, true>(a, [&](auto shape) {
         using S = decltype(shape);
         if (image) {
             relation_grad_image_kernel<S><<<dim3(static_cast<unsigned>(p.blocks), static_cast<unsigned>(p.chunks),
                                                  a.heads), 256, table, st>>>(a, static_cast<int>(p.per), p.columns,
                                                                              part);
         } else {
-            auto* k = p.columns == 32 ? relation_grad_head_kernel<S, true> : relation_grad_head_kernel<S, false>;
+            auto* k = p.columns == 32 ? relation_grad_head_kernel<S, 32> : relation_grad_head_kernel<S, 0>;
+            if constexpr (S::L <= 32)
+                if (p.columns == 16) k = relation_grad_head_kernel<S, 16>;
             ensure_dynamic_smem(reinterpret_cast<const void*>(k), table * p.warps);
             k<<<dim3(static_cast<unsigned>(p.blocks), a.heads), p.warps * 32, table * p.warps, st>>>(a, p.columns,
                                                                                                     part);
