@@ -4,7 +4,8 @@
 //
 // HBM bounds it where the generator's some fifty integer instructions for
 // eight elements hide behind the loads; so a thread loads several blocks of
-// eight before it draws for the first.
+// eight before it draws for the first, and three blocks share an SM (24 warps;
+// two took 110 us).  128 M bf16: 94 us, 5.4 TB/s of the 6.8 that a copy reaches.
 #include "head.cuh"
 #include "internal.h"
 

@@ -188,7 +188,9 @@ __device__ __forceinline__ void each_row_pair(const NormArgs& a, const Spot& p, 
 }
 
 // (mean, squared deviations) of each row piece by column: a vector (ONE: its
-// channels are of one group) or a channel.
+// channels are of one group) or a channel.  Three operations a value; four
+// rows' loads in flight a thread, 32 warps an SM.  16 x 6400 x 256 bf16: 10 us,
+// 5.0 TB/s; the block's ramps (a first load, the join) are a third of it.
 template <typename T, int V, bool ONE>
 __global__ void __launch_bounds__(NT, 4)
 norm_partial_kernel(NormArgs a, NormTile t, NormScratch w)
@@ -385,6 +387,9 @@ __device__ __forceinline__ void load_joined(const NormArgs& a, const Spot& p, co
     __syncthreads();
 }
 
+// The results.  16 x 6400 x 256 bf16, silu: 19 us for 52 MB from L2 and as much
+// written; the sigmoid's two hardware functions a value take 11 us of their
+// pipe, and three blocks an SM (80 registers) hide what latency they can.
 template <typename T, int V, bool ONE, int ACT>
 __global__ void __launch_bounds__(NT, 3)
 norm_apply_kernel(NormArgs a, NormTile t, NormTile from, NormScratch w, bool joined)
@@ -456,7 +461,9 @@ __device__ __forceinline__ void slope_row(const NormArgs& a, const float (&mean)
     act_slopes<V>(dz, z, ACT);
 }
 
-// Sums by channel of dz and dz * (x - mean) of each row piece.
+// Sums by channel of dz and dz * (x - mean) of each row piece.  16 x 1600 x 256
+// bf16, silu: 11 us, latency (seven rows a thread).  8 x 25600 x 128 fp16,
+// gelu and dropout: 40 us, issue: 36 instructions a value.
 template <typename T, int V, bool ONE, int ACT>
 __global__ void __launch_bounds__(NT, ONE ? 3 : 2)
 norm_grad_partial_kernel(NormArgs a, NormTile t, NormScratch w)
@@ -627,6 +634,8 @@ norm_grad_param_kernel(NormArgs a, NormScratch w)
 }
 
 // dx; the blocks past the pieces' (the first to run) write dweight and dbias.
+// dz is worked out again: keeping it would move 8 bytes a value more.  13 us
+// and 44 us at the sizes above.
 template <typename T, int V, bool ONE, int ACT>
 __global__ void __launch_bounds__(NT, ONE ? 3 : 2)
 norm_grad_apply_kernel(NormArgs a, NormTile t, NormTile from, NormScratch w, bool joined)
@@ -810,7 +819,10 @@ struct GroupSums {
     }
 };
 
-// ONE: a vector lies in one group (its channels' sums are one).
+// ONE: a vector lies in one group (its channels' sums are one).  Two readings
+// from shared memory for the moments (the second about the block's mean), one
+// for the results; one exchange.  1 x 400 x 256 bf16: 6.7 us with its launch,
+// latency.
 template <typename T, int V, bool ONE>
 __global__ void __launch_bounds__(NT, 4)
 norm_cluster_kernel(NormArgs a, NormCluster t)

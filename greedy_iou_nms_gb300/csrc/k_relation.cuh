@@ -21,6 +21,13 @@
 //             memory.
 // The gradient by head keeps one head instead and goes through images and
 // queries, since its sums by bucket are per head.
+//
+// Measured (us; TB/s of what has to move): weights 2304 x 8 x 49 x 49 fp16, one
+// map, 49 (3.6), issue: 27 instructions a pair; 16 x 8 x 1000 x 1000 bf16, a map
+// by image, 103 (5.3); 4 x 8 x 2000 x 2000 fp32 172 (6.2).  Gradient 1600 x 8 x
+// 64 x 64 fp16, one map, 72 (4.4); 16 x 8 x 1000 x 1000 bf16, 225 buckets, a map
+// by image, 215 (3.7), latency: 12 warps an SM beside their tables of sums.
+// Odd lengths above 128 keys go element by element and take twice as long.
 #pragma once
 
 #include <type_traits>
@@ -750,9 +757,12 @@ relation_grad_head_kernel(RelationArgs a, int columns, float* part)
         S::load(un, a.buckets + ((a.sets == 1 ? 0 : fb * Q) + fi) * K, K, lane);
         if (keyed) S::load(kn, a.key_mask + fb * K, K, lane);
     };
-    if (bi < rows) fetch(bi + team < rows);
+    // The next row is loaded ahead, but for long rows element by element, whose loads would not fit the registers.
+    constexpr bool AHEAD = EV > 1 || NV <= 16;
+    if (AHEAD && bi < rows) fetch(bi + team < rows);
     for (int turn = 0; bi < rows; turn ^= 1) {
         const bool real = bi + team < rows;
+        if (!AHEAD) fetch(real);
         T* ds = static_cast<T*>(a.out) + off_next;
         Buckets<S> bucket;
         Valid<S> valid;
@@ -772,7 +782,7 @@ relation_grad_head_kernel(RelationArgs a, int columns, float* part)
             i -= Q;
             ++b;
         }
-        if (bi < rows) fetch(bi + team < rows);
+        if (AHEAD && bi < rows) fetch(bi + team < rows);
         grad_rows<S, 1>(x, d, bucket, a, ds, 0, lane, real ? 1 : 0, red[turn]);
         if (COLUMNS == 32) {
             float* column = mine + lane_id();
