@@ -86,6 +86,10 @@ struct NormTile {
     int values;  // channels of a column of the partial planes: a vector's (of one group), one, or a group's
 };
 
+// A sum of squares that rounding took below 0 is 0; a NaN (an infinity in the
+// group) stays one.
+__device__ __forceinline__ float not_below_0(float x) { return x < 0.0f ? 0.0f : x; }
+
 template <typename T, int V>
 __device__ __forceinline__ void widen(float (&v)[V], const Pack<T, V>& q)
 {
@@ -231,7 +235,7 @@ norm_partial_kernel(NormArgs a, NormTile t, NormScratch w)
             const float m = count ? s[i] / count : 0.0f;
             s_high[threadIdx.x * P + i] = first[i];
             s_low[threadIdx.x * P + i] = m;
-            s_m2[threadIdx.x * P + i] = fmaxf(q[i] - s[i] * m, 0.0f);
+            s_m2[threadIdx.x * P + i] = not_below_0(q[i] - s[i] * m);
         }
     }
     __syncthreads();
@@ -256,7 +260,7 @@ norm_partial_kernel(NormArgs a, NormTile t, NormScratch w)
             m2 += fmaf(k * d, d, s_m2[at]);
         }
         low *= each;
-        m2 = fmaxf(m2 - n * low * low, 0.0f);
+        m2 = not_below_0(m2 - n * low * low);
         if (by_group) {  // entry c has been read by this thread alone
             s_high[c] = mean;
             s_low[c] = low;
@@ -286,7 +290,7 @@ norm_partial_kernel(NormArgs a, NormTile t, NormScratch w)
         low *= share;
         const int64_t at = (p.image * t.pieces + p.piece) * a.groups + g;
         w.pa[at] = mean;
-        w.pb[at] = fmaxf(m2 - n * each * low * low, 0.0f);
+        w.pb[at] = not_below_0(m2 - n * each * low * low);
         w.pc[at] = low;
     }
 }
@@ -364,7 +368,7 @@ __device__ __forceinline__ void join_moments(const NormArgs& a, const NormTile& 
         low = team_sum(low, j.team, red);
         m2 = team_sum(m2, j.team, red);
         if (lane == 0 && k < j.groups) {
-            const float m = mean + low, r = 1.0f / sqrtf(fmaxf(m2 / all - low * low, 0.0f) + a.eps);
+            const float m = mean + low, r = 1.0f / sqrtf(not_below_0(m2 / all - low * low) + a.eps);
             s_mean[k] = m;
             s_rstd[k] = r;
             if (p.piece == 0 && g * D >= first_channel) {
@@ -897,7 +901,7 @@ norm_cluster_kernel(NormArgs a, NormCluster t)
     if (t.ctas > 1) cluster_wait();
     if (threadIdx.x < p.groups) {  // groups <= NT
         const int g = threadIdx.x;
-        const float low = s_sum[g] * each_n, m2 = fmaxf(s_sum[G + g] - s_sum[g] * low, 0.0f);
+        const float low = s_sum[g] * each_n, m2 = not_below_0(s_sum[G + g] - s_sum[g] * low);
         float* at = s_piece + p.rank * 3 * G + g;
         for (int k = 0; k < t.ctas; ++k) {
             if (t.ctas > 1) {
@@ -940,7 +944,7 @@ norm_cluster_kernel(NormArgs a, NormCluster t)
             m = mean;
         }
         m += low;
-        const float r = 1.0f / sqrtf(fmaxf(m2 / all, 0.0f) + a.eps);
+        const float r = 1.0f / sqrtf(not_below_0(m2 / all) + a.eps);
         s_mean[g] = m;
         s_rstd[g] = r;
         if (p.rank == 0) {

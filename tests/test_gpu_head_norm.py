@@ -7,6 +7,8 @@ by a few units of 2^-24 of (|u| + |mean| / spread), so 64 * 2^-24 * (1 + the
 largest magnitude of z) covers u, the affine map and the activation.  Sums of
 the gradient are chains of at most some hundred additions: 256 * 2^-24 of the
 sum of their terms' sizes."""
+import math
+
 import numpy as np
 import pytest
 
@@ -274,3 +276,24 @@ def test_slabs_over_blocks_and_pieces(t, N, S, C, groups):
     """Slabs over two to eight blocks of a cluster with a short last one, and
     images of few and of many pieces."""
     _check(*_inputs(S, N, S, C, t), groups, "gelu", p=0.1)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
+@pytest.mark.parametrize("S,C,groups", [(40, 16, 4), (300, 90, 6), (9000, 32, 8), (700, 48, 3)])
+@pytest.mark.parametrize("where", [0.0, 0.5, 1.0])
+def test_infinity_leaves_no_number_in_its_group(act, S, C, groups, where):
+    """inf - inf: mean and variance of such a group are no numbers, nor are
+    its results and its input's gradient; other groups keep their bits."""
+    x, dy, w, b = (v.cuda() for v in _inputs(1, 2, S, C, torch.bfloat16))
+    clean = g.group_norm_act(x, groups, w, b, act=act, return_stats=True)
+    dclean = g.group_norm_act_grad(dy, x, *clean[1:], groups, w, b, act=act)[0]
+    D = C // groups
+    bad = slice(D, 2 * D)
+    for value in (math.inf, -math.inf):
+        x[1, int(where * (S - 1)), D + int(where * (D - 1))] = value
+        y, mean, rstd = g.group_norm_act(x, groups, w, b, act=act, return_stats=True)
+        assert y[1, :, bad].isnan().all() and not mean[1, 1].isfinite() and rstd[1, 1].isnan()
+        dx = g.group_norm_act_grad(dy, x, mean, rstd, groups, w, b, act=act)[0]
+        assert dx[1, :, bad].isnan().all()
+        y[1, :, bad], dx[1, :, bad] = clean[0][1, :, bad], dclean[1, :, bad]
+        assert torch.equal(y, clean[0]) and torch.equal(dx, dclean)
