@@ -221,4 +221,13 @@ __device__ __forceinline__ float warp_max(float v)
     return v;
 }
 
+// --------------------------------------------------------------------- host
+
+// Blocks of so many threads of a kernel that an SM holds.
+inline int resident_blocks(int threads, const void* kernel)
+{
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) == cudaSuccess && n > 0 ? n : 1;
+}
+
 }  // namespace gbnms

@@ -1337,13 +1337,6 @@ static bool norm_in_clusters(const NormArgs& a, void* ws, cudaStream_t st, bool 
     return false;
 }
 
-// Blocks of NT threads of a kernel that an SM holds.
-inline int resident_blocks(const void* kernel)
-{
-    int n = 0;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, NT, 0) == cudaSuccess && n > 0 ? n : 1;
-}
-
 // The tile with pieces for one wave of `resident` blocks on every SM, at most
 // those of the workspace.
 inline NormTile one_wave(const NormArgs& a, NormTile t, int resident)
@@ -1365,8 +1358,8 @@ static void norm_streamed(const NormArgs& a, void* ws, cudaStream_t st, bool gra
     // Whether the join takes a launch of its own.
     auto own = [&](const NormTile& t) { return t.pieces * (a.channels / a.groups / t.values) > OWN_JOIN; };
     if (!grad) {
-        static const int sums = resident_blocks(reinterpret_cast<const void*>(norm_partial_kernel<T, V, ONE>));
-        static const int rows = resident_blocks(reinterpret_cast<const void*>(norm_apply_kernel<T, V, ONE, ACT>));
+        static const int sums = resident_blocks(NT, reinterpret_cast<const void*>(norm_partial_kernel<T, V, ONE>));
+        static const int rows = resident_blocks(NT, reinterpret_cast<const void*>(norm_apply_kernel<T, V, ONE, ACT>));
         const NormTile t = one_wave(a, most, sums), u = one_wave(a, most, rows);
         NormArgs b = a;
         norm_partial_kernel<T, V, ONE><<<grid(t), block, 0, st>>>(a, t, w);
@@ -1378,8 +1371,8 @@ static void norm_streamed(const NormArgs& a, void* ws, cudaStream_t st, bool gra
         }
         launch_pdl(norm_apply_kernel<T, V, ONE, ACT>, grid(u), block, 0, st, b, u, t, w, joined);
     } else {
-        static const int sums = resident_blocks(reinterpret_cast<const void*>(norm_grad_partial_kernel<T, V, ONE, ACT>));
-        static const int rows = resident_blocks(reinterpret_cast<const void*>(norm_grad_apply_kernel<T, V, ONE, ACT>));
+        static const int sums = resident_blocks(NT, reinterpret_cast<const void*>(norm_grad_partial_kernel<T, V, ONE, ACT>));
+        static const int rows = resident_blocks(NT, reinterpret_cast<const void*>(norm_grad_apply_kernel<T, V, ONE, ACT>));
         const NormTile t = one_wave(a, most, sums), u = one_wave(a, most, rows);
         norm_grad_partial_kernel<T, V, ONE, ACT><<<grid(t), block, 0, st>>>(a, t, w);
         const unsigned params = a.dweight || a.dbias ? (a.channels + PARAMS - 1) / PARAMS : 0;

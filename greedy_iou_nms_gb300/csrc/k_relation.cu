@@ -121,6 +121,7 @@ RelationGradPlan relation_grad_plan(int64_t batch, int heads, int64_t queries, i
         const int64_t want = SMS * resident / (p.blocks * heads);  // one wave
         const int64_t least = (batch + 1023) / 1024;  // chains of at most 1024 additions
         p.chunks = want < least ? least : want > batch ? batch : want;
+        if (p.chunks > 65535) p.chunks = 65535;  // of a grid's second axis
         p.per = (batch + p.chunks - 1) / p.chunks;
         p.chunks = (batch + p.per - 1) / p.per;
         return p;

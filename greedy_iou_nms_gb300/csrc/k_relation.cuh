@@ -314,7 +314,7 @@ inline bool stretches(const RelationArgs& a)
 
 template <typename S, bool BY_IMAGE, bool STAGED>
 __global__ void __launch_bounds__(256, S::BLOCKS)
-relation_softmax_kernel(RelationArgs a, int per)
+relation_softmax_kernel(RelationArgs a, unsigned per)
 {
     using T = typename S::T;
     constexpr int EV = S::EV, NV = S::NV, L = S::L;
@@ -324,10 +324,11 @@ relation_softmax_kernel(RelationArgs a, int per)
     using Rows = Stretch<S>;
     const int K = static_cast<int>(a.keys), nb = a.num_buckets, H = a.heads;
     const int lane = static_cast<int>(threadIdx.x) % L;
-    const int inner = static_cast<int>(BY_IMAGE ? a.batch : H);
-    const int t0 = static_cast<int>(blockIdx.y) * per, t1 = t0 + per < inner ? t0 + per : inner;
+    // Unsigned: up to 2^31 - 1 images, and the loop counts past them.
+    const unsigned inner = static_cast<unsigned>(BY_IMAGE ? a.batch : H);
+    const unsigned t0 = blockIdx.y * per, t1 = t0 + per < inner ? t0 + per : inner;
     if (!BY_IMAGE) {
-        for (int x = threadIdx.x; x < (t1 - t0) * (nb + 1); x += 256) {
+        for (int x = threadIdx.x; x < static_cast<int>(t1 - t0) * (nb + 1); x += 256) {
             const int h = x / (nb + 1), u = x % (nb + 1);
             tab[x] = u < nb ? a.table[static_cast<int64_t>(u) * H + t0 + h] : -INFINITY;
         }
@@ -353,7 +354,7 @@ relation_softmax_kernel(RelationArgs a, int per)
     const int64_t start = t0 * step + static_cast<int64_t>(blockIdx.x) * pitch;
     const T* from = static_cast<const T*>(a.scores) + start;
     T* to_all = static_cast<T*>(a.out) + start;
-    auto fetch = [&](int t, int half) {
+    auto fetch = [&](unsigned t, int half) {
 #pragma unroll
         for (int r = 0; r < R; ++r, from += step)
             if (t + r < t1) rows.fetch(stage + (half * R + r) * pitch, from);
@@ -380,7 +381,7 @@ relation_softmax_kernel(RelationArgs a, int per)
             }
     }
     const float* row_tab = tab;
-    for (int t = t0; t < t1; t += R) {
+    for (unsigned t = t0; t < t1; t += R) {
         float x[R][NV][EV], top[R], sum[R], inv[R];
         T* mine[R];  // staged: the team's row
         if constexpr (STAGED) {
@@ -630,7 +631,7 @@ __device__ __forceinline__ void grad_rows(float (&p)[R][S::NV][S::EV], float (&d
 // By image: block (x, y, z) = (query tile, image chunk, head).
 template <typename S>
 __global__ void __launch_bounds__(256, S::GRAD_BLOCKS)
-relation_grad_image_kernel(RelationArgs a, int per, int columns, float* part)
+relation_grad_image_kernel(RelationArgs a, unsigned per, int columns, float* part)
 {
     using T = typename S::T;
     constexpr int EV = S::EV, NV = S::NV, L = S::L;
@@ -638,8 +639,8 @@ relation_grad_image_kernel(RelationArgs a, int per, int columns, float* part)
     __shared__ float red[2][8];
     const int K = static_cast<int>(a.keys), nb = a.num_buckets, head = static_cast<int>(blockIdx.z);
     const int lane = static_cast<int>(threadIdx.x) % L;
-    const int batch = static_cast<int>(a.batch);
-    const int t0 = static_cast<int>(blockIdx.y) * per, t1 = t0 + per < batch ? t0 + per : batch;
+    const unsigned batch = static_cast<unsigned>(a.batch);  // the loop counts past it
+    const unsigned t0 = blockIdx.y * per, t1 = t0 + per < batch ? t0 + per : batch;
     for (int x = threadIdx.x; x < (nb + 1) * columns; x += 256) hist[x] = 0.0f;
     const unsigned Q = static_cast<unsigned>(a.queries), want = blockIdx.x * (256 / L) + threadIdx.x / L;
     const bool real = want < Q;
@@ -670,8 +671,8 @@ relation_grad_image_kernel(RelationArgs a, int per, int columns, float* part)
     for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int e = 0; e < EV; ++e) acc[v][e] = 0.0f;
-    for (int t = t0; t < t1; t += R) {
-        const int rows = t + R < t1 ? R : t1 - t;
+    for (unsigned t = t0; t < t1; t += R) {
+        const int rows = t + R < t1 ? R : static_cast<int>(t1 - t);
         if (R > 1) {  // past the last row: that row again, neither stored nor added
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -916,13 +917,6 @@ inline void relation_shape(const RelationArgs& a, F f)
 
 constexpr int64_t blocks_over(int64_t n, int64_t each) { return (n + each - 1) / each; }
 
-// Blocks of 256 threads of a kernel that an SM holds.
-inline int resident_blocks(const void* kernel)
-{
-    int n = 0;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, 256, 0) == cudaSuccess && n > 0 ? n : 1;
-}
-
 template <typename T>
 inline void softmax_type(const RelationArgs& a, cudaStream_t st)
 {
@@ -939,7 +933,7 @@ inline void softmax_type(const RelationArgs& a, cudaStream_t st)
         const bool staged = image && stretches<S>(a);
         size_t smem = staged ? 2 * S::ROWS * sizeof(T) * Stretch<S>::TEAMS * a.keys : 0;
         // Chunks of the inner index: one wave of resident blocks.
-        static const int held = resident_blocks(reinterpret_cast<const void*>(relation_softmax_kernel<S, true, false>));
+        static const int held = resident_blocks(256, reinterpret_cast<const void*>(relation_softmax_kernel<S, true, false>));
         const int fit = staged ? static_cast<int>(220 * 1024 / (smem + 1024)) : held;
         int64_t chunks = SMS * (!image ? S::BLOCKS : fit < held ? fit : held) / blocks;
         if (chunks < 1) chunks = 1;
@@ -948,7 +942,7 @@ inline void softmax_type(const RelationArgs& a, cudaStream_t st)
             const int64_t most = 40 * 1024 / (4 * (a.num_buckets + 1));
             if (chunks < blocks_over(inner, most)) chunks = blocks_over(inner, most);
         }
-        const int per = static_cast<int>(blocks_over(inner, chunks));
+        const unsigned per = static_cast<unsigned>(blocks_over(inner, chunks));
         const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(blocks_over(inner, per)));
         auto run = [&](auto* kernel) {
             if (smem > 40 * 1024) ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
@@ -982,7 +976,7 @@ inline void grad_type(const RelationArgs& a, float* part, cudaStream_t st)
         using S = decltype(shape);
         if (image) {
             relation_grad_image_kernel<S><<<dim3(static_cast<unsigned>(p.blocks), static_cast<unsigned>(p.chunks),
-                                                 a.heads), 256, table, st>>>(a, static_cast<int>(p.per), p.columns,
+                                                 a.heads), 256, table, st>>>(a, static_cast<unsigned>(p.per), p.columns,
                                                                              part);
         } else {
             auto* k = p.columns == 32 ? relation_grad_head_kernel<S, 32> : relation_grad_head_kernel<S, 0>;

@@ -257,3 +257,19 @@ def test_short_odd_rows_by_image(t, B, H, Q, K):
     16 bytes or not, the last block's rows end inside a vector, images in
     fours and a remainder."""
     _check(*_inputs(B + K, B, H, Q, K, t, 31, 1))
+
+
+def test_as_many_images_as_rows_may_be():
+    """2^31 - 1 images of one pair: past 2^16 chunks and to the end of 32-bit
+    counts.  da is 1/4 everywhere; the table's entry is chains of at most
+    2^15 images and 2^13 partial sums."""
+    n = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 32e9:
+        pytest.skip("memory")
+    m = torch.zeros(1, 1, 1, dtype=torch.int16, device="cuda")
+    x = torch.zeros(n, 1, 1, 1, dtype=torch.float16, device="cuda")
+    probs = g.relation_softmax(x, torch.ones(1, 1, device="cuda"), m)
+    assert probs.min() == 1 and probs.max() == 1
+    ds, dt = g.relation_softmax_grad(x.fill_(1.0), probs.fill_(0.5), m, 1)
+    assert ds.min() == 0.25 and ds.max() == 0.25
+    assert abs(float(dt) - n / 4) <= (2 ** 15 + 2 ** 13 + 64) * R.EPS * n / 4
