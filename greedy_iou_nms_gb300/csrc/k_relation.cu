@@ -131,14 +131,15 @@ RelationGradPlan relation_grad_plan(int64_t batch, int heads, int64_t queries, i
     // else 32 or fewer for one block of six warps.
     constexpr int ROOM = 208 * 1024;
     const int row = 4 * (num_buckets + 1), need = lanes == 256 ? 8 : 6;
-    if (lanes <= 32 && keys <= RELATION_MOST && 12 * 32 * row > ROOM && 4 * 16 * row <= ROOM / 2) {
+    const bool pairs = lanes <= 32 && keys <= RELATION_MOST;  // 16 columns: the kernel whose lanes share them
+    if (pairs && 12 * 32 * row > ROOM && 4 * 16 * row <= ROOM / 2) {
         p.columns = 16;
         const int fit = ROOM / 2 / (16 * row);
-        p.warps = fit > 6 ? 6 : fit;
+        p.warps = fit > RELATION_PAIR_WARPS ? RELATION_PAIR_WARPS : fit;
     } else {
         for (p.columns = 32; p.columns > 4 && need * p.columns * row > ROOM; p.columns /= 2) {}
-        const int fit = ROOM / (p.columns * row);
-        p.warps = fit > 8 ? 8 : fit;
+        const int fit = ROOM / (p.columns * row), most = pairs && p.columns == 16 ? RELATION_PAIR_WARPS : 8;
+        p.warps = fit > most ? most : fit;
     }
     const int64_t teams = p.warps * 32 / lanes, rows = batch * queries, want = (rows + teams - 1) / teams;
     const int resident = ROOM / (p.warps * p.columns * row);

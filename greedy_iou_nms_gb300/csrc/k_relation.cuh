@@ -725,7 +725,7 @@ relation_grad_image_kernel(RelationArgs a, unsigned per, int columns, float* par
 // its own, of COLUMNS columns: 32 (one a lane), 16 (lanes l and l + 16 share
 // one), or fewer, taken in turns (0: `columns` says how many).
 template <typename S, int COLUMNS>
-__global__ void __launch_bounds__(COLUMNS == 16 ? 192 : 256, COLUMNS == 16 ? 2 : 1)
+__global__ void __launch_bounds__(COLUMNS == 16 ? 32 * RELATION_PAIR_WARPS : 256, COLUMNS == 16 ? 2 : 1)
 relation_grad_head_kernel(RelationArgs a, int columns, float* part)
 {
     using T = typename S::T;

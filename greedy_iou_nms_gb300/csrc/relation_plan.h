@@ -7,6 +7,8 @@ namespace gbnms {
 
 constexpr int64_t RELATION_MOST = 8192;  // keys of a row that a block holds
 
+constexpr int RELATION_PAIR_WARPS = 6;  // of a block whose lanes share 16 columns, at most
+
 inline bool relation_by_image(const RelationArgs& a) { return a.sets == 1 && !a.key_mask && a.batch > 1; }
 
 // Geometry of the gradient, a function of the shapes alone but for `image`

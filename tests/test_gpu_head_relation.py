@@ -273,3 +273,12 @@ def test_as_many_images_as_rows_may_be():
     ds, dt = g.relation_softmax_grad(x.fill_(1.0), probs.fill_(0.5), m, 1)
     assert ds.min() == 0.25 and ds.max() == 0.25
     assert abs(float(dt) - n / 4) <= (2 ** 15 + 2 ** 13 + 64) * R.EPS * n / 4
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("nb", [100, 138, 225, 414, 415, 416, 440, 474, 475, 476, 831, 951, 1024])
+@pytest.mark.parametrize("K", [5, 64, 100, 300, 1000])
+def test_bucket_counts_by_head(t, nb, K):
+    """A map by image: the gradient's tables of every size that changes how
+    many columns and warps share the memory."""
+    _check(*_inputs(nb + K, 2, 3, 7, K, t, nb, 2))
