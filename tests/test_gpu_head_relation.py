@@ -282,3 +282,43 @@ def test_bucket_counts_by_head(t, nb, K):
     """A map by image: the gradient's tables of every size that changes how
     many columns and warps share the memory."""
     _check(*_inputs(nb + K, 2, 3, 7, K, t, nb, 2))
+
+
+@pytest.mark.parametrize("t,K", [(torch.bfloat16, 1000), (torch.float16, 300), (torch.float32, 1000), (torch.float32, 46),
+                                 (torch.bfloat16, 999), (torch.bfloat16, 128), (torch.float16, 64)])
+@pytest.mark.parametrize("nb", [138, 225, 414, 440, 553])
+def test_table_sums_of_lanes_that_share_a_column(t, K, nb):
+    """Two lanes to a column of sums: no addition is lost where one lane's
+    bucket is the other's a step before or behind, equal to it, or masked.
+    Every weight is 2^-10 and the gradients are whole numbers that add up to 0
+    in a row, so da = dprobs / 2^10 and its sums are exact in any order."""
+    r = torch.Generator().manual_seed(K + nb)
+    B, H, Q = 5, 2, 24
+    dp = torch.randint(-8, 9, (B, H, Q, K), generator=r).float()
+    half = K // 2
+    dp[..., half:2 * half] = -dp[..., :half]
+    if K % 2:
+        dp[..., -1] = 0
+    j = torch.arange(K)
+    lane, e = j // 8 % 32, j % 8
+    apart = torch.where(lane < 16, e, e - 1) + j // 256 * 8       # an element behind
+    other = torch.where(lane < 16, e, e + 1) + j // 256 * 8       # an element ahead
+    masked = torch.where(e % 2 == 0, -1, e)                       # masked in both lanes, or in one
+    masked[::3] = -1
+    rows = torch.stack([apart % nb, other % nb, j % 2, j * 0, masked, j % 16, j // 16 % nb,
+                        torch.randint(0, nb, (K,), generator=r)])
+    m = rows[torch.arange(B * Q) % 8].view(B, Q, K).to(torch.int16)
+    m = torch.where((m < 0) & (torch.arange(K) >= 2 * half), torch.zeros_like(m), m)
+    # A masked pair's partner of the row's other half is masked too: the row still adds up to 0.
+    gone = m < 0
+    gone[..., :half] |= gone[..., half:2 * half].clone()
+    gone[..., half:2 * half] |= gone[..., :half].clone()
+    m[gone] = -1
+    probs = torch.full((B, H, Q, K), 2.0 ** -10).to(t).cuda()
+    want = torch.zeros(nb + 1, H, dtype=torch.float64)
+    at = torch.where(m < 0, nb, m.long())
+    for h in range(H):
+        want[:, h].index_add_(0, at.reshape(-1), dp[:, h].double().reshape(-1) / 1024)
+    for _ in range(5):
+        got = g.relation_softmax_grad(dp.to(t).cuda(), probs, m.cuda(), nb)[1]
+        assert torch.equal(got.cpu().double(), want[:nb])
