@@ -668,7 +668,7 @@ norm_grad_apply_kernel(NormArgs a, NormTile t, NormTile from, NormScratch w, boo
         const int g = (p.channel + i) / D;
         const float r = a.rstd[p.image * a.groups + g];
         m1[i] = -r * s_a[g - j.first] * each_all;
-        m2[i] = -r * r * r * s_b[g - j.first] * each_all;
+        m2[i] = -(r * s_b[g - j.first] * each_all) * r * r;  // r^3 leaves binary32 where this does not
     }
     each_row_pair<2, T, V>(a, p, [&](const Pack<T, V>& x, const Pack<T, V>& dy, int64_t at) {
         float d[V], dz[V];

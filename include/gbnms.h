@@ -479,7 +479,9 @@ nms_status nms_dropout_run(const void* x, const void* residual, int32_t type, in
  *   mean, rstd device float [batch][groups] for the gradient, or NULL.  With
  *              no pixels both are 0.  A NaN or an infinity in a group leaves
  *              no number in its statistics, its kept results and its dx.
- *              Squares are summed in binary32: deviations stay below 2^60.
+ *              Squares are summed in binary32: those of a group's deviations
+ *              add up to less than 2^126, and with eps = 0 the variance is 0
+ *              or above 2^-110.
  *   workspace  >= nms_group_norm_workspace_size() bytes, 256-byte aligned.
  * The gradient, from the incoming gradient dy (laid out like x, with strides
  * of its own) and the forward's mean, rstd and dropout numbers:

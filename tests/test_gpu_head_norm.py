@@ -297,3 +297,14 @@ def test_infinity_leaves_no_number_in_its_group(act, S, C, groups, where):
         assert dx[1, :, bad].isnan().all()
         y[1, :, bad], dx[1, :, bad] = clean[0][1, :, bad], dclean[1, :, bad]
         assert torch.equal(y, clean[0]) and torch.equal(dx, dclean)
+
+
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("spread,eps", [(1e13, 1e-5), (1e15, 1e-5), (1e16, 0.0), (1e-6, 0.0), (1e-13, 0.0),
+                                        (1e-16, 0.0)])
+@pytest.mark.parametrize("S,C,groups", [(40, 16, 4), (9000, 32, 8), (700, 258, 3), (30000, 20, 2)])
+def test_spreads_far_from_one(t, spread, eps, S, C, groups):
+    """Small maps and large ones alike; the gradient goes along with x, so
+    that its projections on u count."""
+    x, dy, w, b = _inputs(S, 2, S, C, torch.float32)
+    _check((x * spread).to(t), (dy + 2 * x).to(t), w, b, groups, "silu", eps=eps)
