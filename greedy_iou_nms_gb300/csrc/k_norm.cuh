@@ -7,13 +7,15 @@
 //   dx = rstd * (du - avg(du) - u * avg(du * u)) with du = dz * weight.
 //
 // Statistics are pieces (count, mean, sum of squared deviations).  A thread
-// sums deviations from the first value it sees of a channel, so nothing is
-// lost to a mean far above the spread (an outlier as that first value costs
-// at most count * 2^-24 of the variance that it brings itself).  Pieces are
-// joined in a fixed order, in two steps: the mean m of their means, then the
-// deviations d of their means from m, M2 = sum of M2_i + n_i d_i^2 - n (avg
-// d)^2.  A piece's mean is a pair (high + low), so that d is right to its own
-// size and not to the mean's.
+// sums deviations from an origin: the mean of the first row that it sees, moved
+// to the mean of all that it has seen after 1, 2, 4, ... batches of rows.  So
+// nothing is lost to a mean far above the spread, and an outlier among the
+// first values costs a few roundings of its own square (as a fixed origin it
+// would add that square for every later value, to be taken off again: up to
+// 1 % of rstd over 2048 values).  Pieces are joined in a fixed order, in two
+// steps: the mean m of their means, then the deviations d of their means from
+// m, M2 = sum of M2_i + n_i d_i^2 - n (avg d)^2.  A piece's mean is a pair
+// (high + low), so that d is right to its own size and not to the mean's.
 #pragma once
 
 #include <type_traits>
@@ -33,8 +35,9 @@ constexpr int NT = 256;  // threads of a block
 // comes from L2 as far as that holds the map: the last launch goes through the
 // pieces backwards.
 
-// Rows of a piece, at most: a thread's sums are chains of some hundred
-// additions.
+// Rows of a piece, at most: 256 of a thread, whose sums by channel are chains
+// of so many additions (sums by group: 64 batches of 32 values, each added up
+// on its own).
 constexpr int MOST_ROWS = 1024;
 
 // Row pieces of an image, at most: 32 rows each at least, and one wave of
@@ -191,12 +194,100 @@ __device__ __forceinline__ void each_row_pair(const NormArgs& a, const Spot& p, 
         if (k < n) f(q[k], d[k], at);
 }
 
+// f(B vectors, how many of them are rows) for a thread's rows, all loaded
+// before f; the count is a constant but for the last.
+template <int B, typename T, int V, typename F>
+__device__ __forceinline__ void each_batch(const NormArgs& a, const Spot& p, F f)
+{
+    int n = (p.row_end - p.row - p.ty + p.rows - 1) / p.rows;  // rows of this thread; below 1 for none
+    const T* x = static_cast<const T*>(a.x) + p.image * a.x_image + (p.row + p.ty) * a.x_pixel + p.channel;
+    const int64_t stride = p.rows * a.x_pixel;
+    Pack<T, V> q[B];
+    for (; n >= B; n -= B) {
+#pragma unroll
+        for (int k = 0; k < B; ++k, x += stride) q[k] = *reinterpret_cast<const Pack<T, V>*>(x);
+        f(q, B);
+    }
+#pragma unroll
+    for (int k = 0; k < B - 1; ++k, x += stride)
+        if (k < n) q[k] = *reinterpret_cast<const Pack<T, V>*>(x);
+    if (n > 0) f(q, n);
+}
+
+// Running sums of a thread's deviations and their squares, by channel of its
+// vector or (ONE) of the whole vector.
+template <int V, bool ONE>
+struct Moments {
+    static constexpr int P = ONE ? 1 : V;
+    float origin[P], s[P], q[P];
+    int rows, moves_at;  // rows so far; the origin moves when there are so many
+    float each;          // 1 / values of moves_at rows
+
+    __device__ __forceinline__ Moments()
+    {
+#pragma unroll
+        for (int i = 0; i < P; ++i) origin[i] = s[i] = q[i] = 0.0f;
+        rows = moves_at = 0;
+    }
+
+    template <typename T, int B>
+    __device__ __forceinline__ void add(const Pack<T, V> (&pack)[B], int n)
+    {
+        if (rows == 0) {
+            float v[V];
+            widen(v, pack[0]);
+#pragma unroll
+            for (int i = 0; i < P; ++i) origin[i] = v[i];
+            if (ONE) {  // equal values give exactly that mean
+                float d = 0.0f;
+#pragma unroll
+                for (int i = 1; i < V; ++i) d += v[i] - v[0];
+                origin[0] += d * (1.0f / V);
+            }
+            moves_at = B;
+            each = 1.0f / (B * (ONE ? V : 1));
+        }
+        float row_s[B], row_q[B];  // ONE: of each row, added up in pairs
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            row_s[k] = row_q[k] = 0.0f;
+            if (k >= n) continue;
+            float v[V];
+            widen(v, pack[k]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float d = v[i] - origin[ONE ? 0 : i];
+                float &to_s = ONE ? row_s[k] : s[ONE ? 0 : i], &to_q = ONE ? row_q[k] : q[ONE ? 0 : i];
+                to_s += d;
+                to_q = fmaf(d, d, to_q);
+            }
+        }
+        if (ONE) {
+            static_assert(B == 4, "pairs of rows");
+            s[0] += (row_s[0] + row_s[1]) + (row_s[2] + row_s[3]);
+            q[0] += (row_q[0] + row_q[1]) + (row_q[2] + row_q[3]);
+        }
+        rows += n;
+        if (rows != moves_at) return;
+        const float values = static_cast<float>(rows * (ONE ? V : 1));
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float to = fmaf(s[i], each, origin[i]), d = to - origin[i];  // as far as it moves
+            q[i] = fmaf(d, fmaf(values, d, -2.0f * s[i]), q[i]);
+            s[i] = fmaf(-values, d, s[i]);
+            origin[i] = to;
+        }
+        moves_at *= 2;
+        each *= 0.5f;
+    }
+};
+
 // (mean, squared deviations) of each row piece by column: a vector (ONE: its
 // channels are of one group) or a channel.  Three operations a value; four
 // rows' loads in flight a thread, 32 warps an SM.  16 x 6400 x 256 bf16: 10 us,
 // 5.0 TB/s; the block's ramps (a first load, the join) are a third of it.
 template <typename T, int V, bool ONE>
-__global__ void __launch_bounds__(NT, 4)
+__global__ void __launch_bounds__(NT, ONE || V < 8 ? 4 : 3)
 norm_partial_kernel(NormArgs a, NormTile t, NormScratch w)
 {
     constexpr int P = ONE ? 1 : V;
@@ -204,38 +295,18 @@ norm_partial_kernel(NormArgs a, NormTile t, NormScratch w)
     __shared__ int s_count[NT];
     pdl_release();
     const Spot p = spot<V>(a, t, blockIdx.x);
-    float first[P], s[P], q[P];
-    int rows = 0;
-#pragma unroll
-    for (int i = 0; i < P; ++i) first[i] = s[i] = q[i] = 0.0f;
-    if (p.in) {
-        const int begin = p.row + p.ty;
-        if (begin < p.row_end) {
-            const T* x = static_cast<const T*>(a.x) + p.image * a.x_image + begin * a.x_pixel + p.channel;
-#pragma unroll
-            for (int i = 0; i < P; ++i) first[i] = to_f32(x[i]);
-            rows = (p.row_end - begin + p.rows - 1) / p.rows;
-        }
-        each_row<4, T, V>(a, p, [&](const Pack<T, V>& pack, int64_t) {
-            float v[V];
-            widen(v, pack);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = v[i] - first[ONE ? 0 : i];
-                s[ONE ? 0 : i] += d;
-                q[ONE ? 0 : i] = fmaf(d, d, q[ONE ? 0 : i]);
-            }
-        });
-    }
-    const int count = rows * (ONE ? V : 1);
+    Moments<V, ONE> sums;
+    if (p.in)
+        each_batch<4, T, V>(a, p, [&](const Pack<T, V>(&pack)[4], int rows) { sums.template add<T, 4>(pack, rows); });
     if (p.ty < p.rows) {
+        const int count = sums.rows * (ONE ? V : 1);
         s_count[threadIdx.x] = count;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const float m = count ? s[i] / count : 0.0f;
-            s_high[threadIdx.x * P + i] = first[i];
+            const float m = count ? sums.s[i] / count : 0.0f;
+            s_high[threadIdx.x * P + i] = sums.origin[i];
             s_low[threadIdx.x * P + i] = m;
-            s_m2[threadIdx.x * P + i] = not_below_0(q[i] - s[i] * m);
+            s_m2[threadIdx.x * P + i] = not_below_0(sums.q[i] - sums.s[i] * m);
         }
     }
     __syncthreads();

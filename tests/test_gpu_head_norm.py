@@ -308,3 +308,23 @@ def test_spreads_far_from_one(t, spread, eps, S, C, groups):
     that its projections on u count."""
     x, dy, w, b = _inputs(S, 2, S, C, torch.float32)
     _check((x * spread).to(t), (dy + 2 * x).to(t), w, b, groups, "silu", eps=eps)
+
+
+@pytest.mark.parametrize("t,N,S,C,groups", [(torch.bfloat16, 16, 25600, 512, 32), (torch.bfloat16, 16, 25600, 504, 84),
+                                            (torch.float32, 16, 25600, 256, 16), (torch.bfloat16, 16, 25600, 510, 17)])
+@pytest.mark.parametrize("far", [1e3, 1e5])
+def test_outliers_at_the_start_of_long_pieces(t, N, S, C, groups, far):
+    """Pieces of about a thousand rows, 256 and 2048 values to a thread, whose
+    first values stand far out; mean and rstd against 64 bits."""
+    gen = torch.Generator(device="cuda").manual_seed(C)
+    x = torch.randn(N, S, C, generator=gen, device="cuda").to(t)
+    D = C // groups
+    for k in range(groups):
+        x[k % N, 0, k * D] = far
+        x[k % N, S // 2 // 1024 * 1024, k * D] = -far
+        x[k % N, k, k * D + D - 1] = far
+    _, mean, rstd = g.group_norm_act(x, groups, return_stats=True)
+    for n in range(N):
+        var, m = torch.var_mean(x[n].double().view(S, groups, D), dim=(0, 2), correction=0)
+        R.close(mean[n], m.cpu(), (64 * R.EPS * (var.sqrt() + m.abs())).cpu())
+        R.close(rstd[n], (1 / torch.sqrt(var + 1e-5)).cpu(), (64 * R.EPS / torch.sqrt(var + 1e-5)).cpu())
