@@ -497,7 +497,7 @@ norm_apply_kernel(NormArgs a, NormTile t, NormTile from, NormScratch w, bool joi
         widen(v, q);
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = fmaf(v[i] - mean[ONE ? 0 : i], scale[i], shift[i]);
-        act_values<V>(v, ACT);
+        act_values<T, V>(v, ACT);
         if (dropping) drop<V>(v, static_cast<uint64_t>(at), a.drop);
         store_row<T, V>(y + at, v);
     });
@@ -533,7 +533,7 @@ __device__ __forceinline__ void slope_row(const NormArgs& a, const float (&mean)
         d[i] -= mean[P == 1 ? 0 : i];
         z[i] = fmaf(d[i], scale[i], bias[i]);
     }
-    act_slopes<V>(dz, z, ACT);
+    act_slopes<T, V>(dz, z, ACT);
 }
 
 // Sums by channel of dz and dz * (x - mean) of each row piece.  16 x 1600 x 256
@@ -1044,7 +1044,7 @@ norm_cluster_kernel(NormArgs a, NormCluster t)
             widen(v, *from);
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = fmaf(v[i] - mean[ONE ? 0 : i], scale[i], shift[i]);
-            act_values<V>(v, a.act);
+            act_values<T, V>(v, a.act);
             if (a.drop.limit < 65536u) drop<V>(v, static_cast<uint64_t>(at), a.drop);
             store_row<T, V>(y, v);
         }
@@ -1155,7 +1155,7 @@ norm_grad_cluster_kernel(NormArgs a, NormCluster t, NormScratch w)
                 z[i] = fmaf(u[i], weight[i], bias[i]);
             }
             if (a.drop.limit < 65536u) drop_mask<V>(dz, static_cast<uint64_t>(at), a.drop);
-            act_slopes<V>(dz, z, a.act);
+            act_slopes<T, V>(dz, z, a.act);
             keep_floats<V>(dat, dz);
 #pragma unroll
             for (int i = 0; i < V; ++i) {

@@ -328,3 +328,32 @@ def test_outliers_at_the_start_of_long_pieces(t, N, S, C, groups, far):
         var, m = torch.var_mean(x[n].double().view(S, groups, D), dim=(0, 2), correction=0)
         R.close(mean[n], m.cpu(), (64 * R.EPS * (var.sqrt() + m.abs())).cpu())
         R.close(rstd[n], (1 / torch.sqrt(var + 1e-5)).cpu(), (64 * R.EPS / torch.sqrt(var + 1e-5)).cpu())
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("groups", [1, 512])
+def test_gelu_from_tail_to_tail(t, groups):
+    """z given exactly (as the bias, with weight 0), on a large and a small
+    map.  The density's exponent z^2 log2(e) / 2 (+ 1.33) is off by three
+    roundings (3 ln 2 of them, 1.5 z^2, in the density) and 2^x and 1/x by 2^-22.
+    The distribution function: in binary32 for z < 0 within 2^-24 (20 + 2 z^2) of
+    itself and beyond 0 by that of the tail and a rounding; in 16 bits within
+    2^-21, and for z < 0 within 3e-5 of itself."""
+    z = torch.cat([torch.linspace(-10, 10, 4001), torch.linspace(-0.1, 0.1, 95)])
+    C = z.numel()
+    zero = torch.zeros(C, device="cuda")
+    x = torch.randn(1, 8, C, generator=torch.Generator().manual_seed(1)).to(t).cuda()
+    dy = torch.zeros_like(x)
+    dy[0, 0] = 1
+    y, mean, rstd = g.group_norm_act(x, groups, zero, z.cuda(), act="gelu", return_stats=True)
+    slope = g.group_norm_act_grad(dy, x, mean, rstd, groups, zero, z.cuda(), act="gelu")[2]  # dbias
+    z = z.double()
+    cdf = 0.5 * torch.special.erfc(-z / math.sqrt(2))
+    part = z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    if t == torch.float32:
+        off = torch.where(z < 0, cdf, 1 - cdf) * (20 + 2 * z * z) * R.EPS + torch.where(z < 0, 0.0, R.EPS)
+    else:
+        off = torch.where(z < 0, torch.clamp(3e-5 * cdf, max=2.0 ** -21), torch.full_like(z, 2.0 ** -21))
+    density_off = (8 + 2 * z * z) * R.EPS
+    R.close(y[0, 0], z * cdf, z.abs() * off + R.EPS * (z * cdf).abs())
+    R.close(slope, cdf + part, off + part.abs() * density_off + 2 * R.EPS * (cdf + part.abs()))
