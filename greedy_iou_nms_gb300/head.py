@@ -5,7 +5,7 @@ buckets of relative position.
 
 The raw entry points carry the names of the C functions (device addresses as
 ints, the status code returned); the functions below them work on CUDA
-tensors, run on the current stream and never synchronise.
+tensors, run on their device's current stream and never synchronise.
 greedy_iou_nms_gb300.autograd has the same operators for torch's autograd.
 """
 from __future__ import annotations
@@ -176,6 +176,16 @@ def _stream(x) -> int:
     return _torch().cuda.current_stream(x.device).cuda_stream
 
 
+def _launch(x, entry, *args) -> int:
+    """entry(*args, the current stream of x's device), that device current:
+    a launch goes to the current one."""
+    cuda, at = _torch_module.cuda, x.get_device()
+    if cuda.current_device() == at:
+        return entry(*args, _stream(x))
+    with cuda.device(at):
+        return entry(*args, _stream(x))
+
+
 def _like(x):
     """An uninitialised contiguous tensor of x's shape and type."""
     if x.is_contiguous():
@@ -266,10 +276,9 @@ def group_norm_act(x, groups: int, weight=None, bias=None, *, eps: float = 1e-5,
         mean = torch.empty((batch, groups), dtype=torch.float32, device=x.device)
         rstd = torch.empty_like(mean)
     ws = torch.empty(wsb, dtype=torch.uint8, device=x.device)
-    st = _lib().nms_group_norm_run(xs.data_ptr(), image, pixel, kind, batch, pixels, channels, groups, wp, bp, ptype,
-                                   eps, code, p, seed, offset, y.data_ptr(),
-                                   mean.data_ptr() if return_stats else None,
-                                   rstd.data_ptr() if return_stats else None, ws.data_ptr(), wsb, _stream(x))
+    st = _launch(x, _lib().nms_group_norm_run, xs.data_ptr(), image, pixel, kind, batch, pixels, channels, groups, wp,
+                 bp, ptype, eps, code, p, seed, offset, y.data_ptr(), mean.data_ptr() if return_stats else None,
+                 rstd.data_ptr() if return_stats else None, ws.data_ptr(), wsb)
     if st:
         _raise(st, "nms_group_norm_run")
     return (y, mean, rstd) if return_stats else y
@@ -301,10 +310,9 @@ def group_norm_act_grad(dy, x, mean, rstd, groups: int, weight=None, bias=None, 
     dweight = torch.empty(channels, dtype=torch.float32, device=x.device)
     dbias = torch.empty_like(dweight)
     ws = torch.empty(wsb, dtype=torch.uint8, device=x.device)
-    st = _lib().nms_group_norm_grad_run(dys.data_ptr(), dimage, dpixel, xs.data_ptr(), image, pixel, kind, batch,
-                                        pixels, channels, groups, mean.data_ptr(), rstd.data_ptr(), wp, bp, ptype,
-                                        code, p, seed, offset, dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(),
-                                        ws.data_ptr(), wsb, _stream(x))
+    st = _launch(x, _lib().nms_group_norm_grad_run, dys.data_ptr(), dimage, dpixel, xs.data_ptr(), image, pixel, kind,
+                 batch, pixels, channels, groups, mean.data_ptr(), rstd.data_ptr(), wp, bp, ptype, code, p, seed,
+                 offset, dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(), ws.data_ptr(), wsb)
     if st:
         _raise(st, "nms_group_norm_grad_run")
     return dx, dweight, dbias
@@ -321,8 +329,8 @@ def dropout(x, p: float, seed: int, offset: int = 0, *, residual=None):
         residual = residual.contiguous()
     x = x.contiguous()
     y = _torch_module.empty_like(x)
-    st = _lib().nms_dropout_run(x.data_ptr(), None if residual is None else residual.data_ptr(), kind, x.numel(), p,
-                                seed, offset, y.data_ptr(), _stream(x))
+    st = _launch(x, _lib().nms_dropout_run, x.data_ptr(), None if residual is None else residual.data_ptr(), kind,
+                 x.numel(), p, seed, offset, y.data_ptr())
     if st:
         _raise(st, "nms_dropout_run")
     return y
@@ -384,8 +392,8 @@ def relation_buckets(q_pos, k_pos, lut):
         raise ValueError("relation_buckets: q_pos and k_pos must have as many sets, or one of them one")
     q_pos, k_pos, lut = q_pos.contiguous(), k_pos.contiguous(), lut.contiguous()
     out = torch.empty((ks if qs == 1 else qs, Q, K), dtype=torch.int16, device=q_pos.device)
-    st = _lib().nms_relation_buckets_run(q_pos.data_ptr(), qs, k_pos.data_ptr(), ks, Q, K, axes, lut.data_ptr(),
-                                         width // 2, out.data_ptr(), _stream(q_pos))
+    st = _launch(q_pos, _lib().nms_relation_buckets_run, q_pos.data_ptr(), qs, k_pos.data_ptr(), ks, Q, K, axes,
+                 lut.data_ptr(), width // 2, out.data_ptr())
     if st:
         _raise(st, "nms_relation_buckets_run")
     return out
@@ -431,9 +439,8 @@ def relation_softmax(scores, table, buckets, *, scale: float = 1.0, key_mask=Non
         table = table.to(torch.float32)
     table, scores = table.contiguous(), scores.contiguous()
     out = torch.empty_like(scores)
-    st = _lib().nms_relation_softmax_run(scores.data_ptr(), kind, B, H, Q, K, buckets.data_ptr(), sets,
-                                         table.data_ptr(), table.shape[0], mask, scale, out.data_ptr(),
-                                         _stream(scores))
+    st = _launch(scores, _lib().nms_relation_softmax_run, scores.data_ptr(), kind, B, H, Q, K, buckets.data_ptr(),
+                 sets, table.data_ptr(), table.shape[0], mask, scale, out.data_ptr())
     if st:
         _raise(st, "nms_relation_softmax_run")
     return out
@@ -453,9 +460,9 @@ def relation_softmax_grad(dprobs, probs, buckets, num_buckets: int, *, scale: fl
     ws = torch.empty(wsb, dtype=torch.uint8, device=probs.device)
     ds = torch.empty_like(probs)
     dtable = torch.empty((num_buckets, H), dtype=torch.float32, device=probs.device)
-    st = _lib().nms_relation_softmax_grad_run(dprobs.data_ptr(), probs.data_ptr(), kind, B, H, Q, K,
-                                              buckets.data_ptr(), sets, num_buckets, mask, scale, ds.data_ptr(),
-                                              dtable.data_ptr(), ws.data_ptr(), wsb, _stream(probs))
+    st = _launch(probs, _lib().nms_relation_softmax_grad_run, dprobs.data_ptr(), probs.data_ptr(), kind, B, H, Q, K,
+                 buckets.data_ptr(), sets, num_buckets, mask, scale, ds.data_ptr(), dtable.data_ptr(), ws.data_ptr(),
+                 wsb)
     if st:
         _raise(st, "nms_relation_softmax_grad_run")
     return ds, dtable

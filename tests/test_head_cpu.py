@@ -133,3 +133,59 @@ def test_logarithmic_table():
 def test_cell_table():
     lut = g.relation_lut_cells(1, 2)
     assert lut.tolist() == [[0, 0, 5, 10, 10], [0, 1, 2, 3, 4]] and lut.dtype == torch.int32
+
+
+class OnSecond(torch.Tensor):
+    """A CPU tensor that says it lies on the second CUDA device."""
+    is_cuda = True
+
+    def get_device(self):
+        return 1
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_launches_go_to_the_tensors_device(lib, monkeypatch, current):
+    """Another device being current, each tensor function makes its operands'
+    device current for the launch and hands over that device's stream."""
+    from greedy_iou_nms_gb300 import head
+    head._torch()
+    now, calls = [current], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *_):
+            now[0] = self.before
+
+    class Recorder:
+        def __getattr__(self, name):
+            if not name.endswith("_run"):
+                return getattr(lib, name)
+            return lambda *args: calls.append((name, now[0], args[-1])) or 0
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(head, "_raw_stream", lambda index: 1000 + index)
+    monkeypatch.setattr(head, "_loaded", Recorder())
+
+    def on(v):
+        return v.as_subclass(OnSecond)
+
+    x, stats = on(torch.randn(2, 9, 12)), on(torch.ones(2, 3))
+    scores, table = on(torch.randn(2, 3, 4, 5)), on(torch.randn(6, 3))
+    pos, lut = on(torch.zeros(1, 4, 2, dtype=torch.int32)), on(torch.zeros(2, 5, dtype=torch.int32))
+    m = on(torch.zeros(1, 4, 5, dtype=torch.int16))
+    g.group_norm_act(x, 3)
+    g.group_norm_act_grad(x, x, stats, stats, 3)
+    g.dropout(x, 0.5, 1)
+    g.relation_buckets(pos, pos, lut)
+    g.relation_softmax(scores, table, m)
+    g.relation_softmax_grad(scores, scores, m, 6)
+    assert [c[0] for c in calls] == ["nms_group_norm_run", "nms_group_norm_grad_run", "nms_dropout_run",
+                                     "nms_relation_buckets_run", "nms_relation_softmax_run",
+                                     "nms_relation_softmax_grad_run"]
+    assert all(at == 1 and stream == 1001 for _, at, stream in calls) and now[0] == current
