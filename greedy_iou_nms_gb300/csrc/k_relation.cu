@@ -149,11 +149,38 @@ RelationGradPlan relation_grad_plan(int64_t batch, int heads, int64_t queries, i
     return p;
 }
 
+// Images from which the gradient of one map for all goes by image.  A block by image ends with a table of sums for
+// its few queries, which costs the more the more elements a lane holds; by head the tables are few, but each image's
+// rows cost more, most where lanes take turns at the columns.  Us by image and by head, 8 heads:
+//   rows up to 320 keys            2 x 300 x 300 bf16     25 and 29    64 x 300 x 300           73 and 109
+//   lanes in turns                 4 x 200 x 1100 bf16    82 and 91    2 x 200 x 1100           76 and 56
+//   up to 16 elements, 16 bits     16 x 512 x 512 bf16    75 and 68    64 x 512 x 512          166 and 194
+//   more                           16 x 1000 x 1000 bf16 326 and 202   2 x 1000 x 1000         205 and 50
+//   binary32, odd rows             8 x 1000 x 1000 fp32  302 and 294   2 x 1000 x 1000         218 and 97
+static int64_t images_to_go_by(int64_t batch, int heads, int64_t queries, int64_t keys, int num_buckets, bool packed)
+{
+    if (keys <= 320) return 2;
+    const RelationGradPlan head = relation_grad_plan(batch, heads, queries, keys, num_buckets, false);
+    const int lanes = team_lanes(keys);
+    if (head.columns < (lanes <= 32 ? 16 : 32)) return 4;  // turns
+    return !packed ? 8 : (keys + lanes - 1) / lanes <= 16 ? 16 : 64;
+}
+
+bool relation_grad_by_image(const RelationArgs& a)
+{
+    return relation_by_image(a) && a.keys <= RELATION_MOST &&
+           a.batch >= images_to_go_by(a.batch, a.heads, a.queries, a.keys, a.num_buckets,
+                                      a.type != NMS_TYPE_F32 && a.keys % 2 == 0);
+}
+
 size_t relation_grad_workspace_bytes(int64_t batch, int heads, int64_t queries, int64_t keys, int num_buckets)
 {
     if (batch == 0 || queries == 0 || keys == 0) return 256;
     const int64_t a = relation_grad_plan(batch, heads, queries, keys, num_buckets, false).parts();
-    const int64_t b = relation_grad_plan(batch, heads, queries, keys, num_buckets, true).parts();
+    // By image as well where the type, the map and the mask may have it so.
+    const int64_t least = images_to_go_by(batch, heads, queries, keys, num_buckets, false);
+    const bool image = keys <= RELATION_MOST && batch >= least;
+    const int64_t b = image ? relation_grad_plan(batch, heads, queries, keys, num_buckets, true).parts() : 0;
     return 4 * static_cast<size_t>(heads) * (a > b ? a : b) * num_buckets + 256;
 }
 
@@ -183,7 +210,7 @@ void launch_relation_grad(const RelationArgs& a, void* workspace, cudaStream_t s
     else if (a.type == NMS_TYPE_F16) relation_grad_f16(a, part, st);
     else relation_grad_bf16(a, part, st);
     const int64_t parts = relation_grad_plan(a.batch, a.heads, a.queries, a.keys, a.num_buckets,
-                                             relation_by_image(a) && a.keys <= RELATION_MOST).parts();
+                                             relation_grad_by_image(a)).parts();
     relation_table_kernel<<<dim3((a.num_buckets + 31) / 32, a.heads), 256, 0, st>>>(part, parts, a.num_buckets,
                                                                                      a.heads, a.dtable);
 }

@@ -966,7 +966,7 @@ inline void softmax_type(const RelationArgs& a, cudaStream_t st)
 template <typename T>
 inline void grad_type(const RelationArgs& a, float* part, cudaStream_t st)
 {
-    const bool image = relation_by_image(a) && a.keys <= RELATION_MOST;
+    const bool image = relation_grad_by_image(a);
     const RelationGradPlan p = relation_grad_plan(a.batch, a.heads, a.queries, a.keys, a.num_buckets, image);
     const size_t table = 4 * static_cast<size_t>(a.num_buckets + 1) * p.columns;
     if (a.keys > RELATION_MOST) {

@@ -284,8 +284,8 @@ def test_bucket_counts_by_head(t, nb, K):
     _check(*_inputs(nb + K, 2, 3, 7, K, t, nb, 2))
 
 
-@pytest.mark.parametrize("t,K", [(torch.bfloat16, 1000), (torch.float16, 300), (torch.float32, 1000), (torch.float32, 46),
-                                 (torch.bfloat16, 999), (torch.bfloat16, 128), (torch.float16, 64)])
+@pytest.mark.parametrize("t,K", [(torch.bfloat16, 1000), (torch.float16, 300), (torch.float32, 1000),
+                                 (torch.float32, 46), (torch.bfloat16, 999), (torch.bfloat16, 128), (torch.float16, 64)])
 @pytest.mark.parametrize("nb", [138, 225, 414, 440, 553])
 def test_table_sums_of_lanes_that_share_a_column(t, K, nb):
     """Two lanes to a column of sums: no addition is lost where one lane's
@@ -322,3 +322,12 @@ def test_table_sums_of_lanes_that_share_a_column(t, K, nb):
     for _ in range(5):
         got = g.relation_softmax_grad(dp.to(t).cuda(), probs, m.cuda(), nb)[1]
         assert torch.equal(got.cpu().double(), want[:nb])
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("K,nb", [(320, 40), (321, 40), (400, 225), (513, 225), (601, 9), (1000, 1000), (1100, 225),
+                                  (1100, 32), (4100, 32)])
+@pytest.mark.parametrize("B", [2, 3, 4, 7, 8, 15, 16, 63, 64])
+def test_one_map_for_few_and_many_images(t, K, nb, B):
+    """Both sides of every number of images at which the gradient goes another way."""
+    _check(*_inputs(K + B, B, 1, 3, K, t, nb, 1))

@@ -189,3 +189,15 @@ def test_launches_go_to_the_tensors_device(lib, monkeypatch, current):
                                      "nms_relation_buckets_run", "nms_relation_softmax_run",
                                      "nms_relation_softmax_grad_run"]
     assert all(at == 1 and stream == 1001 for _, at, stream in calls) and now[0] == current
+
+
+@pytest.mark.parametrize("batch", [1, 2, 3, 4, 16, 64])
+@pytest.mark.parametrize("heads,queries,keys,nb", [(32, 8192, 8192, 1024), (8, 1000, 1025, 225), (8, 4096, 512, 1024),
+                                                   (16, 3000, 65, 1024), (1, 100, 9000, 32), (4, 5000, 1000, 32)])
+def test_relation_gradient_workspace_stays_beside_the_operands(batch, heads, queries, keys, nb):
+    """The tables of sums take no more than a third of what three 16-bit
+    operands do, beside one wave of tables; one image, or two of long rows,
+    need that wave alone (a table for each of an SM's 16 warps at most)."""
+    wave = 4 * nb * (152 * 4 + heads) + 256
+    room = wave + (0 if batch == 1 or batch < 4 and keys > 1024 else batch * heads * queries * keys * 6 // 3)
+    assert g.nms_relation_grad_workspace_size(batch, heads, queries, keys, nb) <= room
