@@ -220,7 +220,7 @@ static nms_status check_relation(int32_t type, int64_t batch, int32_t heads, int
                                  int64_t sets, int32_t num_buckets, float scale)
 {
     if (!known_type(type) || batch < 0 || heads < 1 || queries < 0 || keys < 0 || num_buckets < 1 ||
-        (sets != 1 && sets != batch) || std::isnan(scale))
+        (sets != 1 && sets != batch) || !std::isfinite(scale))
         return NMS_ERR_INVALID_ARG;
     if (heads > NMS_RELATION_MAX_HEADS || num_buckets > NMS_RELATION_MAX_BUCKETS) return NMS_ERR_CAPACITY;
     const int64_t bh = product(batch, heads, kMostRows), rows = bh < 0 ? -1 : product(bh, queries, kMostRows);

@@ -551,6 +551,8 @@ nms_status nms_relation_buckets_run(const int32_t* q_pos, int64_t q_sets, const 
  *                 pairs too.
  *   key_mask      device uint8 [batch][keys], non-zero where the key takes
  *                 part, or NULL (all do).
+ *   scale         finite (an infinite one would leave no number in masked
+ *                 places).
  * The gradient, from the incoming gradient dprobs and the forward's probs
  * (what stands in masked places changes nothing again):
  *   da = probs * (dprobs - sum_j probs * dprobs), dscores = scale * da (0 for

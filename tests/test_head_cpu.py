@@ -201,3 +201,15 @@ def test_relation_gradient_workspace_stays_beside_the_operands(batch, heads, que
     wave = 4 * nb * (152 * 4 + heads) + 256
     room = wave + (0 if batch == 1 or batch < 4 and keys > 1024 else batch * heads * queries * keys * 6 // 3)
     assert g.nms_relation_grad_workspace_size(batch, heads, queries, keys, nb) <= room
+
+
+@pytest.mark.parametrize("scale", [math.inf, -math.inf, 1e39])
+def test_relation_refuses_an_infinite_scale(scale):
+    """scale * 0 in a masked place has to be 0; 1e39 is infinite in binary32."""
+    f = dict(scores=FAKE, type=g.NMS_TYPE_F16, batch=0, heads=3, queries=4, keys=5, buckets=FAKE, sets=1, table=FAKE,
+             num_buckets=6, key_mask=0, scale=1.0, probs=FAKE, stream=0)
+    assert g.nms_relation_softmax_run(**f) == g.NMS_OK  # no images: nothing is launched
+    assert g.nms_relation_softmax_run(**dict(f, scale=scale)) == BAD
+    b = dict(dprobs=FAKE, probs=FAKE, type=g.NMS_TYPE_F16, batch=2, heads=3, queries=4, keys=5, buckets=FAKE, sets=2,
+             num_buckets=6, key_mask=0, scale=scale, dscores=FAKE, dtable=FAKE, workspace=0, workspace_bytes=0, stream=0)
+    assert g.nms_relation_softmax_grad_run(**b) == BAD
