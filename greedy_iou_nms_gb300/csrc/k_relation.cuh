@@ -223,13 +223,6 @@ struct Valid {
         }
     }
 
-    __device__ __forceinline__ bool operator()(int v, int e) const
-    {
-        const int k = v * S::EV + e;
-        if (S::PACKED) return (m[k / 2] >> (k & 1 ? 16 : 0)) & 1u;
-        return BITS ? (m[0] >> k) & 1u : m[k] != 0;
-    }
-
     // Vector v as binary32, 0 where the pair is masked.
     __device__ __forceinline__ void take(float (&x)[S::EV], const Pack<typename S::T, S::EV>& q, int v) const
     {

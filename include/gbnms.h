@@ -543,7 +543,8 @@ nms_status nms_relation_buckets_run(const int32_t* q_pos, int64_t q_sets, const 
  * A pair is masked when its bucket is outside [0, num_buckets) or its key's
  * mask is 0; a masked pair has weight 0 and its score (NaN and infinities
  * too) changes nothing; a row whose pairs are all masked, or all -inf, is all
- * 0.  A weight below 2^-126 may be 0.
+ * 0.  2^x and 1/x are the hardware's, right to 2^-22 each; a weight below
+ * 2^-126 may be 0.
  *   scores, probs device [batch][heads][queries][keys] of `type`.
  *   buckets       device int16 [sets][queries][keys], sets = 1 (one map for
  *                 all images) or batch.
@@ -554,7 +555,8 @@ nms_status nms_relation_buckets_run(const int32_t* q_pos, int64_t q_sets, const 
  *   scale         finite (an infinite one would leave no number in masked
  *                 places).
  * The gradient, from the incoming gradient dprobs and the forward's probs
- * (what stands in masked places changes nothing again):
+ * (what stands in places masked by bucket or key changes nothing again; at
+ * an entry of -inf the weight is 0 and dprobs has to be finite):
  *   da = probs * (dprobs - sum_j probs * dprobs), dscores = scale * da (0 for
  *   a masked pair), dtable[u][h] = sum of da over the pairs of bucket u
  *   (float [num_buckets][heads], every entry written), summed in a fixed
