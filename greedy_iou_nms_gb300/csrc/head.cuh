@@ -241,6 +241,25 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// A sum of any number of terms: what each addition rounds off is added up
+// beside it (Neumaier, 1974), so that roundings that go one way do not mount.
+struct LongSum {
+    float sum, off;
+    __device__ __forceinline__ void add(float v)
+    {
+        const float t = __fadd_rn(sum, v);
+        off += fabsf(sum) >= fabsf(v) ? (sum - t) + v : (v - t) + sum;
+        sum = t;
+    }
+    __device__ __forceinline__ void add(const LongSum& o)
+    {
+        add(o.sum);
+        off += o.off;
+    }
+    // An infinite sum has left no number in `off`.
+    __device__ __forceinline__ float value() const { return fabsf(off) < INFINITY ? sum + off : sum; }
+};
+
 // --------------------------------------------------------------------- host
 
 // Blocks of so many threads of a kernel that an SM holds.

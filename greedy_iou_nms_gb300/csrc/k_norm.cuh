@@ -662,17 +662,17 @@ constexpr int PARAMS = 8;  // channels of a block that sums dweight and dbias
 // channel, joined in order.
 __device__ __forceinline__ void param_pieces(const NormArgs& a, const NormTile& from, const NormScratch& w, int c0)
 {
-    __shared__ float s_a[NT], s_b[NT];
+    __shared__ LongSum s_a[NT], s_b[NT];
     const int x = static_cast<int>(threadIdx.x) % PARAMS, y = static_cast<int>(threadIdx.x) / PARAMS, c = c0 + x;
-    float va = 0.0f, vb = 0.0f;
+    LongSum va{}, vb{};
     if (c < a.channels) {
         const unsigned items = static_cast<unsigned>(a.batch) * from.pieces, pieces = from.pieces;
         const int g = c / (a.channels / a.groups);
 #pragma unroll 4
         for (unsigned i = y; i < items; i += NT / PARAMS) {
             const int64_t at = static_cast<int64_t>(i) * a.channels + c;
-            va += w.pa[at];
-            vb = fmaf(w.pb[at], a.rstd[static_cast<int64_t>(i / pieces) * a.groups + g], vb);  // u = (x - mean) * rstd
+            va.add(w.pa[at]);
+            vb.add(__fmul_rn(w.pb[at], a.rstd[static_cast<int64_t>(i / pieces) * a.groups + g]));  // u = (x - mean) * rstd
         }
     }
     s_a[threadIdx.x] = va;
@@ -680,25 +680,25 @@ __device__ __forceinline__ void param_pieces(const NormArgs& a, const NormTile& 
     __syncthreads();
     if (y == 0 && c < a.channels) {
         for (int k = 1; k < NT / PARAMS; ++k) {
-            va += s_a[k * PARAMS + x];
-            vb += s_b[k * PARAMS + x];
+            va.add(s_a[k * PARAMS + x]);
+            vb.add(s_b[k * PARAMS + x]);
         }
-        if (a.dbias) a.dbias[c] = va;
-        if (a.dweight) a.dweight[c] = vb;
+        if (a.dbias) a.dbias[c] = va.value();
+        if (a.dweight) a.dweight[c] = vb.value();
     }
 }
 
 // dweight and dbias of channel c: the images' sums, added in order.
 __device__ __forceinline__ void param_sums(const NormArgs& a, const float* ca, const float* cb, int c)
 {
-    float va = 0.0f, vb = 0.0f;
+    LongSum va{}, vb{};
 #pragma unroll 8
     for (int64_t n = 0; n < a.batch; ++n) {
-        va += ca[n * a.channels + c];
-        vb += cb[n * a.channels + c];
+        va.add(ca[n * a.channels + c]);
+        vb.add(cb[n * a.channels + c]);
     }
-    if (a.dbias) a.dbias[c] = va;
-    if (a.dweight) a.dweight[c] = vb;
+    if (a.dbias) a.dbias[c] = va.value();
+    if (a.dweight) a.dweight[c] = vb.value();
 }
 
 static __global__ void __launch_bounds__(NT)

@@ -357,3 +357,22 @@ def test_gelu_from_tail_to_tail(t, groups):
     density_off = (8 + 2 * z * z) * R.EPS
     R.close(y[0, 0], z * cdf, z.abs() * off + R.EPS * (z * cdf).abs())
     R.close(slope, cdf + part, off + part.abs() * density_off + 2 * R.EPS * (cdf + part.abs()))
+
+
+@pytest.mark.parametrize("N,S,C,groups", [(40000, 1, 8, 1), (300000, 1, 8, 1), (1, 3000000, 2, 1), (5000, 3, 24, 3)])
+def test_parameter_gradients_of_many_images(N, S, C, groups):
+    """Terms of one size and sign, whose roundings go one way: their sums are
+    as right as those of a few hundred."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    x = torch.randn(N, S, C, generator=gen, device="cuda")
+    dy = torch.full_like(x, 0.1)
+    _, mean, rstd = g.group_norm_act(x, groups, return_stats=True)
+    dx, dw, db = g.group_norm_act_grad(dy, x, mean, rstd, groups)
+    u = x.double().view(N, S, groups, -1).sub(mean.double()[:, None, :, None]).mul(rstd.double()[:, None, :, None])
+    dz = dy[0, 0, 0].double() * u.view(-1, C)
+    R.close(db, torch.full((C,), float(dy[0, 0, 0].double() * N * S), dtype=torch.float64),
+            256 * R.EPS * float(dy[0, 0, 0]) * N * S)
+    R.close(dw, dz.sum(0).cpu(), 256 * R.EPS * dz.abs().sum(0).cpu())
+    dw = g.group_norm_act_grad(u.view_as(x).float(), x, mean, rstd, groups)[1]  # terms that go along with u
+    square = u.view(-1, C).float().double() * u.view(-1, C)
+    R.close(dw, square.sum(0).cpu(), 256 * R.EPS * square.sum(0).cpu())
