@@ -672,7 +672,8 @@ __device__ __forceinline__ void param_pieces(const NormArgs& a, const NormTile& 
         for (unsigned i = y; i < items; i += NT / PARAMS) {
             const int64_t at = static_cast<int64_t>(i) * a.channels + c;
             va.add(w.pa[at]);
-            vb.add(__fmul_rn(w.pb[at], a.rstd[static_cast<int64_t>(i / pieces) * a.groups + g]));  // u = (x - mean) * rstd
+            // u = (x - mean) * rstd
+            vb.add(__fmul_rn(w.pb[at], a.rstd[static_cast<int64_t>(i / pieces) * a.groups + g]));
         }
     }
     s_a[threadIdx.x] = va;
@@ -688,17 +689,16 @@ __device__ __forceinline__ void param_pieces(const NormArgs& a, const NormTile& 
     }
 }
 
-// dweight and dbias of channel c: the images' sums, added in order.
+// dweight and dbias of channel c: the sums of at most 16 images, added in order.
 __device__ __forceinline__ void param_sums(const NormArgs& a, const float* ca, const float* cb, int c)
 {
-    LongSum va{}, vb{};
-#pragma unroll 8
+    float va = 0.0f, vb = 0.0f;
     for (int64_t n = 0; n < a.batch; ++n) {
-        va.add(ca[n * a.channels + c]);
-        vb.add(cb[n * a.channels + c]);
+        va += ca[n * a.channels + c];
+        vb += cb[n * a.channels + c];
     }
-    if (a.dbias) a.dbias[c] = va.value();
-    if (a.dweight) a.dweight[c] = vb.value();
+    if (a.dbias) a.dbias[c] = va;
+    if (a.dweight) a.dweight[c] = vb;
 }
 
 static __global__ void __launch_bounds__(NT)
@@ -1357,12 +1357,17 @@ template <typename T, int V>
 static bool norm_in_clusters(const NormArgs& a, void* ws, cudaStream_t st, bool grad)
 {
     const int e = sizeof(T), D = a.channels / a.groups, vecs = a.channels / V;
-    // One launch and one reading where latency counts; beyond these sizes streaming is faster.  bf16, 256 channels in
-    // 32 groups, cluster and streaming: forward 1 x 400 pixels 5.8 and 6.9 us, 16 x 400 7.2 and 9.0, 4 x 1600 8.5 and
-    // 11.9, 1 x 6400 11.7 and 9.0, 16 x 1600 15.9 and 14.6; backward 1 x 400 5.9 and 8.6, 4 x 400 7.2 and 8.8,
-    // 16 x 400 13.6 and 10.7, 16 x 1600 38 and 23.
+    // One launch and one reading where latency counts; beyond these sizes streaming is faster.  Us, in clusters and
+    // streamed:
+    //   forward, 256 channels bf16   1 x 400 pixels 5.7 and 7.0, 1 x 1600 7.4 and 9.5, 1 x 4000 9.4 and 8.1,
+    //                                16 x 400 6.9 and 9.1, 16 x 1600 15.6 and 15.0
+    //            256 fp32            1 x 400 5.6 and 7.7, 4 x 400 5.8 and 7.8, 1 x 4000 8.1 and 8.8
+    //            90, groups of 15    1 x 400 fp32 5.9 and 6.6, 4 x 1600 fp32 7.0 and 8.2, 1 x 1600 bf16 9.1 and 7.6
+    //   backward, 256 bf16           1 x 400 5.0 and 8.6, 4 x 400 6.1 and 8.6, 16 x 100 6.4 and 7.9, 16 x 400 13.9 and
+    //                                10.7, 64 x 10 29 and 6.8
+    //            64 fp16             1 x 400 4.2 and 5.5, 4 x 400 5.1 and 5.6, 16 x 100 7.0 and 5.5
     const double size = static_cast<double>(a.batch) * a.pixels * a.channels * e;
-    if (grad ? size > 1.5e6 : size > 4e6 || a.pixels > 4096) return false;
+    if (grad ? size > 1.5e6 || a.batch > (a.channels < 256 ? 4 : 16) : size > 4e6 || a.pixels > 2048) return false;
     int whole = 1;  // vectors that hold whole groups: lcm(D, V) / V
     while (whole * V % D != 0) ++whole;
     const int pass = NT * V * (grad ? e + 4 : e);  // bytes that a pass over the block's rows keeps
@@ -1382,7 +1387,10 @@ static bool norm_in_clusters(const NormArgs& a, void* ws, cudaStream_t st, bool 
                 return passes > ctas * most || (passes > ctas * 2 && a.batch * t.tiles * ctas * 2 <= SMS);
             };
             for (t.ctas = 1; t.ctas < 8 && more(t.ctas); t.ctas *= 2) {}
-            if (passes > static_cast<int64_t>(t.ctas) * most || a.batch * t.tiles * t.ctas > INT32_MAX) continue;
+            if (passes > static_cast<int64_t>(t.ctas) * most) continue;
+            // Many images of little work each: some 6 ns a block, where streaming takes 17 an image (1000 x 4 pixels bf16:
+            // 256 channels, eight blocks an image, 50 us and 17; 90, two, 13 and 17).
+            if (a.batch * t.tiles * t.ctas > 4 * SMS && t.tiles * t.ctas > 2) return false;
             t.held = static_cast<int>((passes + t.ctas - 1) / t.ctas);
             t.rows = t.held * step;
             const int CW = t.wide * V;

@@ -376,3 +376,11 @@ def test_parameter_gradients_of_many_images(N, S, C, groups):
     dw = g.group_norm_act_grad(u.view_as(x).float(), x, mean, rstd, groups)[1]  # terms that go along with u
     square = u.view(-1, C).float().double() * u.view(-1, C)
     R.close(dw, square.sum(0).cpu(), 256 * R.EPS * square.sum(0).cpu())
+
+
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N,S,C,groups", [(4, 100, 64, 8), (5, 100, 64, 8), (16, 40, 256, 32), (17, 40, 256, 32),
+                                          (1, 2048, 64, 8), (1, 2049, 64, 8), (76, 4, 256, 32), (77, 4, 256, 32),
+                                          (700, 3, 48, 3), (3, 400, 90, 6)])
+def test_both_sides_of_the_cluster_sizes(t, N, S, C, groups):
+    _check(*_inputs(N * S, N, S, C, t), groups, "silu")
