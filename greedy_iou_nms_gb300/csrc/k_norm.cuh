@@ -284,8 +284,9 @@ struct Moments {
 
 // (mean, squared deviations) of each row piece by column: a vector (ONE: its
 // channels are of one group) or a channel.  Three operations a value; four
-// rows' loads in flight a thread, 32 warps an SM.  16 x 6400 x 256 bf16: 10 us,
-// 5.0 TB/s; the block's ramps (a first load, the join) are a third of it.
+// rows' loads in flight a thread, 32 warps an SM (24 where eight channels'
+// moments are kept).  16 x 6400 x 256 bf16: 13 us under the profiler, 4.0 TB/s;
+// the block's ramps (a first load, the join) are a third of it.
 template <typename T, int V, bool ONE>
 __global__ void __launch_bounds__(NT, ONE || V < 8 ? 4 : 3)
 norm_partial_kernel(NormArgs a, NormTile t, NormScratch w)
@@ -462,8 +463,8 @@ __device__ __forceinline__ void load_joined(const NormArgs& a, const Spot& p, co
     __syncthreads();
 }
 
-// The results.  16 x 6400 x 256 bf16, silu: 19 us for 52 MB from L2 and as much
-// written; the sigmoid's two hardware functions a value take 11 us of their
+// The results.  16 x 6400 x 256 bf16, silu: 21 us of the two launches' 34, for 52
+// MB read again and as much written; the sigmoid's two hardware functions a value take 11 us of their
 // pipe, and three blocks an SM (80 registers) hide what latency they can.
 template <typename T, int V, bool ONE, int ACT>
 __global__ void __launch_bounds__(NT, 3)
@@ -537,9 +538,9 @@ __device__ __forceinline__ void slope_row(const NormArgs& a, const float (&mean)
 }
 
 // Sums by channel of dz and dz * (x - mean) of each row piece.  16 x 1600 x 256
-// bf16, silu: 11 us, latency (seven rows a thread).  8 x 25600 x 128 fp16,
-// gelu and dropout: 40 us, 36 instructions a value at 16 warps an SM; two values
-// an instruction changed nothing.
+// bf16, silu: 14 us under the profiler, latency (seven rows a thread).  8 x 25600
+// x 128 fp16, gelu and dropout: 41 us, 35 instructions a value at 16 warps an SM;
+// two values an instruction changed nothing.
 template <typename T, int V, bool ONE, int ACT>
 __global__ void __launch_bounds__(NT, ONE ? 3 : 2)
 norm_grad_partial_kernel(NormArgs a, NormTile t, NormScratch w)
@@ -710,8 +711,8 @@ norm_grad_param_kernel(NormArgs a, NormScratch w)
 }
 
 // dx; the blocks past the pieces' (the first to run) write dweight and dbias.
-// dz is worked out again: keeping it would move 8 bytes a value more.  13 us
-// and 44 us at the sizes above.
+// dz is worked out again: keeping it would move 8 bytes a value more.  17 us and
+// 50 us under the profiler at the sizes above, 25 and 85 for both launches without.
 template <typename T, int V, bool ONE, int ACT>
 __global__ void __launch_bounds__(NT, ONE ? 3 : 2)
 norm_grad_apply_kernel(NormArgs a, NormTile t, NormTile from, NormScratch w, bool joined)

@@ -23,10 +23,10 @@
 // queries, since its sums by bucket are per head.
 //
 // Measured (us; TB/s of what has to move): weights 2304 x 8 x 49 x 49 fp16, one
-// map, 49 (3.6), issue: 27 instructions a pair; 16 x 8 x 1000 x 1000 bf16, a map
-// by image, 103 (5.3); 4 x 8 x 2000 x 2000 fp32 172 (6.2).  Gradient 1600 x 8 x
-// 64 x 64 fp16, one map, 72 (4.4); 16 x 8 x 1000 x 1000 bf16, 225 buckets, a map
-// by image, 215 (3.7), latency: 12 warps an SM beside their tables of sums.
+// map, 47 (3.8), issue: 27 instructions a place; 16 x 8 x 1000 x 1000 bf16, a map
+// by image, 104 (5.2); 4 x 8 x 2000 x 2000 fp32 187 (5.6).  Gradient 1600 x 8 x
+// 64 x 64 fp16, one map, 69 (4.6); 16 x 8 x 1000 x 1000 bf16, 225 buckets, a map
+// by image, 218 (3.7), latency: 12 warps an SM beside their tables of sums.
 // Odd lengths above 128 keys go element by element and take twice as long.
 #pragma once
 
@@ -484,7 +484,9 @@ relation_softmax_kernel(RelationArgs a, unsigned per)
 }
 
 // Rows longer than a block holds: one block a row, twice over the keys, the
-// first time with a running maximum and sum.
+// first time with a running maximum and sum.  4 x 8 x 100 x 9000 bf16: 126 us,
+// 1.0 TB/s, element by element; a row is not split, so few of them leave SMs idle
+// (eight of a million keys: 3 ms).
 template <typename T>
 __global__ void __launch_bounds__(256)
 relation_softmax_long_kernel(RelationArgs a, int64_t rows)
@@ -812,7 +814,8 @@ relation_grad_head_kernel(RelationArgs a, int columns, float* part)
     join_columns(hist, warps, columns, nb, part + (static_cast<int64_t>(head) * gridDim.x + blockIdx.x) * nb);
 }
 
-// Rows longer than a block holds: one warp a row, twice over the keys.
+// Rows longer than a block holds: one warp a row, twice over the keys.  4 x 8 x
+// 100 x 9000 bf16: 285 us; eight rows of a million keys 20 ms.
 template <typename T>
 __global__ void __launch_bounds__(256)
 relation_grad_long_kernel(RelationArgs a, int columns, float* part)
