@@ -10,9 +10,9 @@ greedy_iou_nms_gb300.autograd has the same operators for torch's autograd.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import functools
-import math
 
 NMS_TYPE_F32 = 0
 NMS_TYPE_F16 = 1
@@ -354,10 +354,19 @@ def relation_lut_log(num_buckets: int, max_distance: int, *, ahead: str = "mirro
         raise ValueError("relation_lut_log: num_buckets >= 2, max_distance >= num_buckets // 2, ahead one of "
                          "'mirror', 'own', 'mask'")
     exact = num_buckets // 2
-    parts = []
-    for d in range(max_distance + 1):
-        far = math.log(d / exact) / math.log(max_distance / exact) if exact < d < max_distance else float(d >= max_distance)
-        parts.append(d if d < exact else min(num_buckets - 1, exact + int(far * (num_buckets - exact))))
+    span = num_buckets - exact
+    # The first distance of bucket exact + k: (d / exact)^span >= (max_distance / exact)^k, settled in whole numbers (a
+    # logarithm's rounding puts distances on a boundary into the bucket before).
+    firsts = []
+    for k in range(1, span):
+        least = max_distance ** k * exact ** (span - k)
+        d = max(exact, int(exact * (max_distance / exact) ** (k / span)))
+        while d ** span < least:
+            d += 1
+        while d > exact and (d - 1) ** span >= least:
+            d -= 1
+        firsts.append(d)
+    parts = [d if d < exact else exact + bisect.bisect_right(firsts, d) for d in range(max_distance + 1)]
     front = {"mirror": parts, "own": [num_buckets + b for b in parts], "mask": [-1] * len(parts)}[ahead]
     return _torch().tensor([parts[:0:-1] + [parts[0]] + front[1:]], dtype=_torch().int32)
 

@@ -213,3 +213,24 @@ def test_relation_refuses_an_infinite_scale(scale):
     b = dict(dprobs=FAKE, probs=FAKE, type=g.NMS_TYPE_F16, batch=2, heads=3, queries=4, keys=5, buckets=FAKE, sets=2,
              num_buckets=6, key_mask=0, scale=scale, dscores=FAKE, dtable=FAKE, workspace=0, workspace_bytes=0, stream=0)
     assert g.nms_relation_softmax_grad_run(**b) == BAD
+
+
+@pytest.mark.parametrize("num_buckets,max_distance", [(9, 128), (10, 160), (19, 288), (39, 608), (2, 1), (3, 1),
+                                                      (8, 4), (7, 50), (32, 128), (33, 1000)])
+def test_logarithmic_table_on_its_boundaries(num_buckets, max_distance):
+    """Against whole numbers: bucket exact + k from (d / exact)^span >= (max /
+    exact)^k on, distances that meet it with equality among them."""
+    exact = num_buckets // 2
+    span = num_buckets - exact
+    back = g.relation_lut_log(num_buckets, max_distance)[0].tolist()[max_distance:]
+    for d, bucket in enumerate(back):
+        if d < exact:
+            assert bucket == d
+            continue
+        k = max(k for k in range(span) if d ** span * exact ** k >= max_distance ** k * exact ** span)
+        assert bucket == exact + k, d
+
+
+def test_logarithmic_table_of_the_largest_sizes():
+    back = g.relation_lut_log(1024, 1 << 20)[0][1 << 20:]
+    assert (back[1:] >= back[:-1]).all() and back[511] == 511 and back[-1] == 1023
