@@ -222,9 +222,8 @@ def lane_nms(props, scores, dist_thr: float, *, max_out: int = 0):
     count = torch.empty(1, dtype=torch.int64, device=props.device)
     wsb = nms_lane_workspace_size(n)
     ws = torch.empty(max(wsb, 256), dtype=torch.uint8, device=props.device)
-    st = nms_lane_run(props.data_ptr() if n else 0, scores.data_ptr() if n else 0, n, dist_thr, max_out,
-                      keep.data_ptr(), cap, count.data_ptr(), 0, ws.data_ptr(), wsb,
-                      torch.cuda.current_stream(props.device).cuda_stream)
+    st = head._launch(props, nms_lane_run, props.data_ptr() if n else 0, scores.data_ptr() if n else 0, n, dist_thr,
+                      max_out, keep.data_ptr(), cap, count.data_ptr(), 0, ws.data_ptr(), wsb)
     if st != NMS_OK:
         raise NmsError(st, "nms_lane_run")
     return keep[: int(count.item())]
@@ -250,11 +249,10 @@ def matrix_nms(boxes, scores, decay_thr: float, *, sigma: float = 0.5, decay: st
     count = torch.empty(1, dtype=torch.int64, device=dev)
     ws_bytes = nms_matrix_workspace_size(n)
     ws = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=dev)
-    st = nms_matrix_run(boxes.data_ptr() if n else 0, scores.data_ptr() if n else 0, n,
-                        NMS_DECAY_LINEAR if decay == "linear" else NMS_DECAY_GAUSSIAN, sigma,
-                        -math.inf if score_thr is None else score_thr, decay_thr, max_out, keep.data_ptr(),
-                        ks.data_ptr(), cap, count.data_ptr(), 0, ws.data_ptr(), ws_bytes,
-                        torch.cuda.current_stream(dev).cuda_stream)
+    st = head._launch(boxes, nms_matrix_run, boxes.data_ptr() if n else 0, scores.data_ptr() if n else 0, n,
+                      NMS_DECAY_LINEAR if decay == "linear" else NMS_DECAY_GAUSSIAN, sigma,
+                      -math.inf if score_thr is None else score_thr, decay_thr, max_out, keep.data_ptr(),
+                      ks.data_ptr(), cap, count.data_ptr(), 0, ws.data_ptr(), ws_bytes)
     if st != NMS_OK:
         raise NmsError(st, "nms_matrix_run")
     k = int(count.item())
@@ -368,10 +366,10 @@ def nms(boxes, scores, iou_thr: float, *, class_ids=None, num_classes: Optional[
     counts = torch.empty(max(B, 1), dtype=torch.int64, device=dev)
     status = torch.empty(1, dtype=torch.int32, device=dev)
     ws = workspace if workspace is not None else Workspace(n, B, C, device=dev)
-    st = (nms_fast_run if fast else nms_run)(boxes.data_ptr() if n else 0, scores.data_ptr() if n else 0, n, cls_ptr, C,
-                 off_ptr, B, iou_thr, -math.inf if score_thr is None else score_thr, max_out,
-                 keep.data_ptr(), cap, counts.data_ptr(), status.data_ptr(), ws.ptr, ws.bytes,
-                 torch.cuda.current_stream(dev).cuda_stream)
+    st = head._launch(boxes, nms_fast_run if fast else nms_run, boxes.data_ptr() if n else 0,
+                      scores.data_ptr() if n else 0, n, cls_ptr, C, off_ptr, B, iou_thr,
+                      -math.inf if score_thr is None else score_thr, max_out, keep.data_ptr(), cap, counts.data_ptr(),
+                      status.data_ptr(), ws.ptr, ws.bytes)
     if st != NMS_OK:
         raise NmsError(st, "nms_run")
     cnt = counts.cpu()
@@ -422,6 +420,7 @@ class HostPipeline:
         self._graphs = {}
         self._d_in = torch.empty(5 * self.n_max + 4, dtype=torch.float32, device=self.device)
         self._in_addr = self._d_in.data_ptr()
+        self.device = self._d_in.device  # with its index, whichever device is current later
         self.zero_copy = False
         if zero_copy:
             din, dout = nms_mapped_pointer(self._h_in.data_ptr()), nms_mapped_pointer(self._h_out.data_ptr())
@@ -485,6 +484,9 @@ class HostPipeline:
         """Enqueue one call on the current stream (the captured graph) without
         waiting; ``result`` waits and returns the kept indices."""
         torch = _torch()
+        if torch.cuda.current_device() != self.device.index:  # kernels and graphs go to the current device
+            with torch.cuda.device(self.device):
+                return self.launch(iou_thr, score_thr, max_out)
         key = (self.n, float(iou_thr), score_thr, int(max_out))
         graph = self._graphs.get(key)
         if graph is None:
@@ -518,8 +520,8 @@ def iou_mask(boxes_sorted, iou_thr: float):
     n = boxes_sorted.shape[0]
     ldw = nms_mask_row_words(n)
     mask = torch.zeros((n, max(ldw, 1)), dtype=torch.int64, device=boxes_sorted.device)
-    st = nms_iou_mask(boxes_sorted.data_ptr() if n else 0, n, iou_thr, mask.data_ptr(),
-                      mask.numel(), torch.cuda.current_stream(boxes_sorted.device).cuda_stream)
+    st = head._launch(boxes_sorted, nms_iou_mask, boxes_sorted.data_ptr() if n else 0, n, iou_thr, mask.data_ptr(),
+                      mask.numel())
     if st != NMS_OK:
         raise NmsError(st, "nms_iou_mask")
     return mask[:, :ldw]
@@ -535,9 +537,9 @@ def resolve_mask(mask, max_out: int = 0, perm=None, workspace: Optional[Workspac
     if perm is not None:
         perm = perm.to(device=mask.device, dtype=torch.int32).contiguous()
     ws = workspace if workspace is not None else Workspace(n, device=mask.device)
-    st = nms_resolve_mask(mask.data_ptr() if n else 0, n, perm.data_ptr() if perm is not None else 0,
-                          max_out, keep.data_ptr(), count.data_ptr(), ws.ptr, ws.bytes,
-                          torch.cuda.current_stream(mask.device).cuda_stream)
+    st = head._launch(mask, nms_resolve_mask, mask.data_ptr() if n else 0, n,
+                      perm.data_ptr() if perm is not None else 0, max_out, keep.data_ptr(), count.data_ptr(), ws.ptr,
+                      ws.bytes)
     if st != NMS_OK:
         raise NmsError(st, "nms_resolve_mask")
     return keep[: int(count.item())]
@@ -591,8 +593,8 @@ def decode_boxes7(preds, conf_thr: float, max_objects: int):
     wsb = nms_decode_workspace_size(batch, anchors)
     ws = torch.empty(max(wsb, 256), dtype=torch.uint8, device=dev)
     status = torch.zeros(1, dtype=torch.int32, device=dev)
-    st = nms_decode_boxes7(preds.data_ptr(), batch, anchors, width - 5, conf_thr, max_objects, out.data_ptr(),
-                           status.data_ptr(), ws.data_ptr(), wsb, torch.cuda.current_stream(dev).cuda_stream)
+    st = head._launch(preds, nms_decode_boxes7, preds.data_ptr(), batch, anchors, width - 5, conf_thr, max_objects,
+                      out.data_ptr(), status.data_ptr(), ws.data_ptr(), wsb)
     if st != NMS_OK:
         raise NmsError(st, "nms_decode_boxes7")
     dst = int(status.item())
@@ -616,8 +618,8 @@ def boxes7_nms(buffers, num_classes: int, iou_thr: float, *, fast: bool = False)
     wsb = nms_boxes7_workspace_size(batch, max_objects, num_classes)
     ws = torch.empty(max(wsb, 256), dtype=torch.uint8, device=dev)
     status = torch.zeros(1, dtype=torch.int32, device=dev)
-    st = nms_boxes7_run(buffers.data_ptr(), batch, max_objects, num_classes, iou_thr, 1 if fast else 0,
-                        status.data_ptr(), ws.data_ptr(), wsb, torch.cuda.current_stream(dev).cuda_stream)
+    st = head._launch(buffers, nms_boxes7_run, buffers.data_ptr(), batch, max_objects, num_classes, iou_thr,
+                      1 if fast else 0, status.data_ptr(), ws.data_ptr(), wsb)
     if st != NMS_OK:
         raise NmsError(st, "nms_boxes7_run")
     dst = int(status.item())

@@ -179,7 +179,7 @@ def _stream(x) -> int:
 def _launch(x, entry, *args) -> int:
     """entry(*args, the current stream of x's device), that device current:
     a launch goes to the current one."""
-    cuda, at = _torch_module.cuda, x.get_device()
+    cuda, at = _torch().cuda, x.get_device()
     if cuda.current_device() == at:
         return entry(*args, _stream(x))
     with cuda.device(at):

@@ -234,3 +234,47 @@ def test_logarithmic_table_on_its_boundaries(num_buckets, max_distance):
 def test_logarithmic_table_of_the_largest_sizes():
     back = g.relation_lut_log(1024, 1 << 20)[0][1 << 20:]
     assert (back[1:] >= back[:-1]).all() and back[511] == 511 and back[-1] == 1023
+
+
+def test_the_suppressions_launches_too(lib, monkeypatch):
+    """The same of the tensor functions of the suppression and the decode."""
+    from greedy_iou_nms_gb300 import head
+    head._torch()
+    now, calls = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *_):
+            now[0] = self.before
+
+    class Recorder:
+        def __getattr__(self, name):
+            if not (name.endswith("_run") or name in ("nms_iou_mask", "nms_resolve_mask", "nms_decode_boxes7")):
+                return getattr(lib, name)
+            return lambda *args: calls.append((name, now[0], args[-1])) or 0
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch, "empty", torch.zeros)  # counts and statuses that no kernel writes
+    monkeypatch.setattr(head, "_raw_stream", lambda index: 1000 + index)
+    monkeypatch.setattr(g, "_lib", Recorder())
+
+    def on(*shape):
+        return torch.zeros(*shape).as_subclass(OnSecond)
+
+    g.nms(on(8, 4), on(8), 0.5)
+    g.nms(on(8, 4), on(8), 0.5, fast=True)
+    g.matrix_nms(on(8, 4), on(8), 0.1)
+    g.lane_nms(on(8, 77), on(8), 0.5)
+    g.iou_mask(on(8, 4), 0.5)
+    g.resolve_mask(torch.zeros(8, 2, dtype=torch.int64).as_subclass(OnSecond))
+    g.decode_boxes7(on(2, 9, 7), 0.3, 5)
+    g.boxes7_nms(on(2, 36), 2, 0.5)
+    assert [c[0] for c in calls] == ["nms_run", "nms_fast_run", "nms_matrix_run", "nms_lane_run", "nms_iou_mask",
+                                     "nms_resolve_mask", "nms_decode_boxes7", "nms_boxes7_run"]
+    assert all(at == 1 and stream == 1001 for _, at, stream in calls) and now[0] == 0
