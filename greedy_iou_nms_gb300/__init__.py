@@ -17,7 +17,12 @@ import math
 import os
 from typing import Optional
 
-from . import head
+from . import block, head
+from .block import (NMS_LAYER_MAX_WIDTH, NMS_LINEAR_MAX_WIDTH, NMS_POSITION_I32, NMS_ROTARY_MAX_AXES,  # noqa: F401
+                    NMS_ROTARY_MAX_DIM, layer_norm, layer_norm_grad, linear_act, linear_act_grad,
+                    nms_layer_norm_grad_run, nms_layer_norm_run, nms_layer_norm_workspace_size, nms_linear_grad_run,
+                    nms_linear_grad_workspace_size, nms_linear_run, nms_linear_workspace_size, nms_rotary_run, rotary,
+                    rotary_grad, rotary_lut)
 from .head import (NMS_ACT_GELU, NMS_ACT_NONE, NMS_ACT_RELU, NMS_ACT_SILU, NMS_NORM_MAX_BATCH,  # noqa: F401
                    NMS_NORM_MAX_CHANNELS, NMS_NORM_MAX_PIXELS, NMS_RELATION_MAX_AXES, NMS_RELATION_MAX_BUCKETS,
                    NMS_RELATION_MAX_HEADS, NMS_RELATION_MAX_REACH, NMS_TYPE_BF16, NMS_TYPE_F16, NMS_TYPE_F32, dropout,
@@ -43,7 +48,7 @@ EXPORTED = ("nms_status_string", "nms_workspace_size", "nms_run", "nms_fast_run"
             "nms_matrix_workspace_size", "nms_matrix_run", "nms_mask_row_words", "nms_iou_mask",
             "nms_resolve_mask", "nms_resolve_mask_noalloc", "nms_decode_workspace_size", "nms_decode_boxes7",
             "nms_boxes7_workspace_size", "nms_boxes7_run", "nms_mapped_pointer", "nms_copy", "nms_lane_workspace_size",
-            "nms_lane_run") + head.EXPORTED
+            "nms_lane_run") + head.EXPORTED + block.EXPORTED
 NMS_NOALLOC_MAX_N = 16384
 NMS_LANE_VALUES = 77  # values of one lane candidate (nms_lane_run)
 NMS_LANE_ROWS = 72
@@ -116,6 +121,7 @@ def load():
     lib.nms_lane_run.argtypes = [vp, vp, i64, f32, i32, vp, i64, vp, vp, vp, sz, vp]
     lib.nms_lane_run.restype = ctypes.c_int
     head.declare(lib)
+    block.declare(lib)
     _lib = lib
     return lib
 

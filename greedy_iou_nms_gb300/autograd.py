@@ -1,4 +1,5 @@
-"""The detection-head operators for torch's autograd.
+"""The operators of a detection head and of a transformer block among its
+candidates for torch's autograd.
 
 Functions of the names and arguments of greedy_iou_nms_gb300 whose results
 carry gradients, each by the library's own gradient kernels; nothing but what
@@ -10,7 +11,7 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import head
+from . import block, head
 
 
 class _GroupNormAct(torch.autograd.Function):
@@ -63,6 +64,60 @@ class _RelationSoftmax(torch.autograd.Function):
         return dscores, dtable.to(ctx.table_type), None, None, None
 
 
+class _LinearAct(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, act, residual):
+        keep = act != "none" and any(ctx.needs_input_grad[:3])
+        out = block.linear_act(x, weight, bias, act=act, residual=residual, return_pre=keep)
+        y, pre = out if keep else (out, None)
+        ctx.save_for_backward(x, weight, pre)
+        ctx.act, ctx.bias_type = act, None if bias is None else bias.dtype
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, pre = ctx.saved_tensors
+        dx, dweight, dbias = block.linear_act_grad(dy, x, weight, pre, act=ctx.act, need=ctx.needs_input_grad[:3]) \
+            if any(ctx.needs_input_grad[:3]) else (None, None, None)
+        return dx, dweight, None if dbias is None else dbias.to(ctx.bias_type), None, \
+            dy if ctx.needs_input_grad[4] else None
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, residual):
+        out = block.layer_norm(x, weight, bias, eps=eps, residual=residual, return_stats=True)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x if residual is None else out[1], weight, *out[-2:])
+        ctx.bias_type = None if bias is None else bias.dtype
+        return out[0] if residual is None else out[:2]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dsum=None):
+        rows, weight, mean, rstd = ctx.saved_tensors
+        if dy is None:
+            return dsum, None, None, None, dsum if ctx.needs_input_grad[4] else None
+        dx, dweight, dbias = block.layer_norm_grad(dy, rows, mean, rstd, weight, dsum=dsum)
+        return (dx, None if weight is None else dweight.to(weight.dtype),
+                None if ctx.bias_type is None else dbias.to(ctx.bias_type), None, dx if ctx.needs_input_grad[4] else None)
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, positions, lut, halves):
+        ctx.save_for_backward(positions, lut)
+        ctx.halves = halves
+        return block.rotary(x, positions, lut, halves=halves)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        positions, lut = ctx.saved_tensors
+        return block.rotary_grad(dy, positions, lut, halves=ctx.halves), None, None, None
+
+
 def group_norm_act(x, groups: int, weight=None, bias=None, *, eps: float = 1e-5, act: str = "none", p: float = 0.0,
                    seed: int = 0, offset: int = 0):
     """`greedy_iou_nms_gb300.group_norm_act` with gradients to x, weight and bias."""
@@ -77,3 +132,19 @@ def dropout(x, p: float, seed: int, offset: int = 0, *, residual=None):
 def relation_softmax(scores, table, buckets, *, scale: float = 1.0, key_mask=None):
     """`greedy_iou_nms_gb300.relation_softmax` with gradients to the scores and the table."""
     return _RelationSoftmax.apply(scores, table, buckets, scale, key_mask)
+
+
+def linear_act(x, weight, bias=None, *, act: str = "none", residual=None):
+    """`greedy_iou_nms_gb300.linear_act` with gradients to x, weight, bias and the residual."""
+    return _LinearAct.apply(x, weight, bias, act, residual)
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, residual=None):
+    """`greedy_iou_nms_gb300.layer_norm` (y, or (y, sum) with a residual) with gradients to x, weight, bias and the
+    residual."""
+    return _LayerNorm.apply(x, weight, bias, eps, residual)
+
+
+def rotary(x, positions, lut, *, halves: bool = True):
+    """`greedy_iou_nms_gb300.rotary` with the gradient to x."""
+    return _Rotary.apply(x, positions, lut, halves)

@@ -1,0 +1,312 @@
+// The C entry points of a transformer block's operators: linear layer, layer
+// normalisation and rotary positions.  Argument checks and launches; no host
+// synchronisation, no allocation.
+#include <cmath>
+#include <cstdint>
+
+#include "block.h"
+#include "common.cuh"
+
+using namespace gbnms;
+
+namespace {
+
+bool misaligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+nms_status cuda_status() { return cudaGetLastError() == cudaSuccess ? NMS_OK : NMS_ERR_CUDA; }
+
+bool known_type(int32_t t) { return t == NMS_TYPE_F32 || t == NMS_TYPE_F16 || t == NMS_TYPE_BF16; }
+
+uintptr_t type_bytes(int32_t t) { return t == NMS_TYPE_F32 ? 4 : 2; }
+
+constexpr int64_t kMostElements = int64_t(1) << 38;
+constexpr int64_t kMostRows = INT32_MAX;
+
+// Whether n rows at a stride reach beyond kMostElements.
+bool too_far(int64_t n, int64_t stride) { return n > 0 && stride > kMostElements / n; }
+
+size_t round_up(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
+int64_t padded(int64_t width) { return (width + 7) / 8 * 8; }
+
+nms_status check_linear(int32_t type, int64_t rows, int32_t inner, int32_t outer)
+{
+    if (!known_type(type) || rows < 0 || inner < 1 || outer < 1) return NMS_ERR_INVALID_ARG;
+    if (inner > NMS_LINEAR_MAX_WIDTH || outer > NMS_LINEAR_MAX_WIDTH || rows > kMostRows || too_far(rows, inner) ||
+        too_far(rows, outer) || too_far(outer, inner))
+        return NMS_ERR_CAPACITY;
+    return NMS_OK;
+}
+
+bool bad_row(int64_t row, int64_t rows) { return row < 0 || too_far(rows, row); }
+
+}  // namespace
+
+extern "C" nms_status nms_linear_workspace_size(int32_t type, int64_t rows, int32_t inner, int32_t outer,
+                                                int32_t aligned, size_t* bytes)
+{
+    if (!bytes) return NMS_ERR_INVALID_ARG;
+    const nms_status s = check_linear(type, rows, inner, outer);
+    if (s != NMS_OK) return s;
+    (void)aligned;
+    *bytes = 0;
+    return NMS_OK;
+}
+
+extern "C" nms_status nms_linear_run(const void* x, int64_t x_row, int32_t type, int64_t rows, int32_t inner,
+                                     const void* weight, int64_t weight_row, int32_t outer, const void* bias,
+                                     int32_t bias_type, int32_t act, const void* residual, int64_t residual_row,
+                                     void* y, void* pre, int32_t* dev_status, void* workspace, size_t workspace_bytes,
+                                     void* stream)
+{
+    const nms_status s = check_linear(type, rows, inner, outer);
+    if (s != NMS_OK) return s;
+    if ((bias_type != NMS_TYPE_F32 && bias_type != type) || act < NMS_ACT_NONE || act > NMS_ACT_GELU)
+        return NMS_ERR_INVALID_ARG;
+    if (bad_row(x_row, rows) || bad_row(weight_row, outer) || bad_row(residual_row, rows)) return NMS_ERR_INVALID_ARG;
+    if (misaligned(bias, type_bytes(bias_type)) || misaligned(dev_status, 4)) return NMS_ERR_INVALID_ARG;
+    if (rows == 0) return NMS_OK;
+    const uintptr_t e = type_bytes(type);
+    if (!x || !weight || !y || misaligned(x, e) || misaligned(weight, e) || misaligned(y, e) || misaligned(pre, e) ||
+        misaligned(residual, e))
+        return NMS_ERR_INVALID_ARG;
+    (void)workspace;
+    (void)workspace_bytes;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaGetLastError();
+    ProductArgs p{};
+    p.a = x;
+    p.a_row = x_row;
+    p.b = weight;
+    p.b_row = weight_row;
+    p.type = type;
+    p.m = rows;
+    p.n = outer;
+    p.k = inner;
+    p.bias = bias;
+    p.bias_f32 = bias_type == NMS_TYPE_F32;
+    p.act = act;
+    p.residual = residual;
+    p.residual_row = residual ? residual_row : 0;
+    p.out = y;
+    p.pre = pre;
+    p.status = dev_status;
+    launch_product(p, st);
+    return cuda_status();
+}
+
+extern "C" nms_status nms_linear_grad_workspace_size(int32_t type, int64_t rows, int32_t inner, int32_t outer,
+                                                     int32_t aligned, size_t* bytes)
+{
+    if (!bytes) return NMS_ERR_INVALID_ARG;
+    const nms_status s = check_linear(type, rows, inner, outer);
+    if (s != NMS_OK) return s;
+    *bytes = 0;
+    if (rows == 0) return NMS_OK;
+    *bytes = round_up(type_bytes(type) * rows * padded(outer)) + round_up(slope_workspace_bytes(rows, outer));
+    (void)aligned;
+    return NMS_OK;
+}
+
+extern "C" nms_status nms_linear_grad_run(const void* dy, int64_t dy_row, const void* x, int64_t x_row, int32_t type,
+                                          int64_t rows, int32_t inner, const void* weight, int64_t weight_row,
+                                          int32_t outer, const void* pre, int32_t act, void* dx, void* dweight,
+                                          float* dbias, int32_t* dev_status, void* workspace, size_t workspace_bytes,
+                                          void* stream)
+{
+    const nms_status s = check_linear(type, rows, inner, outer);
+    if (s != NMS_OK) return s;
+    if (act < NMS_ACT_NONE || act > NMS_ACT_GELU) return NMS_ERR_INVALID_ARG;
+    if (bad_row(dy_row, rows) || bad_row(x_row, rows) || bad_row(weight_row, outer)) return NMS_ERR_INVALID_ARG;
+    const uintptr_t e = type_bytes(type);
+    if (misaligned(dx, e) || misaligned(dweight, e) || misaligned(dbias, 4) || misaligned(dev_status, 4))
+        return NMS_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaGetLastError();
+    if (rows == 0) {
+        if (dweight) cudaMemsetAsync(dweight, 0, e * outer * inner, st);
+        if (dbias) cudaMemsetAsync(dbias, 0, sizeof(float) * outer, st);
+        return cuda_status();
+    }
+    if (!dy || misaligned(dy, e) || misaligned(x, e) || misaligned(weight, e) || misaligned(pre, e) ||
+        (dx && !weight) || (dweight && !x) || (act != NMS_ACT_NONE && !pre))
+        return NMS_ERR_INVALID_ARG;
+    size_t need;
+    nms_linear_grad_workspace_size(type, rows, inner, outer, 1, &need);
+    if (!workspace || misaligned(workspace, 256) || workspace_bytes < need) return NMS_ERR_WORKSPACE;
+    char* rest = static_cast<char*>(workspace) + round_up(e * rows * padded(outer));
+    void* sums = rest;
+    const bool copied = (dx || dweight) && act != NMS_ACT_NONE;
+    if (copied || dbias) {
+        SlopeArgs a{};
+        a.dy = dy;
+        a.dy_row = dy_row;
+        a.pre = act != NMS_ACT_NONE ? pre : nullptr;
+        a.type = type;
+        a.rows = rows;
+        a.width = outer;
+        a.act = act;
+        a.dz = copied ? workspace : nullptr;
+        a.dz_row = padded(outer);
+        a.dbias = dbias;
+        launch_slope(a, sums, st);
+    }
+    ProductArgs p{};
+    p.type = type;
+    p.act = NMS_ACT_NONE;
+    p.a = copied ? workspace : dy;
+    p.a_row = copied ? padded(outer) : dy_row;
+    p.status = dev_status;
+    if (dx) {
+        p.b = weight;
+        p.b_row = weight_row;
+        p.b_across = 1;
+        p.m = rows;
+        p.n = inner;
+        p.k = outer;
+        p.out = dx;
+        launch_product(p, st);
+    }
+    if (dweight) {
+        p.a_across = 1;
+        p.b = x;
+        p.b_row = x_row;
+        p.b_across = 1;
+        p.m = outer;
+        p.n = inner;
+        p.k = rows;
+        p.out = dweight;
+        launch_product(p, st);
+    }
+    return cuda_status();
+}
+
+static nms_status check_layer(int32_t type, int32_t param_type, int64_t rows, int32_t width)
+{
+    if (!known_type(type) || (param_type != NMS_TYPE_F32 && param_type != type) || rows < 0 || width < 1)
+        return NMS_ERR_INVALID_ARG;
+    if (width > NMS_LAYER_MAX_WIDTH || rows > kMostRows) return NMS_ERR_CAPACITY;
+    return NMS_OK;
+}
+
+extern "C" nms_status nms_layer_norm_run(const void* x, int64_t x_row, const void* residual, int64_t residual_row,
+                                         int32_t type, int64_t rows, int32_t width, const void* weight,
+                                         const void* bias, int32_t param_type, float eps, void* y, void* sum,
+                                         float* mean, float* rstd, void* stream)
+{
+    const nms_status s = check_layer(type, param_type, rows, width);
+    if (s != NMS_OK) return s;
+    if (!(eps >= 0.0f) || std::isinf(eps) || bad_row(x_row, rows) || bad_row(residual_row, rows) ||
+        (rows > 0 && (residual != nullptr) != (sum != nullptr)))
+        return NMS_ERR_INVALID_ARG;
+    const uintptr_t e = type_bytes(type), pe = type_bytes(param_type);
+    if (misaligned(weight, pe) || misaligned(bias, pe) || misaligned(mean, 4) || misaligned(rstd, 4))
+        return NMS_ERR_INVALID_ARG;
+    if (rows == 0) return NMS_OK;
+    if (!x || !y || misaligned(x, e) || misaligned(y, e) || misaligned(residual, e) || misaligned(sum, e))
+        return NMS_ERR_INVALID_ARG;
+    cudaGetLastError();
+    LayerArgs a{};
+    a.x = x;
+    a.x_row = x_row;
+    a.second = residual;
+    a.second_row = residual ? residual_row : 0;
+    a.type = type;
+    a.rows = rows;
+    a.width = width;
+    a.weight = weight;
+    a.bias = bias;
+    a.param_f32 = param_type == NMS_TYPE_F32;
+    a.eps = eps;
+    a.out = y;
+    a.sum = sum;
+    a.mean = mean;
+    a.rstd = rstd;
+    launch_layer_norm(a, static_cast<cudaStream_t>(stream));
+    return cuda_status();
+}
+
+extern "C" nms_status nms_layer_norm_workspace_size(int64_t rows, int32_t width, size_t* bytes)
+{
+    if (!bytes) return NMS_ERR_INVALID_ARG;
+    const nms_status s = check_layer(NMS_TYPE_F32, NMS_TYPE_F32, rows, width);
+    if (s != NMS_OK) return s;
+    *bytes = rows == 0 ? 0 : round_up(layer_grad_workspace_bytes(rows, width));
+    return NMS_OK;
+}
+
+extern "C" nms_status nms_layer_norm_grad_run(const void* dy, int64_t dy_row, const void* x, int64_t x_row,
+                                              const void* dsum, int64_t dsum_row, int32_t type, int64_t rows,
+                                              int32_t width, const float* mean, const float* rstd, const void* weight,
+                                              int32_t param_type, void* dx, float* dweight, float* dbias,
+                                              void* workspace, size_t workspace_bytes, void* stream)
+{
+    const nms_status s = check_layer(type, param_type, rows, width);
+    if (s != NMS_OK) return s;
+    if (bad_row(dy_row, rows) || bad_row(x_row, rows) || bad_row(dsum_row, rows)) return NMS_ERR_INVALID_ARG;
+    const uintptr_t e = type_bytes(type);
+    if (misaligned(weight, type_bytes(param_type)) || misaligned(mean, 4) || misaligned(rstd, 4) ||
+        misaligned(dweight, 4) || misaligned(dbias, 4))
+        return NMS_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaGetLastError();
+    if (rows == 0) {
+        if (dweight) cudaMemsetAsync(dweight, 0, sizeof(float) * width, st);
+        if (dbias) cudaMemsetAsync(dbias, 0, sizeof(float) * width, st);
+        return cuda_status();
+    }
+    if (!dy || !x || !dx || !mean || !rstd || misaligned(dy, e) || misaligned(x, e) || misaligned(dx, e) ||
+        misaligned(dsum, e))
+        return NMS_ERR_INVALID_ARG;
+    if (!workspace || misaligned(workspace, 256) || workspace_bytes < layer_grad_workspace_bytes(rows, width))
+        return NMS_ERR_WORKSPACE;
+    LayerArgs a{};
+    a.x = x;
+    a.x_row = x_row;
+    a.second = dsum;
+    a.second_row = dsum ? dsum_row : 0;
+    a.dy = dy;
+    a.dy_row = dy_row;
+    a.type = type;
+    a.rows = rows;
+    a.width = width;
+    a.weight = weight;
+    a.param_f32 = param_type == NMS_TYPE_F32;
+    a.out = dx;
+    a.mean = const_cast<float*>(mean);
+    a.rstd = const_cast<float*>(rstd);
+    a.dweight = dweight;
+    a.dbias = dbias;
+    launch_layer_grad(a, workspace, st);
+    return cuda_status();
+}
+
+extern "C" nms_status nms_rotary_run(const void* x, int64_t x_batch, int64_t x_token, int64_t x_head, int32_t type,
+                                     int64_t batch, int64_t tokens, int32_t heads, int32_t dim, const void* positions,
+                                     int32_t position_type, int64_t sets, int32_t axes, const int64_t* lut,
+                                     int32_t pairs, int32_t halves, int32_t inverse, void* y, int64_t y_batch,
+                                     int64_t y_token, int64_t y_head, void* stream)
+{
+    if (!known_type(type) || (position_type != NMS_TYPE_F32 && position_type != NMS_POSITION_I32) || batch < 0 ||
+        tokens < 0 || heads < 0 || dim < 1 || axes < 1 || pairs < 0 || pairs > dim / 2 || (sets != 1 && sets != batch))
+        return NMS_ERR_INVALID_ARG;
+    if (axes > NMS_ROTARY_MAX_AXES || dim > NMS_ROTARY_MAX_DIM || heads > (1 << 20) || batch > kMostRows ||
+        tokens > kMostRows || batch * tokens > kMostRows || too_far(batch * tokens, static_cast<int64_t>(heads) * dim))
+        return NMS_ERR_CAPACITY;
+    const bool empty = batch == 0 || tokens == 0 || heads == 0;
+    if (empty) return NMS_OK;
+    for (const int64_t* st : {&x_batch, &y_batch})
+        if (bad_row(*st, batch)) return NMS_ERR_INVALID_ARG;
+    if (bad_row(x_token, tokens) || bad_row(y_token, tokens) || bad_row(x_head, heads) || bad_row(y_head, heads))
+        return NMS_ERR_INVALID_ARG;
+    const uintptr_t e = type_bytes(type);
+    if (!x || !y || misaligned(x, e) || misaligned(y, e) || (pairs > 0 && (!positions || !lut)) ||
+        misaligned(positions, 4) || misaligned(lut, 8))
+        return NMS_ERR_INVALID_ARG;
+    cudaGetLastError();
+    RotaryArgs a{x,     x_batch, x_token, x_head, type,  batch,  tokens,  heads, dim,     positions, sets,
+                 position_type == NMS_TYPE_F32,   axes,  lut,    pairs,   halves != 0,    inverse != 0, y,
+                 y_batch, y_token, y_head};
+    launch_rotary(a, static_cast<cudaStream_t>(stream));
+    return cuda_status();
+}

@@ -1,0 +1,68 @@
+// Layer normalisation: launches by type, and the join of the parameters'
+// gradients.
+#include "k_layer.cuh"
+
+namespace gbnms {
+
+namespace {
+
+constexpr int JOIN_COLUMNS = 32, JOIN_SLOTS = 32;
+
+// A column's parts go to JOIN_SLOTS threads in turn, whose sums are added in order.
+__global__ void __launch_bounds__(JOIN_COLUMNS * JOIN_SLOTS)
+column_join_kernel(const float* parts, int64_t blocks, int64_t columns, int64_t split, float* first, float* second)
+{
+    __shared__ LongSum sums[JOIN_SLOTS][JOIN_COLUMNS];
+    pdl_wait();  // the parts are there
+    const int64_t e = static_cast<int64_t>(blockIdx.x) * JOIN_COLUMNS + threadIdx.x;
+    LongSum s{0.0f, 0.0f};
+    if (e < columns)
+        for (int64_t b = threadIdx.y; b < blocks; b += JOIN_SLOTS) s.add(parts[b * columns + e]);
+    sums[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && e < columns) {
+        for (int k = 1; k < JOIN_SLOTS; ++k) s.add(sums[k][threadIdx.x]);
+        float* out = e < split ? first : second;
+        if (out) out[e < split ? e : e - split] = s.value();
+    }
+}
+
+void launch_rows(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
+{
+    if (a.type == NMS_TYPE_F32) launch_layer_f32(a, parts, grad, st);
+    else if (a.type == NMS_TYPE_F16) launch_layer_f16(a, parts, grad, st);
+    else launch_layer_bf16(a, parts, grad, st);
+}
+
+}  // namespace
+
+void launch_layer_norm(const LayerArgs& a, cudaStream_t st) { launch_rows(a, nullptr, false, st); }
+
+size_t layer_grad_workspace_bytes(int64_t rows, int width)
+{
+    return static_cast<size_t>(layer_grad_blocks(rows, width)) * 2 * width * sizeof(float);
+}
+
+void launch_layer_grad(const LayerArgs& a, void* workspace, cudaStream_t st)
+{
+    float* parts = a.dweight || a.dbias ? static_cast<float*>(workspace) : nullptr;
+    launch_rows(a, parts, true, st);
+    if (!parts) return;
+    launch_column_join(parts, layer_grad_blocks(a.rows, a.width), 2 * static_cast<int64_t>(a.width), a.width, a.dweight,
+                       a.dbias, st);
+}
+
+void launch_column_join(const float* parts, int64_t blocks, int64_t columns, int64_t split, float* first, float* second,
+                        cudaStream_t st)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>((columns + JOIN_COLUMNS - 1) / JOIN_COLUMNS));
+    cfg.blockDim = dim3(JOIN_COLUMNS, JOIN_SLOTS);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, column_join_kernel, parts, blocks, columns, split, first, second);
+}
+
+}  // namespace gbnms

@@ -578,6 +578,132 @@ nms_status nms_relation_softmax_grad_run(const void* dprobs, const void* probs, 
                                          void* dscores, float* dtable, void* workspace, size_t workspace_bytes,
                                          void* stream);
 
+/*
+ * Operators of a transformer block among a detector's candidates: what stands
+ * around the attention weights above.  Conventions as for the head's
+ * operators; rows are `width` (inner, outer, dim) consecutive elements at a
+ * stride of their own (input rows may coincide: a stride of 0 repeats one).
+ */
+#define NMS_LAYER_MAX_WIDTH 16384
+#define NMS_LINEAR_MAX_WIDTH (1 << 20)
+#define NMS_ROTARY_MAX_AXES 8
+#define NMS_ROTARY_MAX_DIM 4096
+
+/*
+ * Linear layer:
+ *   z = x weight^T + bias,  y = act(z) + residual,
+ * x [rows][inner], weight [outer][inner], y [rows][outer]; sums in binary32.
+ *   x, weight  device, `type`, rows x_row and weight_row elements apart.
+ *   bias       device [outer] of bias_type (NMS_TYPE_F32, or `type`), or NULL.
+ *   act        NMS_ACT_*.
+ *   residual   device [rows][outer], `type`, rows residual_row apart, or NULL.
+ *   y, pre     device [rows][outer] contiguous, `type`; pre (z, which the
+ *              gradient of an activation reads) may be NULL.  y may be
+ *              residual itself where that is contiguous.
+ *   dev_status optional device int32: NMS_ERR_TIMEOUT when a bounded wait of
+ *              the kernel gave up, which leaves NaNs in y and pre.
+ *   workspace  >= nms_linear_workspace_size() bytes, 256-byte aligned.
+ *              `aligned` says that x and the weight start at multiples of 16
+ *              bytes and so do their rows, which do not overlap; without it
+ *              there is room for copies, which 16-bit operands need then.
+ * The gradient, from dy (rows dy_row apart), the forward's x and weight and,
+ * with an activation, its pre [rows][outer] contiguous:
+ *   dz = dy * act'(pre),  dx = dz weight,  dweight = dz^T x,  dbias = sum dz,
+ * dx [rows][inner], dweight [outer][inner] contiguous and of `type`, dbias
+ * float [outer]; each may be NULL and is left out then.  The residual's
+ * gradient is dy.  With an activation the products take dz rounded to `type`;
+ * dbias is summed before that.  `aligned` there speaks of dy too.  Sums are
+ * taken in a fixed order: the same call gives the same bits.
+ * Errors: NMS_ERR_INVALID_ARG (types, act, shapes, negative strides, NULL or
+ *         misaligned pointers), NMS_ERR_CAPACITY (inner or outer above
+ *         NMS_LINEAR_MAX_WIDTH, rows above 2^31 - 1, more than 2^38 elements
+ *         of an operand), NMS_ERR_WORKSPACE, NMS_ERR_CUDA.
+ */
+nms_status nms_linear_workspace_size(int32_t type, int64_t rows, int32_t inner, int32_t outer, int32_t aligned,
+                                     size_t* bytes);
+nms_status nms_linear_run(const void* x, int64_t x_row, int32_t type, int64_t rows, int32_t inner,
+                          const void* weight, int64_t weight_row, int32_t outer, const void* bias, int32_t bias_type,
+                          int32_t act, const void* residual, int64_t residual_row, void* y, void* pre,
+                          int32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream);
+nms_status nms_linear_grad_workspace_size(int32_t type, int64_t rows, int32_t inner, int32_t outer, int32_t aligned,
+                                          size_t* bytes);
+nms_status nms_linear_grad_run(const void* dy, int64_t dy_row, const void* x, int64_t x_row, int32_t type,
+                               int64_t rows, int32_t inner, const void* weight, int64_t weight_row, int32_t outer,
+                               const void* pre, int32_t act, void* dx, void* dweight, float* dbias,
+                               int32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Layer normalisation of rows:
+ *   s = x + residual (rounded to `type`),  u = (s - mean) * rstd,
+ *   y = u * weight + bias,
+ * mean and the biased variance over a row's width elements, rstd = 1 /
+ * sqrt(variance + eps).
+ *   x, residual  device, `type`, rows x_row and residual_row apart; residual
+ *                may be NULL (s = x).
+ *   weight, bias device [width] of param_type (NMS_TYPE_F32, or `type`), or
+ *                NULL (1 and 0).
+ *   y, sum       device [rows][width] contiguous, `type`; sum is s, wanted
+ *                exactly with a residual, and may be x or residual itself
+ *                where that is contiguous.
+ *   mean, rstd   device float [rows] for the gradient, or NULL.  A NaN or an
+ *                infinity in a row leaves no number in its statistics and
+ *                results.  Squares are summed in binary32: those of a row's
+ *                deviations add up to less than 2^126.
+ * The gradient, from dy, the normalised rows s (as x) and the forward's mean
+ * and rstd:
+ *   du = dy * weight,  dx = rstd * (du - avg(du) - u * avg(du * u)) + dsum,
+ *   dweight = sum dy * u,  dbias = sum dy over the rows;
+ * dsum [rows][width], `type`, rows dsum_row apart, is what reaches s by other
+ * ways (NULL: nothing); dx is the gradient of x and of the residual alike.
+ * dweight and dbias (float [width]) may be NULL.  Sums are taken in a fixed
+ * order: the same call gives the same bits.
+ *   workspace  >= nms_layer_norm_workspace_size() bytes, 256-byte aligned.
+ * Errors: NMS_ERR_INVALID_ARG (types, eps < 0 or not finite, shapes, negative
+ *         strides, NULL or misaligned pointers, a sum without residual or the
+ *         other way round), NMS_ERR_CAPACITY (width above NMS_LAYER_MAX_WIDTH,
+ *         rows above 2^31 - 1), NMS_ERR_WORKSPACE, NMS_ERR_CUDA.
+ */
+nms_status nms_layer_norm_run(const void* x, int64_t x_row, const void* residual, int64_t residual_row, int32_t type,
+                              int64_t rows, int32_t width, const void* weight, const void* bias, int32_t param_type,
+                              float eps, void* y, void* sum, float* mean, float* rstd, void* stream);
+nms_status nms_layer_norm_workspace_size(int64_t rows, int32_t width, size_t* bytes);
+nms_status nms_layer_norm_grad_run(const void* dy, int64_t dy_row, const void* x, int64_t x_row, const void* dsum,
+                                   int64_t dsum_row, int32_t type, int64_t rows, int32_t width, const float* mean,
+                                   const float* rstd, const void* weight, int32_t param_type, void* dx,
+                                   float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * Rotary positions on several axes.  Vector (b, t, h) of x is `dim`
+ * consecutive elements; its pair i (of `pairs`, 2 * pairs <= dim) turns by the
+ * angle of its token:
+ *   (p, q) -> (p cos - q sin, q cos + p sin),  angle = 2 pi * fraction of
+ *   position[axis] * turns,  turns = lut[i] / 2^64, axis = lut[pairs + i].
+ * halves != 0: pair i is elements i and i + pairs; 0: elements 2 i and 2 i + 1.
+ * Elements from 2 * pairs on are copied, a pair whose axis is not one of the
+ * positions' is not turned.  inverse != 0 turns the other way, which is the
+ * gradient.
+ *   x, y       device, `type`; strides in elements by batch, token and head,
+ *              not negative; y may be x itself with x's strides, and its
+ *              vectors must not overlap.
+ *   positions  device [sets][tokens][axes], sets 1 or batch; int32, or float
+ *              with position_type NMS_TYPE_F32 (else NMS_POSITION_I32), of
+ *              which a NaN, an infinity or |position| >= 2^31 turns to NaN.
+ *              Whole turns are left out exactly, so far positions lose
+ *              nothing.
+ *   lut        device int64 [2][pairs], unsigned fractions of a turn first.
+ * Errors: NMS_ERR_INVALID_ARG (types, shapes, strides, NULL or misaligned
+ *         pointers), NMS_ERR_CAPACITY (axes, dim above the limits, heads above
+ *         2^20, batch * tokens above 2^31 - 1, more than 2^38 elements),
+ *         NMS_ERR_CUDA.
+ */
+#define NMS_POSITION_I32 16
+nms_status nms_rotary_run(const void* x, int64_t x_batch, int64_t x_token, int64_t x_head, int32_t type,
+                          int64_t batch, int64_t tokens, int32_t heads, int32_t dim, const void* positions,
+                          int32_t position_type, int64_t sets, int32_t axes, const int64_t* lut, int32_t pairs,
+                          int32_t halves, int32_t inverse, void* y, int64_t y_batch, int64_t y_token,
+                          int64_t y_head, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
