@@ -321,6 +321,9 @@ def layer_norm_grad(dy, x, mean, rstd, weight=None, *, dsum=None):
 
 # --------------------------------------------------------- rotary positions
 
+_RADIAN = (1 << 128) * 10 ** 50 // 628318530717958647692528676655900576839433879875021  # of a turn, in units of 2^-128
+
+
 def rotary_lut(*pairs: int, base: float = 10000.0):
     """Table for `rotary`: pairs[a] pairs of elements turn by axis a of the
     positions, pair j of n by base^(-j / n) radians a position.  int64 [2,
@@ -329,11 +332,16 @@ def rotary_lut(*pairs: int, base: float = 10000.0):
         raise ValueError("rotary_lut: numbers of pairs by axis (not negative, one pair at least, "
                          f"{NMS_ROTARY_MAX_AXES} axes at most) and a base of 1 or more")
     with decimal.localcontext() as c:
-        c.prec = 60
-        turn = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+        c.prec = 45
         log = decimal.Decimal(base).ln()
-        turns = [int((decimal.Decimal(1 << 64) / turn * (-log * j / n).exp()).to_integral_value())
-                 for n in pairs for j in range(n)]
+        # Factors from pair to pair, in units of 2^-128.
+        factors = [int((-log / n).exp() * (1 << 128)) if n else 0 for n in pairs]
+    turns = []
+    for n, factor in zip(pairs, factors):
+        f = _RADIAN
+        for _ in range(n):
+            turns.append((f + (1 << 63)) >> 64)
+            f = f * factor >> 128
     axes = [a for a, n in enumerate(pairs) for _ in range(n)]
     torch = head._torch()
     return torch.tensor([turns, axes], dtype=torch.int64)

@@ -40,6 +40,32 @@ nms_status check_linear(int32_t type, int64_t rows, int32_t inner, int32_t outer
 
 bool bad_row(int64_t row, int64_t rows) { return row < 0 || too_far(rows, row); }
 
+// Whether the tensor cores' loads cannot take an operand of 16 bits as it lies.
+bool uneven(int32_t type, const void* p, int64_t row, int64_t rows, int64_t width)
+{
+    return type != NMS_TYPE_F32 && (misaligned(p, 16) || row % 8 != 0 || row < width);
+}
+
+size_t copy_bytes(int64_t rows, int64_t width) { return round_up(2 * rows * padded(width)); }
+
+// The operand itself, or a copy of it in the workspace, which moves on.
+const void* even(int32_t type, const void* p, int64_t& row, int64_t rows, int64_t width, char*& workspace, cudaStream_t st)
+{
+    if (!p || !uneven(type, p, row, rows, width)) return p;
+    void* copy = workspace;
+    workspace += copy_bytes(rows, width);
+    launch_copy_rows(p, row, rows, width, copy, padded(width), st);
+    row = padded(width);
+    return copy;
+}
+
+bool launch_product(const ProductArgs& p, cudaStream_t st)
+{
+    if (p.type != NMS_TYPE_F32) return launch_product_tc(p, st);
+    launch_product_f32(p, st);
+    return true;
+}
+
 }  // namespace
 
 extern "C" nms_status nms_linear_workspace_size(int32_t type, int64_t rows, int32_t inner, int32_t outer,
@@ -48,8 +74,7 @@ extern "C" nms_status nms_linear_workspace_size(int32_t type, int64_t rows, int3
     if (!bytes) return NMS_ERR_INVALID_ARG;
     const nms_status s = check_linear(type, rows, inner, outer);
     if (s != NMS_OK) return s;
-    (void)aligned;
-    *bytes = 0;
+    *bytes = type == NMS_TYPE_F32 || aligned || rows == 0 ? 0 : copy_bytes(rows, inner) + copy_bytes(outer, inner);
     return NMS_OK;
 }
 
@@ -70,14 +95,17 @@ extern "C" nms_status nms_linear_run(const void* x, int64_t x_row, int32_t type,
     if (!x || !weight || !y || misaligned(x, e) || misaligned(weight, e) || misaligned(y, e) || misaligned(pre, e) ||
         misaligned(residual, e))
         return NMS_ERR_INVALID_ARG;
-    (void)workspace;
-    (void)workspace_bytes;
+    const bool aligned = !uneven(type, x, x_row, rows, inner) && !uneven(type, weight, weight_row, outer, inner);
+    size_t need;
+    nms_linear_workspace_size(type, rows, inner, outer, aligned, &need);
+    if (need && (!workspace || misaligned(workspace, 256) || workspace_bytes < need)) return NMS_ERR_WORKSPACE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaGetLastError();
+    char* rest = static_cast<char*>(workspace);
     ProductArgs p{};
-    p.a = x;
+    p.a = even(type, x, x_row, rows, inner, rest, st);
     p.a_row = x_row;
-    p.b = weight;
+    p.b = even(type, weight, weight_row, outer, inner, rest, st);
     p.b_row = weight_row;
     p.type = type;
     p.m = rows;
@@ -91,7 +119,7 @@ extern "C" nms_status nms_linear_run(const void* x, int64_t x_row, int32_t type,
     p.out = y;
     p.pre = pre;
     p.status = dev_status;
-    launch_product(p, st);
+    if (!launch_product(p, st)) return NMS_ERR_CUDA;
     return cuda_status();
 }
 
@@ -104,7 +132,7 @@ extern "C" nms_status nms_linear_grad_workspace_size(int32_t type, int64_t rows,
     *bytes = 0;
     if (rows == 0) return NMS_OK;
     *bytes = round_up(type_bytes(type) * rows * padded(outer)) + round_up(slope_workspace_bytes(rows, outer));
-    (void)aligned;
+    if (type != NMS_TYPE_F32 && !aligned) *bytes += copy_bytes(rows, inner) + copy_bytes(outer, inner);
     return NMS_OK;
 }
 
@@ -131,12 +159,16 @@ extern "C" nms_status nms_linear_grad_run(const void* dy, int64_t dy_row, const 
     if (!dy || misaligned(dy, e) || misaligned(x, e) || misaligned(weight, e) || misaligned(pre, e) ||
         (dx && !weight) || (dweight && !x) || (act != NMS_ACT_NONE && !pre))
         return NMS_ERR_INVALID_ARG;
+    const bool dy_uneven = uneven(type, dy, dy_row, rows, outer);
+    const bool aligned = !dy_uneven && !(x && uneven(type, x, x_row, rows, inner)) &&
+                         !(weight && uneven(type, weight, weight_row, outer, inner));
     size_t need;
-    nms_linear_grad_workspace_size(type, rows, inner, outer, 1, &need);
+    nms_linear_grad_workspace_size(type, rows, inner, outer, aligned, &need);
     if (!workspace || misaligned(workspace, 256) || workspace_bytes < need) return NMS_ERR_WORKSPACE;
     char* rest = static_cast<char*>(workspace) + round_up(e * rows * padded(outer));
     void* sums = rest;
-    const bool copied = (dx || dweight) && act != NMS_ACT_NONE;
+    rest += round_up(slope_workspace_bytes(rows, outer));
+    const bool products = dx || dweight, copied = products && (act != NMS_ACT_NONE || dy_uneven);
     if (copied || dbias) {
         SlopeArgs a{};
         a.dy = dy;
@@ -158,25 +190,25 @@ extern "C" nms_status nms_linear_grad_run(const void* dy, int64_t dy_row, const 
     p.a_row = copied ? padded(outer) : dy_row;
     p.status = dev_status;
     if (dx) {
-        p.b = weight;
+        p.b = even(type, weight, weight_row, outer, inner, rest, st);
         p.b_row = weight_row;
         p.b_across = 1;
         p.m = rows;
         p.n = inner;
         p.k = outer;
         p.out = dx;
-        launch_product(p, st);
+        if (!launch_product(p, st)) return NMS_ERR_CUDA;
     }
     if (dweight) {
         p.a_across = 1;
-        p.b = x;
+        p.b = even(type, x, x_row, rows, inner, rest, st);
         p.b_row = x_row;
         p.b_across = 1;
         p.m = outer;
         p.n = inner;
         p.k = rows;
         p.out = dweight;
-        launch_product(p, st);
+        if (!launch_product(p, st)) return NMS_ERR_CUDA;
     }
     return cuda_status();
 }

@@ -127,7 +127,10 @@ layer_kernel(const LayerArgs a)
         }
     team_sums<TEAM>(off, squares, shared[1]);
     off *= share;
-    const float variance = fmaf(-off, off, squares * share);  // a NaN stays one
+    squares *= share;
+    // The deviations' own roundings leave up to some 2^-22 of their size in it: below that the first mean is nearer.
+    if (off * off < 0x1p-42f * squares) off = 0.0f;
+    const float variance = fmaf(-off, off, squares);  // a NaN stays one
     const float rstd = 1.0f / sqrtf((variance < 0.0f ? 0.0f : variance) + a.eps);
     if (t == 0) {
         if (a.mean) a.mean[row] = mean + off;

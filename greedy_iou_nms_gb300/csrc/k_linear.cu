@@ -1,7 +1,7 @@
-// Matrix products with bias, activation and residual in their epilogue.
-//
-// product_kernel works on the plain arithmetic units: a block has a tile of
-// TILE x TILE results, its 256 threads S x S of them each, in binary32.
+// Matrix products of binary32 operands with bias, activation and residual in
+// their epilogue, on the plain arithmetic units: a block has a tile of TILE x
+// TILE results, its 256 threads S x S of them each.  And the copy of 16-bit
+// rows whose places the tensor cores' loads cannot take.
 #include "block.h"
 #include "head.cuh"
 #include "internal.h"
@@ -59,7 +59,7 @@ product_kernel(const ProductArgs p, int64_t tiles_n)
     const int64_t tm = blockIdx.x / tiles_n, tn = blockIdx.x - tm * tiles_n;
     const int64_t m0 = tm * TILE, n0 = tn * TILE;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    float acc[S][S] = {};
+    float acc[S][S] = {}, total[S][S] = {};
     Step<T, TILE> a, b;
     const int64_t steps = (p.k + PR_DEPTH - 1) / PR_DEPTH;
     auto load = [&](int64_t s) {
@@ -86,6 +86,16 @@ product_kernel(const ProductArgs p, int64_t tiles_n)
 #pragma unroll
                 for (int j = 0; j < S; ++j) acc[i][j] = fmaf(x[i], w[j], acc[i][j]);
         }
+        // Sums of 256 products, added up: a chain over all of k would round off with k.
+        if (s % 16 == 15 || s + 1 == steps) {
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+#pragma unroll
+                for (int j = 0; j < S; ++j) {
+                    total[i][j] += acc[i][j];
+                    acc[i][j] = 0.0f;
+                }
+        }
         if (s + 1 < steps) {
             a.store(as[at ^ 1], p.a_across);
             b.store(bs[at ^ 1], p.b_across);
@@ -102,7 +112,7 @@ product_kernel(const ProductArgs p, int64_t tiles_n)
         for (int j = 0; j < S; ++j) {
             const int64_t n = n0 + (j / 4) * 64 + tx * 4 + j % 4;
             if (n >= p.n) continue;
-            float z[1] = {acc[i][j] + (p.bias ? load_param<T>(p.bias, p.bias_f32, n) : 0.0f)};
+            float z[1] = {total[i][j] + (p.bias ? load_param<T>(p.bias, p.bias_f32, n) : 0.0f)};
             if (pre) pre[m * p.n + n] = from_f32<T>(z[0]);
             act_values<T>(z, p.act);
             if (p.residual) z[0] += to_f32(static_cast<const T*>(p.residual)[m * p.residual_row + n]);
@@ -111,21 +121,38 @@ product_kernel(const ProductArgs p, int64_t tiles_n)
     }
 }
 
-template <typename T>
-void launch(const ProductArgs& p, cudaStream_t st)
+// Eight elements of a row a thread.
+__global__ void __launch_bounds__(256)
+copy_rows_kernel(const uint16_t* from, int64_t from_row, int64_t rows, int64_t width, uint16_t* to, int64_t to_row)
 {
-    auto tiles = [&](int64_t t) { return ((p.m + t - 1) / t) * ((p.n + t - 1) / t); };
-    if (tiles(128) >= SMS) product_kernel<T, 8><<<static_cast<unsigned>(tiles(128)), 256, 0, st>>>(p, (p.n + 127) / 128);
-    else product_kernel<T, 4><<<static_cast<unsigned>(tiles(64)), 256, 0, st>>>(p, (p.n + 63) / 64);
+    const int64_t parts = (width + 7) / 8, n = rows * parts;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t row = i / parts, e = (i - row * parts) * 8;
+        const uint16_t* p = from + row * from_row + e;
+        Pack<uint16_t, 8> q;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q.v[k] = e + k < width ? p[k] : 0;
+        *reinterpret_cast<Pack<uint16_t, 8>*>(to + row * to_row + e) = q;
+    }
 }
 
 }  // namespace
 
-void launch_product(const ProductArgs& p, cudaStream_t st)
+void launch_product_f32(const ProductArgs& p, cudaStream_t st)
 {
-    if (p.type == NMS_TYPE_F32) launch<float>(p, st);
-    else if (p.type == NMS_TYPE_F16) launch<__half>(p, st);
-    else launch<__nv_bfloat16>(p, st);
+    auto tiles = [&](int64_t t) { return ((p.m + t - 1) / t) * ((p.n + t - 1) / t); };
+    if (tiles(128) >= SMS)
+        product_kernel<float, 8><<<static_cast<unsigned>(tiles(128)), 256, 0, st>>>(p, (p.n + 127) / 128);
+    else
+        product_kernel<float, 4><<<static_cast<unsigned>(tiles(64)), 256, 0, st>>>(p, (p.n + 63) / 64);
+}
+
+void launch_copy_rows(const void* from, int64_t from_row, int64_t rows, int64_t width, void* to, int64_t to_row,
+                      cudaStream_t st)
+{
+    const int64_t want = (rows * ((width + 7) / 8) + 255) / 256, most = SMS * 8;
+    copy_rows_kernel<<<static_cast<unsigned>(want < most ? want : most), 256, 0, st>>>(
+        static_cast<const uint16_t*>(from), from_row, rows, width, static_cast<uint16_t*>(to), to_row);
 }
 
 }  // namespace gbnms

@@ -1,0 +1,550 @@
+// Matrix products of 16-bit operands on the tensor cores (tcgen05), with bias,
+// activation and residual in the epilogue:
+//   out[m][n] = act(sum_k A[m][k] B[n][k] + bias[n]) + residual[m][n].
+//
+// A block has tiles of 128 x BN results.  One thread feeds a ring of shared-
+// memory stages by TMA (64 columns of k a stage, 128-byte swizzle), one thread
+// issues the matrix instructions, whose accumulators lie in tensor memory, and
+// eight warps carry accumulators to the outputs: those of one tile while the
+// next one is multiplied (two sets of accumulators).  An operand that lies
+// across ([k][m], as both do for a weight's gradient) is taken as it lies: the
+// instruction reads either order, only boxes and descriptors differ.
+//
+// Few rows of A (a step of serving): A and B change places, so that the long
+// side fills the 128 lanes and BN is 16 to 64.  Few tiles: the blocks of a
+// cluster share one, each a stretch of k, and add up their parts through
+// distributed shared memory, in order.
+#include <cuda.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "block.h"
+#include "head.cuh"
+#include "internal.h"
+
+namespace gbnms {
+
+namespace {
+
+constexpr int TC_M = 128, TC_K = 64;        // of a tile, of a stage
+constexpr int TC_WRITERS = 256;             // threads of the epilogue: warps 2 to 9
+constexpr int TC_THREADS = TC_WRITERS + 64;
+constexpr uint64_t TC_PATIENCE = 2000000000;  // ns before a wait gives up; a tile's whole sum over k may take longer:
+constexpr uint64_t TC_TILE_PATIENCE = 10000000000;  // 2^31 of k take a second
+constexpr int A_BYTES = TC_M * TC_K * 2;
+constexpr int HALF_BYTES = 64 * TC_K * 2;   // a box of an operand that lies across: 64 of m or n, 64 of k
+
+template <int BN> constexpr int TC_STAGES = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+template <int BN> constexpr int TC_SMEM = 1024 + TC_STAGES<BN> * (A_BYTES + BN * TC_K * 2);  // from a multiple of 1024 on
+
+struct TcArgs {
+    int a_across, b_across;
+    int64_t m, n, k;
+    int64_t tiles_m, tiles_n;
+    int split;  // blocks of a cluster, which share a tile along k
+    const void* bias;
+    int bias_f32, act;
+    const void* residual;
+    int64_t residual_m, residual_n;  // strides
+    void* out;
+    void* pre;
+    int64_t out_m, out_n;  // strides of out and pre
+    int vector;            // rows of out, pre and residual start at multiples of 16 bytes
+    int32_t* status;
+};
+
+// ------------------------------------------------------------- instructions
+
+__device__ __forceinline__ uint32_t shared_address(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ void barrier_init(uint32_t bar, int count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void barrier_expect(uint32_t bar, int bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool barrier_done(uint32_t bar, int parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done;
+}
+
+// Waits for the phase of this parity; false when it gave up.
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, int parity, uint64_t patience = TC_PATIENCE)
+{
+    if (barrier_done(bar, parity)) return true;
+    uint64_t start, now;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(start));
+    do {
+        if (barrier_done(bar, parity)) return true;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+    } while (now - start < patience);
+    return false;
+}
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t form, bool add)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(form), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+
+// The barrier completes when all matrix instructions issued so far have.
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// N columns of this thread's lane of tensor memory.
+template <int N>
+__device__ __forceinline__ void tensor_load(float (&v)[N], uint32_t at)
+{
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    if constexpr (N == 32) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+            "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+              "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+              "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+            : "r"(at));
+    } else {
+        static_assert(N == 8, "8 or 32 columns");
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(at));
+    }
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Shared-memory descriptor of an operand with 128-byte swizzle, at address 0:
+// 16-byte units; version 1 in bits 46 on, swizzle code 2 in bits 61 on.  Along
+// k: groups of eight rows 1024 bytes apart.  Across: groups of eight k 1024
+// bytes apart, the next 64 of m or n a box further.
+__device__ __forceinline__ uint64_t operand_form(int across)
+{
+    const uint64_t leading = across ? HALF_BYTES / 16 : 1, stride = 1024 / 16;
+    return (leading << 16) | (stride << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// Instruction descriptor: binary32 accumulators, both operands of T, 128 x bn.
+template <typename T>
+__device__ __forceinline__ uint32_t instruction_form(int a_across, int b_across, int bn)
+{
+    const uint32_t kind = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
+    return (1u << 4) | (kind << 7) | (kind << 10) | (static_cast<uint32_t>(a_across) << 15) |
+           (static_cast<uint32_t>(b_across) << 16) | (static_cast<uint32_t>(bn / 8) << 17) |
+           (static_cast<uint32_t>(TC_M / 16) << 24);
+}
+
+// -------------------------------------------------------------------- tiles
+
+struct Place {
+    int64_t m, n;
+};
+
+// Tile t: strips of 16 tiles along n, within a strip n first, so that the tiles
+// that run together share rows of both operands in L2.
+__device__ __forceinline__ Place tile_place(const TcArgs& p, int64_t t, int bn)
+{
+    const int64_t strip = t / (16 * p.tiles_m), left = t - strip * 16 * p.tiles_m;
+    const int64_t width = min(static_cast<int64_t>(16), p.tiles_n - strip * 16);
+    const int64_t m = left / width;
+    return {m * TC_M, (strip * 16 + left - m * width) * bn};
+}
+
+// One result.
+template <typename T>
+__device__ __forceinline__ void finish_one(const TcArgs& p, int64_t m, int64_t n, float sum, float bias)
+{
+    float z[1] = {sum + bias};
+    const int64_t at = m * p.out_m + n * p.out_n;
+    if (p.pre) static_cast<T*>(p.pre)[at] = from_f32<T>(z[0]);
+    act_values<T>(z, p.act);
+    if (p.residual) z[0] += to_f32(static_cast<const T*>(p.residual)[m * p.residual_m + n * p.residual_n]);
+    static_cast<T*>(p.out)[at] = from_f32<T>(z[0]);
+}
+
+// Eight results of a row, all of them there and aligned.
+template <typename T>
+__device__ __forceinline__ void finish_eight(const TcArgs& p, int64_t m, int64_t n, const float* sum, const float* bias)
+{
+    float z[8];
+    const int64_t at = m * p.out_m + n;
+    Pack<T, 8> r;
+    if (p.residual) r = *reinterpret_cast<const Pack<T, 8>*>(static_cast<const T*>(p.residual) + m * p.residual_m + n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = sum[i] + bias[i];
+    if (p.pre) *reinterpret_cast<Pack<T, 8>*>(static_cast<T*>(p.pre) + at) = pack_results<T, 8>(z);
+    act_values<T, 8>(z, p.act);
+    if (p.residual) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] += to_f32(r.v[i]);
+    }
+    *reinterpret_cast<Pack<T, 8>*>(static_cast<T*>(p.out) + at) = pack_results<T, 8>(z);
+}
+
+__device__ __forceinline__ uint32_t peer_address(uint32_t at, int rank)
+{
+    uint32_t peer;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(at), "r"(rank));
+    return peer;
+}
+
+// SWAP: A's rows are results' columns (the operands changed places); bias by m.
+template <typename T, int BN, bool SWAP>
+__global__ void __launch_bounds__(TC_THREADS, 1)
+product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const TcArgs p)
+{
+    constexpr int STAGES = TC_STAGES<BN>, B_BYTES = BN * TC_K * 2, STAGE = A_BYTES + B_BYTES;
+    constexpr int COLUMNS = 2 * BN < 32 ? 32 : 2 * BN;  // of tensor memory
+    constexpr int CHUNK = BN >= 64 ? 32 : 8;            // columns that a thread carries at a time
+    extern __shared__ char dynamic[];
+    __shared__ alignas(8) uint64_t bars[2 * STAGES + 4];
+    __shared__ uint32_t tensor_at;
+    __shared__ alignas(16) float bias_s[2][SWAP ? TC_M : BN];
+    const uint32_t ring = (shared_address(dynamic) + 1023) & ~1023u;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t full = shared_address(bars), empty = full + 8 * STAGES, done = empty + 8 * STAGES, free_ = done + 16;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            barrier_init(full + 8 * s, 1);
+            barrier_init(empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            barrier_init(done + 8 * b, 1);
+            barrier_init(free_ + 8 * b, TC_WRITERS / 32);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_address(&tensor_at)),
+                     "n"(COLUMNS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tensor = tensor_at;
+    pdl_wait();
+    const int rank = static_cast<int>(blockIdx.x) % p.split;
+    const int64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + TC_K - 1) / TC_K;
+    const int64_t each = (steps + p.split - 1) / p.split;
+    const int64_t first = min(steps, rank * each), last = min(steps, first + each);  // of k, this block's
+    const int64_t tile0 = blockIdx.x / p.split, tile_step = gridDim.x / p.split;
+    bool waited = true;  // false: a wait gave up
+
+    if (warp == 0 && lane == 0) {  // ---- operands to the ring
+        int64_t count = 0;
+        for (int64_t t = tile0; t < tiles && waited; t += tile_step) {
+            const Place at = tile_place(p, t, BN);
+            for (int64_t k = first; k < last; ++k, ++count) {
+                const int s = static_cast<int>(count % STAGES), turn = static_cast<int>(count / STAGES) & 1;
+                waited = barrier_wait(empty + 8 * s, turn ^ 1);
+                if (!waited) break;
+                const uint32_t bar = full + 8 * s, a = ring + s * STAGE, b = a + A_BYTES;
+                barrier_expect(bar, STAGE);
+                const int x = static_cast<int>(k * TC_K), m = static_cast<int>(at.m), n = static_cast<int>(at.n);
+                if (p.a_across) {
+#pragma unroll
+                    for (int h = 0; h < TC_M / 64; ++h) tma_load(a + h * HALF_BYTES, &map_a, m + 64 * h, x, bar);
+                } else {
+                    tma_load(a, &map_a, x, m, bar);
+                }
+                if (BN >= 64 && p.b_across) {
+#pragma unroll
+                    for (int h = 0; h < BN / 64; ++h) tma_load(b + h * HALF_BYTES, &map_b, n + 64 * h, x, bar);
+                } else {
+                    tma_load(b, &map_b, x, n, bar);
+                }
+            }
+        }
+        if (!waited)  // what is in flight has to land before the block ends
+            for (int64_t c = count < STAGES ? 0 : count - STAGES; c < count; ++c)
+                barrier_wait(full + 8 * static_cast<int>(c % STAGES), static_cast<int>(c / STAGES) & 1);
+    } else if (warp == 1 && lane == 0) {  // ---- matrix instructions
+        const uint32_t form = instruction_form<T>(p.a_across, p.b_across, BN);
+        const uint64_t form_a = operand_form(p.a_across), form_b = operand_form(p.b_across);
+        const uint32_t step_a = p.a_across ? 128 : 2, step_b = p.b_across ? 128 : 2;  // 16 of k, in 16 bytes
+        int64_t count = 0, tile_count = 0;
+        for (int64_t t = tile0; t < tiles && waited; t += tile_step, ++tile_count) {
+            const int set = static_cast<int>(tile_count & 1), turn = static_cast<int>(tile_count >> 1) & 1;
+            waited = barrier_wait(free_ + 8 * set, turn ^ 1);
+            if (!waited) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            for (int64_t k = first; k < last; ++k, ++count) {
+                const int s = static_cast<int>(count % STAGES);
+                waited = barrier_wait(full + 8 * s, static_cast<int>(count / STAGES) & 1);
+                if (!waited) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                // Descriptors have 14 bits of an address; a cluster's blocks have their rank above bit 23 of it.
+                const uint32_t a = ((ring + s * STAGE) & 0x3ffff) >> 4, b = a + A_BYTES / 16;
+#pragma unroll
+                for (int i = 0; i < TC_K / 16; ++i)
+                    mma(tensor + set * BN, form_a | (a + i * step_a), form_b | (b + i * step_b), form, k > first || i > 0);
+                mma_commit(empty + 8 * s);
+            }
+            if (waited) mma_commit(done + 8 * set);
+        }
+        if (!waited) {  // instructions in flight end before the block does
+            mma_commit(done);
+            barrier_wait(done, 0);
+        }
+    } else if (warp >= 2) {  // ---- results
+        const int writer = threadIdx.x - 64, quarter = warp % 4, row = quarter * 32 + lane, side = (warp - 2) / 4;
+        int64_t tile_count = 0;
+        for (int64_t t = tile0; t < tiles; t += tile_step, ++tile_count) {
+            const Place at = tile_place(p, t, BN);
+            const int set = static_cast<int>(tile_count & 1), turn = static_cast<int>(tile_count >> 1) & 1;
+            const int64_t bias0 = SWAP ? at.m : at.n, biases = SWAP ? p.m : p.n;
+            for (int e = writer; e < (SWAP ? TC_M : BN); e += TC_WRITERS)
+                bias_s[set][e] = p.bias && bias0 + e < biases ? load_param<T>(p.bias, p.bias_f32, bias0 + e) : 0.0f;
+            asm volatile("bar.sync 1, %0;" ::"n"(TC_WRITERS) : "memory");
+            if (waited) waited = barrier_wait(done + 8 * set, turn, TC_TILE_PATIENCE);
+            // Given up: no number comes out of what should have been summed.
+            const float lost = waited ? 0.0f : NAN;
+            if (!waited && p.status && writer == 0) set_status(p.status, NMS_ERR_TIMEOUT);
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t acc = tensor + set * BN + (static_cast<uint32_t>(quarter * 32) << 16);
+            const int64_t m = at.m + row;
+            if (p.split > 1) {
+                // The block's part to its own shared memory: the ring is empty by now.
+                float* part = reinterpret_cast<float*>(dynamic + (ring - shared_address(dynamic))) + row * (BN + 4);
+#pragma unroll
+                for (int c = side * (BN / 2); c < (side + 1) * (BN / 2); c += 8) {
+                    float v[8];
+                    tensor_load(v, acc + c);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) part[c + i] = first < last ? v[i] + lost : 0.0f;
+                }
+                break;  // one tile a cluster
+            }
+#pragma unroll 1
+            for (int c = side * (BN / 2); c < (side + 1) * (BN / 2); c += CHUNK) {
+                float v[CHUNK];
+                __syncwarp();
+                tensor_load(v, acc + c);
+                if (lost != 0.0f) {
+#pragma unroll
+                    for (int i = 0; i < CHUNK; ++i) v[i] = lost;
+                }
+                if (m >= p.m) continue;
+                if constexpr (SWAP) {
+#pragma unroll
+                    for (int i = 0; i < CHUNK; ++i)
+                        if (at.n + c + i < p.n) finish_one<T>(p, m, at.n + c + i, v[i], bias_s[set][row]);
+                } else {
+                    if (p.vector && at.n + c + CHUNK <= p.n) {
+#pragma unroll
+                        for (int i = 0; i < CHUNK; i += 8) finish_eight<T>(p, m, at.n + c + i, v + i, &bias_s[set][c + i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < CHUNK; ++i)
+                            if (at.n + c + i < p.n) finish_one<T>(p, m, at.n + c + i, v[i], bias_s[set][c + i]);
+                    }
+                }
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) barrier_arrive(free_ + 8 * set);
+        }
+    }
+    __syncwarp();
+    if (p.split > 1) {
+        asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (warp >= 2) {
+            // This block's rows of the tile, the parts added in the blocks' order.
+            const Place at = tile_place(p, tile0, BN);
+            const int rows = TC_M / p.split, writer = threadIdx.x - 64;
+            for (int e = writer; e < rows * BN; e += TC_WRITERS) {
+                const int r = rank * rows + (SWAP ? e % rows : e / BN), c = SWAP ? e / rows : e % BN;
+                if (at.m + r >= p.m || at.n + c >= p.n) continue;
+                float sum = 0.0f;
+                for (int b = 0; b < p.split; ++b) {
+                    float v;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(v)
+                                 : "r"(peer_address(ring + 4 * (r * (BN + 4) + c), b)));
+                    sum += v;
+                }
+                finish_one<T>(p, at.m + r, at.n + c, sum, bias_s[0][SWAP ? r : c]);
+            }
+        }
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tensor), "n"(COLUMNS));
+}
+
+// --------------------------------------------------------------------- host
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder()
+{
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// Rows of an operand, 64 columns a box (128 bytes: one swizzle span).
+bool encode(CUtensorMap* map, int type, const void* p, int64_t width, int64_t rows, int64_t row, int box_rows)
+{
+    const cuuint64_t size[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(row) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
+    const EncodeTiled fn = encoder();
+    return fn && fn(map, type == NMS_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                    const_cast<void*>(p), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int BN, bool SWAP>
+bool launch_tile(const CUtensorMap& a, const CUtensorMap& b, const TcArgs& p, cudaStream_t st)
+{
+    auto kernel = product_tc_kernel<T, BN, SWAP>;
+    // Once for each device: the attribute belongs to the kernel on the current one.
+    static std::atomic<uint64_t> ready{0};
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return false;
+    const uint64_t bit = uint64_t(1) << (device & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TC_SMEM<BN>) != cudaSuccess) return false;
+        if (device < 64) ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    const int64_t tiles = p.tiles_m * p.tiles_n;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.split > 1 ? tiles * p.split : tiles < SMS ? tiles : SMS));
+    cfg.blockDim = dim3(TC_THREADS);
+    cfg.dynamicSmemBytes = TC_SMEM<BN>;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a, b, p) == cudaSuccess;
+}
+
+template <typename T>
+bool launch_swapped(int bn, const CUtensorMap& a, const CUtensorMap& b, const TcArgs& p, cudaStream_t st)
+{
+    if (bn == 16) return launch_tile<T, 16, true>(a, b, p, st);
+    if (bn == 32) return launch_tile<T, 32, true>(a, b, p, st);
+    return launch_tile<T, 64, true>(a, b, p, st);
+}
+
+template <typename T>
+bool launch_straight(int bn, const CUtensorMap& a, const CUtensorMap& b, const TcArgs& p, cudaStream_t st)
+{
+    if (bn == 64) return launch_tile<T, 64, false>(a, b, p, st);
+    if (bn == 128) return launch_tile<T, 128, false>(a, b, p, st);
+    return launch_tile<T, 256, false>(a, b, p, st);
+}
+
+}  // namespace
+
+bool launch_product_tc(const ProductArgs& q, cudaStream_t st)
+{
+    TcArgs p{};
+    const bool swap = q.m <= 64 && !q.a_across;
+    p.k = q.k;
+    p.bias = q.bias;
+    p.bias_f32 = q.bias_f32;
+    p.act = q.act;
+    p.residual = q.residual;
+    p.out = q.out;
+    p.pre = q.pre;
+    p.status = q.status;
+    const void *a = q.a, *b = q.b;
+    int64_t a_row = q.a_row, b_row = q.b_row;
+    int bn;
+    if (swap) {
+        a = q.b;
+        b = q.a;
+        a_row = q.b_row;
+        b_row = q.a_row;
+        p.a_across = q.b_across;
+        p.b_across = q.a_across;
+        p.m = q.n;
+        p.n = q.m;
+        p.residual_m = p.out_m = 1;
+        p.residual_n = q.residual_row;
+        p.out_n = q.n;
+        bn = q.m <= 16 ? 16 : q.m <= 32 ? 32 : 64;
+    } else {
+        p.a_across = q.a_across;
+        p.b_across = q.b_across;
+        p.m = q.m;
+        p.n = q.n;
+        p.residual_m = q.residual_row;
+        p.out_m = q.n;
+        p.residual_n = p.out_n = 1;
+        auto aligned = [](const void* v) { return reinterpret_cast<uintptr_t>(v) % 16 == 0; };
+        p.vector = q.n % 8 == 0 && aligned(q.out) && aligned(q.pre) && aligned(q.residual) && q.residual_row % 8 == 0;
+        // The width whose waves of tiles cost least; a tile's time is its width's and a fixed part.
+        bn = 0;
+        int64_t best = 0;
+        for (int w : {256, 128, 64}) {
+            const int64_t tiles = ((p.m + TC_M - 1) / TC_M) * ((p.n + w - 1) / w);
+            const int64_t cost = ((tiles + SMS - 1) / SMS) * (w + 64);
+            if (bn == 0 || cost < best) {
+                bn = w;
+                best = cost;
+            }
+        }
+    }
+    p.tiles_m = (p.m + TC_M - 1) / TC_M;
+    p.tiles_n = (p.n + bn - 1) / bn;
+    const int64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + TC_K - 1) / TC_K;
+    p.split = 1;
+    while (p.split < 8 && tiles * p.split * 2 <= SMS && steps >= p.split * 4) p.split *= 2;
+    CUtensorMap map_a, map_b;
+    const bool known = (p.a_across ? encode(&map_a, q.type, a, p.m, p.k, a_row, 64) : encode(&map_a, q.type, a, p.k, p.m, a_row, TC_M)) &&
+                       (p.b_across ? encode(&map_b, q.type, b, p.n, p.k, b_row, 64) : encode(&map_b, q.type, b, p.k, p.n, b_row, bn));
+    if (!known) return false;
+    if (q.type == NMS_TYPE_F16)
+        return swap ? launch_swapped<__half>(bn, map_a, map_b, p, st) : launch_straight<__half>(bn, map_a, map_b, p, st);
+    return swap ? launch_swapped<__nv_bfloat16>(bn, map_a, map_b, p, st)
+                : launch_straight<__nv_bfloat16>(bn, map_a, map_b, p, st);
+}
+
+}  // namespace gbnms
