@@ -8,30 +8,42 @@ namespace {
 
 constexpr int JOIN_COLUMNS = 32, JOIN_SLOTS = 32;
 
-// A column's parts go to JOIN_SLOTS threads in turn, whose sums are added in order.
+// A column's parts go to JOIN_SLOTS threads in turn; then a warp has a column,
+// a lane a thread's sum, and joins them in a tree.
 __global__ void __launch_bounds__(JOIN_COLUMNS * JOIN_SLOTS)
 column_join_kernel(const float* parts, int64_t blocks, int64_t columns, int64_t split, float* first, float* second)
 {
-    __shared__ LongSum sums[JOIN_SLOTS][JOIN_COLUMNS];
+    __shared__ LongSum sums[JOIN_SLOTS][JOIN_COLUMNS + 1];
     pdl_wait();  // the parts are there
     const int64_t e = static_cast<int64_t>(blockIdx.x) * JOIN_COLUMNS + threadIdx.x;
     LongSum s{0.0f, 0.0f};
-    if (e < columns)
-        for (int64_t b = threadIdx.y; b < blocks; b += JOIN_SLOTS) s.add(parts[b * columns + e]);
+    if (e < columns) {
+        constexpr int AHEAD = 8;
+        for (int64_t b = threadIdx.y; b < blocks; b += AHEAD * JOIN_SLOTS) {
+            float v[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) v[k] = b + k * JOIN_SLOTS < blocks ? parts[(b + k * JOIN_SLOTS) * columns + e] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) s.add(v[k]);
+        }
+    }
     sums[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    if (threadIdx.y == 0 && e < columns) {
-        for (int k = 1; k < JOIN_SLOTS; ++k) s.add(sums[k][threadIdx.x]);
-        float* out = e < split ? first : second;
-        if (out) out[e < split ? e : e - split] = s.value();
+    s = sums[threadIdx.x][threadIdx.y];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s.add(LongSum{__shfl_down_sync(FULL, s.sum, o), __shfl_down_sync(FULL, s.off, o)});
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * JOIN_COLUMNS + threadIdx.y;
+    if (threadIdx.x == 0 && c < columns) {
+        float* out = c < split ? first : second;
+        if (out) out[c < split ? c : c - split] = s.value();
     }
 }
 
-void launch_rows(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
+int64_t launch_rows(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
 {
-    if (a.type == NMS_TYPE_F32) launch_layer_f32(a, parts, grad, st);
-    else if (a.type == NMS_TYPE_F16) launch_layer_f16(a, parts, grad, st);
-    else launch_layer_bf16(a, parts, grad, st);
+    if (a.type == NMS_TYPE_F32) return launch_layer_f32(a, parts, grad, st);
+    if (a.type == NMS_TYPE_F16) return launch_layer_f16(a, parts, grad, st);
+    return launch_layer_bf16(a, parts, grad, st);
 }
 
 }  // namespace
@@ -46,9 +58,9 @@ size_t layer_grad_workspace_bytes(int64_t rows, int width)
 void launch_layer_grad(const LayerArgs& a, void* workspace, cudaStream_t st)
 {
     float* parts = a.dweight || a.dbias ? static_cast<float*>(workspace) : nullptr;
-    launch_rows(a, parts, true, st);
+    const int64_t blocks = launch_rows(a, parts, true, st);
     if (!parts) return;
-    launch_column_join(parts, layer_grad_blocks(a.rows, a.width), 2 * static_cast<int64_t>(a.width), a.width, a.dweight,
+    launch_column_join(parts, blocks, 2 * static_cast<int64_t>(a.width), a.width, a.dweight,
                        a.dbias, st);
 }
 

@@ -44,7 +44,8 @@ __device__ __forceinline__ void team_sums(float& a, float& b, float (*shared)[2]
     }
 }
 
-// V consecutive parameters from element e on (the caller keeps e below the width).
+// V consecutive parameters from element e on (the caller keeps e below the
+// width), by the read-only path, so that they are fetched ahead of the stores.
 template <typename T, int V>
 __device__ __forceinline__ void load_params(float (&v)[V], const void* p, int is_f32, int e, float absent)
 {
@@ -52,17 +53,31 @@ __device__ __forceinline__ void load_params(float (&v)[V], const void* p, int is
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = absent;
     } else if (is_f32 || sizeof(T) == 4) {
-        constexpr int W = V > 4 ? 4 : V;
+        const float* q = static_cast<const float*>(p) + e;
+        if constexpr (V % 4 == 0) {
 #pragma unroll
-        for (int i = 0; i < V; i += W) {
-            const Pack<float, W> q = *reinterpret_cast<const Pack<float, W>*>(static_cast<const float*>(p) + e + i);
+            for (int i = 0; i < V; i += 4) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(q + i));
+                v[i] = f.x;
+                v[i + 1] = f.y;
+                v[i + 2] = f.z;
+                v[i + 3] = f.w;
+            }
+        } else {
 #pragma unroll
-            for (int j = 0; j < W; ++j) v[i + j] = q.v[j];
+            for (int i = 0; i < V; ++i) v[i] = __ldg(q + i);
         }
-    } else {
-        const Pack<T, V> q = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(p) + e);
+    } else if constexpr (sizeof(T) == 2) {
+        const T* q = static_cast<const T*>(p) + e;
+        if constexpr (V == 8) {
+            const uint4 f = __ldg(reinterpret_cast<const uint4*>(q));
+            const Pack<T, 8> h = *reinterpret_cast<const Pack<T, 8>*>(&f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = to_f32(q.v[i]);
+            for (int i = 0; i < V; ++i) v[i] = to_f32(h.v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = to_f32(__ldg(q + i));
+        }
     }
 }
 
@@ -95,12 +110,11 @@ layer_kernel(const LayerArgs a)
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int e = (k * TEAM + t) * V;
-            if (e >= a.width) break;
             float v[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = to_f32(q[k].v[i]) + to_f32(p[k].v[i]);
             q[k] = pack_results<T, V>(v);
-            *reinterpret_cast<Pack<T, V>*>(sum + e) = q[k];
+            if (e < a.width) *reinterpret_cast<Pack<T, V>*>(sum + e) = q[k];
         }
     }
     const float share = 1.0f / static_cast<float>(a.width);
@@ -140,116 +154,186 @@ layer_kernel(const LayerArgs a)
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int e = (k * TEAM + t) * V;
-        if (e >= a.width) break;
-        float w[V], b[V], v[V];
-        load_params<T, V>(w, a.weight, a.param_f32, e, 1.0f);
-        load_params<T, V>(b, a.bias, a.param_f32, e, 0.0f);
+        if (e < a.width) {
+            float w[V], b[V], v[V];
+            load_params<T, V>(w, a.weight, a.param_f32, e, 1.0f);
+            load_params<T, V>(b, a.bias, a.param_f32, e, 0.0f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = fmaf(((to_f32(q[k].v[i]) - mean) - off) * rstd, w[i], b[i]);
-        *reinterpret_cast<Pack<T, V>*>(y + e) = pack_results<T, V>(v);
+            for (int i = 0; i < V; ++i) v[i] = fmaf(((to_f32(q[k].v[i]) - mean) - off) * rstd, w[i], b[i]);
+            *reinterpret_cast<Pack<T, V>*>(y + e) = pack_results<T, V>(v);
+        }
     }
 }
 
-// Each block's sums of dy * u and of dy go to parts[block][2][width].
+// The gradient's rows on their way: each thread copies its own elements of x,
+// dy and dsum to its own places in shared memory (cp.async), a row ahead of the
+// one that is worked on, so nothing but the thread itself waits for them.
+template <int BYTES>
+__device__ __forceinline__ void copy_ahead(void* to, const void* from)
+{
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
+}
+
+// Whether a block's rows and weights fit: else rows are read where they are needed.
 template <typename T, int V, int NV, int TEAM, int THREADS>
-__global__ void __launch_bounds__(THREADS, TEAM == 32 ? 3 : 1)
+constexpr bool LAYER_AHEAD = sizeof(T) * V >= 4 && 2 * 3 * THREADS * NV * V * sizeof(T) + TEAM * NV * V * 4 <= 112 * 1024;
+
+template <typename T, int V, int NV, int TEAM, int THREADS>
+constexpr int LAYER_GRAD_SMEM = TEAM * NV * V * 4 + (TEAM < THREADS ? TEAM * NV * V * 8 : 0) +
+                                (LAYER_AHEAD<T, V, NV, TEAM, THREADS> ? 2 * 3 * THREADS * NV * V * static_cast<int>(sizeof(T)) : 0);
+
+// Each block's sums of dy * u and of dy go to parts[block][2][width].
+template <typename T, int V, int NV, int TEAM, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS)
 layer_grad_kernel(const LayerArgs a, float* parts)
 {
     static_assert(TEAM == 32 || TEAM == THREADS, "a team is a warp or the block");
+    using Vec = Pack<T, V>;
+    constexpr bool AHEAD = LAYER_AHEAD<T, V, NV, TEAM, THREADS>;
+    constexpr int TEAMS = THREADS / TEAM, SPAN = TEAM * NV * V;
     __shared__ float shared[2][THREADS / 32][2];
-    extern __shared__ float columns[];  // [2][width], with a team a warp
-    constexpr int TEAMS = THREADS / TEAM;
+    extern __shared__ __align__(16) char dynamic[];
+    float* weights = reinterpret_cast<float*>(dynamic);   // [SPAN], 0 behind the width
+    float* columns = weights + SPAN;                      // [2][SPAN] where teams are warps
+    Vec* rows = reinterpret_cast<Vec*>(columns + (TEAMS > 1 ? 2 * SPAN : 0));  // [2][3][NV][THREADS]
     const int t = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + team;
+    auto fetch = [&](int64_t r, int set) {
+        const T* x = static_cast<const T*>(a.x) + r * a.x_row;
+        const T* dy = static_cast<const T*>(a.dy) + r * a.dy_row;
+        const T* more = a.second ? static_cast<const T*>(a.second) + r * a.second_row : nullptr;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int e = (k * TEAM + t) * V;
+            if (e < a.width) {
+                Vec* to = rows + (set * 3 * NV + k) * THREADS + threadIdx.x;
+                copy_ahead<sizeof(Vec)>(to, x + e);
+                copy_ahead<sizeof(Vec)>(to + NV * THREADS, dy + e);
+                if (more) copy_ahead<sizeof(Vec)>(to + 2 * NV * THREADS, more + e);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if constexpr (AHEAD) {
+        if (row < a.rows) fetch(row, 0);
+    }
+    float mean = 0.0f, rstd = 0.0f;
+    if (row < a.rows) {
+        mean = a.mean[row];
+        rstd = a.rstd[row];
+    }
+    for (int e = threadIdx.x; e < SPAN; e += THREADS)
+        weights[e] = e < a.width ? (a.weight ? load_param<T>(a.weight, a.param_f32, e) : 1.0f) : 0.0f;
+    __syncthreads();
     const float share = 1.0f / static_cast<float>(a.width);
     float dw[NV][V], db[NV][V];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.0f;
-    int turn = 0;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + team; row < a.rows;
-         row += static_cast<int64_t>(gridDim.x) * TEAMS) {
-        const T* x = static_cast<const T*>(a.x) + row * a.x_row;
-        const T* dy = static_cast<const T*>(a.dy) + row * a.dy_row;
-        Pack<T, V> q[NV], g[NV];
+    const Vec none{};
+    for (int set = 0; row < a.rows; row += step, set ^= 1) {
+        const float m = mean, r = rstd;
+        Vec q[AHEAD ? 1 : NV], g[AHEAD ? 1 : NV];
+        const Vec* here = rows + set * 3 * NV * THREADS + threadIdx.x;
+        if (row + step < a.rows) {
+            mean = a.mean[row + step];
+            rstd = a.rstd[row + step];
+        }
+        if constexpr (AHEAD) {
+            if (row + step < a.rows) {
+                fetch(row + step, set ^ 1);
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            }
+        } else {
+            const T* x = static_cast<const T*>(a.x) + row * a.x_row;
+            const T* dy = static_cast<const T*>(a.dy) + row * a.dy_row;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int e = (k * TEAM + t) * V;
-            if (e < a.width) {
-                q[k] = *reinterpret_cast<const Pack<T, V>*>(x + e);
-                g[k] = *reinterpret_cast<const Pack<T, V>*>(dy + e);
+            for (int k = 0; k < NV; ++k) {
+                const int e = (k * TEAM + t) * V;
+                q[k] = e < a.width ? *reinterpret_cast<const Vec*>(x + e) : none;
+                g[k] = e < a.width ? *reinterpret_cast<const Vec*>(dy + e) : none;
             }
         }
-        const float mean = a.mean[row], rstd = a.rstd[row];
         float first = 0.0f, along = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int e = (k * TEAM + t) * V;
-            if (e >= a.width) break;
-            float w[V];
-            load_params<T, V>(w, a.weight, a.param_f32, e, 1.0f);
+            const bool in = e < a.width;
+            const Vec xk = AHEAD ? (in ? here[k * THREADS] : none) : q[AHEAD ? 0 : k];
+            const Vec gk = AHEAD ? (in ? here[(NV + k) * THREADS] : none) : g[AHEAD ? 0 : k];
+            const Pack<float, V> w = *reinterpret_cast<const Pack<float, V>*>(weights + e);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float u = (to_f32(q[k].v[i]) - mean) * rstd, d = to_f32(g[k].v[i]), du = d * w[i];
+                const float u = (to_f32(xk.v[i]) - m) * r, d = to_f32(gk.v[i]), du = d * w.v[i];
                 dw[k][i] = fmaf(d, u, dw[k][i]);
                 db[k][i] += d;
                 first += du;
                 along = fmaf(du, u, along);
             }
         }
-        team_sums<TEAM>(first, along, shared[turn]);
-        turn ^= 1;
+        team_sums<TEAM>(first, along, shared[set]);
         first *= share;
         along *= share;
         T* dx = static_cast<T*>(a.out) + row * a.width;
-        const T* more = static_cast<const T*>(a.second) + (a.second ? row * a.second_row : 0);
+        const T* more = a.second ? static_cast<const T*>(a.second) + row * a.second_row : nullptr;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int e = (k * TEAM + t) * V;
-            if (e >= a.width) break;
-            float w[V], v[V];
-            load_params<T, V>(w, a.weight, a.param_f32, e, 1.0f);
+            if (e < a.width) {
+                const Vec xk = AHEAD ? here[k * THREADS] : q[AHEAD ? 0 : k], gk = AHEAD ? here[(NV + k) * THREADS] : g[AHEAD ? 0 : k];
+                const Pack<float, V> w = *reinterpret_cast<const Pack<float, V>*>(weights + e);
+                float v[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float u = (to_f32(q[k].v[i]) - mean) * rstd, du = to_f32(g[k].v[i]) * w[i];
-                v[i] = rstd * fmaf(-u, along, du - first);
-            }
-            if (a.second) {
-                const Pack<T, V> p = *reinterpret_cast<const Pack<T, V>*>(more + e);
+                for (int i = 0; i < V; ++i) {
+                    const float u = (to_f32(xk.v[i]) - m) * r, du = to_f32(gk.v[i]) * w.v[i];
+                    v[i] = r * fmaf(-u, along, du - first);
+                }
+                if (more) {
+                    const Vec p = AHEAD ? here[(2 * NV + k) * THREADS] : *reinterpret_cast<const Vec*>(more + e);
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] += to_f32(p.v[i]);
+                    for (int i = 0; i < V; ++i) v[i] += to_f32(p.v[i]);
+                }
+                *reinterpret_cast<Vec*>(dx + e) = pack_results<T, V>(v);
             }
-            *reinterpret_cast<Pack<T, V>*>(dx + e) = pack_results<T, V>(v);
         }
     }
     if (!parts) return;
     float* part = parts + static_cast<int64_t>(blockIdx.x) * 2 * a.width;
     if constexpr (TEAMS > 1) {
         // The block's teams one after another: a fixed order.
-        for (int turn_of = 0; turn_of < TEAMS; ++turn_of) {
-            if (team == turn_of) {
+        for (int now = 0; now < TEAMS; ++now) {
+            if (team == now) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         const int e = (k * TEAM + t) * V + i;
-                        if (e >= a.width) break;
-                        columns[e] = (turn_of ? columns[e] : 0.0f) + dw[k][i];
-                        columns[a.width + e] = (turn_of ? columns[a.width + e] : 0.0f) + db[k][i];
+                        columns[e] = (now ? columns[e] : 0.0f) + dw[k][i];
+                        columns[SPAN + e] = (now ? columns[SPAN + e] : 0.0f) + db[k][i];
                     }
             }
             __syncthreads();
         }
-        for (int e = threadIdx.x; e < 2 * a.width; e += THREADS) part[e] = columns[e];
+        for (int e = threadIdx.x; e < a.width; e += THREADS) {
+            part[e] = columns[e];
+            part[a.width + e] = columns[SPAN + e];
+        }
     } else {
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int e = (k * TEAM + t) * V + i;
-                if (e >= a.width) break;
-                part[e] = dw[k][i];
-                part[a.width + e] = db[k][i];
+                if (e < a.width) {
+                    part[e] = dw[k][i];
+                    part[a.width + e] = db[k][i];
+                }
             }
     }
 }
@@ -266,66 +350,75 @@ inline LayerShape layer_shape(int width)
 }
 constexpr int LAYER_GRAD_THREADS = 128;  // of a block whose teams are warps
 
-// Blocks of the gradient: all that the SMs hold, and more where a team's sums
-// would run over more than 256 rows.
+// Blocks of the gradient at most: all that the SMs hold, and more where a
+// team's sums would run over more than 256 rows.
 inline int64_t layer_grad_blocks(int64_t rows, int width)
 {
     const LayerShape s = layer_shape(width);
     const int64_t teams = s.team == 32 ? LAYER_GRAD_THREADS / 32 : 1;
-    const int64_t want = (rows + teams - 1) / teams, full = SMS * (s.team == 32 ? 3 : s.team == 128 ? 3 : 1);
+    const int64_t want = (rows + teams - 1) / teams, full = SMS * (s.team == 32 ? 6 : s.team == 128 ? 4 : 1);
     const int64_t least = (rows + 256 * teams - 1) / (256 * teams);
     return want < full ? want : least > full ? least : full;
 }
 
 template <typename T, int V, int TEAM, int VALUES>
-void launch_layer_rows(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
+int64_t launch_layer_rows(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
 {
     if (grad) {
         constexpr int THREADS = TEAM == 32 ? LAYER_GRAD_THREADS : TEAM;
-        const unsigned grid = static_cast<unsigned>(layer_grad_blocks(a.rows, a.width));
-        const size_t smem = TEAM == 32 ? 2 * a.width * sizeof(float) : 0;
-        layer_grad_kernel<T, V, VALUES / V, TEAM, THREADS><<<grid, THREADS, smem, st>>>(a, parts);
-    } else {
-        constexpr int THREADS = TEAM == 32 ? 256 : TEAM;
-        const int64_t teams = THREADS / TEAM;
-        const unsigned grid = static_cast<unsigned>((a.rows + teams - 1) / teams);
-        layer_kernel<T, V, VALUES / V, TEAM, THREADS><<<grid, THREADS, 0, st>>>(a);
+        // Registers: two sums a value, and some fifty.
+        constexpr int BLOCKS = TEAM == 512 ? 1 : VALUES == 32 ? 4 : VALUES == 16 ? 5 : 6;
+        constexpr int SMEM = LAYER_GRAD_SMEM<T, V, VALUES / V, TEAM, THREADS>;
+        constexpr int FIT = SMEM * BLOCKS <= 220 * 1024 ? BLOCKS : 220 * 1024 / SMEM;
+        auto kernel = layer_grad_kernel<T, V, VALUES / V, TEAM, THREADS, FIT>;
+        if (SMEM > 40 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        const int64_t most = layer_grad_blocks(a.rows, a.width), full = SMS * FIT;
+        // A team's rows: no more than 256, or one wave of blocks.
+        const int64_t teams = THREADS / TEAM, least = (a.rows + 256 * teams - 1) / (256 * teams);
+        const int64_t grid = most < full ? most : least > full ? least : full;
+        kernel<<<static_cast<unsigned>(grid), THREADS, SMEM, st>>>(a, parts);
+        return grid;
     }
+    constexpr int THREADS = TEAM == 32 ? 256 : TEAM;
+    const int64_t teams = THREADS / TEAM;
+    const unsigned grid = static_cast<unsigned>((a.rows + teams - 1) / teams);
+    layer_kernel<T, V, VALUES / V, TEAM, THREADS><<<grid, THREADS, 0, st>>>(a);
+    return 0;
 }
 
+// Returns the blocks that left parts.
 template <typename T, int V>
-void launch_layer_width(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
+int64_t launch_layer_width(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
 {
     const LayerShape s = layer_shape(a.width);
     if (s.team == 32) {
-        if (s.values == 8) launch_layer_rows<T, V, 32, 8>(a, parts, grad, st);
-        else if (s.values == 16) launch_layer_rows<T, V, 32, 16>(a, parts, grad, st);
-        else launch_layer_rows<T, V, 32, 32>(a, parts, grad, st);
-    } else if (s.team == 128) {
-        if (s.values == 16) launch_layer_rows<T, V, 128, 16>(a, parts, grad, st);
-        else launch_layer_rows<T, V, 128, 32>(a, parts, grad, st);
-    } else {
-        if (s.values == 16) launch_layer_rows<T, V, 512, 16>(a, parts, grad, st);
-        else launch_layer_rows<T, V, 512, 32>(a, parts, grad, st);
+        if (s.values == 8) return launch_layer_rows<T, V, 32, 8>(a, parts, grad, st);
+        if (s.values == 16) return launch_layer_rows<T, V, 32, 16>(a, parts, grad, st);
+        return launch_layer_rows<T, V, 32, 32>(a, parts, grad, st);
     }
+    if (s.team == 128) {
+        if (s.values == 16) return launch_layer_rows<T, V, 128, 16>(a, parts, grad, st);
+        return launch_layer_rows<T, V, 128, 32>(a, parts, grad, st);
+    }
+    if (s.values == 16) return launch_layer_rows<T, V, 512, 16>(a, parts, grad, st);
+    return launch_layer_rows<T, V, 512, 32>(a, parts, grad, st);
 }
 
 // Accesses of 16 bytes where every row starts at a multiple of them, else of
 // one element.
 template <typename T>
-void launch_layer_type(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
+int64_t launch_layer_type(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
 {
     constexpr int MOST = 16 / sizeof(T);
     auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     const bool wide = a.width % MOST == 0 && a.x_row % MOST == 0 && a.second_row % MOST == 0 && a.dy_row % MOST == 0 &&
                       aligned(a.x) && aligned(a.second) && aligned(a.dy) && aligned(a.out) && aligned(a.sum) &&
                       aligned(a.weight) && aligned(a.bias);
-    if (wide) launch_layer_width<T, MOST>(a, parts, grad, st);
-    else launch_layer_width<T, 1>(a, parts, grad, st);
+    return wide ? launch_layer_width<T, MOST>(a, parts, grad, st) : launch_layer_width<T, 1>(a, parts, grad, st);
 }
 
-void launch_layer_f32(const LayerArgs& a, float* parts, bool grad, cudaStream_t st);
-void launch_layer_f16(const LayerArgs& a, float* parts, bool grad, cudaStream_t st);
-void launch_layer_bf16(const LayerArgs& a, float* parts, bool grad, cudaStream_t st);
+int64_t launch_layer_f32(const LayerArgs& a, float* parts, bool grad, cudaStream_t st);
+int64_t launch_layer_f16(const LayerArgs& a, float* parts, bool grad, cudaStream_t st);
+int64_t launch_layer_bf16(const LayerArgs& a, float* parts, bool grad, cudaStream_t st);
 
 }  // namespace gbnms

@@ -3,9 +3,9 @@
 
 namespace gbnms {
 
-void launch_layer_bf16(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
+int64_t launch_layer_bf16(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
 {
-    launch_layer_type<__nv_bfloat16>(a, parts, grad, st);
+    return launch_layer_type<__nv_bfloat16>(a, parts, grad, st);
 }
 
 }  // namespace gbnms

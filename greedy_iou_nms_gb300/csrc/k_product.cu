@@ -10,6 +10,13 @@
 // across ([k][m], as both do for a weight's gradient) is taken as it lies: the
 // instruction reads either order, only boxes and descriptors differ.
 //
+// Two blocks on neighbouring SMs share a tile of 256 x BN where there are tiles
+// enough (PAIR): one thread's instructions work on both SMs' tensor cores, each
+// of which has its own 128 rows of A and half of B's in shared memory.  A block
+// alone has to write and read 24 KB there for every 256 cycles of multiplying
+// (48 KB a stage in, 48 KB out, 512 cycles), more than the 128 bytes a cycle
+// that shared memory moves; a pair has to move a third less.
+//
 // Few rows of A (a step of serving): A and B change places, so that the long
 // side fills the 128 lanes and BN is 16 to 64.  Few tiles: the blocks of a
 // cluster share one, each a stretch of k, and add up their parts through
@@ -35,8 +42,9 @@ constexpr uint64_t TC_TILE_PATIENCE = 10000000000;  // 2^31 of k take a second
 constexpr int A_BYTES = TC_M * TC_K * 2;
 constexpr int HALF_BYTES = 64 * TC_K * 2;   // a box of an operand that lies across: 64 of m or n, 64 of k
 
-template <int BN> constexpr int TC_STAGES = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-template <int BN> constexpr int TC_SMEM = 1024 + TC_STAGES<BN> * (A_BYTES + BN * TC_K * 2);  // from a multiple of 1024 on
+// BB: rows of B in a block's stage.
+template <int BB> constexpr int TC_STAGES = BB == 256 ? 4 : BB == 128 ? 6 : 8;
+template <int BB> constexpr int TC_SMEM = 1024 + TC_STAGES<BB> * (A_BYTES + BB * TC_K * 2);  // from a multiple of 1024 on
 
 struct TcArgs {
     int a_across, b_across;
@@ -71,6 +79,19 @@ __device__ __forceinline__ void barrier_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __forceinline__ uint32_t peer_address(uint32_t at, int rank)
+{
+    uint32_t peer;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(at), "r"(rank));
+    return peer;
+}
+
+// Arrives at a barrier of another block of the cluster.
+__device__ __forceinline__ void barrier_arrive_at(uint32_t peer)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer) : "memory");
+}
+
 __device__ __forceinline__ bool barrier_done(uint32_t bar, int parity)
 {
     uint32_t done;
@@ -95,27 +116,62 @@ __device__ __forceinline__ bool barrier_wait(uint32_t bar, int parity, uint64_t 
     return false;
 }
 
+// PAIR: the barrier is the pair's first block's (an address without the rank's bit).
+template <bool PAIR>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(map), "r"(bar), "r"(x), "r"(y)
-        : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+            "[%2];" ::"r"(dst),
+            "l"(map), "r"(bar & 0xfeffffffu), "r"(x), "r"(y)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+            "l"(map), "r"(bar), "r"(x), "r"(y)
+            : "memory");
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t form, bool add)
 {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(form), "r"(static_cast<uint32_t>(add))
-        : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(form), "r"(static_cast<uint32_t>(add))
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(form), "r"(static_cast<uint32_t>(add))
+            : "memory");
 }
 
-// The barrier completes when all matrix instructions issued so far have.
+// The barrier (PAIR: each block's) completes when all matrix instructions
+// issued so far have.
+template <bool PAIR>
 __device__ __forceinline__ void mma_commit(uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// After a wait that gave up: what is in flight (copies, matrix instructions)
+// ends long before this does.
+__device__ __forceinline__ void settle()
+{
+    uint64_t start, now;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(start));
+    do asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+    while (now - start < 1000000);
 }
 
 // N columns of this thread's lane of tensor memory.
@@ -151,14 +207,14 @@ __device__ __forceinline__ uint64_t operand_form(int across)
     return (leading << 16) | (stride << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
-// Instruction descriptor: binary32 accumulators, both operands of T, 128 x bn.
+// Instruction descriptor: binary32 accumulators, both operands of T, rows x bn.
 template <typename T>
-__device__ __forceinline__ uint32_t instruction_form(int a_across, int b_across, int bn)
+__device__ __forceinline__ uint32_t instruction_form(int a_across, int b_across, int rows, int bn)
 {
     const uint32_t kind = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
     return (1u << 4) | (kind << 7) | (kind << 10) | (static_cast<uint32_t>(a_across) << 15) |
            (static_cast<uint32_t>(b_across) << 16) | (static_cast<uint32_t>(bn / 8) << 17) |
-           (static_cast<uint32_t>(TC_M / 16) << 24);
+           (static_cast<uint32_t>(rows / 16) << 24);
 }
 
 // -------------------------------------------------------------------- tiles
@@ -169,12 +225,12 @@ struct Place {
 
 // Tile t: strips of 16 tiles along n, within a strip n first, so that the tiles
 // that run together share rows of both operands in L2.
-__device__ __forceinline__ Place tile_place(const TcArgs& p, int64_t t, int bn)
+__device__ __forceinline__ Place tile_place(const TcArgs& p, int64_t t, int rows, int bn)
 {
     const int64_t strip = t / (16 * p.tiles_m), left = t - strip * 16 * p.tiles_m;
     const int64_t width = min(static_cast<int64_t>(16), p.tiles_n - strip * 16);
     const int64_t m = left / width;
-    return {m * TC_M, (strip * 16 + left - m * width) * bn};
+    return {m * rows, (strip * 16 + left - m * width) * bn};
 }
 
 // One result.
@@ -208,19 +264,18 @@ __device__ __forceinline__ void finish_eight(const TcArgs& p, int64_t m, int64_t
     *reinterpret_cast<Pack<T, 8>*>(static_cast<T*>(p.out) + at) = pack_results<T, 8>(z);
 }
 
-__device__ __forceinline__ uint32_t peer_address(uint32_t at, int rank)
+__device__ __forceinline__ void cluster_barrier()
 {
-    uint32_t peer;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(at), "r"(rank));
-    return peer;
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // SWAP: A's rows are results' columns (the operands changed places); bias by m.
-template <typename T, int BN, bool SWAP>
+template <typename T, int BN, bool SWAP, bool PAIR>
 __global__ void __launch_bounds__(TC_THREADS, 1)
 product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const TcArgs p)
 {
-    constexpr int STAGES = TC_STAGES<BN>, B_BYTES = BN * TC_K * 2, STAGE = A_BYTES + B_BYTES;
+    constexpr int BB = PAIR ? BN / 2 : BN, ROWS = PAIR ? 2 * TC_M : TC_M;  // of B in this block, of A in a tile
+    constexpr int STAGES = TC_STAGES<BB>, B_BYTES = BB * TC_K * 2, STAGE = A_BYTES + B_BYTES;
     constexpr int COLUMNS = 2 * BN < 32 ? 32 : 2 * BN;  // of tensor memory
     constexpr int CHUNK = BN >= 64 ? 32 : 8;            // columns that a thread carries at a time
     extern __shared__ char dynamic[];
@@ -237,58 +292,66 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         }
         for (int b = 0; b < 2; ++b) {
             barrier_init(done + 8 * b, 1);
-            barrier_init(free_ + 8 * b, TC_WRITERS / 32);
+            barrier_init(free_ + 8 * b, (PAIR ? 2 : 1) * TC_WRITERS / 32);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_address(&tensor_at)),
-                     "n"(COLUMNS)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_address(&tensor_at)),
+                         "n"(COLUMNS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_address(&tensor_at)),
+                         "n"(COLUMNS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
+    if constexpr (PAIR) cluster_barrier();  // the other block's barriers are there
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tensor = tensor_at;
     pdl_wait();
-    const int rank = static_cast<int>(blockIdx.x) % p.split;
+    const int share = PAIR ? 2 : p.split, rank = static_cast<int>(blockIdx.x) % share;  // of the cluster
     const int64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + TC_K - 1) / TC_K;
     const int64_t each = (steps + p.split - 1) / p.split;
-    const int64_t first = min(steps, rank * each), last = min(steps, first + each);  // of k, this block's
-    const int64_t tile0 = blockIdx.x / p.split, tile_step = gridDim.x / p.split;
+    const int64_t first = PAIR ? 0 : min(steps, rank * each), last = min(steps, first + each);  // of k, this block's
+    const int64_t tile0 = blockIdx.x / share, tile_step = gridDim.x / share;
     bool waited = true;  // false: a wait gave up
 
     if (warp == 0 && lane == 0) {  // ---- operands to the ring
         int64_t count = 0;
         for (int64_t t = tile0; t < tiles && waited; t += tile_step) {
-            const Place at = tile_place(p, t, BN);
+            const Place at = tile_place(p, t, ROWS, BN);
+            const int m = static_cast<int>(at.m) + (PAIR ? rank * TC_M : 0), n = static_cast<int>(at.n) + (PAIR ? rank * BB : 0);
             for (int64_t k = first; k < last; ++k, ++count) {
                 const int s = static_cast<int>(count % STAGES), turn = static_cast<int>(count / STAGES) & 1;
                 waited = barrier_wait(empty + 8 * s, turn ^ 1);
                 if (!waited) break;
                 const uint32_t bar = full + 8 * s, a = ring + s * STAGE, b = a + A_BYTES;
-                barrier_expect(bar, STAGE);
-                const int x = static_cast<int>(k * TC_K), m = static_cast<int>(at.m), n = static_cast<int>(at.n);
+                if (!PAIR) barrier_expect(bar, STAGE);
+                else if (rank == 0) barrier_expect(bar, 2 * STAGE);
+                const int x = static_cast<int>(k * TC_K);
                 if (p.a_across) {
 #pragma unroll
-                    for (int h = 0; h < TC_M / 64; ++h) tma_load(a + h * HALF_BYTES, &map_a, m + 64 * h, x, bar);
+                    for (int h = 0; h < TC_M / 64; ++h) tma_load<PAIR>(a + h * HALF_BYTES, &map_a, m + 64 * h, x, bar);
                 } else {
-                    tma_load(a, &map_a, x, m, bar);
+                    tma_load<PAIR>(a, &map_a, x, m, bar);
                 }
-                if (BN >= 64 && p.b_across) {
+                if (BB >= 64 && p.b_across) {
 #pragma unroll
-                    for (int h = 0; h < BN / 64; ++h) tma_load(b + h * HALF_BYTES, &map_b, n + 64 * h, x, bar);
+                    for (int h = 0; h < BB / 64; ++h) tma_load<PAIR>(b + h * HALF_BYTES, &map_b, n + 64 * h, x, bar);
                 } else {
-                    tma_load(b, &map_b, x, n, bar);
+                    tma_load<PAIR>(b, &map_b, x, n, bar);
                 }
             }
         }
-        if (!waited)  // what is in flight has to land before the block ends
-            for (int64_t c = count < STAGES ? 0 : count - STAGES; c < count; ++c)
-                barrier_wait(full + 8 * static_cast<int>(c % STAGES), static_cast<int>(c / STAGES) & 1);
-    } else if (warp == 1 && lane == 0) {  // ---- matrix instructions
-        const uint32_t form = instruction_form<T>(p.a_across, p.b_across, BN);
+        if (!waited) settle();
+    } else if (warp == 1 && lane == 0 && (!PAIR || rank == 0)) {  // ---- matrix instructions
+        const uint32_t form = instruction_form<T>(p.a_across, p.b_across, ROWS, BN);
         const uint64_t form_a = operand_form(p.a_across), form_b = operand_form(p.b_across);
         const uint32_t step_a = p.a_across ? 128 : 2, step_b = p.b_across ? 128 : 2;  // 16 of k, in 16 bytes
         int64_t count = 0, tile_count = 0;
@@ -306,20 +369,18 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 const uint32_t a = ((ring + s * STAGE) & 0x3ffff) >> 4, b = a + A_BYTES / 16;
 #pragma unroll
                 for (int i = 0; i < TC_K / 16; ++i)
-                    mma(tensor + set * BN, form_a | (a + i * step_a), form_b | (b + i * step_b), form, k > first || i > 0);
-                mma_commit(empty + 8 * s);
+                    mma<PAIR>(tensor + set * BN, form_a | (a + i * step_a), form_b | (b + i * step_b), form, k > first || i > 0);
+                mma_commit<PAIR>(empty + 8 * s);
             }
-            if (waited) mma_commit(done + 8 * set);
+            if (waited) mma_commit<PAIR>(done + 8 * set);
         }
-        if (!waited) {  // instructions in flight end before the block does
-            mma_commit(done);
-            barrier_wait(done, 0);
-        }
+        if (!waited) settle();
     } else if (warp >= 2) {  // ---- results
         const int writer = threadIdx.x - 64, quarter = warp % 4, row = quarter * 32 + lane, side = (warp - 2) / 4;
         int64_t tile_count = 0;
         for (int64_t t = tile0; t < tiles; t += tile_step, ++tile_count) {
-            const Place at = tile_place(p, t, BN);
+            Place at = tile_place(p, t, ROWS, BN);
+            if (PAIR) at.m += rank * TC_M;
             const int set = static_cast<int>(tile_count & 1), turn = static_cast<int>(tile_count >> 1) & 1;
             const int64_t bias0 = SWAP ? at.m : at.n, biases = SWAP ? p.m : p.n;
             for (int e = writer; e < (SWAP ? TC_M : BN); e += TC_WRITERS)
@@ -332,7 +393,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tensor + set * BN + (static_cast<uint32_t>(quarter * 32) << 16);
             const int64_t m = at.m + row;
-            if (p.split > 1) {
+            if (!PAIR && p.split > 1) {
                 // The block's part to its own shared memory: the ring is empty by now.
                 float* part = reinterpret_cast<float*>(dynamic + (ring - shared_address(dynamic))) + row * (BN + 4);
 #pragma unroll
@@ -371,15 +432,18 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
-            if (lane == 0) barrier_arrive(free_ + 8 * set);
+            if (lane == 0) {
+                if constexpr (PAIR) barrier_arrive_at(peer_address(free_ + 8 * set, 0));
+                else barrier_arrive(free_ + 8 * set);
+            }
         }
     }
     __syncwarp();
-    if (p.split > 1) {
-        asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (!PAIR && p.split > 1) {
+        cluster_barrier();
         if (warp >= 2) {
             // This block's rows of the tile, the parts added in the blocks' order.
-            const Place at = tile_place(p, tile0, BN);
+            const Place at = tile_place(p, tile0, ROWS, BN);
             const int rows = TC_M / p.split, writer = threadIdx.x - 64;
             for (int e = writer; e < rows * BN; e += TC_WRITERS) {
                 const int r = rank * rows + (SWAP ? e % rows : e / BN), c = SWAP ? e / rows : e % BN;
@@ -396,12 +460,16 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             }
         }
         __syncwarp();
-        asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    __syncthreads();
+    // No block leaves while another reads its shared memory or arrives at its barriers.
+    if (PAIR || p.split > 1) cluster_barrier();
+    else __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tensor), "n"(COLUMNS));
+    if (warp == 1) {
+        if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tensor), "n"(COLUMNS));
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tensor), "n"(COLUMNS));
+    }
 }
 
 // --------------------------------------------------------------------- host
@@ -436,28 +504,30 @@ bool encode(CUtensorMap* map, int type, const void* p, int64_t width, int64_t ro
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int BN, bool SWAP>
+template <typename T, int BN, bool SWAP, bool PAIR>
 bool launch_tile(const CUtensorMap& a, const CUtensorMap& b, const TcArgs& p, cudaStream_t st)
 {
-    auto kernel = product_tc_kernel<T, BN, SWAP>;
+    auto kernel = product_tc_kernel<T, BN, SWAP, PAIR>;
+    constexpr int SMEM = TC_SMEM<PAIR ? BN / 2 : BN>;
     // Once for each device: the attribute belongs to the kernel on the current one.
     static std::atomic<uint64_t> ready{0};
     int device = 0;
     if (cudaGetDevice(&device) != cudaSuccess) return false;
     const uint64_t bit = uint64_t(1) << (device & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TC_SMEM<BN>) != cudaSuccess) return false;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) return false;
         if (device < 64) ready.fetch_or(bit, std::memory_order_relaxed);
     }
     const int64_t tiles = p.tiles_m * p.tiles_n;
+    const int share = PAIR ? 2 : p.split;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.split > 1 ? tiles * p.split : tiles < SMS ? tiles : SMS));
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * share < SMS ? tiles * share : SMS / share * share));
     cfg.blockDim = dim3(TC_THREADS);
-    cfg.dynamicSmemBytes = TC_SMEM<BN>;
+    cfg.dynamicSmemBytes = SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = p.split;
+    attr[1].val.clusterDim.x = share;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
@@ -465,19 +535,17 @@ bool launch_tile(const CUtensorMap& a, const CUtensorMap& b, const TcArgs& p, cu
 }
 
 template <typename T>
-bool launch_swapped(int bn, const CUtensorMap& a, const CUtensorMap& b, const TcArgs& p, cudaStream_t st)
+bool launch_type(int bn, bool swap, bool pair, const CUtensorMap& a, const CUtensorMap& b, const TcArgs& p, cudaStream_t st)
 {
-    if (bn == 16) return launch_tile<T, 16, true>(a, b, p, st);
-    if (bn == 32) return launch_tile<T, 32, true>(a, b, p, st);
-    return launch_tile<T, 64, true>(a, b, p, st);
-}
-
-template <typename T>
-bool launch_straight(int bn, const CUtensorMap& a, const CUtensorMap& b, const TcArgs& p, cudaStream_t st)
-{
-    if (bn == 64) return launch_tile<T, 64, false>(a, b, p, st);
-    if (bn == 128) return launch_tile<T, 128, false>(a, b, p, st);
-    return launch_tile<T, 256, false>(a, b, p, st);
+    if (swap) {
+        if (bn == 16) return launch_tile<T, 16, true, false>(a, b, p, st);
+        if (bn == 32) return launch_tile<T, 32, true, false>(a, b, p, st);
+        return launch_tile<T, 64, true, false>(a, b, p, st);
+    }
+    if (pair) return bn == 128 ? launch_tile<T, 128, false, true>(a, b, p, st) : launch_tile<T, 256, false, true>(a, b, p, st);
+    if (bn == 64) return launch_tile<T, 64, false, false>(a, b, p, st);
+    if (bn == 128) return launch_tile<T, 128, false, false>(a, b, p, st);
+    return launch_tile<T, 256, false, false>(a, b, p, st);
 }
 
 }  // namespace
@@ -486,6 +554,7 @@ bool launch_product_tc(const ProductArgs& q, cudaStream_t st)
 {
     TcArgs p{};
     const bool swap = q.m <= 64 && !q.a_across;
+    bool pair = false;
     p.k = q.k;
     p.bias = q.bias;
     p.bias_f32 = q.bias_f32;
@@ -520,31 +589,37 @@ bool launch_product_tc(const ProductArgs& q, cudaStream_t st)
         p.residual_n = p.out_n = 1;
         auto aligned = [](const void* v) { return reinterpret_cast<uintptr_t>(v) % 16 == 0; };
         p.vector = q.n % 8 == 0 && aligned(q.out) && aligned(q.pre) && aligned(q.residual) && q.residual_row % 8 == 0;
-        // The width whose waves of tiles cost least; a tile's time is its width's and a fixed part.
+        // The tile whose waves cost least: a tile takes its width (a third more where one block has it alone, see above)
+        // and a fixed part.
         bn = 0;
         int64_t best = 0;
-        for (int w : {256, 128, 64}) {
-            const int64_t tiles = ((p.m + TC_M - 1) / TC_M) * ((p.n + w - 1) / w);
-            const int64_t cost = ((tiles + SMS - 1) / SMS) * (w + 64);
-            if (bn == 0 || cost < best) {
-                bn = w;
-                best = cost;
+        for (int two = 1; two >= 0; --two)
+            for (int w : {256, 128, 64}) {
+                if (two && w == 64) continue;
+                const int64_t rows = two ? 2 * TC_M : TC_M, slots = two ? SMS / 2 : SMS;
+                const int64_t tiles = ((p.m + rows - 1) / rows) * ((p.n + w - 1) / w);
+                const int64_t cost = ((tiles + slots - 1) / slots) * ((two ? 3 * w : 4 * w) + 192);
+                if (bn == 0 || cost < best) {
+                    bn = w;
+                    pair = two;
+                    best = cost;
+                }
             }
-        }
     }
-    p.tiles_m = (p.m + TC_M - 1) / TC_M;
+    const int64_t rows = pair ? 2 * TC_M : TC_M;
+    p.tiles_m = (p.m + rows - 1) / rows;
     p.tiles_n = (p.n + bn - 1) / bn;
     const int64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + TC_K - 1) / TC_K;
     p.split = 1;
-    while (p.split < 8 && tiles * p.split * 2 <= SMS && steps >= p.split * 4) p.split *= 2;
+    while (!pair && p.split < 8 && tiles * p.split * 2 <= SMS && steps >= p.split * 4) p.split *= 2;
     CUtensorMap map_a, map_b;
-    const bool known = (p.a_across ? encode(&map_a, q.type, a, p.m, p.k, a_row, 64) : encode(&map_a, q.type, a, p.k, p.m, a_row, TC_M)) &&
-                       (p.b_across ? encode(&map_b, q.type, b, p.n, p.k, b_row, 64) : encode(&map_b, q.type, b, p.k, p.n, b_row, bn));
+    const bool known =
+        (p.a_across ? encode(&map_a, q.type, a, p.m, p.k, a_row, 64) : encode(&map_a, q.type, a, p.k, p.m, a_row, TC_M)) &&
+        (p.b_across ? encode(&map_b, q.type, b, p.n, p.k, b_row, 64)
+                    : encode(&map_b, q.type, b, p.k, p.n, b_row, pair ? bn / 2 : bn));
     if (!known) return false;
-    if (q.type == NMS_TYPE_F16)
-        return swap ? launch_swapped<__half>(bn, map_a, map_b, p, st) : launch_straight<__half>(bn, map_a, map_b, p, st);
-    return swap ? launch_swapped<__nv_bfloat16>(bn, map_a, map_b, p, st)
-                : launch_straight<__nv_bfloat16>(bn, map_a, map_b, p, st);
+    return q.type == NMS_TYPE_F16 ? launch_type<__half>(bn, swap, pair, map_a, map_b, p, st)
+                                  : launch_type<__nv_bfloat16>(bn, swap, pair, map_a, map_b, p, st);
 }
 
 }  // namespace gbnms
