@@ -323,12 +323,11 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     bool waited = true;  // false: a wait gave up
 
     if (warp == 0 && lane == 0) {  // ---- operands to the ring
-        int64_t count = 0;
+        int s = 0, turn = 0;
         for (int64_t t = tile0; t < tiles && waited; t += tile_step) {
             const Place at = tile_place(p, t, ROWS, BN);
             const int m = static_cast<int>(at.m) + (PAIR ? rank * TC_M : 0), n = static_cast<int>(at.n) + (PAIR ? rank * BB : 0);
-            for (int64_t k = first; k < last; ++k, ++count) {
-                const int s = static_cast<int>(count % STAGES), turn = static_cast<int>(count / STAGES) & 1;
+            for (int64_t k = first; k < last; ++k) {
                 waited = barrier_wait(empty + 8 * s, turn ^ 1);
                 if (!waited) break;
                 const uint32_t bar = full + 8 * s, a = ring + s * STAGE, b = a + A_BYTES;
@@ -347,6 +346,10 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 } else {
                     tma_load<PAIR>(b, &map_b, x, n, bar);
                 }
+                if (++s == STAGES) {
+                    s = 0;
+                    turn ^= 1;
+                }
             }
         }
         if (!waited) settle();
@@ -354,15 +357,13 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         const uint32_t form = instruction_form<T>(p.a_across, p.b_across, ROWS, BN);
         const uint64_t form_a = operand_form(p.a_across), form_b = operand_form(p.b_across);
         const uint32_t step_a = p.a_across ? 128 : 2, step_b = p.b_across ? 128 : 2;  // 16 of k, in 16 bytes
-        int64_t count = 0, tile_count = 0;
-        for (int64_t t = tile0; t < tiles && waited; t += tile_step, ++tile_count) {
-            const int set = static_cast<int>(tile_count & 1), turn = static_cast<int>(tile_count >> 1) & 1;
-            waited = barrier_wait(free_ + 8 * set, turn ^ 1);
+        int s = 0, turn = 0, set = 0, set_turn = 0;
+        for (int64_t t = tile0; t < tiles && waited; t += tile_step) {
+            waited = barrier_wait(free_ + 8 * set, set_turn ^ 1);
             if (!waited) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            for (int64_t k = first; k < last; ++k, ++count) {
-                const int s = static_cast<int>(count % STAGES);
-                waited = barrier_wait(full + 8 * s, static_cast<int>(count / STAGES) & 1);
+            for (int64_t k = first; k < last; ++k) {
+                waited = barrier_wait(full + 8 * s, turn);
                 if (!waited) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 // Descriptors have 14 bits of an address; a cluster's blocks have their rank above bit 23 of it.
@@ -371,8 +372,14 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 for (int i = 0; i < TC_K / 16; ++i)
                     mma<PAIR>(tensor + set * BN, form_a | (a + i * step_a), form_b | (b + i * step_b), form, k > first || i > 0);
                 mma_commit<PAIR>(empty + 8 * s);
+                if (++s == STAGES) {
+                    s = 0;
+                    turn ^= 1;
+                }
             }
             if (waited) mma_commit<PAIR>(done + 8 * set);
+            set_turn ^= set;
+            set ^= 1;
         }
         if (!waited) settle();
     } else if (warp >= 2) {  // ---- results
@@ -445,18 +452,26 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             // This block's rows of the tile, the parts added in the blocks' order.
             const Place at = tile_place(p, tile0, ROWS, BN);
             const int rows = TC_M / p.split, writer = threadIdx.x - 64;
-            for (int e = writer; e < rows * BN; e += TC_WRITERS) {
-                const int r = rank * rows + (SWAP ? e % rows : e / BN), c = SWAP ? e / rows : e % BN;
+            for (int e = writer; e < rows * BN / 4; e += TC_WRITERS) {
+                const int r = rank * rows + (SWAP ? e % rows : e / (BN / 4)), c = 4 * (SWAP ? e / rows : e % (BN / 4));
                 if (at.m + r >= p.m || at.n + c >= p.n) continue;
-                float sum = 0.0f;
-                for (int b = 0; b < p.split; ++b) {
-                    float v;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                 : "=f"(v)
-                                 : "r"(peer_address(ring + 4 * (r * (BN + 4) + c), b)));
-                    sum += v;
-                }
-                finish_one<T>(p, at.m + r, at.n + c, sum, bias_s[0][SWAP ? r : c]);
+                const uint32_t from = ring + 4 * (r * (BN + 4) + c);
+                float sum[4] = {}, v[8][4];
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                    if (b < p.split)
+                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(v[b][0]), "=f"(v[b][1]), "=f"(v[b][2]), "=f"(v[b][3])
+                                     : "r"(peer_address(from, b)));
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                    if (b < p.split) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sum[i] += v[b][i];
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (at.n + c + i < p.n) finish_one<T>(p, at.m + r, at.n + c + i, sum[i], bias_s[0][SWAP ? r : c + i]);
             }
         }
         __syncwarp();
@@ -611,7 +626,7 @@ bool launch_product_tc(const ProductArgs& q, cudaStream_t st)
     p.tiles_n = (p.n + bn - 1) / bn;
     const int64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + TC_K - 1) / TC_K;
     p.split = 1;
-    while (!pair && p.split < 8 && tiles * p.split * 2 <= SMS && steps >= p.split * 4) p.split *= 2;
+    while (!pair && p.split < 8 && tiles * p.split * 2 <= SMS && steps >= p.split * 8) p.split *= 2;
     CUtensorMap map_a, map_b;
     const bool known =
         (p.a_across ? encode(&map_a, q.type, a, p.m, p.k, a_row, 64) : encode(&map_a, q.type, a, p.k, p.m, a_row, TC_M)) &&

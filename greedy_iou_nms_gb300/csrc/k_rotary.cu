@@ -18,6 +18,9 @@ namespace gbnms {
 namespace {
 
 constexpr int RO_THREADS = 256;
+#ifndef RO_ENOUGH
+#define RO_ENOUGH 2048
+#endif
 
 struct RotaryPlan {
     int units;       // threads' shares of a token: turned ones, then copied ones
@@ -77,8 +80,8 @@ __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d)
 }
 
 // VP: pairs of a thread; with VP > 1 they are two accesses of VP elements a head.
-template <typename T, int VP, int HB>
-__global__ void __launch_bounds__(RO_THREADS)
+template <typename T, int VP, int HB, bool HALVES>
+__global__ void __launch_bounds__(RO_THREADS, 3)
 rotary_kernel(const RotaryArgs a, const RotaryPlan plan)
 {
     const int64_t item = static_cast<int64_t>(blockIdx.x) * RO_THREADS + threadIdx.x;
@@ -100,7 +103,7 @@ rotary_kernel(const RotaryArgs a, const RotaryPlan plan)
     }
     const int pair = unit * VP;
     // Elements of the two accesses: first and second of each pair, or pairs one after another.
-    const int e0 = a.halves ? pair : 2 * pair, e1 = a.halves ? pair + a.pairs : 2 * pair + VP;
+    const int e0 = HALVES ? pair : 2 * pair, e1 = HALVES ? pair + a.pairs : 2 * pair + VP;
     const int64_t where = ((a.sets == 1 ? 0 : batch) * a.tokens + token) * a.axes;
     float s[VP], c[VP];
     Vec lo[HB], hi[HB];
@@ -116,31 +119,28 @@ rotary_kernel(const RotaryArgs a, const RotaryPlan plan)
 #pragma unroll
         for (int b = 0; b < HB; ++b) {
             if (h + b >= last) break;
-            float p[VP], q[VP];
-#pragma unroll
-            for (int i = 0; i < VP; ++i) {
-                p[i] = to_f32(lo[b].v[i]);
-                q[i] = to_f32(hi[b].v[i]);
-            }
+            const Vec p = lo[b], q = hi[b];
             if (h + HB + b < last) {  // the next heads' while these are worked on
                 lo[b] = *reinterpret_cast<const Vec*>(x + (HB + b) * a.x_head + e0);
                 hi[b] = *reinterpret_cast<const Vec*>(x + (HB + b) * a.x_head + e1);
             }
             float u[VP], v[VP];
-            if (a.halves || VP == 1) {
+            if constexpr (HALVES || VP == 1) {
 #pragma unroll
                 for (int i = 0; i < VP; ++i) {
-                    u[i] = fmaf(p[i], c[i], -q[i] * s[i]);
-                    v[i] = fmaf(q[i], c[i], p[i] * s[i]);
+                    const float pi = to_f32(p.v[i]), qi = to_f32(q.v[i]);
+                    u[i] = fmaf(pi, c[i], -qi * s[i]);
+                    v[i] = fmaf(qi, c[i], pi * s[i]);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < VP; i += 2) {
                     const int k = i / 2, m = VP / 2 + k;
-                    u[i] = fmaf(p[i], c[k], -p[i + 1] * s[k]);
-                    u[i + 1] = fmaf(p[i + 1], c[k], p[i] * s[k]);
-                    v[i] = fmaf(q[i], c[m], -q[i + 1] * s[m]);
-                    v[i + 1] = fmaf(q[i + 1], c[m], q[i] * s[m]);
+                    const float p0 = to_f32(p.v[i]), p1 = to_f32(p.v[i + 1]), q0 = to_f32(q.v[i]), q1 = to_f32(q.v[i + 1]);
+                    u[i] = fmaf(p0, c[k], -p1 * s[k]);
+                    u[i + 1] = fmaf(p1, c[k], p0 * s[k]);
+                    v[i] = fmaf(q0, c[m], -q1 * s[m]);
+                    v[i + 1] = fmaf(q1, c[m], q0 * s[m]);
                 }
             }
             *reinterpret_cast<Vec*>(y + b * a.y_head + e0) = pack_results<T, VP>(u);
@@ -165,15 +165,16 @@ void launch(const RotaryArgs& a, cudaStream_t st)
     p.turned = a.pairs / vp;
     p.units = p.turned + (a.dim - 2 * a.pairs) / vp;
     // A thread takes all heads of its token once there are threads enough for every SM without splitting them.
-    const int64_t tokens = a.batch * a.tokens, whole = tokens * p.units, enough = static_cast<int64_t>(SMS) * 2048;
+    const int64_t tokens = a.batch * a.tokens, whole = tokens * p.units, enough = static_cast<int64_t>(SMS) * RO_ENOUGH;
     p.head_step = a.heads;
     while (p.head_step > 1 && whole * ((a.heads + p.head_step - 1) / p.head_step) < enough)
         p.head_step = (p.head_step + 1) / 2;
     p.head_parts = (a.heads + p.head_step - 1) / p.head_step;
     p.items = whole * p.head_parts;
     const unsigned grid = static_cast<unsigned>((p.items + RO_THREADS - 1) / RO_THREADS);
-    if (wide) rotary_kernel<T, MOST, 2><<<grid, RO_THREADS, 0, st>>>(a, p);
-    else rotary_kernel<T, 1, 4><<<grid, RO_THREADS, 0, st>>>(a, p);
+    auto run = [&](auto kernel) { kernel<<<grid, RO_THREADS, 0, st>>>(a, p); };
+    if (wide) a.halves ? run(rotary_kernel<T, MOST, 2, true>) : run(rotary_kernel<T, MOST, 2, false>);
+    else a.halves ? run(rotary_kernel<T, 1, 4, true>) : run(rotary_kernel<T, 1, 4, false>);
 }
 
 }  // namespace

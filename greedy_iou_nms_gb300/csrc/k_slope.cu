@@ -16,7 +16,7 @@ namespace {
 constexpr int SL_SLOTS = 8;
 
 template <typename T, int V>
-__global__ void __launch_bounds__(32 * SL_SLOTS)
+__global__ void __launch_bounds__(32 * SL_SLOTS, 4)
 slope_kernel(const SlopeArgs s, int64_t run, float* parts)
 {
     __shared__ float sums[SL_SLOTS][32 * V];
@@ -27,7 +27,7 @@ slope_kernel(const SlopeArgs s, int64_t run, float* parts)
         const T* dy = static_cast<const T*>(s.dy) + e;
         const T* pre = static_cast<const T*>(s.pre) + e;
         T* dz = static_cast<T*>(s.dz) + e;
-        constexpr int AHEAD = 4;  // rows of a lane in flight
+        constexpr int AHEAD = 2;  // rows of a lane in flight
         for (int64_t row = first + threadIdx.y; row < last; row += AHEAD * SL_SLOTS) {
             Pack<T, V> g[AHEAD], z[AHEAD];
 #pragma unroll
