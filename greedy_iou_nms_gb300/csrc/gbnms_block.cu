@@ -323,7 +323,8 @@ extern "C" nms_status nms_rotary_run(const void* x, int64_t x_batch, int64_t x_t
         tokens < 0 || heads < 0 || dim < 1 || axes < 1 || pairs < 0 || pairs > dim / 2 || (sets != 1 && sets != batch))
         return NMS_ERR_INVALID_ARG;
     if (axes > NMS_ROTARY_MAX_AXES || dim > NMS_ROTARY_MAX_DIM || heads > (1 << 20) || batch > kMostRows ||
-        tokens > kMostRows || batch * tokens > kMostRows || too_far(batch * tokens, static_cast<int64_t>(heads) * dim))
+        tokens > kMostRows || batch * tokens > kMostRows || static_cast<int64_t>(heads) * dim > kMostRows ||
+        too_far(batch * tokens, static_cast<int64_t>(heads) * dim))
         return NMS_ERR_CAPACITY;
     const bool empty = batch == 0 || tokens == 0 || heads == 0;
     if (empty) return NMS_OK;

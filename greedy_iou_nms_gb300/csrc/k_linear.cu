@@ -10,76 +10,88 @@ namespace gbnms {
 
 namespace {
 
-constexpr int PR_DEPTH = 16;  // of a step along k
+constexpr int PR_DEPTH = 16;   // of a step along k
+constexpr int PR_STAGES = 4;   // steps in shared memory
 
-// A step of one operand in registers: element i of a thread is at (mn, k).
-template <typename T, int TILE>
-struct Step {
-    static constexpr int N = TILE * PR_DEPTH / 256;
-    float v[N];
-    __device__ __forceinline__ static void place(int i, int across, int& mn, int& k)
+// One operand's way to shared memory, [k][m or n], element by element
+// (cp.async), so that any stride and start will do and either order of the
+// operand.  Element i of a thread lies i * delta behind its first.
+template <int TILE, bool ACROSS>
+struct Feed {
+    static constexpr int N = TILE * PR_DEPTH / 256, STRIDE = TILE + 4;
+    const float* from;
+    int64_t delta, step;
+    uint32_t to;
+    int64_t left_mn, left_k;  // elements from this thread's first on
+    __device__ __forceinline__ Feed(const float* p, int64_t row, int64_t mn0, int64_t mns, int64_t ks, const void* shared)
     {
-        const int at = i * 256 + threadIdx.x;
-        if (across) {
-            mn = at % TILE;
-            k = at / TILE;
-        } else {
-            k = at % PR_DEPTH;
-            mn = at / PR_DEPTH;
-        }
+        const int t = threadIdx.x, mn = ACROSS ? t % TILE : t / PR_DEPTH, k = ACROSS ? t / TILE : t % PR_DEPTH;
+        from = p + (ACROSS ? k * row + mn0 + mn : (mn0 + mn) * row + k);
+        delta = ACROSS ? (256 / TILE) * row : (256 / PR_DEPTH) * row;
+        step = ACROSS ? PR_DEPTH * row : PR_DEPTH;
+        to = static_cast<uint32_t>(__cvta_generic_to_shared(shared)) + 4 * (k * STRIDE + mn);
+        left_mn = mns - mn0 - mn;
+        left_k = ks - k;
     }
-    __device__ __forceinline__ void load(const T* p, int64_t row, int across, int64_t mn0, int64_t mns, int64_t k0,
-                                         int64_t ks)
+    // The next step; what lies outside becomes 0.
+    __device__ __forceinline__ void next(int stage)
     {
+        const float* p = from;
+        const uint32_t at = to + stage * (PR_DEPTH * STRIDE * 4);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            int mn, k;
-            place(i, across, mn, k);
-            const int64_t a = mn0 + mn, b = k0 + k;
-            v[i] = a < mns && b < ks ? to_f32(p[across ? b * row + a : a * row + b]) : 0.0f;
+        for (int i = 0; i < N; ++i, p += delta) {
+            const bool in = ACROSS ? left_mn > 0 && left_k > i * (256 / TILE) : left_k > 0 && left_mn > i * (256 / PR_DEPTH);
+            const uint32_t dst = at + 4 * i * (ACROSS ? (256 / TILE) * STRIDE : 256 / PR_DEPTH);
+            if (in) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(p) : "memory");
+            else asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst), "f"(0.0f) : "memory");
         }
-    }
-    __device__ __forceinline__ void store(float (*s)[TILE + 4], int across) const
-    {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            int mn, k;
-            place(i, across, mn, k);
-            s[k][mn] = v[i];
-        }
+        from += step;
+        left_k -= PR_DEPTH;
     }
 };
 
-template <typename T, int S>
+template <int S, bool A_ACROSS, bool B_ACROSS>
 __global__ void __launch_bounds__(256)
 product_kernel(const ProductArgs p, int64_t tiles_n)
 {
-    constexpr int TILE = 16 * S;
-    __shared__ float as[2][PR_DEPTH][TILE + 4], bs[2][PR_DEPTH][TILE + 4];
+    using T = float;
+    constexpr int TILE = 16 * S, STRIDE = TILE + 4;
+    extern __shared__ __align__(16) float stages[];  // [2][PR_STAGES][PR_DEPTH][STRIDE]
+    float* const as = stages;
+    float* const bs = stages + PR_STAGES * PR_DEPTH * STRIDE;
     const int64_t tm = blockIdx.x / tiles_n, tn = blockIdx.x - tm * tiles_n;
     const int64_t m0 = tm * TILE, n0 = tn * TILE;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     float acc[S][S] = {}, total[S][S] = {};
-    Step<T, TILE> a, b;
+    Feed<TILE, A_ACROSS> a(static_cast<const float*>(p.a), p.a_row, m0, p.m, p.k, as);
+    Feed<TILE, B_ACROSS> b(static_cast<const float*>(p.b), p.b_row, n0, p.n, p.k, bs);
     const int64_t steps = (p.k + PR_DEPTH - 1) / PR_DEPTH;
-    auto load = [&](int64_t s) {
-        a.load(static_cast<const T*>(p.a), p.a_row, p.a_across, m0, p.m, s * PR_DEPTH, p.k);
-        b.load(static_cast<const T*>(p.b), p.b_row, p.b_across, n0, p.n, s * PR_DEPTH, p.k);
-    };
-    load(0);
-    a.store(as[0], p.a_across);
-    b.store(bs[0], p.b_across);
-    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < PR_STAGES - 1; ++s) {
+        if (s < steps) {
+            a.next(s);
+            b.next(s);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    int at = 0, ahead = PR_STAGES - 1;
     for (int64_t s = 0; s < steps; ++s) {
-        const int at = static_cast<int>(s & 1);
-        if (s + 1 < steps) load(s + 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(PR_STAGES - 2) : "memory");
+        __syncthreads();  // step s is there, and step s - 1 is no longer read
+        if (s + PR_STAGES - 1 < steps) {
+            a.next(ahead);
+            b.next(ahead);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        const float* const ak = as + at * PR_DEPTH * STRIDE;
+        const float* const bk = bs + at * PR_DEPTH * STRIDE;
 #pragma unroll
         for (int k = 0; k < PR_DEPTH; ++k) {
             alignas(16) float x[S], w[S];
 #pragma unroll
             for (int i = 0; i < S; i += 4) {
-                *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(&as[at][k][i * 16 + ty * 4]);
-                *reinterpret_cast<float4*>(w + i) = *reinterpret_cast<const float4*>(&bs[at][k][i * 16 + tx * 4]);
+                *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(ak + k * STRIDE + i * 16 + ty * 4);
+                *reinterpret_cast<float4*>(w + i) = *reinterpret_cast<const float4*>(bk + k * STRIDE + i * 16 + tx * 4);
             }
 #pragma unroll
             for (int i = 0; i < S; ++i)
@@ -96,11 +108,8 @@ product_kernel(const ProductArgs p, int64_t tiles_n)
                     acc[i][j] = 0.0f;
                 }
         }
-        if (s + 1 < steps) {
-            a.store(as[at ^ 1], p.a_across);
-            b.store(bs[at ^ 1], p.b_across);
-            __syncthreads();
-        }
+        at = at + 1 == PR_STAGES ? 0 : at + 1;
+        ahead = ahead + 1 == PR_STAGES ? 0 : ahead + 1;
     }
     T* out = static_cast<T*>(p.out);
     T* pre = static_cast<T*>(p.pre);
@@ -138,13 +147,23 @@ copy_rows_kernel(const uint16_t* from, int64_t from_row, int64_t rows, int64_t w
 
 }  // namespace
 
+template <int S>
+static void launch_tiles(const ProductArgs& p, cudaStream_t st)
+{
+    constexpr int TILE = 16 * S, SMEM = 2 * PR_STAGES * PR_DEPTH * (TILE + 4) * 4;
+    const int64_t tiles_n = (p.n + TILE - 1) / TILE, tiles = ((p.m + TILE - 1) / TILE) * tiles_n;
+    auto run = [&](auto kernel) {
+        if (SMEM > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        kernel<<<static_cast<unsigned>(tiles), 256, SMEM, st>>>(p, tiles_n);
+    };
+    if (p.a_across) run(product_kernel<S, true, true>);
+    else p.b_across ? run(product_kernel<S, false, true>) : run(product_kernel<S, false, false>);
+}
+
 void launch_product_f32(const ProductArgs& p, cudaStream_t st)
 {
-    auto tiles = [&](int64_t t) { return ((p.m + t - 1) / t) * ((p.n + t - 1) / t); };
-    if (tiles(128) >= SMS)
-        product_kernel<float, 8><<<static_cast<unsigned>(tiles(128)), 256, 0, st>>>(p, (p.n + 127) / 128);
-    else
-        product_kernel<float, 4><<<static_cast<unsigned>(tiles(64)), 256, 0, st>>>(p, (p.n + 63) / 64);
+    if (((p.m + 127) / 128) * ((p.n + 127) / 128) >= SMS) launch_tiles<8>(p, st);
+    else launch_tiles<4>(p, st);
 }
 
 void launch_copy_rows(const void* from, int64_t from_row, int64_t rows, int64_t width, void* to, int64_t to_row,

@@ -5,10 +5,13 @@
 // the table's turns per position, a 64-bit product whose overflow is whole
 // turns.  So a position far into a history loses nothing (a binary32 angle of
 // 10^6 radians is off by 0.03), at the price of a few integer instructions; the
-// fraction's top 32 bits go to sincospif.
+// fraction's top 32 bits go on to the sine.
 //
-// A thread has VP pairs of one token and goes through its heads, so an angle's
-// sine and cosine are worked out once for all of them.
+// HBM bounds it, so an angle's sine and cosine are worked out once for all heads
+// of a token: a block has a run of tokens, makes their table in shared memory
+// and then goes through the tokens' vectors in the order in which they lie.  48
+// warps an SM with one access pair each in flight hide more than 32 with two (79
+// us for 91) or 24 with four.
 #include "block.h"
 #include "head.cuh"
 #include "internal.h"
@@ -18,16 +21,18 @@ namespace gbnms {
 namespace {
 
 constexpr int RO_THREADS = 256;
-#ifndef RO_ENOUGH
-#define RO_ENOUGH 2048
-#endif
+constexpr int RO_TABLE = 4096;  // sines and cosines of a block at most, 32 KB
+// Tokens of a block at most.  Blocks that start at different times overlap one's table with another's stream: 16 took
+// 79 us for 4 x 25600 x 16 x 64 bf16, 64 took 90, 4 took 104.
+constexpr int RO_TOKENS = 16;
 
 struct RotaryPlan {
-    int units;       // threads' shares of a token: turned ones, then copied ones
-    int turned;      // of these the turned ones
-    int head_parts;  // threads that share a token's heads
-    int head_step;   // heads of each
-    int64_t items;   // threads in all
+    int units;       // accesses of a vector: turned pairs of them, then copied ones
+    int turned;      // of these the turned pairs
+    int64_t each;    // accesses of a token: of all its heads
+    int slots;       // threads of a block that share a token
+    int run;         // tokens of a block
+    int64_t tokens;  // of all
 };
 
 // Fraction of a turn, in units of 2^-64, of position p; `known` is false where
@@ -61,9 +66,12 @@ __device__ __forceinline__ void sine(const RotaryArgs& a, const void* at, int i,
     // 2^-27 of a half turn and not by 2^-25.
     const int32_t half = static_cast<int32_t>(t >> 32);
     const uint32_t quarter = (static_cast<uint32_t>(half) + 0x20000000u) >> 30;
-    float sr, cr;
-    sincospif(static_cast<float>(static_cast<int32_t>(static_cast<uint32_t>(half) - (quarter << 30))) * 0x1p-31f, &sr,
-              &cr);
+    const float r = static_cast<float>(static_cast<int32_t>(static_cast<uint32_t>(half) - (quarter << 30))) * 0x1p-31f;
+    // Sine and cosine of pi r, |r| <= 1/4: polynomials in r^2 whose largest error is least, 2^-28 of the sine (whose
+    // first factor is pi in two parts) and 2^-34; sincospif took 3 us more for 102400 x 32 of them.
+    const float r2 = r * r;
+    const float sr = fmaf(r, 3.14159274f, r * fmaf(r2, fmaf(r2, fmaf(r2, -0.589012210f, 2.54976105f), -5.16770768f), -9.76113e-08f));
+    const float cr = fmaf(r2, fmaf(r2, fmaf(r2, fmaf(r2, 0.231429548f, -1.33505846f), 4.05870790f), -4.93480217f), 1.0f);
     s = quarter & 1 ? cr : sr;
     c = quarter & 1 ? sr : cr;
     if (quarter & 2) s = -s;
@@ -72,82 +80,99 @@ __device__ __forceinline__ void sine(const RotaryArgs& a, const void* at, int i,
     if (a.inverse) s = -s;
 }
 
-// n / d of non-negative numbers, in 32 bits where they fit.
-__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d)
-{
-    if (((n | d) >> 32) == 0) return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
-    return n / d;
-}
-
-// VP: pairs of a thread; with VP > 1 they are two accesses of VP elements a head.
-template <typename T, int VP, int HB, bool HALVES>
-__global__ void __launch_bounds__(RO_THREADS, 3)
+// VP: pairs of an item, two accesses of VP elements.  An item behind the turned
+// ones is one access of copied elements.
+template <typename T, int VP, bool HALVES>
+__global__ void __launch_bounds__(RO_THREADS, 6)
 rotary_kernel(const RotaryArgs a, const RotaryPlan plan)
 {
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * RO_THREADS + threadIdx.x;
-    if (item >= plan.items) return;
-    const int64_t rest = quotient(item, plan.units);
-    const int unit = static_cast<int>(item - rest * plan.units);
-    const int64_t at = quotient(rest, plan.head_parts);  // token of all
-    const int part = static_cast<int>(rest - at * plan.head_parts);
-    const int64_t batch = quotient(at, a.tokens), token = at - batch * a.tokens;
-    const int first = part * plan.head_step, last = min(a.heads, first + plan.head_step);
-    const T* x = static_cast<const T*>(a.x) + batch * a.x_batch + token * a.x_token + first * a.x_head;
-    T* y = static_cast<T*>(a.y) + batch * a.y_batch + token * a.y_token + first * a.y_head;
     using Vec = Pack<T, VP>;
-    if (unit >= plan.turned) {  // elements behind the pairs
-        const int64_t e = 2 * static_cast<int64_t>(a.pairs) + static_cast<int64_t>(unit - plan.turned) * VP;
-        for (int h = first; h < last; ++h, x += a.x_head, y += a.y_head)
-            *reinterpret_cast<Vec*>(y + e) = *reinterpret_cast<const Vec*>(x + e);
-        return;
+    constexpr int BATCH = sizeof(Vec) == 16 ? 1 : 4;  // tokens of a thread on their way
+    extern __shared__ __align__(16) float2 table[];   // cosine, sine [run][pairs]
+    __shared__ int64_t places[RO_TOKENS][3];          // of a token's vectors in x and y, of its positions
+    const int64_t token0 = static_cast<int64_t>(blockIdx.x) * plan.run;
+    const int run = static_cast<int>(min(static_cast<int64_t>(plan.run), plan.tokens - token0));
+    for (int i = threadIdx.x; i < run; i += RO_THREADS) {
+        const int64_t batch = (token0 + i) / a.tokens, token = token0 + i - batch * a.tokens;
+        places[i][0] = batch * a.x_batch + token * a.x_token;
+        places[i][1] = batch * a.y_batch + token * a.y_token;
+        places[i][2] = (a.sets == 1 ? token : token0 + i) * a.axes;
     }
-    const int pair = unit * VP;
-    // Elements of the two accesses: first and second of each pair, or pairs one after another.
-    const int e0 = HALVES ? pair : 2 * pair, e1 = HALVES ? pair + a.pairs : 2 * pair + VP;
-    const int64_t where = ((a.sets == 1 ? 0 : batch) * a.tokens + token) * a.axes;
-    float s[VP], c[VP];
-    Vec lo[HB], hi[HB];
+    __syncthreads();
+    for (int i = threadIdx.x; i < run * a.pairs; i += RO_THREADS) {
+        const int at = static_cast<unsigned>(i) / static_cast<unsigned>(a.pairs);
+        float s, c;
+        sine(a, static_cast<const int32_t*>(a.positions) + places[at][2], i - at * a.pairs, s, c);
+        table[i] = make_float2(c, s);
+    }
+    __syncthreads();
+    // A thread has one item, or every so many items, of each of its tokens, so that its place in a vector is worked
+    // out once: `slots` threads a token.
+    const int slot = threadIdx.x % plan.slots, first = threadIdx.x / plan.slots, step = RO_THREADS / plan.slots;
+    if (first >= step) return;
+    for (int64_t item = slot; item < plan.each; item += plan.slots) {
+        const int64_t head = item / plan.units;
+        const int unit = static_cast<int>(item - head * plan.units);
+        const bool turned = unit < plan.turned;
+        const int e = !turned ? 2 * a.pairs + (unit - plan.turned) * VP : HALVES ? unit * VP : 2 * unit * VP;
+        const int apart = HALVES ? a.pairs : VP;
+        const T* x = static_cast<const T*>(a.x) + head * a.x_head + e;
+        T* y = static_cast<T*>(a.y) + head * a.y_head + e;
+        const float2* turn = table + unit * VP;
+        for (int at = first; at < run; at += BATCH * step) {
+            Vec p[BATCH], q[BATCH];
 #pragma unroll
-    for (int b = 0; b < HB; ++b)
-        if (first + b < last) {
-            lo[b] = *reinterpret_cast<const Vec*>(x + b * a.x_head + e0);
-            hi[b] = *reinterpret_cast<const Vec*>(x + b * a.x_head + e1);
-        }
-#pragma unroll
-    for (int i = 0; i < VP; ++i) sine(a, static_cast<const int32_t*>(a.positions) + where, pair + i, s[i], c[i]);
-    for (int h = first; h < last; h += HB) {
-#pragma unroll
-        for (int b = 0; b < HB; ++b) {
-            if (h + b >= last) break;
-            const Vec p = lo[b], q = hi[b];
-            if (h + HB + b < last) {  // the next heads' while these are worked on
-                lo[b] = *reinterpret_cast<const Vec*>(x + (HB + b) * a.x_head + e0);
-                hi[b] = *reinterpret_cast<const Vec*>(x + (HB + b) * a.x_head + e1);
-            }
-            float u[VP], v[VP];
-            if constexpr (HALVES || VP == 1) {
-#pragma unroll
-                for (int i = 0; i < VP; ++i) {
-                    const float pi = to_f32(p.v[i]), qi = to_f32(q.v[i]);
-                    u[i] = fmaf(pi, c[i], -qi * s[i]);
-                    v[i] = fmaf(qi, c[i], pi * s[i]);
+            for (int b = 0; b < BATCH; ++b)
+                if (at + b * step < run) {
+                    const T* from = x + places[at + b * step][0];
+                    p[b] = *reinterpret_cast<const Vec*>(from);
+                    if (turned) q[b] = *reinterpret_cast<const Vec*>(from + apart);
                 }
-            } else {
 #pragma unroll
-                for (int i = 0; i < VP; i += 2) {
-                    const int k = i / 2, m = VP / 2 + k;
-                    const float p0 = to_f32(p.v[i]), p1 = to_f32(p.v[i + 1]), q0 = to_f32(q.v[i]), q1 = to_f32(q.v[i + 1]);
-                    u[i] = fmaf(p0, c[k], -p1 * s[k]);
-                    u[i + 1] = fmaf(p1, c[k], p0 * s[k]);
-                    v[i] = fmaf(q0, c[m], -q1 * s[m]);
-                    v[i + 1] = fmaf(q1, c[m], q0 * s[m]);
+            for (int b = 0; b < BATCH; ++b) {
+                const int token = at + b * step;
+                if (token >= run) break;
+                T* to = y + places[token][1];
+                if (!turned) {
+                    *reinterpret_cast<Vec*>(to) = p[b];
+                    continue;
                 }
+                const float2* t2 = turn + token * a.pairs;
+                float2 t[VP];
+                if constexpr (VP == 1) {
+                    t[0] = t2[0];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VP; i += 2) {
+                        const float4 two = *reinterpret_cast<const float4*>(t2 + i);
+                        t[i] = make_float2(two.x, two.y);
+                        t[i + 1] = make_float2(two.z, two.w);
+                    }
+                }
+                float u[VP], v[VP];
+                if constexpr (HALVES || VP == 1) {
+#pragma unroll
+                    for (int i = 0; i < VP; ++i) {
+                        const float c = to_f32(p[b].v[i]), d = to_f32(q[b].v[i]);
+                        u[i] = fmaf(c, t[i].x, -d * t[i].y);
+                        v[i] = fmaf(d, t[i].x, c * t[i].y);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VP; i += 2) {
+                        const float2 f = t[i / 2], g = t[VP / 2 + i / 2];
+                        const float c0 = to_f32(p[b].v[i]), c1 = to_f32(p[b].v[i + 1]);
+                        const float d0 = to_f32(q[b].v[i]), d1 = to_f32(q[b].v[i + 1]);
+                        u[i] = fmaf(c0, f.x, -c1 * f.y);
+                        u[i + 1] = fmaf(c1, f.x, c0 * f.y);
+                        v[i] = fmaf(d0, g.x, -d1 * g.y);
+                        v[i + 1] = fmaf(d1, g.x, d0 * g.y);
+                    }
+                }
+                *reinterpret_cast<Vec*>(to) = pack_results<T, VP>(u);
+                *reinterpret_cast<Vec*>(to + apart) = pack_results<T, VP>(v);
             }
-            *reinterpret_cast<Vec*>(y + b * a.y_head + e0) = pack_results<T, VP>(u);
-            *reinterpret_cast<Vec*>(y + b * a.y_head + e1) = pack_results<T, VP>(v);
         }
-        x += HB * a.x_head;
-        y += HB * a.y_head;
     }
 }
 
@@ -164,17 +189,18 @@ void launch(const RotaryArgs& a, cudaStream_t st)
     RotaryPlan p;
     p.turned = a.pairs / vp;
     p.units = p.turned + (a.dim - 2 * a.pairs) / vp;
-    // A thread takes all heads of its token once there are threads enough for every SM without splitting them.
-    const int64_t tokens = a.batch * a.tokens, whole = tokens * p.units, enough = static_cast<int64_t>(SMS) * RO_ENOUGH;
-    p.head_step = a.heads;
-    while (p.head_step > 1 && whole * ((a.heads + p.head_step - 1) / p.head_step) < enough)
-        p.head_step = (p.head_step + 1) / 2;
-    p.head_parts = (a.heads + p.head_step - 1) / p.head_step;
-    p.items = whole * p.head_parts;
-    const unsigned grid = static_cast<unsigned>((p.items + RO_THREADS - 1) / RO_THREADS);
-    auto run = [&](auto kernel) { kernel<<<grid, RO_THREADS, 0, st>>>(a, p); };
-    if (wide) a.halves ? run(rotary_kernel<T, MOST, 2, true>) : run(rotary_kernel<T, MOST, 2, false>);
-    else a.halves ? run(rotary_kernel<T, 1, 4, true>) : run(rotary_kernel<T, 1, 4, false>);
+    p.each = static_cast<int64_t>(a.heads) * p.units;
+    p.slots = static_cast<int>(p.each < RO_THREADS ? p.each : RO_THREADS);
+    p.tokens = a.batch * a.tokens;
+    // Runs as long as leave every SM a few blocks.
+    const int64_t most = a.pairs ? RO_TABLE / a.pairs : RO_TOKENS, share = p.tokens / (SMS * 8);
+    p.run = static_cast<int>(share < 1 ? 1 : share < most ? share : most);
+    if (p.run > RO_TOKENS) p.run = RO_TOKENS;
+    const unsigned grid = static_cast<unsigned>((p.tokens + p.run - 1) / p.run);
+    const size_t table = sizeof(float2) * p.run * a.pairs;
+    auto run = [&](auto kernel) { kernel<<<grid, RO_THREADS, table, st>>>(a, p); };
+    if (wide) a.halves ? run(rotary_kernel<T, MOST, true>) : run(rotary_kernel<T, MOST, false>);
+    else a.halves ? run(rotary_kernel<T, 1, true>) : run(rotary_kernel<T, 1, false>);
 }
 
 }  // namespace

@@ -694,7 +694,8 @@ nms_status nms_layer_norm_grad_run(const void* dy, int64_t dy_row, const void* x
  *   lut        device int64 [2][pairs], unsigned fractions of a turn first.
  * Errors: NMS_ERR_INVALID_ARG (types, shapes, strides, NULL or misaligned
  *         pointers), NMS_ERR_CAPACITY (axes, dim above the limits, heads above
- *         2^20, batch * tokens above 2^31 - 1, more than 2^38 elements),
+ *         2^20, heads * dim or batch * tokens above 2^31 - 1, more than 2^38
+ *         elements),
  *         NMS_ERR_CUDA.
  */
 #define NMS_POSITION_I32 16
