@@ -108,81 +108,77 @@ def test_table_of_turns():
             g.rotary_lut(4, base=base)
 
 
-class Beside(torch.Tensor):
-    """A CPU tensor that says it lies on the second CUDA device."""
-    is_cuda = True
-
-    def get_device(self):
-        return 1
+def _z(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype)
 
 
-def _on(*shape, dtype=torch.float32):
-    return torch.zeros(shape, dtype=dtype).as_subclass(Beside)
+X, W, HALF = _z(3, 8), _z(5, 8), _z(3, 8, dtype=torch.float16)
+VEC, POS, LUT, STATS = _z(2, 4, 3, 8), _z(2, 4, 2, dtype=torch.int32), _z(2, 4, dtype=torch.int64), _z(3)
 
 
-def test_tensor_functions_refuse():
-    cpu = torch.randn(3, 8)
-    x, w, half = _on(3, 8), _on(5, 8), _on(3, 8, dtype=torch.float16)
-    vec, pos, lut = _on(2, 4, 3, 8), _on(2, 4, 2, dtype=torch.int32), _on(2, 4, dtype=torch.int64)
-    stats = _on(3)
-    for call in (lambda: g.linear_act(cpu, cpu), lambda: g.linear_act(_on(3, 8, dtype=torch.float64), w),
-                 lambda: g.linear_act(x, _on(5, 7)), lambda: g.linear_act(x, _on(5, 8, dtype=torch.float16)),
-                 lambda: g.linear_act(x, w[0]), lambda: g.linear_act(x, torch.zeros(5, 8)), lambda: g.linear_act(x, w, _on(4)),
-                 lambda: g.linear_act(x, w, _on(10)[::2]), lambda: g.linear_act(half, half, _on(3, dtype=torch.bfloat16)),
-                 lambda: g.linear_act(x, w, act="tanh"), lambda: g.linear_act(x, w, residual=x),
-                 lambda: g.linear_act(x, w, residual=_on(3, 5, dtype=torch.float16)), lambda: g.linear_act(_on(), w),
-                 lambda: g.linear_act_grad(x, x, w), lambda: g.linear_act_grad(_on(3, 5), x, w, act="gelu"),
-                 lambda: g.linear_act_grad(_on(3, 5), x, w, _on(3, 4), act="gelu"),
-                 lambda: g.linear_act_grad(_on(3, 5, dtype=torch.float16), x, w),
-                 lambda: g.layer_norm(cpu), lambda: g.layer_norm(x, _on(7)), lambda: g.layer_norm(x, residual=half),
-                 lambda: g.layer_norm(x, residual=cpu), lambda: g.layer_norm(_on()),
-                 lambda: g.layer_norm_grad(half, x, stats, stats), lambda: g.layer_norm_grad(x, x, _on(4), stats),
-                 lambda: g.layer_norm_grad(x, x, stats, _on(3, dtype=torch.float16)),
-                 lambda: g.layer_norm_grad(x, x, stats, stats, dsum=half),
-                 lambda: g.rotary(vec[0], pos, lut), lambda: g.rotary(vec, pos.long(), lut), lambda: g.rotary(vec, pos[0], lut),
-                 lambda: g.rotary(vec, _on(3, 4, 2, dtype=torch.int32), lut), lambda: g.rotary(vec, pos, lut.int()),
-                 lambda: g.rotary(vec, pos, _on(2, 5, dtype=torch.int64)), lambda: g.rotary(vec, pos, lut[:1]),
-                 lambda: g.rotary(vec, torch.zeros(2, 4, 2, dtype=torch.int32), lut),
-                 lambda: g.rotary(torch.zeros(2, 4, 3, 8), pos, lut)):
-        with pytest.raises(ValueError):
-            call()
+# That the operands lie on a CUDA device is the last thing to be looked at, so everything before it shows here.
+@pytest.mark.parametrize("message,call", [
+    ("x must be a float32", lambda: g.linear_act(_z(3, 8, dtype=torch.float64), W)),
+    ("x must be a tensor", lambda: g.linear_act(None, W)),
+    ("rows must be", lambda: g.linear_act(_z(), W)),
+    ("weight must be a tensor", lambda: g.linear_act(X, None)),
+    ("weight must be .outer, inner", lambda: g.linear_act(X, _z(5, 7))),
+    ("weight must be .outer, inner", lambda: g.linear_act(X, _z(5, 8, dtype=torch.float16))),
+    ("weight must be .outer, inner", lambda: g.linear_act(X, W[0])),
+    ("weight must be .outer, inner", lambda: g.linear_act(X, W.to("meta"))),
+    ("bias must be a contiguous", lambda: g.linear_act(X, W, _z(4))),
+    ("bias must be a contiguous", lambda: g.linear_act(X, W, _z(10)[::2])),
+    ("bias must be a contiguous", lambda: g.linear_act(X, W, _z(1, 5))),
+    ("bias must be a contiguous", lambda: g.linear_act(HALF, W.half(), _z(5, dtype=torch.bfloat16))),
+    ("act must be", lambda: g.linear_act(X, W, act="tanh")),
+    ("residual must be", lambda: g.linear_act(X, W, residual=X)),
+    ("residual must be", lambda: g.linear_act(X, W, residual=_z(3, 5, dtype=torch.float16))),
+    ("dy must be", lambda: g.linear_act_grad(X, X, W)),
+    ("dy must be", lambda: g.linear_act_grad(_z(3, 5, dtype=torch.float16), X, W)),
+    ("needs the forward's pre", lambda: g.linear_act_grad(_z(3, 5), X, W, act="gelu")),
+    ("pre must have", lambda: g.linear_act_grad(_z(3, 5), X, W, _z(3, 4), act="gelu")),
+    ("pre must have", lambda: g.linear_act_grad(_z(3, 5), X, W, _z(3, 5, dtype=torch.float16), act="gelu")),
+    ("act must be", lambda: g.linear_act_grad(_z(3, 5), X, W, act=None)),
+    ("rows must be", lambda: g.layer_norm(_z())),
+    ("weight must be a contiguous", lambda: g.layer_norm(X, _z(7))),
+    ("bias must be a contiguous", lambda: g.layer_norm(X, _z(8), _z(8, dtype=torch.float16))),
+    ("all of them alike", lambda: g.layer_norm(HALF, _z(8), _z(8, dtype=torch.float16))),
+    ("residual must have", lambda: g.layer_norm(X, residual=HALF)),
+    ("residual must have", lambda: g.layer_norm(X, residual=_z(1, 8))),
+    ("dy must have", lambda: g.layer_norm_grad(HALF, X, STATS, STATS)),
+    ("mean and rstd", lambda: g.layer_norm_grad(X, X, _z(4), STATS)),
+    ("mean and rstd", lambda: g.layer_norm_grad(X, X, STATS, STATS.half())),
+    ("mean and rstd", lambda: g.layer_norm_grad(X, X, STATS, _z(6)[::2])),
+    ("dsum must have", lambda: g.layer_norm_grad(X, X, STATS, STATS, dsum=HALF)),
+    ("x must be .batch, tokens", lambda: g.rotary(VEC[0], POS, LUT)),
+    ("positions must be", lambda: g.rotary(VEC, POS.long(), LUT)),
+    ("positions must be", lambda: g.rotary(VEC, POS[0], LUT)),
+    ("positions must be", lambda: g.rotary(VEC, _z(3, 4, 2, dtype=torch.int32), LUT)),
+    ("positions must be", lambda: g.rotary_grad(VEC, POS[:, :3], LUT)),
+    ("lut must be", lambda: g.rotary(VEC, POS, LUT.int())),
+    ("lut must be", lambda: g.rotary(VEC, POS, _z(2, 5, dtype=torch.int64))),
+    ("lut must be", lambda: g.rotary(VEC, POS, LUT[:1])),
+    ("x must be a float32, float16 or bfloat16 CUDA", lambda: g.linear_act(X, W)),
+    ("x must be a float32, float16 or bfloat16 CUDA", lambda: g.linear_act_grad(_z(3, 5), X, W)),
+    ("x must be a float32, float16 or bfloat16 CUDA", lambda: g.layer_norm(X, residual=X)),
+    ("x must be a float32, float16 or bfloat16 CUDA", lambda: g.layer_norm_grad(X, X, STATS, STATS)),
+    ("x must be a float32, float16 or bfloat16 CUDA", lambda: g.rotary(VEC, POS, LUT))])
+def test_tensor_functions_refuse(message, call):
+    with pytest.raises(ValueError, match=message):
+        call()
 
 
-@pytest.mark.parametrize("current", [0, 1])
-def test_launches_go_to_the_tensors_device(lib, monkeypatch, current):
-    """Another device being current, each tensor function makes its operands'
-    device current for the launch and hands over that device's stream."""
-    from greedy_iou_nms_gb300 import head
-    head._torch()
-    now, calls = [current], []
+def test_arguments_that_are_no_numbers():
+    with pytest.raises(TypeError):
+        g.layer_norm(X, eps="small")
+    with pytest.raises(TypeError):
+        g.linear_act_grad(_z(3, 5), X, W, need=(True, True))
 
-    class Device:
-        def __init__(self, index):
-            self.index = index
 
-        def __enter__(self):
-            self.before, now[0] = now[0], self.index
-
-        def __exit__(self, *_):
-            now[0] = self.before
-
-    class Recorder:
-        def __getattr__(self, name):
-            if not name.endswith("_run"):
-                return getattr(lib, name)
-            return lambda *args: calls.append((name, now[0], args[-1])) or 0
-
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
-    monkeypatch.setattr(torch.cuda, "device", Device)
-    monkeypatch.setattr(head, "_raw_stream", lambda index: 1000 + index)
-    monkeypatch.setattr(head, "_loaded", Recorder())
-    x, w = _on(3, 8), _on(5, 8)
-    g.linear_act(x, w)
-    g.linear_act_grad(_on(3, 5), x, w)
-    g.layer_norm(x)
-    g.layer_norm_grad(x, x, _on(3), _on(3))
-    g.rotary(_on(2, 4, 3, 8), _on(2, 4, 1, dtype=torch.int32), _on(2, 4, dtype=torch.int64))
-    g.rotary_grad(_on(2, 4, 3, 8), _on(2, 4, 1, dtype=torch.int32), _on(2, 4, dtype=torch.int64))
-    assert [c[0] for c in calls] == ["nms_linear_run", "nms_linear_grad_run", "nms_layer_norm_run",
-                                     "nms_layer_norm_grad_run", "nms_rotary_run", "nms_rotary_run"]
-    assert all(at == 1 and stream == 1001 for _, at, stream in calls) and now[0] == current
+def test_a_missing_binding_raises(monkeypatch):
+    """No other path stands in for the C++ half."""
+    from greedy_iou_nms_gb300 import _build, block
+    monkeypatch.setattr(block, "_native_module", None)
+    monkeypatch.setattr(_build, "BINDING_LIB", _build.BINDING_LIB + ".missing")
+    with pytest.raises(RuntimeError, match="not built"):
+        g.layer_norm(X)
