@@ -77,10 +77,10 @@ struct ProductArgs {
     void* pre;        // A B^T + bias [m][n] contiguous, or NULL
     int32_t* status;  // or NULL
 };
-// Binary32, by the plain arithmetic units.
-void launch_product_f32(const ProductArgs& p, cudaStream_t st);
+// Binary32, by the plain arithmetic units.  False: the driver refused a launch.
+bool launch_product_f32(const ProductArgs& p, cudaStream_t st);
 // 16 bits, by the tensor cores: operands and their rows start at multiples of
-// 16 bytes and do not overlap.  False: the driver refused a launch.
+// 16 bytes and do not overlap.
 bool launch_product_tc(const ProductArgs& p, cudaStream_t st);
 // Rows of 16-bit elements to rows `to_row` apart.
 void launch_copy_rows(const void* from, int64_t from_row, int64_t rows, int64_t width, void* to, int64_t to_row,

@@ -61,9 +61,7 @@ const void* even(int32_t type, const void* p, int64_t& row, int64_t rows, int64_
 
 bool launch_product(const ProductArgs& p, cudaStream_t st)
 {
-    if (p.type != NMS_TYPE_F32) return launch_product_tc(p, st);
-    launch_product_f32(p, st);
-    return true;
+    return p.type == NMS_TYPE_F32 ? launch_product_f32(p, st) : launch_product_tc(p, st);
 }
 
 }  // namespace

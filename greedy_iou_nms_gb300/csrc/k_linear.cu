@@ -1,7 +1,10 @@
 // Matrix products of binary32 operands with bias, activation and residual in
-// their epilogue, on the plain arithmetic units: a block has a tile of TILE x
-// TILE results, its 256 threads S x S of them each.  And the copy of 16-bit
-// rows whose places the tensor cores' loads cannot take.
+// their epilogue, on the plain arithmetic units: a block has a tile of 16 SM x
+// 16 SN results, its 256 threads SM x SN of them each.  Tiles of 128 x 64 leave
+// room for two blocks an SM, one of which multiplies while the other waits.  Few
+// tiles: the blocks of a cluster share one, each a stretch of k, and add up
+// their parts through distributed shared memory, in order.  And the copy of
+// 16-bit rows whose places the tensor cores' loads cannot take.
 #include "block.h"
 #include "head.cuh"
 #include "internal.h"
@@ -11,7 +14,7 @@ namespace gbnms {
 namespace {
 
 constexpr int PR_DEPTH = 16;   // of a step along k
-constexpr int PR_STAGES = 4;   // steps in shared memory
+constexpr int PR_STAGES = 3;   // steps in shared memory
 
 // One operand's way to shared memory, [k][m or n], element by element
 // (cp.async), so that any stride and start will do and either order of the
@@ -23,10 +26,11 @@ struct Feed {
     int64_t delta, step;
     uint32_t to;
     int64_t left_mn, left_k;  // elements from this thread's first on
-    __device__ __forceinline__ Feed(const float* p, int64_t row, int64_t mn0, int64_t mns, int64_t ks, const void* shared)
+    __device__ __forceinline__ Feed(const float* p, int64_t row, int64_t mn0, int64_t mns, int64_t k0, int64_t ks,
+                                    const void* shared)
     {
         const int t = threadIdx.x, mn = ACROSS ? t % TILE : t / PR_DEPTH, k = ACROSS ? t / TILE : t % PR_DEPTH;
-        from = p + (ACROSS ? k * row + mn0 + mn : (mn0 + mn) * row + k);
+        from = p + (ACROSS ? (k0 + k) * row + mn0 + mn : (mn0 + mn) * row + k0 + k);
         delta = ACROSS ? (256 / TILE) * row : (256 / PR_DEPTH) * row;
         step = ACROSS ? PR_DEPTH * row : PR_DEPTH;
         to = static_cast<uint32_t>(__cvta_generic_to_shared(shared)) + 4 * (k * STRIDE + mn);
@@ -50,22 +54,39 @@ struct Feed {
     }
 };
 
-template <int S, bool A_ACROSS, bool B_ACROSS>
-__global__ void __launch_bounds__(256)
-product_kernel(const ProductArgs p, int64_t tiles_n)
+__device__ __forceinline__ void cluster_barrier()
 {
-    using T = float;
-    constexpr int TILE = 16 * S, STRIDE = TILE + 4;
-    extern __shared__ __align__(16) float stages[];  // [2][PR_STAGES][PR_DEPTH][STRIDE]
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void finish(const ProductArgs& p, int64_t m, int64_t n, float sum)
+{
+    float z[1] = {sum + (p.bias ? static_cast<const float*>(p.bias)[n] : 0.0f)};
+    if (p.pre) static_cast<float*>(p.pre)[m * p.n + n] = z[0];
+    act_values<float>(z, p.act);
+    if (p.residual) z[0] += static_cast<const float*>(p.residual)[m * p.residual_row + n];
+    static_cast<float*>(p.out)[m * p.n + n] = z[0];
+}
+
+template <int SM, int SN, bool A_ACROSS, bool B_ACROSS>
+__global__ void __launch_bounds__(256, SM == 8 ? 2 : 3)
+product_kernel(const ProductArgs p, int64_t tiles_n, int split)
+{
+    constexpr int TM = 16 * SM, TN = 16 * SN, AS = TM + 4, BS = TN + 4;
+    static_assert(TM * BS <= PR_STAGES * PR_DEPTH * (AS + BS), "a block's part fits in the stages");
+    extern __shared__ __align__(16) float stages[];  // [PR_STAGES][PR_DEPTH] of AS, of BS; then the block's part [TM][BS]
     float* const as = stages;
-    float* const bs = stages + PR_STAGES * PR_DEPTH * STRIDE;
-    const int64_t tm = blockIdx.x / tiles_n, tn = blockIdx.x - tm * tiles_n;
-    const int64_t m0 = tm * TILE, n0 = tn * TILE;
+    float* const bs = stages + PR_STAGES * PR_DEPTH * AS;
+    const int64_t tile = blockIdx.x / split, rank = blockIdx.x - tile * split;
+    const int64_t tm = tile / tiles_n, tn = tile - tm * tiles_n;
+    const int64_t m0 = tm * TM, n0 = tn * TN;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    float acc[S][S] = {}, total[S][S] = {};
-    Feed<TILE, A_ACROSS> a(static_cast<const float*>(p.a), p.a_row, m0, p.m, p.k, as);
-    Feed<TILE, B_ACROSS> b(static_cast<const float*>(p.b), p.b_row, n0, p.n, p.k, bs);
-    const int64_t steps = (p.k + PR_DEPTH - 1) / PR_DEPTH;
+    float acc[SM][SN] = {}, total[SM][SN] = {};
+    const int64_t all = (p.k + PR_DEPTH - 1) / PR_DEPTH, each = (all + split - 1) / split;
+    const int64_t from = min(p.k, rank * each * PR_DEPTH), count = min(p.k - from, each * PR_DEPTH);  // of k, this block's
+    Feed<TM, A_ACROSS> a(static_cast<const float*>(p.a), p.a_row, m0, p.m, from, count, as);
+    Feed<TN, B_ACROSS> b(static_cast<const float*>(p.b), p.b_row, n0, p.n, from, count, bs);
+    const int64_t steps = (count + PR_DEPTH - 1) / PR_DEPTH;
 #pragma unroll
     for (int s = 0; s < PR_STAGES - 1; ++s) {
         if (s < steps) {
@@ -83,27 +104,28 @@ product_kernel(const ProductArgs p, int64_t tiles_n)
             b.next(ahead);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        const float* const ak = as + at * PR_DEPTH * STRIDE;
-        const float* const bk = bs + at * PR_DEPTH * STRIDE;
+        const float* const ak = as + at * PR_DEPTH * AS;
+        const float* const bk = bs + at * PR_DEPTH * BS;
 #pragma unroll
         for (int k = 0; k < PR_DEPTH; ++k) {
-            alignas(16) float x[S], w[S];
+            alignas(16) float x[SM], w[SN];
 #pragma unroll
-            for (int i = 0; i < S; i += 4) {
-                *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(ak + k * STRIDE + i * 16 + ty * 4);
-                *reinterpret_cast<float4*>(w + i) = *reinterpret_cast<const float4*>(bk + k * STRIDE + i * 16 + tx * 4);
-            }
+            for (int i = 0; i < SM; i += 4)
+                *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(ak + k * AS + i * 16 + ty * 4);
 #pragma unroll
-            for (int i = 0; i < S; ++i)
+            for (int j = 0; j < SN; j += 4)
+                *reinterpret_cast<float4*>(w + j) = *reinterpret_cast<const float4*>(bk + k * BS + j * 16 + tx * 4);
 #pragma unroll
-                for (int j = 0; j < S; ++j) acc[i][j] = fmaf(x[i], w[j], acc[i][j]);
+            for (int i = 0; i < SM; ++i)
+#pragma unroll
+                for (int j = 0; j < SN; ++j) acc[i][j] = fmaf(x[i], w[j], acc[i][j]);
         }
         // Sums of 256 products, added up: a chain over all of k would round off with k.
         if (s % 16 == 15 || s + 1 == steps) {
 #pragma unroll
-            for (int i = 0; i < S; ++i)
+            for (int i = 0; i < SM; ++i)
 #pragma unroll
-                for (int j = 0; j < S; ++j) {
+                for (int j = 0; j < SN; ++j) {
                     total[i][j] += acc[i][j];
                     acc[i][j] = 0.0f;
                 }
@@ -111,23 +133,46 @@ product_kernel(const ProductArgs p, int64_t tiles_n)
         at = at + 1 == PR_STAGES ? 0 : at + 1;
         ahead = ahead + 1 == PR_STAGES ? 0 : ahead + 1;
     }
-    T* out = static_cast<T*>(p.out);
-    T* pre = static_cast<T*>(p.pre);
+    if (split == 1) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-        const int64_t m = m0 + (i / 4) * 64 + ty * 4 + i % 4;
-        if (m >= p.m) continue;
+        for (int i = 0; i < SM; ++i) {
+            const int64_t m = m0 + (i / 4) * 64 + ty * 4 + i % 4;
 #pragma unroll
-        for (int j = 0; j < S; ++j) {
-            const int64_t n = n0 + (j / 4) * 64 + tx * 4 + j % 4;
-            if (n >= p.n) continue;
-            float z[1] = {total[i][j] + (p.bias ? load_param<T>(p.bias, p.bias_f32, n) : 0.0f)};
-            if (pre) pre[m * p.n + n] = from_f32<T>(z[0]);
-            act_values<T>(z, p.act);
-            if (p.residual) z[0] += to_f32(static_cast<const T*>(p.residual)[m * p.residual_row + n]);
-            out[m * p.n + n] = from_f32<T>(z[0]);
+            for (int j = 0; j < SN; ++j) {
+                const int64_t n = n0 + (j / 4) * 64 + tx * 4 + j % 4;
+                if (m < p.m && n < p.n) finish(p, m, n, total[i][j]);
+            }
         }
+        return;
     }
+    __syncthreads();  // the stages are no longer read
+#pragma unroll
+    for (int i = 0; i < SM; ++i)
+#pragma unroll
+        for (int j = 0; j < SN; j += 4)
+            *reinterpret_cast<float4*>(stages + ((i / 4) * 64 + ty * 4 + i % 4) * BS + j * 16 + tx * 4) =
+                make_float4(total[i][j], total[i][j + 1], total[i][j + 2], total[i][j + 3]);
+    cluster_barrier();
+    const uint32_t part = static_cast<uint32_t>(__cvta_generic_to_shared(stages));
+    const int rows = TM / split;
+    for (int e = threadIdx.x; e < rows * TN; e += 256) {
+        const int r = static_cast<int>(rank) * rows + e / TN, c = e % TN;
+        if (m0 + r >= p.m || n0 + c >= p.n) continue;
+        float v[8], sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < split) {
+                uint32_t peer;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(part + 4 * (r * BS + c)), "r"(q));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[q]) : "r"(peer));
+            }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < split) sum += v[q];
+        finish(p, m0 + r, n0 + c, sum);
+    }
+    __syncwarp();
+    cluster_barrier();  // no block leaves while another reads its part
 }
 
 // Eight elements of a row a thread.
@@ -147,23 +192,36 @@ copy_rows_kernel(const uint16_t* from, int64_t from_row, int64_t rows, int64_t w
 
 }  // namespace
 
-template <int S>
-static void launch_tiles(const ProductArgs& p, cudaStream_t st)
+template <int SM, int SN>
+static bool launch_tiles(const ProductArgs& p, cudaStream_t st)
 {
-    constexpr int TILE = 16 * S, SMEM = 2 * PR_STAGES * PR_DEPTH * (TILE + 4) * 4;
-    const int64_t tiles_n = (p.n + TILE - 1) / TILE, tiles = ((p.m + TILE - 1) / TILE) * tiles_n;
-    auto run = [&](auto kernel) {
-        if (SMEM > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-        kernel<<<static_cast<unsigned>(tiles), 256, SMEM, st>>>(p, tiles_n);
-    };
-    if (p.a_across) run(product_kernel<S, true, true>);
-    else p.b_across ? run(product_kernel<S, false, true>) : run(product_kernel<S, false, false>);
+    constexpr int TM = 16 * SM, TN = 16 * SN, SMEM = PR_STAGES * PR_DEPTH * (TM + 4 + TN + 4) * 4;
+    static_assert(SMEM <= 48 * 1024, "no attribute needed");
+    const int64_t tiles_n = (p.n + TN - 1) / TN, tiles = ((p.m + TM - 1) / TM) * tiles_n;
+    const int64_t steps = (p.k + PR_DEPTH - 1) / PR_DEPTH;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= SMS * 4 && steps >= split * 8) split *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1]{};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto run = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, p, tiles_n, split) == cudaSuccess; };
+    if (p.a_across) return run(product_kernel<SM, SN, true, true>);
+    return p.b_across ? run(product_kernel<SM, SN, false, true>) : run(product_kernel<SM, SN, false, false>);
 }
 
-void launch_product_f32(const ProductArgs& p, cudaStream_t st)
+bool launch_product_f32(const ProductArgs& p, cudaStream_t st)
 {
-    if (((p.m + 127) / 128) * ((p.n + 127) / 128) >= SMS) launch_tiles<8>(p, st);
-    else launch_tiles<4>(p, st);
+    // The larger tile where it fills the SMs: it reads a quarter less.
+    if (((p.m + 127) / 128) * ((p.n + 63) / 64) >= 2 * SMS) return launch_tiles<8, 4>(p, st);
+    return launch_tiles<4, 4>(p, st);
 }
 
 void launch_copy_rows(const void* from, int64_t from_row, int64_t rows, int64_t width, void* to, int64_t to_row,
