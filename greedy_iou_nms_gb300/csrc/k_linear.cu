@@ -1,10 +1,17 @@
 // Matrix products of binary32 operands with bias, activation and residual in
-// their epilogue, on the plain arithmetic units: a block has a tile of 16 SM x
-// 16 SN results, its 256 threads SM x SN of them each.  Tiles of 128 x 64 leave
-// room for two blocks an SM, one of which multiplies while the other waits.  Few
-// tiles: the blocks of a cluster share one, each a stretch of k, and add up
-// their parts through distributed shared memory, in order.  And the copy of
-// 16-bit rows whose places the tensor cores' loads cannot take.
+// their epilogue, on the plain arithmetic units, and the copy of 16-bit rows
+// whose places the tensor cores' loads cannot take.
+//
+// product_kernel: a block has a tile of 16 SM x 16 SN results, its 256 threads SM
+// x SN of them each.  Tiles of 128 x 64 leave room for two blocks an SM, one of
+// which multiplies while the other waits (8 x 8 a thread, two blocks an SM, took
+// 530 us for 2048 x 2048 x 2048, 8 x 4 504).  Few tiles: the blocks of a cluster
+// share one, each a stretch of k, and add up their parts through distributed
+// shared memory, in order.
+//
+// Up to 16 rows are a stream of the weight, whose elements are used once a row:
+// few_along_kernel and few_across_kernel read it straight to registers, all of an
+// SM's warps at once.
 #include "block.h"
 #include "head.cuh"
 #include "internal.h"
@@ -57,6 +64,24 @@ struct Feed {
 __device__ __forceinline__ void cluster_barrier()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The sum over the cluster's blocks of what each has at its own `at`.
+__device__ __forceinline__ float cluster_sum(const float* at, int split)
+{
+    const uint32_t own = static_cast<uint32_t>(__cvta_generic_to_shared(at));
+    float v[8], sum = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        if (q < split) {
+            uint32_t peer;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(own), "r"(q));
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[q]) : "r"(peer));
+        }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        if (q < split) sum += v[q];
+    return sum;
 }
 
 __device__ __forceinline__ void finish(const ProductArgs& p, int64_t m, int64_t n, float sum)
@@ -153,26 +178,120 @@ product_kernel(const ProductArgs p, int64_t tiles_n, int split)
             *reinterpret_cast<float4*>(stages + ((i / 4) * 64 + ty * 4 + i % 4) * BS + j * 16 + tx * 4) =
                 make_float4(total[i][j], total[i][j + 1], total[i][j + 2], total[i][j + 3]);
     cluster_barrier();
-    const uint32_t part = static_cast<uint32_t>(__cvta_generic_to_shared(stages));
     const int rows = TM / split;
     for (int e = threadIdx.x; e < rows * TN; e += 256) {
         const int r = static_cast<int>(rank) * rows + e / TN, c = e % TN;
-        if (m0 + r >= p.m || n0 + c >= p.n) continue;
-        float v[8], sum = 0.0f;
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (q < split) {
-                uint32_t peer;
-                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(part + 4 * (r * BS + c)), "r"(q));
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[q]) : "r"(peer));
-            }
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (q < split) sum += v[q];
-        finish(p, m0 + r, n0 + c, sum);
+        if (m0 + r < p.m && n0 + c < p.n) finish(p, m0 + r, n0 + c, cluster_sum(stages + r * BS + c, split));
     }
     __syncwarp();
     cluster_barrier();  // no block leaves while another reads its part
+}
+
+// Results of up to R rows and eight columns a block; B's rows are columns of the
+// result.  Four of a block's warps share four columns, each a quarter of k.
+template <int R, int V>
+__global__ void __launch_bounds__(256)
+few_along_kernel(const ProductArgs p)
+{
+    __shared__ float parts[8][4 * R];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quarter = warp % 4;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 8 + warp / 4 * 4;
+    const float* const x = static_cast<const float*>(p.a);
+    const float* const w = static_cast<const float*>(p.b);
+    float acc[4][R] = {};
+    for (int64_t k = (quarter * 32 + lane) * V; k < p.k; k += 128 * V) {  // V divides k
+        Pack<float, V> wv[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (n0 + c < p.n) wv[c] = *reinterpret_cast<const Pack<float, V>*>(w + (n0 + c) * p.b_row + k);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (r >= p.m) break;
+            const Pack<float, V> xv = *reinterpret_cast<const Pack<float, V>*>(x + r * p.a_row + k);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[c][r] = fmaf(xv.v[i], wv[c].v[i], acc[c][r]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float sum = warp_sum(acc[c][r]);
+            if (lane == 0) parts[warp][c * R + r] = sum;
+        }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 8 * R; e += 256) {
+        const int r = e / 8, c = e % 8, first = c / 4 * 4, at = c % 4 * R + r;
+        const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 + c;
+        if (r < p.m && n < p.n)
+            finish(p, r, n, ((parts[first][at] + parts[first + 1][at]) + parts[first + 2][at]) + parts[first + 3][at]);
+    }
+}
+
+// Results of up to R rows and 32 V columns a cluster, B lying across: a block
+// has a stretch of k, in chunks of 64 whose part of A it keeps in shared memory,
+// a warp eight rows of B of each chunk, a lane V columns.
+template <int R, int V>
+__global__ void __launch_bounds__(256)
+few_across_kernel(const ProductArgs p, int split)
+{
+    extern __shared__ __align__(16) float dynamic[];
+    constexpr int COLUMNS = 32 * V, CHUNK = 64, EACH = CHUNK / 8;
+    float* const xs = dynamic;                                // [CHUNK][R]
+    float* const parts = dynamic + CHUNK * R;                 // [8][R][COLUMNS]
+    float* const sums = parts + 8 * R * COLUMNS;              // [R][COLUMNS]
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t group = blockIdx.x / split, rank = blockIdx.x - group * split;
+    const int64_t n = group * COLUMNS + lane * V;
+    const float* const x = static_cast<const float*>(p.a);
+    const float* const w = static_cast<const float*>(p.b) + n;
+    const int64_t each = ((p.k + split - 1) / split + CHUNK - 1) / CHUNK * CHUNK;
+    const int64_t first = min(p.k, rank * each), last = min(p.k, first + each);
+    float acc[R][V] = {};
+    for (int64_t k0 = first; k0 < last; k0 += CHUNK) {
+        Pack<float, V> wv[EACH];
+        const int64_t k = k0 + warp * EACH;
+#pragma unroll
+        for (int q = 0; q < EACH; ++q) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) wv[q].v[i] = 0.0f;
+            if (n < p.n && k + q < last) wv[q] = *reinterpret_cast<const Pack<float, V>*>(w + (k + q) * p.b_row);  // V divides n
+        }
+        __syncthreads();  // nobody reads the last chunk's part of A
+        for (int e = threadIdx.x; e < CHUNK * R; e += 256) {
+            const int r = e / CHUNK, c = e % CHUNK;
+            xs[c * R + r] = r < p.m && k0 + c < last ? x[r * p.a_row + k0 + c] : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < EACH; ++q)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float xv = xs[(warp * EACH + q) * R + r];
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[r][i] = fmaf(xv, wv[q].v[i], acc[r][i]);
+            }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < V; ++i) parts[(warp * R + r) * COLUMNS + lane * V + i] = acc[r][i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < R * COLUMNS; e += 256) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum += parts[q * R * COLUMNS + e];
+        sums[e] = sum;
+    }
+    cluster_barrier();
+    for (int e = static_cast<int>(rank) * 256 + threadIdx.x; e < R * COLUMNS; e += 256 * split) {
+        const int r = e / COLUMNS, c = e % COLUMNS;
+        if (r < p.m && group * COLUMNS + c < p.n) finish(p, r, group * COLUMNS + c, cluster_sum(sums + e, split));
+    }
+    __syncwarp();
+    cluster_barrier();  // no block leaves while another reads its sums
 }
 
 // Eight elements of a row a thread.
@@ -192,19 +311,17 @@ copy_rows_kernel(const uint16_t* from, int64_t from_row, int64_t rows, int64_t w
 
 }  // namespace
 
-template <int SM, int SN>
-static bool launch_tiles(const ProductArgs& p, cudaStream_t st)
+// A kernel over clusters of `split` blocks of 256 threads.
+template <typename Kernel, typename... Args>
+static bool launch_clusters(Kernel kernel, int64_t clusters, int split, int smem, cudaStream_t st, Args... args)
 {
-    constexpr int TM = 16 * SM, TN = 16 * SN, SMEM = PR_STAGES * PR_DEPTH * (TM + 4 + TN + 4) * 4;
-    static_assert(SMEM <= 48 * 1024, "no attribute needed");
-    const int64_t tiles_n = (p.n + TN - 1) / TN, tiles = ((p.m + TM - 1) / TM) * tiles_n;
-    const int64_t steps = (p.k + PR_DEPTH - 1) / PR_DEPTH;
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= SMS * 4 && steps >= split * 8) split *= 2;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return false;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * split));
     cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = SMEM;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1]{};
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -212,13 +329,49 @@ static bool launch_tiles(const ProductArgs& p, cudaStream_t st)
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto run = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, p, tiles_n, split) == cudaSuccess; };
-    if (p.a_across) return run(product_kernel<SM, SN, true, true>);
-    return p.b_across ? run(product_kernel<SM, SN, false, true>) : run(product_kernel<SM, SN, false, false>);
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
+template <int R>
+static bool launch_few(const ProductArgs& p, cudaStream_t st)
+{
+    auto even = [](const void* v, int64_t row) { return reinterpret_cast<uintptr_t>(v) % 16 == 0 && row % 4 == 0; };
+    if (!p.b_across) {
+        const bool wide = p.k % 4 == 0 && even(p.a, p.a_row) && even(p.b, p.b_row);
+        const unsigned grid = static_cast<unsigned>((p.n + 7) / 8);
+        if (wide) few_along_kernel<R, 4><<<grid, 256, 0, st>>>(p);
+        else few_along_kernel<R, 1><<<grid, 256, 0, st>>>(p);
+        return true;
+    }
+    const bool wide = p.n % 4 == 0 && even(p.b, p.b_row);
+    const int columns = wide ? 128 : 32;
+    const int64_t groups = (p.n + columns - 1) / columns;
+    int split = 1;
+    while (split < 8 && groups * split * 2 <= SMS * 4 && p.k >= split * 128) split *= 2;
+    const int smem = (64 * R + 9 * R * columns) * 4;
+    if (wide) return launch_clusters(few_across_kernel<R, 4>, groups, split, smem, st, p, split);
+    return launch_clusters(few_across_kernel<R, 1>, groups, split, smem, st, p, split);
+}
+
+template <int SM, int SN>
+static bool launch_tiles(const ProductArgs& p, cudaStream_t st)
+{
+    constexpr int TM = 16 * SM, TN = 16 * SN, SMEM = PR_STAGES * PR_DEPTH * (TM + 4 + TN + 4) * 4;
+    const int64_t tiles_n = (p.n + TN - 1) / TN, tiles = ((p.m + TM - 1) / TM) * tiles_n;
+    const int64_t steps = (p.k + PR_DEPTH - 1) / PR_DEPTH;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= SMS * 4 && steps >= split * 8) split *= 2;
+    if (p.a_across) return launch_clusters(product_kernel<SM, SN, true, true>, tiles, split, SMEM, st, p, tiles_n, split);
+    if (p.b_across) return launch_clusters(product_kernel<SM, SN, false, true>, tiles, split, SMEM, st, p, tiles_n, split);
+    return launch_clusters(product_kernel<SM, SN, false, false>, tiles, split, SMEM, st, p, tiles_n, split);
 }
 
 bool launch_product_f32(const ProductArgs& p, cudaStream_t st)
 {
+    if (p.m <= 16 && !p.a_across) {
+        if (p.m == 1) return launch_few<1>(p, st);
+        return p.m <= 4 ? launch_few<4>(p, st) : launch_few<16>(p, st);
+    }
     // The larger tile where it fills the SMs: it reads a quarter less.
     if (((p.m + 127) / 128) * ((p.n + 63) / 64) >= 2 * SMS) return launch_tiles<8, 4>(p, st);
     return launch_tiles<4, 4>(p, st);
