@@ -48,20 +48,48 @@ bool uneven(int32_t type, const void* p, int64_t row, int64_t rows, int64_t widt
 
 size_t copy_bytes(int64_t rows, int64_t width) { return round_up(2 * rows * padded(width)); }
 
-// The operand itself, or a copy of it in the workspace, which moves on.
-const void* even(int32_t type, const void* p, int64_t& row, int64_t rows, int64_t width, char*& workspace, cudaStream_t st)
+size_t plane_bytes(int64_t rows, int64_t width) { return round_up(3 * 2 * rows * padded(width)); }
+
+// Whether a binary32 product of m x n results goes by planes; `few`: it has a
+// kernel for up to 16 rows.
+bool by_planes(int32_t type, int64_t m, int64_t n, int64_t k, bool few)
 {
-    if (!p || !uneven(type, p, row, rows, width)) return p;
-    void* copy = workspace;
-    workspace += copy_bytes(rows, width);
-    launch_copy_rows(p, row, rows, width, copy, padded(width), st);
-    row = padded(width);
-    return copy;
+    return type == NMS_TYPE_F32 && !(few && m <= 16) && split_pays(m, n, k);
 }
 
-bool launch_product(const ProductArgs& p, cudaStream_t st)
+// An operand of a product: itself, or what the tensor cores take in its place, in
+// the workspace, which moves on.
+struct Operand {
+    const void* p;
+    int64_t row, rows, width;
+    int32_t type;
+    const void* planes = nullptr;
+    void ready(bool as_planes, char*& workspace, cudaStream_t st)
+    {
+        if (as_planes) {
+            if (planes) return;
+            planes = workspace;
+            launch_split_rows(static_cast<const float*>(p), row, rows, width, workspace, padded(width), st);
+            workspace += plane_bytes(rows, width);
+        } else if (uneven(type, p, row, rows, width)) {
+            launch_copy_rows(p, row, rows, width, workspace, padded(width), st);
+            p = workspace;
+            row = padded(width);
+            workspace += copy_bytes(rows, width);
+        }
+    }
+};
+
+bool launch_product(ProductArgs& q, Operand& a, Operand& b, bool as_planes, char*& workspace, cudaStream_t st)
 {
-    return p.type == NMS_TYPE_F32 ? launch_product_f32(p, st) : launch_product_tc(p, st);
+    a.ready(as_planes, workspace, st);
+    b.ready(as_planes, workspace, st);
+    q.a = as_planes ? a.planes : a.p;
+    q.b = as_planes ? b.planes : b.p;
+    q.a_row = as_planes ? padded(a.width) : a.row;
+    q.b_row = as_planes ? padded(b.width) : b.row;
+    if (as_planes) return launch_product_split(q, st);
+    return q.type == NMS_TYPE_F32 ? launch_product_f32(q, st) : launch_product_tc(q, st);
 }
 
 }  // namespace
@@ -72,7 +100,10 @@ extern "C" nms_status nms_linear_workspace_size(int32_t type, int64_t rows, int3
     if (!bytes) return NMS_ERR_INVALID_ARG;
     const nms_status s = check_linear(type, rows, inner, outer);
     if (s != NMS_OK) return s;
-    *bytes = type == NMS_TYPE_F32 || aligned || rows == 0 ? 0 : copy_bytes(rows, inner) + copy_bytes(outer, inner);
+    *bytes = 0;
+    if (rows == 0) return NMS_OK;
+    if (by_planes(type, rows, outer, inner, true)) *bytes = plane_bytes(rows, inner) + plane_bytes(outer, inner);
+    else if (type != NMS_TYPE_F32 && !aligned) *bytes = copy_bytes(rows, inner) + copy_bytes(outer, inner);
     return NMS_OK;
 }
 
@@ -100,11 +131,8 @@ extern "C" nms_status nms_linear_run(const void* x, int64_t x_row, int32_t type,
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaGetLastError();
     char* rest = static_cast<char*>(workspace);
+    Operand a{x, x_row, rows, inner, type}, b{weight, weight_row, outer, inner, type};
     ProductArgs p{};
-    p.a = even(type, x, x_row, rows, inner, rest, st);
-    p.a_row = x_row;
-    p.b = even(type, weight, weight_row, outer, inner, rest, st);
-    p.b_row = weight_row;
     p.type = type;
     p.m = rows;
     p.n = outer;
@@ -117,7 +145,7 @@ extern "C" nms_status nms_linear_run(const void* x, int64_t x_row, int32_t type,
     p.out = y;
     p.pre = pre;
     p.status = dev_status;
-    if (!launch_product(p, st)) return NMS_ERR_CUDA;
+    if (!launch_product(p, a, b, by_planes(type, rows, outer, inner, true), rest, st)) return NMS_ERR_CUDA;
     return cuda_status();
 }
 
@@ -130,7 +158,10 @@ extern "C" nms_status nms_linear_grad_workspace_size(int32_t type, int64_t rows,
     *bytes = 0;
     if (rows == 0) return NMS_OK;
     *bytes = round_up(type_bytes(type) * rows * padded(outer)) + round_up(slope_workspace_bytes(rows, outer));
-    if (type != NMS_TYPE_F32 && !aligned) *bytes += copy_bytes(rows, inner) + copy_bytes(outer, inner);
+    if (by_planes(type, rows, inner, outer, true) || by_planes(type, outer, inner, rows, false))
+        *bytes += plane_bytes(rows, outer) + plane_bytes(outer, inner) + plane_bytes(rows, inner);
+    else if (type != NMS_TYPE_F32 && !aligned)
+        *bytes += copy_bytes(rows, inner) + copy_bytes(outer, inner);
     return NMS_OK;
 }
 
@@ -181,32 +212,26 @@ extern "C" nms_status nms_linear_grad_run(const void* dy, int64_t dy_row, const 
         a.dbias = dbias;
         launch_slope(a, sums, st);
     }
+    Operand z{copied ? workspace : dy, copied ? padded(outer) : dy_row, rows, outer, type};
+    Operand xs{x, x_row, rows, inner, type}, ws{weight, weight_row, outer, inner, type};
     ProductArgs p{};
     p.type = type;
     p.act = NMS_ACT_NONE;
-    p.a = copied ? workspace : dy;
-    p.a_row = copied ? padded(outer) : dy_row;
     p.status = dev_status;
+    p.b_across = 1;
+    p.n = inner;
     if (dx) {
-        p.b = even(type, weight, weight_row, outer, inner, rest, st);
-        p.b_row = weight_row;
-        p.b_across = 1;
         p.m = rows;
-        p.n = inner;
         p.k = outer;
         p.out = dx;
-        if (!launch_product(p, st)) return NMS_ERR_CUDA;
+        if (!launch_product(p, z, ws, by_planes(type, rows, inner, outer, true), rest, st)) return NMS_ERR_CUDA;
     }
     if (dweight) {
         p.a_across = 1;
-        p.b = even(type, x, x_row, rows, inner, rest, st);
-        p.b_row = x_row;
-        p.b_across = 1;
         p.m = outer;
-        p.n = inner;
         p.k = rows;
         p.out = dweight;
-        if (!launch_product(p, st)) return NMS_ERR_CUDA;
+        if (!launch_product(p, z, xs, by_planes(type, outer, inner, rows, false), rest, st)) return NMS_ERR_CUDA;
     }
     return cuda_status();
 }

@@ -1,0 +1,381 @@
+// Matrix products of binary32 operands on the tensor cores (tcgen05).
+//
+// A binary32 number is the sum of three of bfloat16, x = h + m + l: h is x rounded,
+// m the rest rounded, l what is left, 8 significant bits each.  Of the nine
+// products of two such sums six are taken; the others are below 2^-26 of x y.
+//
+// The tensor cores add up in binary32, but cut off below two more bits than its
+// 24 after every 16 products (measured: 1 + 1.5 * 2^-24 stays 1), which leaves a
+// sum over k = 4096 off by 4e-6.  So an accumulator takes 64 of k only, smallest
+// products first, and the writers add it to binary32 sums in registers (rounded
+// to nearest) while the next 64 go to a second one.
+//
+// A block has tiles of 128 x 128: 32 KB of operands in 16-bit planes, three times,
+// for 24 instructions of 64 cycles each, which read 128 bytes of shared memory a
+// cycle: that bounds it.  Few tiles: a cluster's blocks share one, as in
+// k_product.cu.
+#include <atomic>
+
+#include "tensor_core.cuh"
+
+namespace gbnms {
+
+namespace {
+
+constexpr int SP_N = 128, SP_PLANES = 3, SP_STAGES = 2;
+constexpr int SP_STAGE = SP_PLANES * 2 * A_BYTES;  // A's planes, then B's, of as many rows
+constexpr int SP_SMEM = 1024 + SP_STAGES * SP_STAGE;
+constexpr int SP_PITCH = SP_N + 4;  // of a block's part, in shared memory
+
+struct SplitArgs {
+    int a_across, b_across;
+    int64_t m, n, k;
+    int64_t tiles_m, tiles_n;
+    int split;
+    const float* bias;
+    int act;
+    const float* residual;
+    int64_t residual_row;
+    float* out;
+    float* pre;
+    int vector;  // rows of out, pre and residual start at multiples of 16 bytes
+    int32_t* status;
+};
+
+__device__ __forceinline__ void tma_load_plane(uint32_t dst, const CUtensorMap* map, int x, int y, int plane, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(plane)
+        : "memory");
+}
+
+// Four results of a row, those below n.
+__device__ __forceinline__ void finish_four(const SplitArgs& p, int64_t m, int64_t n, const float* sum, const float* bias)
+{
+    const int64_t at = m * p.n + n;
+    float z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] = sum[i] + bias[i];
+    if (p.vector) {
+        if (p.pre) *reinterpret_cast<float4*>(p.pre + at) = make_float4(z[0], z[1], z[2], z[3]);
+        act_values<float>(z, p.act);
+        if (p.residual) {
+            const float4 r = *reinterpret_cast<const float4*>(p.residual + m * p.residual_row + n);
+            z[0] += r.x;
+            z[1] += r.y;
+            z[2] += r.z;
+            z[3] += r.w;
+        }
+        *reinterpret_cast<float4*>(p.out + at) = make_float4(z[0], z[1], z[2], z[3]);
+        return;
+    }
+    if (p.pre) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < p.n) p.pre[at + i] = z[i];
+    }
+    act_values<float>(z, p.act);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + i < p.n) p.out[at + i] = p.residual ? z[i] + p.residual[m * p.residual_row + n + i] : z[i];
+}
+
+__global__ void __launch_bounds__(TC_THREADS, 1)
+product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const SplitArgs p)
+{
+    constexpr int COLUMNS = 2 * SP_N;
+    extern __shared__ char dynamic[];
+    __shared__ alignas(8) uint64_t bars[2 * SP_STAGES + 4];
+    __shared__ uint32_t tensor_at;
+    __shared__ alignas(16) float bias_s[SP_N];
+    const uint32_t ring = (shared_address(dynamic) + 1023) & ~1023u;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t full = shared_address(bars), empty = full + 8 * SP_STAGES, done = empty + 8 * SP_STAGES, free_ = done + 16;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < SP_STAGES; ++s) {
+            barrier_init(full + 8 * s, 1);
+            barrier_init(empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            barrier_init(done + 8 * b, 1);
+            barrier_init(free_ + 8 * b, TC_WRITERS / 32);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_address(&tensor_at)),
+                     "n"(COLUMNS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tensor = tensor_at;
+    pdl_wait();
+    const int rank = static_cast<int>(blockIdx.x) % p.split;
+    const int64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + TC_K - 1) / TC_K, each = (steps + p.split - 1) / p.split;
+    const int64_t first = min(steps, rank * each), last = min(steps, first + each);  // of k, this block's
+    const int64_t tile0 = blockIdx.x / p.split, tile_step = gridDim.x / p.split;
+    bool waited = true;  // false: a wait gave up
+
+    if (warp == 0 && lane == 0) {  // ---- operands to the ring
+        int s = 0, turn = 0;
+        for (int64_t t = tile0; t < tiles && waited; t += tile_step) {
+            const Place at = tile_place(t, p.tiles_m, p.tiles_n, TC_M, SP_N);
+            const int m = static_cast<int>(at.m), n = static_cast<int>(at.n);
+            for (int64_t k = first; k < last; ++k) {
+                waited = barrier_wait(empty + 8 * s, turn ^ 1);
+                if (!waited) break;
+                const uint32_t bar = full + 8 * s, a = ring + s * SP_STAGE, b = a + SP_PLANES * A_BYTES;
+                barrier_expect(bar, SP_STAGE);
+                const int x = static_cast<int>(k * TC_K);
+#pragma unroll
+                for (int q = 0; q < SP_PLANES; ++q) {
+                    if (p.a_across) {
+                        tma_load_plane(a + q * A_BYTES, &map_a, m, x, q, bar);
+                        tma_load_plane(a + q * A_BYTES + HALF_BYTES, &map_a, m + 64, x, q, bar);
+                    } else {
+                        tma_load_plane(a + q * A_BYTES, &map_a, x, m, q, bar);
+                    }
+                    if (p.b_across) {
+                        tma_load_plane(b + q * A_BYTES, &map_b, n, x, q, bar);
+                        tma_load_plane(b + q * A_BYTES + HALF_BYTES, &map_b, n + 64, x, q, bar);
+                    } else {
+                        tma_load_plane(b + q * A_BYTES, &map_b, x, n, q, bar);
+                    }
+                }
+                if (++s == SP_STAGES) {
+                    s = 0;
+                    turn ^= 1;
+                }
+            }
+        }
+        if (!waited) settle();
+    } else if (warp == 1 && lane == 0) {  // ---- matrix instructions
+        const uint32_t form = instruction_form<__nv_bfloat16>(p.a_across, p.b_across, TC_M, SP_N);
+        const uint64_t form_a = operand_form(p.a_across), form_b = operand_form(p.b_across);
+        const uint32_t step_a = p.a_across ? 128 : 2, step_b = p.b_across ? 128 : 2;  // 16 of k, in 16 bytes
+        int s = 0, turn = 0, set = 0, set_turn = 0;
+        for (int64_t t = tile0; t < tiles && waited; t += tile_step) {
+            for (int64_t k = first; k < last; ++k) {
+                waited = barrier_wait(free_ + 8 * set, set_turn ^ 1) && barrier_wait(full + 8 * s, turn);
+                if (!waited) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                // Descriptors have 14 bits of an address; a cluster's blocks have their rank above bit 23 of it.
+                const uint32_t a = ((ring + s * SP_STAGE) & 0x3ffff) >> 4, b = a + SP_PLANES * A_BYTES / 16;
+                constexpr int OF_A[6] = {0, 2, 1, 0, 1, 0}, OF_B[6] = {2, 0, 1, 1, 0, 0};  // h l, l h, m m, h m, m h, h h
+#pragma unroll
+                for (int q = 0; q < 6; ++q)
+#pragma unroll
+                    for (int i = 0; i < TC_K / 16; ++i)
+                        mma<false>(tensor + set * SP_N, form_a | (a + OF_A[q] * (A_BYTES / 16) + i * step_a),
+                                   form_b | (b + OF_B[q] * (A_BYTES / 16) + i * step_b), form, q > 0 || i > 0);
+                mma_commit<false>(empty + 8 * s);
+                mma_commit<false>(done + 8 * set);
+                if (++s == SP_STAGES) {
+                    s = 0;
+                    turn ^= 1;
+                }
+                set_turn ^= set;
+                set ^= 1;
+            }
+        }
+        if (!waited) settle();
+    } else if (warp >= 2) {  // ---- results
+        const int writer = threadIdx.x - 64, quarter = warp % 4, row = quarter * 32 + lane, c0 = (warp - 2) / 4 * (SP_N / 2);
+        int set = 0, set_turn = 0;
+        for (int64_t t = tile0; t < tiles; t += tile_step) {
+            const Place at = tile_place(t, p.tiles_m, p.tiles_n, TC_M, SP_N);
+            asm volatile("bar.sync 1, %0;" ::"n"(TC_WRITERS) : "memory");  // nobody reads the last tile's bias
+            for (int e = writer; e < SP_N; e += TC_WRITERS) bias_s[e] = p.bias && at.n + e < p.n ? p.bias[at.n + e] : 0.0f;
+            asm volatile("bar.sync 1, %0;" ::"n"(TC_WRITERS) : "memory");
+            float sum[SP_N / 2];
+#pragma unroll
+            for (int i = 0; i < SP_N / 2; ++i) sum[i] = 0.0f;
+            for (int64_t k = first; k < last; ++k) {
+                if (waited) waited = barrier_wait(done + 8 * set, set_turn);
+                __syncwarp();
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t acc = tensor + set * SP_N + (static_cast<uint32_t>(quarter * 32) << 16) + c0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v[32];
+                    tensor_load(v, acc + 32 * h);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sum[32 * h + i] += v[i];
+                }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) barrier_arrive(free_ + 8 * set);
+                set_turn ^= set;
+                set ^= 1;
+            }
+            if (!waited) {  // no number comes out of what should have been summed
+#pragma unroll
+                for (int i = 0; i < SP_N / 2; ++i) sum[i] = NAN;
+                if (p.status && writer == 0) set_status(p.status, NMS_ERR_TIMEOUT);
+            }
+            if (p.split > 1) {
+                // The block's part to its own shared memory: the ring is empty by now.
+                float* part = reinterpret_cast<float*>(dynamic + (ring - shared_address(dynamic))) + row * SP_PITCH + c0;
+#pragma unroll
+                for (int i = 0; i < SP_N / 2; i += 4)
+                    *reinterpret_cast<float4*>(part + i) = make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
+                break;  // one tile a cluster
+            }
+            const int64_t m = at.m + row;
+#pragma unroll
+            for (int i = 0; i < SP_N / 2; i += 4)
+                if (m < p.m && at.n + c0 + i < p.n) finish_four(p, m, at.n + c0 + i, sum + i, bias_s + c0 + i);
+        }
+    }
+    __syncwarp();
+    if (p.split > 1) {
+        cluster_barrier();
+        if (warp >= 2) {
+            // This block's rows of the tile, the parts added in the blocks' order.
+            const Place at = tile_place(tile0, p.tiles_m, p.tiles_n, TC_M, SP_N);
+            const int rows = TC_M / p.split, writer = threadIdx.x - 64;
+            for (int e = writer; e < rows * SP_N / 4; e += TC_WRITERS) {
+                const int r = rank * rows + e / (SP_N / 4), c = e % (SP_N / 4) * 4;
+                if (at.m + r >= p.m || at.n + c >= p.n) continue;
+                const uint32_t from = ring + 4 * (r * SP_PITCH + c);
+                float sum[4] = {}, v[8][4];
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                    if (b < p.split)
+                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(v[b][0]), "=f"(v[b][1]), "=f"(v[b][2]), "=f"(v[b][3])
+                                     : "r"(peer_address(from, b)));
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                    if (b < p.split) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sum[i] += v[b][i];
+                    }
+                finish_four(p, at.m + r, at.n + c, sum, bias_s + c);
+            }
+        }
+        __syncwarp();
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    // No block leaves while another reads its shared memory.
+    if (p.split > 1) cluster_barrier();
+    else __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tensor), "n"(COLUMNS));
+}
+
+// x = h + m + l, eight elements of a row a thread.  Where x rounds to an infinity
+// (and is none) its first part is cut instead; of a NaN or an infinity the first
+// part is all there is.
+template <bool WIDE>
+__global__ void __launch_bounds__(256)
+split_rows_kernel(const float* from, int64_t from_row, int64_t rows, int64_t width, __nv_bfloat16* to, int64_t to_row)
+{
+    const int64_t parts = to_row / 8, n = rows * parts, plane = rows * to_row;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t row = i / parts, e = (i - row * parts) * 8;
+        const float* p = from + row * from_row + e;
+        float x[8];
+        if (WIDE) {  // 8 divides the width
+            const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = e + k < width ? p[k] : 0.0f;
+        }
+        Pack<__nv_bfloat16, 8> h, m, l;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const bool finite = fabsf(x[k]) < INFINITY;
+            h.v[k] = __float2bfloat16_rn(x[k]);
+            if (finite && fabsf(to_f32(h.v[k])) == INFINITY) h.v[k] = __float2bfloat16_rz(x[k]);
+            const float rest = finite ? x[k] - to_f32(h.v[k]) : 0.0f;
+            m.v[k] = __float2bfloat16_rn(rest);
+            l.v[k] = __float2bfloat16_rn(rest - to_f32(m.v[k]));
+        }
+        __nv_bfloat16* q = to + row * to_row + e;
+        *reinterpret_cast<Pack<__nv_bfloat16, 8>*>(q) = h;
+        *reinterpret_cast<Pack<__nv_bfloat16, 8>*>(q + plane) = m;
+        *reinterpret_cast<Pack<__nv_bfloat16, 8>*>(q + 2 * plane) = l;
+    }
+}
+
+bool encode_planes(CUtensorMap* map, const void* p, int64_t width, int64_t rows, int64_t row, int box_rows)
+{
+    const cuuint64_t size[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows), SP_PLANES};
+    const cuuint64_t stride[2] = {static_cast<cuuint64_t>(row) * 2, static_cast<cuuint64_t>(row) * rows * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, step[3] = {1, 1, 1};
+    const EncodeTiled fn = encoder();
+    return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), size, stride, box, step,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+void launch_split_rows(const float* from, int64_t from_row, int64_t rows, int64_t width, void* to, int64_t to_row,
+                       cudaStream_t st)
+{
+    const int64_t want = (rows * (to_row / 8) + 255) / 256, most = SMS * 8;
+    const unsigned grid = static_cast<unsigned>(want < most ? want : most);
+    __nv_bfloat16* planes = static_cast<__nv_bfloat16*>(to);
+    if (width % 8 == 0 && from_row % 4 == 0 && reinterpret_cast<uintptr_t>(from) % 16 == 0)
+        split_rows_kernel<true><<<grid, 256, 0, st>>>(from, from_row, rows, width, planes, to_row);
+    else
+        split_rows_kernel<false><<<grid, 256, 0, st>>>(from, from_row, rows, width, planes, to_row);
+}
+
+bool launch_product_split(const ProductArgs& q, cudaStream_t st)
+{
+    static std::atomic<uint64_t> ready{0};  // devices on which the kernel may have so much shared memory
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return false;
+    const uint64_t bit = uint64_t(1) << (device & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        if (cudaFuncSetAttribute(product_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SP_SMEM) != cudaSuccess)
+            return false;
+        if (device < 64) ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    SplitArgs p{};
+    p.a_across = q.a_across;
+    p.b_across = q.b_across;
+    p.m = q.m;
+    p.n = q.n;
+    p.k = q.k;
+    p.tiles_m = (q.m + TC_M - 1) / TC_M;
+    p.tiles_n = (q.n + SP_N - 1) / SP_N;
+    p.bias = static_cast<const float*>(q.bias);
+    p.act = q.act;
+    p.residual = static_cast<const float*>(q.residual);
+    p.residual_row = q.residual_row;
+    p.out = static_cast<float*>(q.out);
+    p.pre = static_cast<float*>(q.pre);
+    p.status = q.status;
+    auto aligned = [](const void* v) { return reinterpret_cast<uintptr_t>(v) % 16 == 0; };
+    p.vector = q.n % 4 == 0 && q.residual_row % 4 == 0 && aligned(q.out) && aligned(q.pre) && aligned(q.residual);
+    const int64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + TC_K - 1) / TC_K;
+    p.split = 1;
+    while (p.split < 8 && tiles * p.split * 2 <= SMS && steps >= p.split * 4) p.split *= 2;
+    CUtensorMap map_a, map_b;
+    if (!(p.a_across ? encode_planes(&map_a, q.a, p.m, p.k, q.a_row, 64) : encode_planes(&map_a, q.a, p.k, p.m, q.a_row, TC_M)) ||
+        !(p.b_across ? encode_planes(&map_b, q.b, p.n, p.k, q.b_row, 64) : encode_planes(&map_b, q.b, p.k, p.n, q.b_row, SP_N)))
+        return false;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split < SMS ? tiles * p.split : SMS / p.split * p.split));
+    cfg.blockDim = dim3(TC_THREADS);
+    cfg.dynamicSmemBytes = SP_SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, product_split_kernel, map_a, map_b, p) == cudaSuccess;
+}
+
+}  // namespace gbnms
