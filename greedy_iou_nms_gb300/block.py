@@ -18,7 +18,7 @@ from . import head
 from .head import _ACTS, _lib, _raise
 
 NMS_LAYER_MAX_WIDTH = 16384
-NMS_LINEAR_MAX_WIDTH = 1 << 20
+NMS_LINEAR_MAX_WIDTH = 1 << 18
 NMS_ROTARY_MAX_AXES = 8
 NMS_ROTARY_MAX_DIM = 4096
 NMS_POSITION_I32 = 16

@@ -60,8 +60,6 @@ void launch_rotary(const RotaryArgs& a, cudaStream_t st);
 void launch_column_join(const float* parts, int64_t blocks, int64_t columns, int64_t split, float* first, float* second,
                         cudaStream_t st);
 
-constexpr int64_t SPLIT_LEAST = int64_t(1) << 26;  // multiplications
-
 // out = act(A B^T + bias) + residual, A m x k, B n x k.
 struct ProductArgs {
     const void* a;  // [m][k], or [k][m] with a_across; rows a_row apart
@@ -78,6 +76,8 @@ struct ProductArgs {
     void* out;        // [m][n] contiguous
     void* pre;        // A B^T + bias [m][n] contiguous, or NULL
     int32_t* status;  // or NULL
+    int segments;     // 1; more: stretches of k whose sums go to parts [segments][m][n] in place of out
+    float* parts;
 };
 // Binary32, by the plain arithmetic units.  False: the driver refused a launch.
 bool launch_product_f32(const ProductArgs& p, cudaStream_t st);
@@ -87,8 +87,8 @@ bool launch_product_split(const ProductArgs& p, cudaStream_t st);
 // Rows of binary32 to planes [3][rows][to_row], to_row a multiple of 8.
 void launch_split_rows(const float* from, int64_t from_row, int64_t rows, int64_t width, void* to, int64_t to_row,
                        cudaStream_t st);
-// Which of the two: the tensor cores where their rate outweighs the planes.
-inline bool split_pays(int64_t m, int64_t n, int64_t k) { return m * n >= SPLIT_LEAST / k; }
+// out = sums over the parts [segments][n], of any type, in order.
+void launch_join_parts(const float* parts, int segments, int64_t n, void* out, int type, cudaStream_t st);
 // 16 bits, by the tensor cores: operands and their rows start at multiples of
 // 16 bytes and do not overlap.
 bool launch_product_tc(const ProductArgs& p, cudaStream_t st);

@@ -50,12 +50,34 @@ size_t copy_bytes(int64_t rows, int64_t width) { return round_up(2 * rows * padd
 
 size_t plane_bytes(int64_t rows, int64_t width) { return round_up(3 * 2 * rows * padded(width)); }
 
-// Whether a binary32 product of m x n results goes by planes; `few`: it has a
-// kernel for up to 16 rows.
-bool by_planes(int32_t type, int64_t m, int64_t n, int64_t k, bool few)
+// Whether a binary32 product of m x n results goes by planes to the tensor cores:
+// from 2^27 multiplications on (planes and product took 19 us of 1517 x 333 x 251,
+// 2^26.9, as much as the plain units; 21 of 1200 x 512 x 512, 2^28.2).  A weight's
+// gradient also where it is few results of many rows.
+bool by_planes(int32_t type, int64_t m, int64_t n, int64_t k, bool gradient)
 {
-    return type == NMS_TYPE_F32 && !(few && m <= 16) && split_pays(m, n, k);
+    if (type != NMS_TYPE_F32) return false;
+    if (gradient && k >= 8192) return true;
+    return (gradient || m > 16) && m * n >= (int64_t(1) << 27) / k;
 }
+
+// Stretches of k of a weight's gradient on the tensor cores: where clusters of
+// eight leave half of the SMs idle, one for each SM; and no 16-bit sum over more
+// than 2^18 of k (see k_product_split.cu on what those lose).
+int gradient_segments(int32_t type, int64_t m, int64_t n, int64_t k)
+{
+    if (type == NMS_TYPE_F32 && !by_planes(type, m, n, k, true)) return 1;
+    const int64_t width = type == NMS_TYPE_F32 ? 128 : 64, tiles = ((m + 127) / 128) * ((n + width - 1) / width);
+    int64_t segments = type == NMS_TYPE_F32 ? 1 : (k + (1 << 18) - 1) >> 18;
+    if (tiles * 8 <= SMS / 2 && k >= 8192) {
+        const int64_t fill = SMS / tiles, most = k / 512;
+        const int64_t want = fill < most ? fill : most;
+        if (want > segments) segments = want;
+    }
+    return static_cast<int>(segments);
+}
+
+size_t parts_bytes(int segments, int64_t m, int64_t n) { return segments > 1 ? round_up(4 * segments * m * n) : 0; }
 
 // An operand of a product: itself, or what the tensor cores take in its place, in
 // the workspace, which moves on.
@@ -102,7 +124,7 @@ extern "C" nms_status nms_linear_workspace_size(int32_t type, int64_t rows, int3
     if (s != NMS_OK) return s;
     *bytes = 0;
     if (rows == 0) return NMS_OK;
-    if (by_planes(type, rows, outer, inner, true)) *bytes = plane_bytes(rows, inner) + plane_bytes(outer, inner);
+    if (by_planes(type, rows, outer, inner, false)) *bytes = plane_bytes(rows, inner) + plane_bytes(outer, inner);
     else if (type != NMS_TYPE_F32 && !aligned) *bytes = copy_bytes(rows, inner) + copy_bytes(outer, inner);
     return NMS_OK;
 }
@@ -145,7 +167,8 @@ extern "C" nms_status nms_linear_run(const void* x, int64_t x_row, int32_t type,
     p.out = y;
     p.pre = pre;
     p.status = dev_status;
-    if (!launch_product(p, a, b, by_planes(type, rows, outer, inner, true), rest, st)) return NMS_ERR_CUDA;
+    p.segments = 1;
+    if (!launch_product(p, a, b, by_planes(type, rows, outer, inner, false), rest, st)) return NMS_ERR_CUDA;
     return cuda_status();
 }
 
@@ -158,7 +181,8 @@ extern "C" nms_status nms_linear_grad_workspace_size(int32_t type, int64_t rows,
     *bytes = 0;
     if (rows == 0) return NMS_OK;
     *bytes = round_up(type_bytes(type) * rows * padded(outer)) + round_up(slope_workspace_bytes(rows, outer));
-    if (by_planes(type, rows, inner, outer, true) || by_planes(type, outer, inner, rows, false))
+    *bytes += parts_bytes(gradient_segments(type, outer, inner, rows), outer, inner);
+    if (by_planes(type, rows, inner, outer, false) || by_planes(type, outer, inner, rows, true))
         *bytes += plane_bytes(rows, outer) + plane_bytes(outer, inner) + plane_bytes(rows, inner);
     else if (type != NMS_TYPE_F32 && !aligned)
         *bytes += copy_bytes(rows, inner) + copy_bytes(outer, inner);
@@ -220,18 +244,25 @@ extern "C" nms_status nms_linear_grad_run(const void* dy, int64_t dy_row, const 
     p.status = dev_status;
     p.b_across = 1;
     p.n = inner;
+    p.segments = 1;
     if (dx) {
         p.m = rows;
         p.k = outer;
         p.out = dx;
-        if (!launch_product(p, z, ws, by_planes(type, rows, inner, outer, true), rest, st)) return NMS_ERR_CUDA;
+        if (!launch_product(p, z, ws, by_planes(type, rows, inner, outer, false), rest, st)) return NMS_ERR_CUDA;
     }
     if (dweight) {
         p.a_across = 1;
         p.m = outer;
         p.k = rows;
         p.out = dweight;
-        if (!launch_product(p, z, xs, by_planes(type, outer, inner, rows, false), rest, st)) return NMS_ERR_CUDA;
+        p.segments = gradient_segments(type, outer, inner, rows);
+        if (p.segments > 1) {
+            p.parts = reinterpret_cast<float*>(rest);
+            rest += parts_bytes(p.segments, outer, inner);
+        }
+        if (!launch_product(p, z, xs, by_planes(type, outer, inner, rows, true), rest, st)) return NMS_ERR_CUDA;
+        if (p.segments > 1) launch_join_parts(p.parts, p.segments, static_cast<int64_t>(outer) * inner, dweight, type, st);
     }
     return cuda_status();
 }

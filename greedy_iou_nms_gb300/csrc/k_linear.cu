@@ -2,12 +2,11 @@
 // their epilogue, on the plain arithmetic units, and the copy of 16-bit rows
 // whose places the tensor cores' loads cannot take.
 //
-// product_kernel: a block has a tile of 16 SM x 16 SN results, its 256 threads SM
-// x SN of them each.  Tiles of 128 x 64 leave room for two blocks an SM, one of
-// which multiplies while the other waits (8 x 8 a thread, two blocks an SM, took
-// 530 us for 2048 x 2048 x 2048, 8 x 4 504).  Few tiles: the blocks of a cluster
-// share one, each a stretch of k, and add up their parts through distributed
-// shared memory, in order.
+// product_kernel, for products of less than 2^27 multiplications (larger ones go
+// to the tensor cores, k_product_split.cu): a block has a tile of 64 x 64 results,
+// its 256 threads 4 x 4 of them each.  Few tiles: the blocks of a cluster share
+// one, each a stretch of k, and add up their parts through distributed shared
+// memory, in order.
 //
 // Up to 16 rows are a stream of the weight, whose elements are used once a row:
 // few_along_kernel and few_across_kernel read it straight to registers, all of an
@@ -22,13 +21,14 @@ namespace {
 
 constexpr int PR_DEPTH = 16;   // of a step along k
 constexpr int PR_STAGES = 3;   // steps in shared memory
+constexpr int PR_TILE = 64, PR_STRIDE = PR_TILE + 4;
 
 // One operand's way to shared memory, [k][m or n], element by element
 // (cp.async), so that any stride and start will do and either order of the
 // operand.  Element i of a thread lies i * delta behind its first.
-template <int TILE, bool ACROSS>
+template <bool ACROSS>
 struct Feed {
-    static constexpr int N = TILE * PR_DEPTH / 256, STRIDE = TILE + 4;
+    static constexpr int TILE = PR_TILE, STRIDE = PR_STRIDE, N = TILE * PR_DEPTH / 256;
     const float* from;
     int64_t delta, step;
     uint32_t to;
@@ -93,24 +93,23 @@ __device__ __forceinline__ void finish(const ProductArgs& p, int64_t m, int64_t 
     static_cast<float*>(p.out)[m * p.n + n] = z[0];
 }
 
-template <int SM, int SN, bool A_ACROSS, bool B_ACROSS>
-__global__ void __launch_bounds__(256, SM == 8 ? 2 : 3)
+template <bool A_ACROSS, bool B_ACROSS>
+__global__ void __launch_bounds__(256, 3)
 product_kernel(const ProductArgs p, int64_t tiles_n, int split)
 {
-    constexpr int TM = 16 * SM, TN = 16 * SN, AS = TM + 4, BS = TN + 4;
-    static_assert(TM * BS <= PR_STAGES * PR_DEPTH * (AS + BS), "a block's part fits in the stages");
-    extern __shared__ __align__(16) float stages[];  // [PR_STAGES][PR_DEPTH] of AS, of BS; then the block's part [TM][BS]
+    static_assert(PR_TILE <= 2 * PR_STAGES * PR_DEPTH, "a block's part fits in the stages");
+    extern __shared__ __align__(16) float stages[];  // [2][PR_STAGES][PR_DEPTH][PR_STRIDE]; then the block's part
     float* const as = stages;
-    float* const bs = stages + PR_STAGES * PR_DEPTH * AS;
+    float* const bs = stages + PR_STAGES * PR_DEPTH * PR_STRIDE;
     const int64_t tile = blockIdx.x / split, rank = blockIdx.x - tile * split;
     const int64_t tm = tile / tiles_n, tn = tile - tm * tiles_n;
-    const int64_t m0 = tm * TM, n0 = tn * TN;
+    const int64_t m0 = tm * PR_TILE, n0 = tn * PR_TILE;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    float acc[SM][SN] = {}, total[SM][SN] = {};
+    float acc[4][4] = {}, total[4][4] = {};
     const int64_t all = (p.k + PR_DEPTH - 1) / PR_DEPTH, each = (all + split - 1) / split;
     const int64_t from = min(p.k, rank * each * PR_DEPTH), count = min(p.k - from, each * PR_DEPTH);  // of k, this block's
-    Feed<TM, A_ACROSS> a(static_cast<const float*>(p.a), p.a_row, m0, p.m, from, count, as);
-    Feed<TN, B_ACROSS> b(static_cast<const float*>(p.b), p.b_row, n0, p.n, from, count, bs);
+    Feed<A_ACROSS> a(static_cast<const float*>(p.a), p.a_row, m0, p.m, from, count, as);
+    Feed<B_ACROSS> b(static_cast<const float*>(p.b), p.b_row, n0, p.n, from, count, bs);
     const int64_t steps = (count + PR_DEPTH - 1) / PR_DEPTH;
 #pragma unroll
     for (int s = 0; s < PR_STAGES - 1; ++s) {
@@ -129,28 +128,28 @@ product_kernel(const ProductArgs p, int64_t tiles_n, int split)
             b.next(ahead);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        const float* const ak = as + at * PR_DEPTH * AS;
-        const float* const bk = bs + at * PR_DEPTH * BS;
+        const float* const ak = as + at * PR_DEPTH * PR_STRIDE;
+        const float* const bk = bs + at * PR_DEPTH * PR_STRIDE;
 #pragma unroll
         for (int k = 0; k < PR_DEPTH; ++k) {
-            alignas(16) float x[SM], w[SN];
+            alignas(16) float x[4], w[4];
 #pragma unroll
-            for (int i = 0; i < SM; i += 4)
-                *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(ak + k * AS + i * 16 + ty * 4);
+            for (int i = 0; i < 4; i += 4)
+                *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(ak + k * PR_STRIDE + i * 16 + ty * 4);
 #pragma unroll
-            for (int j = 0; j < SN; j += 4)
-                *reinterpret_cast<float4*>(w + j) = *reinterpret_cast<const float4*>(bk + k * BS + j * 16 + tx * 4);
+            for (int j = 0; j < 4; j += 4)
+                *reinterpret_cast<float4*>(w + j) = *reinterpret_cast<const float4*>(bk + k * PR_STRIDE + j * 16 + tx * 4);
 #pragma unroll
-            for (int i = 0; i < SM; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < SN; ++j) acc[i][j] = fmaf(x[i], w[j], acc[i][j]);
+                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], w[j], acc[i][j]);
         }
         // Sums of 256 products, added up: a chain over all of k would round off with k.
         if (s % 16 == 15 || s + 1 == steps) {
 #pragma unroll
-            for (int i = 0; i < SM; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < SN; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     total[i][j] += acc[i][j];
                     acc[i][j] = 0.0f;
                 }
@@ -160,10 +159,10 @@ product_kernel(const ProductArgs p, int64_t tiles_n, int split)
     }
     if (split == 1) {
 #pragma unroll
-        for (int i = 0; i < SM; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const int64_t m = m0 + (i / 4) * 64 + ty * 4 + i % 4;
 #pragma unroll
-            for (int j = 0; j < SN; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 const int64_t n = n0 + (j / 4) * 64 + tx * 4 + j % 4;
                 if (m < p.m && n < p.n) finish(p, m, n, total[i][j]);
             }
@@ -172,16 +171,16 @@ product_kernel(const ProductArgs p, int64_t tiles_n, int split)
     }
     __syncthreads();  // the stages are no longer read
 #pragma unroll
-    for (int i = 0; i < SM; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < SN; j += 4)
-            *reinterpret_cast<float4*>(stages + ((i / 4) * 64 + ty * 4 + i % 4) * BS + j * 16 + tx * 4) =
+        for (int j = 0; j < 4; j += 4)
+            *reinterpret_cast<float4*>(stages + ((i / 4) * 64 + ty * 4 + i % 4) * PR_STRIDE + j * 16 + tx * 4) =
                 make_float4(total[i][j], total[i][j + 1], total[i][j + 2], total[i][j + 3]);
     cluster_barrier();
-    const int rows = TM / split;
-    for (int e = threadIdx.x; e < rows * TN; e += 256) {
-        const int r = static_cast<int>(rank) * rows + e / TN, c = e % TN;
-        if (m0 + r < p.m && n0 + c < p.n) finish(p, m0 + r, n0 + c, cluster_sum(stages + r * BS + c, split));
+    const int rows = PR_TILE / split;
+    for (int e = threadIdx.x; e < rows * PR_TILE; e += 256) {
+        const int r = static_cast<int>(rank) * rows + e / PR_TILE, c = e % PR_TILE;
+        if (m0 + r < p.m && n0 + c < p.n) finish(p, m0 + r, n0 + c, cluster_sum(stages + r * PR_STRIDE + c, split));
     }
     __syncwarp();
     cluster_barrier();  // no block leaves while another reads its part
@@ -294,6 +293,25 @@ few_across_kernel(const ProductArgs p, int split)
     cluster_barrier();  // no block leaves while another reads its sums
 }
 
+template <typename T>
+__global__ void __launch_bounds__(256)
+join_parts_kernel(const float* parts, int segments, int64_t n, T* out)
+{
+    pdl_wait();  // the parts are there
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+        constexpr int AHEAD = 8;
+        float sum = 0.0f;
+        for (int s = 0; s < segments; s += AHEAD) {
+            float v[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) v[k] = s + k < segments ? parts[(s + k) * n + i] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) sum += v[k];
+        }
+        out[i] = from_f32<T>(sum);
+    }
+}
+
 // Eight elements of a row a thread.
 __global__ void __launch_bounds__(256)
 copy_rows_kernel(const uint16_t* from, int64_t from_row, int64_t rows, int64_t width, uint16_t* to, int64_t to_row)
@@ -353,17 +371,16 @@ static bool launch_few(const ProductArgs& p, cudaStream_t st)
     return launch_clusters(few_across_kernel<R, 1>, groups, split, smem, st, p, split);
 }
 
-template <int SM, int SN>
 static bool launch_tiles(const ProductArgs& p, cudaStream_t st)
 {
-    constexpr int TM = 16 * SM, TN = 16 * SN, SMEM = PR_STAGES * PR_DEPTH * (TM + 4 + TN + 4) * 4;
-    const int64_t tiles_n = (p.n + TN - 1) / TN, tiles = ((p.m + TM - 1) / TM) * tiles_n;
+    constexpr int SMEM = 2 * PR_STAGES * PR_DEPTH * PR_STRIDE * 4;
+    const int64_t tiles_n = (p.n + PR_TILE - 1) / PR_TILE, tiles = ((p.m + PR_TILE - 1) / PR_TILE) * tiles_n;
     const int64_t steps = (p.k + PR_DEPTH - 1) / PR_DEPTH;
     int split = 1;
     while (split < 8 && tiles * split * 2 <= SMS * 4 && steps >= split * 8) split *= 2;
-    if (p.a_across) return launch_clusters(product_kernel<SM, SN, true, true>, tiles, split, SMEM, st, p, tiles_n, split);
-    if (p.b_across) return launch_clusters(product_kernel<SM, SN, false, true>, tiles, split, SMEM, st, p, tiles_n, split);
-    return launch_clusters(product_kernel<SM, SN, false, false>, tiles, split, SMEM, st, p, tiles_n, split);
+    if (p.a_across) return launch_clusters(product_kernel<true, true>, tiles, split, SMEM, st, p, tiles_n, split);
+    if (p.b_across) return launch_clusters(product_kernel<false, true>, tiles, split, SMEM, st, p, tiles_n, split);
+    return launch_clusters(product_kernel<false, false>, tiles, split, SMEM, st, p, tiles_n, split);
 }
 
 bool launch_product_f32(const ProductArgs& p, cudaStream_t st)
@@ -372,9 +389,23 @@ bool launch_product_f32(const ProductArgs& p, cudaStream_t st)
         if (p.m == 1) return launch_few<1>(p, st);
         return p.m <= 4 ? launch_few<4>(p, st) : launch_few<16>(p, st);
     }
-    // The larger tile where it fills the SMs: it reads a quarter less.
-    if (((p.m + 127) / 128) * ((p.n + 63) / 64) >= 2 * SMS) return launch_tiles<8, 4>(p, st);
-    return launch_tiles<4, 4>(p, st);
+    return launch_tiles(p, st);
+}
+
+void launch_join_parts(const float* parts, int segments, int64_t n, void* out, int type, cudaStream_t st)
+{
+    const int64_t want = (n + 255) / 256, most = SMS * 8;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(want < most ? want : most));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (type == NMS_TYPE_F32) cudaLaunchKernelEx(&cfg, join_parts_kernel<float>, parts, segments, n, static_cast<float*>(out));
+    else if (type == NMS_TYPE_F16)
+        cudaLaunchKernelEx(&cfg, join_parts_kernel<__half>, parts, segments, n, static_cast<__half*>(out));
+    else cudaLaunchKernelEx(&cfg, join_parts_kernel<__nv_bfloat16>, parts, segments, n, static_cast<__nv_bfloat16*>(out));
 }
 
 void launch_copy_rows(const void* from, int64_t from_row, int64_t rows, int64_t width, void* to, int64_t to_row,

@@ -37,7 +37,9 @@ struct TcArgs {
     int a_across, b_across;
     int64_t m, n, k;
     int64_t tiles_m, tiles_n;
-    int split;  // blocks of a cluster, which share a tile along k
+    int split;     // blocks of a cluster, which share a tile along k
+    int segments;  // stretches of k whose sums go to parts [segments][m][n], 1: none
+    float* parts;
     const void* bias;
     int bias_f32, act;
     const void* residual;
@@ -98,8 +100,26 @@ struct Patch {
         for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const Vec*>(own + i * 16);
         __syncwarp();
     }
-    // One row a lane to memory.
-    __device__ __forceinline__ void put(const float (&z)[32], T* at, int64_t stride, int64_t row, int64_t m, int lane) const
+    // The same of rows that start anywhere: a lane has a column, the 32 rows one after another.
+    __device__ __forceinline__ void spread_columns(const T* at, int64_t stride, int64_t row, int64_t m, int64_t columns,
+                                                   int lane) const
+    {
+        T* const patch = reinterpret_cast<T*>(own - lane * TC_PITCH) + lane;
+        if (lane < columns)
+            for (int r = 0; r < 32 && row + r < m; ++r) patch[r * (TC_PITCH / 2)] = at[(row + r) * stride + lane];
+        __syncwarp();
+    }
+    __device__ __forceinline__ void put_columns(const float (&z)[32], T* at, int64_t stride, int64_t row, int64_t m,
+                                                int64_t columns, int lane) const
+    {
+        const T* const patch = reinterpret_cast<const T*>(own - lane * TC_PITCH) + lane;
+        leave(z);
+        if (lane < columns)
+            for (int r = 0; r < 32 && row + r < m; ++r) at[(row + r) * stride + lane] = patch[r * (TC_PITCH / 2)];
+        __syncwarp();
+    }
+    // One row a lane.
+    __device__ __forceinline__ void leave(const float (&z)[32]) const
     {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -109,6 +129,10 @@ struct Patch {
             *reinterpret_cast<Vec*>(own + i * 16) = pack_results<T, 8>(e);
         }
         __syncwarp();
+    }
+    __device__ __forceinline__ void put(const float (&z)[32], T* at, int64_t stride, int64_t row, int64_t m, int lane) const
+    {
+        leave(z);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t r = row + i * 8 + lane / 4;
@@ -165,16 +189,23 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     const uint32_t tensor = tensor_at;
     pdl_wait();
     const int share = PAIR ? 2 : p.split, rank = static_cast<int>(blockIdx.x) % share;  // of the cluster
-    const int64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + TC_K - 1) / TC_K;
-    const int64_t each = (steps + p.split - 1) / p.split;
-    const int64_t first = PAIR ? 0 : min(steps, rank * each), last = min(steps, first + each);  // of k, this block's
+    const int64_t tiles = p.tiles_m * p.tiles_n, items = tiles * p.segments, steps = (p.k + TC_K - 1) / TC_K;
+    const int64_t sharers = p.segments > 1 ? p.segments : p.split, each = (steps + sharers - 1) / sharers;
+    // Item t: a tile and this block's stretch of k.
+    auto item = [&](int64_t t, int64_t& first, int64_t& last) {
+        const int64_t segment = p.segments > 1 ? t / tiles : PAIR ? 0 : rank;
+        first = min(steps, segment * each);
+        last = min(steps, first + each);
+        return tile_place(p.segments > 1 ? t - segment * tiles : t, p.tiles_m, p.tiles_n, ROWS, BN);
+    };
     const int64_t tile0 = blockIdx.x / share, tile_step = gridDim.x / share;
     bool waited = true;  // false: a wait gave up
 
     if (warp == 0 && lane == 0) {  // ---- operands to the ring
         int s = 0, turn = 0;
-        for (int64_t t = tile0; t < tiles && waited; t += tile_step) {
-            const Place at = tile_place(t, p.tiles_m, p.tiles_n, ROWS, BN);
+        for (int64_t t = tile0; t < items && waited; t += tile_step) {
+            int64_t first, last;
+            const Place at = item(t, first, last);
             const int m = static_cast<int>(at.m) + (PAIR ? rank * TC_M : 0), n = static_cast<int>(at.n) + (PAIR ? rank * BB : 0);
             for (int64_t k = first; k < last; ++k) {
                 waited = barrier_wait(empty + 8 * s, turn ^ 1);
@@ -207,7 +238,9 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         const uint64_t form_a = operand_form(p.a_across), form_b = operand_form(p.b_across);
         const uint32_t step_a = p.a_across ? 128 : 2, step_b = p.b_across ? 128 : 2;  // 16 of k, in 16 bytes
         int s = 0, turn = 0, set = 0, set_turn = 0;
-        for (int64_t t = tile0; t < tiles && waited; t += tile_step) {
+        for (int64_t t = tile0; t < items && waited; t += tile_step) {
+            int64_t first, last;
+            item(t, first, last);
             waited = barrier_wait(free_ + 8 * set, set_turn ^ 1);
             if (!waited) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -236,8 +269,9 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         char* const ring_at = dynamic + (ring - shared_address(dynamic));
         const Patch<T> patch(ring_at + STAGES * STAGE + (warp - 2) * TC_PATCH, lane);
         int64_t tile_count = 0;
-        for (int64_t t = tile0; t < tiles; t += tile_step, ++tile_count) {
-            Place at = tile_place(t, p.tiles_m, p.tiles_n, ROWS, BN);
+        for (int64_t t = tile0; t < items; t += tile_step, ++tile_count) {
+            int64_t first, last;
+            Place at = item(t, first, last);
             if (PAIR) at.m += rank * TC_M;
             const int set = static_cast<int>(tile_count & 1), turn = static_cast<int>(tile_count >> 1) & 1;
             const int64_t bias0 = SWAP ? at.m : at.n, biases = SWAP ? p.m : p.n;
@@ -268,7 +302,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                     float v[8];
                     tensor_load(v, acc + c);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) part[c + i] = first < last ? v[i] + lost : 0.0f;
+                    for (int i = 0; i < 8; ++i) part[c + i] = first < last ? v[i] + lost : lost;
                 }
                 break;  // one tile a cluster
             }
@@ -281,17 +315,38 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll
                     for (int i = 0; i < CHUNK; ++i) v[i] = lost;
                 }
-                if constexpr (SWAP) {
+                if (!SWAP && p.segments > 1) {
+                    // Of a stretch without steps nothing was summed.
+                    float* part = p.parts + (t / tiles * p.m + m) * p.n + at.n + c;
+                    if (m < p.m) {
+#pragma unroll
+                        for (int i = 0; i < CHUNK; i += 4) {
+                            if (first == last) v[i] = v[i + 1] = v[i + 2] = v[i + 3] = lost;
+                            if (p.n % 4 == 0 && at.n + c + i < p.n) {
+                                *reinterpret_cast<float4*>(part + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                            } else {
+#pragma unroll
+                                for (int j = i; j < i + 4; ++j)
+                                    if (at.n + c + j < p.n) part[j] = v[j];
+                            }
+                        }
+                    }
+                } else if constexpr (SWAP) {
                     if (m < p.m) {
 #pragma unroll
                         for (int i = 0; i < CHUNK; ++i)
                             if (at.n + c + i < p.n) finish_one<T>(p, m, at.n + c + i, v[i], bias_s[set][row]);
                     }
-                } else if (p.vector && at.n + c + CHUNK <= p.n) {
+                } else {
+                    const bool whole = p.vector && at.n + c + CHUNK <= p.n;
+                    const int64_t columns = p.n - (at.n + c);
                     Pack<T, 8> add[4];
-                    if (more) {
+                    if (whole && more) {
                         patch.spread(ahead);
                         if (c + CHUNK < c0 + BN / 2) fetch(c + CHUNK);
+                        patch.take(add);
+                    } else if (p.residual) {
+                        patch.spread_columns(static_cast<const T*>(p.residual) + at.n + c, p.residual_m, row0, p.m, columns, lane);
                         patch.take(add);
                     }
 #pragma unroll
@@ -302,17 +357,18 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                         v[i + 2] += b.z;
                         v[i + 3] += b.w;
                     }
-                    if (p.pre) patch.put(v, static_cast<T*>(p.pre) + at.n + c, p.out_m, row0, p.m, lane);
+                    auto put = [&](void* to) {
+                        T* const t = static_cast<T*>(to) + at.n + c;
+                        if (whole) patch.put(v, t, p.out_m, row0, p.m, lane);
+                        else patch.put_columns(v, t, p.out_m, row0, p.m, columns, lane);
+                    };
+                    if (p.pre) put(p.pre);
                     act_values<T, CHUNK>(v, p.act);
-                    if (more) {
+                    if (p.residual) {
 #pragma unroll
                         for (int i = 0; i < CHUNK; ++i) v[i] += to_f32(add[i / 8].v[i % 8]);
                     }
-                    patch.put(v, static_cast<T*>(p.out) + at.n + c, p.out_m, row0, p.m, lane);
-                } else if (m < p.m) {
-#pragma unroll
-                    for (int i = 0; i < CHUNK; ++i)
-                        if (at.n + c + i < p.n) finish_one<T>(p, m, at.n + c + i, v[i], bias_s[set][c + i]);
+                    put(p.out);
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -394,10 +450,10 @@ bool launch_tile(const CUtensorMap& a, const CUtensorMap& b, const TcArgs& p, cu
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) return false;
         if (device < 64) ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    const int64_t tiles = p.tiles_m * p.tiles_n;
+    const int64_t items = p.tiles_m * p.tiles_n * p.segments;
     const int share = PAIR ? 2 : p.split;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * share < SMS ? tiles * share : SMS / share * share));
+    cfg.gridDim = dim3(static_cast<unsigned>(items * share < SMS ? items * share : SMS / share * share));
     cfg.blockDim = dim3(TC_THREADS);
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = st;
@@ -439,6 +495,8 @@ bool launch_product_tc(const ProductArgs& q, cudaStream_t st)
     p.out = q.out;
     p.pre = q.pre;
     p.status = q.status;
+    p.segments = q.segments;
+    p.parts = q.parts;
     const void *a = q.a, *b = q.b;
     int64_t a_row = q.a_row, b_row = q.b_row;
     int bn;
@@ -473,7 +531,7 @@ bool launch_product_tc(const ProductArgs& q, cudaStream_t st)
             for (int w : {256, 128, 64}) {
                 if (two && w == 64) continue;
                 const int64_t rows = two ? 2 * TC_M : TC_M, slots = two ? SMS / 2 : SMS;
-                const int64_t tiles = ((p.m + rows - 1) / rows) * ((p.n + w - 1) / w);
+                const int64_t tiles = ((p.m + rows - 1) / rows) * ((p.n + w - 1) / w) * p.segments;
                 const int64_t cost = ((tiles + slots - 1) / slots) * ((two ? 3 * w : 4 * w) + 192);
                 if (bn == 0 || cost < best) {
                     bn = w;
@@ -487,7 +545,7 @@ bool launch_product_tc(const ProductArgs& q, cudaStream_t st)
     p.tiles_n = (p.n + bn - 1) / bn;
     const int64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + TC_K - 1) / TC_K;
     p.split = 1;
-    while (!pair && p.split < 8 && tiles * p.split * 2 <= SMS && steps >= p.split * 8) p.split *= 2;
+    while (!pair && p.segments == 1 && p.split < 8 && tiles * p.split * 2 <= SMS && steps >= p.split * 8) p.split *= 2;
     CUtensorMap map_a, map_b;
     const bool known =
         (p.a_across ? encode(&map_a, q.type, a, p.m, p.k, a_row, 64) : encode(&map_a, q.type, a, p.k, p.m, a_row, TC_M)) &&

@@ -32,6 +32,8 @@ struct SplitArgs {
     int64_t m, n, k;
     int64_t tiles_m, tiles_n;
     int split;
+    int segments;  // as for the 16-bit product
+    float* parts;
     const float* bias;
     int act;
     const float* residual;
@@ -115,15 +117,23 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     const uint32_t tensor = tensor_at;
     pdl_wait();
     const int rank = static_cast<int>(blockIdx.x) % p.split;
-    const int64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + TC_K - 1) / TC_K, each = (steps + p.split - 1) / p.split;
-    const int64_t first = min(steps, rank * each), last = min(steps, first + each);  // of k, this block's
+    const int64_t tiles = p.tiles_m * p.tiles_n, items = tiles * p.segments, steps = (p.k + TC_K - 1) / TC_K;
+    const int64_t sharers = p.segments > 1 ? p.segments : p.split, each = (steps + sharers - 1) / sharers;
+    // Item t: a tile and this block's stretch of k.
+    auto item = [&](int64_t t, int64_t& first, int64_t& last) {
+        const int64_t segment = p.segments > 1 ? t / tiles : rank;
+        first = min(steps, segment * each);
+        last = min(steps, first + each);
+        return tile_place(p.segments > 1 ? t - segment * tiles : t, p.tiles_m, p.tiles_n, TC_M, SP_N);
+    };
     const int64_t tile0 = blockIdx.x / p.split, tile_step = gridDim.x / p.split;
     bool waited = true;  // false: a wait gave up
 
     if (warp == 0 && lane == 0) {  // ---- operands to the ring
         int s = 0, turn = 0;
-        for (int64_t t = tile0; t < tiles && waited; t += tile_step) {
-            const Place at = tile_place(t, p.tiles_m, p.tiles_n, TC_M, SP_N);
+        for (int64_t t = tile0; t < items && waited; t += tile_step) {
+            int64_t first, last;
+            const Place at = item(t, first, last);
             const int m = static_cast<int>(at.m), n = static_cast<int>(at.n);
             for (int64_t k = first; k < last; ++k) {
                 waited = barrier_wait(empty + 8 * s, turn ^ 1);
@@ -158,7 +168,9 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
         const uint64_t form_a = operand_form(p.a_across), form_b = operand_form(p.b_across);
         const uint32_t step_a = p.a_across ? 128 : 2, step_b = p.b_across ? 128 : 2;  // 16 of k, in 16 bytes
         int s = 0, turn = 0, set = 0, set_turn = 0;
-        for (int64_t t = tile0; t < tiles && waited; t += tile_step) {
+        for (int64_t t = tile0; t < items && waited; t += tile_step) {
+            int64_t first, last;
+            item(t, first, last);
             for (int64_t k = first; k < last; ++k) {
                 waited = barrier_wait(free_ + 8 * set, set_turn ^ 1) && barrier_wait(full + 8 * s, turn);
                 if (!waited) break;
@@ -186,8 +198,9 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     } else if (warp >= 2) {  // ---- results
         const int writer = threadIdx.x - 64, quarter = warp % 4, row = quarter * 32 + lane, c0 = (warp - 2) / 4 * (SP_N / 2);
         int set = 0, set_turn = 0;
-        for (int64_t t = tile0; t < tiles; t += tile_step) {
-            const Place at = tile_place(t, p.tiles_m, p.tiles_n, TC_M, SP_N);
+        for (int64_t t = tile0; t < items; t += tile_step) {
+            int64_t first, last;
+            const Place at = item(t, first, last);
             asm volatile("bar.sync 1, %0;" ::"n"(TC_WRITERS) : "memory");  // nobody reads the last tile's bias
             for (int e = writer; e < SP_N; e += TC_WRITERS) bias_s[e] = p.bias && at.n + e < p.n ? p.bias[at.n + e] : 0.0f;
             asm volatile("bar.sync 1, %0;" ::"n"(TC_WRITERS) : "memory");
@@ -226,6 +239,20 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 break;  // one tile a cluster
             }
             const int64_t m = at.m + row;
+            if (p.segments > 1) {
+                float* part = p.parts + (t / tiles * p.m + m) * p.n + at.n + c0;
+#pragma unroll
+                for (int i = 0; i < SP_N / 2; i += 4) {
+                    if (m < p.m && p.n % 4 == 0 && at.n + c0 + i < p.n) {
+                        *reinterpret_cast<float4*>(part + i) = make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
+                    } else if (m < p.m) {
+#pragma unroll
+                        for (int j = i; j < i + 4; ++j)
+                            if (at.n + c0 + j < p.n) part[j] = sum[j];
+                    }
+                }
+                continue;
+            }
 #pragma unroll
             for (int i = 0; i < SP_N / 2; i += 4)
                 if (m < p.m && at.n + c0 + i < p.n) finish_four(p, m, at.n + c0 + i, sum + i, bias_s + c0 + i);
@@ -348,6 +375,8 @@ bool launch_product_split(const ProductArgs& q, cudaStream_t st)
     p.k = q.k;
     p.tiles_m = (q.m + TC_M - 1) / TC_M;
     p.tiles_n = (q.n + SP_N - 1) / SP_N;
+    p.segments = q.segments;
+    p.parts = q.parts;
     p.bias = static_cast<const float*>(q.bias);
     p.act = q.act;
     p.residual = static_cast<const float*>(q.residual);
@@ -359,13 +388,14 @@ bool launch_product_split(const ProductArgs& q, cudaStream_t st)
     p.vector = q.n % 4 == 0 && q.residual_row % 4 == 0 && aligned(q.out) && aligned(q.pre) && aligned(q.residual);
     const int64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + TC_K - 1) / TC_K;
     p.split = 1;
-    while (p.split < 8 && tiles * p.split * 2 <= SMS && steps >= p.split * 4) p.split *= 2;
+    while (p.segments == 1 && p.split < 8 && tiles * p.split * 2 <= SMS && steps >= p.split * 4) p.split *= 2;
     CUtensorMap map_a, map_b;
     if (!(p.a_across ? encode_planes(&map_a, q.a, p.m, p.k, q.a_row, 64) : encode_planes(&map_a, q.a, p.k, p.m, q.a_row, TC_M)) ||
         !(p.b_across ? encode_planes(&map_b, q.b, p.n, p.k, q.b_row, 64) : encode_planes(&map_b, q.b, p.k, p.n, q.b_row, SP_N)))
         return false;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split < SMS ? tiles * p.split : SMS / p.split * p.split));
+    const int64_t blocks = tiles * p.segments * p.split;
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks < SMS ? blocks : SMS / p.split * p.split));
     cfg.blockDim = dim3(TC_THREADS);
     cfg.dynamicSmemBytes = SP_SMEM;
     cfg.stream = st;

@@ -585,7 +585,7 @@ nms_status nms_relation_softmax_grad_run(const void* dprobs, const void* probs, 
  * stride of their own (input rows may coincide: a stride of 0 repeats one).
  */
 #define NMS_LAYER_MAX_WIDTH 16384
-#define NMS_LINEAR_MAX_WIDTH (1 << 20)
+#define NMS_LINEAR_MAX_WIDTH (1 << 18)
 #define NMS_ROTARY_MAX_AXES 8
 #define NMS_ROTARY_MAX_DIM 4096
 

@@ -70,7 +70,7 @@ def _backward(x, w, z, dy, act, seed=0):
 
 SIZES = [(1, 1, 1), (1, 8, 8), (3, 5, 7), (16, 64, 128), (17, 72, 200), (5, 513, 33), (130, 127, 129), (128, 128, 256),
          (300, 256, 1024), (257, 264, 520), (64, 1000, 40), (1, 4096, 1000), (2, 48, 4096), (2000, 40, 24),
-         (1000, 136, 8)]
+         (1000, 136, 8), (9000, 24, 40), (400, 600, 603)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
