@@ -84,9 +84,14 @@ bool launch_product_f32(const ProductArgs& p, cudaStream_t st);
 // Binary32, by the tensor cores: operands of three planes of 16 bits, as
 // launch_split_rows leaves them.
 bool launch_product_split(const ProductArgs& p, cudaStream_t st);
-// Rows of binary32 to planes [3][rows][to_row], to_row a multiple of 8.
-void launch_split_rows(const float* from, int64_t from_row, int64_t rows, int64_t width, void* to, int64_t to_row,
-                       cudaStream_t st);
+// Rows of binary32 and their planes [3][rows][to_row], to_row a multiple of 8.
+struct SplitRows {
+    const float* from;
+    int64_t from_row, rows, width;
+    void* to;
+    int64_t to_row;
+};
+void launch_split_rows(const SplitRows* of, int count, cudaStream_t st);  // one or two operands
 // out = sums over the parts [segments][n], of any type, in order.
 void launch_join_parts(const float* parts, int segments, int64_t n, void* out, int type, cudaStream_t st);
 // 16 bits, by the tensor cores: operands and their rows start at multiples of

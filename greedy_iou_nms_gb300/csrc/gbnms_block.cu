@@ -48,17 +48,21 @@ bool uneven(int32_t type, const void* p, int64_t row, int64_t rows, int64_t widt
 
 size_t copy_bytes(int64_t rows, int64_t width) { return round_up(2 * rows * padded(width)); }
 
+// Multiplications from which a binary32 product is worth making planes for: 300 x
+// 256 x 1024, 2^26.2, took 14.6 us by them and 16.4 on the plain units; 300 x 256 x
+// 512, 2^25.2, 14.4 and 12.5.
+constexpr int64_t SPLIT_LEAST = int64_t(1) << 26;
+
 size_t plane_bytes(int64_t rows, int64_t width) { return round_up(3 * 2 * rows * padded(width)); }
 
 // Whether a binary32 product of m x n results goes by planes to the tensor cores:
-// from 2^27 multiplications on (planes and product took 19 us of 1517 x 333 x 251,
-// 2^26.9, as much as the plain units; 21 of 1200 x 512 x 512, 2^28.2).  A weight's
-// gradient also where it is few results of many rows.
+// from SPLIT_LEAST multiplications on.  A weight's gradient also where it is few
+// results of many rows.
 bool by_planes(int32_t type, int64_t m, int64_t n, int64_t k, bool gradient)
 {
     if (type != NMS_TYPE_F32) return false;
     if (gradient && k >= 8192) return true;
-    return (gradient || m > 16) && m * n >= (int64_t(1) << 27) / k;
+    return (gradient || m > 16) && m * n >= SPLIT_LEAST / k;
 }
 
 // Stretches of k of a weight's gradient on the tensor cores: where clusters of
@@ -79,33 +83,31 @@ int gradient_segments(int32_t type, int64_t m, int64_t n, int64_t k)
 
 size_t parts_bytes(int segments, int64_t m, int64_t n) { return segments > 1 ? round_up(4 * segments * m * n) : 0; }
 
-// An operand of a product: itself, or what the tensor cores take in its place, in
-// the workspace, which moves on.
+// An operand of a product: itself, or what the tensor cores take in its place.
 struct Operand {
     const void* p;
     int64_t row, rows, width;
-    int32_t type;
     const void* planes = nullptr;
-    void ready(bool as_planes, char*& workspace, cudaStream_t st)
-    {
-        if (as_planes) {
-            if (planes) return;
-            planes = workspace;
-            launch_split_rows(static_cast<const float*>(p), row, rows, width, workspace, padded(width), st);
-            workspace += plane_bytes(rows, width);
-        } else if (uneven(type, p, row, rows, width)) {
-            launch_copy_rows(p, row, rows, width, workspace, padded(width), st);
-            p = workspace;
-            row = padded(width);
-            workspace += copy_bytes(rows, width);
-        }
-    }
 };
 
+// The product, its operands made ready in the workspace, which moves on.
 bool launch_product(ProductArgs& q, Operand& a, Operand& b, bool as_planes, char*& workspace, cudaStream_t st)
 {
-    a.ready(as_planes, workspace, st);
-    b.ready(as_planes, workspace, st);
+    SplitRows split[2];
+    int splits = 0;
+    for (Operand* o : {&a, &b}) {
+        if (as_planes && !o->planes) {
+            split[splits++] = {static_cast<const float*>(o->p), o->row, o->rows, o->width, workspace, padded(o->width)};
+            o->planes = workspace;
+            workspace += plane_bytes(o->rows, o->width);
+        } else if (uneven(q.type, o->p, o->row, o->rows, o->width)) {
+            launch_copy_rows(o->p, o->row, o->rows, o->width, workspace, padded(o->width), st);
+            o->p = workspace;
+            o->row = padded(o->width);
+            workspace += copy_bytes(o->rows, o->width);
+        }
+    }
+    if (splits) launch_split_rows(split, splits, st);
     q.a = as_planes ? a.planes : a.p;
     q.b = as_planes ? b.planes : b.p;
     q.a_row = as_planes ? padded(a.width) : a.row;
@@ -153,7 +155,7 @@ extern "C" nms_status nms_linear_run(const void* x, int64_t x_row, int32_t type,
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaGetLastError();
     char* rest = static_cast<char*>(workspace);
-    Operand a{x, x_row, rows, inner, type}, b{weight, weight_row, outer, inner, type};
+    Operand a{x, x_row, rows, inner}, b{weight, weight_row, outer, inner};
     ProductArgs p{};
     p.type = type;
     p.m = rows;
@@ -236,8 +238,8 @@ extern "C" nms_status nms_linear_grad_run(const void* dy, int64_t dy_row, const 
         a.dbias = dbias;
         launch_slope(a, sums, st);
     }
-    Operand z{copied ? workspace : dy, copied ? padded(outer) : dy_row, rows, outer, type};
-    Operand xs{x, x_row, rows, inner, type}, ws{weight, weight_row, outer, inner, type};
+    Operand z{copied ? workspace : dy, copied ? padded(outer) : dy_row, rows, outer};
+    Operand xs{x, x_row, rows, inner}, ws{weight, weight_row, outer, inner};
     ProductArgs p{};
     p.type = type;
     p.act = NMS_ACT_NONE;

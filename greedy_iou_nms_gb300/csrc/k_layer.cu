@@ -6,10 +6,10 @@ namespace gbnms {
 
 namespace {
 
-constexpr int JOIN_COLUMNS = 32, JOIN_SLOTS = 32;
+constexpr int JOIN_COLUMNS = 8, JOIN_SLOTS = 128;
 
-// A column's parts go to JOIN_SLOTS threads in turn; then a warp has a column,
-// a lane a thread's sum, and joins them in a tree.
+// A column's parts go to JOIN_SLOTS threads in turn; then a warp has a column, a
+// lane every 32nd of its threads' sums, and joins them in a tree.
 __global__ void __launch_bounds__(JOIN_COLUMNS * JOIN_SLOTS)
 column_join_kernel(const float* parts, int64_t blocks, int64_t columns, int64_t split, float* first, float* second)
 {
@@ -18,22 +18,27 @@ column_join_kernel(const float* parts, int64_t blocks, int64_t columns, int64_t 
     const int64_t e = static_cast<int64_t>(blockIdx.x) * JOIN_COLUMNS + threadIdx.x;
     LongSum s{0.0f, 0.0f};
     if (e < columns) {
-        constexpr int AHEAD = 8;
+        constexpr int AHEAD = 4;
         for (int64_t b = threadIdx.y; b < blocks; b += AHEAD * JOIN_SLOTS) {
             float v[AHEAD];
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) v[k] = b + k * JOIN_SLOTS < blocks ? parts[(b + k * JOIN_SLOTS) * columns + e] : 0.0f;
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k) s.add(v[k]);
+            for (int k = 0; k < AHEAD; ++k)
+                if (b + k * JOIN_SLOTS < blocks) s.add(v[k]);
         }
     }
     sums[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    s = sums[threadIdx.x][threadIdx.y];
+    const int warp = (threadIdx.y * JOIN_COLUMNS + threadIdx.x) / 32, lane = (threadIdx.y * JOIN_COLUMNS + threadIdx.x) % 32;
+    if (warp >= JOIN_COLUMNS) return;
+    s = sums[lane][warp];
+#pragma unroll
+    for (int k = 32; k < JOIN_SLOTS; k += 32) s.add(sums[k + lane][warp]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) s.add(LongSum{__shfl_down_sync(FULL, s.sum, o), __shfl_down_sync(FULL, s.off, o)});
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * JOIN_COLUMNS + threadIdx.y;
-    if (threadIdx.x == 0 && c < columns) {
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * JOIN_COLUMNS + warp;
+    if (lane == 0 && c < columns) {
         float* out = c < split ? first : second;
         if (out) out[c < split ? c : c - split] = s.value();
     }

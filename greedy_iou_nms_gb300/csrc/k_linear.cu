@@ -2,7 +2,7 @@
 // their epilogue, on the plain arithmetic units, and the copy of 16-bit rows
 // whose places the tensor cores' loads cannot take.
 //
-// product_kernel, for products of less than 2^27 multiplications (larger ones go
+// product_kernel, for products of less than 2^26 multiplications (larger ones go
 // to the tensor cores, k_product_split.cu): a block has a tile of 64 x 64 results,
 // its 256 threads 4 x 4 of them each.  Few tiles: the blocks of a cluster share
 // one, each a stretch of k, and add up their parts through distributed shared

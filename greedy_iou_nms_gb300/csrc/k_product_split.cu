@@ -300,19 +300,20 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
 // part is all there is.
 template <bool WIDE>
 __global__ void __launch_bounds__(256)
-split_rows_kernel(const float* from, int64_t from_row, int64_t rows, int64_t width, __nv_bfloat16* to, int64_t to_row)
+split_rows_kernel(const SplitRows first, const SplitRows second)
 {
-    const int64_t parts = to_row / 8, n = rows * parts, plane = rows * to_row;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t row = i / parts, e = (i - row * parts) * 8;
-        const float* p = from + row * from_row + e;
+    const int64_t n0 = first.rows * (first.to_row / 8), n = n0 + second.rows * (second.to_row / 8);
+    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < n; at += static_cast<int64_t>(gridDim.x) * 256) {
+        const SplitRows& s = at < n0 ? first : second;
+        const int64_t i = at < n0 ? at : at - n0, parts = s.to_row / 8, row = i / parts, e = (i - row * parts) * 8;
+        const float* p = s.from + row * s.from_row + e;
         float x[8];
         if (WIDE) {  // 8 divides the width
             const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
             x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = e + k < width ? p[k] : 0.0f;
+            for (int k = 0; k < 8; ++k) x[k] = e + k < s.width ? p[k] : 0.0f;
         }
         Pack<__nv_bfloat16, 8> h, m, l;
 #pragma unroll
@@ -324,10 +325,10 @@ split_rows_kernel(const float* from, int64_t from_row, int64_t rows, int64_t wid
             m.v[k] = __float2bfloat16_rn(rest);
             l.v[k] = __float2bfloat16_rn(rest - to_f32(m.v[k]));
         }
-        __nv_bfloat16* q = to + row * to_row + e;
+        __nv_bfloat16* q = static_cast<__nv_bfloat16*>(s.to) + row * s.to_row + e;
         *reinterpret_cast<Pack<__nv_bfloat16, 8>*>(q) = h;
-        *reinterpret_cast<Pack<__nv_bfloat16, 8>*>(q + plane) = m;
-        *reinterpret_cast<Pack<__nv_bfloat16, 8>*>(q + 2 * plane) = l;
+        *reinterpret_cast<Pack<__nv_bfloat16, 8>*>(q + s.rows * s.to_row) = m;
+        *reinterpret_cast<Pack<__nv_bfloat16, 8>*>(q + 2 * s.rows * s.to_row) = l;
     }
 }
 
@@ -344,16 +345,20 @@ bool encode_planes(CUtensorMap* map, const void* p, int64_t width, int64_t rows,
 
 }  // namespace
 
-void launch_split_rows(const float* from, int64_t from_row, int64_t rows, int64_t width, void* to, int64_t to_row,
-                       cudaStream_t st)
+void launch_split_rows(const SplitRows* of, int count, cudaStream_t st)
 {
-    const int64_t want = (rows * (to_row / 8) + 255) / 256, most = SMS * 8;
+    SplitRows second{};
+    if (count > 1) second = of[1];
+    bool wide = true;
+    int64_t n = 0;
+    for (int i = 0; i < count; ++i) {
+        wide = wide && of[i].width % 8 == 0 && of[i].from_row % 4 == 0 && reinterpret_cast<uintptr_t>(of[i].from) % 16 == 0;
+        n += of[i].rows * (of[i].to_row / 8);
+    }
+    const int64_t want = (n + 255) / 256, most = SMS * 8;
     const unsigned grid = static_cast<unsigned>(want < most ? want : most);
-    __nv_bfloat16* planes = static_cast<__nv_bfloat16*>(to);
-    if (width % 8 == 0 && from_row % 4 == 0 && reinterpret_cast<uintptr_t>(from) % 16 == 0)
-        split_rows_kernel<true><<<grid, 256, 0, st>>>(from, from_row, rows, width, planes, to_row);
-    else
-        split_rows_kernel<false><<<grid, 256, 0, st>>>(from, from_row, rows, width, planes, to_row);
+    if (wide) split_rows_kernel<true><<<grid, 256, 0, st>>>(of[0], second);
+    else split_rows_kernel<false><<<grid, 256, 0, st>>>(of[0], second);
 }
 
 bool launch_product_split(const ProductArgs& q, cudaStream_t st)

@@ -16,7 +16,7 @@ namespace {
 constexpr int SL_SLOTS = 8;
 
 template <typename T, int V>
-__global__ void __launch_bounds__(32 * SL_SLOTS, 4)
+__global__ void __launch_bounds__(32 * SL_SLOTS, 5)
 slope_kernel(const SlopeArgs s, int64_t run, float* parts)
 {
     __shared__ float sums[SL_SLOTS][32 * V];
@@ -27,34 +27,22 @@ slope_kernel(const SlopeArgs s, int64_t run, float* parts)
         const T* dy = static_cast<const T*>(s.dy) + e;
         const T* pre = static_cast<const T*>(s.pre) + e;
         T* dz = static_cast<T*>(s.dz) + e;
-        constexpr int AHEAD = 2;  // rows of a lane in flight
-        for (int64_t row = first + threadIdx.y; row < last; row += AHEAD * SL_SLOTS) {
-            Pack<T, V> g[AHEAD], z[AHEAD];
+        for (int64_t row = first + threadIdx.y; row < last; row += SL_SLOTS) {
+            const Pack<T, V> g = *reinterpret_cast<const Pack<T, V>*>(dy + row * s.dy_row);
+            Pack<T, V> z{};
+            if (s.pre) z = *reinterpret_cast<const Pack<T, V>*>(pre + row * s.width);
+            float d[V], v[V];
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                const int64_t r = row + k * SL_SLOTS;
-                if (r < last) {
-                    g[k] = *reinterpret_cast<const Pack<T, V>*>(dy + r * s.dy_row);
-                    if (s.pre) z[k] = *reinterpret_cast<const Pack<T, V>*>(pre + r * s.width);
-                }
+            for (int i = 0; i < V; ++i) {
+                d[i] = to_f32(g.v[i]);
+                v[i] = to_f32(z.v[i]);
             }
+            if (s.pre) act_slopes<T, V>(d, v, s.act);
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                const int64_t r = row + k * SL_SLOTS;
-                if (r >= last) break;
-                float d[V], v[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    d[i] = to_f32(g[k].v[i]);
-                    v[i] = s.pre ? to_f32(z[k].v[i]) : 0.0f;
-                }
-                if (s.pre) act_slopes<T, V>(d, v, s.act);
-#pragma unroll
-                for (int i = 0; i < V; ++i) sum[i] += d[i];
-                // Rounded here to the type that the products take: half a step of a factor, no more than the
-                // factors themselves came with.
-                if (s.dz) *reinterpret_cast<Pack<T, V>*>(dz + r * s.dz_row) = pack_results<T, V>(d);
-            }
+            for (int i = 0; i < V; ++i) sum[i] += d[i];
+            // Rounded here to the type that the products take: half a step of a factor, no more than the factors
+            // themselves came with.
+            if (s.dz) *reinterpret_cast<Pack<T, V>*>(dz + row * s.dz_row) = pack_results<T, V>(d);
         }
     }
     if (!parts) return;
