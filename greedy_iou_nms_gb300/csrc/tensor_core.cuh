@@ -50,13 +50,16 @@ __device__ __forceinline__ void barrier_arrive_at(uint32_t peer)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer) : "memory");
 }
 
+// Sleeps until the phase of this parity is complete, a millisecond at most; the
+// warps that wait for a tile's sums would else take issue slots and power from
+// those that feed the tensor cores.
 __device__ __forceinline__ bool barrier_done(uint32_t bar, int parity)
 {
     uint32_t done;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(done)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "r"(1000000)
         : "memory");
     return done;
 }
