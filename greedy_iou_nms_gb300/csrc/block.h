@@ -97,6 +97,20 @@ void launch_join_parts(const float* parts, int segments, int64_t n, void* out, i
 // 16 bits, by the tensor cores: operands and their rows start at multiples of
 // 16 bytes and do not overlap.
 bool launch_product_tc(const ProductArgs& p, cudaStream_t st);
+// Rows of 16-bit elements to rows `to_row` apart, a multiple of 8.
+struct CopyRows {
+    const void* from;
+    int64_t from_row, rows, width;
+    void* to;
+    int64_t to_row;
+};
+void launch_copy_rows(const CopyRows* of, int count, cudaStream_t st);  // one or two operands
+
+// out = sums over the parts [segments][n], of any type, in order.
+void launch_join_parts(const float* parts, int segments, int64_t n, void* out, int type, cudaStream_t st);
+// 16 bits, by the tensor cores: operands and their rows start at multiples of
+// 16 bytes and do not overlap.
+bool launch_product_tc(const ProductArgs& p, cudaStream_t st);
 // Rows of 16-bit elements to rows `to_row` apart.
 void launch_copy_rows(const void* from, int64_t from_row, int64_t rows, int64_t width, void* to, int64_t to_row,
                       cudaStream_t st);

@@ -94,20 +94,22 @@ struct Operand {
 bool launch_product(ProductArgs& q, Operand& a, Operand& b, bool as_planes, char*& workspace, cudaStream_t st)
 {
     SplitRows split[2];
-    int splits = 0;
+    CopyRows copy[2];
+    int splits = 0, copies = 0;
     for (Operand* o : {&a, &b}) {
         if (as_planes && !o->planes) {
             split[splits++] = {static_cast<const float*>(o->p), o->row, o->rows, o->width, workspace, padded(o->width)};
             o->planes = workspace;
             workspace += plane_bytes(o->rows, o->width);
         } else if (uneven(q.type, o->p, o->row, o->rows, o->width)) {
-            launch_copy_rows(o->p, o->row, o->rows, o->width, workspace, padded(o->width), st);
+            copy[copies++] = {o->p, o->row, o->rows, o->width, workspace, padded(o->width)};
             o->p = workspace;
             o->row = padded(o->width);
             workspace += copy_bytes(o->rows, o->width);
         }
     }
     if (splits) launch_split_rows(split, splits, st);
+    if (copies) launch_copy_rows(copy, copies, st);
     q.a = as_planes ? a.planes : a.p;
     q.b = as_planes ? b.planes : b.p;
     q.a_row = as_planes ? padded(a.width) : a.row;

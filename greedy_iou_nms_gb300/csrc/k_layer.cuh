@@ -6,7 +6,8 @@
 //   dweight = sum dy * u, dbias = sum dy over the rows.
 //
 // HBM bounds both: a row is read once and stays in the registers of a team of
-// threads (a warp up to 1024 elements, 128 threads up to 4096, 512 up to 16384)
+// threads (a warp up to 1024 elements, 128 threads up to 4096, 512 up to 8192,
+// 1024 up to 16384)
 // from its moments to its results.  The gradient's teams go through many rows
 // and keep the parameters' sums of their own columns in registers too; blocks
 // leave theirs in the workspace and one short kernel joins them in order.
@@ -69,7 +70,12 @@ __device__ __forceinline__ void load_params(float (&v)[V], const void* p, int is
         }
     } else if constexpr (sizeof(T) == 2) {
         const T* q = static_cast<const T*>(p) + e;
-        if constexpr (V == 8) {
+        if constexpr (V == 2) {
+            const uint32_t f = __ldg(reinterpret_cast<const uint32_t*>(q));
+            const Pack<T, 2> h = *reinterpret_cast<const Pack<T, 2>*>(&f);
+            v[0] = to_f32(h.v[0]);
+            v[1] = to_f32(h.v[1]);
+        } else if constexpr (V == 8) {
             const uint4 f = __ldg(reinterpret_cast<const uint4*>(q));
             const Pack<T, 8> h = *reinterpret_cast<const Pack<T, 8>*>(&f);
 #pragma unroll
@@ -346,7 +352,7 @@ inline LayerShape layer_shape(int width)
 {
     if (width <= 1024) return {32, width <= 256 ? 8 : width <= 512 ? 16 : 32};
     if (width <= 4096) return {128, width <= 2048 ? 16 : 32};
-    return {512, width <= 8192 ? 16 : 32};
+    return width <= 8192 ? LayerShape{512, 16} : LayerShape{1024, 16};
 }
 constexpr int LAYER_GRAD_THREADS = 128;  // of a block whose teams are warps
 
@@ -367,7 +373,7 @@ int64_t launch_layer_rows(const LayerArgs& a, float* parts, bool grad, cudaStrea
     if (grad) {
         constexpr int THREADS = TEAM == 32 ? LAYER_GRAD_THREADS : TEAM;
         // Registers: two sums a value, and some fifty.
-        constexpr int BLOCKS = TEAM == 512 ? 1 : VALUES == 32 ? 4 : VALUES == 16 ? 5 : 6;
+        constexpr int BLOCKS = TEAM >= 512 ? 1 : VALUES == 32 ? 4 : VALUES == 16 ? 5 : 6;
         constexpr int SMEM = LAYER_GRAD_SMEM<T, V, VALUES / V, TEAM, THREADS>;
         constexpr int FIT = SMEM * BLOCKS <= 220 * 1024 ? BLOCKS : 220 * 1024 / SMEM;
         auto kernel = layer_grad_kernel<T, V, VALUES / V, TEAM, THREADS, FIT>;
@@ -400,21 +406,25 @@ int64_t launch_layer_width(const LayerArgs& a, float* parts, bool grad, cudaStre
         if (s.values == 16) return launch_layer_rows<T, V, 128, 16>(a, parts, grad, st);
         return launch_layer_rows<T, V, 128, 32>(a, parts, grad, st);
     }
-    if (s.values == 16) return launch_layer_rows<T, V, 512, 16>(a, parts, grad, st);
-    return launch_layer_rows<T, V, 512, 32>(a, parts, grad, st);
+    if (s.team == 512) return launch_layer_rows<T, V, 512, 16>(a, parts, grad, st);
+    return launch_layer_rows<T, V, 1024, 16>(a, parts, grad, st);
 }
 
-// Accesses of 16 bytes where every row starts at a multiple of them, else of
-// one element.
+// Accesses of 16 bytes where every row starts at a multiple of them, else of two
+// elements or of one.
 template <typename T>
 int64_t launch_layer_type(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
 {
     constexpr int MOST = 16 / sizeof(T);
-    auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-    const bool wide = a.width % MOST == 0 && a.x_row % MOST == 0 && a.second_row % MOST == 0 && a.dy_row % MOST == 0 &&
-                      aligned(a.x) && aligned(a.second) && aligned(a.dy) && aligned(a.out) && aligned(a.sum) &&
-                      aligned(a.weight) && aligned(a.bias);
-    return wide ? launch_layer_width<T, MOST>(a, parts, grad, st) : launch_layer_width<T, 1>(a, parts, grad, st);
+    const uintptr_t pe = a.param_f32 ? 4 : sizeof(T);
+    auto even = [&](int v) {
+        auto starts = [&](const void* p, uintptr_t e) { return reinterpret_cast<uintptr_t>(p) % (v * e < 16 ? v * e : 16) == 0; };
+        return a.width % v == 0 && a.x_row % v == 0 && a.second_row % v == 0 && a.dy_row % v == 0 &&
+               starts(a.x, sizeof(T)) && starts(a.second, sizeof(T)) && starts(a.dy, sizeof(T)) && starts(a.out, sizeof(T)) &&
+               starts(a.sum, sizeof(T)) && starts(a.weight, pe) && starts(a.bias, pe);
+    };
+    if (even(MOST)) return launch_layer_width<T, MOST>(a, parts, grad, st);
+    return even(2) ? launch_layer_width<T, 2>(a, parts, grad, st) : launch_layer_width<T, 1>(a, parts, grad, st);
 }
 
 int64_t launch_layer_f32(const LayerArgs& a, float* parts, bool grad, cudaStream_t st);

@@ -157,18 +157,6 @@ product_kernel(const ProductArgs p, int64_t tiles_n, int split)
         at = at + 1 == PR_STAGES ? 0 : at + 1;
         ahead = ahead + 1 == PR_STAGES ? 0 : ahead + 1;
     }
-    if (split == 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t m = m0 + (i / 4) * 64 + ty * 4 + i % 4;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t n = n0 + (j / 4) * 64 + tx * 4 + j % 4;
-                if (m < p.m && n < p.n) finish(p, m, n, total[i][j]);
-            }
-        }
-        return;
-    }
     __syncthreads();  // the stages are no longer read
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -176,6 +164,15 @@ product_kernel(const ProductArgs p, int64_t tiles_n, int split)
         for (int j = 0; j < 4; j += 4)
             *reinterpret_cast<float4*>(stages + ((i / 4) * 64 + ty * 4 + i % 4) * PR_STRIDE + j * 16 + tx * 4) =
                 make_float4(total[i][j], total[i][j + 1], total[i][j + 2], total[i][j + 3]);
+    // From shared memory a warp's results are neighbours in a row.
+    if (split == 1) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < PR_TILE * PR_TILE; e += 256) {
+            const int r = e / PR_TILE, c = e % PR_TILE;
+            if (m0 + r < p.m && n0 + c < p.n) finish(p, m0 + r, n0 + c, stages[r * PR_STRIDE + c]);
+        }
+        return;
+    }
     cluster_barrier();
     const int rows = PR_TILE / split;
     for (int e = threadIdx.x; e < rows * PR_TILE; e += 256) {
@@ -314,16 +311,17 @@ join_parts_kernel(const float* parts, int segments, int64_t n, T* out)
 
 // Eight elements of a row a thread.
 __global__ void __launch_bounds__(256)
-copy_rows_kernel(const uint16_t* from, int64_t from_row, int64_t rows, int64_t width, uint16_t* to, int64_t to_row)
+copy_rows_kernel(const CopyRows first, const CopyRows second)
 {
-    const int64_t parts = (width + 7) / 8, n = rows * parts;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t row = i / parts, e = (i - row * parts) * 8;
-        const uint16_t* p = from + row * from_row + e;
+    const int64_t n0 = first.rows * (first.to_row / 8), n = n0 + second.rows * (second.to_row / 8);
+    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < n; at += static_cast<int64_t>(gridDim.x) * 256) {
+        const CopyRows& c = at < n0 ? first : second;
+        const int64_t i = at < n0 ? at : at - n0, parts = c.to_row / 8, row = i / parts, e = (i - row * parts) * 8;
+        const uint16_t* p = static_cast<const uint16_t*>(c.from) + row * c.from_row + e;
         Pack<uint16_t, 8> q;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) q.v[k] = e + k < width ? p[k] : 0;
-        *reinterpret_cast<Pack<uint16_t, 8>*>(to + row * to_row + e) = q;
+        for (int k = 0; k < 8; ++k) q.v[k] = e + k < c.width ? p[k] : 0;
+        *reinterpret_cast<Pack<uint16_t, 8>*>(static_cast<uint16_t*>(c.to) + row * c.to_row + e) = q;
     }
 }
 
@@ -408,12 +406,13 @@ void launch_join_parts(const float* parts, int segments, int64_t n, void* out, i
     else cudaLaunchKernelEx(&cfg, join_parts_kernel<__nv_bfloat16>, parts, segments, n, static_cast<__nv_bfloat16*>(out));
 }
 
-void launch_copy_rows(const void* from, int64_t from_row, int64_t rows, int64_t width, void* to, int64_t to_row,
-                      cudaStream_t st)
+void launch_copy_rows(const CopyRows* of, int count, cudaStream_t st)
 {
-    const int64_t want = (rows * ((width + 7) / 8) + 255) / 256, most = SMS * 8;
-    copy_rows_kernel<<<static_cast<unsigned>(want < most ? want : most), 256, 0, st>>>(
-        static_cast<const uint16_t*>(from), from_row, rows, width, static_cast<uint16_t*>(to), to_row);
+    CopyRows second{};
+    if (count > 1) second = of[1];
+    const int64_t n = of[0].rows * (of[0].to_row / 8) + second.rows * (second.to_row / 8);
+    const int64_t want = (n + 255) / 256, most = SMS * 8;
+    copy_rows_kernel<<<static_cast<unsigned>(want < most ? want : most), 256, 0, st>>>(of[0], second);
 }
 
 }  // namespace gbnms

@@ -24,7 +24,10 @@ namespace {
 
 constexpr int SP_N = 128, SP_PLANES = 3, SP_STAGES = 2;
 constexpr int SP_STAGE = SP_PLANES * 2 * A_BYTES;  // A's planes, then B's, of as many rows
-constexpr int SP_SMEM = 1024 + SP_STAGES * SP_STAGE;
+// A warp's 32 rows of 16 results on their way from one row a lane to 64 bytes of a
+// row for four lanes (or 16), rows SP_PATCH_ROW bytes apart.
+constexpr int SP_PATCH_ROW = 80, SP_PATCH = 32 * SP_PATCH_ROW;
+constexpr int SP_SMEM = 1024 + SP_STAGES * SP_STAGE + TC_WRITERS / 32 * SP_PATCH;
 constexpr int SP_PITCH = SP_N + 4;  // of a block's part, in shared memory
 
 struct SplitArgs {
@@ -52,35 +55,31 @@ __device__ __forceinline__ void tma_load_plane(uint32_t dst, const CUtensorMap* 
         : "memory");
 }
 
-// Four results of a row, those below n.
+__device__ __forceinline__ void finish_single(const SplitArgs& p, int64_t m, int64_t n, float sum, float bias)
+{
+    float z[1] = {sum + bias};
+    if (p.pre) p.pre[m * p.n + n] = z[0];
+    act_values<float>(z, p.act);
+    p.out[m * p.n + n] = p.residual ? z[0] + p.residual[m * p.residual_row + n] : z[0];
+}
+
+// Four results of a row, all of them there and aligned.
 __device__ __forceinline__ void finish_four(const SplitArgs& p, int64_t m, int64_t n, const float* sum, const float* bias)
 {
     const int64_t at = m * p.n + n;
     float z[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) z[i] = sum[i] + bias[i];
-    if (p.vector) {
-        if (p.pre) *reinterpret_cast<float4*>(p.pre + at) = make_float4(z[0], z[1], z[2], z[3]);
-        act_values<float>(z, p.act);
-        if (p.residual) {
-            const float4 r = *reinterpret_cast<const float4*>(p.residual + m * p.residual_row + n);
-            z[0] += r.x;
-            z[1] += r.y;
-            z[2] += r.z;
-            z[3] += r.w;
-        }
-        *reinterpret_cast<float4*>(p.out + at) = make_float4(z[0], z[1], z[2], z[3]);
-        return;
-    }
-    if (p.pre) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n + i < p.n) p.pre[at + i] = z[i];
-    }
+    if (p.pre) *reinterpret_cast<float4*>(p.pre + at) = make_float4(z[0], z[1], z[2], z[3]);
     act_values<float>(z, p.act);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (n + i < p.n) p.out[at + i] = p.residual ? z[i] + p.residual[m * p.residual_row + n + i] : z[i];
+    if (p.residual) {
+        const float4 r = *reinterpret_cast<const float4*>(p.residual + m * p.residual_row + n);
+        z[0] += r.x;
+        z[1] += r.y;
+        z[2] += r.z;
+        z[3] += r.w;
+    }
+    *reinterpret_cast<float4*>(p.out + at) = make_float4(z[0], z[1], z[2], z[3]);
 }
 
 __global__ void __launch_bounds__(TC_THREADS, 1)
@@ -253,9 +252,34 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 }
                 continue;
             }
+            char* const patch = dynamic + (ring - shared_address(dynamic)) + SP_STAGES * SP_STAGE + (warp - 2) * SP_PATCH;
 #pragma unroll
-            for (int i = 0; i < SP_N / 2; i += 4)
-                if (m < p.m && at.n + c0 + i < p.n) finish_four(p, m, at.n + c0 + i, sum + i, bias_s + c0 + i);
+            for (int c = 0; c < SP_N / 2; c += 16) {
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<float4*>(patch + lane * SP_PATCH_ROW + 4 * i) =
+                        make_float4(sum[c + i], sum[c + i + 1], sum[c + i + 2], sum[c + i + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = i * 8 + lane / 4, n = c0 + c + lane % 4 * 4;
+                    const int64_t to = at.m + quarter * 32 + r;
+                    if (p.vector && to < p.m && at.n + n < p.n)
+                        finish_four(p, to, at.n + n, reinterpret_cast<const float*>(patch + r * SP_PATCH_ROW) + lane % 4 * 4,
+                                    bias_s + n);
+                }
+                if (!p.vector) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int r = 2 * i + lane / 16, n = c0 + c + lane % 16;
+                        const int64_t to = at.m + quarter * 32 + r;
+                        if (to < p.m && at.n + n < p.n)
+                            finish_single(p, to, at.n + n, reinterpret_cast<const float*>(patch + r * SP_PATCH_ROW)[lane % 16],
+                                          bias_s[n]);
+                    }
+                }
+                __syncwarp();
+            }
         }
     }
     __syncwarp();
@@ -282,7 +306,13 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
 #pragma unroll
                         for (int i = 0; i < 4; ++i) sum[i] += v[b][i];
                     }
-                finish_four(p, at.m + r, at.n + c, sum, bias_s + c);
+                if (p.vector) {
+                    finish_four(p, at.m + r, at.n + c, sum, bias_s + c);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (at.n + c + i < p.n) finish_single(p, at.m + r, at.n + c + i, sum[i], bias_s[c + i]);
+                }
             }
         }
         __syncwarp();

@@ -63,7 +63,7 @@ slope_kernel(const SlopeArgs s, int64_t run, float* parts)
 int64_t slope_runs(int64_t rows, int64_t width)
 {
     const int64_t strips = (width + 255) / 256, full = (SMS * 8 + strips - 1) / strips;
-    const int64_t want = (rows + 4 * SL_SLOTS - 1) / (4 * SL_SLOTS), least = (rows + 256 * SL_SLOTS - 1) / (256 * SL_SLOTS);
+    const int64_t want = (rows + 8 * SL_SLOTS - 1) / (8 * SL_SLOTS), least = (rows + 256 * SL_SLOTS - 1) / (256 * SL_SLOTS);
     return want < full ? want : least > full ? (least < 65535 ? least : 65535) : full;
 }
 
@@ -71,17 +71,20 @@ template <typename T>
 void launch(const SlopeArgs& s, float* parts, cudaStream_t st)
 {
     constexpr int MOST = 16 / sizeof(T);
-    auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-    const bool wide = s.width % MOST == 0 && s.dy_row % MOST == 0 && s.dz_row % MOST == 0 && aligned(s.dy) &&
-                      aligned(s.pre) && aligned(s.dz);
+    auto even = [&](int v) {
+        auto starts = [&](const void* p) { return reinterpret_cast<uintptr_t>(p) % (v * sizeof(T)) == 0; };
+        return s.width % v == 0 && s.dy_row % v == 0 && s.dz_row % v == 0 && starts(s.dy) && starts(s.pre) && starts(s.dz);
+    };
+    const int v = even(MOST) ? MOST : even(2) ? 2 : 1;
     int64_t runs = slope_runs(s.rows, s.width);
     const int64_t run = (s.rows + runs - 1) / runs;
     runs = (s.rows + run - 1) / run;
-    const int v = wide ? MOST : 1;
+    if (runs == 1 && parts) parts = s.dbias;
     const dim3 grid(static_cast<unsigned>((s.width + 32 * v - 1) / (32 * v)), static_cast<unsigned>(runs));
-    if (wide) slope_kernel<T, MOST><<<grid, dim3(32, SL_SLOTS), 0, st>>>(s, run, parts);
+    if (v == MOST) slope_kernel<T, MOST><<<grid, dim3(32, SL_SLOTS), 0, st>>>(s, run, parts);
+    else if (v == 2) slope_kernel<T, 2><<<grid, dim3(32, SL_SLOTS), 0, st>>>(s, run, parts);
     else slope_kernel<T, 1><<<grid, dim3(32, SL_SLOTS), 0, st>>>(s, run, parts);
-    if (parts) launch_column_join(parts, runs, s.width, s.width, s.dbias, nullptr, st);
+    if (runs > 1 && parts) launch_column_join(parts, runs, s.width, s.width, s.dbias, nullptr, st);
 }
 
 }  // namespace
