@@ -62,7 +62,7 @@ bool by_planes(int32_t type, int64_t m, int64_t n, int64_t k, bool gradient)
 {
     if (type != NMS_TYPE_F32) return false;
     if (gradient && k >= 8192) return true;
-    return (gradient || m > 16) && m * n >= SPLIT_LEAST / k;
+    return (gradient || m > 16) && m * n >= (k >= 1024 ? SPLIT_LEAST / 32 : SPLIT_LEAST) / k;
 }
 
 // Stretches of k of a weight's gradient on the tensor cores: where clusters of

@@ -6,42 +6,65 @@ namespace gbnms {
 
 namespace {
 
-constexpr int JOIN_COLUMNS = 8, JOIN_SLOTS = 128;
-
-// A column's parts go to JOIN_SLOTS threads in turn; then a warp has a column, a
-// lane every 32nd of its threads' sums, and joins them in a tree.
-__global__ void __launch_bounds__(JOIN_COLUMNS * JOIN_SLOTS)
+// A column's parts go to SLOTS threads in turn; their sums are joined in order by
+// one thread, or in a tree by a warp where there are many.
+template <int COLUMNS, int SLOTS>
+__global__ void __launch_bounds__(COLUMNS * SLOTS)
 column_join_kernel(const float* parts, int64_t blocks, int64_t columns, int64_t split, float* first, float* second)
 {
-    __shared__ LongSum sums[JOIN_SLOTS][JOIN_COLUMNS + 1];
+    __shared__ LongSum sums[SLOTS][COLUMNS + 1];
     pdl_wait();  // the parts are there
-    const int64_t e = static_cast<int64_t>(blockIdx.x) * JOIN_COLUMNS + threadIdx.x;
+    const int64_t e = static_cast<int64_t>(blockIdx.x) * COLUMNS + threadIdx.x;
     LongSum s{0.0f, 0.0f};
     if (e < columns) {
         constexpr int AHEAD = 4;
-        for (int64_t b = threadIdx.y; b < blocks; b += AHEAD * JOIN_SLOTS) {
+        for (int64_t b = threadIdx.y; b < blocks; b += AHEAD * SLOTS) {
             float v[AHEAD];
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k) v[k] = b + k * JOIN_SLOTS < blocks ? parts[(b + k * JOIN_SLOTS) * columns + e] : 0.0f;
+            for (int k = 0; k < AHEAD; ++k) v[k] = b + k * SLOTS < blocks ? parts[(b + k * SLOTS) * columns + e] : 0.0f;
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k)
-                if (b + k * JOIN_SLOTS < blocks) s.add(v[k]);
+                if (b + k * SLOTS < blocks) s.add(v[k]);
         }
     }
     sums[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    const int warp = (threadIdx.y * JOIN_COLUMNS + threadIdx.x) / 32, lane = (threadIdx.y * JOIN_COLUMNS + threadIdx.x) % 32;
-    if (warp >= JOIN_COLUMNS) return;
-    s = sums[lane][warp];
+    const int thread = threadIdx.y * COLUMNS + threadIdx.x;
+    int64_t c = static_cast<int64_t>(blockIdx.x) * COLUMNS;
+    if constexpr (SLOTS > 32) {
+        const int warp = thread / 32, lane = thread % 32;
+        if (warp >= COLUMNS) return;
+        c += warp;
+        s = sums[lane][warp];
 #pragma unroll
-    for (int k = 32; k < JOIN_SLOTS; k += 32) s.add(sums[k + lane][warp]);
+        for (int k = 32; k < SLOTS; k += 32) s.add(sums[k + lane][warp]);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) s.add(LongSum{__shfl_down_sync(FULL, s.sum, o), __shfl_down_sync(FULL, s.off, o)});
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * JOIN_COLUMNS + warp;
-    if (lane == 0 && c < columns) {
+        for (int o = 16; o; o >>= 1) s.add(LongSum{__shfl_down_sync(FULL, s.sum, o), __shfl_down_sync(FULL, s.off, o)});
+        if (lane) return;
+    } else {
+        if (thread >= COLUMNS) return;
+        c += thread;
+        s = sums[0][thread];
+#pragma unroll
+        for (int k = 1; k < SLOTS; ++k) s.add(sums[k][thread]);
+    }
+    if (c < columns) {
         float* out = c < split ? first : second;
         if (out) out[c < split ? c : c - split] = s.value();
     }
+}
+
+template <int COLUMNS, int SLOTS>
+void launch_join(const float* parts, int64_t blocks, int64_t columns, int64_t split, float* first, float* second, cudaStream_t st)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>((columns + COLUMNS - 1) / COLUMNS));
+    cfg.blockDim = dim3(COLUMNS, SLOTS);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, column_join_kernel<COLUMNS, SLOTS>, parts, blocks, columns, split, first, second);
 }
 
 int64_t launch_rows(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
@@ -72,14 +95,9 @@ void launch_layer_grad(const LayerArgs& a, void* workspace, cudaStream_t st)
 void launch_column_join(const float* parts, int64_t blocks, int64_t columns, int64_t split, float* first, float* second,
                         cudaStream_t st)
 {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>((columns + JOIN_COLUMNS - 1) / JOIN_COLUMNS));
-    cfg.blockDim = dim3(JOIN_COLUMNS, JOIN_SLOTS);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1] = {pdl_attribute()};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, column_join_kernel, parts, blocks, columns, split, first, second);
+    if (blocks <= 32) launch_join<64, 4>(parts, blocks, columns, split, first, second, st);
+    else if (blocks <= 256) launch_join<32, 16>(parts, blocks, columns, split, first, second, st);
+    else launch_join<8, 128>(parts, blocks, columns, split, first, second, st);
 }
 
 }  // namespace gbnms

@@ -184,7 +184,8 @@ __device__ __forceinline__ void copy_ahead(void* to, const void* from)
 
 // Whether a block's rows and weights fit: else rows are read where they are needed.
 template <typename T, int V, int NV, int TEAM, int THREADS>
-constexpr bool LAYER_AHEAD = sizeof(T) * V >= 4 && 2 * 3 * THREADS * NV * V * sizeof(T) + TEAM * NV * V * 4 <= 112 * 1024;
+constexpr bool LAYER_AHEAD =
+    sizeof(T) * V >= 4 && 2 * 3 * THREADS * NV * V * sizeof(T) + TEAM * NV * V * 4 <= (TEAM >= 512 ? 220 : 112) * 1024;
 
 template <typename T, int V, int NV, int TEAM, int THREADS>
 constexpr int LAYER_GRAD_SMEM = TEAM * NV * V * 4 + (TEAM < THREADS ? TEAM * NV * V * 8 : 0) +
@@ -231,8 +232,14 @@ layer_grad_kernel(const LayerArgs a, float* parts)
         mean = a.mean[row];
         rstd = a.rstd[row];
     }
-    for (int e = threadIdx.x; e < SPAN; e += THREADS)
-        weights[e] = e < a.width ? (a.weight ? load_param<T>(a.weight, a.param_f32, e) : 1.0f) : 0.0f;
+    for (int e = threadIdx.x * V; e < SPAN; e += THREADS * V) {
+        float w[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[i] = 0.0f;
+        if (e < a.width) load_params<T, V>(w, a.weight, a.param_f32, e, 1.0f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) weights[e + i] = w[i];
+    }
     __syncthreads();
     const float share = 1.0f / static_cast<float>(a.width);
     float dw[NV][V], db[NV][V];

@@ -84,13 +84,23 @@ __device__ __forceinline__ float cluster_sum(const float* at, int split)
     return sum;
 }
 
-__device__ __forceinline__ void finish(const ProductArgs& p, int64_t m, int64_t n, float sum)
+// What a result gets added.
+struct Addends {
+    float bias, residual;
+    __device__ __forceinline__ Addends(const ProductArgs& p, int64_t m, int64_t n)
+        : bias(p.bias ? __ldg(static_cast<const float*>(p.bias) + n) : 0.0f),
+          residual(p.residual ? static_cast<const float*>(p.residual)[m * p.residual_row + n] : 0.0f)
+    {
+    }
+    __device__ __forceinline__ Addends() {}
+};
+
+__device__ __forceinline__ void finish(const ProductArgs& p, int64_t m, int64_t n, float sum, const Addends& add)
 {
-    float z[1] = {sum + (p.bias ? static_cast<const float*>(p.bias)[n] : 0.0f)};
+    float z[1] = {sum + add.bias};
     if (p.pre) static_cast<float*>(p.pre)[m * p.n + n] = z[0];
     act_values<float>(z, p.act);
-    if (p.residual) z[0] += static_cast<const float*>(p.residual)[m * p.residual_row + n];
-    static_cast<float*>(p.out)[m * p.n + n] = z[0];
+    static_cast<float*>(p.out)[m * p.n + n] = z[0] + add.residual;
 }
 
 template <bool A_ACROSS, bool B_ACROSS>
@@ -167,9 +177,18 @@ product_kernel(const ProductArgs p, int64_t tiles_n, int split)
     // From shared memory a warp's results are neighbours in a row.
     if (split == 1) {
         __syncthreads();
-        for (int e = threadIdx.x; e < PR_TILE * PR_TILE; e += 256) {
-            const int r = e / PR_TILE, c = e % PR_TILE;
-            if (m0 + r < p.m && n0 + c < p.n) finish(p, m0 + r, n0 + c, stages[r * PR_STRIDE + c]);
+        for (int e0 = threadIdx.x; e0 < PR_TILE * PR_TILE; e0 += 8 * 256) {
+            Addends add[8];  // the residual may be what is written: read before the first of these results
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = (e0 + i * 256) / PR_TILE, c = (e0 + i * 256) % PR_TILE;
+                if (m0 + r < p.m && n0 + c < p.n) add[i] = Addends(p, m0 + r, n0 + c);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = (e0 + i * 256) / PR_TILE, c = (e0 + i * 256) % PR_TILE;
+                if (m0 + r < p.m && n0 + c < p.n) finish(p, m0 + r, n0 + c, stages[r * PR_STRIDE + c], add[i]);
+            }
         }
         return;
     }
@@ -177,7 +196,8 @@ product_kernel(const ProductArgs p, int64_t tiles_n, int split)
     const int rows = PR_TILE / split;
     for (int e = threadIdx.x; e < rows * PR_TILE; e += 256) {
         const int r = static_cast<int>(rank) * rows + e / PR_TILE, c = e % PR_TILE;
-        if (m0 + r < p.m && n0 + c < p.n) finish(p, m0 + r, n0 + c, cluster_sum(stages + r * PR_STRIDE + c, split));
+        if (m0 + r < p.m && n0 + c < p.n) 
+            finish(p, m0 + r, n0 + c, cluster_sum(stages + r * PR_STRIDE + c, split), Addends(p, m0 + r, n0 + c));
     }
     __syncwarp();
     cluster_barrier();  // no block leaves while another reads its part
@@ -222,7 +242,8 @@ few_along_kernel(const ProductArgs p)
         const int r = e / 8, c = e % 8, first = c / 4 * 4, at = c % 4 * R + r;
         const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 + c;
         if (r < p.m && n < p.n)
-            finish(p, r, n, ((parts[first][at] + parts[first + 1][at]) + parts[first + 2][at]) + parts[first + 3][at]);
+            finish(p, r, n, ((parts[first][at] + parts[first + 1][at]) + parts[first + 2][at]) + parts[first + 3][at],
+                   Addends(p, r, n));
     }
 }
 
@@ -258,7 +279,7 @@ few_across_kernel(const ProductArgs p, int split)
         __syncthreads();  // nobody reads the last chunk's part of A
         for (int e = threadIdx.x; e < CHUNK * R; e += 256) {
             const int r = e / CHUNK, c = e % CHUNK;
-            xs[c * R + r] = r < p.m && k0 + c < last ? x[r * p.a_row + k0 + c] : 0.0f;
+            xs[c * R + r] = r < p.m && k0 + c < last ? __ldg(x + r * p.a_row + k0 + c) : 0.0f;
         }
         __syncthreads();
 #pragma unroll
@@ -284,7 +305,8 @@ few_across_kernel(const ProductArgs p, int split)
     cluster_barrier();
     for (int e = static_cast<int>(rank) * 256 + threadIdx.x; e < R * COLUMNS; e += 256 * split) {
         const int r = e / COLUMNS, c = e % COLUMNS;
-        if (r < p.m && group * COLUMNS + c < p.n) finish(p, r, group * COLUMNS + c, cluster_sum(sums + e, split));
+        const int64_t at = group * COLUMNS + c;
+        if (r < p.m && at < p.n) finish(p, r, at, cluster_sum(sums + e, split), Addends(p, r, at));
     }
     __syncwarp();
     cluster_barrier();  // no block leaves while another reads its sums

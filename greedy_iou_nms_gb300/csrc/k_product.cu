@@ -53,14 +53,30 @@ struct TcArgs {
 
 // One result.
 template <typename T>
-__device__ __forceinline__ void finish_one(const TcArgs& p, int64_t m, int64_t n, float sum, float bias)
+__device__ __forceinline__ void finish_one(const TcArgs& p, int64_t m, int64_t n, float sum, float bias, T residual)
 {
     float z[1] = {sum + bias};
     const int64_t at = m * p.out_m + n * p.out_n;
     if (p.pre) static_cast<T*>(p.pre)[at] = from_f32<T>(z[0]);
     act_values<T>(z, p.act);
-    if (p.residual) z[0] += to_f32(static_cast<const T*>(p.residual)[m * p.residual_m + n * p.residual_n]);
+    if (p.residual) z[0] += to_f32(residual);
     static_cast<T*>(p.out)[at] = from_f32<T>(z[0]);
+}
+
+// N results of one m; the residual, which may be what is written, is read before
+// the first of them.
+template <typename T, int N>
+__device__ __forceinline__ void finish_some(const TcArgs& p, int64_t m, int64_t n, const float (&sum)[N], const float* bias, int bias_step)
+{
+    T r[N];
+    if (p.residual) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (n + i < p.n) r[i] = static_cast<const T*>(p.residual)[m * p.residual_m + (n + i) * p.residual_n];
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (n + i < p.n) finish_one<T>(p, m, n + i, sum[i], bias[i * bias_step], r[i]);
 }
 
 // A warp's 32 rows of 32 results, on their way between one row a lane, as
@@ -105,8 +121,12 @@ struct Patch {
                                                    int lane) const
     {
         T* const patch = reinterpret_cast<T*>(own - lane * TC_PITCH) + lane;
-        if (lane < columns)
-            for (int r = 0; r < 32 && row + r < m; ++r) patch[r * (TC_PITCH / 2)] = at[(row + r) * stride + lane];
+        T v[32];  // all on their way before the first is put down
+#pragma unroll
+        for (int r = 0; r < 32; ++r)
+            if (lane < columns && row + r < m) v[r] = at[(row + r) * stride + lane];
+#pragma unroll
+        for (int r = 0; r < 32; ++r) patch[r * (TC_PITCH / 2)] = v[r];
         __syncwarp();
     }
     __device__ __forceinline__ void put_columns(const float (&z)[32], T* at, int64_t stride, int64_t row, int64_t m,
@@ -332,11 +352,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                         }
                     }
                 } else if constexpr (SWAP) {
-                    if (m < p.m) {
-#pragma unroll
-                        for (int i = 0; i < CHUNK; ++i)
-                            if (at.n + c + i < p.n) finish_one<T>(p, m, at.n + c + i, v[i], bias_s[set][row]);
-                    }
+                    if (m < p.m) finish_some<T>(p, m, at.n + c, v, &bias_s[set][row], 0);
                 } else {
                     const bool whole = p.vector && at.n + c + CHUNK <= p.n;
                     const int64_t columns = p.n - (at.n + c);
@@ -403,9 +419,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll
                         for (int i = 0; i < 4; ++i) sum[i] += v[b][i];
                     }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (at.n + c + i < p.n) finish_one<T>(p, at.m + r, at.n + c + i, sum[i], bias_s[0][SWAP ? r : c + i]);
+                finish_some<T>(p, at.m + r, at.n + c, sum, &bias_s[0][SWAP ? r : c], SWAP ? 0 : 1);
             }
         }
         __syncwarp();

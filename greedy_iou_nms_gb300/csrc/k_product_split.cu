@@ -55,31 +55,96 @@ __device__ __forceinline__ void tma_load_plane(uint32_t dst, const CUtensorMap* 
         : "memory");
 }
 
-__device__ __forceinline__ void finish_single(const SplitArgs& p, int64_t m, int64_t n, float sum, float bias)
-{
-    float z[1] = {sum + bias};
-    if (p.pre) p.pre[m * p.n + n] = z[0];
-    act_values<float>(z, p.act);
-    p.out[m * p.n + n] = p.residual ? z[0] + p.residual[m * p.residual_row + n] : z[0];
-}
-
-// Four results of a row, all of them there and aligned.
+// Four results of a row, of which those below n are there.
 __device__ __forceinline__ void finish_four(const SplitArgs& p, int64_t m, int64_t n, const float* sum, const float* bias)
 {
     const int64_t at = m * p.n + n;
-    float z[4];
+    float z[4], r[4] = {};
+    if (p.residual) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < p.n) r[i] = p.residual[m * p.residual_row + n + i];
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) z[i] = sum[i] + bias[i];
-    if (p.pre) *reinterpret_cast<float4*>(p.pre + at) = make_float4(z[0], z[1], z[2], z[3]);
-    act_values<float>(z, p.act);
-    if (p.residual) {
-        const float4 r = *reinterpret_cast<const float4*>(p.residual + m * p.residual_row + n);
-        z[0] += r.x;
-        z[1] += r.y;
-        z[2] += r.z;
-        z[3] += r.w;
+    if (p.pre) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < p.n) p.pre[at + i] = z[i];
     }
-    *reinterpret_cast<float4*>(p.out + at) = make_float4(z[0], z[1], z[2], z[3]);
+    act_values<float>(z, p.act);
+    if (p.vector) {
+        *reinterpret_cast<float4*>(p.out + at) = make_float4(z[0] + r[0], z[1] + r[1], z[2] + r[2], z[3] + r[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < p.n) p.out[at + i] = z[i] + r[i];
+    }
+}
+
+// A warp's 32 rows of 16 values, one row a lane, to memory from (row, n) on.
+__device__ __forceinline__ void patch_out(const SplitArgs& p, char* patch, const float (&v)[16], float* to, int64_t row, int64_t n,
+                                          int lane)
+{
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<float4*>(patch + lane * SP_PATCH_ROW + 4 * i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    __syncwarp();
+    if (p.vector) {
+        const int64_t at = n + lane % 4 * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + lane / 4;
+            if (row + r < p.m && at < p.n)
+                *reinterpret_cast<float4*>(to + (row + r) * p.n + at) =
+                    *reinterpret_cast<const float4*>(patch + r * SP_PATCH_ROW + lane % 4 * 16);
+        }
+    } else {
+        const int64_t at = n + lane % 16;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int r = 2 * i + lane / 16;
+            if (row + r < p.m && at < p.n)
+                to[(row + r) * p.n + at] = *reinterpret_cast<const float*>(patch + r * SP_PATCH_ROW + lane % 16 * 4);
+        }
+    }
+    __syncwarp();
+}
+
+// v += the residual's rows.
+__device__ __forceinline__ void patch_add(const SplitArgs& p, char* patch, float (&v)[16], int64_t row, int64_t n, int lane)
+{
+    if (p.vector) {
+        const int64_t at = n + lane % 4 * 4;
+        float4 r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t from = row + i * 8 + lane / 4;
+            if (from < p.m && at < p.n) r[i] = *reinterpret_cast<const float4*>(p.residual + from * p.residual_row + at);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(patch + (i * 8 + lane / 4) * SP_PATCH_ROW + lane % 4 * 16) = r[i];
+    } else {
+        const int64_t at = n + lane % 16;
+        float r[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int64_t from = row + 2 * i + lane / 16;
+            if (from < p.m && at < p.n) r[i] = p.residual[from * p.residual_row + at];
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) *reinterpret_cast<float*>(patch + (2 * i + lane / 16) * SP_PATCH_ROW + lane % 16 * 4) = r[i];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(patch + lane * SP_PATCH_ROW + 4 * i);
+        v[i] += q.x;
+        v[i + 1] += q.y;
+        v[i + 2] += q.z;
+        v[i + 3] += q.w;
+    }
+    __syncwarp();
 }
 
 __global__ void __launch_bounds__(TC_THREADS, 1)
@@ -253,32 +318,17 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 continue;
             }
             char* const patch = dynamic + (ring - shared_address(dynamic)) + SP_STAGES * SP_STAGE + (warp - 2) * SP_PATCH;
+            const int64_t row0 = at.m + quarter * 32;
 #pragma unroll
             for (int c = 0; c < SP_N / 2; c += 16) {
+                const int64_t n = at.n + c0 + c;
+                float v[16];
 #pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                    *reinterpret_cast<float4*>(patch + lane * SP_PATCH_ROW + 4 * i) =
-                        make_float4(sum[c + i], sum[c + i + 1], sum[c + i + 2], sum[c + i + 3]);
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = i * 8 + lane / 4, n = c0 + c + lane % 4 * 4;
-                    const int64_t to = at.m + quarter * 32 + r;
-                    if (p.vector && to < p.m && at.n + n < p.n)
-                        finish_four(p, to, at.n + n, reinterpret_cast<const float*>(patch + r * SP_PATCH_ROW) + lane % 4 * 4,
-                                    bias_s + n);
-                }
-                if (!p.vector) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int r = 2 * i + lane / 16, n = c0 + c + lane % 16;
-                        const int64_t to = at.m + quarter * 32 + r;
-                        if (to < p.m && at.n + n < p.n)
-                            finish_single(p, to, at.n + n, reinterpret_cast<const float*>(patch + r * SP_PATCH_ROW)[lane % 16],
-                                          bias_s[n]);
-                    }
-                }
-                __syncwarp();
+                for (int i = 0; i < 16; ++i) v[i] = sum[c + i] + bias_s[c0 + c + i];
+                if (p.pre) patch_out(p, patch, v, p.pre, row0, n, lane);
+                act_values<float>(v, p.act);
+                if (p.residual) patch_add(p, patch, v, row0, n, lane);
+                patch_out(p, patch, v, p.out, row0, n, lane);
             }
         }
     }
@@ -306,13 +356,7 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
 #pragma unroll
                         for (int i = 0; i < 4; ++i) sum[i] += v[b][i];
                     }
-                if (p.vector) {
-                    finish_four(p, at.m + r, at.n + c, sum, bias_s + c);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (at.n + c + i < p.n) finish_single(p, at.m + r, at.n + c + i, sum[i], bias_s[c + i]);
-                }
+                finish_four(p, at.m + r, at.n + c, sum, bias_s + c);
             }
         }
         __syncwarp();

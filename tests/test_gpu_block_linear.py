@@ -70,7 +70,7 @@ def _backward(x, w, z, dy, act, seed=0):
 
 SIZES = [(1, 1, 1), (1, 8, 8), (3, 5, 7), (16, 64, 128), (17, 72, 200), (5, 513, 33), (130, 127, 129), (128, 128, 256),
          (300, 256, 1024), (257, 264, 520), (64, 1000, 40), (1, 4096, 1000), (2, 48, 4096), (2000, 40, 24),
-         (1000, 136, 8), (9000, 24, 40), (400, 600, 603)]
+         (1000, 136, 8), (9000, 24, 40), (400, 600, 603), (70, 1030, 64), (20, 24, 1100)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
@@ -173,6 +173,21 @@ def test_only_what_is_needed():
             assert torch.equal(got, ref) if wanted else got is None
 
 
+def test_far_apart_sizes():
+    """Binary32 operands whose parts differ by many powers of two, and whose results nearly cancel."""
+    r = torch.Generator().manual_seed(12)
+    for rows, inner, outer in ((40, 64, 48), (300, 520, 520)):
+        x = torch.randn(rows, inner, generator=r) * 2.0 ** torch.randint(-30, 30, (rows, 1), generator=r)
+        w = torch.randn(outer, inner, generator=r) * 2.0 ** torch.randint(-30, 30, (outer, 1), generator=r)
+        x[:, 1::2] = -x[:, ::2] * (1 + 2.0 ** -12 * torch.randn(rows, inner // 2, generator=r))
+        w[:, 1::2] = w[:, ::2]
+        y = g.linear_act(x.cuda(), w.cuda())
+        _check(y, x.double() @ w.double().T, R.product_bound(x, w.T, torch.float32))
+    x = torch.full((300, 520), 3.4e38)  # rounds to an infinity in 8 bits
+    y = g.linear_act(x.cuda(), torch.eye(520).mul(0.5).cuda())
+    assert torch.equal(y.cpu(), x / 2)
+
+
 def test_no_rows():
     for kind in ("f32", "f16"):
         x, w, dy = (torch.empty(s, dtype=R.TYPES[kind], device="cuda") for s in ((2, 0, 24), (40, 24), (2, 0, 40)))
@@ -183,8 +198,8 @@ def test_no_rows():
 
 def test_not_finite_stays_in_its_rows():
     for kind in ("f32", "bf16"):
-        for rows in (3, 200):
-            x, w, b, dy = (v.cuda() for v in _inputs(rows, 72, 136, kind, 9))
+        for rows, outer in ((3, 136), (200, 136), (600, 1600)):  # the last one: binary32 on the tensor cores too
+            x, w, b, dy = (v.cuda() for v in _inputs(rows, 72, outer, kind, 9))
             x[1, 5] = float("nan")
             x[rows - 1, 71] = float("inf")
             y = g.linear_act(x, w, b, act="silu")
