@@ -592,7 +592,14 @@ nms_status nms_relation_softmax_grad_run(const void* dprobs, const void* probs, 
 /*
  * Linear layer:
  *   z = x weight^T + bias,  y = act(z) + residual,
- * x [rows][inner], weight [outer][inner], y [rows][outer]; sums in binary32.
+ * x [rows][inner], weight [outer][inner], y [rows][outer].  Sums are held in
+ * binary32.  Operands of 16 bits go to the tensor cores, which cut what 16
+ * products add below 2^-25 of the sum so far: a sum of k products is off by up to
+ * k 2^-29 of its largest part.  Larger products of binary32 operands go there
+ * as three bfloat16 parts of each element, 64 products at a time, and are as near
+ * as a binary32 sum; elements below 2^-100 keep fewer than 24 bits there, and an
+ * infinity may leave a NaN.  (Rows of NaN or infinities leave no number in their
+ * own results and none in others'.)
  *   x, weight  device, `type`, rows x_row and weight_row elements apart.
  *   bias       device [outer] of bias_type (NMS_TYPE_F32, or `type`), or NULL.
  *   act        NMS_ACT_*.
