@@ -80,7 +80,13 @@ void launch_layer_norm(const LayerArgs& a, cudaStream_t st) { launch_rows(a, nul
 
 size_t layer_grad_workspace_bytes(int64_t rows, int width)
 {
-    return static_cast<size_t>(layer_grad_blocks(rows, width)) * 2 * width * sizeof(float);
+    int64_t most = 0;
+    for (const bool single : {false, true}) {
+        const LayerShape s = layer_shape(width, single);
+        const int64_t blocks = layer_grad_blocks(rows, s.team, layer_grad_resident(s.team, s.values));
+        if (blocks > most) most = blocks;
+    }
+    return static_cast<size_t>(most) * 2 * width * sizeof(float);
 }
 
 void launch_layer_grad(const LayerArgs& a, void* workspace, cudaStream_t st)

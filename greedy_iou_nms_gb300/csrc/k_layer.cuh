@@ -191,6 +191,8 @@ template <typename T, int V, int NV, int TEAM, int THREADS>
 constexpr int LAYER_GRAD_SMEM = TEAM * NV * V * 4 + (TEAM < THREADS ? TEAM * NV * V * 8 : 0) +
                                 (LAYER_AHEAD<T, V, NV, TEAM, THREADS> ? 2 * 3 * THREADS * NV * V * static_cast<int>(sizeof(T)) : 0);
 
+constexpr int LAYER_GRAD_THREADS = 128;  // of a block whose teams are warps
+
 // Each block's sums of dy * u and of dy go to parts[block][2][width].
 template <typename T, int V, int NV, int TEAM, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS)
@@ -351,25 +353,32 @@ layer_grad_kernel(const LayerArgs a, float* parts)
     }
 }
 
-// Threads of a team and the values that one holds.
+// Threads of a team and the values that one holds.  Rows that move element by
+// element have more threads with fewer values, each a register and an access of
+// its own (40000 x 999 bf16, gradient: ELEMENTWISE_NOTE).
 struct LayerShape {
     int team, values;
 };
-inline LayerShape layer_shape(int width)
+inline LayerShape layer_shape(int width, bool single)
 {
+    if (width > 4096) return width <= 8192 ? LayerShape{512, 16} : LayerShape{1024, 16};
+    if (single) return width <= 256 ? LayerShape{32, 8} : width <= 1024 ? LayerShape{128, 8} : LayerShape{512, 8};
     if (width <= 1024) return {32, width <= 256 ? 8 : width <= 512 ? 16 : 32};
-    if (width <= 4096) return {128, width <= 2048 ? 16 : 32};
-    return width <= 8192 ? LayerShape{512, 16} : LayerShape{1024, 16};
+    return {128, width <= 2048 ? 16 : 32};
 }
-constexpr int LAYER_GRAD_THREADS = 128;  // of a block whose teams are warps
 
-// Blocks of the gradient at most: all that the SMs hold, and more where a
-// team's sums would run over more than 256 rows.
-inline int64_t layer_grad_blocks(int64_t rows, int width)
+// Blocks of the gradient that an SM holds by their registers: two sums a value,
+// and some fifty.
+constexpr int layer_grad_resident(int team, int values)
 {
-    const LayerShape s = layer_shape(width);
-    const int64_t teams = s.team == 32 ? LAYER_GRAD_THREADS / 32 : 1;
-    const int64_t want = (rows + teams - 1) / teams, full = SMS * (s.team == 32 ? 6 : s.team == 128 ? 4 : 1);
+    return team == 1024 ? 1 : team == 512 ? (values == 8 ? 2 : 1) : values == 32 ? 4 : values == 16 ? 5 : team == 32 ? 6 : 8;
+}
+
+// Blocks of the gradient: one wave of `resident`, and more where a team's sums
+// would run over more than 256 rows.
+inline int64_t layer_grad_blocks(int64_t rows, int team, int resident)
+{
+    const int64_t teams = team == 32 ? LAYER_GRAD_THREADS / 32 : 1, want = (rows + teams - 1) / teams, full = SMS * resident;
     const int64_t least = (rows + 256 * teams - 1) / (256 * teams);
     return want < full ? want : least > full ? least : full;
 }
@@ -378,17 +387,12 @@ template <typename T, int V, int TEAM, int VALUES>
 int64_t launch_layer_rows(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
 {
     if (grad) {
-        constexpr int THREADS = TEAM == 32 ? LAYER_GRAD_THREADS : TEAM;
-        // Registers: two sums a value, and some fifty.
-        constexpr int BLOCKS = TEAM >= 512 ? 1 : VALUES == 32 ? 4 : VALUES == 16 ? 5 : 6;
+        constexpr int THREADS = TEAM == 32 ? LAYER_GRAD_THREADS : TEAM, BLOCKS = layer_grad_resident(TEAM, VALUES);
         constexpr int SMEM = LAYER_GRAD_SMEM<T, V, VALUES / V, TEAM, THREADS>;
         constexpr int FIT = SMEM * BLOCKS <= 220 * 1024 ? BLOCKS : 220 * 1024 / SMEM;
         auto kernel = layer_grad_kernel<T, V, VALUES / V, TEAM, THREADS, FIT>;
         if (SMEM > 40 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-        const int64_t most = layer_grad_blocks(a.rows, a.width), full = SMS * FIT;
-        // A team's rows: no more than 256, or one wave of blocks.
-        const int64_t teams = THREADS / TEAM, least = (a.rows + 256 * teams - 1) / (256 * teams);
-        const int64_t grid = most < full ? most : least > full ? least : full;
+        const int64_t grid = layer_grad_blocks(a.rows, TEAM, FIT);
         kernel<<<static_cast<unsigned>(grid), THREADS, SMEM, st>>>(a, parts);
         return grid;
     }
@@ -403,15 +407,21 @@ int64_t launch_layer_rows(const LayerArgs& a, float* parts, bool grad, cudaStrea
 template <typename T, int V>
 int64_t launch_layer_width(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
 {
-    const LayerShape s = layer_shape(a.width);
-    if (s.team == 32) {
-        if (s.values == 8) return launch_layer_rows<T, V, 32, 8>(a, parts, grad, st);
-        if (s.values == 16) return launch_layer_rows<T, V, 32, 16>(a, parts, grad, st);
-        return launch_layer_rows<T, V, 32, 32>(a, parts, grad, st);
-    }
-    if (s.team == 128) {
-        if (s.values == 16) return launch_layer_rows<T, V, 128, 16>(a, parts, grad, st);
-        return launch_layer_rows<T, V, 128, 32>(a, parts, grad, st);
+    const LayerShape s = layer_shape(a.width, V == 1);
+    if constexpr (V == 1) {
+        if (s.team == 32) return launch_layer_rows<T, V, 32, 8>(a, parts, grad, st);
+        if (s.team == 128) return launch_layer_rows<T, V, 128, 8>(a, parts, grad, st);
+        if (s.values == 8) return launch_layer_rows<T, V, 512, 8>(a, parts, grad, st);
+    } else {
+        if (s.team == 32) {
+            if (s.values == 8) return launch_layer_rows<T, V, 32, 8>(a, parts, grad, st);
+            if (s.values == 16) return launch_layer_rows<T, V, 32, 16>(a, parts, grad, st);
+            return launch_layer_rows<T, V, 32, 32>(a, parts, grad, st);
+        }
+        if (s.team == 128) {
+            if (s.values == 16) return launch_layer_rows<T, V, 128, 16>(a, parts, grad, st);
+            return launch_layer_rows<T, V, 128, 32>(a, parts, grad, st);
+        }
     }
     if (s.team == 512) return launch_layer_rows<T, V, 512, 16>(a, parts, grad, st);
     return launch_layer_rows<T, V, 1024, 16>(a, parts, grad, st);

@@ -563,7 +563,7 @@ bool launch_product_tc(const ProductArgs& q, cudaStream_t st)
     const int64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + TC_K - 1) / TC_K;
     p.split = 1;
     // Joining the parts costs a few microseconds: 300 x 256 x 1024, four stages a tile, took 7.7 us by two blocks a tile
-    // and 5.5 by one; 16 x 1024 x 4096, sixteen stages, 6.2 by four and 7.9 by one.
+    // and 5.5 by one; 16 x 1024 x 4096, sixteen stages, 6.2 by four and 6.6 by two.
     while (!pair && p.segments == 1 && p.split < 8 && tiles * p.split * 2 <= SMS && steps >= p.split * 8) p.split *= 2;
     CUtensorMap map_a, map_b;
     const bool known =

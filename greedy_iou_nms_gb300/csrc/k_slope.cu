@@ -15,9 +15,15 @@ namespace {
 
 constexpr int SL_SLOTS = 8;
 
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// joined: the runs of a strip are a cluster, whose first block adds up their sums.
 template <typename T, int V>
 __global__ void __launch_bounds__(32 * SL_SLOTS, 5)
-slope_kernel(const SlopeArgs s, int64_t run, float* parts)
+slope_kernel(const SlopeArgs s, int64_t run, float* parts, bool joined)
 {
     __shared__ float sums[SL_SLOTS][32 * V];
     const int64_t e = (static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x) * V;
@@ -49,13 +55,35 @@ slope_kernel(const SlopeArgs s, int64_t run, float* parts)
 #pragma unroll
     for (int i = 0; i < V; ++i) sums[threadIdx.y][i * 32 + threadIdx.x] = sum[i];
     __syncthreads();
-    if (threadIdx.y == 0 && e < s.width) {
+    if (threadIdx.y == 0) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             for (int k = 1; k < SL_SLOTS; ++k) sum[i] += sums[k][i * 32 + threadIdx.x];
-            parts[blockIdx.y * s.width + e + i] = sum[i];
+            if (gridDim.y == 1 || !joined) {
+                if (e < s.width) parts[blockIdx.y * s.width + e + i] = sum[i];
+            } else {
+                sums[0][i * 32 + threadIdx.x] = sum[i];
+            }
         }
     }
+    if (gridDim.y == 1 || !joined) return;
+    cluster_barrier();
+    if (blockIdx.y == 0 && threadIdx.y == 0 && e < s.width) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t own = static_cast<uint32_t>(__cvta_generic_to_shared(&sums[0][i * 32 + threadIdx.x]));
+            for (unsigned k = 1; k < gridDim.y; ++k) {
+                uint32_t peer;
+                float v;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(own), "r"(k));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer));
+                sum[i] += v;
+            }
+            s.dbias[e + i] = sum[i];
+        }
+    }
+    __syncwarp();
+    cluster_barrier();  // no block leaves while the first reads its sums
 }
 
 // Runs of rows: as many blocks as fill the SMs, and a warp's sums over 256
@@ -80,11 +108,22 @@ void launch(const SlopeArgs& s, float* parts, cudaStream_t st)
     const int64_t run = (s.rows + runs - 1) / runs;
     runs = (s.rows + run - 1) / run;
     if (runs == 1 && parts) parts = s.dbias;
-    const dim3 grid(static_cast<unsigned>((s.width + 32 * v - 1) / (32 * v)), static_cast<unsigned>(runs));
-    if (v == MOST) slope_kernel<T, MOST><<<grid, dim3(32, SL_SLOTS), 0, st>>>(s, run, parts);
-    else if (v == 2) slope_kernel<T, 2><<<grid, dim3(32, SL_SLOTS), 0, st>>>(s, run, parts);
-    else slope_kernel<T, 1><<<grid, dim3(32, SL_SLOTS), 0, st>>>(s, run, parts);
-    if (runs > 1 && parts) launch_column_join(parts, runs, s.width, s.width, s.dbias, nullptr, st);
+    const bool joined = parts && runs > 1 && runs <= 8;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>((s.width + 32 * v - 1) / (32 * v)), static_cast<unsigned>(runs));
+    cfg.blockDim = dim3(32, SL_SLOTS);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1]{};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = attr[0].val.clusterDim.z = 1;
+    attr[0].val.clusterDim.y = joined ? static_cast<unsigned>(runs) : 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto go = [&](auto kernel) { cudaLaunchKernelEx(&cfg, kernel, s, run, parts, joined); };
+    if (v == MOST) go(slope_kernel<T, MOST>);
+    else if (v == 2) go(slope_kernel<T, 2>);
+    else go(slope_kernel<T, 1>);
+    if (runs > 1 && parts && !joined) launch_column_join(parts, runs, s.width, s.width, s.dbias, nullptr, st);
 }
 
 }  // namespace
