@@ -6,11 +6,13 @@
 //   dweight = sum dy * u, dbias = sum dy over the rows.
 //
 // HBM bounds both: a row is read once and stays in the registers of a team of
-// threads (a warp up to 1024 elements, 128 threads up to 4096, 512 up to 8192,
-// 1024 up to 16384)
-// from its moments to its results.  The gradient's teams go through many rows
-// and keep the parameters' sums of their own columns in registers too; blocks
-// leave theirs in the workspace and one short kernel joins them in order.
+// threads (8 up to 64 elements, 16 up to 128, a warp up to 1024, 128 threads up
+// to 4096, 512 up to 8192, 1024 up to 16384) from its moments to its results.
+// The gradient's teams go through many rows and keep the parameters' sums of
+// their own columns in registers too; blocks leave theirs in the workspace and
+// one short kernel joins them in order.  102400 x 1024 bf16: 140 us with residual
+// and statistics, 131 the gradient (6.0 and 6.4 of 6.8 TB/s); a warp a row for 50
+// elements took 39 us for the gradient of 100000, four rows a warp 20.
 #pragma once
 
 #include "block.h"
@@ -19,13 +21,14 @@
 
 namespace gbnms {
 
-// Two sums over a team of TEAM threads; with more than a warp, TEAM is the
-// block and `shared` holds two values a warp (two sets, used in turn).
+// Two sums over a team of TEAM threads, all of whose warp's lanes take part; with
+// more than a warp, TEAM is the block and `shared` holds two values a warp (two
+// sets, used in turn).
 template <int TEAM>
 __device__ __forceinline__ void team_sums(float& a, float& b, float (*shared)[2])
 {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
+    for (int o = (TEAM < 32 ? TEAM : 32) / 2; o; o >>= 1) {
         a += __shfl_xor_sync(FULL, a, o);
         b += __shfl_xor_sync(FULL, b, o);
     }
@@ -92,11 +95,13 @@ template <typename T, int V, int NV, int TEAM, int THREADS>
 __global__ void __launch_bounds__(THREADS)
 layer_kernel(const LayerArgs a)
 {
-    static_assert(TEAM == 32 || TEAM == THREADS, "a team is a warp or the block");
+    static_assert(TEAM <= 32 || TEAM == THREADS, "a team lies in a warp or is the block");
     __shared__ float shared[2][THREADS / 32][2];
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (THREADS / TEAM) + threadIdx.x / TEAM;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * (THREADS / TEAM) + threadIdx.x / TEAM;
     const int t = threadIdx.x % TEAM;
-    if (row >= a.rows) return;  // a whole team, and with TEAM == THREADS no block
+    if (TEAM == 32 && row >= a.rows) return;
+    const bool here = row < a.rows;  // teams that share a warp go on together, the last ones with the last row again
+    if (!here) row = a.rows - 1;
     const T* x = static_cast<const T*>(a.x) + row * a.x_row;
     Pack<T, V> q[NV];
 #pragma unroll
@@ -120,7 +125,7 @@ layer_kernel(const LayerArgs a)
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = to_f32(q[k].v[i]) + to_f32(p[k].v[i]);
             q[k] = pack_results<T, V>(v);
-            if (e < a.width) *reinterpret_cast<Pack<T, V>*>(sum + e) = q[k];
+            if (here && e < a.width) *reinterpret_cast<Pack<T, V>*>(sum + e) = q[k];
         }
     }
     const float share = 1.0f / static_cast<float>(a.width);
@@ -152,7 +157,7 @@ layer_kernel(const LayerArgs a)
     if (off * off < 0x1p-42f * squares) off = 0.0f;
     const float variance = fmaf(-off, off, squares);  // a NaN stays one
     const float rstd = 1.0f / sqrtf((variance < 0.0f ? 0.0f : variance) + a.eps);
-    if (t == 0) {
+    if (here && t == 0) {
         if (a.mean) a.mean[row] = mean + off;
         if (a.rstd) a.rstd[row] = rstd;
     }
@@ -160,7 +165,7 @@ layer_kernel(const LayerArgs a)
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int e = (k * TEAM + t) * V;
-        if (e < a.width) {
+        if (here && e < a.width) {
             float w[V], b[V], v[V];
             load_params<T, V>(w, a.weight, a.param_f32, e, 1.0f);
             load_params<T, V>(b, a.bias, a.param_f32, e, 0.0f);
@@ -206,7 +211,7 @@ template <typename T, int V, int NV, int TEAM, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS)
 layer_grad_kernel(const LayerArgs a, float* parts)
 {
-    static_assert(TEAM == 32 || TEAM == THREADS, "a team is a warp or the block");
+    static_assert(TEAM <= 32 || TEAM == THREADS, "a team lies in a warp or is the block");
     using Vec = Pack<T, V>;
     constexpr int AHEAD = LAYER_AHEAD<T, V, NV, TEAM, THREADS>;
     constexpr int TEAMS = THREADS / TEAM, SPAN = TEAM * NV * V;
@@ -218,6 +223,8 @@ layer_grad_kernel(const LayerArgs a, float* parts)
     const int t = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
     const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
     int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + team;
+    // Teams that share a warp go on together, by the row of its first one; rows that are not there count as nothing.
+    const int behind = TEAM < 32 ? team % (32 / TEAM) : 0;
     auto fetch = [&](int64_t r, int set) {
         const T* x = static_cast<const T*>(a.x) + r * a.x_row;
         const T* dy = static_cast<const T*>(a.dy) + r * a.dy_row;
@@ -237,7 +244,7 @@ layer_grad_kernel(const LayerArgs a, float* parts)
     if constexpr (AHEAD > 0) {
         if (row < a.rows) fetch(row, 0);
     }
-    float mean = 0.0f, rstd = 0.0f;
+    float mean = 0.0f, rstd = 0.0f;  // 0 where there is no row, so that 0 * u is 0
     if (row < a.rows) {
         mean = a.mean[row];
         rstd = a.rstd[row];
@@ -258,14 +265,14 @@ layer_grad_kernel(const LayerArgs a, float* parts)
 #pragma unroll
         for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.0f;
     const Vec none{};
-    for (int set = 0; row < a.rows; row += step, set ^= 1) {
+    for (int set = 0; row - behind < a.rows; row += step, set ^= 1) {
         const float m = mean, r = rstd;
+        const bool there = TEAM >= 32 || row < a.rows;
         Vec q[AHEAD ? 1 : NV], g[AHEAD ? 1 : NV];
         const Vec* here = rows + set * AHEAD * NV * THREADS + threadIdx.x;
-        if (row + step < a.rows) {
-            mean = a.mean[row + step];
-            rstd = a.rstd[row + step];
-        }
+        const bool next = row + step < a.rows;
+        mean = next ? a.mean[row + step] : 0.0f;
+        rstd = next ? a.rstd[row + step] : 0.0f;
         if constexpr (AHEAD > 0) {
             if (row + step < a.rows) {
                 fetch(row + step, set ^ 1);
@@ -273,21 +280,22 @@ layer_grad_kernel(const LayerArgs a, float* parts)
             } else {
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
             }
+            __syncwarp();
         } else {
             const T* x = static_cast<const T*>(a.x) + row * a.x_row;
             const T* dy = static_cast<const T*>(a.dy) + row * a.dy_row;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int e = (k * TEAM + t) * V;
-                q[k] = e < a.width ? *reinterpret_cast<const Vec*>(x + e) : none;
-                g[k] = e < a.width ? *reinterpret_cast<const Vec*>(dy + e) : none;
+                q[k] = there && e < a.width ? *reinterpret_cast<const Vec*>(x + e) : none;
+                g[k] = there && e < a.width ? *reinterpret_cast<const Vec*>(dy + e) : none;
             }
         }
         float first = 0.0f, along = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int e = (k * TEAM + t) * V;
-            const bool in = e < a.width;
+            const bool in = there && e < a.width;
             const Vec xk = AHEAD ? (in ? here[k * THREADS] : none) : q[AHEAD ? 0 : k];
             const Vec gk = AHEAD ? (in ? here[(NV + k) * THREADS] : none) : g[AHEAD ? 0 : k];
             const Pack<float, V> w = *reinterpret_cast<const Pack<float, V>*>(weights + e);
@@ -308,7 +316,7 @@ layer_grad_kernel(const LayerArgs a, float* parts)
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int e = (k * TEAM + t) * V;
-            if (e < a.width) {
+            if (there && e < a.width) {
                 const Vec xk = AHEAD ? here[k * THREADS] : q[AHEAD ? 0 : k], gk = AHEAD ? here[(NV + k) * THREADS] : g[AHEAD ? 0 : k];
                 const Pack<float, V> w = *reinterpret_cast<const Pack<float, V>*>(weights + e);
                 float v[V];
@@ -329,9 +337,18 @@ layer_grad_kernel(const LayerArgs a, float* parts)
     if (!parts) return;
     float* part = parts + static_cast<int64_t>(blockIdx.x) * 2 * a.width;
     if constexpr (TEAMS > 1) {
-        // The block's teams one after another: a fixed order.
-        for (int now = 0; now < TEAMS; ++now) {
-            if (team == now) {
+        // The teams of a warp in a tree, the block's warps one after another: a fixed order.
+#pragma unroll
+        for (int o = TEAM; o < 32; o <<= 1)
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    dw[k][i] += __shfl_xor_sync(FULL, dw[k][i], o);
+                    db[k][i] += __shfl_xor_sync(FULL, db[k][i], o);
+                }
+        for (int now = 0; now < THREADS / 32; ++now) {
+            if (threadIdx.x / 32 == now && threadIdx.x % 32 < TEAM) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -370,6 +387,7 @@ struct LayerShape {
 inline LayerShape layer_shape(int width, bool single)
 {
     if (width > 4096) return width <= 8192 ? LayerShape{512, 16} : LayerShape{1024, 16};
+    if (width <= 128) return {width <= 64 ? 8 : 16, 8};
     if (single) return width <= 256 ? LayerShape{32, 8} : width <= 1024 ? LayerShape{128, 8} : LayerShape{512, 8};
     if (width <= 1024) return {32, width <= 256 ? 8 : width <= 512 ? 16 : 32};
     return {128, width <= 2048 ? 16 : 32};
@@ -379,14 +397,14 @@ inline LayerShape layer_shape(int width, bool single)
 // and some fifty.
 constexpr int layer_grad_resident(int team, int values)
 {
-    return team == 1024 ? 1 : team == 512 ? (values == 8 ? 2 : 1) : values == 32 ? 4 : values == 16 ? 5 : team == 32 ? 6 : 8;
+    return team == 1024 ? 1 : team == 512 ? (values == 8 ? 2 : 1) : values == 32 ? 4 : values == 16 ? 5 : team <= 32 ? 6 : 8;
 }
 
 // Blocks of the gradient: one wave of `resident`, and more where a team's sums
 // would run over more than 256 rows.
 inline int64_t layer_grad_blocks(int64_t rows, int team, int resident)
 {
-    const int64_t teams = team == 32 ? LAYER_GRAD_THREADS / 32 : 1, want = (rows + teams - 1) / teams, full = SMS * resident;
+    const int64_t teams = team <= 32 ? LAYER_GRAD_THREADS / team : 1, want = (rows + teams - 1) / teams, full = SMS * resident;
     const int64_t least = (rows + 256 * teams - 1) / (256 * teams);
     return want < full ? want : least > full ? least : full;
 }
@@ -395,7 +413,7 @@ template <typename T, int V, int TEAM, int VALUES>
 int64_t launch_layer_rows(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
 {
     if (grad) {
-        constexpr int THREADS = TEAM == 32 ? LAYER_GRAD_THREADS : TEAM, BLOCKS = layer_grad_resident(TEAM, VALUES);
+        constexpr int THREADS = TEAM <= 32 ? LAYER_GRAD_THREADS : TEAM, BLOCKS = layer_grad_resident(TEAM, VALUES);
         constexpr int SMEM = LAYER_GRAD_SMEM<T, V, VALUES / V, TEAM, THREADS>;
         constexpr int FIT = SMEM * BLOCKS <= 220 * 1024 ? BLOCKS : 220 * 1024 / SMEM;
         auto kernel = layer_grad_kernel<T, V, VALUES / V, TEAM, THREADS, FIT>;
@@ -404,7 +422,7 @@ int64_t launch_layer_rows(const LayerArgs& a, float* parts, bool grad, cudaStrea
         kernel<<<static_cast<unsigned>(grid), THREADS, SMEM, st>>>(a, parts);
         return grid;
     }
-    constexpr int THREADS = TEAM == 32 ? 256 : TEAM;
+    constexpr int THREADS = TEAM <= 32 ? 256 : TEAM;
     const int64_t teams = THREADS / TEAM;
     const unsigned grid = static_cast<unsigned>((a.rows + teams - 1) / teams);
     layer_kernel<T, V, VALUES / V, TEAM, THREADS><<<grid, THREADS, 0, st>>>(a);
@@ -416,6 +434,8 @@ template <typename T, int V>
 int64_t launch_layer_width(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
 {
     const LayerShape s = layer_shape(a.width, V == 1);
+    if (s.team == 8) return launch_layer_rows<T, V, 8, 8>(a, parts, grad, st);
+    if (s.team == 16) return launch_layer_rows<T, V, 16, 8>(a, parts, grad, st);
     if constexpr (V == 1) {
         if (s.team == 32) return launch_layer_rows<T, V, 32, 8>(a, parts, grad, st);
         if (s.team == 128) return launch_layer_rows<T, V, 128, 8>(a, parts, grad, st);

@@ -50,7 +50,7 @@ def _check_forward(x, w, b, more, eps=1e-5):
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("rows,width", [(1, 1), (1, 8), (3, 7), (5, 33), (300, 256), (17, 264), (9, 512), (4, 1000),
                                         (4, 1024), (3, 1025), (3, 2048), (2, 2056), (2, 4096), (2, 4104), (2, 8192),
-                                        (1, 16383), (2, 16384), (3, 50), (2, 8986)])
+                                        (1, 16383), (2, 16384), (3, 50), (2, 8986), (1003, 8), (37, 64), (66, 63), (33, 10), (35, 65), (21, 128)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_forward(rows, width, kind, residual):
     x, w, b, more, _ = _inputs(rows, width, kind, residual, rows + width)
@@ -59,7 +59,7 @@ def test_forward(rows, width, kind, residual):
 
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("rows,width", [(1, 8), (3, 7), (5, 33), (301, 256), (700, 264), (2000, 12), (4, 1000),
-                                        (1300, 1024), (3, 1025), (2, 2056), (700, 4096), (2, 4104), (2, 16384), (300, 50), (5, 8186), (5, 8986), (3, 12345)])
+                                        (1300, 1024), (3, 1025), (2, 2056), (700, 4096), (2, 4104), (2, 16384), (300, 50), (5, 8186), (5, 8986), (3, 12345), (20003, 8), (37, 64), (66, 63), (33, 10), (1, 64), (35, 65), (21, 128), (9999, 100)])
 @pytest.mark.parametrize("more", [False, True])
 def test_gradient(rows, width, kind, more):
     x, w, _, dsum, dy = _inputs(rows, width, kind, more, rows * width)
