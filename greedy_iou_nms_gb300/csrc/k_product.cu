@@ -15,10 +15,9 @@
 // of which has its own 128 rows of A and half of B's in shared memory.  A block
 // alone moves 96 KB there for 512 cycles of multiplying (a stage of 48 KB in, and
 // out), 192 bytes a cycle of the 128 that shared memory has; a block of a pair 64
-// KB.  16384 x 4096 x 4096 bf16 without activation: 286 us (1.92 PFLOP/s, what
-// torch.matmul reaches on the same card within 6%; back to back, where the power
-// limit sets the clock, 338 us both); with gelu and residual 326, fp16 back to
-// back 380.
+// KB.  16384 x 4096 x 4096: bf16 without activation 286 us, 1.92 PFLOP/s, within
+// 6% of torch's own product on the same card; fp16 with gelu and residual 328, and
+// 380 back to back, where the power limit sets the clock (338 without either).
 //
 // Few rows of A (a step of serving): A and B change places, so that the long
 // side fills the 128 lanes and BN is 16 to 64.  Few tiles: the blocks of a

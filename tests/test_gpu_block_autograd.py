@@ -26,7 +26,8 @@ def _leaves(*tensors):
 def _near(got, ref, steps=1e-5):
     """Within 1e-5 of the largest entry: some tens of roundings of sums whose
     terms are no larger than a few times it."""
-    assert float((got.cpu().double() - ref).abs().max()) <= steps * float(ref.abs().max())
+    got, ref = got.detach().cpu().double(), ref.detach()
+    assert float((got - ref).abs().max()) <= steps * float(ref.abs().max())
 
 
 def test_linear_act():
