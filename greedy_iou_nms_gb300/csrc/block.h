@@ -31,6 +31,7 @@ struct LayerArgs {
     float* rstd;
     float* dweight;  // gradient only; may be NULL
     float* dbias;
+    bool once;  // the operands are more than L2 keeps (set by the launcher)
 };
 void launch_layer_norm(const LayerArgs& a, cudaStream_t st);
 size_t layer_grad_workspace_bytes(int64_t rows, int width);
@@ -52,6 +53,7 @@ struct RotaryArgs {
     int halves, inverse;
     void* y;
     int64_t y_batch, y_token, y_head;
+    bool once;  // the vectors are more than L2 keeps (set by the launcher)
 };
 void launch_rotary(const RotaryArgs& a, cudaStream_t st);
 

@@ -67,8 +67,10 @@ void launch_join(const float* parts, int64_t blocks, int64_t columns, int64_t sp
     cudaLaunchKernelEx(&cfg, column_join_kernel<COLUMNS, SLOTS>, parts, blocks, columns, split, first, second);
 }
 
-int64_t launch_rows(const LayerArgs& a, float* parts, bool grad, cudaStream_t st)
+int64_t launch_rows(const LayerArgs& args, float* parts, bool grad, cudaStream_t st)
 {
+    LayerArgs a = args;
+    a.once = beyond_l2((grad ? 3 : 2) * (a.type == NMS_TYPE_F32 ? 4 : 2) * a.rows * a.width);
     if (a.type == NMS_TYPE_F32) return launch_layer_f32(a, parts, grad, st);
     if (a.type == NMS_TYPE_F16) return launch_layer_f16(a, parts, grad, st);
     return launch_layer_bf16(a, parts, grad, st);

@@ -10,14 +10,16 @@
 // to 4096, 512 up to 8192, 1024 up to 16384) from its moments to its results.
 // The gradient's teams go through many rows and keep the parameters' sums of
 // their own columns in registers too; blocks leave theirs in the workspace and
-// one short kernel joins them in order.  102400 x 1024 bf16: 140 us with residual
-// and statistics, 131 the gradient (6.0 and 6.4 of 6.8 TB/s); a warp a row for 50
-// elements took 39 us for the gradient of 100000, four rows a warp 20.
+// one short kernel joins them in order.  102400 x 1024 bf16: 124 us with residual
+// and statistics (141 without the streaming accesses of once.cuh), 131 the
+// gradient: 6.8 and 6.4 of 6.8 TB/s.  A warp a row for 50 elements took 39 us for
+// the gradient of 100000, four rows a warp 20.
 #pragma once
 
 #include "block.h"
 #include "head.cuh"
 #include "internal.h"
+#include "once.cuh"
 
 namespace gbnms {
 
@@ -102,12 +104,13 @@ layer_kernel(const LayerArgs a)
     if (TEAM == 32 && row >= a.rows) return;
     const bool here = row < a.rows;  // teams that share a warp go on together, the last ones with the last row again
     if (!here) row = a.rows - 1;
+    const uint64_t policy = once_policy(a.once);
     const T* x = static_cast<const T*>(a.x) + row * a.x_row;
     Pack<T, V> q[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int e = (k * TEAM + t) * V;
-        if (e < a.width) q[k] = *reinterpret_cast<const Pack<T, V>*>(x + e);
+        if (e < a.width) q[k] = load_once(reinterpret_cast<const Pack<T, V>*>(x + e), policy);
     }
     if (a.second) {
         const T* r = static_cast<const T*>(a.second) + row * a.second_row;
@@ -116,7 +119,7 @@ layer_kernel(const LayerArgs a)
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int e = (k * TEAM + t) * V;
-            if (e < a.width) p[k] = *reinterpret_cast<const Pack<T, V>*>(r + e);
+            if (e < a.width) p[k] = load_once(reinterpret_cast<const Pack<T, V>*>(r + e), policy);
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -125,7 +128,7 @@ layer_kernel(const LayerArgs a)
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = to_f32(q[k].v[i]) + to_f32(p[k].v[i]);
             q[k] = pack_results<T, V>(v);
-            if (here && e < a.width) *reinterpret_cast<Pack<T, V>*>(sum + e) = q[k];
+            if (here && e < a.width) store_once(reinterpret_cast<Pack<T, V>*>(sum + e), q[k], policy);
         }
     }
     const float share = 1.0f / static_cast<float>(a.width);
@@ -171,7 +174,7 @@ layer_kernel(const LayerArgs a)
             load_params<T, V>(b, a.bias, a.param_f32, e, 0.0f);
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = fmaf(((to_f32(q[k].v[i]) - mean) - off) * rstd, w[i], b[i]);
-            *reinterpret_cast<Pack<T, V>*>(y + e) = pack_results<T, V>(v);
+            store_once(reinterpret_cast<Pack<T, V>*>(y + e), pack_results<T, V>(v), policy);
         }
     }
 }
@@ -220,6 +223,7 @@ layer_grad_kernel(const LayerArgs a, float* parts)
     float* weights = reinterpret_cast<float*>(dynamic);   // [SPAN], 0 behind the width
     float* columns = weights + SPAN;                      // [2][SPAN] where teams are warps
     Vec* rows = reinterpret_cast<Vec*>(columns + (TEAMS > 1 ? 2 * SPAN : 0));  // [2][AHEAD][NV][THREADS]
+    const uint64_t policy = once_policy(a.once);
     const int t = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
     const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
     int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + team;
@@ -330,7 +334,7 @@ layer_grad_kernel(const LayerArgs a, float* parts)
 #pragma unroll
                     for (int i = 0; i < V; ++i) v[i] += to_f32(p.v[i]);
                 }
-                *reinterpret_cast<Vec*>(dx + e) = pack_results<T, V>(v);
+                store_once(reinterpret_cast<Vec*>(dx + e), pack_results<T, V>(v), policy);
             }
         }
     }

@@ -15,6 +15,7 @@
 #include "block.h"
 #include "head.cuh"
 #include "internal.h"
+#include "once.cuh"
 
 namespace gbnms {
 
@@ -108,6 +109,7 @@ rotary_kernel(const RotaryArgs a, const RotaryPlan plan)
     __syncthreads();
     // A thread has one item, or every so many items, of each of its tokens, so that its place in a vector is worked
     // out once: `slots` threads a token.
+    const uint64_t policy = once_policy(a.once);
     const int slot = threadIdx.x % plan.slots, first = threadIdx.x / plan.slots, step = RO_THREADS / plan.slots;
     if (first >= step) return;
     for (int64_t item = slot; item < plan.each; item += plan.slots) {
@@ -125,8 +127,8 @@ rotary_kernel(const RotaryArgs a, const RotaryPlan plan)
             for (int b = 0; b < BATCH; ++b)
                 if (at + b * step < run) {
                     const T* from = x + places[at + b * step][0];
-                    p[b] = *reinterpret_cast<const Vec*>(from);
-                    if (turned) q[b] = *reinterpret_cast<const Vec*>(from + apart);
+                    p[b] = load_once(reinterpret_cast<const Vec*>(from), policy);
+                    if (turned) q[b] = load_once(reinterpret_cast<const Vec*>(from + apart), policy);
                 }
 #pragma unroll
             for (int b = 0; b < BATCH; ++b) {
@@ -169,8 +171,8 @@ rotary_kernel(const RotaryArgs a, const RotaryPlan plan)
                         v[i + 1] = fmaf(d1, g.x, d0 * g.y);
                     }
                 }
-                *reinterpret_cast<Vec*>(to) = pack_results<T, VP>(u);
-                *reinterpret_cast<Vec*>(to + apart) = pack_results<T, VP>(v);
+                store_once(reinterpret_cast<Vec*>(to), pack_results<T, VP>(u), policy);
+                store_once(reinterpret_cast<Vec*>(to + apart), pack_results<T, VP>(v), policy);
             }
         }
     }
@@ -205,8 +207,10 @@ void launch(const RotaryArgs& a, cudaStream_t st)
 
 }  // namespace
 
-void launch_rotary(const RotaryArgs& a, cudaStream_t st)
+void launch_rotary(const RotaryArgs& args, cudaStream_t st)
 {
+    RotaryArgs a = args;
+    a.once = beyond_l2(2 * (a.type == NMS_TYPE_F32 ? 4 : 2) * a.batch * a.tokens * a.heads * a.dim);
     if (a.type == NMS_TYPE_F32) launch<float>(a, st);
     else if (a.type == NMS_TYPE_F16) launch<__half>(a, st);
     else launch<__nv_bfloat16>(a, st);

@@ -8,6 +8,7 @@
 #include "block.h"
 #include "head.cuh"
 #include "internal.h"
+#include "once.cuh"
 
 namespace gbnms {
 
@@ -29,14 +30,15 @@ slope_kernel(const SlopeArgs s, int64_t run, float* parts, bool joined)
     const int64_t e = (static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x) * V;
     const int64_t first = blockIdx.y * run, last = min(s.rows, first + run);
     float sum[V] = {};
+    const uint64_t once = once_policy(s.dz != nullptr);  // the products read dz in place of dy: L2 is for that
     if (e < s.width) {
         const T* dy = static_cast<const T*>(s.dy) + e;
         const T* pre = static_cast<const T*>(s.pre) + e;
         T* dz = static_cast<T*>(s.dz) + e;
         for (int64_t row = first + threadIdx.y; row < last; row += SL_SLOTS) {
-            const Pack<T, V> g = *reinterpret_cast<const Pack<T, V>*>(dy + row * s.dy_row);
+            const Pack<T, V> g = load_once(reinterpret_cast<const Pack<T, V>*>(dy + row * s.dy_row), once);
             Pack<T, V> z{};
-            if (s.pre) z = *reinterpret_cast<const Pack<T, V>*>(pre + row * s.width);
+            if (s.pre) z = load_once(reinterpret_cast<const Pack<T, V>*>(pre + row * s.width), once);
             float d[V], v[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
