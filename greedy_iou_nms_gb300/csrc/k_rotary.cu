@@ -11,7 +11,8 @@
 // of a token: a block has a run of tokens, makes their table in shared memory
 // and then goes through the tokens' vectors in the order in which they lie.  48
 // warps an SM with one access pair each in flight hide more than 32 with two (79
-// us for 91) or 24 with four.
+// us for 91 at 4 x 25600 x 16 x 64 bf16) or 24 with four; with the table no larger
+// than its run and streaming accesses 72, 5.8 TB/s.
 #include "block.h"
 #include "head.cuh"
 #include "internal.h"
