@@ -128,6 +128,7 @@ struct SlopeArgs {
     int act;
     void* dz;
     int64_t dz_row;
+    void* planes;  // binary32: dz as planes [3][rows][dz_row] in place of dz
     float* dbias;
 };
 size_t slope_workspace_bytes(int64_t rows, int64_t width);

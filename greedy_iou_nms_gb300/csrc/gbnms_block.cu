@@ -56,13 +56,18 @@ constexpr int64_t SPLIT_LEAST = int64_t(1) << 26;
 size_t plane_bytes(int64_t rows, int64_t width) { return round_up(3 * 2 * rows * padded(width)); }
 
 // Whether a binary32 product of m x n results goes by planes to the tensor cores:
-// from SPLIT_LEAST multiplications on.  A weight's gradient also where it is few
-// results of many rows.
+// from SPLIT_LEAST multiplications on; from a thirty-second of them where k is long,
+// so that there are few results (70 x 64 of k = 2816: 16.8 us by planes, 24.5 on the
+// plain units; 43 x 192 of 3776: 18.7 and 30.8).  A weight's gradient also where it
+// is few results of many rows (64 x 64 of 100000: 54 us and 592), but of up to 32
+// rows not: a tile has 128, and x need be read once only (10 x 3624 of 14309: 57 us
+// by few_across_kernel, 178 by planes; 32 x 3500 of 18000: 161 and 214).
 bool by_planes(int32_t type, int64_t m, int64_t n, int64_t k, bool gradient)
 {
     if (type != NMS_TYPE_F32) return false;
+    if (m <= (gradient ? 32 : 16)) return false;
     if (gradient && k >= 8192) return true;
-    return (gradient || m > 16) && m * n >= (k >= 1024 ? SPLIT_LEAST / 32 : SPLIT_LEAST) / k;
+    return m * n >= (k >= 1024 ? SPLIT_LEAST / 32 : SPLIT_LEAST) / k;
 }
 
 // Stretches of k of a weight's gradient on the tensor cores: where clusters of
@@ -70,6 +75,11 @@ bool by_planes(int32_t type, int64_t m, int64_t n, int64_t k, bool gradient)
 // than 2^18 of k (see k_product_split.cu on what those lose).
 int gradient_segments(int32_t type, int64_t m, int64_t n, int64_t k)
 {
+    if (type == NMS_TYPE_F32 && m <= 32) {  // blocks of few_across_kernel: two an SM
+        const int64_t columns = m <= 16 ? 128 : 64, fill = 2 * SMS / ((n + columns - 1) / columns), most = k / 1024, want = fill < most ? fill : most;
+        const int64_t least = (k + (1 << 16) - 1) >> 16;  // a thread's chain: 2^13 products
+        return static_cast<int>(want > least ? want : least);
+    }
     if (type == NMS_TYPE_F32 && !by_planes(type, m, n, k, true)) return 1;
     const int64_t width = type == NMS_TYPE_F32 ? 128 : 64, tiles = ((m + 127) / 128) * ((n + width - 1) / width);
     int64_t segments = type == NMS_TYPE_F32 ? 1 : (k + (1 << 18) - 1) >> 18;
@@ -225,8 +235,17 @@ extern "C" nms_status nms_linear_grad_run(const void* dy, int64_t dy_row, const 
     char* rest = static_cast<char*>(workspace) + round_up(e * rows * padded(outer));
     void* sums = rest;
     rest += round_up(slope_workspace_bytes(rows, outer));
-    const bool products = dx || dweight, copied = products && (act != NMS_ACT_NONE || dy_uneven);
-    if (copied || dbias) {
+    const bool dx_planes = by_planes(type, rows, inner, outer, false), dw_planes = by_planes(type, outer, inner, rows, true);
+    const bool products = dx || dweight, changed = products && (act != NMS_ACT_NONE || dy_uneven);
+    // What reads dz for its sums or slopes makes its planes on the way, where nothing else takes it.
+    const bool planes = products && (!dx || dx_planes) && (!dweight || dw_planes) && (changed || dbias);
+    const bool copied = changed && !planes;
+    Operand z{copied ? workspace : dy, copied ? padded(outer) : dy_row, rows, outer};
+    if (planes) {
+        z.planes = rest;
+        rest += plane_bytes(rows, outer);
+    }
+    if (copied || planes || dbias) {
         SlopeArgs a{};
         a.dy = dy;
         a.dy_row = dy_row;
@@ -237,10 +256,10 @@ extern "C" nms_status nms_linear_grad_run(const void* dy, int64_t dy_row, const 
         a.act = act;
         a.dz = copied ? workspace : nullptr;
         a.dz_row = padded(outer);
+        a.planes = const_cast<void*>(z.planes);
         a.dbias = dbias;
         launch_slope(a, sums, st);
     }
-    Operand z{copied ? workspace : dy, copied ? padded(outer) : dy_row, rows, outer};
     Operand xs{x, x_row, rows, inner}, ws{weight, weight_row, outer, inner};
     ProductArgs p{};
     p.type = type;
@@ -253,7 +272,7 @@ extern "C" nms_status nms_linear_grad_run(const void* dy, int64_t dy_row, const 
         p.m = rows;
         p.k = outer;
         p.out = dx;
-        if (!launch_product(p, z, ws, by_planes(type, rows, inner, outer, false), rest, st)) return NMS_ERR_CUDA;
+        if (!launch_product(p, z, ws, dx_planes, rest, st)) return NMS_ERR_CUDA;
     }
     if (dweight) {
         p.a_across = 1;
@@ -265,8 +284,13 @@ extern "C" nms_status nms_linear_grad_run(const void* dy, int64_t dy_row, const 
             p.parts = reinterpret_cast<float*>(rest);
             rest += parts_bytes(p.segments, outer, inner);
         }
-        if (!launch_product(p, z, xs, by_planes(type, outer, inner, rows, true), rest, st)) return NMS_ERR_CUDA;
-        if (p.segments > 1) launch_join_parts(p.parts, p.segments, static_cast<int64_t>(outer) * inner, dweight, type, st);
+        if (!launch_product(p, z, xs, dw_planes, rest, st)) return NMS_ERR_CUDA;
+        // The join of columns is made for many parts of few results.
+        if (p.segments > 32 && type == NMS_TYPE_F32)
+            launch_column_join(p.parts, p.segments, static_cast<int64_t>(outer) * inner, static_cast<int64_t>(outer) * inner,
+                               static_cast<float*>(dweight), nullptr, st);
+        else if (p.segments > 1)
+            launch_join_parts(p.parts, p.segments, static_cast<int64_t>(outer) * inner, dweight, type, st);
     }
     return cuda_status();
 }

@@ -9,8 +9,9 @@
 // memory, in order.
 //
 // Up to 16 rows are a stream of the weight, whose elements are used once a row:
-// few_along_kernel and few_across_kernel read it straight to registers, all of an
-// SM's warps at once.
+// few_along_kernel reads it straight to registers, all of an SM's warps at once,
+// few_across_kernel has it copied ahead.  The gradient of a weight of up to 32 rows
+// is such a stream of x.
 #include "block.h"
 #include "head.cuh"
 #include "internal.h"
@@ -247,50 +248,93 @@ few_along_kernel(const ProductArgs p)
     }
 }
 
-// Results of up to R rows and 32 V columns a cluster, B lying across: a block
-// has a stretch of k, in chunks of 64 whose part of A it keeps in shared memory,
-// a warp eight rows of B of each chunk, a lane V columns.
+constexpr int FEW_CHUNK = 32, FEW_STAGES = 4;
+template <int R> constexpr int FEW_PITCH = R == 1 ? 1 : R + 4;  // of A's chunk: 32 lanes fill it over its columns
+template <int R, int V> constexpr int FEW_STAGE = FEW_CHUNK * 32 * V + FEW_CHUNK * FEW_PITCH<R>;  // floats
 template <int R, int V>
-__global__ void __launch_bounds__(256)
+constexpr int FEW_SMEM = 4 * (FEW_STAGES * FEW_STAGE<R, V> > 9 * R * 32 * V ? FEW_STAGES * FEW_STAGE<R, V> : 9 * R * 32 * V);
+
+// BYTES to shared memory, or as many zeros.
+template <int BYTES>
+__device__ __forceinline__ void copy_or_zero(float* to, const float* from, bool in)
+{
+    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(in ? 16 : 0) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(from), "n"(BYTES), "r"(in ? BYTES : 0) : "memory");
+}
+
+// Results of up to R rows and 32 V columns a cluster, B lying across: a block
+// has a stretch of k, in chunks of 32 on their way to shared memory three ahead, a
+// warp four rows of B of each chunk, a lane V columns.  The gradient of a weight
+// of up to 32 rows (A across too) has segments of k along the grid's second axis.
+// HBM bounds it, and from 16 rows on its arithmetic as much: gradient of 8 x 8192 by a
+// weight of 8192 x 8192 52 us (5.2 TB/s; a chunk at a time through registers 100), 16 x
+// 4096 by 11008 x 4096 51; two blocks an SM, without that bound 84.
+template <int R, int V>
+__global__ void __launch_bounds__(256, 2)
 few_across_kernel(const ProductArgs p, int split)
 {
     extern __shared__ __align__(16) float dynamic[];
-    constexpr int COLUMNS = 32 * V, CHUNK = 64, EACH = CHUNK / 8;
-    float* const xs = dynamic;                                // [CHUNK][R]
-    float* const parts = dynamic + CHUNK * R;                 // [8][R][COLUMNS]
+    constexpr int COLUMNS = 32 * V, EACH = FEW_CHUNK / 8, PITCH = FEW_PITCH<R>;
+    float* const stages = dynamic;                            // [FEW_STAGES], a chunk's rows of B [EACH][256][V], of A [FEW_CHUNK][PITCH]
+    float* const parts = dynamic;                             // after them [8][R][COLUMNS]
     float* const sums = parts + 8 * R * COLUMNS;              // [R][COLUMNS]
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t group = blockIdx.x / split, rank = blockIdx.x - group * split;
     const int64_t n = group * COLUMNS + lane * V;
     const float* const x = static_cast<const float*>(p.a);
     const float* const w = static_cast<const float*>(p.b) + n;
-    const int64_t each = ((p.k + split - 1) / split + CHUNK - 1) / CHUNK * CHUNK;
-    const int64_t first = min(p.k, rank * each), last = min(p.k, first + each);
+    const int64_t sharers = static_cast<int64_t>(p.segments) * split;
+    const int64_t each = ((p.k + sharers - 1) / sharers + FEW_CHUNK - 1) / FEW_CHUNK * FEW_CHUNK;
+    const int64_t first = min(p.k, (static_cast<int64_t>(blockIdx.y) * split + rank) * each), last = min(p.k, first + each);
+    // A chunk on its way; what is not there becomes 0.
+    auto fetch = [&](int64_t k0, int stage) {
+        float* const to = stages + stage * FEW_STAGE<R, V>;
+        if (k0 < last) {
+#pragma unroll
+            for (int q = 0; q < EACH; ++q) {
+                const int64_t k = k0 + warp * EACH + q;
+                const bool in = n < p.n && k < last;  // V divides n
+                copy_or_zero<4 * V>(to + (q * 256 + threadIdx.x) * V, in ? w + k * p.b_row : static_cast<const float*>(p.b), in);
+            }
+#pragma unroll
+            for (int e = threadIdx.x; e < FEW_CHUNK * R; e += 256) {
+                const int r = p.a_across ? e % R : e / FEW_CHUNK, c = p.a_across ? e / R : e % FEW_CHUNK;
+                const bool in = r < p.m && k0 + c < last;
+                const int64_t at = p.a_across ? (k0 + c) * p.a_row + r : r * p.a_row + k0 + c;
+                copy_or_zero<4>(to + EACH * 256 * V + c * PITCH + r, in ? x + at : x, in);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     float acc[R][V] = {};
-    for (int64_t k0 = first; k0 < last; k0 += CHUNK) {
-        Pack<float, V> wv[EACH];
-        const int64_t k = k0 + warp * EACH;
+#pragma unroll
+    for (int s = 0; s < FEW_STAGES - 1; ++s) fetch(first + s * FEW_CHUNK, s);
+    int at = 0, ahead = FEW_STAGES - 1;
+    for (int64_t k0 = first; k0 < last; k0 += FEW_CHUNK) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(FEW_STAGES - 2) : "memory");
+        __syncthreads();  // this chunk is there, and the last one no longer read
+        fetch(k0 + (FEW_STAGES - 1) * FEW_CHUNK, ahead);
+        const float* const now = stages + at * FEW_STAGE<R, V>;
+        const float* const xs = now + EACH * 256 * V + warp * EACH * PITCH;
 #pragma unroll
         for (int q = 0; q < EACH; ++q) {
+            const Pack<float, V> wv = *reinterpret_cast<const Pack<float, V>*>(now + (q * 256 + threadIdx.x) * V);
+            constexpr int TOGETHER = R == 1 ? 1 : 4;
 #pragma unroll
-            for (int i = 0; i < V; ++i) wv[q].v[i] = 0.0f;
-            if (n < p.n && k + q < last) wv[q] = *reinterpret_cast<const Pack<float, V>*>(w + (k + q) * p.b_row);  // V divides n
-        }
-        __syncthreads();  // nobody reads the last chunk's part of A
-        for (int e = threadIdx.x; e < CHUNK * R; e += 256) {
-            const int r = e / CHUNK, c = e % CHUNK;
-            xs[c * R + r] = r < p.m && k0 + c < last ? __ldg(x + r * p.a_row + k0 + c) : 0.0f;
-        }
-        __syncthreads();
+            for (int r = 0; r < R; r += TOGETHER) {
+                const Pack<float, TOGETHER> xv = *reinterpret_cast<const Pack<float, TOGETHER>*>(xs + q * PITCH + r);
 #pragma unroll
-        for (int q = 0; q < EACH; ++q)
+                for (int j = 0; j < TOGETHER; ++j)
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float xv = xs[(warp * EACH + q) * R + r];
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[r][i] = fmaf(xv, wv[q].v[i], acc[r][i]);
+                    for (int i = 0; i < V; ++i) acc[r + j][i] = fmaf(xv.v[j], wv.v[i], acc[r + j][i]);
             }
+        }
+        at = at + 1 == FEW_STAGES ? 0 : at + 1;
+        ahead = ahead + 1 == FEW_STAGES ? 0 : ahead + 1;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the stages are no longer read
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -306,7 +350,10 @@ few_across_kernel(const ProductArgs p, int split)
     for (int e = static_cast<int>(rank) * 256 + threadIdx.x; e < R * COLUMNS; e += 256 * split) {
         const int r = e / COLUMNS, c = e % COLUMNS;
         const int64_t at = group * COLUMNS + c;
-        if (r < p.m && at < p.n) finish(p, r, at, cluster_sum(sums + e, split), Addends(p, r, at));
+        if (r >= p.m || at >= p.n) continue;
+        const float sum = cluster_sum(sums + e, split);
+        if (p.segments > 1) p.parts[(blockIdx.y * p.m + r) * p.n + at] = sum;
+        else finish(p, r, at, sum, Addends(p, r, at));
     }
     __syncwarp();
     cluster_barrier();  // no block leaves while another reads its sums
@@ -351,13 +398,13 @@ copy_rows_kernel(const CopyRows first, const CopyRows second)
 
 // A kernel over clusters of `split` blocks of 256 threads.
 template <typename Kernel, typename... Args>
-static bool launch_clusters(Kernel kernel, int64_t clusters, int split, int smem, cudaStream_t st, Args... args)
+static bool launch_clusters(Kernel kernel, int64_t clusters, int split, int segments, int smem, cudaStream_t st, Args... args)
 {
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return false;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(clusters * split));
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * split), segments);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -370,25 +417,29 @@ static bool launch_clusters(Kernel kernel, int64_t clusters, int split, int smem
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
+static bool even(const void* p, int64_t row, int v) { return reinterpret_cast<uintptr_t>(p) % (4 * v) == 0 && row % v == 0; }
+
+template <int R, int V>
+static bool launch_few_across(const ProductArgs& p, cudaStream_t st)
+{
+    constexpr int COLUMNS = 32 * V;
+    const int64_t groups = (p.n + COLUMNS - 1) / COLUMNS;
+    // A gradient's blocks run all at once; the others' stretches are short.
+    const int64_t most = p.a_across ? SMS * 2 : SMS * 4;
+    int split = 1;
+    while (split < 8 && groups * p.segments * split * 2 <= most && p.k / p.segments >= split * 128) split *= 2;
+    return launch_clusters(few_across_kernel<R, V>, groups, split, p.segments, FEW_SMEM<R, V>, st, p, split);
+}
+
 template <int R>
 static bool launch_few(const ProductArgs& p, cudaStream_t st)
 {
-    auto even = [](const void* v, int64_t row) { return reinterpret_cast<uintptr_t>(v) % 16 == 0 && row % 4 == 0; };
-    if (!p.b_across) {
-        const bool wide = p.k % 4 == 0 && even(p.a, p.a_row) && even(p.b, p.b_row);
-        const unsigned grid = static_cast<unsigned>((p.n + 7) / 8);
-        if (wide) few_along_kernel<R, 4><<<grid, 256, 0, st>>>(p);
-        else few_along_kernel<R, 1><<<grid, 256, 0, st>>>(p);
-        return true;
-    }
-    const bool wide = p.n % 4 == 0 && even(p.b, p.b_row);
-    const int columns = wide ? 128 : 32;
-    const int64_t groups = (p.n + columns - 1) / columns;
-    int split = 1;
-    while (split < 8 && groups * split * 2 <= SMS * 4 && p.k >= split * 128) split *= 2;
-    const int smem = (64 * R + 9 * R * columns) * 4;
-    if (wide) return launch_clusters(few_across_kernel<R, 4>, groups, split, smem, st, p, split);
-    return launch_clusters(few_across_kernel<R, 1>, groups, split, smem, st, p, split);
+    if (p.b_across)
+        return p.n % 4 == 0 && even(p.b, p.b_row, 4) ? launch_few_across<R, 4>(p, st) : launch_few_across<R, 1>(p, st);
+    const unsigned grid = static_cast<unsigned>((p.n + 7) / 8);
+    if (p.k % 4 == 0 && even(p.a, p.a_row, 4) && even(p.b, p.b_row, 4)) few_along_kernel<R, 4><<<grid, 256, 0, st>>>(p);
+    else few_along_kernel<R, 1><<<grid, 256, 0, st>>>(p);
+    return true;
 }
 
 static bool launch_tiles(const ProductArgs& p, cudaStream_t st)
@@ -398,17 +449,20 @@ static bool launch_tiles(const ProductArgs& p, cudaStream_t st)
     const int64_t steps = (p.k + PR_DEPTH - 1) / PR_DEPTH;
     int split = 1;
     while (split < 8 && tiles * split * 2 <= SMS * 4 && steps >= split * 8) split *= 2;
-    if (p.a_across) return launch_clusters(product_kernel<true, true>, tiles, split, SMEM, st, p, tiles_n, split);
-    if (p.b_across) return launch_clusters(product_kernel<false, true>, tiles, split, SMEM, st, p, tiles_n, split);
-    return launch_clusters(product_kernel<false, false>, tiles, split, SMEM, st, p, tiles_n, split);
+    if (p.a_across) return launch_clusters(product_kernel<true, true>, tiles, split, 1, SMEM, st, p, tiles_n, split);
+    if (p.b_across) return launch_clusters(product_kernel<false, true>, tiles, split, 1, SMEM, st, p, tiles_n, split);
+    return launch_clusters(product_kernel<false, false>, tiles, split, 1, SMEM, st, p, tiles_n, split);
 }
 
 bool launch_product_f32(const ProductArgs& p, cudaStream_t st)
 {
-    if (p.m <= 16 && !p.a_across) {
+    if (p.m <= 16) {
         if (p.m == 1) return launch_few<1>(p, st);
-        return p.m <= 4 ? launch_few<4>(p, st) : launch_few<16>(p, st);
+        return p.m <= 4 ? launch_few<4>(p, st) : p.m <= 8 ? launch_few<8>(p, st) : launch_few<16>(p, st);
     }
+    // 32 sums of two columns each are as many registers as 16 of four.
+    if (p.m <= 32 && p.a_across)
+        return p.n % 2 == 0 && even(p.b, p.b_row, 2) ? launch_few_across<32, 2>(p, st) : launch_few_across<32, 1>(p, st);
     return launch_tiles(p, st);
 }
 

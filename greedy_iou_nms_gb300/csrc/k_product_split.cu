@@ -16,6 +16,7 @@
 // k_product.cu.
 #include <atomic>
 
+#include "planes.cuh"
 #include "tensor_core.cuh"
 
 namespace gbnms {
@@ -369,9 +370,7 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tensor), "n"(COLUMNS));
 }
 
-// x = h + m + l, eight elements of a row a thread.  Where x rounds to an infinity
-// (and is none) its first part is cut instead; of a NaN or an infinity the first
-// part is all there is.
+// Rows as planes of parts, eight elements of a row a thread.
 template <bool WIDE>
 __global__ void __launch_bounds__(256)
 split_rows_kernel(const SplitRows first, const SplitRows second)
@@ -390,15 +389,7 @@ split_rows_kernel(const SplitRows first, const SplitRows second)
             for (int k = 0; k < 8; ++k) x[k] = e + k < s.width ? p[k] : 0.0f;
         }
         Pack<__nv_bfloat16, 8> h, m, l;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const bool finite = fabsf(x[k]) < INFINITY;
-            h.v[k] = __float2bfloat16_rn(x[k]);
-            if (finite && fabsf(to_f32(h.v[k])) == INFINITY) h.v[k] = __float2bfloat16_rz(x[k]);
-            const float rest = finite ? x[k] - to_f32(h.v[k]) : 0.0f;
-            m.v[k] = __float2bfloat16_rn(rest);
-            l.v[k] = __float2bfloat16_rn(rest - to_f32(m.v[k]));
-        }
+        split_parts(x, h, m, l);
         __nv_bfloat16* q = static_cast<__nv_bfloat16*>(s.to) + row * s.to_row + e;
         *reinterpret_cast<Pack<__nv_bfloat16, 8>*>(q) = h;
         *reinterpret_cast<Pack<__nv_bfloat16, 8>*>(q + s.rows * s.to_row) = m;

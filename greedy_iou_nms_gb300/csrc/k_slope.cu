@@ -1,7 +1,9 @@
 // dz = dy * act'(pre) and the sums of its columns: what a linear layer's
 // gradient has to do before its two products.
 //
-// HBM bounds it (dy and pre read once, dz written once).  A block has a strip
+// HBM bounds it (dy and pre read once, dz written once, where the products go by
+// planes as those: a pass of its own over dz for them was 8 bytes an element
+// more).  A block has a strip
 // of columns and a run of rows; each of its SL_SLOTS warps goes through every
 // SL_SLOTS-th row, a lane V columns of it, and keeps their sums in registers.
 // The warps' sums are added in order, the runs' by one short kernel.
@@ -9,6 +11,7 @@
 #include "head.cuh"
 #include "internal.h"
 #include "once.cuh"
+#include "planes.cuh"
 
 namespace gbnms {
 
@@ -30,7 +33,7 @@ slope_kernel(const SlopeArgs s, int64_t run, float* parts, bool joined)
     const int64_t e = (static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x) * V;
     const int64_t first = blockIdx.y * run, last = min(s.rows, first + run);
     float sum[V] = {};
-    const uint64_t once = once_policy(s.dz != nullptr);  // the products read dz in place of dy: L2 is for that
+    const uint64_t once = once_policy(s.dz || s.planes);  // the products read dz in place of dy: L2 is for that
     if (e < s.width) {
         const T* dy = static_cast<const T*>(s.dy) + e;
         const T* pre = static_cast<const T*>(s.pre) + e;
@@ -51,6 +54,16 @@ slope_kernel(const SlopeArgs s, int64_t run, float* parts, bool joined)
             // Rounded here to the type that the products take: half a step of a factor, no more than the factors
             // themselves came with.
             if (s.dz) *reinterpret_cast<Pack<T, V>*>(dz + row * s.dz_row) = pack_results<T, V>(d);
+            if constexpr (sizeof(T) == 4) {
+                if (s.planes) {
+                    Pack<__nv_bfloat16, V> h, m, l;
+                    split_parts(d, h, m, l);
+                    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(s.planes) + row * s.dz_row + e;
+                    *reinterpret_cast<Pack<__nv_bfloat16, V>*>(to) = h;
+                    *reinterpret_cast<Pack<__nv_bfloat16, V>*>(to + s.rows * s.dz_row) = m;
+                    *reinterpret_cast<Pack<__nv_bfloat16, V>*>(to + 2 * s.rows * s.dz_row) = l;
+                }
+            }
         }
     }
     if (!parts) return;

@@ -44,7 +44,7 @@ def _stream():
 
 
 SIZES = [(1, 24, 40), (3, 33, 7), (17, 200, 72), (64, 520, 136), (130, 127, 129), (300, 1032, 250), (2100, 64, 1003),
-         (9001, 24, 40), (600, 520, 520)]
+         (9001, 24, 40), (600, 520, 520), (9001, 72, 10), (30000, 24, 4), (1500, 202, 29)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])

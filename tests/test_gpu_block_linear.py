@@ -102,6 +102,35 @@ def test_larger(kind):
     _backward(x, w, R.linear(x, w, b, "none")[1], res, "none")
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,inner,outer", [(20011, 333, 10), (9000, 64, 16), (1500, 2500, 4), (40000, 72, 1),
+                                              (5000, 31, 13), (8200, 29, 17), (3000, 1200, 6), (1023, 4, 2),
+                                              (140001, 6, 32), (700, 402, 33), (2000, 2050, 25)])
+def test_gradient_of_few_outputs(rows, inner, outer, kind):
+    """Weights of a few rows: a stream of x."""
+    x, w, b, dy = _inputs(rows, inner, outer, kind, rows)
+    z = R.linear(x, w, b, "none")[1]
+    for act in ("none", "gelu"):
+        _backward(x, w, z, dy, act)
+
+
+def test_gradient_by_parts_of_rows_with_gaps():
+    """dz goes to the tensor cores' parts straight from dy: rows that lie apart, start anywhere, or are one row."""
+    rows, inner, outer = 900, 300, 523
+    x, w, b, _ = (v.cuda() for v in _inputs(rows, inner, outer, "f32", 21))
+    wide = torch.randn(rows, outer + 14, generator=torch.Generator().manual_seed(22)).cuda()
+    z = g.linear_act(x, w, b)
+    for dy in (wide[:, 3:3 + outer], wide[:, :outer], wide[5:6, :outer].expand(rows, outer)):
+        for act in ("none", "silu"):
+            for need in ((True, True, True), (True, False, False), (False, True, True), (False, False, True)):
+                got = g.linear_act_grad(dy, x, w, z, act=act, need=need)
+                ref = g.linear_act_grad(dy.contiguous(), x, w, z, act=act)
+                for p, q, wanted in zip(got, ref, need):
+                    # The columns' sums are taken in another order where a thread has another number of columns.
+                    assert p is None if not wanted else \
+                        torch.equal(p, q) if p.dim() > 1 else torch.allclose(p, q, rtol=0, atol=1e-3)
+
+
 def test_whole_numbers_are_exact():
     """Small whole numbers have exact products and sums in every type, whatever the order."""
     r = torch.Generator().manual_seed(3)
