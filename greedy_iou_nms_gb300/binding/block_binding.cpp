@@ -41,19 +41,27 @@ struct Refused : std::runtime_error {
 
 [[noreturn]] void refuse(const char* where, const std::string& what) { throw Refused(std::string(where) + ": " + what); }
 
+// A tensor whose memory holds its values (a view can have their negation pending).
+const at::Tensor& unpack(PyObject* o, const char* where, const char* name)
+{
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (t.is_neg()) refuse(where, std::string(name) + " is a negated view: resolve_neg() it");
+    return t;
+}
+
 // A tensor argument, or an undefined tensor for None.
 const at::Tensor& argument(PyObject* o, const char* where, const char* name)
 {
     static const at::Tensor none;
     if (o == Py_None) return none;
     if (!THPVariable_Check(o)) refuse(where, std::string(name) + " must be a tensor");
-    return THPVariable_Unpack(o);
+    return unpack(o, where, name);
 }
 
 const at::Tensor& operand(PyObject* o, const char* where, const char* name)
 {
     if (!THPVariable_Check(o)) refuse(where, std::string(name) + " must be a tensor");
-    return THPVariable_Unpack(o);
+    return unpack(o, where, name);
 }
 
 int type_code(at::ScalarType t)

@@ -168,6 +168,17 @@ def test_tensor_functions_refuse(message, call):
         call()
 
 
+def test_negated_views_are_refused():
+    """A view whose memory holds the values' opposites."""
+    x = torch.randn(3, 1, 2).contiguous().view(3, 2).view(torch.complex64).conj().imag  # [3, 1]
+    assert x.is_neg()
+    w = torch.ones(4, 1)
+    for call in (lambda: g.linear_act(x, w), lambda: g.linear_act(w, w, residual=x), lambda: g.layer_norm(x),
+                 lambda: g.linear_act_grad(x, x, w), lambda: g.rotary(x[:, :, None, None], x, w)):
+        with pytest.raises(ValueError, match="negated view"):
+            call()
+
+
 def test_arguments_that_are_no_numbers():
     with pytest.raises(TypeError):
         g.layer_norm(X, eps="small")
