@@ -18,8 +18,8 @@ import os
 from typing import Optional
 
 from . import block, head
-from .block import (NMS_LAYER_MAX_WIDTH, NMS_LINEAR_MAX_WIDTH, NMS_POSITION_I32, NMS_ROTARY_MAX_AXES,  # noqa: F401
-                    NMS_ROTARY_MAX_DIM, layer_norm, layer_norm_grad, linear_act, linear_act_grad,
+from .block import (NMS_ACT_ROUND_SLOPES, NMS_LAYER_MAX_WIDTH, NMS_LINEAR_MAX_WIDTH, NMS_POSITION_I32,  # noqa: F401
+                    NMS_ROTARY_MAX_AXES, NMS_ROTARY_MAX_DIM, layer_norm, layer_norm_grad, linear_act, linear_act_grad,
                     nms_layer_norm_grad_run, nms_layer_norm_run, nms_layer_norm_workspace_size, nms_linear_grad_run,
                     nms_linear_grad_workspace_size, nms_linear_run, nms_linear_workspace_size, nms_rotary_run, rotary,
                     rotary_grad, rotary_lut)

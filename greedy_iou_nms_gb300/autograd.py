@@ -66,22 +66,23 @@ class _RelationSoftmax(torch.autograd.Function):
 
 class _LinearAct(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, act, residual):
+    def forward(ctx, x, weight, bias, act, residual, round_slopes):
         keep = act != "none" and any(ctx.needs_input_grad[:3])
         out = block.linear_act(x, weight, bias, act=act, residual=residual, return_pre=keep)
         y, pre = out if keep else (out, None)
         ctx.save_for_backward(x, weight, pre)
-        ctx.act, ctx.bias_type = act, None if bias is None else bias.dtype
+        ctx.act, ctx.round_slopes, ctx.bias_type = act, round_slopes, None if bias is None else bias.dtype
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         x, weight, pre = ctx.saved_tensors
-        dx, dweight, dbias = block.linear_act_grad(dy, x, weight, pre, act=ctx.act, need=ctx.needs_input_grad[:3]) \
+        dx, dweight, dbias = block.linear_act_grad(dy, x, weight, pre, act=ctx.act, need=ctx.needs_input_grad[:3],
+                                                   round_slopes=ctx.round_slopes) \
             if any(ctx.needs_input_grad[:3]) else (None, None, None)
         return dx, dweight, None if dbias is None else dbias.to(ctx.bias_type), None, \
-            dy if ctx.needs_input_grad[4] else None
+            dy if ctx.needs_input_grad[4] else None, None
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -134,9 +135,10 @@ def relation_softmax(scores, table, buckets, *, scale: float = 1.0, key_mask=Non
     return _RelationSoftmax.apply(scores, table, buckets, scale, key_mask)
 
 
-def linear_act(x, weight, bias=None, *, act: str = "none", residual=None):
-    """`greedy_iou_nms_gb300.linear_act` with gradients to x, weight, bias and the residual."""
-    return _LinearAct.apply(x, weight, bias, act, residual)
+def linear_act(x, weight, bias=None, *, act: str = "none", residual=None, round_slopes: bool = False):
+    """`greedy_iou_nms_gb300.linear_act` with gradients to x, weight, bias and the residual; round_slopes as for
+    `linear_act_grad`."""
+    return _LinearAct.apply(x, weight, bias, act, residual, round_slopes)
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, residual=None):

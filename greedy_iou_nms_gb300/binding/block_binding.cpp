@@ -267,7 +267,7 @@ PyObject* linear_act_grad(PyObject*, PyObject* const* args, Py_ssize_t n)
             refuse(where, "dy must be [..., outer] of x's type beside x");
         const Rows dys = rows_of(dy, where);
         at::Tensor pre;
-        if (act != NMS_ACT_NONE) {
+        if ((act & ~NMS_ACT_ROUND_SLOPES) != NMS_ACT_NONE) {
             if (!given.defined()) refuse(where, "an activation's gradient needs the forward's pre");
             same(given, dy, where, "pre");
             pre = given.contiguous();

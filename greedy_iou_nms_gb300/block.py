@@ -19,6 +19,7 @@ from .head import _ACTS, _lib, _raise
 
 NMS_LAYER_MAX_WIDTH = 16384
 NMS_LINEAR_MAX_WIDTH = 1 << 18
+NMS_ACT_ROUND_SLOPES = 256
 NMS_ROTARY_MAX_AXES = 8
 NMS_ROTARY_MAX_DIM = 4096
 NMS_POSITION_I32 = 16
@@ -165,12 +166,15 @@ def linear_act(x, weight, bias=None, *, act: str = "none", residual=None, return
     return out if return_pre else out[0]
 
 
-def linear_act_grad(dy, x, weight, pre=None, *, act: str = "none", need=(True, True, True)):
+def linear_act_grad(dy, x, weight, pre=None, *, act: str = "none", need=(True, True, True), round_slopes: bool = False):
     """Gradient of `linear_act`: (dx like x, dweight like weight, dbias float32
     [outer]); the residual's is dy itself.  pre is the forward's (not read
     with act 'none'); need says which of the three are wanted, the others are
-    None."""
-    out = _native().linear_act_grad(dy, x, weight, pre, _act(act, "linear_act_grad"), *need)
+    None.  round_slopes: dy act'(pre) is rounded to a 16-bit type before the
+    products, which then take half as long with silu and gelu and are off by
+    that rounding."""
+    code = _act(act, "linear_act_grad") | (NMS_ACT_ROUND_SLOPES if round_slopes else 0)
+    out = _native().linear_act_grad(dy, x, weight, pre, code, *need)
     if type(out) is int:
         _raise(out, "nms_linear_grad_run")
     return out

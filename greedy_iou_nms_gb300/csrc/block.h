@@ -66,6 +66,7 @@ void launch_column_join(const float* parts, int64_t blocks, int64_t columns, int
 struct ProductArgs {
     const void* a;  // [m][k], or [k][m] with a_across; rows a_row apart
     const void* b;  // [n][k], or [k][n] with b_across
+    const void* a_low;  // 16 bits: what a's elements left out when they were rounded, laid out like a; or NULL
     int64_t a_row, b_row;
     int a_across, b_across;
     int type;
@@ -128,6 +129,7 @@ struct SlopeArgs {
     int act;
     void* dz;
     int64_t dz_row;
+    void* low;     // 16 bits: what rounding dz left out, like dz; or NULL
     void* planes;  // binary32: dz as planes [3][rows][dz_row] in place of dz
     float* dbias;
 };

@@ -50,6 +50,7 @@ struct TcArgs {
     void* pre;
     int64_t out_m, out_n;  // strides of out and pre
     int vector;            // rows of out, pre and residual start at multiples of 16 bytes
+    int low_of;            // operand that comes in two parts (1: A, 2: B, 0: none)
     int32_t* status;
 };
 
@@ -167,7 +168,8 @@ struct Patch {
 // SWAP: A's rows are results' columns (the operands changed places); bias by m.
 template <typename T, int BN, bool SWAP, bool PAIR>
 __global__ void __launch_bounds__(TC_THREADS, 1)
-product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const TcArgs p)
+product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                  const __grid_constant__ CUtensorMap map_low, const TcArgs p)
 {
     constexpr int BB = PAIR ? BN / 2 : BN, ROWS = PAIR ? 2 * TC_M : TC_M;  // of B in this block, of A in a tile
     constexpr int STAGES = TC_STAGES<BB>, B_BYTES = BB * TC_K * 2, STAGE = A_BYTES + B_BYTES;
@@ -211,7 +213,9 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     const uint32_t tensor = tensor_at;
     pdl_wait();
     const int share = PAIR ? 2 : p.split, rank = static_cast<int>(blockIdx.x) % share;  // of the cluster
-    const int64_t tiles = p.tiles_m * p.tiles_n, items = tiles * p.segments, steps = (p.k + TC_K - 1) / TC_K;
+    // An operand of two parts goes through k twice, its lower part first: what sums so small lose counts for nothing.
+    const int64_t once = (p.k + TC_K - 1) / TC_K, low = p.low_of ? once : 0;
+    const int64_t tiles = p.tiles_m * p.tiles_n, items = tiles * p.segments, steps = low + once;
     const int64_t sharers = p.segments > 1 ? p.segments : p.split, each = (steps + sharers - 1) / sharers;
     // Item t: a tile and this block's stretch of k.
     auto item = [&](int64_t t, int64_t& first, int64_t& last) {
@@ -235,18 +239,20 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 const uint32_t bar = full + 8 * s, a = ring + s * STAGE, b = a + A_BYTES;
                 if (!PAIR) barrier_expect(bar, STAGE);
                 else if (rank == 0) barrier_expect(bar, 2 * STAGE);
-                const int x = static_cast<int>(k * TC_K);
+                const int lower = k < low ? p.low_of : 0, x = static_cast<int>((k < low ? k : k - low) * TC_K);
+                const CUtensorMap* const from_a = lower == 1 ? &map_low : &map_a;
+                const CUtensorMap* const from_b = lower == 2 ? &map_low : &map_b;
                 if (p.a_across) {
 #pragma unroll
-                    for (int h = 0; h < TC_M / 64; ++h) tma_load<PAIR>(a + h * HALF_BYTES, &map_a, m + 64 * h, x, bar);
+                    for (int h = 0; h < TC_M / 64; ++h) tma_load<PAIR>(a + h * HALF_BYTES, from_a, m + 64 * h, x, bar);
                 } else {
-                    tma_load<PAIR>(a, &map_a, x, m, bar);
+                    tma_load<PAIR>(a, from_a, x, m, bar);
                 }
                 if (BB >= 64 && p.b_across) {
 #pragma unroll
-                    for (int h = 0; h < BB / 64; ++h) tma_load<PAIR>(b + h * HALF_BYTES, &map_b, n + 64 * h, x, bar);
+                    for (int h = 0; h < BB / 64; ++h) tma_load<PAIR>(b + h * HALF_BYTES, from_b, n + 64 * h, x, bar);
                 } else {
-                    tma_load<PAIR>(b, &map_b, x, n, bar);
+                    tma_load<PAIR>(b, from_b, x, n, bar);
                 }
                 if (++s == STAGES) {
                     s = 0;
@@ -453,7 +459,7 @@ bool encode(CUtensorMap* map, int type, const void* p, int64_t width, int64_t ro
 }
 
 template <typename T, int BN, bool SWAP, bool PAIR>
-bool launch_tile(const CUtensorMap& a, const CUtensorMap& b, const TcArgs& p, cudaStream_t st)
+bool launch_tile(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& low, const TcArgs& p, cudaStream_t st)
 {
     auto kernel = product_tc_kernel<T, BN, SWAP, PAIR>;
     constexpr int SMEM = 1024 + TC_RING<PAIR ? BN / 2 : BN> + (SWAP ? 0 : TC_WRITERS / 32 * TC_PATCH);
@@ -479,21 +485,22 @@ bool launch_tile(const CUtensorMap& a, const CUtensorMap& b, const TcArgs& p, cu
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, a, b, p) == cudaSuccess;
+    return cudaLaunchKernelEx(&cfg, kernel, a, b, low, p) == cudaSuccess;
 }
 
 template <typename T>
-bool launch_type(int bn, bool swap, bool pair, const CUtensorMap& a, const CUtensorMap& b, const TcArgs& p, cudaStream_t st)
+bool launch_type(int bn, bool swap, bool pair, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& low,
+                 const TcArgs& p, cudaStream_t st)
 {
     if (swap) {
-        if (bn == 16) return launch_tile<T, 16, true, false>(a, b, p, st);
-        if (bn == 32) return launch_tile<T, 32, true, false>(a, b, p, st);
-        return launch_tile<T, 64, true, false>(a, b, p, st);
+        if (bn == 16) return launch_tile<T, 16, true, false>(a, b, low, p, st);
+        if (bn == 32) return launch_tile<T, 32, true, false>(a, b, low, p, st);
+        return launch_tile<T, 64, true, false>(a, b, low, p, st);
     }
-    if (pair) return bn == 128 ? launch_tile<T, 128, false, true>(a, b, p, st) : launch_tile<T, 256, false, true>(a, b, p, st);
-    if (bn == 64) return launch_tile<T, 64, false, false>(a, b, p, st);
-    if (bn == 128) return launch_tile<T, 128, false, false>(a, b, p, st);
-    return launch_tile<T, 256, false, false>(a, b, p, st);
+    if (pair) return bn == 128 ? launch_tile<T, 128, false, true>(a, b, low, p, st) : launch_tile<T, 256, false, true>(a, b, low, p, st);
+    if (bn == 64) return launch_tile<T, 64, false, false>(a, b, low, p, st);
+    if (bn == 128) return launch_tile<T, 128, false, false>(a, b, low, p, st);
+    return launch_tile<T, 256, false, false>(a, b, low, p, st);
 }
 
 }  // namespace
@@ -511,6 +518,7 @@ bool launch_product_tc(const ProductArgs& q, cudaStream_t st)
     p.out = q.out;
     p.pre = q.pre;
     p.status = q.status;
+    p.low_of = !q.a_low ? 0 : swap ? 2 : 1;
     p.segments = q.segments;
     p.parts = q.parts;
     const void *a = q.a, *b = q.b;
@@ -559,19 +567,24 @@ bool launch_product_tc(const ProductArgs& q, cudaStream_t st)
     const int64_t rows = pair ? 2 * TC_M : TC_M;
     p.tiles_m = (p.m + rows - 1) / rows;
     p.tiles_n = (p.n + bn - 1) / bn;
-    const int64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + TC_K - 1) / TC_K;
+    const int64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + TC_K - 1) / TC_K * (q.a_low ? 2 : 1);
     p.split = 1;
     // Joining the parts costs a few microseconds: 300 x 256 x 1024, four stages a tile, took 7.7 us by two blocks a tile
     // and 5.5 by one; 16 x 1024 x 4096, sixteen stages, 6.2 by four and 6.6 by two.
     while (!pair && p.segments == 1 && p.split < 8 && tiles * p.split * 2 <= SMS && steps >= p.split * 8) p.split *= 2;
-    CUtensorMap map_a, map_b;
-    const bool known =
-        (p.a_across ? encode(&map_a, q.type, a, p.m, p.k, a_row, 64) : encode(&map_a, q.type, a, p.k, p.m, a_row, TC_M)) &&
-        (p.b_across ? encode(&map_b, q.type, b, p.n, p.k, b_row, 64)
-                    : encode(&map_b, q.type, b, p.k, p.n, b_row, pair ? bn / 2 : bn));
-    if (!known) return false;
-    return q.type == NMS_TYPE_F16 ? launch_type<__half>(bn, swap, pair, map_a, map_b, p, st)
-                                  : launch_type<__nv_bfloat16>(bn, swap, pair, map_a, map_b, p, st);
+    auto encode_a = [&](CUtensorMap* map, const void* at) {
+        return p.a_across ? encode(map, q.type, at, p.m, p.k, a_row, 64) : encode(map, q.type, at, p.k, p.m, a_row, TC_M);
+    };
+    auto encode_b = [&](CUtensorMap* map, const void* at) {
+        return p.b_across ? encode(map, q.type, at, p.n, p.k, b_row, 64)
+                          : encode(map, q.type, at, p.k, p.n, b_row, pair ? bn / 2 : bn);
+    };
+    CUtensorMap map_a, map_b, map_low;
+    if (!encode_a(&map_a, a) || !encode_b(&map_b, b)) return false;
+    if (!p.low_of) map_low = map_a;  // not used
+    else if (!(swap ? encode_b(&map_low, q.a_low) : encode_a(&map_low, q.a_low))) return false;
+    return q.type == NMS_TYPE_F16 ? launch_type<__half>(bn, swap, pair, map_a, map_b, map_low, p, st)
+                                  : launch_type<__nv_bfloat16>(bn, swap, pair, map_a, map_b, map_low, p, st);
 }
 
 }  // namespace gbnms

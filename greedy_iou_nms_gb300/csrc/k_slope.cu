@@ -3,10 +3,11 @@
 //
 // HBM bounds it (dy and pre read once, dz written once, where the products go by
 // planes as those: a pass of its own over dz for them was 8 bytes an element
-// more).  A block has a strip
-// of columns and a run of rows; each of its SL_SLOTS warps goes through every
-// SL_SLOTS-th row, a lane V columns of it, and keeps their sums in registers.
-// The warps' sums are added in order, the runs' by one short kernel.
+// more; of 16 bits, what rounding dz leaves out goes to a second array).  A
+// block has a strip of columns and a run of rows; each of its SL_SLOTS warps
+// goes through every SL_SLOTS-th row, a lane V columns of it, and keeps their
+// sums in registers.  The warps' sums are added in order, the runs' by one short
+// kernel.
 #include "block.h"
 #include "head.cuh"
 #include "internal.h"
@@ -51,10 +52,18 @@ slope_kernel(const SlopeArgs s, int64_t run, float* parts, bool joined)
             if (s.pre) act_slopes<T, V>(d, v, s.act);
 #pragma unroll
             for (int i = 0; i < V; ++i) sum[i] += d[i];
-            // Rounded here to the type that the products take: half a step of a factor, no more than the factors
-            // themselves came with.
-            if (s.dz) *reinterpret_cast<Pack<T, V>*>(dz + row * s.dz_row) = pack_results<T, V>(d);
-            if constexpr (sizeof(T) == 4) {
+            // The type that the products take; without `low` dz is rounded to it, half a step of a factor.
+            if constexpr (sizeof(T) == 2) {
+                if (s.low) {
+                    Pack<T, V> h, l;
+                    split_two(d, h, l);
+                    *reinterpret_cast<Pack<T, V>*>(dz + row * s.dz_row) = h;
+                    *reinterpret_cast<Pack<T, V>*>(static_cast<T*>(s.low) + row * s.dz_row + e) = l;
+                } else if (s.dz) {
+                    *reinterpret_cast<Pack<T, V>*>(dz + row * s.dz_row) = pack_results<T, V>(d);
+                }
+            } else {
+                if (s.dz) *reinterpret_cast<Pack<T, V>*>(dz + row * s.dz_row) = pack_results<T, V>(d);
                 if (s.planes) {
                     Pack<__nv_bfloat16, V> h, m, l;
                     split_parts(d, h, m, l);

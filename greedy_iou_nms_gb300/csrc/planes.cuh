@@ -1,5 +1,6 @@
-// The three bfloat16 parts of a binary32 number that stand for it on the tensor
-// cores (see k_product_split.cu).
+// The 16-bit parts of a binary32 number that stand for it on the tensor cores:
+// three of bfloat16 (see k_product_split.cu), or two where 16 bits are what the
+// other operand has.
 #pragma once
 
 #include "head.cuh"
@@ -20,6 +21,23 @@ __device__ __forceinline__ void split_parts(const float (&x)[V], Pack<__nv_bfloa
         const float rest = finite ? x[k] - to_f32(h.v[k]) : 0.0f;
         m.v[k] = __float2bfloat16_rn(rest);
         l.v[k] = __float2bfloat16_rn(rest - to_f32(m.v[k]));
+    }
+}
+
+__device__ __forceinline__ __half cut(float x, __half) { return __float2half_rz(x); }
+__device__ __forceinline__ __nv_bfloat16 cut(float x, __nv_bfloat16) { return __float2bfloat16_rz(x); }
+
+// x = h + l, to 2^-18 of itself (bfloat16), or to 2^-22 and 2^-25 (binary16).  The
+// same of what rounds to an infinity, and of infinities and NaN.
+template <typename T, int V>
+__device__ __forceinline__ void split_two(const float (&x)[V], Pack<T, V>& h, Pack<T, V>& l)
+{
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const bool finite = fabsf(x[k]) < INFINITY;
+        h.v[k] = from_f32<T>(x[k]);
+        if (finite && fabsf(to_f32(h.v[k])) == INFINITY) h.v[k] = cut(x[k], T());
+        l.v[k] = from_f32<T>(finite ? x[k] - to_f32(h.v[k]) : 0.0f);
     }
 }
 

@@ -586,6 +586,7 @@ nms_status nms_relation_softmax_grad_run(const void* dprobs, const void* probs, 
  */
 #define NMS_LAYER_MAX_WIDTH 16384
 #define NMS_LINEAR_MAX_WIDTH (1 << 18)
+#define NMS_ACT_ROUND_SLOPES 256
 #define NMS_ROTARY_MAX_AXES 8
 #define NMS_ROTARY_MAX_DIM 4096
 
@@ -618,8 +619,11 @@ nms_status nms_relation_softmax_grad_run(const void* dprobs, const void* probs, 
  *   dz = dy * act'(pre),  dx = dz weight,  dweight = dz^T x,  dbias = sum dz,
  * dx [rows][inner], dweight [outer][inner] contiguous and of `type`, dbias
  * float [outer]; each may be NULL and is left out then.  The residual's
- * gradient is dy.  With an activation the products take dz rounded to `type`;
- * dbias is summed before that.  `aligned` there speaks of dy too.  Sums are
+ * gradient is dy.  Of 16 bits, where act is NMS_ACT_SILU or NMS_ACT_GELU, the
+ * products take dz as two numbers of `type`, dz rounded and what that left out;
+ * with act | NMS_ACT_ROUND_SLOPES only the first, half of the multiplications
+ * for results that are off by the rounding of a factor.  dbias is the sum of dz
+ * unrounded either way.  `aligned` there speaks of dy too.  Sums are
  * taken in a fixed order: the same call gives the same bits.
  * Errors: NMS_ERR_INVALID_ARG (types, act, shapes, negative strides, NULL or
  *         misaligned pointers), NMS_ERR_CAPACITY (inner or outer above
