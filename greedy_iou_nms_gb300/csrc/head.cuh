@@ -167,7 +167,7 @@ __device__ __forceinline__ float normal_cdf(float z, float& density)
     if constexpr (sizeof(T) == 4) {
         density = 0.398942280f * exp2_fast(-0.5f * LOG2E * z * z);
         t = reciprocal(fmaf(0.26f, x, 1.0f));
-        const float s = 0.26f * x * t;
+        const float s = 0.26f * fminf(x, 0x1.fffffep127f) * t;  // of an infinity, where t is 0, a number too
         q = fmaf(0.0790923014f, s, -0.237447441f);
         q = fmaf(q, s, 0.101926945f);
         q = fmaf(q, s, 0.350009143f);
