@@ -8,7 +8,11 @@
 namespace gbnms {
 
 // x = h + m + l.  Where x rounds to an infinity (and is none) its first part is
-// cut instead; of a NaN or an infinity the first part is all there is.
+// cut instead; of a NaN the first part is all there is.  An infinity is the last
+// part, with 1 of its sign as the first: the last part is multiplied by first parts
+// only (and first by last), which are 0 for 0 alone, so that products with infinities
+// are what they are in binary32 (infinity times 0 a NaN); a first part of infinity met
+// the zeros in other numbers' lower parts.
 template <int V>
 __device__ __forceinline__ void split_parts(const float (&x)[V], Pack<__nv_bfloat16, V>& h, Pack<__nv_bfloat16, V>& m,
                                             Pack<__nv_bfloat16, V>& l)
@@ -21,6 +25,10 @@ __device__ __forceinline__ void split_parts(const float (&x)[V], Pack<__nv_bfloa
         const float rest = finite ? x[k] - to_f32(h.v[k]) : 0.0f;
         m.v[k] = __float2bfloat16_rn(rest);
         l.v[k] = __float2bfloat16_rn(rest - to_f32(m.v[k]));
+        if (fabsf(x[k]) == INFINITY) {
+            l.v[k] = h.v[k];
+            h.v[k] = __float2bfloat16_rn(copysignf(1.0f, x[k]));
+        }
     }
 }
 

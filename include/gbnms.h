@@ -598,9 +598,9 @@ nms_status nms_relation_softmax_grad_run(const void* dprobs, const void* probs, 
  * products add below 2^-25 of the sum so far: a sum of k products is off by up to
  * k 2^-29 of its largest part.  Larger products of binary32 operands go there
  * as three bfloat16 parts of each element, 64 products at a time, and are as near
- * as a binary32 sum; elements below 2^-100 keep fewer than 24 bits there, and an
- * infinity may leave a NaN.  (Rows of NaN or infinities leave no number in their
- * own results and none in others'.)
+ * as a binary32 sum; elements below 2^-100 keep fewer than 24 bits there.  NaN and
+ * infinities in an operand, and sums beyond binary32, give what they give in
+ * binary32, in the results that they belong to and no others.
  *   x, weight  device, `type`, rows x_row and weight_row elements apart.
  *   bias       device [outer] of bias_type (NMS_TYPE_F32, or `type`), or NULL.
  *   act        NMS_ACT_*.
@@ -622,8 +622,9 @@ nms_status nms_relation_softmax_grad_run(const void* dprobs, const void* probs, 
  * gradient is dy.  Of 16 bits, where act is NMS_ACT_SILU or NMS_ACT_GELU, the
  * products take dz as two numbers of `type`, dz rounded and what that left out;
  * with act | NMS_ACT_ROUND_SLOPES only the first, half of the multiplications
- * for results that are off by the rounding of a factor.  dbias is the sum of dz
- * unrounded either way.  `aligned` there speaks of dy too.  Sums are
+ * for results that are off by the rounding of a factor.  (Two numbers times an
+ * infinity of x or the weight may be a NaN.)  dbias is the sum of dz unrounded
+ * either way.  `aligned` there speaks of dy too.  Sums are
  * taken in a fixed order: the same call gives the same bits.
  * Errors: NMS_ERR_INVALID_ARG (types, act, shapes, negative strides, NULL or
  *         misaligned pointers), NMS_ERR_CAPACITY (inner or outer above
