@@ -600,7 +600,8 @@ nms_status nms_relation_softmax_grad_run(const void* dprobs, const void* probs, 
  * as three bfloat16 parts of each element, 64 products at a time, and are as near
  * as a binary32 sum; elements below 2^-100 keep fewer than 24 bits there.  NaN and
  * infinities in an operand, and sums beyond binary32, give what they give in
- * binary32, in the results that they belong to and no others.
+ * binary32, in the results that they belong to and no others; a single product
+ * beyond 2^128 there may be a NaN, as an infinite one less an infinite part.
  *   x, weight  device, `type`, rows x_row and weight_row elements apart.
  *   bias       device [outer] of bias_type (NMS_TYPE_F32, or `type`), or NULL.
  *   act        NMS_ACT_*.
@@ -624,8 +625,8 @@ nms_status nms_relation_softmax_grad_run(const void* dprobs, const void* probs, 
  * with act | NMS_ACT_ROUND_SLOPES only the first, half of the multiplications
  * for results that are off by the rounding of a factor.  (Two numbers times an
  * infinity of x or the weight may be a NaN.)  dbias is the sum of dz unrounded
- * either way.  `aligned` there speaks of dy too.  Sums are
- * taken in a fixed order: the same call gives the same bits.
+ * either way.  `aligned` there speaks of dy too.  Sums are taken in a fixed
+ * order: the same call gives the same bits.
  * Errors: NMS_ERR_INVALID_ARG (types, act, shapes, negative strides, NULL or
  *         misaligned pointers), NMS_ERR_CAPACITY (inner or outer above
  *         NMS_LINEAR_MAX_WIDTH, rows above 2^31 - 1, more than 2^38 elements
