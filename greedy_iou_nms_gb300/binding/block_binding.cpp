@@ -206,6 +206,15 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, Body body)
     END_HANDLE_TH_ERRORS
 }
 
+// The C entries' dev_status: a tensor argument's word, or NULL for None.
+int32_t* status_word(const at::Tensor& status, const at::Tensor& x, const char* where)
+{
+    if (!status.defined()) return nullptr;
+    if (status.scalar_type() != at::kInt || status.numel() != 1 || status.device() != x.device())
+        refuse(where, "status must be one int32 beside x");
+    return static_cast<int32_t*>(status.data_ptr());
+}
+
 // Whether the C entries' 32-bit sizes hold these.
 bool fits(std::initializer_list<int64_t> sizes)
 {
@@ -214,13 +223,14 @@ bool fits(std::initializer_list<int64_t> sizes)
     return true;
 }
 
-// linear_act(x, weight, bias, act, residual, return_pre) -> (y,) or (y, pre)
+// linear_act(x, weight, bias, act, residual, return_pre, status) -> (y,) or (y, pre)
 PyObject* linear_act(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
-    return guarded(n, 6, [&]() -> PyObject* {
+    return guarded(n, 7, [&]() -> PyObject* {
         const char* where = "linear_act";
         const at::Tensor &x = operand(args[0], where, "x"), &weight = operand(args[1], where, "weight"),
-                         &bias = argument(args[2], where, "bias"), &residual = argument(args[4], where, "residual");
+                         &bias = argument(args[2], where, "bias"), &residual = argument(args[4], where, "residual"),
+                         &status = argument(args[6], where, "status");
         const int act = static_cast<int>(PyLong_AsLong(args[3]));
         const int type = type_of(x, where, "x");
         const Rows xs = rows_of(x, where), ws = weight_rows(x, weight, xs.width, where);
@@ -235,6 +245,7 @@ PyObject* linear_act(PyObject*, PyObject* const* args, Py_ssize_t n)
                 refuse(where, "residual must be [..., outer] of x's type beside x");
             res = rows_of(residual, where);
         }
+        int32_t* const word = status_word(status, x, where);
         on_device(x, where, "x");
         const at::Tensor y = at::empty(shape, x.options());
         const at::Tensor pre = args[5] == Py_True ? at::empty(shape, x.options()) : at::Tensor();
@@ -243,21 +254,22 @@ PyObject* linear_act(PyObject*, PyObject* const* args, Py_ssize_t n)
         if (code != NMS_OK) return result(code, {});
         const at::Tensor work = bytes ? scratch(bytes, x) : at::Tensor();
         code = launch(x, linear_run, xs.at(), xs.row, type, xs.rows, xs.width, ws.at(), ws.row, ws.rows, address(bias),
-                      bias_type, act, address(res.t), res.row, address(y), address(pre), nullptr, address(work), bytes);
+                      bias_type, act, address(res.t), res.row, address(y), address(pre), word, address(work), bytes);
         return pre.defined() ? result(code, {y, pre}) : result(code, {y});
     });
 }
 
-// linear_act_grad(dy, x, weight, pre, act, need_dx, need_dweight, need_dbias) -> (dx, dweight, dbias)
+// linear_act_grad(dy, x, weight, pre, act, status, need_dx, need_dweight, need_dbias) -> (dx, dweight, dbias)
 PyObject* linear_act_grad(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
-    return guarded(n, 8, [&]() -> PyObject* {
+    return guarded(n, 9, [&]() -> PyObject* {
         const char* where = "linear_act_grad";
         const at::Tensor &dy = operand(args[0], where, "dy"), &x = operand(args[1], where, "x"),
-                         &weight = operand(args[2], where, "weight"), &given = argument(args[3], where, "pre");
+                         &weight = operand(args[2], where, "weight"), &given = argument(args[3], where, "pre"),
+                         &status = argument(args[5], where, "status");
         const int act = static_cast<int>(PyLong_AsLong(args[4]));
-        const bool need_x = PyObject_IsTrue(args[5]) == 1, need_w = PyObject_IsTrue(args[6]) == 1,
-                   need_b = PyObject_IsTrue(args[7]) == 1;
+        const bool need_x = PyObject_IsTrue(args[6]) == 1, need_w = PyObject_IsTrue(args[7]) == 1,
+                   need_b = PyObject_IsTrue(args[8]) == 1;
         const int type = type_of(x, where, "x");
         const Rows xs = rows_of(x, where), ws = weight_rows(x, weight, xs.width, where);
         if (!fits({xs.width, ws.rows})) return result(NMS_ERR_CAPACITY, {});
@@ -272,6 +284,7 @@ PyObject* linear_act_grad(PyObject*, PyObject* const* args, Py_ssize_t n)
             same(given, dy, where, "pre");
             pre = given.contiguous();
         }
+        int32_t* const word = status_word(status, x, where);
         on_device(x, where, "x");
         if (!need_x && !need_w && !need_b) return result(NMS_OK, {{}, {}, {}});
         const at::Tensor dx = need_x ? like(x) : at::Tensor();
@@ -283,7 +296,7 @@ PyObject* linear_act_grad(PyObject*, PyObject* const* args, Py_ssize_t n)
         if (code != NMS_OK) return result(code, {});
         const at::Tensor work = scratch(bytes, x);
         code = launch(x, linear_grad_run, dys.at(), dys.row, xs.at(), xs.row, type, xs.rows, xs.width, ws.at(), ws.row,
-                      ws.rows, address(pre), act, address(dx), address(dw), static_cast<float*>(address(db)), nullptr,
+                      ws.rows, address(pre), act, address(dx), address(dw), static_cast<float*>(address(db)), word,
                       address(work), bytes);
         return result(code, {dx, dw, db});
     });

@@ -152,29 +152,35 @@ def _act(act: str, where: str) -> int:
     return code
 
 
-def linear_act(x, weight, bias=None, *, act: str = "none", residual=None, return_pre: bool = False):
+def linear_act(x, weight, bias=None, *, act: str = "none", residual=None, return_pre: bool = False, status=None):
     """y = act(x weight^T + bias) + residual.
 
     x [..., inner] float32, float16 or bfloat16; weight [outer, inner] of x's
     type; bias [outer] float32 or of x's type; act one of none, relu, silu,
     gelu; residual [..., outer] of x's type.  With return_pre also the
     activation's argument like y, which `linear_act_grad` takes.
+
+    Every wait of the kernels on the tensor cores is bounded.  One that gives up
+    (after seconds, where a calculation takes microseconds: the device is not
+    right) leaves NaNs, and NMS_ERR_TIMEOUT in status, one int32 beside x that
+    the caller has set to 0, where it is given.
     """
-    out = _native().linear_act(x, weight, bias, _act(act, "linear_act"), residual, bool(return_pre))
+    out = _native().linear_act(x, weight, bias, _act(act, "linear_act"), residual, bool(return_pre), status)
     if type(out) is int:
         _raise(out, "nms_linear_run")
     return out if return_pre else out[0]
 
 
-def linear_act_grad(dy, x, weight, pre=None, *, act: str = "none", need=(True, True, True), round_slopes: bool = False):
+def linear_act_grad(dy, x, weight, pre=None, *, act: str = "none", need=(True, True, True), round_slopes: bool = False,
+                    status=None):
     """Gradient of `linear_act`: (dx like x, dweight like weight, dbias float32
     [outer]); the residual's is dy itself.  pre is the forward's (not read
     with act 'none'); need says which of the three are wanted, the others are
     None.  round_slopes: dy act'(pre) is rounded to a 16-bit type before the
     products, which then take half as long with silu and gelu and are off by
-    that rounding."""
+    that rounding.  status as for `linear_act`."""
     code = _act(act, "linear_act_grad") | (NMS_ACT_ROUND_SLOPES if round_slopes else 0)
-    out = _native().linear_act_grad(dy, x, weight, pre, code, *need)
+    out = _native().linear_act_grad(dy, x, weight, pre, code, status, *need)
     if type(out) is int:
         _raise(out, "nms_linear_grad_run")
     return out

@@ -62,6 +62,15 @@ void launch_rotary(const RotaryArgs& a, cudaStream_t st);
 void launch_column_join(const float* parts, int64_t blocks, int64_t columns, int64_t split, float* first, float* second,
                         cudaStream_t st);
 
+// How long, in ns, a wait of the tensor-core products that this host thread
+// launches lasts before it gives up; a tile's whole sum has five times as long
+// (2^31 of k take a second).  gbnms_product_patience() sets it, for tests.
+inline uint64_t& product_patience()
+{
+    static thread_local uint64_t ns = 2000000000;
+    return ns;
+}
+
 // out = act(A B^T + bias) + residual, A m x k, B n x k.
 struct ProductArgs {
     const void* a;  // [m][k], or [k][m] with a_across; rows a_row apart

@@ -138,6 +138,9 @@ bool launch_product(ProductArgs& q, Operand& a, Operand& b, bool as_planes, char
 
 }  // namespace
 
+// Not among the public entries: see product_patience().
+extern "C" void gbnms_product_patience(uint64_t ns) { product_patience() = ns; }
+
 extern "C" nms_status nms_linear_workspace_size(int32_t type, int64_t rows, int32_t inner, int32_t outer,
                                                 int32_t aligned, size_t* bytes)
 {

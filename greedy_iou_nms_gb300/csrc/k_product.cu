@@ -50,6 +50,7 @@ struct TcArgs {
     void* pre;
     int64_t out_m, out_n;  // strides of out and pre
     int vector;            // rows of out, pre and residual start at multiples of 16 bytes
+    Patience patience;
     int low_of;            // operand that comes in two parts (1: A, 2: B, 0: none)
     int32_t* status;
 };
@@ -178,6 +179,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     extern __shared__ char dynamic[];
     __shared__ alignas(8) uint64_t bars[2 * STAGES + 4];
     __shared__ uint32_t tensor_at;
+    __shared__ float lost_s;  // 0; a NaN when a part of this block is none
     __shared__ alignas(16) float bias_s[2][SWAP ? TC_M : BN];
     const uint32_t ring = (shared_address(dynamic) + 1023) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -192,6 +194,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             barrier_init(free_ + 8 * b, (PAIR ? 2 : 1) * TC_WRITERS / 32);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        lost_s = 0.0f;
     }
     if (warp == 1) {
         if constexpr (PAIR) {
@@ -234,7 +237,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             const Place at = item(t, first, last);
             const int m = static_cast<int>(at.m) + (PAIR ? rank * TC_M : 0), n = static_cast<int>(at.n) + (PAIR ? rank * BB : 0);
             for (int64_t k = first; k < last; ++k) {
-                waited = barrier_wait(empty + 8 * s, turn ^ 1);
+                waited = barrier_wait(empty + 8 * s, turn ^ 1, p.patience);
                 if (!waited) break;
                 const uint32_t bar = full + 8 * s, a = ring + s * STAGE, b = a + A_BYTES;
                 if (!PAIR) barrier_expect(bar, STAGE);
@@ -260,7 +263,6 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 }
             }
         }
-        if (!waited) settle();
     } else if (warp == 1 && lane == 0 && (!PAIR || rank == 0)) {  // ---- matrix instructions
         const uint32_t form = instruction_form<T>(p.a_across, p.b_across, ROWS, BN);
         const uint64_t form_a = operand_form(p.a_across), form_b = operand_form(p.b_across);
@@ -269,11 +271,11 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         for (int64_t t = tile0; t < items && waited; t += tile_step) {
             int64_t first, last;
             item(t, first, last);
-            waited = barrier_wait(free_ + 8 * set, set_turn ^ 1);
+            waited = barrier_wait(free_ + 8 * set, set_turn ^ 1, p.patience);
             if (!waited) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             for (int64_t k = first; k < last; ++k) {
-                waited = barrier_wait(full + 8 * s, turn);
+                waited = barrier_wait(full + 8 * s, turn, p.patience);
                 if (!waited) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 // Descriptors have 14 bits of an address; a cluster's blocks have their rank above bit 23 of it.
@@ -291,7 +293,6 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             set_turn ^= set;
             set ^= 1;
         }
-        if (!waited) settle();
     } else if (warp >= 2) {  // ---- results
         const int writer = threadIdx.x - 64, quarter = warp % 4, row = quarter * 32 + lane, side = (warp - 2) / 4;
         char* const ring_at = dynamic + (ring - shared_address(dynamic));
@@ -315,22 +316,24 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                     Patch<T>::fetch(ahead, static_cast<const T*>(p.residual) + at.n + c, p.residual_m, row0, p.m, lane);
             };
             if (more && (PAIR || p.split == 1)) fetch(c0);
-            if (waited) waited = barrier_wait(done + 8 * set, turn, TC_TILE_PATIENCE);
+            if (waited) waited = barrier_wait(done + 8 * set, turn, p.patience, 5);
             // Given up: no number comes out of what should have been summed.
             const float lost = waited ? 0.0f : NAN;
-            if (!waited && p.status && writer == 0) set_status(p.status, NMS_ERR_TIMEOUT);
+            __syncwarp();
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tensor + set * BN + (static_cast<uint32_t>(quarter * 32) << 16);
             const int64_t m = at.m + row;
             if (!PAIR && p.split > 1) {
-                // The block's part to its own shared memory: the ring is empty by now.
+                // The block's part to its own shared memory: the ring is empty by now (or the part is none, and a copy may
+                // still land on it).
+                if (!waited) lost_s = NAN;
                 float* part = reinterpret_cast<float*>(ring_at) + row * (BN + 4);
 #pragma unroll
                 for (int c = c0; c < c0 + BN / 2; c += 8) {
                     float v[8];
                     tensor_load(v, acc + c);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) part[c + i] = first < last ? v[i] + lost : lost;
+                    for (int i = 0; i < 8; ++i) part[c + i] = first < last ? v[i] : 0.0f;
                 }
                 break;  // one tile a cluster
             }
@@ -397,7 +400,8 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
-            if (lane == 0) {
+            // A warp that does not wait any more does not speak for those that still read.
+            if (lane == 0 && waited) {
                 if constexpr (PAIR) barrier_arrive_at(peer_address(free_ + 8 * set, 0));
                 else barrier_arrive(free_ + 8 * set);
             }
@@ -406,6 +410,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     __syncwarp();
     if (!PAIR && p.split > 1) {
         cluster_barrier();
+        if (!waited) settle(p.status);
         if (warp >= 2) {
             // This block's rows of the tile, the parts added in the blocks' order.
             const Place at = tile_place(tile0, p.tiles_m, p.tiles_n, ROWS, BN);
@@ -414,7 +419,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 const int r = rank * rows + (SWAP ? e % rows : e / (BN / 4)), c = 4 * (SWAP ? e / rows : e % (BN / 4));
                 if (at.m + r >= p.m || at.n + c >= p.n) continue;
                 const uint32_t from = ring + 4 * (r * (BN + 4) + c);
-                float sum[4] = {}, v[8][4];
+                float v[8][4], lost[8];
 #pragma unroll
                 for (int b = 0; b < 8; ++b)
                     if (b < p.split)
@@ -423,9 +428,14 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                                      : "r"(peer_address(from, b)));
 #pragma unroll
                 for (int b = 0; b < 8; ++b)
+                    if (b < p.split)
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(lost[b]) : "r"(peer_address(shared_address(&lost_s), b)));
+                float sum[4] = {};
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
                     if (b < p.split) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) sum[i] += v[b][i];
+                        for (int i = 0; i < 4; ++i) sum[i] += v[b][i] + lost[b];
                     }
                 finish_some<T>(p, at.m + r, at.n + c, sum, &bias_s[0][SWAP ? r : c], SWAP ? 0 : 1);
             }
@@ -433,9 +443,11 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         __syncwarp();
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    // No block leaves while another reads its shared memory or arrives at its barriers.
+    // No block leaves while another reads its shared memory or arrives at its barriers, or something of its own is in
+    // flight.
+    if ((PAIR || p.split == 1) && __syncthreads_or(!waited)) settle(p.status);
+    __syncwarp();
     if (PAIR || p.split > 1) cluster_barrier();
-    else __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (warp == 1) {
         if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tensor), "n"(COLUMNS));
@@ -518,6 +530,7 @@ bool launch_product_tc(const ProductArgs& q, cudaStream_t st)
     p.out = q.out;
     p.pre = q.pre;
     p.status = q.status;
+    p.patience = patience();
     p.low_of = !q.a_low ? 0 : swap ? 2 : 1;
     p.segments = q.segments;
     p.parts = q.parts;

@@ -45,6 +45,7 @@ struct SplitArgs {
     float* out;
     float* pre;
     int vector;  // rows of out, pre and residual start at multiples of 16 bytes
+    Patience patience;
     int32_t* status;
 };
 
@@ -155,6 +156,7 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     extern __shared__ char dynamic[];
     __shared__ alignas(8) uint64_t bars[2 * SP_STAGES + 4];
     __shared__ uint32_t tensor_at;
+    __shared__ float lost_s;  // 0; a NaN when a part of this block is none
     __shared__ alignas(16) float bias_s[SP_N];
     const uint32_t ring = (shared_address(dynamic) + 1023) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -169,6 +171,7 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             barrier_init(free_ + 8 * b, TC_WRITERS / 32);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        lost_s = 0.0f;
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_address(&tensor_at)),
@@ -201,7 +204,7 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             const Place at = item(t, first, last);
             const int m = static_cast<int>(at.m), n = static_cast<int>(at.n);
             for (int64_t k = first; k < last; ++k) {
-                waited = barrier_wait(empty + 8 * s, turn ^ 1);
+                waited = barrier_wait(empty + 8 * s, turn ^ 1, p.patience);
                 if (!waited) break;
                 const uint32_t bar = full + 8 * s, a = ring + s * SP_STAGE, b = a + SP_PLANES * A_BYTES;
                 barrier_expect(bar, SP_STAGE);
@@ -227,7 +230,6 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 }
             }
         }
-        if (!waited) settle();
     } else if (warp == 1 && lane == 0) {  // ---- matrix instructions
         const uint32_t form = instruction_form<__nv_bfloat16>(p.a_across, p.b_across, TC_M, SP_N);
         const uint64_t form_a = operand_form(p.a_across), form_b = operand_form(p.b_across);
@@ -237,7 +239,7 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             int64_t first, last;
             item(t, first, last);
             for (int64_t k = first; k < last; ++k) {
-                waited = barrier_wait(free_ + 8 * set, set_turn ^ 1) && barrier_wait(full + 8 * s, turn);
+                waited = barrier_wait(free_ + 8 * set, set_turn ^ 1, p.patience) && barrier_wait(full + 8 * s, turn, p.patience);
                 if (!waited) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 // Descriptors have 14 bits of an address; a cluster's blocks have their rank above bit 23 of it.
@@ -259,7 +261,6 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 set ^= 1;
             }
         }
-        if (!waited) settle();
     } else if (warp >= 2) {  // ---- results
         const int writer = threadIdx.x - 64, quarter = warp % 4, row = quarter * 32 + lane, c0 = (warp - 2) / 4 * (SP_N / 2);
         int set = 0, set_turn = 0;
@@ -273,7 +274,7 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
 #pragma unroll
             for (int i = 0; i < SP_N / 2; ++i) sum[i] = 0.0f;
             for (int64_t k = first; k < last; ++k) {
-                if (waited) waited = barrier_wait(done + 8 * set, set_turn);
+                if (waited) waited = barrier_wait(done + 8 * set, set_turn, p.patience);
                 __syncwarp();
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t acc = tensor + set * SP_N + (static_cast<uint32_t>(quarter * 32) << 16) + c0;
@@ -286,17 +287,19 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 }
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) barrier_arrive(free_ + 8 * set);
+                // A warp that does not wait any more does not speak for those that still read.
+                if (lane == 0 && waited) barrier_arrive(free_ + 8 * set);
                 set_turn ^= set;
                 set ^= 1;
             }
             if (!waited) {  // no number comes out of what should have been summed
 #pragma unroll
                 for (int i = 0; i < SP_N / 2; ++i) sum[i] = NAN;
-                if (p.status && writer == 0) set_status(p.status, NMS_ERR_TIMEOUT);
             }
             if (p.split > 1) {
-                // The block's part to its own shared memory: the ring is empty by now.
+                // The block's part to its own shared memory: the ring is empty by now (or the part is none, and a copy may
+                // still land on it).
+                if (!waited) lost_s = NAN;
                 float* part = reinterpret_cast<float*>(dynamic + (ring - shared_address(dynamic))) + row * SP_PITCH + c0;
 #pragma unroll
                 for (int i = 0; i < SP_N / 2; i += 4)
@@ -336,6 +339,7 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     __syncwarp();
     if (p.split > 1) {
         cluster_barrier();
+        if (!waited) settle(p.status);
         if (warp >= 2) {
             // This block's rows of the tile, the parts added in the blocks' order.
             const Place at = tile_place(tile0, p.tiles_m, p.tiles_n, TC_M, SP_N);
@@ -344,7 +348,7 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 const int r = rank * rows + e / (SP_N / 4), c = e % (SP_N / 4) * 4;
                 if (at.m + r >= p.m || at.n + c >= p.n) continue;
                 const uint32_t from = ring + 4 * (r * SP_PITCH + c);
-                float sum[4] = {}, v[8][4];
+                float v[8][4], lost[8];
 #pragma unroll
                 for (int b = 0; b < 8; ++b)
                     if (b < p.split)
@@ -353,9 +357,14 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                                      : "r"(peer_address(from, b)));
 #pragma unroll
                 for (int b = 0; b < 8; ++b)
+                    if (b < p.split)
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(lost[b]) : "r"(peer_address(shared_address(&lost_s), b)));
+                float sum[4] = {};
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
                     if (b < p.split) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) sum[i] += v[b][i];
+                        for (int i = 0; i < 4; ++i) sum[i] += v[b][i] + lost[b];
                     }
                 finish_four(p, at.m + r, at.n + c, sum, bias_s + c);
             }
@@ -363,9 +372,10 @@ product_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
         __syncwarp();
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    // No block leaves while another reads its shared memory.
+    // No block leaves while another reads its shared memory, or something of its own is in flight.
     if (p.split > 1) cluster_barrier();
-    else __syncthreads();
+    else if (__syncthreads_or(!waited)) settle(p.status);
+    __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tensor), "n"(COLUMNS));
 }
@@ -454,6 +464,7 @@ bool launch_product_split(const ProductArgs& q, cudaStream_t st)
     p.out = static_cast<float*>(q.out);
     p.pre = static_cast<float*>(q.pre);
     p.status = q.status;
+    p.patience = patience();
     auto aligned = [](const void* v) { return reinterpret_cast<uintptr_t>(v) % 16 == 0; };
     p.vector = q.n % 4 == 0 && q.residual_row % 4 == 0 && aligned(q.out) && aligned(q.pre) && aligned(q.residual);
     const int64_t tiles = p.tiles_m * p.tiles_n, steps = (p.k + TC_K - 1) / TC_K;

@@ -15,8 +15,6 @@ namespace gbnms {
 constexpr int TC_M = 128, TC_K = 64;        // of a tile, of a stage
 constexpr int TC_WRITERS = 256;             // threads of the epilogue: warps 2 to 9
 constexpr int TC_THREADS = TC_WRITERS + 64;
-constexpr uint64_t TC_PATIENCE = 2000000000;  // ns before a wait gives up; a tile's whole sum over k may take longer:
-constexpr uint64_t TC_TILE_PATIENCE = 10000000000;  // 2^31 of k take a second
 constexpr int A_BYTES = TC_M * TC_K * 2;
 constexpr int HALF_BYTES = 64 * TC_K * 2;   // a box of an operand that lies across: 64 of m or n, 64 of k
 
@@ -50,31 +48,39 @@ __device__ __forceinline__ void barrier_arrive_at(uint32_t peer)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer) : "memory");
 }
 
-// Sleeps until the phase of this parity is complete, a millisecond at most; the
+// Sleeps until the phase of this parity is complete, so many ns at most; the
 // warps that wait for a tile's sums would else take issue slots and power from
 // those that feed the tensor cores.
-__device__ __forceinline__ bool barrier_done(uint32_t bar, int parity)
+__device__ __forceinline__ bool barrier_done(uint32_t bar, int parity, uint32_t most)
 {
     uint32_t done;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(done)
-        : "r"(bar), "r"(parity), "r"(1000000)
+        : "r"(bar), "r"(parity), "r"(most)
         : "memory");
     return done;
 }
 
-// Waits for the phase of this parity; false when it gave up.
-__device__ __forceinline__ bool barrier_wait(uint32_t bar, int parity, uint64_t patience = TC_PATIENCE)
+// How long a wait lasts before it gives up, and how long it sleeps at a time, ns.
+struct Patience {
+    uint64_t all;
+    uint32_t nap;
+};
+
+// Waits for the phase of this parity, `times` its patience; false when it gave up.
+// (The last look is for a wait that was itself kept waiting, as by another process's
+// turn.)
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, int parity, const Patience& p, int times = 1)
 {
-    if (barrier_done(bar, parity)) return true;
+    if (barrier_done(bar, parity, p.nap)) return true;
     uint64_t start, now;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(start));
     do {
-        if (barrier_done(bar, parity)) return true;
+        if (barrier_done(bar, parity, p.nap)) return true;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-    } while (now - start < patience);
-    return false;
+    } while (now - start < times * p.all);
+    return barrier_done(bar, parity, p.nap);
 }
 
 // PAIR: the barrier is the pair's first block's (an address without the rank's bit).
@@ -125,14 +131,16 @@ __device__ __forceinline__ void mma_commit(uint32_t bar)
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// After a wait that gave up: what is in flight (copies, matrix instructions)
-// ends long before this does.
-__device__ __forceinline__ void settle()
+// After a wait that gave up, when the block's threads have met and start nothing
+// more: says so, and what is in flight, copies and matrix instructions, ends long
+// before this does.
+static __device__ __noinline__ void settle(int32_t* status)
 {
     uint64_t start, now;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(start));
     do asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
     while (now - start < 1000000);
+    if (status) set_status(status, NMS_ERR_TIMEOUT);
 }
 
 // N columns of this thread's lane of tensor memory.
@@ -200,6 +208,12 @@ __device__ __forceinline__ void cluster_barrier()
 }
 
 // --------------------------------------------------------------------- host
+
+inline Patience patience()
+{
+    const uint64_t all = product_patience();
+    return {all, static_cast<uint32_t>(all < 1000000 ? all : 1000000)};
+}
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,

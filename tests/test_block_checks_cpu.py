@@ -1,0 +1,26 @@
+"""The transformer block's operators without a GPU: checks that came after the
+first ones."""
+import pytest
+
+import greedy_iou_nms_gb300 as g
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    g.build()
+    return g.load()
+
+
+@pytest.mark.parametrize("status", [torch.zeros(2, dtype=torch.int32), torch.zeros(1), torch.zeros(1, dtype=torch.int64),
+                                    torch.zeros(1, dtype=torch.int32, device="meta")])
+def test_status_is_one_int32_beside_x(status):
+    x, w, dy = torch.zeros(3, 8), torch.zeros(5, 8), torch.zeros(3, 5)
+    for call in (lambda s: g.linear_act(x, w, status=s), lambda s: g.linear_act_grad(dy, x, w, status=s)):
+        with pytest.raises(ValueError, match="status must be one int32"):
+            call(status)
+        with pytest.raises(ValueError, match="status must be a tensor"):
+            call(3)
+        with pytest.raises(ValueError, match="CUDA"):  # the last check
+            call(torch.zeros(1, dtype=torch.int32))
