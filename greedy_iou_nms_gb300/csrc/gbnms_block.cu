@@ -71,9 +71,10 @@ bool by_planes(int32_t type, int64_t m, int64_t n, int64_t k, bool gradient)
 }
 
 // Stretches of k of a weight's gradient on the tensor cores: where clusters of
-// eight leave half of the SMs idle, one for each SM; and no 16-bit sum over more
-// than 2^18 of k (see k_product_split.cu on what those lose); `low`: dz comes in two
-// parts, each of which goes through k.
+// eight leave half of the SMs idle, one for each SM; and no sum over more than 2^18
+// of k, as none of a width is: of 16 bits for what their accumulators cut (see
+// k_product_split.cu), of binary32 so that a chain has 2^12 additions at most.  `low`:
+// dz comes in two parts, each of which goes through k.
 int gradient_segments(int32_t type, int64_t m, int64_t n, int64_t k, bool low)
 {
     if (type == NMS_TYPE_F32 && m <= 32) {  // blocks of few_across_kernel: two an SM
@@ -83,7 +84,7 @@ int gradient_segments(int32_t type, int64_t m, int64_t n, int64_t k, bool low)
     }
     if (type == NMS_TYPE_F32 && !by_planes(type, m, n, k, true)) return 1;
     const int64_t width = type == NMS_TYPE_F32 ? 128 : 64, tiles = ((m + 127) / 128) * ((n + width - 1) / width);
-    int64_t segments = type == NMS_TYPE_F32 ? 1 : (k + (1 << 18) - 1) >> 18;
+    int64_t segments = (k + (1 << 18) - 1) >> 18;
     if (low && segments > 1) segments *= 2;
     if (tiles * 8 <= SMS / 2 && k >= 8192) {
         const int64_t fill = SMS / tiles, most = k / 512;

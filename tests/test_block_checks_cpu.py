@@ -24,3 +24,14 @@ def test_status_is_one_int32_beside_x(status):
             call(3)
         with pytest.raises(ValueError, match="CUDA"):  # the last check
             call(torch.zeros(1, dtype=torch.int32))
+
+
+def test_long_sums_of_a_weights_gradient_are_cut():
+    """From 2^18 rows on there is room for the sums of two stretches, whatever the type and however many the results."""
+    for kind in (g.NMS_TYPE_F32, g.NMS_TYPE_F16, g.NMS_TYPE_BF16):
+        for inner, outer in ((2048, 2048), (40, 4096)):
+            few, more = (g.nms_linear_grad_workspace_size(kind, rows, inner, outer, 1) for rows in (1 << 18, (1 << 18) + 1))
+            assert more - few >= 2 * 4 * inner * outer
+    # Products on the plain units: a chain of theirs is 2^16 long at most.
+    few, more = (g.nms_linear_grad_workspace_size(g.NMS_TYPE_F32, rows, 1 << 15, 32, 1) for rows in (1 << 16, (1 << 16) + 1))
+    assert more - few >= 2 * 4 * 32 << 15
