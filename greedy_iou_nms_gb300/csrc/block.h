@@ -90,7 +90,10 @@ struct ProductArgs {
     int32_t* status;  // or NULL
     int segments;     // 1; more: stretches of k whose sums go to parts [segments][m][n] in place of out
     float* parts;
+    float* scratch;  // 16 bits: product_scratch_bytes()
 };
+// What 16-bit products keep there for sums over k (the larger one of two products').
+size_t product_scratch_bytes(int type, int64_t k);
 // Binary32, by the plain arithmetic units.  False: the driver refused a launch.
 bool launch_product_f32(const ProductArgs& p, cudaStream_t st);
 // Binary32, by the tensor cores: operands of three planes of 16 bits, as
@@ -117,15 +120,6 @@ struct CopyRows {
     int64_t to_row;
 };
 void launch_copy_rows(const CopyRows* of, int count, cudaStream_t st);  // one or two operands
-
-// out = sums over the parts [segments][n], of any type, in order.
-void launch_join_parts(const float* parts, int segments, int64_t n, void* out, int type, cudaStream_t st);
-// 16 bits, by the tensor cores: operands and their rows start at multiples of
-// 16 bytes and do not overlap.
-bool launch_product_tc(const ProductArgs& p, cudaStream_t st);
-// Rows of 16-bit elements to rows `to_row` apart.
-void launch_copy_rows(const void* from, int64_t from_row, int64_t rows, int64_t width, void* to, int64_t to_row,
-                      cudaStream_t st);
 
 // dz = dy * act'(pre) [rows][width], rows dz_row apart (none: dz NULL), and
 // the sums of its columns before they are rounded (none: dbias NULL).

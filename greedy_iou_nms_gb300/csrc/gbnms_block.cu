@@ -72,9 +72,8 @@ bool by_planes(int32_t type, int64_t m, int64_t n, int64_t k, bool gradient)
 
 // Stretches of k of a weight's gradient on the tensor cores: where clusters of
 // eight leave half of the SMs idle, one for each SM; and no sum over more than 2^18
-// of k, as none of a width is: of 16 bits for what their accumulators cut (see
-// k_product_split.cu), of binary32 so that a chain has 2^12 additions at most.  `low`:
-// dz comes in two parts, each of which goes through k.
+// of k, as none of a width is, so that a chain in binary32 has 2^12 additions at most.
+// `low`: dz comes in two parts, each of which goes through k.
 int gradient_segments(int32_t type, int64_t m, int64_t n, int64_t k, bool low)
 {
     if (type == NMS_TYPE_F32 && m <= 32) {  // blocks of few_across_kernel: two an SM
@@ -152,6 +151,7 @@ extern "C" nms_status nms_linear_workspace_size(int32_t type, int64_t rows, int3
     if (rows == 0) return NMS_OK;
     if (by_planes(type, rows, outer, inner, false)) *bytes = plane_bytes(rows, inner) + plane_bytes(outer, inner);
     else if (type != NMS_TYPE_F32 && !aligned) *bytes = copy_bytes(rows, inner) + copy_bytes(outer, inner);
+    *bytes += product_scratch_bytes(type, inner);
     return NMS_OK;
 }
 
@@ -179,6 +179,8 @@ extern "C" nms_status nms_linear_run(const void* x, int64_t x_row, int32_t type,
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaGetLastError();
     char* rest = static_cast<char*>(workspace);
+    float* const scratch = reinterpret_cast<float*>(rest);
+    rest += product_scratch_bytes(type, inner);
     Operand a{x, x_row, rows, inner}, b{weight, weight_row, outer, inner};
     ProductArgs p{};
     p.type = type;
@@ -193,6 +195,7 @@ extern "C" nms_status nms_linear_run(const void* x, int64_t x_row, int32_t type,
     p.out = y;
     p.pre = pre;
     p.status = dev_status;
+    p.scratch = scratch;
     p.segments = 1;
     if (!launch_product(p, a, b, by_planes(type, rows, outer, inner, false), rest, st)) return NMS_ERR_CUDA;
     return cuda_status();
@@ -210,6 +213,7 @@ extern "C" nms_status nms_linear_grad_workspace_size(int32_t type, int64_t rows,
     const bool two = type != NMS_TYPE_F32;
     *bytes = (two ? 2 : 1) * round_up(type_bytes(type) * rows * padded(outer)) + round_up(slope_workspace_bytes(rows, outer));
     *bytes += parts_bytes(gradient_segments(type, outer, inner, rows, two), outer, inner);
+    *bytes += product_scratch_bytes(type, outer > rows ? outer : rows);
     if (by_planes(type, rows, inner, outer, false) || by_planes(type, outer, inner, rows, true))
         *bytes += plane_bytes(rows, outer) + plane_bytes(outer, inner) + plane_bytes(rows, inner);
     else if (type != NMS_TYPE_F32 && !aligned)
@@ -285,6 +289,8 @@ extern "C" nms_status nms_linear_grad_run(const void* dy, int64_t dy_row, const 
         a.dbias = dbias;
         launch_slope(a, sums, st);
     }
+    float* const scratch = reinterpret_cast<float*>(rest);
+    rest += product_scratch_bytes(type, outer > rows ? outer : rows);
     Operand xs{x, x_row, rows, inner}, ws{weight, weight_row, outer, inner};
     if (planes && dx && dweight) {  // both products' other operands at once
         const SplitRows split[2] = {as_split(ws, rest), as_split(xs, rest)};
@@ -295,6 +301,7 @@ extern "C" nms_status nms_linear_grad_run(const void* dy, int64_t dy_row, const 
     p.act = NMS_ACT_NONE;
     p.status = dev_status;
     p.a_low = lower;
+    p.scratch = scratch;
     p.b_across = 1;
     p.n = inner;
     p.segments = 1;

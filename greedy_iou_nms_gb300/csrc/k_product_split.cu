@@ -4,9 +4,10 @@
 // m the rest rounded, l what is left, 8 significant bits each.  Of the nine
 // products of two such sums six are taken; the others are below 2^-26 of x y.
 //
-// The tensor cores add up in binary32, but cut off below two more bits than its
-// 24 after every 16 products (measured: 1 + 1.5 * 2^-24 stays 1), which leaves a
-// sum over k = 4096 off by 4e-6.  So an accumulator takes 64 of k only, smallest
+// The tensor cores add up in binary32, but cut each of 16 products below 2^-25 of
+// the sum so far and the new sum to 24 bits (measured: 1 and eight times 1.25 2^-24
+// are 1 + 16 2^-24, 1 + 1.5 2^-24 is 1), which leaves a sum over k = 4096 off by 4e-6
+// and more.  So an accumulator takes 64 of k only, smallest
 // products first, and the writers add it to binary32 sums in registers (rounded
 // to nearest) while the next 64 go to a second one.
 //

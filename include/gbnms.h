@@ -594,9 +594,11 @@ nms_status nms_relation_softmax_grad_run(const void* dprobs, const void* probs, 
  * Linear layer:
  *   z = x weight^T + bias,  y = act(z) + residual,
  * x [rows][inner], weight [outer][inner], y [rows][outer].  Sums are held in
- * binary32.  Operands of 16 bits go to the tensor cores, which cut what 16
- * products add below 2^-25 of the sum so far: a sum of k products is off by up to
- * k 2^-29 of its largest part.  Larger products of binary32 operands go there
+ * binary32.  Operands of 16 bits go to the tensor cores, which cut each product
+ * below 2^-25 of the sum so far and that below 2^-23 after 16 of them; they add up
+ * 4096 products of binary16, 32768 of bfloat16, whose cuts are less than a third
+ * of the half step that a result is rounded by, and the rest is added to nearest.
+ * Larger products of binary32 operands go there
  * as three bfloat16 parts of each element, 64 products at a time, and are as near
  * as a binary32 sum; elements below 2^-100 keep fewer than 24 bits there.  NaN and
  * infinities in an operand, and sums beyond binary32, give what they give in

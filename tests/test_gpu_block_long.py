@@ -27,7 +27,48 @@ def _product(a, b, step=25000):
     return sum(a[i:i + step].double().T @ b[i:i + step].double() for i in range(0, a.shape[0], step))
 
 
-@pytest.mark.parametrize("kind,act", [("f32", "none"), ("f32", "silu")])
+def _cut(t):
+    """Relative to a sum of one sign: the tensor cores cut each product below 2^-25 of the sum so far, and that below 2^-23
+    after 16 of them, as many products as they add up by themselves."""
+    return (2 ** 12 if t is torch.float16 else 2 ** 15) * (2.0 ** -25 + 2.0 ** -27)
+
+
+# Operands that changed places, tiles split over blocks, pairs with several tiles each.
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,inner,outer", [(16, 1 << 18, 136), (16, 5000, 4096), (300, 1 << 17, 264), (20000, 1 << 16, 1032),
+                                              (5000, 33000, 1600)])
+def test_long_widths(rows, inner, outer, kind):
+    t = R.TYPES[kind]
+    r = torch.Generator("cuda").manual_seed(4)
+    x, w = ((_positive(r, s, torch.float32) / 64).to(t) for s in ((rows, inner), (outer, inner)))
+    b, res = _positive(r, (outer,), torch.float32), _positive(r, (rows, outer), t)
+    y, pre = g.linear_act(x, w, b, act="relu", residual=res, return_pre=True)
+    some = torch.arange(rows) if rows < 200 else torch.cat([torch.arange(100), torch.arange(rows - 100, rows)])
+    z = x[some].double() @ w.double().T + b.double()
+    near = (_cut(t) + 80 * R.U) * z
+    assert bool(((pre[some].double() - z).abs() <= near + (R.half_step(t) + 2 * R.U) * z).all())
+    z = z + res[some].double()
+    assert bool(((y[some].double() - z).abs() <= near + (R.half_step(t) + 4 * R.U) * z).all())
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("rows,inner,outer", [(40, 200, 40000), (3000, 1032, 40000)])
+def test_long_gradients_to_x(rows, inner, outer, act, kind):
+    t = R.TYPES[kind]
+    r = torch.Generator("cuda").manual_seed(5)
+    dy, w, z = ((_positive(r, s, torch.float32) / d).to(t) for s, d in (((rows, outer), 64), ((outer, inner), 64),
+                                                                        ((rows, outer), 1)))
+    x = torch.zeros(rows, inner, dtype=t, device="cuda")
+    dx, dw, _ = g.linear_act_grad(dy, x, w, z, act=act, need=(True, True, False))
+    ref = (dy.double() * R.slope(z.double(), act)) @ w.double()
+    slope = 1.5 * R.act_error(t) * (act != "none")
+    # In two parts: the lower one's sum is cut too.
+    off = _cut(t) * (1 + 2 * R.half_step(t)) + 80 * R.U + R.half_step(t) ** 2 + slope + R.half_step(t) + 2 * R.U
+    assert float((dx.double() / ref - 1).abs().max()) <= off and not bool(dw.any())
+
+
+@pytest.mark.parametrize("kind,act", [("f32", "none"), ("f32", "silu"), ("bf16", "none"), ("bf16", "silu"), ("f16", "none")])
 def test_linear(kind, act):
     """More tiles than the few that are cut for want of blocks."""
     rows, inner, outer = 300000, 1288, 40
@@ -39,9 +80,13 @@ def test_linear(kind, act):
     dz = dy.double() * R.slope(z.double(), act)
     slope = 1.5 * R.act_error(t) * (act != "none")  # relative to slopes of 0.7 and more
     ref = _product(dz, x)
-    # 2^12 sums of 64 one after another, half a step each; 24 steps of the tensor cores in each of them, which cut up
-    # to 2^-25; the products that are left out, two of 2^-25 and one of 2^-34; the slopes.
-    off = (2 ** 12 + 8) * R.U + 24 * 2.0 ** -25 + 2.0 ** -24 + slope
+    if t is torch.float32:
+        # 2^12 sums of 64 one after another, half a step each; 24 times 16 products of the tensor cores in each of them,
+        # cut as above; the products that are left out, two of 2^-25 and one of 2^-34; the slopes.
+        off = (2 ** 12 + 8) * R.U + 24 * 16 * (2.0 ** -25 + 2.0 ** -27) + 2.0 ** -24 + slope
+    else:
+        # The stretches' cuts and their binary32 sum; the lower parts of dz; the result's rounding.
+        off = _cut(t) + 80 * R.U + R.half_step(t) ** 2 + slope + (R.half_step(t) + 2 * R.U)
     assert float((dw.double() / ref - 1).abs().max()) <= off
     # A warp adds 256 rows and its block eight of those; the runs' sums are compensated.
     assert float((db.double() / dz.sum(0) - 1).abs().max()) <= (256 + 8 + 4) * R.U + slope
