@@ -2,9 +2,9 @@
 
 Each translation unit compiles in its own nvcc process (in parallel), then
 nvcc links the shared library.  The C++ half of the Python binding (g++, torch's
-headers) compiles beside them; without torch it is left out.  -fmad=false keeps every binary32 product and
-sum individually rounded (the kernels also use explicit _rn intrinsics); no
-fast-math flag is ever passed.
+headers) compiles beside them; without torch, or with one for CPUs alone, it is
+left out.  -fmad=false keeps every binary32 product and sum individually rounded
+(the kernels also use explicit _rn intrinsics); no fast-math flag is ever passed.
 """
 from __future__ import annotations
 
@@ -26,9 +26,24 @@ LIB = os.path.join(BUILD, "libgbnms.so")
 PROBE_SRC = os.path.join(PKG, "probe", "alu_probe.cu")
 PROBE_LIB = os.path.join(BUILD, "libgbprobe.so")
 
-# Tensor functions of block.py.
+
+def _torch_folder():
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+
+
+def _torch_version() -> str:
+    # From its file: importing torch takes seconds.
+    try:
+        with open(os.path.join(_torch_folder() or "", "version.py")) as f:
+            return next(line.split("=")[-1].strip().strip("'\"") for line in f if line.startswith("__version__"))
+    except (OSError, StopIteration):
+        return "none"
+
+
+# Tensor functions of block.py: for the torch and the interpreter that they are compiled against, and no others.
 BINDING_SRC = os.path.join(PKG, "binding", "block_binding.cpp")
-BINDING_LIB = os.path.join(BUILD, "gbblock.so")
+BINDING_LIB = os.path.join(BUILD, "gbblock-torch%s-%s.so" % (_torch_version(), sysconfig.get_config_var("SOABI")))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-fmad=false", "-Xcompiler", "-fPIC",
@@ -46,9 +61,9 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _torch_folder():
-    spec = importlib.util.find_spec("torch")
-    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+def _with_binding() -> bool:
+    torch = _torch_folder()
+    return torch is not None and os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so"))
 
 
 def _binding_command(out: str):
@@ -67,7 +82,7 @@ def _stale() -> bool:
         return True
     if os.path.getmtime(PROBE_SRC) > os.path.getmtime(PROBE_LIB):
         return True
-    if _torch_folder():
+    if _with_binding():
         if not os.path.exists(BINDING_LIB):
             return True
         if any(os.path.getmtime(d) > os.path.getmtime(BINDING_LIB) for d in
@@ -104,7 +119,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     cmds.append([cc, *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", *extra_flags,
                  "-shared", PROBE_SRC, "-o", probe_tmp])
     binding_tmp = BINDING_LIB + ".tmp%d" % os.getpid()
-    with_binding = _torch_folder() is not None
+    with_binding = _with_binding()
     if with_binding:
         cmds.append(_binding_command(binding_tmp))
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(cmds), os.cpu_count() or 1))) as ex:

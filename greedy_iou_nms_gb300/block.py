@@ -136,7 +136,8 @@ def _native():
 
         from ._build import BINDING_LIB
         if not os.path.exists(BINDING_LIB):
-            raise RuntimeError(f"gbblock.so not built at {BINDING_LIB}: call greedy_iou_nms_gb300.build()")
+            raise RuntimeError(f"the tensor functions are not built at {BINDING_LIB}: call greedy_iou_nms_gb300.build() (with "
+                               "a torch for CUDA)")
         lib = _lib()
         loader = importlib.machinery.ExtensionFileLoader("gbblock", BINDING_LIB)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("gbblock", loader))

@@ -35,3 +35,19 @@ def test_long_sums_of_a_weights_gradient_are_cut():
     # Products on the plain units: a chain of theirs is 2^16 long at most.
     few, more = (g.nms_linear_grad_workspace_size(g.NMS_TYPE_F32, rows, 1 << 15, 32, 1) for rows in (1 << 16, (1 << 16) + 1))
     assert more - few >= 2 * 4 * 32 << 15
+
+
+def test_the_binding_is_of_this_torch_and_interpreter(monkeypatch, tmp_path):
+    """Another torch or interpreter means another file, and a torch without CUDA none: the library builds without it."""
+    import os
+    import sysconfig
+    from greedy_iou_nms_gb300 import _build
+    name = os.path.basename(_build.BINDING_LIB)
+    assert torch.__version__ in name and sysconfig.get_config_var("SOABI") in name
+    assert _build._with_binding() and os.path.exists(_build.BINDING_LIB) and not _build._stale()
+    monkeypatch.setattr(_build, "BINDING_LIB", str(tmp_path / name.replace(torch.__version__, "0.0")))
+    assert _build._stale()
+    (tmp_path / "lib").mkdir()
+    monkeypatch.setattr(_build, "_torch_folder", lambda: str(tmp_path))
+    assert not _build._with_binding() and not _build._stale()
+    assert _build._torch_version() == "none"
