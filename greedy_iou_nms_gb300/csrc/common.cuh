@@ -182,6 +182,12 @@ constexpr int BAND_L = 16;
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
+// All of the cluster's blocks meet, each warp as one.
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void set_status(int32_t* status, int code)
 {
     atomicCAS(reinterpret_cast<int*>(status), 0, code);

@@ -2,11 +2,11 @@
 // their epilogue, on the plain arithmetic units, and the copy of 16-bit rows
 // whose places the tensor cores' loads cannot take.
 //
-// product_kernel, for products of less than 2^26 multiplications (larger ones go
-// to the tensor cores, k_product_split.cu): a block has a tile of 64 x 64 results,
-// its 256 threads 4 x 4 of them each.  Few tiles: the blocks of a cluster share
-// one, each a stretch of k, and add up their parts through distributed shared
-// memory, in order.
+// product_kernel, for what by_planes() (gbnms_block.cu) does not send to the tensor
+// cores (k_product_split.cu): products of less than 2^26 multiplications, 2^21 where
+// k is 1024 and more.  A block has a tile of 64 x 64 results, its 256 threads 4 x 4
+// of them each.  Few tiles: the blocks of a cluster share one, each a stretch of k,
+// and add up their parts through distributed shared memory, in order.
 //
 // Up to 16 rows are a stream of the weight, whose elements are used once a row:
 // few_along_kernel reads it straight to registers, all of an SM's warps at once,
@@ -61,11 +61,6 @@ struct Feed {
         left_k -= PR_DEPTH;
     }
 };
-
-__device__ __forceinline__ void cluster_barrier()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 // The sum over the cluster's blocks of what each has at its own `at`.
 __device__ __forceinline__ float cluster_sum(const float* at, int split)

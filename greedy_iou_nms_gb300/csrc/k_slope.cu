@@ -20,11 +20,6 @@ namespace {
 
 constexpr int SL_SLOTS = 8;
 
-__device__ __forceinline__ void cluster_barrier()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // joined: the runs of a strip are a cluster, whose first block adds up their sums.
 template <typename T, int V>
 __global__ void __launch_bounds__(32 * SL_SLOTS, 5)

@@ -202,11 +202,6 @@ __device__ __forceinline__ Place tile_place(int64_t t, int64_t tiles_m, int64_t 
     return {m * rows, (strip * 16 + left - m * width) * bn};
 }
 
-__device__ __forceinline__ void cluster_barrier()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // --------------------------------------------------------------------- host
 
 inline Patience patience()

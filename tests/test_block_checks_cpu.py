@@ -51,3 +51,19 @@ def test_the_binding_is_of_this_torch_and_interpreter(monkeypatch, tmp_path):
     monkeypatch.setattr(_build, "_torch_folder", lambda: str(tmp_path))
     assert not _build._with_binding() and not _build._stale()
     assert _build._torch_version() == "none"
+
+
+def test_the_largest_widths_of_a_linear_layer():
+    most = g.NMS_LINEAR_MAX_WIDTH
+    for size in (g.nms_linear_workspace_size, g.nms_linear_grad_workspace_size):
+        for kind in (g.NMS_TYPE_F32, g.NMS_TYPE_F16, g.NMS_TYPE_BF16):
+            for inner, outer in ((most, 1), (1, most), (most, most)):
+                assert size(kind, 1, inner, outer, 1) >= 0
+            for inner, outer in ((most + 1, 1), (1, most + 1)):
+                with pytest.raises(g.NmsError) as e:
+                    size(kind, 1, inner, outer, 1)
+                assert e.value.code == g.NMS_ERR_CAPACITY
+            assert size(kind, 1 << 20, most, 1, 1) >= 0  # 2^38 elements
+            with pytest.raises(g.NmsError) as e:
+                size(kind, (1 << 20) + 1, most, 1, 1)
+            assert e.value.code == g.NMS_ERR_CAPACITY
