@@ -50,8 +50,8 @@ bool uneven(int32_t type, const void* p, int64_t row, int64_t rows, int64_t widt
 size_t copy_bytes(int64_t rows, int64_t width) { return round_up(2 * rows * padded(width)); }
 
 // Multiplications from which a binary32 product is worth making planes for, where k
-// is short: 300 x 256 x 1024, 2^26.2, took 14.6 us by them and 16.4 on the plain units; 300 x 256 x
-// 512, 2^25.2, 14.4 and 12.5.
+// is short: 300 x 256 x 1024, 2^26.2, took 14.6 us by them and 16.4 on the plain
+// units; 300 x 256 x 512, 2^25.2, 14.4 and 12.5.
 constexpr int64_t SPLIT_LEAST = int64_t(1) << 26;
 
 size_t plane_bytes(int64_t rows, int64_t width) { return round_up(3 * 2 * rows * padded(width)); }

@@ -23,6 +23,8 @@
 // side fills the 128 lanes and BN is 16 to 64.  Few tiles: the blocks of a
 // cluster share one, each a stretch of k, and add up their parts through
 // distributed shared memory, in order.
+//
+// Long sums: see product_stretch().  An operand of two parts (low_of): k twice.
 #include <atomic>
 
 #include "tensor_core.cuh"

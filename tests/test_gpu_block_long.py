@@ -124,3 +124,37 @@ def test_layer_norm(rows, width, kind):
     # 256 rows a team and its block's teams (16 of them, or one); u itself is off by three roundings.
     assert bool(((dw.double() - ref_w).abs() <= (256 + 16 + 8) * R.U * size).all())
     assert float((db.double() / ref_b - 1).abs().max()) <= (256 + 16 + 4) * R.U
+
+
+def test_same_bits_in_graphs_and_on_two_streams():
+    """Calls at the same time have scratch memory of their own."""
+    r = torch.Generator("cuda").manual_seed(6)
+    x, w = ((_positive(r, s, torch.float32) / 64 - 1 / 64).half() for s in ((9000, 9000), (328, 9000)))
+
+    def both():
+        y, pre = g.linear_act(x, w, act="gelu", return_pre=True)
+        return (y, *g.linear_act_grad(y, x, w, pre, act="gelu"))
+
+    def same(a, b):
+        return all(torch.equal(p, q) for p, q in zip(a, b))
+
+    first = both()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for s in sides:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            outs.append(both())
+    for s in sides:
+        s.synchronize()
+    assert all(same(first, out) for out in outs)
+    graphs, held = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for graph in graphs:
+        with torch.cuda.graph(graph):
+            held.append(both())
+    x.copy_(x.flip(0))
+    for graph in graphs:
+        graph.replay()
+    torch.cuda.synchronize()
+    again = both()
+    assert all(same(again, out) for out in held) and not same(again, first)
